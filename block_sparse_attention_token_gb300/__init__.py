@@ -31,6 +31,8 @@ BWD_SPLIT_KV = 4
 OUT_RASTER = 8
 IN_RASTER = 16
 GRID_CAP_SHIFT = 16
+NORM_RMS, NORM_HEAD = 1, 2
+ROPE_INVERSE, ROPE_IN_BLOCKED, ROPE_OUT_BLOCKED = 1, 2, 4
 
 
 def GRID_CAP(n: int) -> int:
@@ -117,6 +119,13 @@ _SIG = {
     "sparsp_attn_bwd": (_I32, [_P, _P, _P, _P, _P, _P, _P, _P, _P, ctypes.c_float, _P, _P, _P, _P,
                                ctypes.c_size_t, ctypes.c_uint32, _P, _P, _P]),
     "sparsp_csr_transpose": (_I32, [_P, _P, _P, _P, _P, _P, _P]),
+    "sparsp_norm_fwd": (_I32, [_P, ctypes.c_uint32, _P, ctypes.c_int64, _P, _P, ctypes.c_float, _P, _P, _P, _P]),
+    "sparsp_norm_workspace_size": (ctypes.c_size_t, [_P, ctypes.c_uint32]),
+    "sparsp_norm_bwd": (_I32, [_P, ctypes.c_uint32, _P, _P, ctypes.c_int64, _P, _P, _P, _P, ctypes.c_int64, _P, _P, _P,
+                               ctypes.c_size_t, _P]),
+    "sparsp_rope_table_size": (ctypes.c_size_t, [_P]),
+    "sparsp_rope_table": (_I32, [_P, ctypes.c_double, _P, _P, _P, ctypes.c_size_t, _P]),
+    "sparsp_rope": (_I32, [_P, _P, _P, _P, _P, ctypes.c_int64, _P, ctypes.c_int64, ctypes.c_uint32, _P, _P, _P]),
     "sparsp_diag_umma_tile": (_I32, [_P, _P, _P, _I32, _I32, _I32, _P, _P]),
     "sparsp_diag_wait_timeout": (_I32, [ctypes.c_uint64, _P, _P]),
 }
@@ -167,6 +176,159 @@ def _sref(shape: Shape):
 
 def _empty(n_bytes: int, device) -> torch.Tensor:
     return torch.empty(max(int(n_bytes), 16), dtype=torch.uint8, device=device)
+
+
+def _want(name: str, t, dims, dtype, optional: bool = False):
+    """A tensor argument of the calls below: contiguous, on the current device,
+    of this shape and dtype (a plain address is passed through)."""
+    if t is None and optional or isinstance(t, int):
+        return t
+    if (t is None or tuple(t.shape) != tuple(dims) or t.dtype != dtype or not t.is_contiguous()
+            or t.device.index != torch.cuda.current_device()):
+        got = None if t is None else (tuple(t.shape), t.dtype, str(t.device), t.stride())
+        raise ValueError(f"{name}: expected a contiguous {tuple(dims)} {dtype} tensor on the current CUDA device, "
+                         f"got {got}")
+    return t
+
+
+def _token_stride(shape: Shape, name: str, t) -> int:
+    """Elements between the tokens of a raster tensor [B, N, H, d] that may be a
+    slice of a wider one (heads and columns contiguous, batches of N tokens)."""
+    s, dims = shape, (shape.B, shape.N, shape.H, shape.d)
+    if isinstance(t, int):
+        return 0
+    ts = s.H * s.d
+    ok = (t is not None and tuple(t.shape) == dims and t.dtype == s.torch_dtype
+          and t.device.index == torch.cuda.current_device())
+    if ok:
+        st = t.stride()
+        ts = st[1] if s.N > 1 else st[0] if s.B > 1 else ts
+        ok = st[3] == 1 and (s.H == 1 or st[2] == s.d) and (s.B == 1 or st[0] == s.N * ts) and ts >= s.H * s.d
+    if not ok:
+        got = None if t is None else (tuple(t.shape), t.dtype, str(t.device), t.stride())
+        raise ValueError(f"{name}: expected a raster {dims} {s.torch_dtype} tensor on the current CUDA device with "
+                         f"contiguous heads and one stride between tokens, got {got}")
+    return ts
+
+
+# ----------------------------------------------------------------- before step 1: token norm, rotary positions
+
+def _norm_flags(rms: bool, per_head: bool) -> int:
+    return (NORM_RMS if rms else 0) | (NORM_HEAD if per_head else 0)
+
+
+def norm_workspace_size(shape: Shape, rms: bool = False, per_head: bool = False) -> int:
+    return lib().sparsp_norm_workspace_size(_sref(shape), _norm_flags(rms, per_head))
+
+
+def norm_fwd(shape: Shape, x, w=None, b=None, eps: float = 1e-6, rms: bool = False, per_head: bool = False, out=None,
+             mean=None, rstd=None, stream=None):
+    """Layer norm (RMS norm with rms) of raster x [B,N,H,d] over the H*d values of a
+    token, or over each head's d values with per_head. x may be a slice of a fused
+    projection (one stride between tokens). w, b: float32 [H*d] or [d], or None.
+    Returns (y, mean, rstd), the statistics float32 [B,N] ([B,N,H] with per_head);
+    mean is None with rms."""
+    s = shape
+    xs = _token_stride(s, "x", x)
+    cols, stat = ((s.d,), (s.B, s.N, s.H)) if per_head else ((s.H * s.d,), (s.B, s.N))
+    if out is None:
+        out = torch.empty((s.B, s.N, s.H, s.d), dtype=s.torch_dtype, device=x.device)
+    if rms:
+        mean = None
+    elif mean is None:
+        mean = torch.empty(stat, dtype=torch.float32, device=x.device)
+    if rstd is None:
+        rstd = torch.empty(stat, dtype=torch.float32, device=x.device)
+    f32 = torch.float32
+    _check("sparsp_norm_fwd", lib().sparsp_norm_fwd(
+        _sref(s), _norm_flags(rms, per_head), _ptr(x), xs, _ptr(_want("w", w, cols, f32, True)),
+        _ptr(_want("b", b, cols, f32, True)), float(eps),
+        _ptr(_want("out", out, (s.B, s.N, s.H, s.d), s.torch_dtype)), _ptr(_want("mean", mean, stat, f32, True)),
+        _ptr(_want("rstd", rstd, stat, f32)), _stream(stream)))
+    return out, mean, rstd
+
+
+def norm_bwd(shape: Shape, dy, x, w, mean, rstd, rms: bool = False, per_head: bool = False, dx=None, dw=None, db=None,
+             ws=None, stream=None):
+    """Gradients of norm_fwd from its x, mean (None with rms) and rstd: (dx, dw, db),
+    db None with rms unless a buffer is given. dx may be a slice like x."""
+    s = shape
+    xs = _token_stride(s, "x", x)
+    cols, stat = ((s.d,), (s.B, s.N, s.H)) if per_head else ((s.H * s.d,), (s.B, s.N))
+    dims, f32 = (s.B, s.N, s.H, s.d), torch.float32
+    if dx is None:
+        dx = torch.empty(dims, dtype=s.torch_dtype, device=x.device)
+    if dw is None:
+        dw = torch.empty(cols, dtype=f32, device=x.device)
+    if db is None and not rms:
+        db = torch.empty(cols, dtype=f32, device=x.device)
+    if ws is None:
+        ws = _empty(norm_workspace_size(s, rms, per_head), x.device)
+    dxs = _token_stride(s, "dx", dx)
+    _check("sparsp_norm_bwd", lib().sparsp_norm_bwd(
+        _sref(s), _norm_flags(rms, per_head), _ptr(_want("dy", dy, dims, s.torch_dtype)), _ptr(x), xs,
+        _ptr(_want("w", w, cols, f32, True)), _ptr(None if rms else _want("mean", mean, stat, f32)),
+        _ptr(_want("rstd", rstd, stat, f32)), _ptr(dx), dxs, _ptr(_want("dw", dw, cols, f32, True)),
+        _ptr(_want("db", db, cols, f32, True)), _ptr(ws), ws.numel(), _stream(stream)))
+    return dx, dw, db
+
+
+class RopeAxes(ctypes.Structure):
+    _fields_ = [("cols", _I32 * 3), ("extent", _I32 * 3), ("half", _I32)]
+
+
+@dataclass
+class RopeTable:
+    """cos and sin of the three axes (rope_table), kept by the caller."""
+    axes: RopeAxes
+    table: torch.Tensor
+
+
+def rope_table(shape: Shape, cols, theta: float = 10000.0, offset=(0.0, 0.0, 0.0), scale=(1.0, 1.0, 1.0),
+               extent=None, half: bool = False, stream=None) -> RopeTable:
+    """The (cos, sin) table of three-axis rotary positions: cols columns of a head
+    turn with the token's frame, row and column; position p of an axis stands for
+    offset + scale * p. extent: positions per axis (default: the grid)."""
+    cols, ext = [int(c) for c in cols], [int(e) for e in (extent or (shape.T, shape.Y, shape.X))]
+    if len(cols) != 3 or len(ext) != 3 or sum(cols) > shape.d or half and sum(cols) != shape.d:
+        raise ValueError(f"rope_table: columns {cols} (extent {ext}) do not fit a head of {shape.d} "
+                         f"{'paired by halves' if half else ''}")
+    axes = RopeAxes((_I32 * 3)(*cols), (_I32 * 3)(*ext), int(half))
+    n = lib().sparsp_rope_table_size(ctypes.byref(axes))
+    table = torch.empty(max(n // 4, 4), dtype=torch.float32, device=f"cuda:{torch.cuda.current_device()}")
+    d3 = ctypes.c_double * 3
+    _check("sparsp_rope_table", lib().sparsp_rope_table(
+        ctypes.byref(axes), float(theta), ctypes.byref(d3(*offset)), ctypes.byref(d3(*scale)), _ptr(table),
+        table.numel() * 4, _stream(stream)))
+    return RopeTable(axes, table)
+
+
+def rope(shape: Shape, table: RopeTable, x, out=None, inverse: bool = False, in_blocked: bool = False,
+         out_blocked: bool = True, pos=None, means=None, status=None, stream=None):
+    """Turns the rows of x by their positions, from raster [B,N,H,d] (in_blocked:
+    blocked [B,H,N,d]) into tile order (out_blocked=False: raster), and returns
+    out. inverse: the transposed rotation (gradients). pos: int32 [B,N,3] table
+    positions per token, default the grid coordinates. means: float32
+    [B,H,nb,d] buffer for the tile means of the turned values. Raster tensors may
+    be slices of wider ones (one stride between tokens)."""
+    s = shape
+    raster, blocked = (s.B, s.N, s.H, s.d), (s.B, s.H, s.N, s.d)
+    dt, i32 = s.torch_dtype, torch.int32
+    if out is None:
+        out = torch.empty(blocked if out_blocked else raster, dtype=dt, device=x.device)
+    xs = 0 if in_blocked else _token_stride(s, "x", x)
+    os_ = 0 if out_blocked else _token_stride(s, "out", out)
+    if in_blocked:
+        _want("x", x, blocked, dt)
+    if out_blocked:
+        _want("out", out, blocked, dt)
+    flags = ((ROPE_INVERSE if inverse else 0) | (ROPE_IN_BLOCKED if in_blocked else 0)
+             | (ROPE_OUT_BLOCKED if out_blocked else 0))
+    _check("sparsp_rope", lib().sparsp_rope(
+        _sref(s), ctypes.byref(table.axes), _ptr(table.table), _ptr(_want("pos", pos, (s.B, s.N, 3), i32, True)),
+        _ptr(x), xs, _ptr(out), os_, flags,
+        _ptr(_want("means", means, (s.B, s.H, s.nb, s.d), torch.float32, True)), _ptr(status), _stream(stream)))
+    return out
 
 
 # ----------------------------------------------------------------- step 1

@@ -95,6 +95,42 @@ AttnWs attn_ws_layout(const Dims& s, bool backward, void* base) {
   return w;
 }
 
+// A raster tensor's token stride: 0 means contiguous; else at least H*d
+// elements and a multiple of 16 bytes.
+sparsp_status_t check_stride(const Dims& s, int64_t* stride) {
+  const int64_t hd = (int64_t)s.H * s.d;
+  if (*stride == 0) *stride = hd;
+  if (*stride < hd || *stride > INT64_MAX / 8 / (s.B * s.N)) return SPARSP_ERR_SHAPE;
+  if (*stride * s.elem % 16 != 0) return SPARSP_ERR_ALIGN;
+  return SPARSP_OK;
+}
+
+// Do the byte ranges of two raster tensors with these token strides overlap?
+bool overlap(const Dims& s, const void* a, int64_t a_stride, const void* b, int64_t b_stride) {
+  const int64_t last = (int64_t)s.B * s.N - 1, hd = (int64_t)s.H * s.d;
+  const uint8_t *pa = (const uint8_t*)a, *pb = (const uint8_t*)b;
+  return pa < pb + (last * b_stride + hd) * s.elem && pb < pa + (last * a_stride + hd) * s.elem;
+}
+
+constexpr int kNormMaxCols = 16384;
+
+sparsp_status_t check_norm(const sparsp_shape_t* shape, uint32_t flags, Dims* s) {
+  const sparsp_status_t r = check_shape(shape, s);
+  if (r != SPARSP_OK) return r;
+  if (flags & ~(SPARSP_NORM_RMS | SPARSP_NORM_HEAD)) return SPARSP_ERR_INVALID_ARG;
+  if (!(flags & SPARSP_NORM_HEAD) && (int64_t)s->H * s->d > kNormMaxCols) return SPARSP_ERR_UNSUPPORTED;
+  return SPARSP_OK;
+}
+
+// Axes of a rotary table: even column counts, at least one position per axis.
+sparsp_status_t check_rope(const sparsp_rope_t* r) {
+  if (r == nullptr) return SPARSP_ERR_INVALID_ARG;
+  for (int ax = 0; ax < 3; ++ax)
+    if (r->cols[ax] < 0 || r->cols[ax] % 2 || r->cols[ax] > 128 || r->extent[ax] < 1) return SPARSP_ERR_SHAPE;
+  if (rope_table_entries(*r) > INT32_MAX) return SPARSP_ERR_UNSUPPORTED;
+  return SPARSP_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -603,6 +639,112 @@ sparsp_status_t sparsp_attn_bwd(const sparsp_shape_t* shape, const void* q, cons
   return launch_attn_bwd_dkdv(s, (cb)q, (cb)k, (cb)v, (cb)dout, lse, w.delta, w.col_ptr,
                               w.row_idx, scale, (__nv_bfloat16*)dk, (__nv_bfloat16*)dv, w.items2,
                               w.counter + 1, prof, d_status, st);
+}
+
+sparsp_status_t sparsp_norm_fwd(const sparsp_shape_t* shape, uint32_t flags, const void* x, int64_t x_stride,
+                                const float* w, const float* b, float eps, void* y, float* mean, float* rstd,
+                                sparsp_stream_t stream) {
+  Dims s;
+  sparsp_status_t r = check_norm(shape, flags, &s);
+  if (r != SPARSP_OK) return r;
+  if (!(eps >= 0.f) || isinf(eps)) return SPARSP_ERR_INVALID_ARG;
+  CHECK_PTR(x);
+  CHECK_PTR(y);
+  CHECK_OPT_PTR(w);
+  CHECK_OPT_PTR(b);
+  CHECK_OPT_PTR(mean);
+  CHECK_OPT_PTR(rstd);
+  r = check_stride(s, &x_stride);
+  if (r != SPARSP_OK) return r;
+  if (overlap(s, x, x_stride, y, (int64_t)s.H * s.d)) return SPARSP_ERR_INVALID_ARG;
+  return launch_norm_fwd(s, (flags & SPARSP_NORM_HEAD) != 0, (flags & SPARSP_NORM_RMS) != 0, x, x_stride, w, b, eps, y,
+                         mean, rstd, (cudaStream_t)stream);
+}
+
+size_t sparsp_norm_workspace_size(const sparsp_shape_t* shape, uint32_t flags) {
+  Dims s;
+  if (check_norm(shape, flags, &s) != SPARSP_OK) return 0;
+  return norm_ws(s, (flags & SPARSP_NORM_HEAD) != 0);
+}
+
+sparsp_status_t sparsp_norm_bwd(const sparsp_shape_t* shape, uint32_t flags, const void* dy, const void* x,
+                                int64_t x_stride, const float* w, const float* mean, const float* rstd, void* dx,
+                                int64_t dx_stride, float* dw, float* db, void* ws, size_t ws_bytes,
+                                sparsp_stream_t stream) {
+  Dims s;
+  sparsp_status_t r = check_norm(shape, flags, &s);
+  if (r != SPARSP_OK) return r;
+  const bool head = (flags & SPARSP_NORM_HEAD) != 0, rms = (flags & SPARSP_NORM_RMS) != 0;
+  CHECK_PTR(dy);
+  CHECK_PTR(x);
+  CHECK_OPT_PTR(w);
+  if (!rms) CHECK_PTR(mean);
+  CHECK_PTR(rstd);
+  CHECK_PTR(dx);
+  CHECK_OPT_PTR(dw);
+  CHECK_OPT_PTR(db);
+  r = check_stride(s, &x_stride);
+  if (r != SPARSP_OK) return r;
+  r = check_stride(s, &dx_stride);
+  if (r != SPARSP_OK) return r;
+  if (overlap(s, x, x_stride, dx, dx_stride) || overlap(s, dy, (int64_t)s.H * s.d, dx, dx_stride))
+    return SPARSP_ERR_INVALID_ARG;
+  if (dw != nullptr || db != nullptr) {
+    CHECK_PTR(ws);
+    if (ws_bytes < norm_ws(s, head)) return SPARSP_ERR_WORKSPACE;
+  }
+  return launch_norm_bwd(s, head, rms, dy, x, x_stride, w, mean, rstd, dx, dx_stride, dw, db, ws,
+                         (cudaStream_t)stream);
+}
+
+size_t sparsp_rope_table_size(const sparsp_rope_t* rope) {
+  if (check_rope(rope) != SPARSP_OK) return 0;
+  return (size_t)rope_table_entries(*rope) * 2 * sizeof(float);
+}
+
+sparsp_status_t sparsp_rope_table(const sparsp_rope_t* rope, double theta, const double offset[3],
+                                  const double scale[3], float* table, size_t table_bytes, sparsp_stream_t stream) {
+  sparsp_status_t r = check_rope(rope);
+  if (r != SPARSP_OK) return r;
+  if (!(theta > 0.0) || isinf(theta) || offset == nullptr || scale == nullptr) return SPARSP_ERR_INVALID_ARG;
+  for (int ax = 0; ax < 3; ++ax)
+    if (!isfinite(offset[ax]) || !isfinite(scale[ax])) return SPARSP_ERR_INVALID_ARG;
+  CHECK_PTR(table);
+  if (table_bytes < (size_t)rope_table_entries(*rope) * 2 * sizeof(float)) return SPARSP_ERR_WORKSPACE;
+  return launch_rope_table(*rope, theta, offset, scale, table, (cudaStream_t)stream);
+}
+
+sparsp_status_t sparsp_rope(const sparsp_shape_t* shape, const sparsp_rope_t* rope, const float* table,
+                            const int32_t* pos, const void* in, int64_t in_stride, void* out, int64_t out_stride,
+                            uint32_t flags, float* means, int32_t* d_status, sparsp_stream_t stream) {
+  Dims s;
+  sparsp_status_t r = check_shape(shape, &s);
+  if (r != SPARSP_OK) return r;
+  r = check_rope(rope);
+  if (r != SPARSP_OK) return r;
+  if (flags & ~(SPARSP_ROPE_INVERSE | SPARSP_ROPE_IN_BLOCKED | SPARSP_ROPE_OUT_BLOCKED)) return SPARSP_ERR_INVALID_ARG;
+  const int turned = rope->cols[0] + rope->cols[1] + rope->cols[2];
+  if (turned > s.d || (rope->half && turned != s.d)) return SPARSP_ERR_SHAPE;
+  const int grid[3] = {s.T, s.Y, s.X};
+  if (pos == nullptr)
+    for (int ax = 0; ax < 3; ++ax)
+      if (rope->cols[ax] > 0 && rope->extent[ax] < grid[ax]) return SPARSP_ERR_SHAPE;
+  CHECK_PTR(table);
+  CHECK_OPT_PTR(pos);
+  CHECK_PTR(in);
+  CHECK_PTR(out);
+  CHECK_OPT_PTR(means);
+  CHECK_OPT_PTR(d_status);
+  const bool in_blocked = (flags & SPARSP_ROPE_IN_BLOCKED) != 0, out_blocked = (flags & SPARSP_ROPE_OUT_BLOCKED) != 0;
+  if (in_blocked) in_stride = 0;
+  if (out_blocked) out_stride = 0;
+  r = check_stride(s, &in_stride);
+  if (r != SPARSP_OK) return r;
+  r = check_stride(s, &out_stride);
+  if (r != SPARSP_OK) return r;
+  if (overlap(s, in, in_stride, out, out_stride)) return SPARSP_ERR_INVALID_ARG;
+  return launch_rope(s, *rope, table, pos, in, in_stride, in_blocked, out, out_stride, out_blocked,
+                     (flags & SPARSP_ROPE_INVERSE) != 0, means, d_status, (cudaStream_t)stream);
 }
 
 }  // extern "C"

@@ -153,6 +153,23 @@ sparsp_status_t launch_predictor_fit(const Dims& s, int rank, const float* qm, c
                                      float* wk, float lr, float* loss, float* gwq, float* gwk, void* ws,
                                      cudaStream_t st);
 
+// Token norm (rows of H*d values, or of d with `head`); strides are elements
+// between tokens.
+size_t norm_ws(const Dims& s, bool head);
+sparsp_status_t launch_norm_fwd(const Dims& s, bool head, bool rms, const void* x, int64_t x_stride, const float* w,
+                                const float* b, float eps, void* y, float* mean, float* rstd, cudaStream_t st);
+sparsp_status_t launch_norm_bwd(const Dims& s, bool head, bool rms, const void* dy, const void* x, int64_t x_stride,
+                                const float* w, const float* mean, const float* rstd, void* dx, int64_t dx_stride,
+                                float* dw, float* db, void* ws, cudaStream_t st);
+
+// Rotary positions.
+int64_t rope_table_entries(const sparsp_rope_t& r);   // (cos, sin) pairs
+sparsp_status_t launch_rope_table(const sparsp_rope_t& r, double theta, const double* offset, const double* scale,
+                                  float* table, cudaStream_t st);
+sparsp_status_t launch_rope(const Dims& s, const sparsp_rope_t& r, const float* table, const int32_t* pos,
+                            const void* in, int64_t in_stride, bool in_blocked, void* out, int64_t out_stride,
+                            bool out_blocked, bool inverse, float* means, int32_t* d_status, cudaStream_t st);
+
 size_t lpt_ws(const Dims& s);
 // cmax: the largest item cost the flat order distinguishes (0 = nb).
 sparsp_status_t launch_lpt(const Dims& s, const int32_t* row_ptr, bool flat, int32_t* items,

@@ -466,6 +466,89 @@ SPARSP_API sparsp_status_t sparsp_csr_transpose(const sparsp_shape_t* shape, con
                                      const int32_t* col_idx, int32_t* col_ptr, int32_t* row_idx,
                                      int32_t* d_status, sparsp_stream_t stream);
 
+/*
+ * Token norm of query / key rows (or any activations of that shape), raster
+ * order: layer norm, or RMS norm with SPARSP_NORM_RMS, over the H*d values of a
+ * token, or over the d values of each head with SPARSP_NORM_HEAD. C is the
+ * number of values per row (H*d or d), rows are token-major (B*N, or B*N*H):
+ *   mean = sum x / C (0 with RMS), var = sum (x - mean)^2 / C,
+ *   rstd = 1 / sqrt(var + eps),    y = (x - mean) rstd w + b.
+ * x: [B,N,H,d] of shape->dtype with x_stride elements between tokens (0: H*d;
+ * e.g. 3*H*d for one third of a fused projection), y: contiguous [B,N,H,d].
+ * w, b: float32 [C] or NULL (1 and 0). mean, rstd: float32 [B,N] ([B,N,H] with
+ * HEAD) or NULL; RMS does not write mean. eps >= 0. Statistics and products
+ * are fp32, y is rounded once. Strides are multiples of 16 bytes, at least
+ * H*d. C <= 16384 (else SPARSP_ERR_UNSUPPORTED). y and x must not overlap.
+ */
+enum {
+  SPARSP_NORM_RMS = 1u << 0,
+  SPARSP_NORM_HEAD = 1u << 1
+};
+SPARSP_API sparsp_status_t sparsp_norm_fwd(const sparsp_shape_t* shape, uint32_t flags, const void* x,
+                                           int64_t x_stride, const float* w, const float* b, float eps, void* y,
+                                           float* mean, float* rstd, sparsp_stream_t stream);
+/*
+ * Its backward, from the forward's x, mean (not read with RMS) and rstd:
+ *   xh = (x - mean) rstd, g = dy w,
+ *   dx = rstd (g - mean_C(g) - xh mean_C(g xh))   (without mean_C(g) for RMS),
+ *   dw = sum over rows of dy xh,  db = sum over rows of dy.
+ * dy: contiguous [B,N,H,d]; dx: [B,N,H,d] with dx_stride elements between
+ * tokens (values between its tokens are left as they were); dw, db: float32 [C]
+ * or NULL. dx must not overlap dy or x. ws: at least
+ * sparsp_norm_workspace_size(shape, flags) bytes when dw or db is given.
+ * Sums over rows run in a fixed order: results are bitwise reproducible.
+ */
+SPARSP_API size_t sparsp_norm_workspace_size(const sparsp_shape_t* shape, uint32_t flags);
+SPARSP_API sparsp_status_t sparsp_norm_bwd(const sparsp_shape_t* shape, uint32_t flags, const void* dy,
+                                           const void* x, int64_t x_stride, const float* w, const float* mean,
+                                           const float* rstd, void* dx, int64_t dx_stride, float* dw, float* db,
+                                           void* ws, size_t ws_bytes, sparsp_stream_t stream);
+
+/*
+ * Rotary positions with three axes. Columns are paired (2i, 2i+1), or (i, i+d/2)
+ * when half != 0 (then cols must sum to d); the first cols[0]/2 pairs turn with
+ * the frame, the next cols[1]/2 with the row (height), the next cols[2]/2 with
+ * the column (width) of the token; further pairs do not turn. cols are even and
+ * sum to at most d. Pair i of axis a at position p turns by
+ *   phi = (offset[a] + scale[a] p) theta^(-2i / cols[a]).
+ * sparsp_rope_table writes cos and sin (float32 pairs, from 64-bit angles) for
+ * positions 0 .. extent[a]-1 of each axis, [extent[a], cols[a]/2] axis by axis;
+ * sparsp_rope_table_size() is its size in bytes (0 for a bad description). The
+ * table depends on neither data nor batch and is kept by the caller.
+ */
+typedef struct {
+  int32_t cols[3];    /* columns turned by frame, row, column  */
+  int32_t extent[3];  /* table positions per axis              */
+  int32_t half;       /* pairing: 0 (2i, 2i+1), else (i, i+d/2) */
+} sparsp_rope_t;
+SPARSP_API size_t sparsp_rope_table_size(const sparsp_rope_t* rope);
+SPARSP_API sparsp_status_t sparsp_rope_table(const sparsp_rope_t* rope, double theta, const double offset[3],
+                                             const double scale[3], float* table, size_t table_bytes,
+                                             sparsp_stream_t stream);
+/*
+ * The rotation, in the pass that moves rows between raster and tile order.
+ *   in, out: raster [B,N,H,d] with in_stride / out_stride elements between
+ *            tokens (0: H*d), or blocked [B,H,N,d] with SPARSP_ROPE_IN_BLOCKED /
+ *            SPARSP_ROPE_OUT_BLOCKED (the stride is then not used).
+ *   flags    SPARSP_ROPE_INVERSE turns by -phi: the gradient of the rotation.
+ *   pos      NULL: the token's grid coordinates (extent must cover the grid, else
+ *            SPARSP_ERR_SHAPE); or int32 [B,N,3], raster order, the table position
+ *            per axis (e.g. clips packed into one grid). A position outside
+ *            [0, extent) sets SPARSP_ERR_DATA; that axis' pairs are then not turned.
+ *   means    NULL, or float32 [B,H,nb,d]: the tile means of the turned values before
+ *            rounding, for sparsp_block_scores_pooled.
+ * Products are fp32 and rounded once. in and out must not overlap.
+ */
+enum {
+  SPARSP_ROPE_INVERSE = 1u << 0,
+  SPARSP_ROPE_IN_BLOCKED = 1u << 1,
+  SPARSP_ROPE_OUT_BLOCKED = 1u << 2
+};
+SPARSP_API sparsp_status_t sparsp_rope(const sparsp_shape_t* shape, const sparsp_rope_t* rope, const float* table,
+                                       const int32_t* pos, const void* in, int64_t in_stride, void* out,
+                                       int64_t out_stride, uint32_t flags, float* means, int32_t* d_status,
+                                       sparsp_stream_t stream);
+
 /* Number of SMs of the current device (cached), or -1 on error. */
 SPARSP_API int32_t sparsp_device_sm_count(void);
 
