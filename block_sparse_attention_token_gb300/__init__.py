@@ -31,6 +31,7 @@ BWD_SPLIT_KV = 4
 OUT_RASTER = 8
 IN_RASTER = 16
 GRID_CAP_SHIFT = 16
+MASKED_SCORE = -1.0e30
 NORM_RMS, NORM_HEAD = 1, 2
 ROPE_INVERSE, ROPE_IN_BLOCKED, ROPE_OUT_BLOCKED = 1, 2, 4
 
@@ -126,6 +127,14 @@ _SIG = {
     "sparsp_rope_table_size": (ctypes.c_size_t, [_P]),
     "sparsp_rope_table": (_I32, [_P, ctypes.c_double, _P, _P, _P, ctypes.c_size_t, _P]),
     "sparsp_rope": (_I32, [_P, _P, _P, _P, _P, ctypes.c_int64, _P, ctypes.c_int64, ctypes.c_uint32, _P, _P, _P]),
+    "sparsp_mask_plan_size": (ctypes.c_size_t, [_P]),
+    "sparsp_mask_plan": (_I32, [_P, _P, _P, _P, _P, ctypes.c_size_t, _P]),
+    "sparsp_mask_scores": (_I32, [_P, _P, _P, _P]),
+    "sparsp_attn_masked_workspace_size": (ctypes.c_size_t, [_P, _I32]),
+    "sparsp_attn_masked_fwd": (_I32, [_P, _P, _P, _P, _P, _P, ctypes.c_float, ctypes.c_float, _P, _P, _P, _P,
+                                      ctypes.c_size_t, ctypes.c_uint32, _P, _P, _P]),
+    "sparsp_attn_masked_bwd": (_I32, [_P, _P, _P, _P, _P, _P, _P, _P, _P, ctypes.c_float, ctypes.c_float, _P, _P, _P,
+                                      _P, _P, ctypes.c_size_t, ctypes.c_uint32, _P, _P, _P]),
     "sparsp_diag_umma_tile": (_I32, [_P, _P, _P, _I32, _I32, _I32, _P, _P]),
     "sparsp_diag_wait_timeout": (_I32, [ctypes.c_uint64, _P, _P]),
 }
@@ -615,6 +624,93 @@ def attn_bwd(shape: Shape, q, k, v, o, lse, dout, row_ptr, col_idx, scale: float
         _sref(shape), _ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), _ptr(dout), _ptr(row_ptr),
         _ptr(col_idx), float(scale), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(ws), ws.numel(), int(flags),
         _ptr(prof), _ptr(status), _stream(stream)))
+    return dq, dk, dv
+
+
+@dataclass
+class MaskPlan:
+    """A token mask in tile order with its block ranges (mask_plan), for one shape."""
+    dims: tuple
+    plan: torch.Tensor
+
+
+def _mask_dims(s: Shape) -> tuple:
+    return s.B, s.T, s.Y, s.X, s.ta, s.tb, s.tc
+
+
+def mask_plan(shape: Shape, pos, lo, hi, plan: MaskPlan | None = None, stream=None) -> MaskPlan:
+    """The token mask in which query n sees key m where lo[n] <= pos[m] < hi[n]
+    (int32 [B,N], raster order): documents with pos = lo = number and hi = lo + 1,
+    padding with pos = -1 and lo = hi = 0, frames with pos = frame and
+    hi = max(frame + 1, prefix). It serves every layer and step with that mask."""
+    s, i32 = shape, torch.int32
+    for name, t in (("pos", pos), ("lo", lo), ("hi", hi)):
+        _want(name, t, (s.B, s.N), i32)
+    if plan is None:
+        plan = MaskPlan(_mask_dims(s), _empty(lib().sparsp_mask_plan_size(_sref(s)), pos.device))
+    elif plan.dims != _mask_dims(s):
+        raise ValueError(f"mask_plan: the plan is of shape {plan.dims}, not {_mask_dims(s)}")
+    _check("sparsp_mask_plan", lib().sparsp_mask_plan(_sref(s), _ptr(pos), _ptr(lo), _ptr(hi), _ptr(plan.plan),
+                                                      plan.plan.numel(), _stream(stream)))
+    return plan
+
+
+def _plan_ptr(shape: Shape, mask: MaskPlan | None):
+    if mask is None:
+        return None
+    if mask.dims != _mask_dims(shape):
+        raise ValueError(f"the mask plan is of (B, T, Y, X, ta, tb, tc) {mask.dims}, not {_mask_dims(shape)}")
+    return mask.plan.data_ptr()
+
+
+def mask_scores(shape: Shape, mask: MaskPlan, scores, stream=None) -> torch.Tensor:
+    """scores [B,H,nb,nb] in place: MASKED_SCORE for block pairs that see nothing of each other."""
+    _want("scores", scores, (shape.B, shape.H, shape.nb, shape.nb), torch.float32)
+    _check("sparsp_mask_scores", lib().sparsp_mask_scores(_sref(shape), _plan_ptr(shape, mask), _ptr(scores),
+                                                          _stream(stream)))
+    return scores
+
+
+def attn_masked_workspace_size(shape: Shape, backward: bool = False) -> int:
+    return lib().sparsp_attn_masked_workspace_size(_sref(shape), int(backward))
+
+
+def attn_masked_fwd(shape: Shape, q, k, v, row_ptr, col_idx, scale: float = 0.0, cap: float = 0.0,
+                    mask: MaskPlan | None = None, o=None, lse=None, ws=None, flags: int = 0, prof=None, status=None,
+                    stream=None):
+    """attn_fwd over the keys a token mask lets each query see, with the scores
+    capped to cap * tanh(score / cap) when cap > 0. Returns (O, LSE); a query
+    that sees nothing has O = 0, LSE = -inf."""
+    dev = q.device
+    if o is None:
+        o = torch.empty((shape.B, shape.N, shape.H, shape.d) if flags & OUT_RASTER else
+                        (shape.B, shape.H, shape.N, shape.d), dtype=q.dtype, device=dev)
+    if lse is None:
+        lse = torch.empty((shape.B, shape.H, shape.N), dtype=torch.float32, device=dev)
+    if ws is None:
+        ws = _empty(attn_masked_workspace_size(shape, False), dev)
+    _check("sparsp_attn_masked_fwd", lib().sparsp_attn_masked_fwd(
+        _sref(shape), _ptr(q), _ptr(k), _ptr(v), _ptr(row_ptr), _ptr(col_idx), float(scale), float(cap),
+        _plan_ptr(shape, mask), _ptr(o), _ptr(lse), _ptr(ws), ws.numel(), int(flags), _ptr(prof), _ptr(status),
+        _stream(stream)))
+    return o, lse
+
+
+def attn_masked_bwd(shape: Shape, q, k, v, o, lse, dout, row_ptr, col_idx, scale: float = 0.0, cap: float = 0.0,
+                    mask: MaskPlan | None = None, dq=None, dk=None, dv=None, ws=None, flags: int = 0, prof=None,
+                    status=None, stream=None):
+    """Gradients of attn_masked_fwd, (dQ, dK, dV); layouts as attn_bwd."""
+    dev = q.device
+    dims = (shape.B, shape.N, shape.H, shape.d) if flags & OUT_RASTER else tuple(q.shape)
+    dq = torch.empty(dims, dtype=q.dtype, device=dev) if dq is None else dq
+    dk = torch.empty(dims, dtype=k.dtype, device=dev) if dk is None else dk
+    dv = torch.empty(dims, dtype=v.dtype, device=dev) if dv is None else dv
+    if ws is None:
+        ws = _empty(attn_masked_workspace_size(shape, True), dev)
+    _check("sparsp_attn_masked_bwd", lib().sparsp_attn_masked_bwd(
+        _sref(shape), _ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), _ptr(dout), _ptr(row_ptr), _ptr(col_idx),
+        float(scale), float(cap), _plan_ptr(shape, mask), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(ws), ws.numel(),
+        int(flags), _ptr(prof), _ptr(status), _stream(stream)))
     return dq, dk, dv
 
 

@@ -3,6 +3,7 @@
 #include <math.h>
 
 #include "common.cuh"
+#include "mask.cuh"
 
 using namespace sparsp;
 
@@ -67,10 +68,13 @@ struct AttnWs {
   int32_t* items2;     // [rows] order over CSC columns
   float* delta;        // [B*H*N]
   float* lse2;         // [B*H*N] LSE * log2(e)
+  // token masks only: the CSR of the block pairs that see something
+  int32_t* seen_ptr;   // [rows+1]
+  int32_t* seen_idx;   // [B*H*nb*nb]
   size_t bytes;
 };
 
-AttnWs attn_ws_layout(const Dims& s, bool backward, void* base) {
+AttnWs attn_ws_layout(const Dims& s, bool backward, void* base, bool masked = false) {
   AttnWs w{};
   uint8_t* p = (uint8_t*)base;
   size_t off = 0;
@@ -90,6 +94,10 @@ AttnWs attn_ws_layout(const Dims& s, bool backward, void* base) {
     w.items2 = (int32_t*)take(rows * 4);
     w.delta = (float*)take((size_t)s.B * s.H * s.N * 4);
     w.lse2 = (float*)take((size_t)s.B * s.H * s.N * 4);
+  }
+  if (masked) {
+    w.seen_ptr = (int32_t*)take((rows + 1) * 4);
+    w.seen_idx = (int32_t*)take(rows * (size_t)s.nb * 4);
   }
   w.bytes = off;
   return w;
@@ -129,6 +137,183 @@ sparsp_status_t check_rope(const sparsp_rope_t* r) {
     if (r->cols[ax] < 0 || r->cols[ax] % 2 || r->cols[ax] > 128 || r->extent[ax] < 1) return SPARSP_ERR_SHAPE;
   if (rope_table_entries(*r) > INT32_MAX) return SPARSP_ERR_UNSUPPORTED;
   return SPARSP_OK;
+}
+
+// sparsp_attn_fwd, and sparsp_attn_masked_fwd with `masked`: both validate alike;
+// a masked call without plan and cap is the plain one.
+sparsp_status_t attn_fwd(const sparsp_shape_t* shape, const void* q, const void* k, const void* v,
+                         const int32_t* row_ptr, const int32_t* col_idx, float scale, bool masked, float cap,
+                         const void* plan, void* o, float* lse, void* ws, size_t ws_bytes, uint32_t flags,
+                         uint64_t* prof, int32_t* d_status, sparsp_stream_t stream) {
+  Dims s;
+  sparsp_status_t r = check_shape(shape, &s);
+  if (r != SPARSP_OK) return r;
+  if (isnan(scale) || isinf(scale)) return SPARSP_ERR_INVALID_ARG;
+  if (flags & ~kKnownFlags) return SPARSP_ERR_INVALID_ARG;
+  s.max_ctas = (int)((flags & SPARSP_GRID_CAP_MASK) >> SPARSP_GRID_CAP_SHIFT);
+  CHECK_PTR(q);
+  CHECK_PTR(k);
+  CHECK_PTR(v);
+  CHECK_PTR(row_ptr);
+  CHECK_PTR(col_idx);
+  CHECK_PTR(o);
+  CHECK_PTR(lse);
+  CHECK_PTR(ws);
+  CHECK_OPT_PTR(prof);
+  CHECK_OPT_PTR(d_status);
+  CHECK_OPT_PTR(plan);
+  if (!(cap >= 0.f) || isinf(cap)) return SPARSP_ERR_INVALID_ARG;
+  AttnWs w = attn_ws_layout(s, false, ws, masked);
+  if (ws_bytes < w.bytes) return SPARSP_ERR_WORKSPACE;
+  if (scale <= 0.f) scale = 1.0f / sqrtf((float)s.d);
+  const bool tc = s.dtype != SPARSP_F32 && !(flags & SPARSP_KERNEL_PORTABLE) && attn_fwd_tc_supported(s);
+  const bool raster = (flags & SPARSP_OUT_RASTER) != 0;
+  const bool in_raster = (flags & SPARSP_IN_RASTER) != 0;
+  if ((raster || in_raster) && !tc) return SPARSP_ERR_UNSUPPORTED;   // only the tcgen05 kernel reads or writes raster rows
+  if (masked && !tc) return SPARSP_ERR_UNSUPPORTED;
+  masked = plan != nullptr || cap > 0.f;
+  cudaStream_t st = (cudaStream_t)stream;
+  const MaskView mask = mask_view(s, plan);
+  if (plan != nullptr) {
+    r = launch_mask_csr(s, mask, row_ptr, col_idx, w.seen_ptr, w.seen_idx, d_status, st);
+    if (r != SPARSP_OK) return r;
+    row_ptr = w.seen_ptr;
+    col_idx = w.seen_idx;
+  }
+  const bool flat = (flags & SPARSP_SCHED_FLAT) != 0;
+  if (tc && attn_fwd_tc_items_per_head(s) != s.nb) {
+    // the tcgen05 kernel's items are pairs of query blocks: order the pairs,
+    // each costing the sum of its two rows
+    r = launch_pair_ptr(s, row_ptr, w.pair_ptr, st);
+    if (r != SPARSP_OK) return r;
+    Dims sp = s;
+    sp.nb = attn_fwd_tc_items_per_head(s);
+    r = launch_lpt(sp, w.pair_ptr, flat, w.items, w.counter, w.hist, st, 2 * s.nb);
+  } else {
+    r = launch_lpt(s, row_ptr, flat, w.items, w.counter, w.hist, st);
+  }
+  if (r != SPARSP_OK) return r;
+  if (s.dtype == SPARSP_F32)
+    return launch_attn_fwd_f32(s, (const float*)q, (const float*)k, (const float*)v, row_ptr,
+                               col_idx, scale, (float*)o, lse, w.items, w.counter, prof, d_status,
+                               st);
+  if (masked)
+    return launch_attn_fwd_masked(s, (const __nv_bfloat16*)q, (const __nv_bfloat16*)k, (const __nv_bfloat16*)v,
+                                  row_ptr, col_idx, scale, cap, mask, (__nv_bfloat16*)o, lse, raster, in_raster,
+                                  w.items, w.counter, prof, d_status, st);
+  if (tc)
+    return launch_attn_fwd_tc(s, (const __nv_bfloat16*)q, (const __nv_bfloat16*)k,
+                              (const __nv_bfloat16*)v, row_ptr, col_idx, scale,
+                              (__nv_bfloat16*)o, lse, raster, in_raster, w.items, w.counter, prof, d_status, st);
+  return launch_attn_fwd_mma(s, (const __nv_bfloat16*)q, (const __nv_bfloat16*)k,
+                             (const __nv_bfloat16*)v, row_ptr, col_idx, scale, (__nv_bfloat16*)o,
+                             lse, w.items, w.counter, prof, d_status, st);
+}
+
+// sparsp_attn_bwd, and sparsp_attn_masked_bwd with `masked`.
+sparsp_status_t attn_bwd(const sparsp_shape_t* shape, const void* q, const void* k, const void* v, const void* o,
+                         const float* lse, const void* dout, const int32_t* row_ptr, const int32_t* col_idx,
+                         float scale, bool masked, float cap, const void* plan, void* dq, void* dk, void* dv, void* ws,
+                         size_t ws_bytes, uint32_t flags, uint64_t* prof, int32_t* d_status, sparsp_stream_t stream) {
+  Dims s;
+  sparsp_status_t r = check_shape(shape, &s);
+  if (r != SPARSP_OK) return r;
+  if (s.dtype != SPARSP_BF16) return SPARSP_ERR_UNSUPPORTED;
+  if (isnan(scale) || isinf(scale)) return SPARSP_ERR_INVALID_ARG;
+  if (flags & ~kKnownFlags) return SPARSP_ERR_INVALID_ARG;
+  if (flags & SPARSP_IN_RASTER) return SPARSP_ERR_UNSUPPORTED;   // the backward reads block-ordered tiles
+  s.max_ctas = (int)((flags & SPARSP_GRID_CAP_MASK) >> SPARSP_GRID_CAP_SHIFT);
+  CHECK_PTR(q);
+  CHECK_PTR(k);
+  CHECK_PTR(v);
+  CHECK_PTR(o);
+  CHECK_PTR(lse);
+  CHECK_PTR(dout);
+  CHECK_PTR(row_ptr);
+  CHECK_PTR(col_idx);
+  CHECK_PTR(dq);
+  CHECK_PTR(dk);
+  CHECK_PTR(dv);
+  CHECK_PTR(ws);
+  CHECK_OPT_PTR(prof);
+  CHECK_OPT_PTR(d_status);
+  CHECK_OPT_PTR(plan);
+  if (!(cap >= 0.f) || isinf(cap)) return SPARSP_ERR_INVALID_ARG;
+  AttnWs w = attn_ws_layout(s, true, ws, masked);
+  if (ws_bytes < w.bytes) return SPARSP_ERR_WORKSPACE;
+  if (scale <= 0.f) scale = 1.0f / sqrtf((float)s.d);
+  cudaStream_t st = (cudaStream_t)stream;
+  const bool flat = (flags & SPARSP_SCHED_FLAT) != 0;
+  typedef const __nv_bfloat16* cb;
+  const bool tc = !(flags & SPARSP_KERNEL_PORTABLE) && attn_bwd_tc_supported(s);
+  const bool raster = (flags & SPARSP_OUT_RASTER) != 0;
+  if (raster && !tc) return SPARSP_ERR_UNSUPPORTED;   // only the tcgen05 kernels write raster rows
+  if (masked && !tc) return SPARSP_ERR_UNSUPPORTED;
+  masked = plan != nullptr || cap > 0.f;
+  const MaskView mask = mask_view(s, plan);
+  if (plan != nullptr) {
+    r = launch_mask_csr(s, mask, row_ptr, col_idx, w.seen_ptr, w.seen_idx, d_status, st);
+    if (r != SPARSP_OK) return r;
+    row_ptr = w.seen_ptr;
+    col_idx = w.seen_idx;
+  }
+  r = launch_bwd_rowdot(s, (cb)o, (cb)dout, w.delta, lse, tc ? w.lse2 : nullptr, raster, st);
+  if (r != SPARSP_OK) return r;
+  r = launch_csr_transpose(s, row_ptr, col_idx, w.col_ptr, w.row_idx, d_status, st);
+  if (r != SPARSP_OK) return r;
+  // the tcgen05 kernels' items with 64-token blocks are pairs of blocks, each
+  // costing the sum of its two lists (CSR rows for dQ, CSC columns for dK/dV)
+  const bool pairs = tc && attn_bwd_tc_items_per_head(s) != s.nb;
+  Dims sp = s;
+  sp.nb = pairs ? attn_bwd_tc_items_per_head(s) : s.nb;
+  if (pairs) {
+    r = launch_pair_ptr(s, row_ptr, w.pair_ptr, st);
+    if (r != SPARSP_OK) return r;
+    r = launch_lpt(sp, w.pair_ptr, flat, w.items, w.counter, w.hist, st, 2 * s.nb);
+  } else {
+    r = launch_lpt(s, row_ptr, flat, w.items, w.counter, w.hist, st);
+  }
+  if (r != SPARSP_OK) return r;
+  if (tc) {
+    r = masked ? launch_attn_bwd_masked(s, 0, (cb)q, (cb)k, (cb)v, (cb)dout, w.lse2, w.delta, row_ptr, col_idx, scale,
+                                        (__nv_bfloat16*)dq, nullptr, w.items, w.counter, prof, d_status, raster, mask,
+                                        cap, st)
+               : launch_attn_bwd_tc(s, 0, (cb)q, (cb)k, (cb)v, (cb)dout, w.lse2, w.delta, row_ptr, col_idx, scale,
+                                    (__nv_bfloat16*)dq, nullptr, w.items, w.counter, prof, d_status, raster, st);
+    if (r != SPARSP_OK) return r;
+    if (pairs) {   // pair_ptr is free again: the dQ kernel reads only its item list
+      r = launch_pair_ptr(s, w.col_ptr, w.pair_ptr, st);
+      if (r != SPARSP_OK) return r;
+      r = launch_lpt(sp, w.pair_ptr, flat, w.items2, w.counter + 1, w.hist, st, 2 * s.nb);
+    } else {
+      r = launch_lpt(s, w.col_ptr, flat, w.items2, w.counter + 1, w.hist, st);
+    }
+    if (r != SPARSP_OK) return r;
+    if (masked)
+      return launch_attn_bwd_masked(s, 3, (cb)q, (cb)k, (cb)v, (cb)dout, w.lse2, w.delta, w.col_ptr, w.row_idx, scale,
+                                    (__nv_bfloat16*)dk, (__nv_bfloat16*)dv, w.items2, w.counter + 1, prof, d_status,
+                                    raster, mask, cap, st);
+    if (!(flags & SPARSP_BWD_SPLIT_KV))
+      return launch_attn_bwd_tc(s, 3, (cb)q, (cb)k, (cb)v, (cb)dout, w.lse2, w.delta, w.col_ptr, w.row_idx,
+                                scale, (__nv_bfloat16*)dk, (__nv_bfloat16*)dv, w.items2, w.counter + 1, prof,
+                                d_status, raster, st);
+    r = launch_attn_bwd_tc(s, 1, (cb)q, (cb)k, (cb)v, (cb)dout, w.lse2, w.delta, w.col_ptr, w.row_idx,
+                           scale, (__nv_bfloat16*)dk, nullptr, w.items2, w.counter + 1, prof, d_status, raster,
+                           st);
+    if (r != SPARSP_OK) return r;
+    if (cudaMemsetAsync(w.counter + 2, 0, sizeof(int32_t), st) != cudaSuccess) return SPARSP_ERR_CUDA;
+    return launch_attn_bwd_tc(s, 2, (cb)q, (cb)k, (cb)v, (cb)dout, w.lse2, w.delta, w.col_ptr, w.row_idx,
+                              scale, (__nv_bfloat16*)dv, nullptr, w.items2, w.counter + 2, prof, d_status, raster,
+                              st);
+  }
+  r = launch_attn_bwd_dq(s, (cb)q, (cb)k, (cb)v, (cb)dout, lse, w.delta, row_ptr, col_idx, scale,
+                         (__nv_bfloat16*)dq, w.items, w.counter, prof, d_status, st);
+  if (r != SPARSP_OK) return r;
+  r = launch_lpt(s, w.col_ptr, flat, w.items2, w.counter + 1, w.hist, st);
+  if (r != SPARSP_OK) return r;
+  return launch_attn_bwd_dkdv(s, (cb)q, (cb)k, (cb)v, (cb)dout, lse, w.delta, w.col_ptr,
+                              w.row_idx, scale, (__nv_bfloat16*)dk, (__nv_bfloat16*)dv, w.items2,
+                              w.counter + 1, prof, d_status, st);
 }
 
 }  // namespace
@@ -502,54 +687,8 @@ sparsp_status_t sparsp_attn_fwd(const sparsp_shape_t* shape, const void* q, cons
                                 float scale, void* o, float* lse, void* ws, size_t ws_bytes,
                                 uint32_t flags, uint64_t* prof, int32_t* d_status,
                                 sparsp_stream_t stream) {
-  Dims s;
-  sparsp_status_t r = check_shape(shape, &s);
-  if (r != SPARSP_OK) return r;
-  if (isnan(scale) || isinf(scale)) return SPARSP_ERR_INVALID_ARG;
-  if (flags & ~kKnownFlags) return SPARSP_ERR_INVALID_ARG;
-  s.max_ctas = (int)((flags & SPARSP_GRID_CAP_MASK) >> SPARSP_GRID_CAP_SHIFT);
-  CHECK_PTR(q);
-  CHECK_PTR(k);
-  CHECK_PTR(v);
-  CHECK_PTR(row_ptr);
-  CHECK_PTR(col_idx);
-  CHECK_PTR(o);
-  CHECK_PTR(lse);
-  CHECK_PTR(ws);
-  CHECK_OPT_PTR(prof);
-  CHECK_OPT_PTR(d_status);
-  AttnWs w = attn_ws_layout(s, false, ws);
-  if (ws_bytes < w.bytes) return SPARSP_ERR_WORKSPACE;
-  if (scale <= 0.f) scale = 1.0f / sqrtf((float)s.d);
-  const bool tc = s.dtype != SPARSP_F32 && !(flags & SPARSP_KERNEL_PORTABLE) && attn_fwd_tc_supported(s);
-  const bool raster = (flags & SPARSP_OUT_RASTER) != 0;
-  const bool in_raster = (flags & SPARSP_IN_RASTER) != 0;
-  if ((raster || in_raster) && !tc) return SPARSP_ERR_UNSUPPORTED;   // only the tcgen05 kernel reads or writes raster rows
-  cudaStream_t st = (cudaStream_t)stream;
-  const bool flat = (flags & SPARSP_SCHED_FLAT) != 0;
-  if (tc && attn_fwd_tc_items_per_head(s) != s.nb) {
-    // the tcgen05 kernel's items are pairs of query blocks: order the pairs,
-    // each costing the sum of its two rows
-    r = launch_pair_ptr(s, row_ptr, w.pair_ptr, st);
-    if (r != SPARSP_OK) return r;
-    Dims sp = s;
-    sp.nb = attn_fwd_tc_items_per_head(s);
-    r = launch_lpt(sp, w.pair_ptr, flat, w.items, w.counter, w.hist, st, 2 * s.nb);
-  } else {
-    r = launch_lpt(s, row_ptr, flat, w.items, w.counter, w.hist, st);
-  }
-  if (r != SPARSP_OK) return r;
-  if (s.dtype == SPARSP_F32)
-    return launch_attn_fwd_f32(s, (const float*)q, (const float*)k, (const float*)v, row_ptr,
-                               col_idx, scale, (float*)o, lse, w.items, w.counter, prof, d_status,
-                               st);
-  if (tc)
-    return launch_attn_fwd_tc(s, (const __nv_bfloat16*)q, (const __nv_bfloat16*)k,
-                              (const __nv_bfloat16*)v, row_ptr, col_idx, scale,
-                              (__nv_bfloat16*)o, lse, raster, in_raster, w.items, w.counter, prof, d_status, st);
-  return launch_attn_fwd_mma(s, (const __nv_bfloat16*)q, (const __nv_bfloat16*)k,
-                             (const __nv_bfloat16*)v, row_ptr, col_idx, scale, (__nv_bfloat16*)o,
-                             lse, w.items, w.counter, prof, d_status, st);
+  return attn_fwd(shape, q, k, v, row_ptr, col_idx, scale, false, 0.f, nullptr, o, lse, ws, ws_bytes, flags, prof,
+                  d_status, stream);
 }
 
 sparsp_status_t sparsp_attn_bwd(const sparsp_shape_t* shape, const void* q, const void* k,
@@ -558,87 +697,60 @@ sparsp_status_t sparsp_attn_bwd(const sparsp_shape_t* shape, const void* q, cons
                                 void* dq, void* dk, void* dv, void* ws, size_t ws_bytes,
                                 uint32_t flags, uint64_t* prof, int32_t* d_status,
                                 sparsp_stream_t stream) {
+  return attn_bwd(shape, q, k, v, o, lse, dout, row_ptr, col_idx, scale, false, 0.f, nullptr, dq, dk, dv, ws, ws_bytes,
+                  flags, prof, d_status, stream);
+}
+
+size_t sparsp_mask_plan_size(const sparsp_shape_t* shape) {
+  Dims s;
+  if (check_shape(shape, &s) != SPARSP_OK) return 0;
+  return mask_plan_layout(s).bytes;
+}
+
+sparsp_status_t sparsp_mask_plan(const sparsp_shape_t* shape, const int32_t* pos, const int32_t* lo, const int32_t* hi,
+                                 void* plan, size_t plan_bytes, sparsp_stream_t stream) {
   Dims s;
   sparsp_status_t r = check_shape(shape, &s);
   if (r != SPARSP_OK) return r;
-  if (s.dtype != SPARSP_BF16) return SPARSP_ERR_UNSUPPORTED;
-  if (isnan(scale) || isinf(scale)) return SPARSP_ERR_INVALID_ARG;
-  if (flags & ~kKnownFlags) return SPARSP_ERR_INVALID_ARG;
-  if (flags & SPARSP_IN_RASTER) return SPARSP_ERR_UNSUPPORTED;   // the backward reads block-ordered tiles
-  s.max_ctas = (int)((flags & SPARSP_GRID_CAP_MASK) >> SPARSP_GRID_CAP_SHIFT);
-  CHECK_PTR(q);
-  CHECK_PTR(k);
-  CHECK_PTR(v);
-  CHECK_PTR(o);
-  CHECK_PTR(lse);
-  CHECK_PTR(dout);
-  CHECK_PTR(row_ptr);
-  CHECK_PTR(col_idx);
-  CHECK_PTR(dq);
-  CHECK_PTR(dk);
-  CHECK_PTR(dv);
-  CHECK_PTR(ws);
-  CHECK_OPT_PTR(prof);
-  CHECK_OPT_PTR(d_status);
-  AttnWs w = attn_ws_layout(s, true, ws);
-  if (ws_bytes < w.bytes) return SPARSP_ERR_WORKSPACE;
-  if (scale <= 0.f) scale = 1.0f / sqrtf((float)s.d);
-  cudaStream_t st = (cudaStream_t)stream;
-  const bool flat = (flags & SPARSP_SCHED_FLAT) != 0;
-  typedef const __nv_bfloat16* cb;
-  const bool tc = !(flags & SPARSP_KERNEL_PORTABLE) && attn_bwd_tc_supported(s);
-  const bool raster = (flags & SPARSP_OUT_RASTER) != 0;
-  if (raster && !tc) return SPARSP_ERR_UNSUPPORTED;   // only the tcgen05 kernels write raster rows
-  r = launch_bwd_rowdot(s, (cb)o, (cb)dout, w.delta, lse, tc ? w.lse2 : nullptr, raster, st);
+  CHECK_PTR(pos);
+  CHECK_PTR(lo);
+  CHECK_PTR(hi);
+  CHECK_PTR(plan);
+  if (plan_bytes < mask_plan_layout(s).bytes) return SPARSP_ERR_WORKSPACE;
+  return launch_mask_plan(s, pos, lo, hi, plan, (cudaStream_t)stream);
+}
+
+sparsp_status_t sparsp_mask_scores(const sparsp_shape_t* shape, const void* plan, float* scores,
+                                   sparsp_stream_t stream) {
+  Dims s;
+  sparsp_status_t r = check_shape(shape, &s);
   if (r != SPARSP_OK) return r;
-  r = launch_csr_transpose(s, row_ptr, col_idx, w.col_ptr, w.row_idx, d_status, st);
-  if (r != SPARSP_OK) return r;
-  // the tcgen05 kernels' items with 64-token blocks are pairs of blocks, each
-  // costing the sum of its two lists (CSR rows for dQ, CSC columns for dK/dV)
-  const bool pairs = tc && attn_bwd_tc_items_per_head(s) != s.nb;
-  Dims sp = s;
-  sp.nb = pairs ? attn_bwd_tc_items_per_head(s) : s.nb;
-  if (pairs) {
-    r = launch_pair_ptr(s, row_ptr, w.pair_ptr, st);
-    if (r != SPARSP_OK) return r;
-    r = launch_lpt(sp, w.pair_ptr, flat, w.items, w.counter, w.hist, st, 2 * s.nb);
-  } else {
-    r = launch_lpt(s, row_ptr, flat, w.items, w.counter, w.hist, st);
-  }
-  if (r != SPARSP_OK) return r;
-  if (tc) {
-    r = launch_attn_bwd_tc(s, 0, (cb)q, (cb)k, (cb)v, (cb)dout, w.lse2, w.delta, row_ptr, col_idx, scale,
-                           (__nv_bfloat16*)dq, nullptr, w.items, w.counter, prof, d_status, raster, st);
-    if (r != SPARSP_OK) return r;
-    if (pairs) {   // pair_ptr is free again: the dQ kernel reads only its item list
-      r = launch_pair_ptr(s, w.col_ptr, w.pair_ptr, st);
-      if (r != SPARSP_OK) return r;
-      r = launch_lpt(sp, w.pair_ptr, flat, w.items2, w.counter + 1, w.hist, st, 2 * s.nb);
-    } else {
-      r = launch_lpt(s, w.col_ptr, flat, w.items2, w.counter + 1, w.hist, st);
-    }
-    if (r != SPARSP_OK) return r;
-    if (!(flags & SPARSP_BWD_SPLIT_KV))
-      return launch_attn_bwd_tc(s, 3, (cb)q, (cb)k, (cb)v, (cb)dout, w.lse2, w.delta, w.col_ptr, w.row_idx,
-                                scale, (__nv_bfloat16*)dk, (__nv_bfloat16*)dv, w.items2, w.counter + 1, prof,
-                                d_status, raster, st);
-    r = launch_attn_bwd_tc(s, 1, (cb)q, (cb)k, (cb)v, (cb)dout, w.lse2, w.delta, w.col_ptr, w.row_idx,
-                           scale, (__nv_bfloat16*)dk, nullptr, w.items2, w.counter + 1, prof, d_status, raster,
-                           st);
-    if (r != SPARSP_OK) return r;
-    if (cudaMemsetAsync(w.counter + 2, 0, sizeof(int32_t), st) != cudaSuccess) return SPARSP_ERR_CUDA;
-    return launch_attn_bwd_tc(s, 2, (cb)q, (cb)k, (cb)v, (cb)dout, w.lse2, w.delta, w.col_ptr, w.row_idx,
-                              scale, (__nv_bfloat16*)dv, nullptr, w.items2, w.counter + 2, prof, d_status, raster,
-                              st);
-  }
-  r = launch_attn_bwd_dq(s, (cb)q, (cb)k, (cb)v, (cb)dout, lse, w.delta, row_ptr, col_idx, scale,
-                         (__nv_bfloat16*)dq, w.items, w.counter, prof, d_status, st);
-  if (r != SPARSP_OK) return r;
-  r = launch_lpt(s, w.col_ptr, flat, w.items2, w.counter + 1, w.hist, st);
-  if (r != SPARSP_OK) return r;
-  return launch_attn_bwd_dkdv(s, (cb)q, (cb)k, (cb)v, (cb)dout, lse, w.delta, w.col_ptr,
-                              w.row_idx, scale, (__nv_bfloat16*)dk, (__nv_bfloat16*)dv, w.items2,
-                              w.counter + 1, prof, d_status, st);
+  CHECK_PTR(plan);
+  CHECK_PTR(scores);
+  return launch_mask_scores(s, mask_view(s, plan), scores, (cudaStream_t)stream);
+}
+
+size_t sparsp_attn_masked_workspace_size(const sparsp_shape_t* shape, int32_t backward) {
+  Dims s;
+  if (check_shape(shape, &s) != SPARSP_OK) return 0;
+  return attn_ws_layout(s, backward != 0, nullptr, true).bytes;
+}
+
+sparsp_status_t sparsp_attn_masked_fwd(const sparsp_shape_t* shape, const void* q, const void* k, const void* v,
+                                       const int32_t* row_ptr, const int32_t* col_idx, float scale, float cap,
+                                       const void* plan, void* o, float* lse, void* ws, size_t ws_bytes,
+                                       uint32_t flags, uint64_t* prof, int32_t* d_status, sparsp_stream_t stream) {
+  return attn_fwd(shape, q, k, v, row_ptr, col_idx, scale, true, cap, plan, o, lse, ws, ws_bytes, flags, prof, d_status,
+                  stream);
+}
+
+sparsp_status_t sparsp_attn_masked_bwd(const sparsp_shape_t* shape, const void* q, const void* k, const void* v,
+                                       const void* o, const float* lse, const void* dout, const int32_t* row_ptr,
+                                       const int32_t* col_idx, float scale, float cap, const void* plan, void* dq,
+                                       void* dk, void* dv, void* ws, size_t ws_bytes, uint32_t flags, uint64_t* prof,
+                                       int32_t* d_status, sparsp_stream_t stream) {
+  return attn_bwd(shape, q, k, v, o, lse, dout, row_ptr, col_idx, scale, true, cap, plan, dq, dk, dv, ws, ws_bytes,
+                  flags, prof, d_status, stream);
 }
 
 sparsp_status_t sparsp_norm_fwd(const sparsp_shape_t* shape, uint32_t flags, const void* x, int64_t x_stride,

@@ -1,0 +1,62 @@
+// Token mask of attention: query n sees key m where lo[n] <= pos[m] < hi[n].
+// A plan holds the three arrays in tile order and the ranges of each block.
+#pragma once
+
+#include "common.cuh"
+
+namespace sparsp {
+
+// A plan's parts (sparsp_mask_plan), or all null: no mask. A query's interval
+// is lo and its length (0 when hi <= lo), so that with unsigned arithmetic
+// "sees" is pos - lo < len for every int32 value.
+struct MaskView {
+  const int32_t* pos;     // [B, N] tile order
+  const int32_t* lo;      // [B, N]
+  const uint32_t* len;    // [B, N]
+  const int2* krange;     // [B, nb] smallest and largest pos of a block
+  const int2* qrange;     // [B, nb] largest lo and smallest hi of a block: what every query sees
+  const int2* qhull;      // [B, nb] smallest lo and largest hi over queries that see anything
+};
+
+// May some query of a block with hull q see some key of a block with range k?
+__device__ __forceinline__ bool blocks_meet(const int2& q, const int2& k) { return k.y >= q.x && k.x < q.y; }
+
+// Byte layout of a plan.
+struct MaskPlan {
+  size_t pos, lo, len, krange, qrange, qhull, bytes;
+};
+inline MaskPlan mask_plan_layout(const Dims& s) {
+  auto up = [](size_t x) { return (x + 255) & ~(size_t)255; };
+  const size_t t = up((size_t)s.B * s.N * 4), r = up((size_t)s.B * s.nb * 8);
+  return MaskPlan{0, t, 2 * t, 3 * t, 3 * t + r, 3 * t + 2 * r, 3 * t + 3 * r};
+}
+inline MaskView mask_view(const Dims& s, const void* plan) {
+  if (plan == nullptr) return MaskView{};
+  const MaskPlan l = mask_plan_layout(s);
+  const uint8_t* p = (const uint8_t*)plan;
+  return MaskView{(const int32_t*)(p + l.pos),   (const int32_t*)(p + l.lo),   (const uint32_t*)(p + l.len),
+                  (const int2*)(p + l.krange), (const int2*)(p + l.qrange), (const int2*)(p + l.qhull)};
+}
+
+sparsp_status_t launch_mask_plan(const Dims& s, const int32_t* pos, const int32_t* lo, const int32_t* hi, void* plan,
+                                 cudaStream_t st);
+sparsp_status_t launch_mask_scores(const Dims& s, const MaskView& m, float* scores, cudaStream_t st);
+// The CSR without the block pairs that see nothing of each other. A malformed
+// row becomes empty and reports SPARSP_ERR_DATA.
+sparsp_status_t launch_mask_csr(const Dims& s, const MaskView& m, const int32_t* row_ptr, const int32_t* col_idx,
+                                int32_t* out_ptr, int32_t* out_idx, int32_t* d_status, cudaStream_t st);
+
+// tcgen05 attention with a token mask (may be empty) and a score cap (0: none).
+sparsp_status_t launch_attn_fwd_masked(const Dims& s, const __nv_bfloat16* q, const __nv_bfloat16* k,
+                                       const __nv_bfloat16* v, const int32_t* row_ptr, const int32_t* col_idx,
+                                       float scale, float cap, const MaskView& mask, __nv_bfloat16* o, float* lse,
+                                       bool raster, bool in_raster, const int32_t* items, int32_t* counter,
+                                       uint64_t* prof, int32_t* d_status, cudaStream_t st);
+sparsp_status_t launch_attn_bwd_masked(const Dims& s, int mode, const __nv_bfloat16* q, const __nv_bfloat16* k,
+                                       const __nv_bfloat16* v, const __nv_bfloat16* dout, const float* lse2,
+                                       const float* delta, const int32_t* ptr, const int32_t* idx, float scale,
+                                       __nv_bfloat16* out, __nv_bfloat16* out2, const int32_t* items,
+                                       int32_t* counter, uint64_t* prof, int32_t* d_status, bool raster,
+                                       const MaskView& mask, float cap, cudaStream_t st);
+
+}  // namespace sparsp

@@ -549,6 +549,70 @@ SPARSP_API sparsp_status_t sparsp_rope(const sparsp_shape_t* shape, const sparsp
                                        int64_t out_stride, uint32_t flags, float* means, int32_t* d_status,
                                        sparsp_stream_t stream);
 
+/*
+ * Token masks. Query token n sees key token m (of its batch element) where
+ *   lo[n] <= pos[m] < hi[n];      hi <= lo: n sees nothing.
+ * pos, lo, hi: int32 [B,N], raster order, any int32 values. Documents: pos = lo
+ * = the document's number, hi = lo + 1; padding: pos = -1, lo = hi = 0; causal
+ * in frames with a prefix: pos = frame, lo = 0, hi = max(frame + 1, prefix).
+ * sparsp_mask_plan writes them in tile order with the ranges of every block
+ * into `plan` (sparsp_mask_plan_size() bytes), which the caller keeps for every
+ * layer and step with that mask.
+ */
+SPARSP_API size_t sparsp_mask_plan_size(const sparsp_shape_t* shape);
+SPARSP_API sparsp_status_t sparsp_mask_plan(const sparsp_shape_t* shape, const int32_t* pos, const int32_t* lo,
+                                            const int32_t* hi, void* plan, size_t plan_bytes,
+                                            sparsp_stream_t stream);
+/*
+ * scores [B,H,nb,nb], in place: SPARSP_MASKED_SCORE for every pair of blocks
+ * whose ranges show that none of its query tokens sees any of its keys, so
+ * that sparsp_select spends its picks on the others (a row whose pairs are all
+ * masked selects as if its scores were equal; attention leaves those blocks
+ * out). Scores at or below SPARSP_MASKED_SCORE should not occur otherwise.
+ */
+#define SPARSP_MASKED_SCORE (-1.0e30f)
+SPARSP_API sparsp_status_t sparsp_mask_scores(const sparsp_shape_t* shape, const void* plan, float* scores,
+                                              sparsp_stream_t stream);
+/*
+ * sparsp_attn_fwd with a token mask and a cap on the scores: over the keys k of
+ * the selected blocks that q sees,
+ *   y = scale q.k, or cap tanh(scale q.k / cap) where cap > 0,
+ *   O_q = sum_k softmax_k(y) v_k,   LSE_q = ln sum_k exp(y).
+ * plan: of sparsp_mask_plan for this shape, or NULL (every key is seen). cap = 0:
+ * no cap. A query that sees no key gives O = 0, LSE = -inf. Block pairs that
+ * see nothing of each other are dropped before the work is ordered. Values in
+ * keys that a query does not see must be finite (their weight is 0, and 0 times
+ * infinity is not). A malformed row (an index outside [0, nb), more than nb
+ * entries) sets SPARSP_ERR_DATA; with a plan it counts as empty, else it is
+ * skipped.
+ * bf16 on the tcgen05 kernels (Bt and d in {64, 128}, nb <= 1024 when Bt = 64
+ * and d = 128); elsewhere, and with SPARSP_KERNEL_PORTABLE,
+ * SPARSP_ERR_UNSUPPORTED. The other options, scale, prof and layouts as in
+ * sparsp_attn_fwd; with neither plan nor cap the two give the same bits.
+ * ws: at least sparsp_attn_masked_workspace_size(shape, 0) bytes.
+ */
+SPARSP_API size_t sparsp_attn_masked_workspace_size(const sparsp_shape_t* shape, int32_t backward);
+SPARSP_API sparsp_status_t sparsp_attn_masked_fwd(const sparsp_shape_t* shape, const void* q, const void* k,
+                                                  const void* v, const int32_t* row_ptr, const int32_t* col_idx,
+                                                  float scale, float cap, const void* plan, void* o, float* lse,
+                                                  void* ws, size_t ws_bytes, uint32_t flags, uint64_t* prof,
+                                                  int32_t* d_status, sparsp_stream_t stream);
+/*
+ * Its backward, as sparsp_attn_bwd, from the forward's o and lse:
+ *   P = exp(y - LSE) on the keys seen, dS = P (dO V^T - D) (1 - tanh^2(scale q.k / cap))
+ * (the last factor with a cap), dQ = scale dS K, dK = scale dS^T Q, dV = P^T dO.
+ * Queries that see nothing and keys that nobody sees get zero gradients; all
+ * values must be finite there too. dK and dV always come from one kernel
+ * (SPARSP_BWD_SPLIT_KV is ignored unless there is neither plan nor cap).
+ * ws: at least sparsp_attn_masked_workspace_size(shape, 1) bytes.
+ */
+SPARSP_API sparsp_status_t sparsp_attn_masked_bwd(const sparsp_shape_t* shape, const void* q, const void* k,
+                                                  const void* v, const void* o, const float* lse, const void* dout,
+                                                  const int32_t* row_ptr, const int32_t* col_idx, float scale,
+                                                  float cap, const void* plan, void* dq, void* dk, void* dv,
+                                                  void* ws, size_t ws_bytes, uint32_t flags, uint64_t* prof,
+                                                  int32_t* d_status, sparsp_stream_t stream);
+
 /* Number of SMs of the current device (cached), or -1 on error. */
 SPARSP_API int32_t sparsp_device_sm_count(void);
 
