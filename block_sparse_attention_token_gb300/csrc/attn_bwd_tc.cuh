@@ -634,15 +634,19 @@ attn_bwd_tc_kernel(const __grid_constant__ CUtensorMap ta1, const __grid_constan
       const float own_l2 = MODE == 0 && exists ? p.lse2[row] : 0.f;
       const float own_d = MODE == 0 && exists ? p.delta[row] : 0.f;
       const uint16_t* mk = reinterpret_cast<const uint16_t*>(masks + ri * (C::kMaskBytes + 16));
-      // MOD: this row's interval (mode 0, a query) or position (mode 3, a key),
-      // and the stage's column blocks with their ranges, fetched a stage ahead
+      // MOD: this row's interval (mode 0, a query) or position (mode 3, a key), the
+      // next stage's column blocks and their ranges (fetched a stage ahead), and
+      // the positions or intervals of this lane's columns where the mask cuts
       uint32_t ilo = 0u, ilen = 0u;
       int ipos = 0;
       int64_t tok0 = 0, blk0 = 0;
-      int j1 = 0, j2 = 0, n1 = 0, n2 = 0;
+      int n1 = 0, n2 = 0;
       int2 cr1 = make_int2(0, 0), cr2 = cr1;
+      int32_t ca[4];
+      uint32_t cb[4];
       int32_t e0 = 0;
-      bool masked = false;
+      bool masked = false, full1 = true, full2 = true;
+      RowGroups groups{};
       UnionWalk walk(bits + ri * 2 * C::MAXW, bits + ri * 2 * C::MAXW + C::MAXW, PAIR && MOD != 0 ? words : 0);
       auto next_blocks = [&](int e) {
         if constexpr (PAIR) {
@@ -660,6 +664,19 @@ attn_bwd_tc_kernel(const __grid_constant__ CUtensorMap ta1, const __grid_constan
       auto inside = [&](const int2& c) {
         return MODE == 0 ? (uint32_t)c.x - ilo < ilen && (uint32_t)c.y - ilo < ilen : c.x <= ipos && ipos < c.y;
       };
+      auto next_cut = [&]() {
+        full1 = __all_sync(0xffffffffu, inside(cr1));
+        full2 = PAIR ? __all_sync(0xffffffffu, inside(cr2)) : full1;
+        if (!full1 || !full2) {
+          const int64_t at[4] = {(int64_t)n1 * BTB, (int64_t)n1 * BTB + 32, (int64_t)n2 * BTB + (PAIR ? 0 : 64),
+                                 (int64_t)n2 * BTB + (PAIR ? 32 : 96)};
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            ca[c] = __ldg((MODE == 0 ? p.mask.pos : p.mask.lo) + tok0 + lane + at[c]);
+            if (MODE != 0) cb[c] = __ldg(p.mask.len + tok0 + lane + at[c]);
+          }
+        }
+      };
       if constexpr (MOD != 0) {
         masked = p.mask.pos != nullptr;
         if (masked) {
@@ -668,22 +685,32 @@ attn_bwd_tc_kernel(const __grid_constant__ CUtensorMap ta1, const __grid_constan
           blk0 = b * nb;
           if (exists) {
             const int64_t at = tok0 + (int64_t)i * BTB + o;
-            ilo = (uint32_t)p.mask.lo[at];
-            ilen = p.mask.len[at];
-            ipos = p.mask.pos[at];
+            if (MODE == 0) {
+              ilo = (uint32_t)__ldg(p.mask.lo + at);
+              ilen = __ldg(p.mask.len + at);
+            } else {
+              ipos = __ldg(p.mask.pos + at);
+            }
           }
+          groups.make(MODE == 0 ? ilo : (uint32_t)ipos, ilen, lane);
           if (!PAIR) e0 = p.ptr[item];
           next_blocks(0);
+          next_cut();
         }
       }
       for (int e = 0; e < len && ok; ++e) {
-        bool full1 = true, full2 = true;
+        // bit c of see[2 h + c / 32]: this row sees column c of half h
+        uint32_t see[4] = {0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu};
+        const bool cut1 = MOD != 0 && !full1, cut2 = MOD != 0 && !full2;
         if constexpr (MOD != 0) {
           if (masked) {
-            full1 = __all_sync(0xffffffffu, inside(cr1));
-            full2 = PAIR ? __all_sync(0xffffffffu, inside(cr2)) : full1;
-            j1 = n1;
-            j2 = n2;
+            if (MODE == 0) {
+              if (cut1) query_bits(groups, ilo, ilen, ca[0], ca[1], lane, see[0], see[1]);
+              if (cut2) query_bits(groups, ilo, ilen, ca[2], ca[3], lane, see[2], see[3]);
+            } else {
+              if (cut1) key_bits(groups, ipos, ca[0], cb[0], ca[1], cb[1], lane, see[0], see[1]);
+              if (cut2) key_bits(groups, ipos, ca[2], cb[2], ca[3], cb[3], lane, see[2], see[3]);
+            }
             if (e + 1 < len) next_blocks(e + 1);
           }
         }
@@ -705,28 +732,9 @@ attn_bwd_tc_kernel(const __grid_constant__ CUtensorMap ta1, const __grid_constan
           // pairs: a row block that did not select this half's block (or does not
           // exist) gets X = 0 there (warp-uniform)
           const bool has = !PAIR || (exists && ((msk >> (8 * h + half)) & 1u));
-          // MOD: the scores of this half that the mask clears, as -inf (before the cap)
-          const bool full = h == 0 ? full1 : full2;
-          if constexpr (MOD != 0) {
-            if (!full && has) {
-              const int64_t col = tok0 + (int64_t)(h == 0 ? j1 : j2) * BTB + (PAIR ? 0 : HB * h);
-              const int4* ca = reinterpret_cast<const int4*>((MODE == 0 ? p.mask.pos : p.mask.lo) + col);
-              const int4* cb = reinterpret_cast<const int4*>(p.mask.len + col);
-#pragma unroll
-              for (int c = 0; c < HB / 4; ++c) {
-                const int4 a4 = __ldg(ca + c);
-                const uint32_t aa[4] = {(uint32_t)a4.x, (uint32_t)a4.y, (uint32_t)a4.z, (uint32_t)a4.w};
-                int4 b4 = make_int4(0, 0, 0, 0);
-                if (MODE != 0) b4 = __ldg(cb + c);
-                const uint32_t bb[4] = {(uint32_t)b4.x, (uint32_t)b4.y, (uint32_t)b4.z, (uint32_t)b4.w};
-#pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                  const bool see = MODE == 0 ? aa[u] - ilo < ilen : (uint32_t)ipos - aa[u] < bb[u];
-                  if (!see) sv[4 * c + u] = 0xff800000u;
-                }
-              }
-            }
-          }
+          // MOD: the columns of this half that the row sees
+          const bool cut = h == 0 ? cut1 : cut2;
+          const uint32_t see0 = h == 0 ? see[0] : see[2], see1 = h == 0 ? see[1] : see[3];
           // P of columns x, x + 1 (and 1 - tanh^2 of the cap) from the scores and LSE*log2e
           auto probs = [&](int x, float la, float lb, float& p0, float& p1, float& t0, float& t1) {
             const float s0 = __uint_as_float(sv[x]), s1 = __uint_as_float(sv[x + 1]);
@@ -741,9 +749,10 @@ attn_bwd_tc_kernel(const __grid_constant__ CUtensorMap ta1, const __grid_constan
             }
             p0 = ex2f(e0_);
             p1 = ex2f(e1_);
-            if (MOD != 0 && !full) {
-              if (s0 == -INFINITY) p0 = 0.f;
-              if (s1 == -INFINITY) p1 = 0.f;
+            if (MOD != 0 && cut) {   // x is a constant of the unrolled loop
+              const uint32_t w = x < 32 ? see0 : see1;
+              if (!((w >> (x & 31)) & 1u)) p0 = 0.f;
+              if (!((w >> ((x + 1) & 31)) & 1u)) p1 = 0.f;
             }
           };
           uint32_t xk[HB / 2];
@@ -821,6 +830,7 @@ attn_bwd_tc_kernel(const __grid_constant__ CUtensorMap ta1, const __grid_constan
           }
           ++hg;
         }
+        if (MOD != 0 && masked && e + 1 < len) next_cut();
         ++c_use;
       }
       if (!ok) break;

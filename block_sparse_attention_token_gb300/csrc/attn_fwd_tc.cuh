@@ -657,14 +657,17 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
           continue;
         }
         const uint32_t* mk = masks + ri * C::kMaskWords;
-        // MOD: this row's interval and the key blocks (j1, j2 of a pair) and
-        // positions of the stage, fetched a stage ahead
+        // MOD: this row's interval, the key blocks of the next stage and their
+        // ranges (fetched a stage ahead), and the positions of this lane's four
+        // columns where the mask cuts the stage
         uint32_t ilo = 0u, ilen = 0u;
         int64_t tok0 = 0, blk0 = 0;      // this batch element's first token and block
-        int j1 = 0, j2 = 0, n1 = 0, n2 = 0;
+        int n1 = 0, n2 = 0;
         int2 kr1 = make_int2(0, 0), kr2 = kr1;
+        int32_t kpos[4];
         int32_t e0 = 0;
-        bool masked = false;
+        bool masked = false, full1 = true, full2 = true;
+        RowGroups groups{};
         UnionWalk walk(bits + ri * 2 * C::MAXW, bits + ri * 2 * C::MAXW + C::MAXW, PAIR && MOD != 0 ? words : 0);
         auto next_blocks = [&](int e) {   // key blocks of stage e
           if constexpr (PAIR) {
@@ -674,6 +677,19 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
           } else {
             n1 = n2 = __ldg(p.col_idx + e0 + e);
           }
+          kr1 = __ldg(p.mask.krange + blk0 + n1);
+          if (PAIR) kr2 = __ldg(p.mask.krange + blk0 + n2);
+        };
+        auto next_cut = [&]() {   // does the mask cut the fetched blocks, and where
+          full1 = __all_sync(0xffffffffu, (uint32_t)kr1.x - ilo < ilen && (uint32_t)kr1.y - ilo < ilen);
+          full2 = PAIR ? __all_sync(0xffffffffu, (uint32_t)kr2.x - ilo < ilen && (uint32_t)kr2.y - ilo < ilen) : full1;
+          if (!full1 || !full2) {
+            const int32_t* kp = p.mask.pos + tok0 + lane;
+            kpos[0] = __ldg(kp + (int64_t)n1 * BT);
+            kpos[1] = __ldg(kp + (int64_t)n1 * BT + 32);
+            kpos[2] = __ldg(kp + (int64_t)n2 * BT + (PAIR ? 0 : 64));
+            kpos[3] = __ldg(kp + (int64_t)n2 * BT + (PAIR ? 32 : 96));
+          }
         };
         if constexpr (MOD != 0) {
           masked = p.mask.pos != nullptr;
@@ -682,31 +698,25 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
             tok0 = b * p.N;
             blk0 = b * nb;
             if (i < nb) {
-              ilo = (uint32_t)p.mask.lo[tok0 + (int64_t)i * BT + o];
-              ilen = p.mask.len[tok0 + (int64_t)i * BT + o];
+              ilo = (uint32_t)__ldg(p.mask.lo + tok0 + (int64_t)i * BT + o);
+              ilen = __ldg(p.mask.len + tok0 + (int64_t)i * BT + o);
             }
+            groups.make(ilo, ilen, lane);
             if (!PAIR) e0 = p.row_ptr[item];
             next_blocks(0);
-            kr1 = p.mask.krange[blk0 + n1];
-            if (PAIR) kr2 = p.mask.krange[blk0 + n2];
+            next_cut();
           }
         }
         float m = -INFINITY, l = 0.f;
         for (int e = 0; e < len; ++e) {
-          bool full1 = true, full2 = true;   // no score of this half is masked in this warp's rows
+          // bit c of see[h]: this row sees column 32 h + c
+          uint32_t see[4] = {0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu};
+          const bool cut1 = MOD != 0 && !full1, cut2 = MOD != 0 && !full2;
           if constexpr (MOD != 0) {
             if (masked) {
-              full1 = (uint32_t)kr1.x - ilo < ilen && (uint32_t)kr1.y - ilo < ilen;
-              full2 = PAIR ? (uint32_t)kr2.x - ilo < ilen && (uint32_t)kr2.y - ilo < ilen : full1;
-              j1 = n1;
-              j2 = n2;
-              if (e + 1 < len) {
-                next_blocks(e + 1);
-                kr1 = p.mask.krange[blk0 + n1];
-                if (PAIR) kr2 = p.mask.krange[blk0 + n2];
-              }
-              full1 = __all_sync(0xffffffffu, full1);
-              full2 = PAIR ? __all_sync(0xffffffffu, full2) : full1;
+              if (cut1) query_bits(groups, ilo, ilen, kpos[0], kpos[1], lane, see[0], see[1]);
+              if (cut2) query_bits(groups, ilo, ilen, kpos[2], kpos[3], lane, see[2], see[3]);
+              if (e + 1 < len) next_blocks(e + 1);
             }
           }
           // which halves of this stage's 128 columns this row attends to (warp-uniform)
@@ -735,26 +745,21 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
           ++s_use;
           if constexpr (MOD != 0) {
             // masked scores become -inf, and the maxima are those of what is left
-            auto mask_half = [&](int hh, int j) {
-              const int4* kp = reinterpret_cast<const int4*>(p.mask.pos + tok0 + (int64_t)j * BT + (PAIR ? 0 : 64 * hh));
-              float m0 = -INFINITY, m1 = -INFINITY;
+            auto mask_half = [&](int hh) {
   #pragma unroll
-              for (int c = 0; c < 16; ++c) {
-                const int4 k4 = __ldg(kp + c);
-                const uint32_t kk[4] = {(uint32_t)k4.x, (uint32_t)k4.y, (uint32_t)k4.z, (uint32_t)k4.w};
+              for (int w = 2 * hh; w < 2 * hh + 2; ++w) {
+                float mw = -INFINITY;
   #pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                  uint32_t& x = s[64 * hh + 4 * c + u];
-                  if (!(kk[u] - ilo < ilen)) x = 0xff800000u;   // -inf
-                  if (u & 1) m1 = fmaxf(m1, __uint_as_float(x));
-                  else m0 = fmaxf(m0, __uint_as_float(x));
+                for (int c = 0; c < 32; c += 2) {
+                  if (!((see[w] >> c) & 1u)) s[32 * w + c] = 0xff800000u;
+                  if (!((see[w] >> (c + 1)) & 1u)) s[32 * w + c + 1] = 0xff800000u;
+                  mw = fmaxf(fmaxf(mw, __uint_as_float(s[32 * w + c])), __uint_as_float(s[32 * w + c + 1]));
                 }
+                cm[w] = mw;
               }
-              cm[2 * hh] = m0;
-              cm[2 * hh + 1] = m1;
             };
-            if (!full1 && has1) mask_half(0, j1);
-            if (!full2 && has2) mask_half(1, j2);
+            if (cut1 && has1) mask_half(0);
+            if (cut2 && has2) mask_half(1);
           }
           if (!has1) cm[0] = cm[1] = -INFINITY;
           if (!has2) cm[2] = cm[3] = -INFINITY;
@@ -803,7 +808,7 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
                 fma_x2(__uint_as_float(s[2 * c]), __uint_as_float(s[2 * c + 1]), sl2, -mr, x0, x1);
                 exp_pair(c, x0, x1);
               }
-            } else if (hh == 0 ? full1 : full2) {
+            } else if (!(hh == 0 ? cut1 : cut2)) {
   #pragma unroll
               for (int c = 32 * hh; c < 32 * hh + 32; ++c) {
                 float x0 = rcpf(1.f + ex2f(__uint_as_float(s[2 * c]) * p.c1));
@@ -850,6 +855,7 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
           wait_st();
           fence_before();
           mbar_arrive(bar(P_FULL + b));
+          if (MOD != 0 && masked && e + 1 < len) next_cut();
           }
         }
         if (PAIR) release();

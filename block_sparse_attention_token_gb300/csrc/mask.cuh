@@ -21,6 +21,49 @@ struct MaskView {
 // May some query of a block with hull q see some key of a block with range k?
 __device__ __forceinline__ bool blocks_meet(const int2& q, const int2& k) { return k.y >= q.x && k.x < q.y; }
 
+// Rows of a warp that see alike. The 32 rows of a warp hold few different
+// intervals (or positions), so the keys each row sees come as bits from one
+// ballot per group and 32 columns, not from a comparison per score.
+struct RowGroups {
+  uint32_t mine;      // the lanes of this lane's group
+  uint32_t leaders;   // one lane of each group
+  __device__ __forceinline__ void make(uint32_t a, uint32_t b, int lane) {
+    mine = __match_any_sync(0xffffffffu, a) & __match_any_sync(0xffffffffu, b);
+    leaders = __ballot_sync(0xffffffffu, __ffs(mine) - 1 == lane);
+  }
+};
+// Rows are queries with interval (lo, len); each lane brings the positions k0,
+// k1 of two columns (lane and 32 + lane): bit c of w0 / w1 = the row sees the column.
+__device__ __forceinline__ void query_bits(const RowGroups& g, uint32_t lo, uint32_t len, int32_t k0, int32_t k1,
+                                           int lane, uint32_t& w0, uint32_t& w1) {
+  w0 = w1 = 0u;
+  for (uint32_t rem = g.leaders; rem != 0u; rem &= rem - 1u) {
+    const int l = __ffs(rem) - 1;
+    const uint32_t a = __shfl_sync(0xffffffffu, lo, l), n = __shfl_sync(0xffffffffu, len, l);
+    const uint32_t b0 = __ballot_sync(0xffffffffu, (uint32_t)k0 - a < n);
+    const uint32_t b1 = __ballot_sync(0xffffffffu, (uint32_t)k1 - a < n);
+    if ((g.mine >> l) & 1u) {
+      w0 = b0;
+      w1 = b1;
+    }
+  }
+}
+// Rows are keys at position pos; each lane brings the intervals of two query columns.
+__device__ __forceinline__ void key_bits(const RowGroups& g, int32_t pos, int32_t lo0, uint32_t len0, int32_t lo1,
+                                         uint32_t len1, int lane, uint32_t& w0, uint32_t& w1) {
+  w0 = w1 = 0u;
+  for (uint32_t rem = g.leaders; rem != 0u; rem &= rem - 1u) {
+    const int l = __ffs(rem) - 1;
+    const uint32_t x = (uint32_t)__shfl_sync(0xffffffffu, pos, l);
+    const uint32_t b0 = __ballot_sync(0xffffffffu, x - (uint32_t)lo0 < len0);
+    const uint32_t b1 = __ballot_sync(0xffffffffu, x - (uint32_t)lo1 < len1);
+    if ((g.mine >> l) & 1u) {
+      w0 = b0;
+      w1 = b1;
+    }
+  }
+}
+
 // Byte layout of a plan.
 struct MaskPlan {
   size_t pos, lo, len, krange, qrange, qhull, bytes;
