@@ -139,6 +139,14 @@ sparsp_status_t check_rope(const sparsp_rope_t* r) {
   return SPARSP_OK;
 }
 
+// A score cap: none, or one whose ratio to the scale fp32 holds well.
+bool cap_ok(float cap, float scale, int d) {
+  if (cap == 0.f) return true;
+  if (!(cap >= 9.5367431640625e-7f && cap <= 1048576.f)) return false;   // 2^-20 .. 2^20
+  const float x = (scale <= 0.f ? 1.0f / sqrtf((float)d) : scale) / cap;
+  return isnormal(x) && isfinite(x * 4.f);
+}
+
 // sparsp_attn_fwd, and sparsp_attn_masked_fwd with `masked`: both validate alike;
 // a masked call without plan and cap is the plain one.
 sparsp_status_t attn_fwd(const sparsp_shape_t* shape, const void* q, const void* k, const void* v,
@@ -162,7 +170,7 @@ sparsp_status_t attn_fwd(const sparsp_shape_t* shape, const void* q, const void*
   CHECK_OPT_PTR(prof);
   CHECK_OPT_PTR(d_status);
   CHECK_OPT_PTR(plan);
-  if (!(cap >= 0.f) || isinf(cap)) return SPARSP_ERR_INVALID_ARG;
+  if (!cap_ok(cap, scale, s.d)) return SPARSP_ERR_INVALID_ARG;
   AttnWs w = attn_ws_layout(s, false, ws, masked);
   if (ws_bytes < w.bytes) return SPARSP_ERR_WORKSPACE;
   if (scale <= 0.f) scale = 1.0f / sqrtf((float)s.d);
@@ -238,7 +246,7 @@ sparsp_status_t attn_bwd(const sparsp_shape_t* shape, const void* q, const void*
   CHECK_OPT_PTR(prof);
   CHECK_OPT_PTR(d_status);
   CHECK_OPT_PTR(plan);
-  if (!(cap >= 0.f) || isinf(cap)) return SPARSP_ERR_INVALID_ARG;
+  if (!cap_ok(cap, scale, s.d)) return SPARSP_ERR_INVALID_ARG;
   AttnWs w = attn_ws_layout(s, true, ws, masked);
   if (ws_bytes < w.bytes) return SPARSP_ERR_WORKSPACE;
   if (scale <= 0.f) scale = 1.0f / sqrtf((float)s.d);

@@ -59,12 +59,14 @@
 // with a second bounded wait and TMEM is released.
 //
 // MOD = 1 adds the forward's token mask and MOD = 2 its score cap beside it
-// (modes 0 and 3): with r = 1 / (1 + exp(2 scale s / cap)) the exponent is
-// cap (1 - 2 r) and dS gains the factor 1 - tanh^2 = 4 r (1 - r). A half block
-// that lies inside the intervals of all 32 rows of a warp costs two comparisons;
-// in the others P is cleared score by score (a query that sees no key has
-// LSE = -inf, and is masked everywhere).
+// (modes 0 and 3): dS gains the factor 1 - tanh^2, and tanh is the forward's
+// (cap.cuh). The producer tells with the item which of its blocks the token mask
+// cuts; there P is cleared by the bits of the columns a row sees (a query that
+// sees no key has LSE = -inf, and is cleared everywhere).
 #pragma once
+#include <type_traits>
+
+#include "cap.cuh"
 #include "mask.cuh"
 #include "pairs.cuh"
 #include "tc_helpers.cuh"
@@ -97,7 +99,7 @@ enum Bar {
 // two blocks per column stage (the two halves); each item slot holds the two
 // lists as bitmaps and one byte per union block saying which of the two rows
 // selected it, so that the row warps mask a half for a row block that did not.
-template <int D_, int BTB_>
+template <int D_, int BTB_, int MOD_ = 0>
 struct BCfg {
   static constexpr int D = D_, BTB = BTB_;
   static constexpr bool PAIR = BTB == 64;
@@ -113,7 +115,10 @@ struct BCfg {
   // pairs: bitmap words of one list (up to 1,024 blocks with d = 128, kMaxBlocks with d = 64)
   static constexpr int MAXW = PAIR ? (D == 64 ? kMaxBlocks / 32 : 32) : 0;
   static constexpr uint32_t kOffBits = kOffRing + 16 * kNI;   // [kNI][2][MAXW]
-  static constexpr uint32_t kMaskBytes = 32 * MAXW;           // per slot: one byte per union block (+1)
+  // per slot: one byte per union block (+1); with MOD and no pairs one bit per
+  // block of the list: does the token mask cut it
+  static constexpr uint32_t kMaskBytes = PAIR ? 32 * MAXW : MOD_ != 0 ? kMaxBlocks / 8 : 0;
+  static constexpr bool HOLD = PAIR || MOD_ != 0;   // the row warps read the masks until the item ends
   static constexpr uint32_t kOffMask = kOffBits + kNI * 2 * MAXW * 4;
   static constexpr uint32_t kOffMisc = kOffMask + kNI * (kMaskBytes + (PAIR ? 16 : 0));
   static constexpr uint32_t kSmemBytes = kOffMisc + 16 + 1024;   // + alignment slack
@@ -132,12 +137,6 @@ __device__ __forceinline__ bool wait_raw(uint32_t bar, uint32_t parity, uint64_t
 __device__ __forceinline__ float ex2f(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
-  return y;
-}
-
-__device__ __forceinline__ float rcpf(float x) {
-  float y;
-  asm("rcp.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
   return y;
 }
 
@@ -168,7 +167,8 @@ struct Params {
   int raster;            // outputs in raster order at rm.row(bh, block, token); else block order
   RasterMap rm;
   MaskView mask;      // MOD != 0; mask.pos null: no mask
-  float c1, cap2;     // MOD == 2: 2 scale log2(e) / cap and cap log2(e)
+  // MOD == 2: 2 scale log2(e) / cap, cap log2(e) and scale / cap
+  float c1, cap2, inv_cap;
 };
 
 template <int MODE, int D, int BTB, int MOD>
@@ -176,7 +176,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 attn_bwd_tc_kernel(const __grid_constant__ CUtensorMap ta1, const __grid_constant__ CUtensorMap ta2,
                    const __grid_constant__ CUtensorMap tb1, const __grid_constant__ CUtensorMap tb2,
                    const Params p) {
-  using C = BCfg<D, BTB>;
+  using C = BCfg<D, BTB, MOD>;
   constexpr bool PAIR = C::PAIR;
   constexpr bool kHasDP = MODE != 2;
   // the item's row tiles as the A operand in TMEM; mode 3 with d = 128 has no
@@ -268,7 +268,23 @@ attn_bwd_tc_kernel(const __grid_constant__ CUtensorMap ta1, const __grid_constan
           if (badbits && lane == 0) report(p.d_status, SPARSP_ERR_DATA);
           const int u = union_count(bmA, bmB, words, lane);
           len = (badbits == 3) ? -1 : (u + 1) / 2;   // stages of two blocks
-          union_masks(bmA, bmB, words, u, lane, masks + ri * (C::kMaskBytes + 16));
+          if constexpr (MOD != 0) {
+            const int64_t blk0 = bh / p.rm.H * nb;
+            const bool masked = p.mask.pos != nullptr;
+            const int2* own = MODE == 0 ? p.mask.qrange : p.mask.krange;
+            const int2* other = MODE == 0 ? p.mask.krange : p.mask.qrange;
+            const int2 ra = masked ? __ldg(own + blk0 + iA) : make_int2(0, 0);
+            const int2 rb = masked && iA + 1 < nb ? __ldg(own + blk0 + iA + 1) : ra;
+            union_codes<true>(bmA, bmB, words, u, lane,
+                              reinterpret_cast<uint32_t*>(masks + ri * (C::kMaskBytes + 16)), [&](int c) -> uint32_t {
+              if (!masked) return 0u;
+              const int2 x = __ldg(other + blk0 + c);
+              return ((MODE == 0 ? all_seen(ra, x) : all_seen(x, ra)) ? 0u : 1u) |
+                     ((MODE == 0 ? all_seen(rb, x) : all_seen(x, rb)) ? 0u : 2u);
+            });
+          } else {
+            union_masks(bmA, bmB, words, u, lane, masks + ri * (C::kMaskBytes + 16));
+          }
         } else {
           const int32_t a = p.ptr[item], b = p.ptr[item + 1];
           bool bad = (b < a) || (b - a > nb);
@@ -283,6 +299,22 @@ attn_bwd_tc_kernel(const __grid_constant__ CUtensorMap ta1, const __grid_constan
             len = -1;
           } else {
             len = b - a;
+            if constexpr (MOD != 0) {
+              const int64_t blk0 = (int64_t)item / nb / p.rm.H * nb;
+              const bool masked = p.mask.pos != nullptr;
+              const int2 own = masked ? __ldg((MODE == 0 ? p.mask.qrange : p.mask.krange) + blk0 + item % nb)
+                                      : make_int2(0, 0);
+              uint32_t* words_ = reinterpret_cast<uint32_t*>(masks + ri * (C::kMaskBytes + 16));
+              for (int32_t e = 0; e < len; e += 32) {
+                bool cut = masked && e + lane < len;
+                if (cut) {
+                  const int2 x = __ldg((MODE == 0 ? p.mask.krange : p.mask.qrange) + blk0 + p.idx[a + e + lane]);
+                  cut = !(MODE == 0 ? all_seen(own, x) : all_seen(x, own));
+                }
+                const uint32_t w = __ballot_sync(0xffffffffu, cut);
+                if (lane == 0) words_[e >> 5] = w;
+              }
+            }
           }
         }
       }
@@ -573,18 +605,18 @@ attn_bwd_tc_kernel(const __grid_constant__ CUtensorMap ta1, const __grid_constan
       if (!(ok = wait_warp(bar(I_FULL + ri), (it_use / kNI) & 1u, g))) break;
       const int4 ent = make_int4(ring[ri].x, ring[ri].y, ring[ri].z, 0);
       __syncwarp();
-      // pairs read the slot's masks until the item ends; release it then
+      // pairs and MOD read the slot's masks until the item ends; release it then
       auto release = [&]() {
         if (lane == 0) mbar_arrive(bar(I_EMPTY + ri));
       };
-      if (!PAIR) release();
+      if (!C::HOLD) release();
       ++it_use;
       if (ent.y == -2) {
-        if (PAIR) release();
+        if (C::HOLD) release();
         break;
       }
       if (ent.y == -1) {
-        if (PAIR) release();
+        if (C::HOLD) release();
         continue;
       }
       const int64_t item = ent.x;
@@ -609,7 +641,7 @@ attn_bwd_tc_kernel(const __grid_constant__ CUtensorMap ta1, const __grid_constan
 #pragma unroll
             for (int c = 0; c < D / 8; ++c) orow2[c] = make_uint4(0, 0, 0, 0);
         }
-        if (PAIR) release();
+        if (C::HOLD) release();
         continue;
       }
       if (kRowsInTmem) {
@@ -634,55 +666,50 @@ attn_bwd_tc_kernel(const __grid_constant__ CUtensorMap ta1, const __grid_constan
       const float own_l2 = MODE == 0 && exists ? p.lse2[row] : 0.f;
       const float own_d = MODE == 0 && exists ? p.delta[row] : 0.f;
       const uint16_t* mk = reinterpret_cast<const uint16_t*>(masks + ri * (C::kMaskBytes + 16));
-      // MOD: this row's interval (mode 0, a query) or position (mode 3, a key), the
-      // next stage's column blocks and their ranges (fetched a stage ahead), and
-      // the positions or intervals of this lane's columns where the mask cuts
+      // MOD: this row's interval (mode 0, a query) or position (mode 3, a key), and
+      // of the next stage which halves the mask cuts and there the positions or
+      // intervals of this lane's columns
       uint32_t ilo = 0u, ilen = 0u;
       int ipos = 0;
-      int64_t tok0 = 0, blk0 = 0;
-      int n1 = 0, n2 = 0;
-      int2 cr1 = make_int2(0, 0), cr2 = cr1;
+      int64_t tok0 = 0;
       int32_t ca[4];
       uint32_t cb[4];
-      int32_t e0 = 0;
-      bool masked = false, full1 = true, full2 = true;
+      bool cut1 = false, cut2 = false;
       RowGroups groups{};
-      UnionWalk walk(bits + ri * 2 * C::MAXW, bits + ri * 2 * C::MAXW + C::MAXW, PAIR && MOD != 0 ? words : 0);
-      auto next_blocks = [&](int e) {
+      UnionSeek seek(bits + ri * 2 * C::MAXW, bits + ri * 2 * C::MAXW + C::MAXW, PAIR && MOD != 0 ? words : 0);
+      auto next_cut = [&](int e) {
         if constexpr (PAIR) {
-          n1 = walk.next();
-          n2 = walk.next();
-          if (n2 < 0) n2 = n1;
+          const uint32_t st = mk[e];
+          cut1 = (st >> (2 + half)) & (st >> half) & 1u;
+          cut2 = (st >> (10 + half)) & (st >> (8 + half)) & 1u;
         } else {
-          n1 = n2 = __ldg(p.idx + e0 + e);
+          cut1 = cut2 = (reinterpret_cast<const uint32_t*>(mk)[e >> 5] >> (e & 31)) & 1u;
         }
-        const int2* range = MODE == 0 ? p.mask.krange : p.mask.qrange;
-        cr1 = __ldg(range + blk0 + n1);
-        if (PAIR) cr2 = __ldg(range + blk0 + n2);
-      };
-      // no score of a column block with range c is masked in this row
-      auto inside = [&](const int2& c) {
-        return MODE == 0 ? (uint32_t)c.x - ilo < ilen && (uint32_t)c.y - ilo < ilen : c.x <= ipos && ipos < c.y;
-      };
-      auto next_cut = [&]() {
-        full1 = __all_sync(0xffffffffu, inside(cr1));
-        full2 = PAIR ? __all_sync(0xffffffffu, inside(cr2)) : full1;
-        if (!full1 || !full2) {
-          const int64_t at[4] = {(int64_t)n1 * BTB, (int64_t)n1 * BTB + 32, (int64_t)n2 * BTB + (PAIR ? 0 : 64),
-                                 (int64_t)n2 * BTB + (PAIR ? 32 : 96)};
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            ca[c] = __ldg((MODE == 0 ? p.mask.pos : p.mask.lo) + tok0 + lane + at[c]);
-            if (MODE != 0) cb[c] = __ldg(p.mask.len + tok0 + lane + at[c]);
+        auto fetch = [&](int c, int64_t at) {
+          ca[c] = __ldg((MODE == 0 ? p.mask.pos : p.mask.lo) + at);
+          if (MODE != 0) cb[c] = __ldg(p.mask.len + at);
+        };
+        if (!cut1 && !cut2) return;
+        if constexpr (PAIR) {
+          if (cut1) {
+            const int64_t at = tok0 + lane + (int64_t)seek.at(2 * e) * BTB;
+            fetch(0, at);
+            fetch(1, at + 32);
           }
+          if (cut2) {
+            const int64_t at = tok0 + lane + (int64_t)seek.at(2 * e + 1) * BTB;
+            fetch(2, at);
+            fetch(3, at + 32);
+          }
+        } else {
+          const int64_t at = tok0 + lane + (int64_t)__ldg(p.idx + p.ptr[item] + e) * BTB;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) fetch(c, at + 32 * c);
         }
       };
       if constexpr (MOD != 0) {
-        masked = p.mask.pos != nullptr;
-        if (masked) {
-          const int64_t b = bh / p.rm.H;
-          tok0 = b * p.N;
-          blk0 = b * nb;
+        if (p.mask.pos != nullptr) {
+          tok0 = bh / p.rm.H * p.N;
           if (exists) {
             const int64_t at = tok0 + (int64_t)i * BTB + o;
             if (MODE == 0) {
@@ -693,25 +720,26 @@ attn_bwd_tc_kernel(const __grid_constant__ CUtensorMap ta1, const __grid_constan
             }
           }
           groups.make(MODE == 0 ? ilo : (uint32_t)ipos, ilen, lane);
-          if (!PAIR) e0 = p.ptr[item];
-          next_blocks(0);
-          next_cut();
         }
+        next_cut(0);
       }
       for (int e = 0; e < len && ok; ++e) {
-        // bit c of see[2 h + c / 32]: this row sees column c of half h
+        // bit c of see[2 h + c / 32]: this row sees column c of half h; a half that no
+        // row of the warp sees has X = 0, one that all see whole is not cut
         uint32_t see[4] = {0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu};
-        const bool cut1 = MOD != 0 && !full1, cut2 = MOD != 0 && !full2;
+        bool any1 = true, any2 = true;
         if constexpr (MOD != 0) {
-          if (masked) {
-            if (MODE == 0) {
-              if (cut1) query_bits(groups, ilo, ilen, ca[0], ca[1], lane, see[0], see[1]);
-              if (cut2) query_bits(groups, ilo, ilen, ca[2], ca[3], lane, see[2], see[3]);
-            } else {
-              if (cut1) key_bits(groups, ipos, ca[0], cb[0], ca[1], cb[1], lane, see[0], see[1]);
-              if (cut2) key_bits(groups, ipos, ca[2], cb[2], ca[3], cb[3], lane, see[2], see[3]);
-            }
-            if (e + 1 < len) next_blocks(e + 1);
+          if (cut1) {
+            if (MODE == 0) query_bits(groups, ilo, ilen, ca[0], ca[1], lane, see[0], see[1]);
+            else key_bits(groups, ipos, ca[0], cb[0], ca[1], cb[1], lane, see[0], see[1]);
+            any1 = __any_sync(0xffffffffu, (see[0] | see[1]) != 0u);
+            cut1 = __any_sync(0xffffffffu, (see[0] & see[1]) != 0xffffffffu);
+          }
+          if (cut2) {
+            if (MODE == 0) query_bits(groups, ilo, ilen, ca[2], ca[3], lane, see[2], see[3]);
+            else key_bits(groups, ipos, ca[2], cb[2], ca[3], cb[3], lane, see[2], see[3]);
+            any2 = __any_sync(0xffffffffu, (see[2] | see[3]) != 0u);
+            cut2 = __any_sync(0xffffffffu, (see[2] & see[3]) != 0xffffffffu);
           }
         }
         const uint32_t st = c_use % kNS;
@@ -731,110 +759,137 @@ attn_bwd_tc_kernel(const __grid_constant__ CUtensorMap ta1, const __grid_constan
           wait_ld();
           // pairs: a row block that did not select this half's block (or does not
           // exist) gets X = 0 there (warp-uniform)
-          const bool has = !PAIR || (exists && ((msk >> (8 * h + half)) & 1u));
-          // MOD: the columns of this half that the row sees
-          const bool cut = h == 0 ? cut1 : cut2;
-          const uint32_t see0 = h == 0 ? see[0] : see[2], see1 = h == 0 ? see[1] : see[3];
-          // P of columns x, x + 1 (and 1 - tanh^2 of the cap) from the scores and LSE*log2e
-          auto probs = [&](int x, float la, float lb, float& p0, float& p1, float& t0, float& t1) {
-            const float s0 = __uint_as_float(sv[x]), s1 = __uint_as_float(sv[x + 1]);
-            float e0_, e1_;
-            if constexpr (MOD == 2) {
-              const float r0 = rcpf(1.f + ex2f(s0 * p.c1)), r1 = rcpf(1.f + ex2f(s1 * p.c1));
-              fma_x2(r0, r1, -2.f * p.cap2, p.cap2 - la, p.cap2 - lb, e0_, e1_);
-              t0 = 4.f * r0 * (1.f - r0);
-              t1 = 4.f * r1 * (1.f - r1);
+          const bool has = (!PAIR || (exists && ((msk >> (8 * h + half)) & 1u))) && (MOD == 0 || (h == 0 ? any1 : any2));
+          // MOD 2: do all scores of the half lie within the cap, where the polynomial holds?
+          bool within = true;
+          if constexpr (MOD == 2) {
+            float big[2] = {0.f, 0.f};
+#pragma unroll
+            for (int c = 0; c < HB; c += 2)
+              big[(c >> 1) & 1] = fmaxf(fmaxf(big[(c >> 1) & 1], fabsf(__uint_as_float(sv[c]))),
+                                        fabsf(__uint_as_float(sv[c + 1])));
+            within = __all_sync(0xffffffffu, fmaxf(big[0], big[1]) * p.inv_cap <= 1.f);
+          }
+          // the half's operand(s) X; CUT: the mask hides some of its scores from rows of this warp
+          auto operands = [&](auto cut_c, auto poly_c) {
+            constexpr bool CUT = decltype(cut_c)::value, POLY = decltype(poly_c)::value;
+            // P of columns x, x + 1 from the scores and LSE*log2e, and 1 - tanh^2 of the cap
+            auto probs = [&](int x, float la, float lb, float& p0, float& p1, float& c0, float& c1) {
+              const float s0 = __uint_as_float(sv[x]), s1 = __uint_as_float(sv[x + 1]);
+              float e0, e1;
+              c0 = c1 = 1.f;
+              if constexpr (MOD != 2) {
+                fma_x2(s0, s1, sl2, -la, -lb, e0, e1);
+              } else if constexpr (POLY) {
+                float t0, t1;
+                tanh_poly_x2(s0, s1, p.inv_cap, t0, t1);
+                fma_x2(t0, t1, p.cap2, -la, -lb, e0, e1);
+                fma2_x2(t0, t1, -t0, -t1, 1.f, c0, c1);
+              } else {
+                const float r0 = rcpf(1.f + ex2f(s0 * p.c1)), r1 = rcpf(1.f + ex2f(s1 * p.c1));
+                e0 = fmaf(r0, -2.f * p.cap2, p.cap2) - la;
+                e1 = fmaf(r1, -2.f * p.cap2, p.cap2) - lb;
+                c0 = 4.f * r0 * (1.f - r0);
+                c1 = 4.f * r1 * (1.f - r1);
+              }
+              p0 = ex2f(e0);
+              p1 = ex2f(e1);
+              if constexpr (CUT) {   // x is a constant of the unrolled loop
+                const uint32_t w = h == 0 ? (x < 32 ? see[0] : see[1]) : (x < 32 ? see[2] : see[3]);
+                if (!((w >> (x & 31)) & 1u)) p0 = 0.f;
+                if (!((w >> ((x + 1) & 31)) & 1u)) p1 = 0.f;
+              }
+            };
+            uint32_t xk[HB / 2];
+            if constexpr (MODE == 3) {
+              // P^T over S^T; dS^T = P^T (dP^T - D) over dP^T (both already in registers)
+              uint32_t xd[HB / 2];
+#pragma unroll
+              for (int x = 0; x < HB / 2; ++x) xk[x] = xd[x] = 0u;
+              if (has)
+#pragma unroll
+              for (int x4 = 0; x4 < HB / 4; ++x4) {
+                const float4 L = stats[16 * h + x4];
+                const float4 Dv = stats[32 + 16 * h + x4];
+                const float l2[4] = {L.x, L.y, L.z, L.w}, dd[4] = {Dv.x, Dv.y, Dv.z, Dv.w};
+                float pr[4], ds[4];
+#pragma unroll
+                for (int u = 0; u < 4; u += 2) {   // column pairs: each lane rounds as the scalar form
+                  const int x = 4 * x4 + u;
+                  float t0, t1, c0, c1;
+                  probs(x, l2[u], l2[u + 1], pr[u], pr[u + 1], c0, c1);
+                  sub_x2(__uint_as_float(dv[x]), __uint_as_float(dv[x + 1]), dd[u], dd[u + 1], t0, t1);
+                  mul_x2(pr[u], pr[u + 1], t0, t1, ds[u], ds[u + 1]);
+                  if (MOD == 2) mul_x2(ds[u], ds[u + 1], c0, c1, ds[u], ds[u + 1]);
+                }
+                xk[2 * x4] = pack2(pr[0], pr[1]);
+                xk[2 * x4 + 1] = pack2(pr[2], pr[3]);
+                xd[2 * x4] = pack2(ds[0], ds[1]);
+                xd[2 * x4 + 1] = pack2(ds[2], ds[3]);
+              }
+              tmem_st32(t_row + 128u * b, xk);
+              tmem_st32(t_row + 128u * b + HB, xd);
+              wait_st();
+              fence_before();
+              mbar_arrive(bar(X_FULL + b));
             } else {
-              fma_x2(s0, s1, sl2, -la, -lb, e0_, e1_);
-            }
-            p0 = ex2f(e0_);
-            p1 = ex2f(e1_);
-            if (MOD != 0 && cut) {   // x is a constant of the unrolled loop
-              const uint32_t w = x < 32 ? see0 : see1;
-              if (!((w >> (x & 31)) & 1u)) p0 = 0.f;
-              if (!((w >> ((x + 1) & 31)) & 1u)) p1 = 0.f;
+#pragma unroll
+              for (int x = 0; x < HB / 2; ++x) xk[x] = 0u;
+              if (has)
+#pragma unroll
+              for (int x4 = 0; x4 < HB / 4; ++x4) {
+                float l2[4], dd[4];
+                if (MODE == 0) {
+#pragma unroll
+                  for (int u = 0; u < 4; ++u) { l2[u] = own_l2; dd[u] = own_d; }
+                } else {
+                  const float4 L = stats[16 * h + x4];          // LSE*log2e of columns 64h+4x4 .. +3
+                  const float4 Dv = stats[32 + 16 * h + x4];    // D of the same columns
+                  l2[0] = L.x; l2[1] = L.y; l2[2] = L.z; l2[3] = L.w;
+                  dd[0] = Dv.x; dd[1] = Dv.y; dd[2] = Dv.z; dd[3] = Dv.w;
+                }
+                float v[4];
+#pragma unroll
+                for (int u = 0; u < 4; u += 2) {   // column pairs: each lane rounds as the scalar form
+                  const int x = 4 * x4 + u;
+                  float p0, p1, c0, c1;
+                  probs(x, l2[u], l2[u + 1], p0, p1, c0, c1);
+                  if (kHasDP) {
+                    float t0, t1;
+                    sub_x2(__uint_as_float(dv[x]), __uint_as_float(dv[x + 1]), dd[u], dd[u + 1], t0, t1);
+                    mul_x2(p0, p1, t0, t1, v[u], v[u + 1]);
+                    if (MOD == 2) mul_x2(v[u], v[u + 1], c0, c1, v[u], v[u + 1]);
+                  } else {
+                    v[u] = p0;
+                    v[u + 1] = p1;
+                  }
+                }
+                xk[2 * x4] = pack2(v[0], v[1]);
+                xk[2 * x4 + 1] = pack2(v[2], v[3]);
+              }
+              // X over the first 32 columns of this half's S (already in registers)
+              tmem_st32(t_row + 128u * b, xk);
+              wait_st();
+              fence_before();
+              mbar_arrive(bar(X_FULL + b));
             }
           };
-          uint32_t xk[HB / 2];
-          if constexpr (MODE == 3) {
-            // P^T over S^T; dS^T = P^T (dP^T - D) over dP^T (both already in registers)
-            uint32_t xd[HB / 2];
-#pragma unroll
-            for (int x = 0; x < HB / 2; ++x) xk[x] = xd[x] = 0u;
-            if (has)
-#pragma unroll
-            for (int x4 = 0; x4 < HB / 4; ++x4) {
-              const float4 L = stats[16 * h + x4];
-              const float4 Dv = stats[32 + 16 * h + x4];
-              const float l2[4] = {L.x, L.y, L.z, L.w}, dd[4] = {Dv.x, Dv.y, Dv.z, Dv.w};
-              float pr[4], ds[4];
-#pragma unroll
-              for (int u = 0; u < 4; u += 2) {   // column pairs: each lane rounds as the scalar form
-                const int x = 4 * x4 + u;
-                float t0, t1, c0 = 1.f, c1 = 1.f;
-                probs(x, l2[u], l2[u + 1], pr[u], pr[u + 1], c0, c1);
-                sub_x2(__uint_as_float(dv[x]), __uint_as_float(dv[x + 1]), dd[u], dd[u + 1], t0, t1);
-                mul_x2(pr[u], pr[u + 1], t0, t1, ds[u], ds[u + 1]);
-                if (MOD == 2) mul_x2(ds[u], ds[u + 1], c0, c1, ds[u], ds[u + 1]);
-              }
-              xk[2 * x4] = pack2(pr[0], pr[1]);
-              xk[2 * x4 + 1] = pack2(pr[2], pr[3]);
-              xd[2 * x4] = pack2(ds[0], ds[1]);
-              xd[2 * x4 + 1] = pack2(ds[2], ds[3]);
-            }
-            tmem_st32(t_row + 128u * b, xk);
-            tmem_st32(t_row + 128u * b + HB, xd);
-            wait_st();
-            fence_before();
-            mbar_arrive(bar(X_FULL + b));
+          if constexpr (MOD == 0) {
+            operands(std::false_type{}, std::true_type{});
+          } else if (h == 0 ? cut1 : cut2) {
+            if (MOD == 2 && !within) operands(std::true_type{}, std::false_type{});
+            else operands(std::true_type{}, std::true_type{});
           } else {
-#pragma unroll
-            for (int x = 0; x < HB / 2; ++x) xk[x] = 0u;
-            if (has)
-#pragma unroll
-            for (int x4 = 0; x4 < HB / 4; ++x4) {
-              float l2[4], dd[4];
-              if (MODE == 0) {
-#pragma unroll
-                for (int u = 0; u < 4; ++u) { l2[u] = own_l2; dd[u] = own_d; }
-              } else {
-                const float4 L = stats[16 * h + x4];          // LSE*log2e of columns 64h+4x4 .. +3
-                const float4 Dv = stats[32 + 16 * h + x4];    // D of the same columns
-                l2[0] = L.x; l2[1] = L.y; l2[2] = L.z; l2[3] = L.w;
-                dd[0] = Dv.x; dd[1] = Dv.y; dd[2] = Dv.z; dd[3] = Dv.w;
-              }
-              float v[4];
-#pragma unroll
-              for (int u = 0; u < 4; u += 2) {   // column pairs: each lane rounds as the scalar form
-                const int x = 4 * x4 + u;
-                float p0, p1, c0 = 1.f, c1 = 1.f;
-                probs(x, l2[u], l2[u + 1], p0, p1, c0, c1);
-                if (kHasDP) {
-                  float t0, t1;
-                  sub_x2(__uint_as_float(dv[x]), __uint_as_float(dv[x + 1]), dd[u], dd[u + 1], t0, t1);
-                  mul_x2(p0, p1, t0, t1, v[u], v[u + 1]);
-                  if (MOD == 2) mul_x2(v[u], v[u + 1], c0, c1, v[u], v[u + 1]);
-                } else {
-                  v[u] = p0;
-                  v[u + 1] = p1;
-                }
-              }
-              xk[2 * x4] = pack2(v[0], v[1]);
-              xk[2 * x4 + 1] = pack2(v[2], v[3]);
-            }
-            // X over the first 32 columns of this half's S (already in registers)
-            tmem_st32(t_row + 128u * b, xk);
-            wait_st();
-            fence_before();
-            mbar_arrive(bar(X_FULL + b));
+            if (MOD == 2 && !within) operands(std::false_type{}, std::false_type{});
+            else operands(std::false_type{}, std::true_type{});
           }
           ++hg;
         }
-        if (MOD != 0 && masked && e + 1 < len) next_cut();
+        if (MOD != 0 && e + 1 < len) next_cut(e + 1);
         ++c_use;
       }
       if (!ok) break;
-      if (PAIR) release();
+      if (C::HOLD) release();
       pending = orow;
       pending2 = orow2;
       has_pending = true;
@@ -856,7 +911,7 @@ template <int MODE, int D, int BTB, int MOD>
 sparsp_status_t go(const Dims& s, const CUtensorMap& a1, const CUtensorMap& a2, const CUtensorMap& b1,
                    const CUtensorMap& b2, const Params& prm, cudaStream_t st) {
   auto kern = attn_bwd_tc_kernel<MODE, D, BTB, MOD>;
-  constexpr uint32_t kSmemBytes = BCfg<D, BTB>::kSmemBytes;
+  constexpr uint32_t kSmemBytes = BCfg<D, BTB, MOD>::kSmemBytes;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes) != cudaSuccess)
     return SPARSP_ERR_CUDA;
   const int sms = device_sm_count();
@@ -908,7 +963,7 @@ sparsp_status_t launch_bwd_mod(const Dims& s, int mode, const __nv_bfloat16* q,
   Params prm{ptr, idx, s.N, s.nb, nbp, (int64_t)s.B * s.H * nbp, (int64_t)rows, scale * 1.4426950408889634f,
              mode == 2 ? 1.0f : scale, lse2, delta, out, out2, 1.0f, items, counter, prof, d_status,
              raster ? 1 : 0, raster_map(s), mask, MOD == 2 ? 2.f * scale * 1.4426950408889634f / cap : 0.f,
-             cap * 1.4426950408889634f};
+             cap * 1.4426950408889634f, MOD == 2 ? scale / cap : 0.f};
   if (s.Bt == 64) {
     if (s.d == 64) return launch_d<64, 64, MOD>(mode, m, s, prm, st);
     return launch_d<128, 64, MOD>(mode, m, s, prm, st);

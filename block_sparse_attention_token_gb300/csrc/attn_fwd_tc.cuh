@@ -53,15 +53,14 @@
 // are drained with a second bounded wait, and TMEM is released.
 //
 // MOD = 0 is attention over the selected blocks; MOD = 1 adds a token mask
-// (mask.cuh) and MOD = 2 a score cap beside it:
-//   y = cap tanh(scale s / cap) = cap (1 - 2 r), r = 1 / (1 + exp(2 scale s / cap)),
-// one exponential and one reciprocal per score more, and r is what is kept:
-// the exponent y - m is one multiply-add of r. The cap is monotone, so the row
-// maximum still comes from the raw scores of the load. The softmax threads know
-// the key block of every stage; a stage whose positions lie inside the intervals
-// of all 32 rows of a warp (by the block's smallest and largest position)
-// costs two comparisons, and only the others mask score by score.
+// (mask.cuh), MOD = 2 a score cap of at most kFixedCap beside it and MOD = 3 any
+// cap: y = cap tanh(scale s / cap) (cap.cuh). The producer tells with the item
+// which of its blocks the token mask cuts (by the blocks' ranges); in those each
+// row's visible columns come as bits, the others run as they do without a mask.
 #pragma once
+#include <type_traits>
+
+#include "cap.cuh"
 #include "mask.cuh"
 #include "pairs.cuh"
 #include "tc_helpers.cuh"
@@ -76,14 +75,14 @@ enum Bar {
   Q_FULL = 0, Q_EMPTY, K_FULL, K_EMPTY = K_FULL + kMaxStages, V_FULL = K_EMPTY + kMaxStages,
   V_EMPTY = V_FULL + kMaxStages, S_FULL = V_EMPTY + kMaxStages, S_FREE = S_FULL + 2, P_FULL = S_FREE + 2, PV_DONE = P_FULL + 2, O_FULL = PV_DONE + 2,
   O_EMPTY,
-  I_FULL, I_EMPTY = I_FULL + kNI, TEAR = I_EMPTY + kNI, TEAR_PV, NBAR
+  I_FULL, I_EMPTY = I_FULL + kNI, TEAR = I_EMPTY + kNI, TEAR_PV, EXCH, NBAR = EXCH + 8
 };
 // Tile geometry for blocks of BT tokens and head dimension D. The query tile
 // and a key/value stage are 128 rows each: one block, or two 64-token blocks
 // (PAIR). Tiles are TMA'd as 64-column boxes of 128-byte rows with 128-byte
 // swizzle; a stage of two blocks is two 64-row boxes per column box, the
 // second 64 rows (8 KB, a whole number of 1 KB swizzle atoms) after the first.
-template <int BT_, int D_>
+template <int BT_, int D_, int MOD_ = 0>
 struct Cfg {
   static constexpr int BT = BT_, D = D_, QR = 128, KR = 128;
   static constexpr bool PAIR = BT == 64;
@@ -94,8 +93,11 @@ struct Cfg {
   // a whole 128-column S row in registers (one pass per stage, S released as
   // soon as it is loaded) with the 200 registers the register split below
   // gives them.
-  static constexpr bool DUO = D == 64;
-  static constexpr int NSM = 4;                           // softmax warps
+  static constexpr bool DUO = D == 64 && MOD_ != 2;
+  static constexpr int NSM = MOD_ == 2 ? 8 : 4;           // softmax warps
+  // arrivals of the softmax warps at S_FREE, P_FULL and O_EMPTY: every thread, or with
+  // MOD one lane of each of the four warps concerned
+  static constexpr int kArrivals = MOD_ == 0 ? 32 * NSM : 4;
   // MMA issuer warps: S and PV each get their own with d = 128; with DUO one
   // warp issues both streams (the softmax releases S(e-1) before it writes
   // P(e-1), so S(e) then PV(e-1) in one warp never wait on each other)
@@ -113,9 +115,12 @@ struct Cfg {
                 "register split of the two warpgroups");
   // K and V ring stages: 3 of each fit beside a d = 128 query tile; a DUO CTA
   // has half of the SM's shared memory for tiles of half the size: 3 K and 2 V
-  static constexpr int NK = 3, NV = DUO ? 2 : 3;
+  // (four with MOD 2 and d = 64, which has a CTA's shared memory to itself; two V
+  // stages where its masks need the room of the third)
+  static constexpr int NK = MOD_ == 2 && D == 64 ? 4 : 3;
+  static constexpr int NV = MOD_ == 2 && D == 64 ? 4 : DUO || (MOD_ == 2 && PAIR) ? 2 : 3;
   static constexpr int NSB = DUO ? 1 : 2, NPB = DUO ? 1 : 2;   // S and P buffers in TMEM
-  static constexpr int NI = DUO || PAIR ? 2 : kNI;              // item ring slots
+  static constexpr int NI = DUO || PAIR || MOD_ != 0 ? 2 : kNI;   // item ring slots
   static constexpr int kMinCtas = DUO ? 2 : 1;                  // CTAs per SM
   static constexpr uint32_t kColS = 0, kColO = DUO ? 128 : 256, kColP = DUO ? 192 : 384;
   static constexpr uint32_t kTmemCols = DUO ? 256 : 512;
@@ -137,15 +142,22 @@ struct Cfg {
   // row, bit 1 = the second), two bits per block where shared memory is short
   // (d = 128: stage s is nibble s)
   static constexpr bool MASK_BYTES = DUO;
-  static constexpr uint32_t kMaskWords = !PAIR ? 0 : (MASK_BYTES ? 8 * MAXW + 4 : 2 * MAXW + 1);
+  // with MOD the codes of union_codes (a nibble per block), and without pairs one
+  // bit per block of the row: does the token mask cut it
+  static constexpr uint32_t kMaskWords = !PAIR ? (MOD_ != 0 ? kMaxBlocks / 32 : 0)
+                                               : (MASK_BYTES ? 8 * MAXW + 4 : (MOD_ != 0 ? 4 : 2) * MAXW + 1);
   static constexpr uint32_t kOffMask = kOffBits + kBitsBytes;
-  static constexpr uint32_t kOffMisc = kOffMask + NI * kMaskWords * 4;
+  static constexpr uint32_t kOffEx = kOffMask + (NI * kMaskWords * 4 + 15) / 16 * 16;   // MOD 2: row sums of group 1
+  static constexpr uint32_t kOffMisc = kOffEx + (MOD_ == 2 ? 512 : 0);
   static constexpr uint32_t kSmemBytes = kOffMisc + 16 + 1024;   // + alignment slack
   static_assert(kSmemBytes <= (DUO ? 115712u : 232448u), "shared memory");
 };
 constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr uint64_t kDrainNs = 200000000ull;
 constexpr float kRescaleThreshold = 8.0f;   // log2 units
+// Up to this cap exp(y) needs no reference: P <= 2^73, and with 2^19 keys and
+// values up to 2^35 the sums stay below 2^127; a row's smallest sum is 2^-73.
+constexpr float kFixedCap = 50.0f;
 
 __device__ __forceinline__ bool wait_raw(uint32_t bar, uint32_t parity, uint64_t limit) {
   const uint64_t t0 = globaltimer_ns();
@@ -176,12 +188,6 @@ __device__ __forceinline__ float tmem_ld32_max(uint32_t taddr, uint32_t* r) {
   return m;
 }
 
-__device__ __forceinline__ float rcpf(float x) {
-  float y;
-  asm("rcp.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
-  return y;
-}
-
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<uint32_t*>(&v);
@@ -210,18 +216,19 @@ struct Params {
   uint64_t* prof;
   int32_t* d_status;
   MaskView mask;      // MOD != 0; mask.pos null: no mask
-  float c1, cap2;     // MOD == 2: 2 scale log2(e) / cap and cap log2(e)
+  // MOD 2, 3: 2 scale log2(e) / cap, cap log2(e) and scale / cap
+  float c1, cap2, inv_cap;
 };
 
 template <int BT, int D, int MOD>
-__global__ void __launch_bounds__(Cfg<BT, D>::THREADS, Cfg<BT, D>::kMinCtas)
+__global__ void __launch_bounds__(Cfg<BT, D, MOD>::THREADS, Cfg<BT, D, MOD>::kMinCtas)
 attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                    const __grid_constant__ CUtensorMap tv, const Params p) {
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
   uint8_t* gbase = smem_raw + (base - raw);
-  using C = Cfg<BT, D>;
+  using C = Cfg<BT, D, MOD>;
   constexpr bool PAIR = C::PAIR;
   const uint32_t sQ = base, sK = base + C::kOffK, sV = base + C::kOffV;
   auto bar = [&](int idx) -> uint32_t { return base + C::kOffBar + 8u * (uint32_t)idx; };
@@ -248,19 +255,21 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(bar(S_FULL + b), 1);
-      mbar_init(bar(S_FREE + b), 32 * C::NSM);
-      mbar_init(bar(P_FULL + b), 32 * C::NSM);
+      mbar_init(bar(S_FREE + b), C::kArrivals);
+      mbar_init(bar(P_FULL + b), C::kArrivals);
     }
     mbar_init(bar(PV_DONE), 1);
     mbar_init(bar(PV_DONE + 1), 1);
     mbar_init(bar(O_FULL), 1);
-    mbar_init(bar(O_EMPTY), 32 * C::NSM);
+    mbar_init(bar(O_EMPTY), C::kArrivals);
     for (int r = 0; r < kNI; ++r) {
       mbar_init(bar(I_FULL + r), 1);
       mbar_init(bar(I_EMPTY + r), C::NSM + C::NIS);
     }
     mbar_init(bar(TEAR), 1);
     mbar_init(bar(TEAR_PV), 1);
+    if (MOD != 0)
+      for (int r = 0; r < 8; ++r) mbar_init(bar(EXCH + r), 1);
     *abort_flag = 0;
     fence_barrier_init();
   }
@@ -309,7 +318,17 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
           if (badbits && lane == 0) report(p.d_status, SPARSP_ERR_DATA);
           const int u = union_count(bmA, bmB, words, lane);
           len = (badbits == 3) ? -1 : (u + 1) / 2;   // stages of two key blocks
-          if constexpr (C::MASK_BYTES)
+          if constexpr (MOD != 0) {
+            const int64_t blk0 = bh / p.rm.H * nb;
+            const bool masked = p.mask.pos != nullptr;
+            const int2 qa = masked ? __ldg(p.mask.qrange + blk0 + iA) : make_int2(0, 0);
+            const int2 qb = masked && iA + 1 < nb ? __ldg(p.mask.qrange + blk0 + iA + 1) : qa;
+            union_codes<false>(bmA, bmB, words, u, lane, masks + ri * C::kMaskWords, [&](int j) -> uint32_t {
+              if (!masked) return 0u;
+              const int2 k = __ldg(p.mask.krange + blk0 + j);
+              return (all_seen(qa, k) ? 0u : 1u) | (all_seen(qb, k) ? 0u : 2u);
+            });
+          } else if constexpr (C::MASK_BYTES)
             union_masks(bmA, bmB, words, u, lane, reinterpret_cast<uint8_t*>(masks + ri * C::kMaskWords));
           else
             union_masks2(bmA, bmB, words, u, lane, masks + ri * C::kMaskWords);
@@ -327,6 +346,17 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
             len = -1;
           } else {
             len = b - a;
+            if constexpr (MOD != 0) {
+              const int64_t blk0 = (int64_t)item / nb / p.rm.H * nb;
+              const bool masked = p.mask.pos != nullptr;
+              const int2 q = masked ? __ldg(p.mask.qrange + blk0 + item % nb) : make_int2(0, 0);
+              for (int32_t e = 0; e < len; e += 32) {
+                bool cut = masked && e + lane < len;
+                if (cut) cut = !all_seen(q, __ldg(p.mask.krange + blk0 + p.col_idx[a + e + lane]));
+                const uint32_t w = __ballot_sync(0xffffffffu, cut);
+                if (lane == 0) masks[ri * C::kMaskWords + (e >> 5)] = w;
+              }
+            }
           }
         }
       }
@@ -604,6 +634,486 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
     }
     __syncwarp();
   }
+  } else if constexpr (MOD == 2) {
+    // ------------------------------------------------------------ softmax + epilogue with a cap of at most kFixedCap
+    // Capped scores lie in [-cap, cap], so exp needs no reference: P = exp2(y) and
+    // the row sum stay far inside fp32 and bf16, and no maximum is taken, nothing is
+    // rescaled and stages do not depend on one another. Two groups of four
+    // warps take the stages in turn, whole rows each (group g the stages of S
+    // and P buffer g), so that the waits and loads of one run under the
+    // arithmetic of the other. The stage goes through TMEM 32 columns at a time in a
+    // loop that is not unrolled: unrolled, its variants do not stay in the
+    // instruction cache. Group 1 hands its part of the row sum to group 0, which
+    // writes O and LSE while group 1 goes on.
+    const int grp = warp >> 2, rw = warp & 3, t = (int)(threadIdx.x & 127);
+    const uint32_t t_row = tmem + ((uint32_t)(rw * 32) << 16);
+    float* part = reinterpret_cast<float*>(gbase + C::kOffEx);   // [128] row sums of group 1
+    uint32_t it_use = 0, turn = 0, o_items = 0;                  // turn: stages done by this group
+    uint32_t stages_before = 0;                                  // of this CTA
+    const int half = PAIR ? t >> 6 : 0;   // with pairs, rows 0-63 are query block 2p and rows 64-127 block 2p + 1
+    const uint32_t tS = t_row + C::kColS + grp * 128u, tP = t_row + C::kColP + grp * 64u;
+    auto arrive = [&](uint32_t bar_) {   // for the whole warp
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar_);
+    };
+    for (;;) {
+      const int ri = (int)(it_use % C::NI);
+      if (!wait_warp(bar(I_FULL + ri), (it_use / C::NI) & 1u, g)) break;
+      const int64_t item = ring[ri].x;
+      const int len = ring[ri].y;
+      const int badbits = ring[ri].z;
+      ++it_use;
+      if (len < 0) {
+        arrive(bar(I_EMPTY + ri));
+        if (len == -2) break;
+        continue;
+      }
+      const int64_t bh = item / nbp;
+      const int i = PAIR ? 2 * (int)(item % nbp) + half : (int)(item % nb);   // this thread's query block
+      const int o = PAIR ? t & 63 : t;                                        // its token in the block
+      const int64_t row = bh * p.N + (int64_t)i * BT + o;
+      bool stores = grp == 0 && i < nb && !((badbits >> half) & 1);
+      int64_t orow_idx = row;
+      if (p.raster && stores) orow_idx = p.rm.row(bh, i, o);
+      if (stores) stores = dcheck(row < p.rows_total && orow_idx >= 0 && orow_idx < p.rows_total, p.d_status);
+      uint4* orow = reinterpret_cast<uint4*>(p.o + orow_idx * D);
+      if (len == 0) {
+        if (stores) {
+#pragma unroll
+          for (int c = 0; c < D / 8; ++c) orow[c] = make_uint4(0, 0, 0, 0);
+          p.lse[row] = -INFINITY;
+        }
+        arrive(bar(I_EMPTY + ri));
+        continue;
+      }
+      const uint32_t* mk = masks + ri * C::kMaskWords;
+      uint32_t ilo = 0u, ilen = 0u;      // this row's interval
+      const int32_t* pos0 = p.mask.pos;
+      RowGroups groups{};
+      if (p.mask.pos != nullptr) {
+        const int64_t tok0 = bh / p.rm.H * p.N;   // this batch element's first token
+        pos0 += tok0 + lane;
+        if (i < nb) {
+          ilo = (uint32_t)__ldg(p.mask.lo + tok0 + (int64_t)i * BT + o);
+          ilen = __ldg(p.mask.len + tok0 + (int64_t)i * BT + o);
+        }
+        groups.make(ilo, ilen, lane);
+      }
+      UnionSeek seek(bits + ri * 2 * C::MAXW, bits + ri * 2 * C::MAXW + C::MAXW, PAIR ? words : 0);
+      float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+      bool ok = true;
+      for (int e = (grp ^ (int)(stages_before & 1u)); e < len; e += 2, ++turn) {
+        // bit h of has / cut: the row block selected the key block of half h (64
+        // columns), and the mask cuts it; the positions of this lane's columns there
+        uint32_t has = 3u, cut = 0u;
+        int32_t kp[4];
+        if constexpr (PAIR) {
+          const uint32_t code = reinterpret_cast<const uint8_t*>(mk)[e] >> half;   // bits 0, 4: selected; 2, 6: cut
+          has = (code & 1u) | ((code >> 3) & 2u);
+          cut = has & (((code >> 2) & 1u) | ((code >> 5) & 2u));
+        } else {
+          cut = (mk[e >> 5] >> (e & 31)) & 1u ? 3u : 0u;
+        }
+        uint32_t see[4] = {0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu};   // bit c: column 32 w + c
+        if (cut) {
+          int64_t j1, j2;
+          if constexpr (PAIR) {
+            j1 = seek.at(2 * e);
+            j2 = cut & 2u ? seek.at(2 * e + 1) : j1;
+          } else {
+            j1 = j2 = __ldg(p.col_idx + p.row_ptr[item] + e);
+          }
+          kp[0] = __ldg(pos0 + j1 * BT);
+          kp[1] = __ldg(pos0 + j1 * BT + 32);
+          kp[2] = __ldg(pos0 + j2 * BT + (PAIR ? 0 : 64));
+          kp[3] = __ldg(pos0 + j2 * BT + (PAIR ? 32 : 96));
+          if (cut & 1u) query_bits(groups, ilo, ilen, kp[0], kp[1], lane, see[0], see[1]);
+          if (cut & 2u) query_bits(groups, ilo, ilen, kp[2], kp[3], lane, see[2], see[3]);
+        }
+        if (!(ok = wait_warp(bar(S_FULL + grp), turn & 1u, g))) break;
+        if (turn > 0 && !(ok = wait_warp(bar(PV_DONE + grp), (turn - 1u) & 1u, g))) break;   // P buffer free again
+        fence_after();
+#pragma unroll 1
+        for (int c = 0; c < 4; ++c) {
+          const uint32_t w = c == 0 ? see[0] : c == 1 ? see[1] : c == 2 ? see[2] : see[3];
+          uint32_t pk[16];
+          // columns no row of the warp sees (or of a block the row block did not select)
+          if (!((has >> (c >> 1)) & 1u) || !__any_sync(0xffffffffu, w != 0u)) {
+#pragma unroll
+            for (int x = 0; x < 16; ++x) pk[x] = 0u;
+            tmem_st16(tP + 16u * c, pk);
+            continue;
+          }
+          uint32_t s[32];
+          tmem_ld32(tS + 32u * c, s);
+          wait_ld();
+          float big[2] = {0.f, 0.f};
+#pragma unroll
+          for (int x = 0; x < 32; x += 2)
+            big[(x >> 1) & 1] = fmaxf(fmaxf(big[(x >> 1) & 1], fabsf(__uint_as_float(s[x]))),
+                                      fabsf(__uint_as_float(s[x + 1])));
+          const bool within = __all_sync(0xffffffffu, fmaxf(big[0], big[1]) * p.inv_cap <= 1.f);
+          auto probs = [&](auto poly_c, auto cut_c) {
+            constexpr bool POLY = decltype(poly_c)::value, CUT = decltype(cut_c)::value;
+#pragma unroll
+            for (int x = 0; x < 16; ++x) {
+              const float s0 = __uint_as_float(s[2 * x]), s1 = __uint_as_float(s[2 * x + 1]);
+              float y0, y1;
+              if constexpr (POLY) {
+                cap_poly_x2(s0, s1, p.inv_cap, p.cap2, 0.f, y0, y1);
+              } else {
+                y0 = cap_exp(s0 * p.c1, p.cap2);
+                y1 = cap_exp(s1 * p.c1, p.cap2);
+              }
+              float p0 = ex2f(y0), p1 = ex2f(y1);
+              if constexpr (CUT) {
+                if (!((w >> (2 * x)) & 1u)) p0 = 0.f;
+                if (!((w >> (2 * x + 1)) & 1u)) p1 = 0.f;
+              }
+              add_x2(sum[x & 1].x, sum[x & 1].y, p0, p1);
+              pk[x] = pack2(p0, p1);
+            }
+          };
+          if (!within) probs(std::false_type{}, std::true_type{});
+          else if ((cut >> (c >> 1)) & 1u) probs(std::true_type{}, std::true_type{});
+          else probs(std::true_type{}, std::false_type{});
+          tmem_st16(tP + 16u * c, pk);
+        }
+        fence_before();
+        arrive(bar(S_FREE + grp));
+        wait_st();
+        fence_before();
+        arrive(bar(P_FULL + grp));
+      }
+      if (!ok) break;
+      arrive(bar(I_EMPTY + ri));
+      stages_before += (uint32_t)len;
+      float l = (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+      if (grp == 1) {
+        if (!wait_warp(bar(EXCH + 4 + rw), (o_items & 1u) ^ 1u, g)) break;   // the last item's sums were read
+        part[t] = l;
+        arrive(bar(EXCH + rw));
+        ++o_items;
+        continue;
+      }
+      if (!wait_warp(bar(EXCH + rw), o_items & 1u, g)) break;
+      l += part[t];
+      arrive(bar(EXCH + 4 + rw));
+      if (!wait_warp(bar(O_FULL), o_items & 1u, g)) break;
+      ++o_items;
+      fence_after();
+      const float inv = l > 0.f ? 1.0f / l : 0.f;   // 0: the row saw no key
+#pragma unroll 1
+      for (int c = 0; c < D / 32; ++c) {
+        uint32_t ov[32];
+        tmem_ld32(t_row + C::kColO + c * 32u, ov);
+        wait_ld();
+        if (!stores) continue;
+        uint32_t w[16];
+#pragma unroll
+        for (int x = 0; x < 16; ++x)
+          w[x] = pack2(__uint_as_float(ov[2 * x]) * inv, __uint_as_float(ov[2 * x + 1]) * inv);
+#pragma unroll
+        for (int x = 0; x < 4; ++x) orow[c * 4 + x] = make_uint4(w[4 * x], w[4 * x + 1], w[4 * x + 2], w[4 * x + 3]);
+      }
+      fence_before();
+      arrive(bar(O_EMPTY));
+      if (stores) p.lse[row] = l > 0.f ? log2f(l) * 0.69314718055994531f : -INFINITY;
+    }
+  } else if constexpr (MOD != 0) {
+    if constexpr (C::DUO) regs_increase<C::kRegSoftmax>();
+    // ------------------------------------------------------------ softmax + epilogue with a mask, or a larger cap
+    const uint32_t t_row = tmem + ((uint32_t)(warp * 32) << 16);
+    uint32_t it_use = 0, s_use = 0, o_items = 0;
+    uint64_t blocks_done = 0;
+    const float sl2 = p.scale_log2;
+    const int half = PAIR ? (int)(threadIdx.x >> 6) : 0;   // rows 0-63: query block 2p, rows 64-127: block 2p + 1
+    bool ok = true;
+    auto arrive = [&](uint32_t bar_) {   // for the whole warp
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar_);
+    };
+    for (;;) {
+      const int ri = (int)(it_use % C::NI);
+      if (!wait_warp(bar(I_FULL + ri), (it_use / C::NI) & 1u, g)) break;
+      const int64_t item = ring[ri].x;
+      const int len = ring[ri].y;
+      const int badbits = ring[ri].z;
+      // the item's masks are read until it ends; release the slot then
+      auto release = [&]() { arrive(bar(I_EMPTY + ri)); };
+      ++it_use;
+      if (len < 0) {
+        release();
+        if (len == -2) break;
+        continue;
+      }
+      const int64_t bh = item / nbp;
+      const int i = PAIR ? 2 * (int)(item % nbp) + half : (int)(item % nb);   // this thread's query block
+      const int o = PAIR ? (int)(threadIdx.x & 63) : (int)threadIdx.x;       // its token in the block
+      const int64_t row = bh * p.N + (int64_t)i * BT + o;
+      bool stores = i < nb && !((badbits >> half) & 1);
+      int64_t orow_idx = row;
+      if (p.raster && stores) orow_idx = p.rm.row(bh, i, o);
+      if (stores) stores = dcheck(row < p.rows_total && orow_idx >= 0 && orow_idx < p.rows_total, p.d_status);
+      uint4* orow = reinterpret_cast<uint4*>(p.o + orow_idx * D);
+      if (len == 0) {
+        if (stores) {
+#pragma unroll
+          for (int c = 0; c < D / 8; ++c) orow[c] = make_uint4(0, 0, 0, 0);
+          p.lse[row] = -INFINITY;
+        }
+        release();
+        continue;
+      }
+      const uint32_t* mk = masks + ri * C::kMaskWords;
+      // this row's interval, and of the next stage which halves the row block selected,
+      // which of them the mask cuts, and there the positions of this lane's columns
+      uint32_t ilo = 0u, ilen = 0u;
+      const int32_t* pos0 = p.mask.pos;
+      int32_t kpos[4];
+      bool has1 = true, has2 = true, cut1 = false, cut2 = false;
+      RowGroups groups{};
+      UnionSeek seek(bits + ri * 2 * C::MAXW, bits + ri * 2 * C::MAXW + C::MAXW, PAIR ? words : 0);
+      auto next = [&](int e) {
+        if constexpr (PAIR) {
+          const uint32_t code = reinterpret_cast<const uint8_t*>(mk)[e] >> half;   // bits 0, 4: selected; 2, 6: cut
+          has1 = code & 1u;
+          has2 = (code >> 4) & 1u;
+          cut1 = has1 && ((code >> 2) & 1u);
+          cut2 = has2 && ((code >> 6) & 1u);
+        } else {
+          has1 = has2 = true;
+          cut1 = cut2 = (mk[e >> 5] >> (e & 31)) & 1u;
+        }
+        if (!cut1 && !cut2) return;
+        int64_t j1, j2;
+        if constexpr (PAIR) {
+          j1 = seek.at(2 * e);
+          j2 = cut2 ? seek.at(2 * e + 1) : j1;
+        } else {
+          j1 = j2 = __ldg(p.col_idx + p.row_ptr[item] + e);
+        }
+        kpos[0] = __ldg(pos0 + j1 * BT);
+        kpos[1] = __ldg(pos0 + j1 * BT + 32);
+        kpos[2] = __ldg(pos0 + j2 * BT + (PAIR ? 0 : 64));
+        kpos[3] = __ldg(pos0 + j2 * BT + (PAIR ? 32 : 96));
+      };
+      if (p.mask.pos != nullptr) {
+        const int64_t tok0 = bh / p.rm.H * p.N;   // this batch element's first token
+        pos0 += tok0 + lane;
+        if (i < nb) {
+          ilo = (uint32_t)__ldg(p.mask.lo + tok0 + (int64_t)i * BT + o);
+          ilen = __ldg(p.mask.len + tok0 + (int64_t)i * BT + o);
+        }
+        groups.make(ilo, ilen, lane);
+      }
+      next(0);
+      float m = -INFINITY, l = 0.f;
+      // O *= f; O must not change under the PV of block g - 1 (g = global block index)
+      auto rescale = [&](uint64_t gb, float f) -> bool {
+        const uint64_t gp = gb - 1;
+        if (!wait_warp(bar(PV_DONE + (uint32_t)(gp % C::NPB)), (uint32_t)((gp / C::NPB) & 1u), g)) return false;
+        fence_after();
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t ov[32];
+          tmem_ld32(t_row + C::kColO + c * 32u, ov);
+          wait_ld();
+#pragma unroll
+          for (int x = 0; x < 32; ++x) ov[x] = __float_as_uint(__uint_as_float(ov[x]) * f);
+          tmem_st32(t_row + C::kColO + c * 32u, ov);
+        }
+        return true;
+      };
+      for (int e = 0; e < len; ++e) {
+        const uint32_t b = s_use % C::NSB;
+        const uint64_t gb = blocks_done + e;
+        // a stage whose scores all count as they are: the plain kernel's
+        auto stage = [&]() -> bool {
+          const bool h1 = PAIR ? has1 : true, h2 = PAIR ? has2 : true;
+          if (!wait_warp(bar(S_FULL + b), (s_use / C::NSB) & 1u, g)) return false;
+          fence_after();
+          uint32_t s[C::KR];
+          float cm[C::KR / 32];
+#pragma unroll
+          for (int c = 0; c < C::KR / 32; ++c)
+            cm[c] = tmem_ld32_max(t_row + C::kColS + b * 128u + c * 32u, s + 32 * c);
+          wait_ld();
+          fence_before();
+          arrive(bar(S_FREE + b));
+          ++s_use;
+          if (!h1) cm[0] = cm[1] = -INFINITY;
+          if (!h2) cm[2] = cm[3] = -INFINITY;
+          const float m_new = fmaxf(m, fmaxf(fmaxf(cm[0], cm[1]), fmaxf(cm[2], cm[3])) * sl2);
+          bool resc = false;
+          float f = 1.f;
+          if (__any_sync(0xffffffffu, m_new > m + kRescaleThreshold)) {
+            resc = e > 0;
+            f = ex2f(m - m_new);
+            m = m_new;
+          }
+          uint32_t pk[C::KR / 2];
+          float rs[8];
+#pragma unroll
+          for (int u = 0; u < 8; ++u) rs[u] = 0.f;
+#pragma unroll
+          for (int hh = 0; hh < 2; ++hh) {
+            if (hh == 0 ? h1 : h2) {
+#pragma unroll
+              for (int c = 32 * hh; c < 32 * hh + 32; ++c) {
+                float x0, x1;
+                fma_x2(__uint_as_float(s[2 * c]), __uint_as_float(s[2 * c + 1]), sl2, -m, x0, x1);
+                const float p0 = ex2f(x0), p1 = ex2f(x1);
+                add_x2(rs[2 * (c & 3)], rs[2 * (c & 3) + 1], p0, p1);
+                pk[c] = pack2(p0, p1);
+              }
+            } else {
+#pragma unroll
+              for (int c = 32 * hh; c < 32 * hh + 32; ++c) pk[c] = 0u;
+            }
+          }
+          if (gb >= (uint64_t)C::NPB) {   // P buffer b was last read by the PV of block g - NPB
+            if (!wait_warp(bar(PV_DONE + b), (uint32_t)(((gb - C::NPB) / C::NPB) & 1u), g)) return false;
+            fence_after();
+          }
+#pragma unroll
+          for (int c = 0; c < C::KR / 64; ++c) tmem_st32(t_row + C::kColP + b * 64u + 32u * c, pk + 32 * c);
+          if (resc) {
+            if (!rescale(gb, f)) return false;
+            l *= f;
+          }
+          l += ((rs[0] + rs[1]) + (rs[2] + rs[3])) + ((rs[4] + rs[5]) + (rs[6] + rs[7]));
+          return true;
+        };
+        // A stage the mask cuts for some row of the warp, or (MOD 3) one with a cap:
+        // half by half through TMEM in a loop that is not unrolled (unrolled, the
+        // variants of a stage do not stay in the instruction cache), against
+        // the maximum of the stages before; when that is outgrown by more than the
+        // threshold it starts over with the stage's own.
+        auto stage_mod = [&]() -> bool {
+          // bit c of see[w]: this row sees column 32 w + c; a half that no row of the
+          // warp sees counts as not selected
+          uint32_t see[4] = {0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu};
+          if (cut1) {
+            query_bits(groups, ilo, ilen, kpos[0], kpos[1], lane, see[0], see[1]);
+            has1 = __any_sync(0xffffffffu, (see[0] | see[1]) != 0u);
+          }
+          if (cut2) {
+            query_bits(groups, ilo, ilen, kpos[2], kpos[3], lane, see[2], see[3]);
+            has2 = __any_sync(0xffffffffu, (see[2] | see[3]) != 0u);
+          }
+          if (!wait_warp(bar(S_FULL + b), (s_use / C::NSB) & 1u, g)) return false;
+          fence_after();
+          if (gb >= (uint64_t)C::NPB) {
+            if (!wait_warp(bar(PV_DONE + b), (uint32_t)(((gb - C::NPB) / C::NPB) & 1u), g)) return false;
+            fence_after();
+          }
+          // a half's scores (masked ones -inf) and their maximum in log2 units, capped
+          uint32_t s[64];
+          auto load_half = [&](int hh) -> float {
+            const uint32_t ts = t_row + C::kColS + b * 128u + hh * 64u;
+            tmem_ld32(ts, s);
+            tmem_ld32(ts + 32u, s + 32);
+            wait_ld();
+            const uint32_t w0 = hh ? see[2] : see[0], w1 = hh ? see[3] : see[1];
+            float mw[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+            for (int c = 0; c < 64; c += 2) {
+              const uint32_t w = c < 32 ? w0 : w1;
+              if (!((w >> (c & 31)) & 1u)) s[c] = 0xff800000u;
+              if (!((w >> ((c + 1) & 31)) & 1u)) s[c + 1] = 0xff800000u;
+              mw[(c >> 1) & 1] = fmaxf(fmaxf(mw[(c >> 1) & 1], __uint_as_float(s[c])), __uint_as_float(s[c + 1]));
+            }
+            const float mx = fmaxf(mw[0], mw[1]);
+            if (MOD != 3) return mx * sl2;
+            return mx == -INFINITY ? mx : cap_exp(mx * p.c1, p.cap2);
+          };
+          bool known = false, resc = false;
+          float f = 1.f;
+          float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll 1
+          for (int hh = 0; hh < 2;) {
+            uint32_t pk[32];
+            if (!(hh == 0 ? has1 : has2)) {
+#pragma unroll
+              for (int c = 0; c < 32; ++c) pk[c] = 0u;
+              tmem_st32(t_row + C::kColP + b * 64u + 32u * hh, pk);
+              ++hh;
+              continue;
+            }
+            const float mx = load_half(hh);
+            if (!known && __any_sync(0xffffffffu, mx > m + kRescaleThreshold)) {
+              float m_new = fmaxf(m, mx);
+              if (hh == 0 ? has2 : has1) m_new = fmaxf(m_new, load_half(hh ^ 1));
+              known = true;
+              resc = e > 0;
+              f = m_new == -INFINITY ? 1.f : ex2f(m - m_new);
+              m = m_new;
+              sum[0] = sum[1] = make_float2(0.f, 0.f);
+              hh = 0;
+              continue;
+            }
+            // a row that has seen no key yet: every exponent is -inf against 0
+            const float mr = m == -INFINITY ? 0.f : m;
+#pragma unroll
+            for (int c = 0; c < 32; ++c) {
+              const float s0 = __uint_as_float(s[2 * c]), s1 = __uint_as_float(s[2 * c + 1]);
+              float x0, x1;
+              if constexpr (MOD != 3) {
+                fma_x2(s0, s1, sl2, -mr, x0, x1);
+              } else {   // the cap would bring a masked score back
+                x0 = s0 == -INFINITY ? s0 : cap_exp(s0 * p.c1, p.cap2) - mr;
+                x1 = s1 == -INFINITY ? s1 : cap_exp(s1 * p.c1, p.cap2) - mr;
+              }
+              const float p0 = ex2f(x0), p1 = ex2f(x1);
+              add_x2(sum[c & 1].x, sum[c & 1].y, p0, p1);
+              pk[c] = pack2(p0, p1);
+            }
+            tmem_st32(t_row + C::kColP + b * 64u + 32u * hh, pk);
+            ++hh;
+          }
+          fence_before();
+          arrive(bar(S_FREE + b));
+          ++s_use;
+          if (resc) {
+            if (!rescale(gb, f)) return false;
+            l *= f;
+          }
+          l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+          return true;
+        };
+        if constexpr (MOD == 3) ok = stage_mod();
+        else ok = cut1 || cut2 ? stage_mod() : stage();
+        if (!ok) break;
+        wait_st();
+        fence_before();
+        arrive(bar(P_FULL + b));
+        if (e + 1 < len) next(e + 1);
+      }
+      release();
+      if (!ok) break;
+      blocks_done += (uint64_t)len;
+      if (!(ok = wait_warp(bar(O_FULL), o_items & 1u, g))) break;
+      ++o_items;
+      fence_after();
+      const float inv = l > 0.f ? 1.0f / l : 0.f;   // 0: the row saw no key
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c) {
+        uint32_t ov[32];
+        tmem_ld32(t_row + C::kColO + c * 32u, ov);
+        wait_ld();
+        if (!stores) continue;
+        uint32_t w[16];
+#pragma unroll
+        for (int x = 0; x < 16; ++x)
+          w[x] = pack2(__uint_as_float(ov[2 * x]) * inv, __uint_as_float(ov[2 * x + 1]) * inv);
+#pragma unroll
+        for (int x = 0; x < 4; ++x) orow[c * 4 + x] = make_uint4(w[4 * x], w[4 * x + 1], w[4 * x + 2], w[4 * x + 3]);
+      }
+      fence_before();
+      arrive(bar(O_EMPTY));
+      if (stores) p.lse[row] = l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
+    }
   } else {
     if constexpr (C::DUO) regs_increase<C::kRegSoftmax>();
     {
@@ -657,68 +1167,8 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
           continue;
         }
         const uint32_t* mk = masks + ri * C::kMaskWords;
-        // MOD: this row's interval, the key blocks of the next stage and their
-        // ranges (fetched a stage ahead), and the positions of this lane's four
-        // columns where the mask cuts the stage
-        uint32_t ilo = 0u, ilen = 0u;
-        int64_t tok0 = 0, blk0 = 0;      // this batch element's first token and block
-        int n1 = 0, n2 = 0;
-        int2 kr1 = make_int2(0, 0), kr2 = kr1;
-        int32_t kpos[4];
-        int32_t e0 = 0;
-        bool masked = false, full1 = true, full2 = true;
-        RowGroups groups{};
-        UnionWalk walk(bits + ri * 2 * C::MAXW, bits + ri * 2 * C::MAXW + C::MAXW, PAIR && MOD != 0 ? words : 0);
-        auto next_blocks = [&](int e) {   // key blocks of stage e
-          if constexpr (PAIR) {
-            n1 = walk.next();
-            n2 = walk.next();
-            if (n2 < 0) n2 = n1;
-          } else {
-            n1 = n2 = __ldg(p.col_idx + e0 + e);
-          }
-          kr1 = __ldg(p.mask.krange + blk0 + n1);
-          if (PAIR) kr2 = __ldg(p.mask.krange + blk0 + n2);
-        };
-        auto next_cut = [&]() {   // does the mask cut the fetched blocks, and where
-          full1 = __all_sync(0xffffffffu, (uint32_t)kr1.x - ilo < ilen && (uint32_t)kr1.y - ilo < ilen);
-          full2 = PAIR ? __all_sync(0xffffffffu, (uint32_t)kr2.x - ilo < ilen && (uint32_t)kr2.y - ilo < ilen) : full1;
-          if (!full1 || !full2) {
-            const int32_t* kp = p.mask.pos + tok0 + lane;
-            kpos[0] = __ldg(kp + (int64_t)n1 * BT);
-            kpos[1] = __ldg(kp + (int64_t)n1 * BT + 32);
-            kpos[2] = __ldg(kp + (int64_t)n2 * BT + (PAIR ? 0 : 64));
-            kpos[3] = __ldg(kp + (int64_t)n2 * BT + (PAIR ? 32 : 96));
-          }
-        };
-        if constexpr (MOD != 0) {
-          masked = p.mask.pos != nullptr;
-          if (masked) {
-            const int64_t b = bh / p.rm.H;
-            tok0 = b * p.N;
-            blk0 = b * nb;
-            if (i < nb) {
-              ilo = (uint32_t)__ldg(p.mask.lo + tok0 + (int64_t)i * BT + o);
-              ilen = __ldg(p.mask.len + tok0 + (int64_t)i * BT + o);
-            }
-            groups.make(ilo, ilen, lane);
-            if (!PAIR) e0 = p.row_ptr[item];
-            next_blocks(0);
-            next_cut();
-          }
-        }
         float m = -INFINITY, l = 0.f;
         for (int e = 0; e < len; ++e) {
-          // bit c of see[h]: this row sees column 32 h + c
-          uint32_t see[4] = {0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu};
-          const bool cut1 = MOD != 0 && !full1, cut2 = MOD != 0 && !full2;
-          if constexpr (MOD != 0) {
-            if (masked) {
-              if (cut1) query_bits(groups, ilo, ilen, kpos[0], kpos[1], lane, see[0], see[1]);
-              if (cut2) query_bits(groups, ilo, ilen, kpos[2], kpos[3], lane, see[2], see[3]);
-              if (e + 1 < len) next_blocks(e + 1);
-            }
-          }
           // which halves of this stage's 128 columns this row attends to (warp-uniform)
           bool has1 = true, has2 = true;
           if constexpr (PAIR && C::MASK_BYTES) {
@@ -743,33 +1193,12 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
           fence_before();
           mbar_arrive(bar(S_FREE + b));
           ++s_use;
-          if constexpr (MOD != 0) {
-            // masked scores become -inf, and the maxima are those of what is left
-            auto mask_half = [&](int hh) {
-  #pragma unroll
-              for (int w = 2 * hh; w < 2 * hh + 2; ++w) {
-                float mw = -INFINITY;
-  #pragma unroll
-                for (int c = 0; c < 32; c += 2) {
-                  if (!((see[w] >> c) & 1u)) s[32 * w + c] = 0xff800000u;
-                  if (!((see[w] >> (c + 1)) & 1u)) s[32 * w + c + 1] = 0xff800000u;
-                  mw = fmaxf(fmaxf(mw, __uint_as_float(s[32 * w + c])), __uint_as_float(s[32 * w + c + 1]));
-                }
-                cm[w] = mw;
-              }
-            };
-            if (cut1 && has1) mask_half(0);
-            if (cut2 && has2) mask_half(1);
-          }
           if (!has1) cm[0] = cm[1] = -INFINITY;
           if (!has2) cm[2] = cm[3] = -INFINITY;
           float mx = cm[0];
   #pragma unroll
           for (int c = 1; c < C::KR / 32; ++c) mx = fmaxf(mx, cm[c]);
-          // the exponent's reference in log2 units (of the capped maximum with MOD 2)
-          if (MOD == 2 && mx > -INFINITY) mx = fmaf(rcpf(1.f + ex2f(mx * p.c1)), -2.f * p.cap2, p.cap2);
-          else if (MOD != 2) mx *= sl2;
-          const float m_new = fmaxf(m, mx);
+          const float m_new = fmaxf(m, mx * sl2);
           // a rescale of O (by f) is applied after P is written, when the S row is
           // no longer held in registers
           bool resc = false;
@@ -778,53 +1207,31 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
             m = m_new;
           } else if (__any_sync(0xffffffffu, m_new > m + kRescaleThreshold)) {
             resc = true;
-            f = MOD != 0 && m_new == -INFINITY ? 1.f : ex2f(m - m_new);
+            f = ex2f(m - m_new);
             m = m_new;
           }
-          // a row that has seen no key yet: every exponent is -inf against 0
-          const float mr = MOD != 0 && m == -INFINITY ? 0.f : m;
           uint32_t pk[C::KR / 2];
           float rs[8];
   #pragma unroll
           for (int u = 0; u < 8; ++u) rs[u] = 0.f;
-          // two columns per instruction for the scale-and-subtract and the sums
-          // (packed fp32 pairs: eight running sums, even and odd columns)
-          auto exp_pair = [&](int c, float x0, float x1) {
-            const float p0 = ex2f(x0), p1 = ex2f(x1);
-            add_x2(rs[2 * (c & 3)], rs[2 * (c & 3) + 1], p0, p1);
-            pk[c] = pack2(p0, p1);
-          };
   #pragma unroll
           for (int hh = 0; hh < 2; ++hh) {
             // columns [64*hh, 64*hh + 64): one key block of a pair (both halves of
             // one block otherwise)
-            if (!(hh == 0 ? has1 : has2)) {
-  #pragma unroll
-              for (int c = 32 * hh; c < 32 * hh + 32; ++c) pk[c] = 0u;
-            } else if (MOD != 2) {
+            if (hh == 0 ? has1 : has2) {
+              // two columns per instruction for the scale-and-subtract and the sums
+              // (packed fp32 pairs: eight running sums, even and odd columns)
   #pragma unroll
               for (int c = 32 * hh; c < 32 * hh + 32; ++c) {
                 float x0, x1;
-                fma_x2(__uint_as_float(s[2 * c]), __uint_as_float(s[2 * c + 1]), sl2, -mr, x0, x1);
-                exp_pair(c, x0, x1);
-              }
-            } else if (!(hh == 0 ? cut1 : cut2)) {
-  #pragma unroll
-              for (int c = 32 * hh; c < 32 * hh + 32; ++c) {
-                float x0 = rcpf(1.f + ex2f(__uint_as_float(s[2 * c]) * p.c1));
-                float x1 = rcpf(1.f + ex2f(__uint_as_float(s[2 * c + 1]) * p.c1));
-                fma_x2(x0, x1, -2.f * p.cap2, p.cap2 - mr, x0, x1);
-                exp_pair(c, x0, x1);
+                fma_x2(__uint_as_float(s[2 * c]), __uint_as_float(s[2 * c + 1]), sl2, -m, x0, x1);
+                const float p0 = ex2f(x0), p1 = ex2f(x1);
+                add_x2(rs[2 * (c & 3)], rs[2 * (c & 3) + 1], p0, p1);
+                pk[c] = pack2(p0, p1);
               }
             } else {
   #pragma unroll
-              for (int c = 32 * hh; c < 32 * hh + 32; ++c) {
-                const float s0 = __uint_as_float(s[2 * c]), s1 = __uint_as_float(s[2 * c + 1]);
-                float x0 = rcpf(1.f + ex2f(s0 * p.c1)), x1 = rcpf(1.f + ex2f(s1 * p.c1));
-                fma_x2(x0, x1, -2.f * p.cap2, p.cap2 - mr, x0, x1);
-                // the cap brings a masked score back to -cap
-                exp_pair(c, s0 == -INFINITY ? s0 : x0, s1 == -INFINITY ? s1 : x1);
-              }
+              for (int c = 32 * hh; c < 32 * hh + 32; ++c) pk[c] = 0u;
             }
           }
           // P buffer b was last read by the PV of block g - NPB
@@ -855,7 +1262,6 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
           wait_st();
           fence_before();
           mbar_arrive(bar(P_FULL + b));
-          if (MOD != 0 && masked && e + 1 < len) next_cut();
           }
         }
         if (PAIR) release();
@@ -898,7 +1304,7 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
 template <int BT, int D, int MOD>
 sparsp_status_t go_fwd(const Dims& s, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                        const Params& prm, cudaStream_t st) {
-  using C = Cfg<BT, D>;
+  using C = Cfg<BT, D, MOD>;
   auto kern = attn_fwd_tc_kernel<BT, D, MOD>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmemBytes) != cudaSuccess)
     return SPARSP_ERR_CUDA;
@@ -936,7 +1342,8 @@ sparsp_status_t launch_fwd_mod(const Dims& s, const __nv_bfloat16* q, const __nv
   constexpr float kLog2e = 1.4426950408889634f;
   Params prm{row_ptr, col_idx, s.N, s.nb, nbp, (int64_t)s.B * s.H * nbp, (int64_t)rows, scale * kLog2e, o, lse,
              raster ? 1 : 0, raster_map(s), in_raster ? 1 : 0, raster_box(s), items, counter, prof, d_status,
-             mask, MOD == 2 ? 2.f * scale * kLog2e / cap : 0.f, cap * kLog2e};
+             mask, MOD >= 2 ? 2.f * scale * kLog2e / cap : 0.f, cap * kLog2e,
+             MOD >= 2 ? scale / cap : 0.f};
   if (s.Bt == 128 && s.d == 128) return go_fwd<128, 128, MOD>(s, tq, tk, tv, prm, st);
   if (s.Bt == 128 && s.d == 64) return go_fwd<128, 64, MOD>(s, tq, tk, tv, prm, st);
   if (s.Bt == 64 && s.d == 128) return go_fwd<64, 128, MOD>(s, tq, tk, tv, prm, st);

@@ -1,0 +1,69 @@
+// The score cap y = cap tanh(x), x = scale s / cap, in log2 units (cap2 = cap
+// log2 e), for the tcgen05 attention kernels.
+#pragma once
+
+#include "tc_helpers.cuh"
+
+namespace sparsp {
+namespace tc {
+
+__device__ __forceinline__ float rcpf(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float exp2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// tanh(x) / x on |x| <= 1 as a polynomial of degree 6 in x^2: least squares on
+// Chebyshev points, reweighted until the largest relative error is flat
+// (Lawson's iteration); 5e-8 in exact arithmetic, 1.7e-7 evaluated in fp32.
+// Seven multiply-adds, against an exponential and a reciprocal on the unit that
+// already has the softmax's exponentials to do.
+__device__ constexpr float tanh_coef(int k) {
+  return k == 0   ? 0.9999999403953552f
+         : k == 1 ? -0.33332839608192444f
+         : k == 2 ? 0.13325203955173492f
+         : k == 3 ? -0.05345702916383743f
+         : k == 4 ? 0.020289979875087738f
+         : k == 5 ? -0.006203378085047007f
+                  : 0.001041022245772183f;
+}
+
+__device__ __forceinline__ float cap_poly(float x) {
+  const float u = x * x;
+  float q = tanh_coef(6);
+#pragma unroll
+  for (int k = 5; k >= 0; --k) q = fmaf(q, u, tanh_coef(k));
+  return x * q;
+}
+
+// cap2 tanh by its definition, t = 2 x log2(e): 1 - 2 / (1 + exp(2 x)), for any x
+// (good to a few 2^-24 of the cap).
+__device__ __forceinline__ float cap_exp(float t, float cap2) {
+  return fmaf(rcpf(1.f + exp2_approx(t)), -2.f * cap2, cap2);
+}
+
+// tanh of a pair of scores, x = s inv_cap, by the polynomial
+__device__ __forceinline__ void tanh_poly_x2(float s0, float s1, float inv_cap, float& t0, float& t1) {
+  float x0, x1, u0, u1, q0, q1;
+  mul_x2(s0, s1, inv_cap, inv_cap, x0, x1);
+  mul_x2(x0, x1, x0, x1, u0, u1);
+  fma_x2(u0, u1, tanh_coef(6), tanh_coef(5), q0, q1);
+#pragma unroll
+  for (int k = 4; k >= 0; --k) fma2_x2(q0, q1, u0, u1, tanh_coef(k), q0, q1);
+  mul_x2(x0, x1, q0, q1, t0, t1);
+}
+// cap2 tanh + add of a pair of scores
+__device__ __forceinline__ void cap_poly_x2(float s0, float s1, float inv_cap, float cap2, float add, float& y0,
+                                            float& y1) {
+  float t0, t1;
+  tanh_poly_x2(s0, s1, inv_cap, t0, t1);
+  fma_x2(t0, t1, cap2, add, y0, y1);
+}
+
+}  // namespace tc
+}  // namespace sparsp

@@ -21,6 +21,9 @@ struct MaskView {
 // May some query of a block with hull q see some key of a block with range k?
 __device__ __forceinline__ bool blocks_meet(const int2& q, const int2& k) { return k.y >= q.x && k.x < q.y; }
 
+// Does every query of a block with common range q see every key of a block with range k?
+__device__ __forceinline__ bool all_seen(const int2& q, const int2& k) { return q.x <= k.x && k.y < q.y; }
+
 // Rows of a warp that see alike. The 32 rows of a warp hold few different
 // intervals (or positions), so the keys each row sees come as bits from one
 // ballot per group and 32 columns, not from a comparison per score.

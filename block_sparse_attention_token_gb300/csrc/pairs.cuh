@@ -143,5 +143,66 @@ __device__ __forceinline__ void union_masks2(const uint32_t* a, const uint32_t* 
   __syncwarp();
 }
 
+// Masks with a cut beside them (token masks): per union block of rank r a
+// 4-bit code, bits 0, 1 = which list holds the block (as above) and bits 2, 3 =
+// cut(j), whether the token mask cuts the pair of the first / second row block
+// with block j. BYTES: one byte per block (stage s = bytes 2s, 2s + 1), else one
+// nibble (stage s = byte s). mk holds 32 * words codes and one more, cleared
+// here; warp-collective.
+template <bool BYTES, typename Cut>
+__device__ __forceinline__ void union_codes(const uint32_t* a, const uint32_t* b, int words, int u, int lane,
+                                            uint32_t* mk, Cut cut) {
+  const int nw = BYTES ? (u + 4) / 4 : (u + 8) / 8;
+  for (int w = lane; w < nw; w += 32) mk[w] = 0u;
+  __syncwarp();
+  int base_rank = 0;
+  for (int w0 = 0; w0 < words; w0 += 32) {
+    const int w = w0 + lane;
+    const uint32_t x = w < words ? a[w] : 0u, y = w < words ? b[w] : 0u;
+    uint32_t un = x | y;
+    const int c = __popc(un);
+    int incl = c;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int t = __shfl_up_sync(0xffffffffu, incl, off);
+      if (lane >= off) incl += t;
+    }
+    int rk = base_rank + incl - c;
+    for (; un != 0u; un &= un - 1u, ++rk) {
+      const int bit = __ffs(un) - 1;
+      const uint32_t code = ((x >> bit) & 1u) | (((y >> bit) & 1u) << 1) | (cut(w * 32 + bit) << 2);
+      if (BYTES) reinterpret_cast<uint8_t*>(mk)[rk] = (uint8_t)code;
+      else atomicOr(&mk[rk >> 3], code << (4 * (rk & 7)));
+    }
+    base_rank += __shfl_sync(0xffffffffu, incl, 31);
+  }
+  __syncwarp();
+}
+
+// The block of a given rank in the union of two bitmaps, for ascending ranks.
+struct UnionSeek {
+  const uint32_t* a;
+  const uint32_t* b;
+  int words, w, rank;   // rank of the lowest bit left in cur
+  uint32_t cur;
+  __device__ __forceinline__ UnionSeek(const uint32_t* a_, const uint32_t* b_, int words_)
+      : a(a_), b(b_), words(words_), w(0), rank(0), cur(words_ > 0 ? (a_[0] | b_[0]) : 0u) {}
+  // -1 past the last block
+  __device__ __forceinline__ int at(int r) {
+    int c = __popc(cur);
+    while (r - rank >= c) {
+      rank += c;
+      if (++w >= words) {
+        cur = 0u;
+        return -1;
+      }
+      cur = a[w] | b[w];
+      c = __popc(cur);
+    }
+    for (; rank < r; ++rank) cur &= cur - 1u;
+    return w * 32 + __ffs(cur) - 1;
+  }
+};
+
 }  // namespace tc
 }  // namespace sparsp

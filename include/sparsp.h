@@ -579,7 +579,7 @@ SPARSP_API sparsp_status_t sparsp_mask_scores(const sparsp_shape_t* shape, const
  *   y = scale q.k, or cap tanh(scale q.k / cap) where cap > 0,
  *   O_q = sum_k softmax_k(y) v_k,   LSE_q = ln sum_k exp(y).
  * plan: of sparsp_mask_plan for this shape, or NULL (every key is seen). cap = 0:
- * no cap. A query that sees no key gives O = 0, LSE = -inf. Block pairs that
+ * no cap, else 2^-20 <= cap <= 2^20 (SPARSP_ERR_INVALID_ARG outside). A query that sees no key gives O = 0, LSE = -inf. Block pairs that
  * see nothing of each other are dropped before the work is ordered. Values in
  * keys that a query does not see must be finite (their weight is 0, and 0 times
  * infinity is not). A malformed row (an index outside [0, nb), more than nb
