@@ -218,6 +218,7 @@ struct Params {
   MaskView mask;      // MOD != 0; mask.pos null: no mask
   // MOD 2, 3: 2 scale log2(e) / cap, cap log2(e) and scale / cap
   float c1, cap2, inv_cap;
+  NearCap near;
 };
 
 template <int BT, int D, int MOD>
@@ -752,15 +753,21 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
           for (int x = 0; x < 32; x += 2)
             big[(x >> 1) & 1] = fmaxf(fmaxf(big[(x >> 1) & 1], fabsf(__uint_as_float(s[x]))),
                                       fabsf(__uint_as_float(s[x + 1])));
-          const bool within = __all_sync(0xffffffffu, fmaxf(big[0], big[1]) * p.inv_cap <= 1.f);
-          auto probs = [&](auto poly_c, auto cut_c) {
-            constexpr bool POLY = decltype(poly_c)::value, CUT = decltype(cut_c)::value;
+          // the largest score of the warp's chunk says which form of the cap holds
+          const float most = fmaxf(big[0], big[1]);
+          const bool near = __all_sync(0xffffffffu, most <= p.near.limit);
+          auto probs = [&](auto form_c, auto cut_c) {
+            constexpr int FORM = decltype(form_c)::value;
+            constexpr bool CUT = decltype(cut_c)::value;
 #pragma unroll
             for (int x = 0; x < 16; ++x) {
               const float s0 = __uint_as_float(s[2 * x]), s1 = __uint_as_float(s[2 * x + 1]);
               float y0, y1;
-              if constexpr (POLY) {
-                cap_poly_x2(s0, s1, p.inv_cap, p.cap2, 0.f, y0, y1);
+              if constexpr (FORM == 0) {
+                near_cap_x2(p.near, s0, s1, y0, y1);
+              } else if constexpr (FORM == 1) {
+                tanh_poly_x2(s0, s1, p.inv_cap, y0, y1);
+                mul_x2(y0, y1, p.cap2, p.cap2, y0, y1);
               } else {
                 y0 = cap_exp(s0 * p.c1, p.cap2);
                 y1 = cap_exp(s1 * p.c1, p.cap2);
@@ -774,9 +781,14 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
               pk[x] = pack2(p0, p1);
             }
           };
-          if (!within) probs(std::false_type{}, std::true_type{});
-          else if ((cut >> (c >> 1)) & 1u) probs(std::true_type{}, std::true_type{});
-          else probs(std::true_type{}, std::false_type{});
+          if (near) {
+            if ((cut >> (c >> 1)) & 1u) probs(std::integral_constant<int, 0>{}, std::true_type{});
+            else probs(std::integral_constant<int, 0>{}, std::false_type{});
+          } else if (__all_sync(0xffffffffu, most * p.inv_cap <= 1.f)) {
+            probs(std::integral_constant<int, 1>{}, std::true_type{});
+          } else {
+            probs(std::integral_constant<int, 2>{}, std::true_type{});
+          }
           tmem_st16(tP + 16u * c, pk);
         }
         fence_before();
@@ -1343,7 +1355,8 @@ sparsp_status_t launch_fwd_mod(const Dims& s, const __nv_bfloat16* q, const __nv
   Params prm{row_ptr, col_idx, s.N, s.nb, nbp, (int64_t)s.B * s.H * nbp, (int64_t)rows, scale * kLog2e, o, lse,
              raster ? 1 : 0, raster_map(s), in_raster ? 1 : 0, raster_box(s), items, counter, prof, d_status,
              mask, MOD >= 2 ? 2.f * scale * kLog2e / cap : 0.f, cap * kLog2e,
-             MOD >= 2 ? scale / cap : 0.f};
+             MOD >= 2 ? scale / cap : 0.f,
+             MOD == 2 ? near_cap(scale, cap) : NearCap{}};
   if (s.Bt == 128 && s.d == 128) return go_fwd<128, 128, MOD>(s, tq, tk, tv, prm, st);
   if (s.Bt == 128 && s.d == 64) return go_fwd<128, 64, MOD>(s, tq, tk, tv, prm, st);
   if (s.Bt == 64 && s.d == 128) return go_fwd<64, 128, MOD>(s, tq, tk, tv, prm, st);

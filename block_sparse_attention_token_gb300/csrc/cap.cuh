@@ -65,5 +65,35 @@ __device__ __forceinline__ void cap_poly_x2(float s0, float s1, float inv_cap, f
   fma_x2(t0, t1, cap2, add, y0, y1);
 }
 
+// Where all |x| <= kNearCap a polynomial of degree 4 in s^2 does (the same fit, 1.7e-7
+// evaluated in fp32), with the powers of scale / cap and the factor cap2 folded into
+// its coefficients: six multiply-adds from the score to y. `limit` is the largest
+// |s| it is for; 0 where the folded coefficients would leave fp32's range.
+constexpr float kNearCap = 0.6f;
+struct NearCap {
+  float c[5];
+  float limit;
+};
+inline NearCap near_cap(double scale, double cap) {
+  NearCap n{};
+  const double a = scale / cap;
+  if (!(a >= 1.0 / 16384 && a <= 16384.0)) return n;
+  const double t[5] = {0.9999999403953552, -0.33332309126853943, 0.13310173153877258, -0.05210147798061371,
+                       0.01547542680054903};
+  double f = cap * 1.4426950408889634 * a;
+  for (int k = 0; k < 5; ++k, f *= a * a) n.c[k] = (float)(t[k] * f);
+  n.limit = (float)(kNearCap / a);
+  return n;
+}
+// y of a pair of scores
+__device__ __forceinline__ void near_cap_x2(const NearCap& n, float s0, float s1, float& y0, float& y1) {
+  float u0, u1, q0, q1;
+  mul_x2(s0, s1, s0, s1, u0, u1);
+  fma_x2(u0, u1, n.c[4], n.c[3], q0, q1);
+#pragma unroll
+  for (int k = 2; k >= 0; --k) fma2_x2(q0, q1, u0, u1, n.c[k], q0, q1);
+  mul_x2(s0, s1, q0, q1, y0, y1);
+}
+
 }  // namespace tc
 }  // namespace sparsp
