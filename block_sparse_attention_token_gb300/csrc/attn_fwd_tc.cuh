@@ -94,10 +94,10 @@ struct Cfg {
   // soon as it is loaded) with the 200 registers the register split below
   // gives them.
   static constexpr bool DUO = D == 64 && MOD_ != 2;
-  static constexpr int NSM = MOD_ == 2 ? 8 : 4;           // softmax warps
+  static constexpr int NSM = MOD_ == 2 ? 16 : 4;           // softmax warps
   // arrivals of the softmax warps at S_FREE, P_FULL and O_EMPTY: every thread, or with
-  // MOD one lane of each of the four warps concerned
-  static constexpr int kArrivals = MOD_ == 0 ? 32 * NSM : 4;
+  // MOD one lane of each warp concerned
+  static constexpr int kArrivals = MOD_ == 0 ? 32 * NSM : MOD_ == 2 ? 8 : 4;
   // MMA issuer warps: S and PV each get their own with d = 128; with DUO one
   // warp issues both streams (the softmax releases S(e-1) before it writes
   // P(e-1), so S(e) then PV(e-1) in one warp never wait on each other)
@@ -115,10 +115,10 @@ struct Cfg {
                 "register split of the two warpgroups");
   // K and V ring stages: 3 of each fit beside a d = 128 query tile; a DUO CTA
   // has half of the SM's shared memory for tiles of half the size: 3 K and 2 V
-  // (four with MOD 2 and d = 64, which has a CTA's shared memory to itself; two V
-  // stages where its masks need the room of the third)
+  // (four with MOD 2 and d = 64, which has an SM's shared memory to itself; two V
+  // stages with d = 128, whose row sums and cut bits need the room of the third)
   static constexpr int NK = MOD_ == 2 && D == 64 ? 4 : 3;
-  static constexpr int NV = MOD_ == 2 && D == 64 ? 4 : DUO || (MOD_ == 2 && PAIR) ? 2 : 3;
+  static constexpr int NV = DUO || (MOD_ == 2 && D == 128) ? 2 : MOD_ == 2 ? 4 : 3;
   static constexpr int NSB = DUO ? 1 : 2, NPB = DUO ? 1 : 2;   // S and P buffers in TMEM
   static constexpr int NI = DUO || PAIR || MOD_ != 0 ? 2 : kNI;   // item ring slots
   static constexpr int kMinCtas = DUO ? 2 : 1;                  // CTAs per SM
@@ -147,8 +147,8 @@ struct Cfg {
   static constexpr uint32_t kMaskWords = !PAIR ? (MOD_ != 0 ? kMaxBlocks / 32 : 0)
                                                : (MASK_BYTES ? 8 * MAXW + 4 : (MOD_ != 0 ? 4 : 2) * MAXW + 1);
   static constexpr uint32_t kOffMask = kOffBits + kBitsBytes;
-  static constexpr uint32_t kOffEx = kOffMask + (NI * kMaskWords * 4 + 15) / 16 * 16;   // MOD 2: row sums of group 1
-  static constexpr uint32_t kOffMisc = kOffEx + (MOD_ == 2 ? 512 : 0);
+  static constexpr uint32_t kOffEx = kOffMask + (NI * kMaskWords * 4 + 15) / 16 * 16;   // MOD 2: parts of the row sums
+  static constexpr uint32_t kOffMisc = kOffEx + (MOD_ == 2 ? 2048 : 0);
   static constexpr uint32_t kSmemBytes = kOffMisc + 16 + 1024;   // + alignment slack
   static_assert(kSmemBytes <= (DUO ? 115712u : 232448u), "shared memory");
 };
@@ -270,7 +270,7 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
     mbar_init(bar(TEAR), 1);
     mbar_init(bar(TEAR_PV), 1);
     if (MOD != 0)
-      for (int r = 0; r < 8; ++r) mbar_init(bar(EXCH + r), 1);
+      for (int r = 0; r < 8; ++r) mbar_init(bar(EXCH + r), r < 4 ? 4 : 2);
     *abort_flag = 0;
     fence_barrier_init();
   }
@@ -639,20 +639,20 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
     // ------------------------------------------------------------ softmax + epilogue with a cap of at most kFixedCap
     // Capped scores lie in [-cap, cap], so exp needs no reference: P = exp2(y) and
     // the row sum stay far inside fp32 and bf16, and no maximum is taken, nothing is
-    // rescaled and stages do not depend on one another. Two groups of four
-    // warps take the stages in turn, whole rows each (group g the stages of S
-    // and P buffer g), so that the waits and loads of one run under the
-    // arithmetic of the other. The stage goes through TMEM 32 columns at a time in a
-    // loop that is not unrolled: unrolled, its variants do not stay in the
-    // instruction cache. Group 1 hands its part of the row sum to group 0, which
-    // writes O and LSE while group 1 goes on.
-    const int grp = warp >> 2, rw = warp & 3, t = (int)(threadIdx.x & 127);
+    // rescaled and stages do not depend on one another. Two groups of eight
+    // warps take the stages in turn (group g those of S and P buffer g), two warps
+    // per 32 rows with 64 columns each, so that the waits and loads of some run
+    // under the arithmetic of others. A warp goes through TMEM 32 columns at a
+    // time in a loop that is not unrolled: unrolled, its variants do not stay
+    // in the instruction cache. At the end of an item the parts of the row sum
+    // meet in shared memory and group 0 writes O and LSE while group 1 goes on.
+    const int grp = warp >> 3, hh = (warp >> 2) & 1, rw = warp & 3, t = (int)(threadIdx.x & 127);
     const uint32_t t_row = tmem + ((uint32_t)(rw * 32) << 16);
-    float* part = reinterpret_cast<float*>(gbase + C::kOffEx);   // [128] row sums of group 1
+    float* part = reinterpret_cast<float*>(gbase + C::kOffEx);   // [4][128] parts of the row sums
     uint32_t it_use = 0, turn = 0, o_items = 0;                  // turn: stages done by this group
     uint32_t stages_before = 0;                                  // of this CTA
     const int half = PAIR ? t >> 6 : 0;   // with pairs, rows 0-63 are query block 2p and rows 64-127 block 2p + 1
-    const uint32_t tS = t_row + C::kColS + grp * 128u, tP = t_row + C::kColP + grp * 64u;
+    const uint32_t tS = t_row + C::kColS + grp * 128u + hh * 64u, tP = t_row + C::kColP + grp * 64u + hh * 32u;
     auto arrive = [&](uint32_t bar_) {   // for the whole warp
       __syncwarp();
       if (lane == 0) mbar_arrive(bar_);
@@ -677,12 +677,12 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
       int64_t orow_idx = row;
       if (p.raster && stores) orow_idx = p.rm.row(bh, i, o);
       if (stores) stores = dcheck(row < p.rows_total && orow_idx >= 0 && orow_idx < p.rows_total, p.d_status);
-      uint4* orow = reinterpret_cast<uint4*>(p.o + orow_idx * D);
+      uint4* orow = reinterpret_cast<uint4*>(p.o + orow_idx * D) + hh * (D / 16);   // this thread's half of the row
       if (len == 0) {
         if (stores) {
 #pragma unroll
-          for (int c = 0; c < D / 8; ++c) orow[c] = make_uint4(0, 0, 0, 0);
-          p.lse[row] = -INFINITY;
+          for (int c = 0; c < D / 16; ++c) orow[c] = make_uint4(0, 0, 0, 0);
+          if (hh == 0) p.lse[row] = -INFINITY;
         }
         arrive(bar(I_EMPTY + ri));
         continue;
@@ -704,42 +704,31 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
       float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
       bool ok = true;
       for (int e = (grp ^ (int)(stages_before & 1u)); e < len; e += 2, ++turn) {
-        // bit h of has / cut: the row block selected the key block of half h (64
-        // columns), and the mask cuts it; the positions of this lane's columns there
-        uint32_t has = 3u, cut = 0u;
-        int32_t kp[4];
+        // did the row block select this half's key block, does the mask cut it, and the
+        // columns this row sees then
+        bool has = true, cut;
         if constexpr (PAIR) {
-          const uint32_t code = reinterpret_cast<const uint8_t*>(mk)[e] >> half;   // bits 0, 4: selected; 2, 6: cut
-          has = (code & 1u) | ((code >> 3) & 2u);
-          cut = has & (((code >> 2) & 1u) | ((code >> 5) & 2u));
+          const uint32_t code = reinterpret_cast<const uint8_t*>(mk)[e] >> (4 * hh + half);   // bit 0: selected; 2: cut
+          has = code & 1u;
+          cut = has && ((code >> 2) & 1u);
         } else {
-          cut = (mk[e >> 5] >> (e & 31)) & 1u ? 3u : 0u;
+          cut = (mk[e >> 5] >> (e & 31)) & 1u;
         }
-        uint32_t see[4] = {0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu};   // bit c: column 32 w + c
+        uint32_t see0 = 0xffffffffu, see1 = 0xffffffffu;
         if (cut) {
-          int64_t j1, j2;
-          if constexpr (PAIR) {
-            j1 = seek.at(2 * e);
-            j2 = cut & 2u ? seek.at(2 * e + 1) : j1;
-          } else {
-            j1 = j2 = __ldg(p.col_idx + p.row_ptr[item] + e);
-          }
-          kp[0] = __ldg(pos0 + j1 * BT);
-          kp[1] = __ldg(pos0 + j1 * BT + 32);
-          kp[2] = __ldg(pos0 + j2 * BT + (PAIR ? 0 : 64));
-          kp[3] = __ldg(pos0 + j2 * BT + (PAIR ? 32 : 96));
-          if (cut & 1u) query_bits(groups, ilo, ilen, kp[0], kp[1], lane, see[0], see[1]);
-          if (cut & 2u) query_bits(groups, ilo, ilen, kp[2], kp[3], lane, see[2], see[3]);
+          const int64_t j = PAIR ? seek.at(2 * e + hh) : __ldg(p.col_idx + p.row_ptr[item] + e);
+          const int32_t* kp = pos0 + j * BT + (PAIR ? 0 : 64 * hh);
+          query_bits(groups, ilo, ilen, __ldg(kp), __ldg(kp + 32), lane, see0, see1);
         }
         if (!(ok = wait_warp(bar(S_FULL + grp), turn & 1u, g))) break;
         if (turn > 0 && !(ok = wait_warp(bar(PV_DONE + grp), (turn - 1u) & 1u, g))) break;   // P buffer free again
         fence_after();
 #pragma unroll 1
-        for (int c = 0; c < 4; ++c) {
-          const uint32_t w = c == 0 ? see[0] : c == 1 ? see[1] : c == 2 ? see[2] : see[3];
+        for (int c = 0; c < 2; ++c) {
+          const uint32_t w = c == 0 ? see0 : see1;
           uint32_t pk[16];
           // columns no row of the warp sees (or of a block the row block did not select)
-          if (!((has >> (c >> 1)) & 1u) || !__any_sync(0xffffffffu, w != 0u)) {
+          if (!has || !__any_sync(0xffffffffu, w != 0u)) {
 #pragma unroll
             for (int x = 0; x < 16; ++x) pk[x] = 0u;
             tmem_st16(tP + 16u * c, pk);
@@ -782,7 +771,7 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
             }
           };
           if (near) {
-            if ((cut >> (c >> 1)) & 1u) probs(std::integral_constant<int, 0>{}, std::true_type{});
+            if (cut) probs(std::integral_constant<int, 0>{}, std::true_type{});
             else probs(std::integral_constant<int, 0>{}, std::false_type{});
           } else if (__all_sync(0xffffffffu, most * p.inv_cap <= 1.f)) {
             probs(std::integral_constant<int, 1>{}, std::true_type{});
@@ -801,24 +790,24 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
       arrive(bar(I_EMPTY + ri));
       stages_before += (uint32_t)len;
       float l = (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+      if (!wait_warp(bar(EXCH + 4 + rw), (o_items & 1u) ^ 1u, g)) break;   // the last item's parts were read
+      part[(2 * grp + hh) * 128 + t] = l;
+      arrive(bar(EXCH + rw));
       if (grp == 1) {
-        if (!wait_warp(bar(EXCH + 4 + rw), (o_items & 1u) ^ 1u, g)) break;   // the last item's sums were read
-        part[t] = l;
-        arrive(bar(EXCH + rw));
         ++o_items;
         continue;
       }
       if (!wait_warp(bar(EXCH + rw), o_items & 1u, g)) break;
-      l += part[t];
+      l = (part[t] + part[128 + t]) + (part[256 + t] + part[384 + t]);
       arrive(bar(EXCH + 4 + rw));
       if (!wait_warp(bar(O_FULL), o_items & 1u, g)) break;
       ++o_items;
       fence_after();
       const float inv = l > 0.f ? 1.0f / l : 0.f;   // 0: the row saw no key
 #pragma unroll 1
-      for (int c = 0; c < D / 32; ++c) {
+      for (int c = 0; c < D / 64; ++c) {
         uint32_t ov[32];
-        tmem_ld32(t_row + C::kColO + c * 32u, ov);
+        tmem_ld32(t_row + C::kColO + hh * (D / 2) + c * 32u, ov);
         wait_ld();
         if (!stores) continue;
         uint32_t w[16];
@@ -830,7 +819,7 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
       }
       fence_before();
       arrive(bar(O_EMPTY));
-      if (stores) p.lse[row] = l > 0.f ? log2f(l) * 0.69314718055994531f : -INFINITY;
+      if (stores && hh == 0) p.lse[row] = l > 0.f ? log2f(l) * 0.69314718055994531f : -INFINITY;
     }
   } else if constexpr (MOD != 0) {
     if constexpr (C::DUO) regs_increase<C::kRegSoftmax>();
