@@ -80,7 +80,6 @@ constexpr int TR = 128;   // rows of a row or column tile (the MMA's M; one bloc
 constexpr int kMaxNS = 4, kNI = 4;
 constexpr uint32_t kBox = TR * 64 * 2;        // one 64-column swizzled box of a 128-row tile
 constexpr uint32_t kStats = 1024;             // LSE*log2e [128] + D [128] of a column block
-constexpr int kThreads = 224;
 constexpr int HB = 64;   // columns of a half block
 enum Bar {
   A_FULL = 0, A_EMPTY, AT_FULL, C_FULL, C_EMPTY = C_FULL + kMaxNS, SD_FULL = C_EMPTY + kMaxNS,
@@ -103,6 +102,11 @@ template <int D_, int BTB_, int MOD_ = 0>
 struct BCfg {
   static constexpr int D = D_, BTB = BTB_;
   static constexpr bool PAIR = BTB == 64;
+  static constexpr int NRW = MOD_ == 0 ? 4 : 16;        // row warps, then the producer and the two issuers
+  static constexpr int THREADS = 32 * (NRW + 3);
+  static constexpr int W_PROD = NRW, W_S = NRW + 1, W_ACC = NRW + 2;
+  // arrivals of all row warps, and of a half's at X_FULL: every thread, or with MOD one lane per warp
+  static constexpr int kArrivals = MOD_ == 0 ? 128 : 16, kArrivalsX = MOD_ == 0 ? 128 : 8;
   static constexpr int NBOX = D / 64;
   static constexpr uint32_t kTile = TR * D * 2;
   static constexpr int kNS = D == 64 ? 4 : 2;   // column-tile stages
@@ -118,7 +122,6 @@ struct BCfg {
   // per slot: one byte per union block (+1); with MOD and no pairs one bit per
   // block of the list: does the token mask cut it
   static constexpr uint32_t kMaskBytes = PAIR ? 32 * MAXW : MOD_ != 0 ? kMaxBlocks / 8 : 0;
-  static constexpr bool HOLD = PAIR || MOD_ != 0;   // the row warps read the masks until the item ends
   static constexpr uint32_t kOffMask = kOffBits + kNI * 2 * MAXW * 4;
   static constexpr uint32_t kOffMisc = kOffMask + kNI * (kMaskBytes + (PAIR ? 16 : 0));
   static constexpr uint32_t kSmemBytes = kOffMisc + 16 + 1024;   // + alignment slack
@@ -168,11 +171,12 @@ struct Params {
   RasterMap rm;
   MaskView mask;      // MOD != 0; mask.pos null: no mask
   // MOD == 2: 2 scale log2(e) / cap, cap log2(e) and scale / cap
-  float c1, cap2, inv_cap;
+  float c1, cap2, inv_cap, inv_cap2;   // and 1 / cap2
+  NearCap near;
 };
 
 template <int MODE, int D, int BTB, int MOD>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(BCfg<D, BTB, MOD>::THREADS, 1)
 attn_bwd_tc_kernel(const __grid_constant__ CUtensorMap ta1, const __grid_constant__ CUtensorMap ta2,
                    const __grid_constant__ CUtensorMap tb1, const __grid_constant__ CUtensorMap tb2,
                    const Params p) {
@@ -201,35 +205,35 @@ attn_bwd_tc_kernel(const __grid_constant__ CUtensorMap ta1, const __grid_constan
 
   if (threadIdx.x == 0) {
     mbar_init(bar(A_FULL), 1);
-    mbar_init(bar(A_EMPTY), kRowsInTmem ? 128 : 1);   // else an MMA commit
-    mbar_init(bar(AT_FULL), 128);
+    mbar_init(bar(A_EMPTY), kRowsInTmem ? C::kArrivals : 1);   // else an MMA commit
+    mbar_init(bar(AT_FULL), C::kArrivals);
     for (int s = 0; s < kNS; ++s) {
       mbar_init(bar(C_FULL + s), 1);
       mbar_init(bar(C_EMPTY + s), 1);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(bar(SD_FULL + b), 1);
-      mbar_init(bar(X_FULL + b), 128);
+      mbar_init(bar(X_FULL + b), C::kArrivalsX);
       mbar_init(bar(X_DONE + b), 1);
     }
     mbar_init(bar(ACC_FULL), 1);
-    mbar_init(bar(ACC_EMPTY), 128);
+    mbar_init(bar(ACC_EMPTY), C::kArrivals);
     for (int r = 0; r < kNI; ++r) {
       mbar_init(bar(I_FULL + r), 1);
-      mbar_init(bar(I_EMPTY + r), 6);
+      mbar_init(bar(I_EMPTY + r), C::NRW + 2);
     }
     mbar_init(bar(TEAR), 1);
     mbar_init(bar(TEAR2), 1);
     *abort_flag = 0;
     fence_barrier_init();
   }
-  if (warp == 4 && lane == 0) {
+  if (warp == C::W_PROD && lane == 0) {
     prefetch_tmap(&ta1);
     prefetch_tmap(&ta2);
     prefetch_tmap(&tb1);
     prefetch_tmap(&tb2);
   }
-  if (warp == 5) {
+  if (warp == C::W_S) {
     tmem_alloc(smem_u32(tmem_slot), 512);
     tmem_relinquish();
   }
@@ -241,7 +245,7 @@ attn_bwd_tc_kernel(const __grid_constant__ CUtensorMap ta1, const __grid_constan
   const int nb = p.nb, nbp = p.nbp;
   const int words = (nb + 31) >> 5;
 
-  if (warp == 4) {
+  if (warp == C::W_PROD) {
     // ------------------------------------------------------------ producer
     uint32_t it_fill = 0, a_fill = 0, c_fill = 0;
     for (;;) {
@@ -396,7 +400,7 @@ attn_bwd_tc_kernel(const __grid_constant__ CUtensorMap ta1, const __grid_constan
       for (uint32_t s = 0; s < kNS; ++s)
         if (c_fill > s) wait_raw(bar(C_FULL + s), ((c_fill - 1 - s) / kNS) & 1u, kDrainNs);
     }
-  } else if (warp == 5) {
+  } else if (warp == C::W_S) {
     // ------------------------------------------------------------ S (and dP) issuer
     constexpr uint32_t idS = idesc_bf16(128, HB, 0, 0);
     uint32_t it_use = 0, a_use = 0, c_use = 0, hg = 0;
@@ -478,11 +482,13 @@ attn_bwd_tc_kernel(const __grid_constant__ CUtensorMap ta1, const __grid_constan
       wait_raw(bar(TEAR), 0, kDrainNs);
     }
     __syncwarp();
-  } else if (warp == 6) {
+  } else if (warp == C::W_ACC) {
     // ------------------------------------------------------------ accumulate issuer
     constexpr uint32_t idAcc = idesc_bf16(128, D, 0, 1);
     // the column tile the accumulator multiplies: K_c / Q_c (B1) or dO_c (B2)
     constexpr uint32_t kB3 = MODE == 2 ? kTile : 0u;
+    // TMEM column of X's k-step kk: packed, or with MOD over the S columns of the warp that wrote it
+    auto xcol = [](int kk) { return MOD == 0 ? (uint32_t)kk * 8u : 32u * (uint32_t)(kk >> 1) + 8u * (uint32_t)(kk & 1); };
     uint32_t it_use = 0, c_use = 0, hg = 0, acc_items = 0;
     bool issued_any = false;
     for (;;) {
@@ -511,18 +517,18 @@ attn_bwd_tc_kernel(const __grid_constant__ CUtensorMap ta1, const __grid_constan
               const uint32_t bq = stage(st), bdo = stage(st) + kTile;
 #pragma unroll
               for (int kk = 0; kk < HB / 16; ++kk)   // dV += P^T dO_c
-                mma_ts(tmem + C::kColAcc2, tmem + 128u * b + (uint32_t)kk * 8u,
+                mma_ts(tmem + C::kColAcc2, tmem + 128u * b + xcol(kk),
                        smem_desc(bdo + (uint32_t)(4 * h + kk) * 2048u, kBox, 1024, kSwizzle128B), idAcc,
                        acc | (kk > 0 ? 1u : 0u));
 #pragma unroll
               for (int kk = 0; kk < HB / 16; ++kk)   // dK += dS^T Q_c
-                mma_ts(tmem + C::kColAcc, tmem + 128u * b + HB + (uint32_t)kk * 8u,
+                mma_ts(tmem + C::kColAcc, tmem + 128u * b + HB + xcol(kk),
                        smem_desc(bq + (uint32_t)(4 * h + kk) * 2048u, kBox, 1024, kSwizzle128B), idAcc,
                        acc | (kk > 0 ? 1u : 0u));
             } else {
 #pragma unroll
               for (int kk = 0; kk < HB / 16; ++kk)
-                mma_ts(tmem + C::kColAcc, tmem + 128u * b + (uint32_t)kk * 8u,
+                mma_ts(tmem + C::kColAcc, tmem + 128u * b + xcol(kk),
                        smem_desc(b3 + (uint32_t)(4 * h + kk) * 2048u, kBox, 1024, kSwizzle128B), idAcc,
                        acc | (kk > 0 ? 1u : 0u));
             }
@@ -545,6 +551,273 @@ attn_bwd_tc_kernel(const __grid_constant__ CUtensorMap ta1, const __grid_constan
       wait_raw(bar(TEAR2), 0, kDrainNs);
     }
     __syncwarp();
+  } else if constexpr (MOD != 0) {
+    // ------------------------------------------------------------ P / dS and epilogue with a mask or a cap
+    // Sixteen warps: eight per half block (half h is always half buffer h), two per
+    // 32 rows with 32 columns each, which go through TMEM 16 columns at a time in a
+    // loop that is not unrolled. The chains of a cap or a mask then have three
+    // other warps of the scheduler to run beside, and the code of a half stays in the
+    // instruction cache. A warp writes its X over its own S (and dP) columns.
+    const int hf = warp >> 3, q = (warp >> 2) & 1, rw = warp & 3, t = (int)(threadIdx.x & 127);
+    const int k4 = warp >> 2;                                       // this warp among the four of its rows
+    const uint32_t t_row = tmem + ((uint32_t)(rw * 32) << 16);
+    const uint32_t tS = t_row + 128u * hf + 32u * q, tD = tS + HB;   // its columns of S and dP
+    const float sl2 = p.sl2;
+    uint32_t it_use = 0, stages = 0, acc_items = 0, a_use = 0;
+    uint4* pending = nullptr;    // output row of the previous item, written once its accumulator is full
+    uint4* pending2 = nullptr;   // mode 3: its dV row
+    bool has_pending = false, pend_store = false;
+    bool ok = true;
+    auto arrive = [&](uint32_t bar_) {   // for the whole warp
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar_);
+    };
+    // the accumulators' 32-column chunks are shared out over the four warps
+    auto epilogue = [&](uint4* orow, uint4* orow2, bool store) -> bool {
+      if (!wait_warp(bar(ACC_FULL), acc_items & 1u, g)) return false;
+      ++acc_items;
+      fence_after();
+      constexpr int kChunks = (MODE == 3 ? 2 : 1) * (D / 32);
+#pragma unroll 1
+      for (int c = k4 * kChunks / 4; c < (k4 + 1) * kChunks / 4; ++c) {
+        const bool second = c >= D / 32;
+        const int cc = second ? c - D / 32 : c;
+        uint32_t ov[32];
+        tmem_ld32(t_row + (second ? C::kColAcc2 : C::kColAcc) + cc * 32u, ov);
+        wait_ld();
+        const float scale = second ? p.out_scale2 : p.out_scale;
+        uint32_t w[16];
+#pragma unroll
+        for (int x = 0; x < 16; ++x)
+          w[x] = pack2(__uint_as_float(ov[2 * x]) * scale, __uint_as_float(ov[2 * x + 1]) * scale);
+        uint4* dst = (second ? orow2 : orow) + cc * 4;
+        if (store)
+#pragma unroll
+          for (int x = 0; x < 4; ++x) dst[x] = make_uint4(w[4 * x], w[4 * x + 1], w[4 * x + 2], w[4 * x + 3]);
+      }
+      fence_before();
+      arrive(bar(ACC_EMPTY));
+      return true;
+    };
+    for (;;) {
+      const int ri = (int)(it_use % kNI);
+      if (!(ok = wait_warp(bar(I_FULL + ri), (it_use / kNI) & 1u, g))) break;
+      const int4 ent = make_int4(ring[ri].x, ring[ri].y, ring[ri].z, 0);
+      // the slot's masks are read until the item ends; release it then
+      auto release = [&]() { arrive(bar(I_EMPTY + ri)); };
+      ++it_use;
+      if (ent.y < 0) {
+        release();
+        if (ent.y == -2) break;
+        continue;
+      }
+      const int64_t item = ent.x;
+      const int half = PAIR ? t >> 6 : 0;   // with pairs, rows 0-63 are block 2p and rows 64-127 block 2p + 1
+      const int64_t bh = item / nbp;
+      const int i = PAIR ? 2 * (int)(item % nbp) + half : (int)(item % nb);   // this thread's row block
+      const int o = PAIR ? t & 63 : t;                                        // its token in the block
+      const bool exists = !PAIR || (i < nb && !((ent.z >> half) & 1));       // warp-uniform
+      int64_t row = bh * p.N + (int64_t)i * BTB + o;
+      if (!exists || !dcheck(row >= 0 && row < p.rows_total, p.d_status)) row = 0;
+      int64_t orow_idx = p.raster && exists ? p.rm.row(bh, i, o) : row;
+      if (!dcheck(orow_idx >= 0 && orow_idx < p.rows_total, p.d_status)) orow_idx = 0;
+      uint4* orow = reinterpret_cast<uint4*>(p.out + orow_idx * D);
+      uint4* orow2 = MODE == 3 ? reinterpret_cast<uint4*>(p.out2 + orow_idx * D) : nullptr;
+      const int len = ent.y;
+      if (len == 0) {
+        if (exists)
+          for (int c = k4; c < D / 8; c += 4) {
+            orow[c] = make_uint4(0, 0, 0, 0);
+            if (MODE == 3) orow2[c] = make_uint4(0, 0, 0, 0);
+          }
+        release();
+        continue;
+      }
+      if (kRowsInTmem) {
+        // the item's row tiles -> TMEM (tile hf, box q); the A region is free once the
+        // last S and dP of the previous item, its second half's, have completed
+        if (stages > 0 && !(ok = wait_warp(bar(SD_FULL + 1), (stages - 1u) & 1u, g))) break;
+        if (!(ok = wait_warp(bar(A_FULL), a_use & 1u, g))) break;
+        ++a_use;
+        fence_after();
+        if (q < C::NBOX) {
+          uint32_t w[32];
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            const uint4 v = *reinterpret_cast<const uint4*>(gbase + (hf ? C::kOffA2 : 0u) + (uint32_t)q * kBox +
+                                                            (uint32_t)t * 128u + (uint32_t)((c ^ (t & 7)) * 16));
+            w[4 * c] = v.x;
+            w[4 * c + 1] = v.y;
+            w[4 * c + 2] = v.z;
+            w[4 * c + 3] = v.w;
+          }
+          tmem_st32(t_row + (hf ? C::kColA2 : C::kColA1) + 32u * q, w);
+          wait_st();
+        }
+        fence_before();
+        arrive(bar(A_EMPTY));   // the shared-memory tiles can take the next item's
+        arrive(bar(AT_FULL));   // the S issuer may start this item
+      }
+      // the previous item's output, while this item's first S and dP run
+      if (has_pending) {
+        if (!(ok = epilogue(pending, pending2, pend_store))) break;
+        has_pending = false;
+      }
+      // mode 0: this thread's query row has one LSE and one D
+      const float own_l2 = MODE == 0 && exists ? p.lse2[row] : 0.f;
+      const float own_d = MODE == 0 && exists ? p.delta[row] : 0.f;
+      // this row's interval (mode 0, a query) or position (mode 3, a key)
+      uint32_t ilo = 0u, ilen = 0u;
+      int ipos = 0;
+      int64_t tok0 = 0;
+      RowGroups groups{};
+      if (p.mask.pos != nullptr) {
+        tok0 = bh / p.rm.H * p.N;
+        if (exists) {
+          const int64_t at = tok0 + (int64_t)i * BTB + o;
+          if (MODE == 0) {
+            ilo = (uint32_t)__ldg(p.mask.lo + at);
+            ilen = __ldg(p.mask.len + at);
+          } else {
+            ipos = __ldg(p.mask.pos + at);
+          }
+        }
+        groups.make(MODE == 0 ? ilo : (uint32_t)ipos, ilen, lane);
+      }
+      const uint8_t* mk = masks + ri * (C::kMaskBytes + 16);
+      UnionSeek seek(bits + ri * 2 * C::MAXW, bits + ri * 2 * C::MAXW + C::MAXW, PAIR ? words : 0);
+      for (int e = 0; e < len; ++e, ++stages) {
+        const uint32_t st = stages % kNS;
+        const float4* stats = reinterpret_cast<const float4*>(gbase + C::kOffStage + st * kStageBytes + 2 * kTile);
+        // did the row block select this half's block, does the mask cut it, and the
+        // columns this row sees then
+        bool has = exists, cut;
+        if constexpr (PAIR) {
+          const uint32_t code = mk[2 * e + hf] >> half;   // bit 0: selected; 2: cut
+          has = exists && (code & 1u);
+          cut = has && ((code >> 2) & 1u);
+        } else {
+          cut = (reinterpret_cast<const uint32_t*>(mk)[e >> 5] >> (e & 31)) & 1u;
+        }
+        uint32_t see = 0xffffffffu;
+        if (cut) {
+          const int64_t j = PAIR ? seek.at(2 * e + hf) : __ldg(p.idx + p.ptr[item] + e);
+          const int64_t at = tok0 + j * BTB + (PAIR ? 0 : HB * hf) + 32 * q + lane;
+          if (MODE == 0) see = query_bits(groups, ilo, ilen, __ldg(p.mask.pos + at));
+          else see = key_bits(groups, ipos, __ldg(p.mask.lo + at), __ldg(p.mask.len + at));
+          has = __any_sync(0xffffffffu, see != 0u);
+        }
+        if (!(ok = wait_warp(bar(SD_FULL + hf), stages & 1u, g))) break;
+        fence_after();
+#pragma unroll 1
+        for (int c = 0; c < 2; ++c) {   // columns [16 c, 16 c + 16) of this warp's 32
+          uint32_t xk[8], xd[8];
+          if (!has) {
+#pragma unroll
+            for (int x = 0; x < 8; ++x) xk[x] = xd[x] = 0u;
+            tmem_st8(tS + 8u * c, xk);
+            if (MODE == 3) tmem_st8(tD + 8u * c, xd);
+            continue;
+          }
+          uint32_t sv[16], dv[16];
+          tmem_ld16(tS + 16u * c, sv);
+          tmem_ld16(tD + 16u * c, dv);
+          wait_ld();
+          const uint32_t w = see >> (16 * c);
+          auto operands = [&](auto form_c, auto cut_c) {   // form of the cap: none, near, within, any
+            constexpr int FORM = decltype(form_c)::value;
+            constexpr bool CUT = decltype(cut_c)::value;
+#pragma unroll
+            for (int x4 = 0; x4 < 4; ++x4) {
+              float l2[4], dd[4];
+              if (MODE == 0) {
+#pragma unroll
+                for (int u = 0; u < 4; ++u) { l2[u] = own_l2; dd[u] = own_d; }
+              } else {   // LSE*log2e and D of the columns
+                const float4 L = stats[16 * hf + 8 * q + 4 * c + x4];
+                const float4 Dv = stats[32 + 16 * hf + 8 * q + 4 * c + x4];
+                l2[0] = L.x; l2[1] = L.y; l2[2] = L.z; l2[3] = L.w;
+                dd[0] = Dv.x; dd[1] = Dv.y; dd[2] = Dv.z; dd[3] = Dv.w;
+              }
+              float pr[4], ds[4];
+#pragma unroll
+              for (int u = 0; u < 4; u += 2) {
+                const int x = 4 * x4 + u;
+                const float s0 = __uint_as_float(sv[x]), s1 = __uint_as_float(sv[x + 1]);
+                float e0, e1, c0 = 1.f, c1 = 1.f, t0, t1;
+                if constexpr (FORM == 0) {
+                  fma_x2(s0, s1, sl2, -l2[u], -l2[u + 1], e0, e1);
+                } else if constexpr (FORM == 1) {
+                  near_cap_x2(p.near, s0, s1, e0, e1);
+                  mul_x2(e0, e1, p.inv_cap2, p.inv_cap2, t0, t1);
+                  add_x2(e0, e1, -l2[u], -l2[u + 1]);
+                  fma2_x2(t0, t1, -t0, -t1, 1.f, c0, c1);
+                } else if constexpr (FORM == 2) {
+                  tanh_poly_x2(s0, s1, p.inv_cap, t0, t1);
+                  fma_x2(t0, t1, p.cap2, -l2[u], -l2[u + 1], e0, e1);
+                  fma2_x2(t0, t1, -t0, -t1, 1.f, c0, c1);
+                } else {
+                  const float r0 = rcpf(1.f + ex2f(s0 * p.c1)), r1 = rcpf(1.f + ex2f(s1 * p.c1));
+                  e0 = fmaf(r0, -2.f * p.cap2, p.cap2) - l2[u];
+                  e1 = fmaf(r1, -2.f * p.cap2, p.cap2) - l2[u + 1];
+                  c0 = 4.f * r0 * (1.f - r0);
+                  c1 = 4.f * r1 * (1.f - r1);
+                }
+                pr[u] = ex2f(e0);
+                pr[u + 1] = ex2f(e1);
+                if constexpr (CUT) {
+                  if (!((w >> x) & 1u)) pr[u] = 0.f;
+                  if (!((w >> (x + 1)) & 1u)) pr[u + 1] = 0.f;
+                }
+                sub_x2(__uint_as_float(dv[x]), __uint_as_float(dv[x + 1]), dd[u], dd[u + 1], t0, t1);
+                if (FORM != 0) mul_x2(t0, t1, c0, c1, t0, t1);
+                mul_x2(pr[u], pr[u + 1], t0, t1, ds[u], ds[u + 1]);
+              }
+              if (MODE == 3) {
+                xk[2 * x4] = pack2(pr[0], pr[1]);
+                xk[2 * x4 + 1] = pack2(pr[2], pr[3]);
+                xd[2 * x4] = pack2(ds[0], ds[1]);
+                xd[2 * x4 + 1] = pack2(ds[2], ds[3]);
+              } else {
+                xk[2 * x4] = pack2(ds[0], ds[1]);
+                xk[2 * x4 + 1] = pack2(ds[2], ds[3]);
+              }
+            }
+          };
+          using std::integral_constant;
+          if constexpr (MOD == 1) {
+            if (cut) operands(integral_constant<int, 0>{}, std::true_type{});
+            else operands(integral_constant<int, 0>{}, std::false_type{});
+          } else {
+            // the largest score of the warp's chunk says which form of the cap holds
+            float most = 0.f;
+#pragma unroll
+            for (int x = 0; x < 16; x += 2)
+              most = fmaxf(fmaxf(most, fabsf(__uint_as_float(sv[x]))), fabsf(__uint_as_float(sv[x + 1])));
+            if (__all_sync(0xffffffffu, most <= p.near.limit)) {
+              if (cut) operands(integral_constant<int, 1>{}, std::true_type{});
+              else operands(integral_constant<int, 1>{}, std::false_type{});
+            } else if (__all_sync(0xffffffffu, most * p.inv_cap <= 1.f)) {
+              operands(integral_constant<int, 2>{}, std::true_type{});
+            } else {
+              operands(integral_constant<int, 3>{}, std::true_type{});
+            }
+          }
+          tmem_st8(tS + 8u * c, xk);                  // over S columns read before
+          if (MODE == 3) tmem_st8(tD + 8u * c, xd);   // dS^T over dP^T
+        }
+        wait_st();
+        fence_before();
+        arrive(bar(X_FULL + hf));
+      }
+      if (!ok) break;
+      release();
+      pending = orow;
+      pending2 = orow2;
+      has_pending = true;
+      pend_store = exists;
+    }
+    if (ok && has_pending) epilogue(pending, pending2, pend_store);
   } else {
     // ------------------------------------------------------------ P / dS and epilogue
     const uint32_t t_row = tmem + ((uint32_t)(warp * 32) << 16);
@@ -605,18 +878,18 @@ attn_bwd_tc_kernel(const __grid_constant__ CUtensorMap ta1, const __grid_constan
       if (!(ok = wait_warp(bar(I_FULL + ri), (it_use / kNI) & 1u, g))) break;
       const int4 ent = make_int4(ring[ri].x, ring[ri].y, ring[ri].z, 0);
       __syncwarp();
-      // pairs and MOD read the slot's masks until the item ends; release it then
+      // pairs read the slot's masks until the item ends; release it then
       auto release = [&]() {
         if (lane == 0) mbar_arrive(bar(I_EMPTY + ri));
       };
-      if (!C::HOLD) release();
+      if (!PAIR) release();
       ++it_use;
       if (ent.y == -2) {
-        if (C::HOLD) release();
+        if (PAIR) release();
         break;
       }
       if (ent.y == -1) {
-        if (C::HOLD) release();
+        if (PAIR) release();
         continue;
       }
       const int64_t item = ent.x;
@@ -641,7 +914,7 @@ attn_bwd_tc_kernel(const __grid_constant__ CUtensorMap ta1, const __grid_constan
 #pragma unroll
             for (int c = 0; c < D / 8; ++c) orow2[c] = make_uint4(0, 0, 0, 0);
         }
-        if (C::HOLD) release();
+        if (PAIR) release();
         continue;
       }
       if (kRowsInTmem) {
@@ -666,82 +939,7 @@ attn_bwd_tc_kernel(const __grid_constant__ CUtensorMap ta1, const __grid_constan
       const float own_l2 = MODE == 0 && exists ? p.lse2[row] : 0.f;
       const float own_d = MODE == 0 && exists ? p.delta[row] : 0.f;
       const uint16_t* mk = reinterpret_cast<const uint16_t*>(masks + ri * (C::kMaskBytes + 16));
-      // MOD: this row's interval (mode 0, a query) or position (mode 3, a key), and
-      // of the next stage which halves the mask cuts and there the positions or
-      // intervals of this lane's columns
-      uint32_t ilo = 0u, ilen = 0u;
-      int ipos = 0;
-      int64_t tok0 = 0;
-      int32_t ca[4];
-      uint32_t cb[4];
-      bool cut1 = false, cut2 = false;
-      RowGroups groups{};
-      UnionSeek seek(bits + ri * 2 * C::MAXW, bits + ri * 2 * C::MAXW + C::MAXW, PAIR && MOD != 0 ? words : 0);
-      auto next_cut = [&](int e) {
-        if constexpr (PAIR) {
-          const uint32_t st = mk[e];
-          cut1 = (st >> (2 + half)) & (st >> half) & 1u;
-          cut2 = (st >> (10 + half)) & (st >> (8 + half)) & 1u;
-        } else {
-          cut1 = cut2 = (reinterpret_cast<const uint32_t*>(mk)[e >> 5] >> (e & 31)) & 1u;
-        }
-        auto fetch = [&](int c, int64_t at) {
-          ca[c] = __ldg((MODE == 0 ? p.mask.pos : p.mask.lo) + at);
-          if (MODE != 0) cb[c] = __ldg(p.mask.len + at);
-        };
-        if (!cut1 && !cut2) return;
-        if constexpr (PAIR) {
-          if (cut1) {
-            const int64_t at = tok0 + lane + (int64_t)seek.at(2 * e) * BTB;
-            fetch(0, at);
-            fetch(1, at + 32);
-          }
-          if (cut2) {
-            const int64_t at = tok0 + lane + (int64_t)seek.at(2 * e + 1) * BTB;
-            fetch(2, at);
-            fetch(3, at + 32);
-          }
-        } else {
-          const int64_t at = tok0 + lane + (int64_t)__ldg(p.idx + p.ptr[item] + e) * BTB;
-#pragma unroll
-          for (int c = 0; c < 4; ++c) fetch(c, at + 32 * c);
-        }
-      };
-      if constexpr (MOD != 0) {
-        if (p.mask.pos != nullptr) {
-          tok0 = bh / p.rm.H * p.N;
-          if (exists) {
-            const int64_t at = tok0 + (int64_t)i * BTB + o;
-            if (MODE == 0) {
-              ilo = (uint32_t)__ldg(p.mask.lo + at);
-              ilen = __ldg(p.mask.len + at);
-            } else {
-              ipos = __ldg(p.mask.pos + at);
-            }
-          }
-          groups.make(MODE == 0 ? ilo : (uint32_t)ipos, ilen, lane);
-        }
-        next_cut(0);
-      }
       for (int e = 0; e < len && ok; ++e) {
-        // bit c of see[2 h + c / 32]: this row sees column c of half h; a half that no
-        // row of the warp sees has X = 0, one that all see whole is not cut
-        uint32_t see[4] = {0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu};
-        bool any1 = true, any2 = true;
-        if constexpr (MOD != 0) {
-          if (cut1) {
-            if (MODE == 0) query_bits(groups, ilo, ilen, ca[0], ca[1], lane, see[0], see[1]);
-            else key_bits(groups, ipos, ca[0], cb[0], ca[1], cb[1], lane, see[0], see[1]);
-            any1 = __any_sync(0xffffffffu, (see[0] | see[1]) != 0u);
-            cut1 = __any_sync(0xffffffffu, (see[0] & see[1]) != 0xffffffffu);
-          }
-          if (cut2) {
-            if (MODE == 0) query_bits(groups, ilo, ilen, ca[2], ca[3], lane, see[2], see[3]);
-            else key_bits(groups, ipos, ca[2], cb[2], ca[3], cb[3], lane, see[2], see[3]);
-            any2 = __any_sync(0xffffffffu, (see[2] | see[3]) != 0u);
-            cut2 = __any_sync(0xffffffffu, (see[2] & see[3]) != 0xffffffffu);
-          }
-        }
         const uint32_t st = c_use % kNS;
         const float4* stats = reinterpret_cast<const float4*>(gbase + C::kOffStage + st * kStageBytes + 2 * kTile);
         const uint32_t msk = PAIR ? (uint32_t)mk[e] : 0xffffu;   // byte h: which rows selected block h
@@ -759,137 +957,87 @@ attn_bwd_tc_kernel(const __grid_constant__ CUtensorMap ta1, const __grid_constan
           wait_ld();
           // pairs: a row block that did not select this half's block (or does not
           // exist) gets X = 0 there (warp-uniform)
-          const bool has = (!PAIR || (exists && ((msk >> (8 * h + half)) & 1u))) && (MOD == 0 || (h == 0 ? any1 : any2));
-          // MOD 2: do all scores of the half lie within the cap, where the polynomial holds?
-          bool within = true;
-          if constexpr (MOD == 2) {
-            float big[2] = {0.f, 0.f};
+          const bool has = !PAIR || (exists && ((msk >> (8 * h + half)) & 1u));
+          uint32_t xk[HB / 2];
+          if constexpr (MODE == 3) {
+            // P^T over S^T; dS^T = P^T (dP^T - D) over dP^T (both already in registers)
+            uint32_t xd[HB / 2];
 #pragma unroll
-            for (int c = 0; c < HB; c += 2)
-              big[(c >> 1) & 1] = fmaxf(fmaxf(big[(c >> 1) & 1], fabsf(__uint_as_float(sv[c]))),
-                                        fabsf(__uint_as_float(sv[c + 1])));
-            within = __all_sync(0xffffffffu, fmaxf(big[0], big[1]) * p.inv_cap <= 1.f);
-          }
-          // the half's operand(s) X; CUT: the mask hides some of its scores from rows of this warp
-          auto operands = [&](auto cut_c, auto poly_c) {
-            constexpr bool CUT = decltype(cut_c)::value, POLY = decltype(poly_c)::value;
-            // P of columns x, x + 1 from the scores and LSE*log2e, and 1 - tanh^2 of the cap
-            auto probs = [&](int x, float la, float lb, float& p0, float& p1, float& c0, float& c1) {
-              const float s0 = __uint_as_float(sv[x]), s1 = __uint_as_float(sv[x + 1]);
-              float e0, e1;
-              c0 = c1 = 1.f;
-              if constexpr (MOD != 2) {
-                fma_x2(s0, s1, sl2, -la, -lb, e0, e1);
-              } else if constexpr (POLY) {
-                float t0, t1;
-                tanh_poly_x2(s0, s1, p.inv_cap, t0, t1);
-                fma_x2(t0, t1, p.cap2, -la, -lb, e0, e1);
-                fma2_x2(t0, t1, -t0, -t1, 1.f, c0, c1);
-              } else {
-                const float r0 = rcpf(1.f + ex2f(s0 * p.c1)), r1 = rcpf(1.f + ex2f(s1 * p.c1));
-                e0 = fmaf(r0, -2.f * p.cap2, p.cap2) - la;
-                e1 = fmaf(r1, -2.f * p.cap2, p.cap2) - lb;
-                c0 = 4.f * r0 * (1.f - r0);
-                c1 = 4.f * r1 * (1.f - r1);
+            for (int x = 0; x < HB / 2; ++x) xk[x] = xd[x] = 0u;
+            if (has)
+#pragma unroll
+            for (int x4 = 0; x4 < HB / 4; ++x4) {
+              const float4 L = stats[16 * h + x4];
+              const float4 Dv = stats[32 + 16 * h + x4];
+              const float l2[4] = {L.x, L.y, L.z, L.w}, dd[4] = {Dv.x, Dv.y, Dv.z, Dv.w};
+              float pr[4], ds[4];
+#pragma unroll
+              for (int u = 0; u < 4; u += 2) {   // column pairs: each lane rounds as the scalar form
+                const int x = 4 * x4 + u;
+                float e0, e1, t0, t1;
+                fma_x2(__uint_as_float(sv[x]), __uint_as_float(sv[x + 1]), sl2, -l2[u], -l2[u + 1], e0, e1);
+                pr[u] = ex2f(e0);
+                pr[u + 1] = ex2f(e1);
+                sub_x2(__uint_as_float(dv[x]), __uint_as_float(dv[x + 1]), dd[u], dd[u + 1], t0, t1);
+                mul_x2(pr[u], pr[u + 1], t0, t1, ds[u], ds[u + 1]);
               }
-              p0 = ex2f(e0);
-              p1 = ex2f(e1);
-              if constexpr (CUT) {   // x is a constant of the unrolled loop
-                const uint32_t w = h == 0 ? (x < 32 ? see[0] : see[1]) : (x < 32 ? see[2] : see[3]);
-                if (!((w >> (x & 31)) & 1u)) p0 = 0.f;
-                if (!((w >> ((x + 1) & 31)) & 1u)) p1 = 0.f;
-              }
-            };
-            uint32_t xk[HB / 2];
-            if constexpr (MODE == 3) {
-              // P^T over S^T; dS^T = P^T (dP^T - D) over dP^T (both already in registers)
-              uint32_t xd[HB / 2];
-#pragma unroll
-              for (int x = 0; x < HB / 2; ++x) xk[x] = xd[x] = 0u;
-              if (has)
-#pragma unroll
-              for (int x4 = 0; x4 < HB / 4; ++x4) {
-                const float4 L = stats[16 * h + x4];
-                const float4 Dv = stats[32 + 16 * h + x4];
-                const float l2[4] = {L.x, L.y, L.z, L.w}, dd[4] = {Dv.x, Dv.y, Dv.z, Dv.w};
-                float pr[4], ds[4];
-#pragma unroll
-                for (int u = 0; u < 4; u += 2) {   // column pairs: each lane rounds as the scalar form
-                  const int x = 4 * x4 + u;
-                  float t0, t1, c0, c1;
-                  probs(x, l2[u], l2[u + 1], pr[u], pr[u + 1], c0, c1);
-                  sub_x2(__uint_as_float(dv[x]), __uint_as_float(dv[x + 1]), dd[u], dd[u + 1], t0, t1);
-                  mul_x2(pr[u], pr[u + 1], t0, t1, ds[u], ds[u + 1]);
-                  if (MOD == 2) mul_x2(ds[u], ds[u + 1], c0, c1, ds[u], ds[u + 1]);
-                }
-                xk[2 * x4] = pack2(pr[0], pr[1]);
-                xk[2 * x4 + 1] = pack2(pr[2], pr[3]);
-                xd[2 * x4] = pack2(ds[0], ds[1]);
-                xd[2 * x4 + 1] = pack2(ds[2], ds[3]);
-              }
-              tmem_st32(t_row + 128u * b, xk);
-              tmem_st32(t_row + 128u * b + HB, xd);
-              wait_st();
-              fence_before();
-              mbar_arrive(bar(X_FULL + b));
-            } else {
-#pragma unroll
-              for (int x = 0; x < HB / 2; ++x) xk[x] = 0u;
-              if (has)
-#pragma unroll
-              for (int x4 = 0; x4 < HB / 4; ++x4) {
-                float l2[4], dd[4];
-                if (MODE == 0) {
-#pragma unroll
-                  for (int u = 0; u < 4; ++u) { l2[u] = own_l2; dd[u] = own_d; }
-                } else {
-                  const float4 L = stats[16 * h + x4];          // LSE*log2e of columns 64h+4x4 .. +3
-                  const float4 Dv = stats[32 + 16 * h + x4];    // D of the same columns
-                  l2[0] = L.x; l2[1] = L.y; l2[2] = L.z; l2[3] = L.w;
-                  dd[0] = Dv.x; dd[1] = Dv.y; dd[2] = Dv.z; dd[3] = Dv.w;
-                }
-                float v[4];
-#pragma unroll
-                for (int u = 0; u < 4; u += 2) {   // column pairs: each lane rounds as the scalar form
-                  const int x = 4 * x4 + u;
-                  float p0, p1, c0, c1;
-                  probs(x, l2[u], l2[u + 1], p0, p1, c0, c1);
-                  if (kHasDP) {
-                    float t0, t1;
-                    sub_x2(__uint_as_float(dv[x]), __uint_as_float(dv[x + 1]), dd[u], dd[u + 1], t0, t1);
-                    mul_x2(p0, p1, t0, t1, v[u], v[u + 1]);
-                    if (MOD == 2) mul_x2(v[u], v[u + 1], c0, c1, v[u], v[u + 1]);
-                  } else {
-                    v[u] = p0;
-                    v[u + 1] = p1;
-                  }
-                }
-                xk[2 * x4] = pack2(v[0], v[1]);
-                xk[2 * x4 + 1] = pack2(v[2], v[3]);
-              }
-              // X over the first 32 columns of this half's S (already in registers)
-              tmem_st32(t_row + 128u * b, xk);
-              wait_st();
-              fence_before();
-              mbar_arrive(bar(X_FULL + b));
+              xk[2 * x4] = pack2(pr[0], pr[1]);
+              xk[2 * x4 + 1] = pack2(pr[2], pr[3]);
+              xd[2 * x4] = pack2(ds[0], ds[1]);
+              xd[2 * x4 + 1] = pack2(ds[2], ds[3]);
             }
-          };
-          if constexpr (MOD == 0) {
-            operands(std::false_type{}, std::true_type{});
-          } else if (h == 0 ? cut1 : cut2) {
-            if (MOD == 2 && !within) operands(std::true_type{}, std::false_type{});
-            else operands(std::true_type{}, std::true_type{});
+            tmem_st32(t_row + 128u * b, xk);
+            tmem_st32(t_row + 128u * b + HB, xd);
+            wait_st();
+            fence_before();
+            mbar_arrive(bar(X_FULL + b));
           } else {
-            if (MOD == 2 && !within) operands(std::false_type{}, std::false_type{});
-            else operands(std::false_type{}, std::true_type{});
+#pragma unroll
+            for (int x = 0; x < HB / 2; ++x) xk[x] = 0u;
+            if (has)
+#pragma unroll
+            for (int x4 = 0; x4 < HB / 4; ++x4) {
+              float l2[4], dd[4];
+              if (MODE == 0) {
+#pragma unroll
+                for (int u = 0; u < 4; ++u) { l2[u] = own_l2; dd[u] = own_d; }
+              } else {
+                const float4 L = stats[16 * h + x4];          // LSE*log2e of columns 64h+4x4 .. +3
+                const float4 Dv = stats[32 + 16 * h + x4];    // D of the same columns
+                l2[0] = L.x; l2[1] = L.y; l2[2] = L.z; l2[3] = L.w;
+                dd[0] = Dv.x; dd[1] = Dv.y; dd[2] = Dv.z; dd[3] = Dv.w;
+              }
+              float v[4];
+#pragma unroll
+              for (int u = 0; u < 4; u += 2) {   // column pairs: each lane rounds as the scalar form
+                const int x = 4 * x4 + u;
+                float e0, e1;
+                fma_x2(__uint_as_float(sv[x]), __uint_as_float(sv[x + 1]), sl2, -l2[u], -l2[u + 1], e0, e1);
+                const float p0 = ex2f(e0), p1 = ex2f(e1);
+                if (kHasDP) {
+                  float t0, t1;
+                  sub_x2(__uint_as_float(dv[x]), __uint_as_float(dv[x + 1]), dd[u], dd[u + 1], t0, t1);
+                  mul_x2(p0, p1, t0, t1, v[u], v[u + 1]);
+                } else {
+                  v[u] = p0;
+                  v[u + 1] = p1;
+                }
+              }
+              xk[2 * x4] = pack2(v[0], v[1]);
+              xk[2 * x4 + 1] = pack2(v[2], v[3]);
+            }
+            // X over the first 32 columns of this half's S (already in registers)
+            tmem_st32(t_row + 128u * b, xk);
+            wait_st();
+            fence_before();
+            mbar_arrive(bar(X_FULL + b));
           }
           ++hg;
         }
-        if (MOD != 0 && e + 1 < len) next_cut(e + 1);
         ++c_use;
       }
       if (!ok) break;
-      if (C::HOLD) release();
+      if (PAIR) release();
       pending = orow;
       pending2 = orow2;
       has_pending = true;
@@ -901,7 +1049,7 @@ attn_bwd_tc_kernel(const __grid_constant__ CUtensorMap ta1, const __grid_constan
   fence_before();
   __syncthreads();
   fence_after();
-  if (warp == 5) tmem_dealloc(tmem, 512);
+  if (warp == C::W_S) tmem_dealloc(tmem, 512);
   if (p.prof != nullptr && threadIdx.x == 0)
     atomicAdd((unsigned long long*)&p.prof[smid() % SPARSP_PROF_SLOTS],
               (unsigned long long)(globaltimer_ns() - t_start));
@@ -917,7 +1065,7 @@ sparsp_status_t go(const Dims& s, const CUtensorMap& a1, const CUtensorMap& a2, 
   const int sms = device_sm_count();
   if (sms <= 0) return SPARSP_ERR_CUDA;
   const int64_t grid = cap_grid(s, sms, prm.n_items);
-  kern<<<(unsigned)grid, kThreads, kSmemBytes, st>>>(a1, a2, b1, b2, prm);
+  kern<<<(unsigned)grid, BCfg<D, BTB, MOD>::THREADS, kSmemBytes, st>>>(a1, a2, b1, b2, prm);
   SPARSP_LAUNCH_CHECK();
   return SPARSP_OK;
 }
@@ -963,7 +1111,8 @@ sparsp_status_t launch_bwd_mod(const Dims& s, int mode, const __nv_bfloat16* q,
   Params prm{ptr, idx, s.N, s.nb, nbp, (int64_t)s.B * s.H * nbp, (int64_t)rows, scale * 1.4426950408889634f,
              mode == 2 ? 1.0f : scale, lse2, delta, out, out2, 1.0f, items, counter, prof, d_status,
              raster ? 1 : 0, raster_map(s), mask, MOD == 2 ? 2.f * scale * 1.4426950408889634f / cap : 0.f,
-             cap * 1.4426950408889634f, MOD == 2 ? scale / cap : 0.f};
+             cap * 1.4426950408889634f, MOD == 2 ? scale / cap : 0.f,
+             MOD == 2 ? 0.69314718055994531f / cap : 0.f, MOD == 2 ? near_cap(scale, cap) : NearCap{}};
   if (s.Bt == 64) {
     if (s.d == 64) return launch_d<64, 64, MOD>(mode, m, s, prm, st);
     return launch_d<128, 64, MOD>(mode, m, s, prm, st);

@@ -51,20 +51,27 @@ __device__ __forceinline__ void query_bits(const RowGroups& g, uint32_t lo, uint
     }
   }
 }
-// Rows are keys at position pos; each lane brings the intervals of two query columns.
-__device__ __forceinline__ void key_bits(const RowGroups& g, int32_t pos, int32_t lo0, uint32_t len0, int32_t lo1,
-                                         uint32_t len1, int lane, uint32_t& w0, uint32_t& w1) {
-  w0 = w1 = 0u;
+// The same for 32 columns, one per lane.
+__device__ __forceinline__ uint32_t query_bits(const RowGroups& g, uint32_t lo, uint32_t len, int32_t k) {
+  uint32_t w = 0u;
+  for (uint32_t rem = g.leaders; rem != 0u; rem &= rem - 1u) {
+    const int l = __ffs(rem) - 1;
+    const uint32_t a = __shfl_sync(0xffffffffu, lo, l), n = __shfl_sync(0xffffffffu, len, l);
+    const uint32_t b = __ballot_sync(0xffffffffu, (uint32_t)k - a < n);
+    if ((g.mine >> l) & 1u) w = b;
+  }
+  return w;
+}
+// Rows are keys at position pos; each lane brings the interval of one query column.
+__device__ __forceinline__ uint32_t key_bits(const RowGroups& g, int32_t pos, int32_t lo, uint32_t len) {
+  uint32_t w = 0u;
   for (uint32_t rem = g.leaders; rem != 0u; rem &= rem - 1u) {
     const int l = __ffs(rem) - 1;
     const uint32_t x = (uint32_t)__shfl_sync(0xffffffffu, pos, l);
-    const uint32_t b0 = __ballot_sync(0xffffffffu, x - (uint32_t)lo0 < len0);
-    const uint32_t b1 = __ballot_sync(0xffffffffu, x - (uint32_t)lo1 < len1);
-    if ((g.mine >> l) & 1u) {
-      w0 = b0;
-      w1 = b1;
-    }
+    const uint32_t b = __ballot_sync(0xffffffffu, x - (uint32_t)lo < len);
+    if ((g.mine >> l) & 1u) w = b;
   }
+  return w;
 }
 
 // Byte layout of a plan.
