@@ -554,8 +554,7 @@ attn_bwd_tc_kernel(const __grid_constant__ CUtensorMap ta1, const __grid_constan
   } else if constexpr (MOD != 0) {
     // ------------------------------------------------------------ P / dS and epilogue with a mask or a cap
     // Sixteen warps: eight per half block (half h is always half buffer h), two per
-    // 32 rows with 32 columns each, which go through TMEM 16 columns at a time in a
-    // loop that is not unrolled. The chains of a cap or a mask then have three
+    // 32 rows with 32 columns each. The chains of a cap or a mask then have three
     // other warps of the scheduler to run beside, and the code of a half stays in the
     // instruction cache. A warp writes its X over its own S (and dP) columns.
     const int hf = warp >> 3, q = (warp >> 2) & 1, rw = warp & 3, t = (int)(threadIdx.x & 127);
@@ -709,33 +708,28 @@ attn_bwd_tc_kernel(const __grid_constant__ CUtensorMap ta1, const __grid_constan
         }
         if (!(ok = wait_warp(bar(SD_FULL + hf), stages & 1u, g))) break;
         fence_after();
-#pragma unroll 1
-        for (int c = 0; c < 2; ++c) {   // columns [16 c, 16 c + 16) of this warp's 32
-          uint32_t xk[8], xd[8];
+        {
+          uint32_t xk[16], xd[16];
           if (!has) {
 #pragma unroll
-            for (int x = 0; x < 8; ++x) xk[x] = xd[x] = 0u;
-            tmem_st8(tS + 8u * c, xk);
-            if (MODE == 3) tmem_st8(tD + 8u * c, xd);
-            continue;
-          }
-          uint32_t sv[16], dv[16];
-          tmem_ld16(tS + 16u * c, sv);
-          tmem_ld16(tD + 16u * c, dv);
+            for (int x = 0; x < 16; ++x) xk[x] = xd[x] = 0u;
+          } else {
+          uint32_t sv[32], dv[32];
+          tmem_ld32(tS, sv);
+          tmem_ld32(tD, dv);
           wait_ld();
-          const uint32_t w = see >> (16 * c);
           auto operands = [&](auto form_c, auto cut_c) {   // form of the cap: none, near, within, any
             constexpr int FORM = decltype(form_c)::value;
             constexpr bool CUT = decltype(cut_c)::value;
 #pragma unroll
-            for (int x4 = 0; x4 < 4; ++x4) {
+            for (int x4 = 0; x4 < 8; ++x4) {
               float l2[4], dd[4];
               if (MODE == 0) {
 #pragma unroll
                 for (int u = 0; u < 4; ++u) { l2[u] = own_l2; dd[u] = own_d; }
               } else {   // LSE*log2e and D of the columns
-                const float4 L = stats[16 * hf + 8 * q + 4 * c + x4];
-                const float4 Dv = stats[32 + 16 * hf + 8 * q + 4 * c + x4];
+                const float4 L = stats[16 * hf + 8 * q + x4];
+                const float4 Dv = stats[32 + 16 * hf + 8 * q + x4];
                 l2[0] = L.x; l2[1] = L.y; l2[2] = L.z; l2[3] = L.w;
                 dd[0] = Dv.x; dd[1] = Dv.y; dd[2] = Dv.z; dd[3] = Dv.w;
               }
@@ -766,8 +760,8 @@ attn_bwd_tc_kernel(const __grid_constant__ CUtensorMap ta1, const __grid_constan
                 pr[u] = ex2f(e0);
                 pr[u + 1] = ex2f(e1);
                 if constexpr (CUT) {
-                  if (!((w >> x) & 1u)) pr[u] = 0.f;
-                  if (!((w >> (x + 1)) & 1u)) pr[u + 1] = 0.f;
+                  if (!((see >> x) & 1u)) pr[u] = 0.f;
+                  if (!((see >> (x + 1)) & 1u)) pr[u + 1] = 0.f;
                 }
                 sub_x2(__uint_as_float(dv[x]), __uint_as_float(dv[x + 1]), dd[u], dd[u + 1], t0, t1);
                 if (FORM != 0) mul_x2(t0, t1, c0, c1, t0, t1);
@@ -792,7 +786,7 @@ attn_bwd_tc_kernel(const __grid_constant__ CUtensorMap ta1, const __grid_constan
             // the largest score of the warp's chunk says which form of the cap holds
             float most = 0.f;
 #pragma unroll
-            for (int x = 0; x < 16; x += 2)
+            for (int x = 0; x < 32; x += 2)
               most = fmaxf(fmaxf(most, fabsf(__uint_as_float(sv[x]))), fabsf(__uint_as_float(sv[x + 1])));
             if (__all_sync(0xffffffffu, most <= p.near.limit)) {
               if (cut) operands(integral_constant<int, 1>{}, std::true_type{});
@@ -803,8 +797,9 @@ attn_bwd_tc_kernel(const __grid_constant__ CUtensorMap ta1, const __grid_constan
               operands(integral_constant<int, 3>{}, std::true_type{});
             }
           }
-          tmem_st8(tS + 8u * c, xk);                  // over S columns read before
-          if (MODE == 3) tmem_st8(tD + 8u * c, xd);   // dS^T over dP^T
+          }
+          tmem_st16(tS, xk);                  // over S columns read before
+          if (MODE == 3) tmem_st16(tD, xd);   // dS^T over dP^T
         }
         wait_st();
         fence_before();
