@@ -171,7 +171,7 @@ struct Params {
   RasterMap rm;
   MaskView mask;      // MOD != 0; mask.pos null: no mask
   // MOD == 2: 2 scale log2(e) / cap, cap log2(e) and scale / cap
-  float c1, cap2, inv_cap, inv_cap2;   // and 1 / cap2
+  float c1, cap2, inv_cap;
   NearCap near;
 };
 
@@ -742,9 +742,8 @@ attn_bwd_tc_kernel(const __grid_constant__ CUtensorMap ta1, const __grid_constan
                 if constexpr (FORM == 0) {
                   fma_x2(s0, s1, sl2, -l2[u], -l2[u + 1], e0, e1);
                 } else if constexpr (FORM == 1) {
-                  near_cap_x2(p.near, s0, s1, e0, e1);
-                  mul_x2(e0, e1, p.inv_cap2, p.inv_cap2, t0, t1);
-                  add_x2(e0, e1, -l2[u], -l2[u + 1]);
+                  near_tanh_x2(p.near, s0, s1, t0, t1);
+                  fma_x2(t0, t1, p.cap2, -l2[u], -l2[u + 1], e0, e1);
                   fma2_x2(t0, t1, -t0, -t1, 1.f, c0, c1);
                 } else if constexpr (FORM == 2) {
                   tanh_poly_x2(s0, s1, p.inv_cap, t0, t1);
@@ -1107,7 +1106,7 @@ sparsp_status_t launch_bwd_mod(const Dims& s, int mode, const __nv_bfloat16* q,
              mode == 2 ? 1.0f : scale, lse2, delta, out, out2, 1.0f, items, counter, prof, d_status,
              raster ? 1 : 0, raster_map(s), mask, MOD == 2 ? 2.f * scale * 1.4426950408889634f / cap : 0.f,
              cap * 1.4426950408889634f, MOD == 2 ? scale / cap : 0.f,
-             MOD == 2 ? 0.69314718055994531f / cap : 0.f, MOD == 2 ? near_cap(scale, cap) : NearCap{}};
+             MOD == 2 ? near_cap_backward(scale, cap) : NearCap{}};
   if (s.Bt == 64) {
     if (s.d == 64) return launch_d<64, 64, MOD>(mode, m, s, prm, st);
     return launch_d<128, 64, MOD>(mode, m, s, prm, st);

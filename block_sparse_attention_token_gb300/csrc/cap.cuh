@@ -85,6 +85,27 @@ inline NearCap near_cap(double scale, double cap) {
   n.limit = (float)(kNearCap / a);
   return n;
 }
+// The backward rounds everything it makes of tanh to bf16: degree 3 (2.3e-6) will do
+// there, and tanh itself is what it needs twice (c[4] is not used).
+inline NearCap near_cap_backward(double scale, double cap) {
+  NearCap n{};
+  const double a = scale / cap;
+  if (!(a >= 1.0 / 16384 && a <= 16384.0)) return n;
+  const double t[4] = {0.9999978542327881, -0.33314040303230286, 0.13057856261730194, -0.04092942178249359};
+  double f = a;
+  for (int k = 0; k < 4; ++k, f *= a * a) n.c[k] = (float)(t[k] * f);
+  n.limit = (float)(kNearCap / a);
+  return n;
+}
+// tanh of a pair of scores from the backward's coefficients
+__device__ __forceinline__ void near_tanh_x2(const NearCap& n, float s0, float s1, float& t0, float& t1) {
+  float u0, u1, q0, q1;
+  mul_x2(s0, s1, s0, s1, u0, u1);
+  fma_x2(u0, u1, n.c[3], n.c[2], q0, q1);
+  fma2_x2(q0, q1, u0, u1, n.c[1], q0, q1);
+  fma2_x2(q0, q1, u0, u1, n.c[0], q0, q1);
+  mul_x2(s0, s1, q0, q1, t0, t1);
+}
 // y of a pair of scores
 __device__ __forceinline__ void near_cap_x2(const NearCap& n, float s0, float s1, float& y0, float& y1) {
   float u0, u1, q0, q1;
