@@ -15,6 +15,7 @@
 // row sums are warp shuffles (rows of up to 128 16-byte vectors) or one
 // shared-memory exchange per batch of rows (longer rows, a CTA per row).
 #include "common.cuh"
+#include "tc_helpers.cuh"
 
 namespace sparsp {
 namespace {
@@ -22,18 +23,18 @@ namespace {
 constexpr int kWarpThreads = 256;   // CTA of the shuffle kernels
 constexpr int kMaxWarps = 32;
 
+// 16 bytes of a row as fp32 pairs and back.
 template <typename T>
 struct Vec;
 template <>
 struct Vec<__nv_bfloat16> {
   static constexpr int E = 8;
   static __device__ __forceinline__ void unpack(const uint4& v, float* f) {
-    const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&v);
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const float2 t = __bfloat1622float2(h[e]);
-      f[2 * e] = t.x;
-      f[2 * e + 1] = t.y;
+    for (int e = 0; e < 4; ++e) {   // a bf16 is the upper half of its fp32
+      f[2 * e] = __uint_as_float(w[e] << 16);
+      f[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
     }
   }
   static __device__ __forceinline__ uint4 pack(const float* f) {
@@ -72,10 +73,18 @@ struct Rows {
   }
 };
 
-// Threads of a CTA at most: rows of up to 16,384 values, U vectors a thread.
-template <typename T, int L, int U>
-constexpr int max_threads() {
-  return L != 0 ? kWarpThreads : U == 2 ? 512 : 16384 / (Vec<T>::E * U);
+__device__ __forceinline__ void copy_async16(void* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(tc::smem_u32(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;\n" ::: "memory"); }
+// Until at most n of this thread's copy groups are in flight (n < 4).
+template <int N>
+__device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;\n" ::"n"(N) : "memory"); }
+__device__ __forceinline__ void copy_wait(int n) {
+  if (n == 3) copy_wait<3>();
+  else if (n == 2) copy_wait<2>();
+  else if (n == 1) copy_wait<1>();
+  else copy_wait<0>();
 }
 
 // Sum of K values over the threads that share a row: L lanes of a warp, or the
@@ -96,98 +105,168 @@ __device__ __forceinline__ void row_sum(float (&v)[K], float* sm, int& buf) {
       for (int k = 0; k < K; ++k) s[warp * K + k] = v[k];
     __syncthreads();
 #pragma unroll
-    for (int k = 0; k < K; ++k) {
-      float t = 0.f;
-      for (int w = 0; w < nw; ++w) t += s[w * K + k];
-      v[k] = t;
-    }
+    for (int k = 0; k < K; ++k) v[k] = 0.f;
+#pragma unroll 4
+    for (int w = 0; w < nw; ++w)
+#pragma unroll
+      for (int k = 0; k < K; ++k) v[k] += s[w * K + k];
   }
 }
 
+// One thread's share of a row: U vectors, t + u * T (T threads per row). `cols`
+// is how many of them exist; the others hold zeros.
+template <typename T, int U, bool RMS>
+struct Share {
+  using X = Vec<T>;
+  static constexpr int E = X::E, P = E / 2;
+  static __device__ __forceinline__ void mean_part(const uint4 (&x)[U], float& s) {
+    float a0 = 0.f, a1 = 0.f;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      float f[E];
+      X::unpack(x[u], f);
+#pragma unroll
+      for (int i = 0; i < P; ++i) tc::add_x2(a0, a1, f[2 * i], f[2 * i + 1]);
+    }
+    s = a0 + a1;
+  }
+  // sum of (x - mu)^2 over the vectors that exist (a missing one holds zeros, not the mean)
+  static __device__ __forceinline__ void var_part(const uint4 (&x)[U], float mu, int have, float& s) {
+    float a0 = 0.f, a1 = 0.f;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      float f[E];
+      X::unpack(x[u], f);
+      if (RMS || u < have)
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+          float c0 = f[2 * i], c1 = f[2 * i + 1];
+          if (!RMS) tc::sub_x2(c0, c1, mu, mu, c0, c1);
+          tc::fma2_acc(c0, c1, c0, c1, a0, a1);
+        }
+    }
+    s = a0 + a1;
+  }
+  static __device__ __forceinline__ uint4 out(const uint4& x, float mu, float rs, const float* w, const float* b) {
+    float f[E];
+    X::unpack(x, f);
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+      float& f0 = f[2 * i];
+      float& f1 = f[2 * i + 1];
+      if (!RMS) tc::sub_x2(f0, f1, mu, mu, f0, f1);
+      tc::mul_x2(f0, f1, rs, rs, f0, f1);
+      float r0 = b[2 * i], r1 = b[2 * i + 1];
+      tc::fma2_acc(f0, f1, w[2 * i], w[2 * i + 1], r0, r1);
+      f0 = r0;
+      f1 = r1;
+    }
+    return X::pack(f);
+  }
+  // column sums of dw and db, row sums of g xh and g (g = dy w)
+  static __device__ __forceinline__ void grad_part(const uint4 (&x)[U], const uint4 (&dy)[U], float mu, float rs,
+                                                   const float* w, float* dw, float* db, float& sgx, float& sg) {
+    float a0 = 0.f, a1 = 0.f, c0 = 0.f, c1 = 0.f;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      float f[E], g[E];
+      X::unpack(x[u], f);
+      X::unpack(dy[u], g);   // zero past the row and past the last row
+#pragma unroll
+      for (int i = 0; i < P; ++i) {
+        const int k = u * E + 2 * i;
+        float h0 = f[2 * i], h1 = f[2 * i + 1], g0 = g[2 * i], g1 = g[2 * i + 1];
+        if (!RMS) tc::sub_x2(h0, h1, mu, mu, h0, h1);
+        tc::mul_x2(h0, h1, rs, rs, h0, h1);
+        tc::fma2_acc(g0, g1, h0, h1, dw[k], dw[k + 1]);
+        tc::add_x2(db[k], db[k + 1], g0, g1);
+        tc::mul_x2(g0, g1, w[k], w[k + 1], g0, g1);
+        tc::fma2_acc(g0, g1, h0, h1, a0, a1);
+        if (!RMS) tc::add_x2(c0, c1, g0, g1);
+      }
+    }
+    sgx = a0 + a1;
+    sg = c0 + c1;
+  }
+  // dx = rs (g - mg - xh mgx)
+  static __device__ __forceinline__ uint4 grad_out(const uint4& x, const uint4& dy, float mu, float rs, float mg,
+                                                   float mgx, const float* w) {
+    float f[E], g[E];
+    X::unpack(x, f);
+    X::unpack(dy, g);
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+      float h0 = f[2 * i], h1 = f[2 * i + 1], r0 = -mg, r1 = -mg;
+      if (!RMS) tc::sub_x2(h0, h1, mu, mu, h0, h1);
+      tc::mul_x2(h0, h1, rs, rs, h0, h1);
+      tc::fma2_acc(g[2 * i], g[2 * i + 1], w[2 * i], w[2 * i + 1], r0, r1);
+      tc::fma2_acc(h0, h1, -mgx, -mgx, r0, r1);
+      tc::mul_x2(r0, r1, rs, rs, f[2 * i], f[2 * i + 1]);
+    }
+    return X::pack(f);
+  }
+  // this thread's columns of a parameter vector
+  static __device__ __forceinline__ void params(const float* p, float missing, int t, int T_row, int V, float* out) {
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        const int v = t + u * T_row;
+        out[u * E + e] = v < V && p != nullptr ? p[v * E + e] : missing;
+      }
+  }
+};
+
+// Rows of up to 128 vectors: L lanes per row with U vectors each (two where the
+// row allows: fewer shuffles per value), RB rows in flight per lane group.
 template <typename T, int L, int U, int RB, bool RMS>
-__global__ void __launch_bounds__(max_threads<T, L, U>())
+__global__ void __launch_bounds__(kWarpThreads)
 norm_fwd_kernel(const Rows R, const T* __restrict__ x, int64_t x_stride, const float* __restrict__ w,
                 const float* __restrict__ b, float eps, T* __restrict__ y, float* __restrict__ mean,
                 float* __restrict__ rstd) {
-  using X = Vec<T>;
-  constexpr int E = X::E;
-  __shared__ float sm[L == 0 ? 2 * kMaxWarps * RB : 1];
+  using S = Share<T, U, RMS>;
+  constexpr int E = S::E;
   int buf = 0;
-  const int T_row = L == 0 ? blockDim.x : L;             // threads of a row
-  const int t = L == 0 ? threadIdx.x : threadIdx.x % L;  // this thread's place in its row
-  const int slots = L == 0 ? 1 : blockDim.x / L, slot = L == 0 ? 0 : threadIdx.x / L;
+  const int t = threadIdx.x % L;                          // this thread's place in its row
+  constexpr int slots = kWarpThreads / L;
+  const int slot = threadIdx.x / L;
+  const int have = (R.V - t + L - 1) / L;                 // vectors of this thread that exist
   float wr[U * E], br[U * E];
-#pragma unroll
-  for (int u = 0; u < U; ++u)
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-      const int v = t + u * T_row, c = v * E + e;
-      wr[u * E + e] = v < R.V && w != nullptr ? w[c] : 1.f;
-      br[u * E + e] = v < R.V && b != nullptr ? b[c] : 0.f;
-    }
+  S::params(w, 1.f, t, L, R.V, wr);
+  S::params(b, 0.f, t, L, R.V, br);
   const float inv_c = 1.0f / (float)R.C;
   const int64_t step = (int64_t)gridDim.x * slots * RB;
   for (int64_t base = (int64_t)blockIdx.x * slots * RB; base < R.rows; base += step) {
     uint4 xv[RB][U];
-    float s[RB];
 #pragma unroll
     for (int r = 0; r < RB; ++r) {
       const int64_t row = base + r * slots + slot;
-      const uint4* src = reinterpret_cast<const uint4*>(x + (row < R.rows ? R.at(row, x_stride) : 0));
+      const uint4* src = reinterpret_cast<const uint4*>(x + (row < R.rows ? R.at(row, x_stride) : 0)) + t;
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int v = t + u * T_row;
-        xv[r][u] = row < R.rows && v < R.V ? __ldcs(src + v) : make_uint4(0, 0, 0, 0);
-      }
+      for (int u = 0; u < U; ++u) xv[r][u] = row < R.rows && u < have ? __ldcs(src + u * L) : make_uint4(0, 0, 0, 0);
     }
     float mu[RB], q[RB];
 #pragma unroll
     for (int r = 0; r < RB; ++r) mu[r] = 0.f;
     if (!RMS) {
 #pragma unroll
-      for (int r = 0; r < RB; ++r) {
-        s[r] = 0.f;
+      for (int r = 0; r < RB; ++r) S::mean_part(xv[r], mu[r]);
+      row_sum<L, RB>(mu, nullptr, buf);
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-          float f[E];
-          X::unpack(xv[r][u], f);
-#pragma unroll
-          for (int e = 0; e < E; ++e) s[r] += f[e];
-        }
-      }
-      row_sum<L, RB>(s, sm, buf);
-#pragma unroll
-      for (int r = 0; r < RB; ++r) mu[r] = s[r] * inv_c;
+      for (int r = 0; r < RB; ++r) mu[r] *= inv_c;
     }
 #pragma unroll
-    for (int r = 0; r < RB; ++r) {
-      q[r] = 0.f;
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        float f[E];
-        X::unpack(xv[r][u], f);
-        if (t + u * T_row < R.V)   // a vector past the row holds zeros, not the mean
-#pragma unroll
-          for (int e = 0; e < E; ++e) q[r] += (f[e] - mu[r]) * (f[e] - mu[r]);
-      }
-    }
-    row_sum<L, RB>(q, sm, buf);
+    for (int r = 0; r < RB; ++r) S::var_part(xv[r], mu[r], have, q[r]);
+    row_sum<L, RB>(q, nullptr, buf);
 #pragma unroll
     for (int r = 0; r < RB; ++r) {
       const int64_t row = base + r * slots + slot;
       if (row >= R.rows) continue;
       const float rs = 1.0f / sqrtf(q[r] * inv_c + eps);
-      uint4* dst = reinterpret_cast<uint4*>(y + row * R.C);
+      uint4* dst = reinterpret_cast<uint4*>(y + row * R.C) + t;
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int v = t + u * T_row;
-        if (v >= R.V) continue;
-        float f[E];
-        X::unpack(xv[r][u], f);
-#pragma unroll
-        for (int e = 0; e < E; ++e) f[e] = (f[e] - mu[r]) * rs * wr[u * E + e] + br[u * E + e];
-        __stcs(dst + v, X::pack(f));
-      }
+      for (int u = 0; u < U; ++u)
+        if (u < have) __stcs(dst + u * L, S::out(xv[r][u], mu[r], rs, wr + u * E, br + u * E));
       if (t == 0) {
         if (!RMS && mean != nullptr) mean[row] = mu[r];
         if (rstd != nullptr) rstd[row] = rs;
@@ -196,31 +275,110 @@ norm_fwd_kernel(const Rows R, const T* __restrict__ x, int64_t x_stride, const f
   }
 }
 
+// Longer rows: a CTA per row, RB rows per step. Each thread copies its own vectors
+// of the next rows into its own shared-memory slots (cp.async, `depth` steps of
+// them, as many of four as fit), so nothing but the row sums needs a barrier.
+constexpr int kMaxDepth = 4;
+constexpr size_t kRingBytes = 220000;
+inline int ring_depth(size_t step, int ctas) {
+  int d = kMaxDepth;
+  while (d > 1 && step * d * ctas > kRingBytes) --d;
+  return d;
+}
+template <typename T, int U>
+constexpr int cta_threads() { return U == 2 ? 512 : 16384 / (4 * Vec<T>::E); }   // of rows of up to 16,384 values
+template <typename T, int U, int RB, bool RMS>
+__global__ void __launch_bounds__(cta_threads<T, U>())
+norm_fwd_cta_kernel(const Rows R, const T* __restrict__ x, int64_t x_stride,
+                                    const float* __restrict__ w, const float* __restrict__ b, float eps,
+                                    T* __restrict__ y, float* __restrict__ mean, float* __restrict__ rstd, int depth) {
+  using S = Share<T, U, RMS>;
+  constexpr int E = S::E;
+  extern __shared__ uint4 ring[];   // [depth][RB][U][T_row]
+  __shared__ float sm[2 * kMaxWarps * RB];
+  int buf = 0;
+  const int t = threadIdx.x, T_row = blockDim.x;
+  const int have = (R.V - t + T_row - 1) / T_row;
+  float wr[U * E], br[U * E];
+  S::params(w, 1.f, t, T_row, R.V, wr);
+  S::params(b, 0.f, t, T_row, R.V, br);
+  const float inv_c = 1.0f / (float)R.C;
+  const int64_t step = (int64_t)gridDim.x * RB;
+  auto slot = [&](int st, int r, int u) { return ring + ((st * RB + r) * U + u) * T_row + t; };
+  auto fetch = [&](int64_t base, int st) {
+#pragma unroll
+    for (int r = 0; r < RB; ++r)
+      if (base + r < R.rows) {
+        const uint4* src = reinterpret_cast<const uint4*>(x + R.at(base + r, x_stride)) + t;
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+          if (u < have) copy_async16(slot(st, r, u), src + u * T_row);
+      }
+    copy_commit();
+  };
+  const int64_t first = (int64_t)blockIdx.x * RB;
+  for (int s = 0; s < depth - 1; ++s) fetch(first + s * step, s);
+  int st = 0;
+  for (int64_t base = first; base < R.rows; base += step, st = st + 1 == depth ? 0 : st + 1) {
+    fetch(base + (depth - 1) * step, st == 0 ? depth - 1 : st - 1);   // the slots of the step before
+    copy_wait(depth - 1);
+    uint4 xv[RB][U];
+#pragma unroll
+    for (int r = 0; r < RB; ++r)
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        xv[r][u] = base + r < R.rows && u < have ? *slot(st, r, u) : make_uint4(0, 0, 0, 0);
+    float mu[RB], q[RB];
+#pragma unroll
+    for (int r = 0; r < RB; ++r) mu[r] = 0.f;
+    if (!RMS) {
+#pragma unroll
+      for (int r = 0; r < RB; ++r) S::mean_part(xv[r], mu[r]);
+      row_sum<0, RB>(mu, sm, buf);
+#pragma unroll
+      for (int r = 0; r < RB; ++r) mu[r] *= inv_c;
+    }
+#pragma unroll
+    for (int r = 0; r < RB; ++r) S::var_part(xv[r], mu[r], have, q[r]);
+    row_sum<0, RB>(q, sm, buf);
+#pragma unroll
+    for (int r = 0; r < RB; ++r) {
+      const int64_t row = base + r;
+      if (row >= R.rows) continue;
+      const float rs = 1.0f / sqrtf(q[r] * inv_c + eps);
+      uint4* dst = reinterpret_cast<uint4*>(y + row * R.C) + t;
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (u < have) __stcs(dst + u * T_row, S::out(xv[r][u], mu[r], rs, wr + u * E, br + u * E));
+      if (t == 0) {
+        if (!RMS && mean != nullptr) mean[row] = mu[r];
+        if (rstd != nullptr) rstd[row] = rs;
+      }
+    }
+  }
+  copy_wait<0>();
+}
+
 // Column sums of this CTA's rows go to part[blockIdx][0 or 1][C]; the rows of
 // one CTA are summed per thread in order, then over the CTA's row slots in
 // order, then norm_reduce_kernel adds the CTAs in order: no atomics.
 template <typename T, int L, int U, int RB, bool RMS>
-__global__ void __launch_bounds__(max_threads<T, L, U>())
+__global__ void __launch_bounds__(kWarpThreads, U == 4 ? 1 : 2)
 norm_bwd_kernel(const Rows R, const T* __restrict__ dy, const T* __restrict__ x, int64_t x_stride,
                 const float* __restrict__ w, const float* __restrict__ mean, const float* __restrict__ rstd,
                 T* __restrict__ dx, int64_t dx_stride, float* __restrict__ part, int with_db) {
-  using X = Vec<T>;
-  constexpr int E = X::E;
+  using S = Share<T, U, RMS>;
+  constexpr int E = S::E;
   constexpr int K = RMS ? RB : 2 * RB;
-  __shared__ float sm[L == 0 ? 2 * kMaxWarps * K : 1];
   int buf = 0;
-  const int T_row = L == 0 ? blockDim.x : L;
-  const int t = L == 0 ? threadIdx.x : threadIdx.x % L;
-  const int slots = L == 0 ? 1 : blockDim.x / L, slot = L == 0 ? 0 : threadIdx.x / L;
+  const int t = threadIdx.x % L;
+  constexpr int slots = kWarpThreads / L;
+  const int slot = threadIdx.x / L;
+  const int have = (R.V - t + L - 1) / L;
   float wr[U * E], dw[U * E], db[U * E];
+  S::params(w, 1.f, t, L, R.V, wr);
 #pragma unroll
-  for (int u = 0; u < U; ++u)
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-      const int v = t + u * T_row, c = v * E + e;
-      wr[u * E + e] = v < R.V && w != nullptr ? w[c] : 1.f;
-      dw[u * E + e] = db[u * E + e] = 0.f;
-    }
+  for (int i = 0; i < U * E; ++i) dw[i] = db[i] = 0.f;
   const float inv_c = 1.0f / (float)R.C;
   const int64_t step = (int64_t)gridDim.x * slots * RB;
   for (int64_t base = (int64_t)blockIdx.x * slots * RB; base < R.rows; base += step) {
@@ -230,93 +388,133 @@ norm_bwd_kernel(const Rows R, const T* __restrict__ dy, const T* __restrict__ x,
     for (int r = 0; r < RB; ++r) {
       const int64_t row = base + r * slots + slot;
       const bool ok = row < R.rows;
-      const uint4* src = reinterpret_cast<const uint4*>(x + (ok ? R.at(row, x_stride) : 0));
-      const uint4* gsrc = reinterpret_cast<const uint4*>(dy + (ok ? row * R.C : 0));
+      const uint4* src = reinterpret_cast<const uint4*>(x + (ok ? R.at(row, x_stride) : 0)) + t;
+      const uint4* gsrc = reinterpret_cast<const uint4*>(dy + (ok ? row * R.C : 0)) + t;
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int v = t + u * T_row;
-        const bool in = ok && v < R.V;
-        xv[r][u] = in ? __ldcs(src + v) : make_uint4(0, 0, 0, 0);
-        gv[r][u] = in ? __ldcs(gsrc + v) : make_uint4(0, 0, 0, 0);
+        xv[r][u] = ok && u < have ? __ldcs(src + u * L) : make_uint4(0, 0, 0, 0);
+        gv[r][u] = ok && u < have ? __ldcs(gsrc + u * L) : make_uint4(0, 0, 0, 0);
       }
       mu[r] = !RMS && ok ? mean[row] : 0.f;
       rs[r] = ok ? rstd[row] : 0.f;
     }
 #pragma unroll
     for (int r = 0; r < RB; ++r) {
-      float sg = 0.f, sgx = 0.f;
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        float f[E], g[E];
-        X::unpack(xv[r][u], f);
-        X::unpack(gv[r][u], g);   // zero past the row and past the last row
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-          const float xh = (f[e] - mu[r]) * rs[r], gw = g[e] * wr[u * E + e];
-          dw[u * E + e] += g[e] * xh;
-          db[u * E + e] += g[e];
-          sg += gw;
-          sgx += gw * xh;
-        }
-      }
-      s[RMS ? r : 2 * r] = sgx;
+      float sg;
+      S::grad_part(xv[r], gv[r], mu[r], rs[r], wr, dw, db, s[RMS ? r : 2 * r], sg);
       if (!RMS) s[RMS ? 0 : 2 * r + 1] = sg;
     }
-    row_sum<L, K>(s, sm, buf);
+    row_sum<L, K>(s, nullptr, buf);
 #pragma unroll
     for (int r = 0; r < RB; ++r) {
       const int64_t row = base + r * slots + slot;
       if (row >= R.rows) continue;
       const float mgx = s[RMS ? r : 2 * r] * inv_c, mg = RMS ? 0.f : s[RMS ? 0 : 2 * r + 1] * inv_c;
-      uint4* dst = reinterpret_cast<uint4*>(dx + R.at(row, dx_stride));
+      uint4* dst = reinterpret_cast<uint4*>(dx + R.at(row, dx_stride)) + t;
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int v = t + u * T_row;
-        if (v >= R.V) continue;
-        float f[E], g[E];
-        X::unpack(xv[r][u], f);
-        X::unpack(gv[r][u], g);
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-          const float xh = (f[e] - mu[r]) * rs[r];
-          f[e] = rs[r] * (g[e] * wr[u * E + e] - mg - xh * mgx);
-        }
-        __stcs(dst + v, X::pack(f));
-      }
+      for (int u = 0; u < U; ++u)
+        if (u < have) __stcs(dst + u * L, S::grad_out(xv[r][u], gv[r][u], mu[r], rs[r], mg, mgx, wr + u * E));
     }
   }
   if (part == nullptr) return;
+  // the CTA's row slots, one vector column at a time
   float* out = part + (int64_t)blockIdx.x * 2 * R.C;
-  if (L == 0) {
+  __shared__ float col[kWarpThreads][E + 1];
+  for (int which = 0; which < (with_db ? 2 : 1); ++which)
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int v = t + u * T_row;
-      if (v >= R.V) continue;
+      __syncthreads();
 #pragma unroll
-      for (int e = 0; e < E; ++e) {
-        out[v * E + e] = dw[u * E + e];
-        if (with_db) out[R.C + v * E + e] = db[u * E + e];
+      for (int e = 0; e < E; ++e) col[threadIdx.x][e] = which ? db[u * E + e] : dw[u * E + e];
+      __syncthreads();
+      for (int i = threadIdx.x; i < L * E; i += kWarpThreads) {
+        const int tt = i / E, e = i % E, v = tt + u * L;
+        if (v >= R.V) continue;
+        float sum = 0.f;
+        for (int sl = 0; sl < slots; ++sl) sum += col[sl * L + tt][e];
+        out[which * R.C + v * E + e] = sum;
       }
     }
-  } else {
-    // the CTA's row slots, one vector column at a time
-    __shared__ float col[kWarpThreads][E + 1];
-    for (int which = 0; which < (with_db ? 2 : 1); ++which)
+}
+
+// Longer rows: a CTA per row with the forward's ring, of x and dy. MAXT, MINB:
+// threads and resident CTAs the registers are shared out for.
+template <typename T, int U, bool RMS, int MAXT, int MINB>
+__global__ void __launch_bounds__(MAXT, MINB)
+norm_bwd_cta_kernel(const Rows R, const T* __restrict__ dy, const T* __restrict__ x, int64_t x_stride,
+                    const float* __restrict__ w, const float* __restrict__ mean, const float* __restrict__ rstd,
+                    T* __restrict__ dx, int64_t dx_stride, float* __restrict__ part, int with_db, int depth) {
+  using S = Share<T, U, RMS>;
+  constexpr int E = S::E;
+  constexpr int K = RMS ? 1 : 2;
+  extern __shared__ uint4 ring[];   // [depth][x, dy][U][T_row]
+  __shared__ float sm[2 * kMaxWarps * K];
+  int buf = 0;
+  const int t = threadIdx.x, T_row = blockDim.x;
+  const int have = (R.V - t + T_row - 1) / T_row;
+  float wr[U * E], dw[U * E], db[U * E];
+  S::params(w, 1.f, t, T_row, R.V, wr);
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        __syncthreads();
+  for (int i = 0; i < U * E; ++i) dw[i] = db[i] = 0.f;
+  const float inv_c = 1.0f / (float)R.C;
+  auto slot = [&](int st, int which, int u) { return ring + ((st * 2 + which) * U + u) * T_row + t; };
+  auto fetch = [&](int64_t row, int st) {
+    if (row < R.rows) {
+      const uint4* src = reinterpret_cast<const uint4*>(x + R.at(row, x_stride)) + t;
+      const uint4* gsrc = reinterpret_cast<const uint4*>(dy + row * R.C) + t;
 #pragma unroll
-        for (int e = 0; e < E; ++e) col[threadIdx.x][e] = which ? db[u * E + e] : dw[u * E + e];
-        __syncthreads();
-        for (int i = threadIdx.x; i < T_row * E; i += blockDim.x) {
-          const int tt = i / E, e = i % E, v = tt + u * T_row;
-          if (v >= R.V) continue;
-          float sum = 0.f;
-          for (int sl = 0; sl < slots; ++sl) sum += col[sl * T_row + tt][e];
-          out[which * R.C + v * E + e] = sum;
+      for (int u = 0; u < U; ++u)
+        if (u < have) {
+          copy_async16(slot(st, 0, u), src + u * T_row);
+          copy_async16(slot(st, 1, u), gsrc + u * T_row);
         }
-      }
+    }
+    copy_commit();
+  };
+  const int64_t step = gridDim.x;
+  for (int s = 0; s < depth - 1; ++s) fetch(blockIdx.x + s * step, s);
+  int st = 0;
+  float mu_n = 0.f, rs_n = 0.f;   // the next row's statistics
+  if (blockIdx.x < R.rows) {
+    mu_n = RMS ? 0.f : mean[blockIdx.x];
+    rs_n = rstd[blockIdx.x];
   }
+  for (int64_t row = blockIdx.x; row < R.rows; row += step, st = st + 1 == depth ? 0 : st + 1) {
+    fetch(row + (depth - 1) * step, st == 0 ? depth - 1 : st - 1);
+    copy_wait(depth - 1);
+    const float mu = mu_n, rs = rs_n;
+    if (row + step < R.rows) {
+      mu_n = RMS ? 0.f : mean[row + step];
+      rs_n = rstd[row + step];
+    }
+    uint4 xv[U], gv[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      xv[u] = u < have ? *slot(st, 0, u) : make_uint4(0, 0, 0, 0);
+      gv[u] = u < have ? *slot(st, 1, u) : make_uint4(0, 0, 0, 0);
+    }
+    float s[K], sg;
+    S::grad_part(xv, gv, mu, rs, wr, dw, db, s[0], sg);
+    if (!RMS) s[K - 1] = sg;
+    row_sum<0, K>(s, sm, buf);
+    const float mgx = s[0] * inv_c, mg = RMS ? 0.f : s[K - 1] * inv_c;
+    uint4* dst = reinterpret_cast<uint4*>(dx + R.at(row, dx_stride)) + t;
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (u < have) __stcs(dst + u * T_row, S::grad_out(xv[u], gv[u], mu, rs, mg, mgx, wr + u * E));
+  }
+  copy_wait<0>();
+  if (part == nullptr) return;
+  float* out = part + (int64_t)blockIdx.x * 2 * R.C;
+#pragma unroll
+  for (int u = 0; u < U; ++u)
+    if (u < have)
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        const int c = (t + u * T_row) * E + e;
+        out[c] = dw[u * E + e];
+        if (with_db) out[R.C + c] = db[u * E + e];
+      }
 }
 
 // dw[c] = sum over G CTAs of part[g][0][c], db likewise: 32 columns per CTA,
@@ -352,52 +550,85 @@ Rows rows_of(const Dims& s, bool head) {
   return R;
 }
 
-// CTAs of the backward (its workspace holds one pair of column sums each): one
-// or two per SM for CTA rows, eight for shuffle rows, never more than the
-// batches of rows. `sms` is an upper bound on the SM count.
+// CTAs of the backward (its workspace holds one pair of column sums each), never
+// more than the batches of rows. `sms` is an upper bound on the SM count.
 constexpr int kSmBound = 160;
+int lanes_of(const Rows& R) { return R.V <= 8 ? 4 : R.V <= 16 ? 8 : R.V <= 32 ? 16 : 32; }
 int64_t bwd_ctas(const Rows& R, int sms) {
   const bool cta = R.V > 128;
-  const int64_t per = cta ? 2 : 8;
-  const int64_t slots = cta ? 1 : kWarpThreads / (R.V <= 8 ? 8 : R.V <= 16 ? 16 : 32);
-  const int64_t need = (R.rows + slots - 1) / slots;
-  return need < per * sms ? need : per * sms;
+  const int64_t slots = cta ? 1 : kWarpThreads / lanes_of(R);
+  const int64_t need = (R.rows + slots - 1) / slots, cap = (int64_t)sms * 2;
+  return need < cap ? need : cap;
+}
+
+bool set_smem(const void* kern, size_t bytes) {
+  return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) == cudaSuccess;
 }
 
 template <typename T, bool RMS>
 struct Go {
   template <int L, int U, int RB>
-  static void fwd(const Rows& R, const void* x, int64_t xs, const float* w, const float* b, float eps, void* y,
+  static bool fwd(const Rows& R, const void* x, int64_t xs, const float* w, const float* b, float eps, void* y,
                   float* mean, float* rstd, int sms, cudaStream_t st) {
-    const int threads = L == 0 ? 32 * ((R.V + 32 * U - 1) / (32 * U)) : kWarpThreads;
-    const int64_t slots = L == 0 ? 1 : kWarpThreads / (L == 0 ? 1 : L);
+    constexpr int64_t slots = kWarpThreads / L;
     int64_t grid = (R.rows + slots * RB - 1) / (slots * RB);
-    const int64_t cap = (int64_t)sms * (L == 0 ? (2048 / threads) : 8);
-    if (grid > cap) grid = cap;
-    norm_fwd_kernel<T, L, U, RB, RMS><<<(unsigned)grid, threads, 0, st>>>(R, (const T*)x, xs, w, b, eps, (T*)y, mean,
-                                                                          rstd);
+    if (grid > (int64_t)sms * 8) grid = (int64_t)sms * 8;
+    norm_fwd_kernel<T, L, U, RB, RMS><<<(unsigned)grid, kWarpThreads, 0, st>>>(R, (const T*)x, xs, w, b, eps, (T*)y,
+                                                                               mean, rstd);
+    return true;
+  }
+  template <int U, int RB>
+  static bool fwd_cta(const Rows& R, const void* x, int64_t xs, const float* w, const float* b, float eps, void* y,
+                      float* mean, float* rstd, int sms, cudaStream_t st) {
+    const int threads = 32 * ((R.V + 32 * U - 1) / (32 * U));
+    const size_t step = (size_t)RB * U * threads * 16;
+    const int depth = ring_depth(step, U == 2 ? 2 : 1);   // two CTAs per SM where a thread has two vectors
+    const size_t smem = step * depth;
+    auto kern = norm_fwd_cta_kernel<T, U, RB, RMS>;
+    if (!set_smem((const void*)kern, smem)) return false;
+    int per = 0;
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kern, threads, smem) != cudaSuccess || per < 1) return false;
+    int64_t grid = (R.rows + RB - 1) / RB;
+    if (grid > (int64_t)sms * per) grid = (int64_t)sms * per;
+    kern<<<(unsigned)grid, threads, smem, st>>>(R, (const T*)x, xs, w, b, eps, (T*)y, mean, rstd, depth);
+    return true;
   }
   template <int L, int U, int RB>
-  static void bwd(const Rows& R, const void* dy, const void* x, int64_t xs, const float* w, const float* mean,
+  static bool bwd(const Rows& R, const void* dy, const void* x, int64_t xs, const float* w, const float* mean,
                   const float* rstd, void* dx, int64_t dxs, float* part, int with_db, int64_t grid, cudaStream_t st) {
-    const int threads = L == 0 ? 32 * ((R.V + 32 * U - 1) / (32 * U)) : kWarpThreads;
-    norm_bwd_kernel<T, L, U, RB, RMS><<<(unsigned)grid, threads, 0, st>>>(R, (const T*)dy, (const T*)x, xs, w, mean,
-                                                                          rstd, (T*)dx, dxs, part, with_db);
+    norm_bwd_kernel<T, L, U, RB, RMS><<<(unsigned)grid, kWarpThreads, 0, st>>>(
+        R, (const T*)dy, (const T*)x, xs, w, mean, rstd, (T*)dx, dxs, part, with_db);
+    return true;
+  }
+  template <int U, int MAXT, int MINB>
+  static bool bwd_cta(const Rows& R, const void* dy, const void* x, int64_t xs, const float* w, const float* mean,
+                      const float* rstd, void* dx, int64_t dxs, float* part, int with_db, int64_t grid,
+                      cudaStream_t st) {
+    const int threads = 32 * ((R.V + 32 * U - 1) / (32 * U));
+    const size_t step = (size_t)2 * U * threads * 16;
+    const int depth = ring_depth(step, MINB);
+    constexpr int kThreads = U == 4 ? cta_threads<T, U>() : MAXT;
+    auto kern = norm_bwd_cta_kernel<T, U, RMS, kThreads, MINB>;
+    if (!set_smem((const void*)kern, step * depth)) return false;
+    kern<<<(unsigned)grid, threads, step * depth, st>>>(R, (const T*)dy, (const T*)x, xs, w, mean, rstd, (T*)dx, dxs,
+                                                        part, with_db, depth);
+    return true;
   }
 };
 
 // Threads per row and vectors per thread by the row's length in 16-byte vectors:
-// up to 128 vectors a quarter, half or whole warp; longer rows a CTA with two
-// vectors a thread, four beyond 1,024.
-#define NORM_ROWS(CALL)                          \
+// up to 128 vectors part of a warp, longer rows a CTA with two vectors a
+// thread, four beyond 1,024.
+#define NORM_ROWS(WARP, CTA)                     \
   do {                                           \
-    if (R.V <= 8) CALL(8, 1, 4);                 \
-    else if (R.V <= 16) CALL(16, 1, 4);          \
-    else if (R.V <= 32) CALL(32, 1, 4);          \
-    else if (R.V <= 64) CALL(32, 2, 2);          \
-    else if (R.V <= 128) CALL(32, 4, 1);         \
-    else if (R.V <= 1024) CALL(0, 2, 1);         \
-    else CALL(0, 4, 1);                          \
+    if (R.V <= 8) WARP(4, 2, 2);                 \
+    else if (R.V <= 16) WARP(8, 2, 2);           \
+    else if (R.V <= 32) WARP(16, 2, 2);          \
+    else if (R.V <= 64) WARP(32, 2, 2);          \
+    else if (R.V <= 128) WARP(32, 4, 1);         \
+    else if (R.V <= 640) CTA(2, 320, 2);         \
+    else if (R.V <= 1024) CTA(2, 512, 1);        \
+    else CTA(4, 1024, 1);                        \
   } while (0)
 
 }  // namespace
@@ -412,18 +643,19 @@ sparsp_status_t launch_norm_fwd(const Dims& s, bool head, bool rms, const void* 
   const Rows R = rows_of(s, head);
   const int sms = device_sm_count();
   if (sms <= 0) return SPARSP_ERR_CUDA;
-#define NORM_FWD_CALL(L, U, RB)                                                                        \
-  do {                                                                                                 \
-    if (s.dtype == SPARSP_F32) {                                                                       \
-      if (rms) Go<float, true>::fwd<L, U, RB>(R, x, x_stride, w, b, eps, y, mean, rstd, sms, st);      \
-      else Go<float, false>::fwd<L, U, RB>(R, x, x_stride, w, b, eps, y, mean, rstd, sms, st);         \
-    } else {                                                                                           \
-      if (rms) Go<__nv_bfloat16, true>::fwd<L, U, RB>(R, x, x_stride, w, b, eps, y, mean, rstd, sms, st); \
-      else Go<__nv_bfloat16, false>::fwd<L, U, RB>(R, x, x_stride, w, b, eps, y, mean, rstd, sms, st); \
-    }                                                                                                  \
+  bool ok = false;
+#define NORM_TYPED(CALL)                                                  \
+  do {                                                                    \
+    if (s.dtype == SPARSP_F32) ok = rms ? Go<float, true>::CALL : Go<float, false>::CALL; \
+    else ok = rms ? Go<__nv_bfloat16, true>::CALL : Go<__nv_bfloat16, false>::CALL;      \
   } while (0)
-  NORM_ROWS(NORM_FWD_CALL);
-#undef NORM_FWD_CALL
+#define NORM_WARP(L, U, RB) NORM_TYPED(template fwd<L NORM_COMMA U NORM_COMMA RB>(R, x, x_stride, w, b, eps, y, mean, rstd, sms, st))
+#define NORM_CTA(U, MAXT, MINB) NORM_TYPED(template fwd_cta<U NORM_COMMA (U == 4 ? 1 : 2)>(R, x, x_stride, w, b, eps, y, mean, rstd, sms, st))
+#define NORM_COMMA ,
+  NORM_ROWS(NORM_WARP, NORM_CTA);
+#undef NORM_WARP
+#undef NORM_CTA
+  if (!ok) return SPARSP_ERR_CUDA;
   SPARSP_LAUNCH_CHECK();
   return SPARSP_OK;
 }
@@ -438,18 +670,19 @@ sparsp_status_t launch_norm_bwd(const Dims& s, bool head, bool rms, const void* 
   const int64_t grid = bwd_ctas(R, sms);
   float* part = dw != nullptr || db != nullptr ? (float*)ws : nullptr;
   const int with_db = db != nullptr;
-#define NORM_BWD_CALL(L, U, RB)                                                                                     \
-  do {                                                                                                              \
-    if (s.dtype == SPARSP_F32) {                                                                                    \
-      if (rms) Go<float, true>::bwd<L, U, RB>(R, dy, x, x_stride, w, mean, rstd, dx, dx_stride, part, with_db, grid, st); \
-      else Go<float, false>::bwd<L, U, RB>(R, dy, x, x_stride, w, mean, rstd, dx, dx_stride, part, with_db, grid, st);    \
-    } else {                                                                                                        \
-      if (rms) Go<__nv_bfloat16, true>::bwd<L, U, RB>(R, dy, x, x_stride, w, mean, rstd, dx, dx_stride, part, with_db, grid, st); \
-      else Go<__nv_bfloat16, false>::bwd<L, U, RB>(R, dy, x, x_stride, w, mean, rstd, dx, dx_stride, part, with_db, grid, st);    \
-    }                                                                                                               \
-  } while (0)
-  NORM_ROWS(NORM_BWD_CALL);
-#undef NORM_BWD_CALL
+  bool ok = false;
+#define NORM_WARP(L, U, RB)                                                                                          \
+  NORM_TYPED(template bwd<L NORM_COMMA U NORM_COMMA RB>(R, dy, x, x_stride, w, mean, rstd, dx, dx_stride, part,        \
+                                                        with_db, grid, st))
+#define NORM_CTA(U, MAXT, MINB)                                                                                      \
+  NORM_TYPED(template bwd_cta<U NORM_COMMA MAXT NORM_COMMA MINB>(R, dy, x, x_stride, w, mean, rstd, dx, dx_stride, part, \
+                                                                 with_db, grid, st))
+  NORM_ROWS(NORM_WARP, NORM_CTA);
+#undef NORM_WARP
+#undef NORM_CTA
+#undef NORM_TYPED
+#undef NORM_COMMA
+  if (!ok) return SPARSP_ERR_CUDA;
   SPARSP_LAUNCH_CHECK();
   if (part != nullptr) {
     dim3 g((R.C + 31) / 32, with_db ? 2 : 1);
