@@ -23,39 +23,72 @@ namespace {
 constexpr int kWarpThreads = 256;   // CTA of the shuffle kernels
 constexpr int kMaxWarps = 32;
 
+// Two fp32 values in one 64-bit register pair, for the packed fp32 instructions:
+// held as one operand from load to store, so that no moves are spent on pairing.
+typedef unsigned long long f32x2;
+__device__ __forceinline__ f32x2 pair(float a, float b) {
+  f32x2 r;
+  asm("mov.b64 %0, {%1, %2};\n" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 both(f32x2 v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;\n" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+  f32x2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;\n" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("add.rn.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ float hsum(f32x2 v) {
+  const float2 t = both(v);
+  return t.x + t.y;
+}
+
 // 16 bytes of a row as fp32 pairs and back.
 template <typename T>
 struct Vec;
 template <>
 struct Vec<__nv_bfloat16> {
   static constexpr int E = 8;
-  static __device__ __forceinline__ void unpack(const uint4& v, float* f) {
+  static __device__ __forceinline__ void unpack(const uint4& v, f32x2* f) {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {   // a bf16 is the upper half of its fp32
-      f[2 * e] = __uint_as_float(w[e] << 16);
-      f[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
-    }
+    for (int e = 0; e < 4; ++e)   // a bf16 is the upper half of its fp32
+      f[e] = pair(__uint_as_float(w[e] << 16), __uint_as_float(w[e] & 0xffff0000u));
   }
-  static __device__ __forceinline__ uint4 pack(const float* f) {
+  static __device__ __forceinline__ uint4 pack(const f32x2* f) {
     uint4 v;
     __nv_bfloat162* h = reinterpret_cast<__nv_bfloat162*>(&v);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) h[e] = __floats2bfloat162_rn(f[2 * e], f[2 * e + 1]);
+    for (int e = 0; e < 4; ++e) {
+      const float2 t = both(f[e]);
+      h[e] = __floats2bfloat162_rn(t.x, t.y);
+    }
     return v;
   }
 };
 template <>
 struct Vec<float> {
   static constexpr int E = 4;
-  static __device__ __forceinline__ void unpack(const uint4& v, float* f) {
-    f[0] = __uint_as_float(v.x);
-    f[1] = __uint_as_float(v.y);
-    f[2] = __uint_as_float(v.z);
-    f[3] = __uint_as_float(v.w);
+  static __device__ __forceinline__ void unpack(const uint4& v, f32x2* f) {
+    f[0] = pair(__uint_as_float(v.x), __uint_as_float(v.y));
+    f[1] = pair(__uint_as_float(v.z), __uint_as_float(v.w));
   }
-  static __device__ __forceinline__ uint4 pack(const float* f) {
-    return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+  static __device__ __forceinline__ uint4 pack(const f32x2* f) {
+    const float2 a = both(f[0]), b = both(f[1]);
+    return make_uint4(__float_as_uint(a.x), __float_as_uint(a.y), __float_as_uint(b.x), __float_as_uint(b.y));
   }
 };
 
@@ -68,6 +101,7 @@ struct Rows {
   int C;        // values per row
   int V;        // 16-byte vectors per row
   __device__ __forceinline__ int64_t at(int64_t row, int64_t stride) const {
+    if (stride == (int64_t)groups * C) return row * C;
     const int64_t tok = groups == 1 ? row : (int64_t)((uint32_t)row / (uint32_t)groups);
     return tok * stride + (row - tok * groups) * C;
   }
@@ -104,115 +138,107 @@ __device__ __forceinline__ void row_sum(float (&v)[K], float* sm, int& buf) {
 #pragma unroll
       for (int k = 0; k < K; ++k) s[warp * K + k] = v[k];
     __syncthreads();
+    const int lane = threadIdx.x & 31;
 #pragma unroll
-    for (int k = 0; k < K; ++k) v[k] = 0.f;
-#pragma unroll 4
-    for (int w = 0; w < nw; ++w)
+    for (int k = 0; k < K; ++k) v[k] = lane < nw ? s[lane * K + k] : 0.f;
+    if (nw > 16)
 #pragma unroll
-      for (int k = 0; k < K; ++k) v[k] += s[w * K + k];
+      for (int k = 0; k < K; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], 16);
+    // (with at most 16 warps the upper half of the lanes holds zeros and takes the lower half's sum below)
+#pragma unroll
+    for (int off = 8; off > 0; off >>= 1)
+#pragma unroll
+      for (int k = 0; k < K; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], off);
+    if (nw <= 16)
+#pragma unroll
+      for (int k = 0; k < K; ++k) v[k] = __shfl_sync(0xffffffffu, v[k], lane & 15);
   }
 }
 
-// One thread's share of a row: U vectors, t + u * T (T threads per row). `cols`
+// One thread's share of a row: U vectors, t + u * T (T threads per row). `have`
 // is how many of them exist; the others hold zeros.
 template <typename T, int U, bool RMS>
 struct Share {
   using X = Vec<T>;
-  static constexpr int E = X::E, P = E / 2;
+  static constexpr int E = X::E, P = E / 2;   // values and pairs of a vector
   static __device__ __forceinline__ void mean_part(const uint4 (&x)[U], float& s) {
-    float a0 = 0.f, a1 = 0.f;
+    f32x2 a = pair(0.f, 0.f);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      float f[E];
+      f32x2 f[P];
       X::unpack(x[u], f);
 #pragma unroll
-      for (int i = 0; i < P; ++i) tc::add_x2(a0, a1, f[2 * i], f[2 * i + 1]);
+      for (int i = 0; i < P; ++i) a = add2(a, f[i]);
     }
-    s = a0 + a1;
+    s = hsum(a);
   }
   // sum of (x - mu)^2 over the vectors that exist (a missing one holds zeros, not the mean)
   static __device__ __forceinline__ void var_part(const uint4 (&x)[U], float mu, int have, float& s) {
-    float a0 = 0.f, a1 = 0.f;
+    f32x2 a = pair(0.f, 0.f);
+    const f32x2 m = pair(-mu, -mu);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      float f[E];
+      f32x2 f[P];
       X::unpack(x[u], f);
       if (RMS || u < have)
 #pragma unroll
         for (int i = 0; i < P; ++i) {
-          float c0 = f[2 * i], c1 = f[2 * i + 1];
-          if (!RMS) tc::sub_x2(c0, c1, mu, mu, c0, c1);
-          tc::fma2_acc(c0, c1, c0, c1, a0, a1);
+          const f32x2 c = RMS ? f[i] : add2(f[i], m);
+          a = fma2(c, c, a);
         }
     }
-    s = a0 + a1;
+    s = hsum(a);
   }
-  static __device__ __forceinline__ uint4 out(const uint4& x, float mu, float rs, const float* w, const float* b) {
-    float f[E];
+  // (x - mu) rs w + b
+  static __device__ __forceinline__ uint4 out(const uint4& x, float mu, float rs, const f32x2* w, const f32x2* b) {
+    const f32x2 m = pair(-mu, -mu), r = pair(rs, rs);
+    f32x2 f[P];
     X::unpack(x, f);
 #pragma unroll
-    for (int i = 0; i < P; ++i) {
-      float& f0 = f[2 * i];
-      float& f1 = f[2 * i + 1];
-      if (!RMS) tc::sub_x2(f0, f1, mu, mu, f0, f1);
-      tc::mul_x2(f0, f1, rs, rs, f0, f1);
-      float r0 = b[2 * i], r1 = b[2 * i + 1];
-      tc::fma2_acc(f0, f1, w[2 * i], w[2 * i + 1], r0, r1);
-      f0 = r0;
-      f1 = r1;
-    }
+    for (int i = 0; i < P; ++i) f[i] = fma2(mul2(RMS ? f[i] : add2(f[i], m), r), w[i], b[i]);
     return X::pack(f);
   }
-  // column sums of dw and db, row sums of g xh and g (g = dy w)
+  // column sums of dw and db, row sums of g xh and g (g = dy w, xh = x rs - mu rs),
+  // and xh and g themselves for grad_out
   static __device__ __forceinline__ void grad_part(const uint4 (&x)[U], const uint4 (&dy)[U], float mu, float rs,
-                                                   const float* w, float* dw, float* db, float& sgx, float& sg) {
-    float a0 = 0.f, a1 = 0.f, c0 = 0.f, c1 = 0.f;
+                                                   const f32x2* w, f32x2* dw, f32x2* db, f32x2 (&h)[U * P],
+                                                   f32x2 (&g)[U * P], float& sgx, float& sg) {
+    f32x2 a = pair(0.f, 0.f), c = a;
+    const f32x2 r = pair(rs, rs), shift = pair(-mu * rs, -mu * rs);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      float f[E], g[E];
-      X::unpack(x[u], f);
-      X::unpack(dy[u], g);   // zero past the row and past the last row
+      X::unpack(x[u], h + u * P);
+      X::unpack(dy[u], g + u * P);   // zero past the row and past the last row, whatever xh is there
 #pragma unroll
-      for (int i = 0; i < P; ++i) {
-        const int k = u * E + 2 * i;
-        float h0 = f[2 * i], h1 = f[2 * i + 1], g0 = g[2 * i], g1 = g[2 * i + 1];
-        if (!RMS) tc::sub_x2(h0, h1, mu, mu, h0, h1);
-        tc::mul_x2(h0, h1, rs, rs, h0, h1);
-        tc::fma2_acc(g0, g1, h0, h1, dw[k], dw[k + 1]);
-        tc::add_x2(db[k], db[k + 1], g0, g1);
-        tc::mul_x2(g0, g1, w[k], w[k + 1], g0, g1);
-        tc::fma2_acc(g0, g1, h0, h1, a0, a1);
-        if (!RMS) tc::add_x2(c0, c1, g0, g1);
+      for (int k = u * P; k < (u + 1) * P; ++k) {
+        h[k] = RMS ? mul2(h[k], r) : fma2(h[k], r, shift);
+        dw[k] = fma2(g[k], h[k], dw[k]);
+        db[k] = add2(db[k], g[k]);
+        g[k] = mul2(g[k], w[k]);
+        a = fma2(g[k], h[k], a);
+        if (!RMS) c = add2(c, g[k]);
       }
     }
-    sgx = a0 + a1;
-    sg = c0 + c1;
+    sgx = hsum(a);
+    sg = hsum(c);
   }
-  // dx = rs (g - mg - xh mgx)
-  static __device__ __forceinline__ uint4 grad_out(const uint4& x, const uint4& dy, float mu, float rs, float mg,
-                                                   float mgx, const float* w) {
-    float f[E], g[E];
-    X::unpack(x, f);
-    X::unpack(dy, g);
+  // dx = rs (g - mg - xh mgx) of one vector
+  static __device__ __forceinline__ uint4 grad_out(const f32x2* h, const f32x2* g, float rs, float mg, float mgx) {
+    const f32x2 scale = pair(-rs * mgx, -rs * mgx), offset = pair(-rs * mg, -rs * mg), r = pair(rs, rs);
+    f32x2 f[P];
 #pragma unroll
-    for (int i = 0; i < P; ++i) {
-      float h0 = f[2 * i], h1 = f[2 * i + 1], r0 = -mg, r1 = -mg;
-      if (!RMS) tc::sub_x2(h0, h1, mu, mu, h0, h1);
-      tc::mul_x2(h0, h1, rs, rs, h0, h1);
-      tc::fma2_acc(g[2 * i], g[2 * i + 1], w[2 * i], w[2 * i + 1], r0, r1);
-      tc::fma2_acc(h0, h1, -mgx, -mgx, r0, r1);
-      tc::mul_x2(r0, r1, rs, rs, f[2 * i], f[2 * i + 1]);
-    }
+    for (int i = 0; i < P; ++i) f[i] = fma2(g[i], r, RMS ? mul2(h[i], scale) : fma2(h[i], scale, offset));
     return X::pack(f);
   }
   // this thread's columns of a parameter vector
-  static __device__ __forceinline__ void params(const float* p, float missing, int t, int T_row, int V, float* out) {
+  static __device__ __forceinline__ void params(const float* p, float missing, int t, int T_row, int V, f32x2* out) {
 #pragma unroll
     for (int u = 0; u < U; ++u)
 #pragma unroll
-      for (int e = 0; e < E; ++e) {
+      for (int i = 0; i < P; ++i) {
         const int v = t + u * T_row;
-        out[u * E + e] = v < V && p != nullptr ? p[v * E + e] : missing;
+        const bool there = v < V && p != nullptr;
+        out[u * P + i] = pair(there ? p[v * E + 2 * i] : missing, there ? p[v * E + 2 * i + 1] : missing);
       }
   }
 };
@@ -231,7 +257,7 @@ norm_fwd_kernel(const Rows R, const T* __restrict__ x, int64_t x_stride, const f
   constexpr int slots = kWarpThreads / L;
   const int slot = threadIdx.x / L;
   const int have = (R.V - t + L - 1) / L;                 // vectors of this thread that exist
-  float wr[U * E], br[U * E];
+  f32x2 wr[U * S::P], br[U * S::P];
   S::params(w, 1.f, t, L, R.V, wr);
   S::params(b, 0.f, t, L, R.V, br);
   const float inv_c = 1.0f / (float)R.C;
@@ -266,7 +292,7 @@ norm_fwd_kernel(const Rows R, const T* __restrict__ x, int64_t x_stride, const f
       uint4* dst = reinterpret_cast<uint4*>(y + row * R.C) + t;
 #pragma unroll
       for (int u = 0; u < U; ++u)
-        if (u < have) __stcs(dst + u * L, S::out(xv[r][u], mu[r], rs, wr + u * E, br + u * E));
+        if (u < have) __stcs(dst + u * L, S::out(xv[r][u], mu[r], rs, wr + u * S::P, br + u * S::P));
       if (t == 0) {
         if (!RMS && mean != nullptr) mean[row] = mu[r];
         if (rstd != nullptr) rstd[row] = rs;
@@ -295,11 +321,11 @@ norm_fwd_cta_kernel(const Rows R, const T* __restrict__ x, int64_t x_stride,
   using S = Share<T, U, RMS>;
   constexpr int E = S::E;
   extern __shared__ uint4 ring[];   // [depth][RB][U][T_row]
-  __shared__ float sm[2 * kMaxWarps * RB];
+  __shared__ __align__(16) float sm[2 * kMaxWarps * RB];
   int buf = 0;
   const int t = threadIdx.x, T_row = blockDim.x;
   const int have = (R.V - t + T_row - 1) / T_row;
-  float wr[U * E], br[U * E];
+  f32x2 wr[U * S::P], br[U * S::P];
   S::params(w, 1.f, t, T_row, R.V, wr);
   S::params(b, 0.f, t, T_row, R.V, br);
   const float inv_c = 1.0f / (float)R.C;
@@ -349,7 +375,7 @@ norm_fwd_cta_kernel(const Rows R, const T* __restrict__ x, int64_t x_stride,
       uint4* dst = reinterpret_cast<uint4*>(y + row * R.C) + t;
 #pragma unroll
       for (int u = 0; u < U; ++u)
-        if (u < have) __stcs(dst + u * T_row, S::out(xv[r][u], mu[r], rs, wr + u * E, br + u * E));
+        if (u < have) __stcs(dst + u * T_row, S::out(xv[r][u], mu[r], rs, wr + u * S::P, br + u * S::P));
       if (t == 0) {
         if (!RMS && mean != nullptr) mean[row] = mu[r];
         if (rstd != nullptr) rstd[row] = rs;
@@ -362,6 +388,7 @@ norm_fwd_cta_kernel(const Rows R, const T* __restrict__ x, int64_t x_stride,
 // Column sums of this CTA's rows go to part[blockIdx][0 or 1][C]; the rows of
 // one CTA are summed per thread in order, then over the CTA's row slots in
 // order, then norm_reduce_kernel adds the CTAs in order: no atomics.
+constexpr int kShortDepth = 4;
 template <typename T, int L, int U, int RB, bool RMS>
 __global__ void __launch_bounds__(kWarpThreads, U == 4 ? 1 : 2)
 norm_bwd_kernel(const Rows R, const T* __restrict__ dy, const T* __restrict__ x, int64_t x_stride,
@@ -375,33 +402,70 @@ norm_bwd_kernel(const Rows R, const T* __restrict__ dy, const T* __restrict__ x,
   constexpr int slots = kWarpThreads / L;
   const int slot = threadIdx.x / L;
   const int have = (R.V - t + L - 1) / L;
-  float wr[U * E], dw[U * E], db[U * E];
+  f32x2 wr[U * S::P], dw[U * S::P], db[U * S::P];
   S::params(w, 1.f, t, L, R.V, wr);
 #pragma unroll
-  for (int i = 0; i < U * E; ++i) dw[i] = db[i] = 0.f;
+  for (int i = 0; i < U * S::P; ++i) dw[i] = db[i] = pair(0.f, 0.f);
   const float inv_c = 1.0f / (float)R.C;
   const int64_t step = (int64_t)gridDim.x * slots * RB;
-  for (int64_t base = (int64_t)blockIdx.x * slots * RB; base < R.rows; base += step) {
-    uint4 xv[RB][U], gv[RB][U];
-    float mu[RB], rs[RB], s[K];
+  // each thread copies its own vectors of the next batches into slots of its own
+  extern __shared__ uint4 ring[];   // [kShortDepth][RB][x, dy][U][kWarpThreads]
+  auto place = [&](int st, int r, int which, int u) {
+    return ring + (((st * RB + r) * 2 + which) * U + u) * kWarpThreads + threadIdx.x;
+  };
+  auto fetch = [&](int64_t base, int st) {
 #pragma unroll
     for (int r = 0; r < RB; ++r) {
       const int64_t row = base + r * slots + slot;
-      const bool ok = row < R.rows;
-      const uint4* src = reinterpret_cast<const uint4*>(x + (ok ? R.at(row, x_stride) : 0)) + t;
-      const uint4* gsrc = reinterpret_cast<const uint4*>(dy + (ok ? row * R.C : 0)) + t;
+      if (row < R.rows) {
+        const uint4* src = reinterpret_cast<const uint4*>(x + R.at(row, x_stride)) + t;
+        const uint4* gsrc = reinterpret_cast<const uint4*>(dy + row * R.C) + t;
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+          if (u < have) {
+            copy_async16(place(st, r, 0, u), src + u * L);
+            copy_async16(place(st, r, 1, u), gsrc + u * L);
+          }
+      }
+    }
+    copy_commit();
+  };
+  float mu_n[RB], rs_n[RB];   // the next batch's statistics
+  auto stats = [&](int64_t base) {
+#pragma unroll
+    for (int r = 0; r < RB; ++r) {
+      const int64_t row = base + r * slots + slot;
+      mu_n[r] = !RMS && row < R.rows ? mean[row] : 0.f;
+      rs_n[r] = row < R.rows ? rstd[row] : 0.f;
+    }
+  };
+  const int64_t first = (int64_t)blockIdx.x * slots * RB;
+#pragma unroll
+  for (int s = 0; s < kShortDepth - 1; ++s) fetch(first + s * step, s);
+  stats(first);
+  int st = 0;
+  for (int64_t base = first; base < R.rows; base += step, st = st + 1 == kShortDepth ? 0 : st + 1) {
+    fetch(base + (kShortDepth - 1) * step, st == 0 ? kShortDepth - 1 : st - 1);
+    copy_wait<kShortDepth - 1>();
+    uint4 xv[RB][U], gv[RB][U];
+    f32x2 h[RB][U * S::P], g[RB][U * S::P];
+    float mu[RB], rs[RB], s[K];
+#pragma unroll
+    for (int r = 0; r < RB; ++r) {
+      mu[r] = mu_n[r];
+      rs[r] = rs_n[r];
+      const bool ok = base + r * slots + slot < R.rows;
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        xv[r][u] = ok && u < have ? __ldcs(src + u * L) : make_uint4(0, 0, 0, 0);
-        gv[r][u] = ok && u < have ? __ldcs(gsrc + u * L) : make_uint4(0, 0, 0, 0);
+        xv[r][u] = ok && u < have ? *place(st, r, 0, u) : make_uint4(0, 0, 0, 0);
+        gv[r][u] = ok && u < have ? *place(st, r, 1, u) : make_uint4(0, 0, 0, 0);
       }
-      mu[r] = !RMS && ok ? mean[row] : 0.f;
-      rs[r] = ok ? rstd[row] : 0.f;
     }
+    stats(base + step);
 #pragma unroll
     for (int r = 0; r < RB; ++r) {
       float sg;
-      S::grad_part(xv[r], gv[r], mu[r], rs[r], wr, dw, db, s[RMS ? r : 2 * r], sg);
+      S::grad_part(xv[r], gv[r], mu[r], rs[r], wr, dw, db, h[r], g[r], s[RMS ? r : 2 * r], sg);
       if (!RMS) s[RMS ? 0 : 2 * r + 1] = sg;
     }
     row_sum<L, K>(s, nullptr, buf);
@@ -413,9 +477,11 @@ norm_bwd_kernel(const Rows R, const T* __restrict__ dy, const T* __restrict__ x,
       uint4* dst = reinterpret_cast<uint4*>(dx + R.at(row, dx_stride)) + t;
 #pragma unroll
       for (int u = 0; u < U; ++u)
-        if (u < have) __stcs(dst + u * L, S::grad_out(xv[r][u], gv[r][u], mu[r], rs[r], mg, mgx, wr + u * E));
+        if (u < have)
+          __stcs(dst + u * L, S::grad_out(h[r] + u * S::P, g[r] + u * S::P, rs[r], mg, mgx));
     }
   }
+  copy_wait<0>();
   if (part == nullptr) return;
   // the CTA's row slots, one vector column at a time
   float* out = part + (int64_t)blockIdx.x * 2 * R.C;
@@ -425,7 +491,11 @@ norm_bwd_kernel(const Rows R, const T* __restrict__ dy, const T* __restrict__ x,
     for (int u = 0; u < U; ++u) {
       __syncthreads();
 #pragma unroll
-      for (int e = 0; e < E; ++e) col[threadIdx.x][e] = which ? db[u * E + e] : dw[u * E + e];
+      for (int i = 0; i < S::P; ++i) {
+        const float2 v = both(which ? db[u * S::P + i] : dw[u * S::P + i]);
+        col[threadIdx.x][2 * i] = v.x;
+        col[threadIdx.x][2 * i + 1] = v.y;
+      }
       __syncthreads();
       for (int i = threadIdx.x; i < L * E; i += kWarpThreads) {
         const int tt = i / E, e = i % E, v = tt + u * L;
@@ -448,14 +518,14 @@ norm_bwd_cta_kernel(const Rows R, const T* __restrict__ dy, const T* __restrict_
   constexpr int E = S::E;
   constexpr int K = RMS ? 1 : 2;
   extern __shared__ uint4 ring[];   // [depth][x, dy][U][T_row]
-  __shared__ float sm[2 * kMaxWarps * K];
+  __shared__ __align__(16) float sm[2 * kMaxWarps * K];
   int buf = 0;
   const int t = threadIdx.x, T_row = blockDim.x;
   const int have = (R.V - t + T_row - 1) / T_row;
-  float wr[U * E], dw[U * E], db[U * E];
+  f32x2 wr[U * S::P], dw[U * S::P], db[U * S::P];
   S::params(w, 1.f, t, T_row, R.V, wr);
 #pragma unroll
-  for (int i = 0; i < U * E; ++i) dw[i] = db[i] = 0.f;
+  for (int i = 0; i < U * S::P; ++i) dw[i] = db[i] = pair(0.f, 0.f);
   const float inv_c = 1.0f / (float)R.C;
   auto slot = [&](int st, int which, int u) { return ring + ((st * 2 + which) * U + u) * T_row + t; };
   auto fetch = [&](int64_t row, int st) {
@@ -493,15 +563,17 @@ norm_bwd_cta_kernel(const Rows R, const T* __restrict__ dy, const T* __restrict_
       xv[u] = u < have ? *slot(st, 0, u) : make_uint4(0, 0, 0, 0);
       gv[u] = u < have ? *slot(st, 1, u) : make_uint4(0, 0, 0, 0);
     }
+    f32x2 h[U * S::P], g[U * S::P];
     float s[K], sg;
-    S::grad_part(xv, gv, mu, rs, wr, dw, db, s[0], sg);
+    S::grad_part(xv, gv, mu, rs, wr, dw, db, h, g, s[0], sg);
     if (!RMS) s[K - 1] = sg;
     row_sum<0, K>(s, sm, buf);
     const float mgx = s[0] * inv_c, mg = RMS ? 0.f : s[K - 1] * inv_c;
     uint4* dst = reinterpret_cast<uint4*>(dx + R.at(row, dx_stride)) + t;
 #pragma unroll
     for (int u = 0; u < U; ++u)
-      if (u < have) __stcs(dst + u * T_row, S::grad_out(xv[u], gv[u], mu, rs, mg, mgx, wr + u * E));
+      if (u < have)
+        __stcs(dst + u * T_row, S::grad_out(h + u * S::P, g + u * S::P, rs, mg, mgx));
   }
   copy_wait<0>();
   if (part == nullptr) return;
@@ -510,33 +582,33 @@ norm_bwd_cta_kernel(const Rows R, const T* __restrict__ dy, const T* __restrict_
   for (int u = 0; u < U; ++u)
     if (u < have)
 #pragma unroll
-      for (int e = 0; e < E; ++e) {
-        const int c = (t + u * T_row) * E + e;
-        out[c] = dw[u * E + e];
-        if (with_db) out[R.C + c] = db[u * E + e];
+      for (int i = 0; i < S::P; ++i) {
+        const int c = (t + u * T_row) * E + 2 * i;
+        *reinterpret_cast<float2*>(out + c) = both(dw[u * S::P + i]);
+        if (with_db) *reinterpret_cast<float2*>(out + R.C + c) = both(db[u * S::P + i]);
       }
 }
 
 // dw[c] = sum over G CTAs of part[g][0][c], db likewise: 32 columns per CTA,
-// 8 slices of the CTAs each summed in order, then the slices in order.
-__global__ void __launch_bounds__(256)
+// 32 slices of the CTAs each summed in order, then the slices in order.
+__global__ void __launch_bounds__(1024)
 norm_reduce_kernel(const float* __restrict__ part, int G, int C, float* __restrict__ dw, float* __restrict__ db) {
-  __shared__ float sm[8][33];
+  __shared__ float sm[32][33];
   float* out = blockIdx.y == 0 ? dw : db;
   if (out == nullptr) return;
   const int c = blockIdx.x * 32 + (threadIdx.x & 31), sl = threadIdx.x >> 5;
   float s = 0.f;
   if (c < C) {
     const float* p = part + (int64_t)blockIdx.y * C + c;
-#pragma unroll 8
-    for (int g = sl; g < G; g += 8) s += p[(int64_t)g * 2 * C];
+#pragma unroll 4
+    for (int g = sl; g < G; g += 32) s += p[(int64_t)g * 2 * C];
   }
   sm[sl][threadIdx.x & 31] = s;
   __syncthreads();
   if (sl == 0 && c < C) {
     float t = 0.f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) t += sm[i][threadIdx.x];
+    for (int i = 0; i < 32; ++i) t += sm[i][threadIdx.x];
     out[c] = t;
   }
 }
@@ -596,7 +668,10 @@ struct Go {
   template <int L, int U, int RB>
   static bool bwd(const Rows& R, const void* dy, const void* x, int64_t xs, const float* w, const float* mean,
                   const float* rstd, void* dx, int64_t dxs, float* part, int with_db, int64_t grid, cudaStream_t st) {
-    norm_bwd_kernel<T, L, U, RB, RMS><<<(unsigned)grid, kWarpThreads, 0, st>>>(
+    const size_t smem = (size_t)kShortDepth * RB * 2 * U * kWarpThreads * 16;   // 64 KB with two vectors a thread
+    auto kern = norm_bwd_kernel<T, L, U, RB, RMS>;
+    if (!set_smem((const void*)kern, smem)) return false;
+    kern<<<(unsigned)grid, kWarpThreads, smem, st>>>(
         R, (const T*)dy, (const T*)x, xs, w, mean, rstd, (T*)dx, dxs, part, with_db);
     return true;
   }
@@ -672,7 +747,7 @@ sparsp_status_t launch_norm_bwd(const Dims& s, bool head, bool rms, const void* 
   const int with_db = db != nullptr;
   bool ok = false;
 #define NORM_WARP(L, U, RB)                                                                                          \
-  NORM_TYPED(template bwd<L NORM_COMMA U NORM_COMMA RB>(R, dy, x, x_stride, w, mean, rstd, dx, dx_stride, part,        \
+  NORM_TYPED(template bwd<L NORM_COMMA U NORM_COMMA 1>(R, dy, x, x_stride, w, mean, rstd, dx, dx_stride, part,        \
                                                         with_db, grid, st))
 #define NORM_CTA(U, MAXT, MINB)                                                                                      \
   NORM_TYPED(template bwd_cta<U NORM_COMMA MAXT NORM_COMMA MINB>(R, dy, x, x_stride, w, mean, rstd, dx, dx_stride, part, \
@@ -686,7 +761,7 @@ sparsp_status_t launch_norm_bwd(const Dims& s, bool head, bool rms, const void* 
   SPARSP_LAUNCH_CHECK();
   if (part != nullptr) {
     dim3 g((R.C + 31) / 32, with_db ? 2 : 1);
-    norm_reduce_kernel<<<g, 256, 0, st>>>(part, (int)grid, R.C, dw, db);
+    norm_reduce_kernel<<<g, 1024, 0, st>>>(part, (int)grid, R.C, dw, db);
     SPARSP_LAUNCH_CHECK();
   }
   return SPARSP_OK;

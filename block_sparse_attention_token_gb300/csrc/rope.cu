@@ -15,8 +15,10 @@
 // Bound by HBM: each row is read and written once. A CTA takes one tile and
 // several heads. All heads of a token turn alike, so a thread loads the (cos,
 // sin) of its tokens and columns once, keeps them in registers and sweeps the
-// heads with 16-byte accesses, all loads of a head issued before its stores.
+// heads; the 16-byte vectors of the next heads are on their way meanwhile, each
+// thread's into shared-memory slots of its own (cp.async).
 #include "common.cuh"
+#include "tc_helpers.cuh"
 
 namespace sparsp {
 namespace {
@@ -83,6 +85,15 @@ struct RopeCfg {
   static_assert(THREADS % UPR == 0 && U >= 1 && U * THREADS == BT * UPR, "tile split");
 };
 
+constexpr int kDepth = 3;   // heads in flight per CTA (three tiles: up to 96 KB with bf16, two CTAs per SM)
+
+__device__ __forceinline__ void copy_async16(void* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(tc::smem_u32(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;\n" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;\n" ::"n"(N) : "memory"); }
+
 template <typename T, int D, int BT, bool HALF, bool POOL>
 __global__ void __launch_bounds__(RopeCfg<T, D, BT, HALF>::THREADS)
 rope_kernel(const T* __restrict__ in, const Side si, T* __restrict__ out, const Side so, const RasterMap rm,
@@ -91,7 +102,10 @@ rope_kernel(const T* __restrict__ in, const Side si, T* __restrict__ out, const 
   using X = Row16<T>;
   constexpr int E = C::E;
   __shared__ int4 tok[BT];   // raster token, and its table row per axis
-  __shared__ float part[POOL ? C::THREADS : 1][POOL ? C::NV * E + 1 : 1];
+  // POOL: per warp the sums of its unit columns (lanes UPR apart share one)
+  constexpr int kPart = C::THREADS / 32 * C::UPR;
+  __shared__ float part[POOL ? 2 : 1][POOL ? kPart : 1][POOL ? C::NV * E + 1 : 1];
+  extern __shared__ uint4 ring[];   // [min(kDepth, heads)][U][NV][THREADS]
   const int j = blockIdx.x, b = blockIdx.z, H = rm.H;
   const int h0 = blockIdx.y * heads_per_cta, h1 = min(H, h0 + heads_per_cta);
   for (int o = threadIdx.x; o < BT; o += C::THREADS) {
@@ -133,17 +147,27 @@ rope_kernel(const T* __restrict__ in, const Side si, T* __restrict__ out, const 
       cs[u][k] = make_float2(v.x, v.y * a.sign);
     }
   }
-  for (int h = h0; h < h1; ++h) {
-    uint4 buf[C::U][C::NV];
-    const int64_t blocked0 = (((int64_t)b * H + h) * rm.N + (int64_t)j * BT) * D;
+  auto place = [&](int st, int u, int v) { return ring + ((st * C::U + u) * C::NV + v) * C::THREADS + threadIdx.x; };
+  auto fetch = [&](int h, int st) {
+    if (h < h1) {
+      const T* src0 = in + (si.blocked ? (((int64_t)b * H + h) * rm.N + (int64_t)j * BT) * D
+                                       : (int64_t)b * rm.N * si.stride + (int64_t)h * D) + c0 * E;
 #pragma unroll
-    for (int u = 0; u < C::U; ++u) {
-      const int o = o0 + u * kRowStep;
-      const T* src = in + (si.blocked ? blocked0 + (int64_t)o * D
-                                      : ((int64_t)b * rm.N + tok[o].x) * si.stride + (int64_t)h * D);
+      for (int u = 0; u < C::U; ++u) {
+        const int o = o0 + u * kRowStep;
+        const T* src = src0 + (si.blocked ? (int64_t)o * D : (int64_t)tok[o].x * si.stride);
 #pragma unroll
-      for (int v = 0; v < C::NV; ++v) buf[u][v] = __ldcs(reinterpret_cast<const uint4*>(src + c0 * E + v * (D / 2)));
+        for (int v = 0; v < C::NV; ++v) copy_async16(place(st, u, v), src + v * (D / 2));
+      }
     }
+    copy_commit();
+  };
+  for (int s = 0; s < kDepth - 1; ++s) fetch(h0 + s, s);
+  int st = 0;
+  for (int h = h0; h < h1; ++h, st = st + 1 == kDepth ? 0 : st + 1) {
+    fetch(h + kDepth - 1, st == 0 ? kDepth - 1 : st - 1);   // the slots of the head before
+    copy_wait<kDepth - 1>();
+    const int64_t blocked0 = (((int64_t)b * H + h) * rm.N + (int64_t)j * BT) * D;
     float acc[C::NV * E];
 #pragma unroll
     for (int e = 0; e < C::NV * E; ++e) acc[e] = 0.f;
@@ -151,7 +175,7 @@ rope_kernel(const T* __restrict__ in, const Side si, T* __restrict__ out, const 
     for (int u = 0; u < C::U; ++u) {
       float f[C::NV * E];
 #pragma unroll
-      for (int v = 0; v < C::NV; ++v) X::unpack(buf[u][v], f + v * E);
+      for (int v = 0; v < C::NV; ++v) X::unpack(*place(st, u, v), f + v * E);
 #pragma unroll
       for (int k = 0; k < C::NP; ++k) {
         float& x = f[HALF ? k : 2 * k];
@@ -169,20 +193,28 @@ rope_kernel(const T* __restrict__ in, const Side si, T* __restrict__ out, const 
 #pragma unroll
       for (int v = 0; v < C::NV; ++v) __stcs(reinterpret_cast<uint4*>(dst + c0 * E + v * (D / 2)), X::pack(f + v * E));
     }
-    if (POOL) {   // the means of the fp32 values, summed per thread, then over the threads of a column in order
-      __syncthreads();
+    // the means of the fp32 values: summed per thread, over the lanes that share its
+    // columns, then over the warps in order
+    if constexpr (POOL) {
+      float (*sum)[C::NV * E + 1] = part[(h - h0) & 1];   // the other one may still be read
 #pragma unroll
-      for (int e = 0; e < C::NV * E; ++e) part[threadIdx.x][e] = acc[e];
+      for (int off = 16; off >= C::UPR; off >>= 1)
+#pragma unroll
+        for (int e = 0; e < C::NV * E; ++e) acc[e] += __shfl_xor_sync(0xffffffffu, acc[e], off);
+      if ((threadIdx.x & 31) < C::UPR)
+#pragma unroll
+        for (int e = 0; e < C::NV * E; ++e) sum[(threadIdx.x >> 5) * C::UPR + c0][e] = acc[e];
       __syncthreads();
       for (int c = threadIdx.x; c < D; c += C::THREADS) {
         const int v = HALF ? c / (D / 2) : 0, cc = HALF ? c % (D / 2) : c;
         float s = 0.f;
-#pragma unroll 4
-        for (int g = 0; g < kRowStep; ++g) s += part[g * C::UPR + cc / E][v * E + cc % E];
+#pragma unroll
+        for (int g = 0; g < C::THREADS / 32; ++g) s += sum[g * C::UPR + cc / E][v * E + cc % E];
         means[(((int64_t)b * H + h) * (rm.N / BT) + j) * D + c] = s * (1.0f / (float)BT);
       }
     }
   }
+  copy_wait<0>();
 }
 
 __global__ void __launch_bounds__(256)
@@ -215,7 +247,7 @@ RopeArgs args_of(const sparsp_rope_t& r, const float* table) {
 }
 
 template <typename T, int D, int BT, bool HALF>
-void go(const Dims& s, const void* in, const Side& si, void* out, const Side& so, const RopeArgs& a, float* means,
+bool go(const Dims& s, const void* in, const Side& si, void* out, const Side& so, const RopeArgs& a, float* means,
         int32_t* d_status, cudaStream_t st) {
   using C = RopeCfg<T, D, BT, HALF>;
   // heads per CTA: as many as leave about four CTAs per SM
@@ -224,21 +256,21 @@ void go(const Dims& s, const void* in, const Side& si, void* out, const Side& so
   int64_t hpc = tiles * s.H / ((int64_t)(sms > 0 ? sms : 152) * 4);
   hpc = hpc < 1 ? 1 : hpc > 8 ? 8 : hpc;
   const dim3 grid((unsigned)s.nb, (unsigned)((s.H + hpc - 1) / hpc), (unsigned)s.B);
-  if (means != nullptr)
-    rope_kernel<T, D, BT, HALF, true><<<grid, C::THREADS, 0, st>>>((const T*)in, si, (T*)out, so, raster_map(s), a,
-                                                                   (int)hpc, means, d_status);
-  else
-    rope_kernel<T, D, BT, HALF, false><<<grid, C::THREADS, 0, st>>>((const T*)in, si, (T*)out, so, raster_map(s), a,
-                                                                    (int)hpc, nullptr, d_status);
+  const size_t smem = (size_t)(hpc < kDepth ? hpc : kDepth) * C::VECS * 16;
+  auto kern = means != nullptr ? rope_kernel<T, D, BT, HALF, true> : rope_kernel<T, D, BT, HALF, false>;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+    return false;
+  kern<<<grid, C::THREADS, smem, st>>>((const T*)in, si, (T*)out, so, raster_map(s), a, (int)hpc, means, d_status);
+  return true;
 }
 
 template <typename T, bool HALF>
-void go_shape(const Dims& s, const void* in, const Side& si, void* out, const Side& so, const RopeArgs& a,
+bool go_shape(const Dims& s, const void* in, const Side& si, void* out, const Side& so, const RopeArgs& a,
               float* means, int32_t* d_status, cudaStream_t st) {
-  if (s.d == 64 && s.Bt == 64) go<T, 64, 64, HALF>(s, in, si, out, so, a, means, d_status, st);
-  else if (s.d == 64) go<T, 64, 128, HALF>(s, in, si, out, so, a, means, d_status, st);
-  else if (s.Bt == 64) go<T, 128, 64, HALF>(s, in, si, out, so, a, means, d_status, st);
-  else go<T, 128, 128, HALF>(s, in, si, out, so, a, means, d_status, st);
+  if (s.d == 64 && s.Bt == 64) return go<T, 64, 64, HALF>(s, in, si, out, so, a, means, d_status, st);
+  if (s.d == 64) return go<T, 64, 128, HALF>(s, in, si, out, so, a, means, d_status, st);
+  if (s.Bt == 64) return go<T, 128, 64, HALF>(s, in, si, out, so, a, means, d_status, st);
+  return go<T, 128, 128, HALF>(s, in, si, out, so, a, means, d_status, st);
 }
 
 }  // namespace
@@ -268,13 +300,15 @@ sparsp_status_t launch_rope(const Dims& s, const sparsp_rope_t& r, const float* 
   a.pos = pos;
   a.sign = inverse ? -1.f : 1.f;
   const Side si{in_stride, in_blocked}, so{out_stride, out_blocked};
+  bool ok;
   if (s.dtype == SPARSP_F32) {
-    if (r.half) go_shape<float, true>(s, in, si, out, so, a, means, d_status, st);
-    else go_shape<float, false>(s, in, si, out, so, a, means, d_status, st);
+    if (r.half) ok = go_shape<float, true>(s, in, si, out, so, a, means, d_status, st);
+    else ok = go_shape<float, false>(s, in, si, out, so, a, means, d_status, st);
   } else {
-    if (r.half) go_shape<__nv_bfloat16, true>(s, in, si, out, so, a, means, d_status, st);
-    else go_shape<__nv_bfloat16, false>(s, in, si, out, so, a, means, d_status, st);
+    if (r.half) ok = go_shape<__nv_bfloat16, true>(s, in, si, out, so, a, means, d_status, st);
+    else ok = go_shape<__nv_bfloat16, false>(s, in, si, out, so, a, means, d_status, st);
   }
+  if (!ok) return SPARSP_ERR_CUDA;
   SPARSP_LAUNCH_CHECK();
   return SPARSP_OK;
 }
