@@ -124,7 +124,7 @@ __device__ __forceinline__ void copy_wait(int n) {
 // Sum of K values over the threads that share a row: L lanes of a warp, or the
 // whole CTA (L = 0) through shared memory, in a fixed order. `buf` alternates
 // between calls so that one barrier per call is enough.
-template <int L, int K>
+template <int L, int K, int MAXT = 1024>
 __device__ __forceinline__ void row_sum(float (&v)[K], float* sm, int& buf) {
 #pragma unroll
   for (int off = (L == 0 ? 32 : L) / 2; off > 0; off >>= 1)
@@ -133,25 +133,27 @@ __device__ __forceinline__ void row_sum(float (&v)[K], float* sm, int& buf) {
   if (L == 0) {
     float* s = sm + buf * (kMaxWarps * K);
     buf ^= 1;
-    const int warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
+    const int warp = threadIdx.x >> 5;
     if ((threadIdx.x & 31) == 0)
 #pragma unroll
       for (int k = 0; k < K; ++k) s[warp * K + k] = v[k];
     __syncthreads();
-    const int lane = threadIdx.x & 31;
+    // four values per load: 4 / K warps' sums (zeros past the last warp), all loads at once
+    static_assert(K == 1 || K == 2 || K == 4, "row sums per step");
+    float4 q = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-    for (int k = 0; k < K; ++k) v[k] = lane < nw ? s[lane * K + k] : 0.f;
-    if (nw > 16)
+    for (int w = 0; w < MAXT / 32; w += 4 / K) {
+      const float4 p = reinterpret_cast<const float4*>(s)[w * K / 4];
+      q.x += p.x;
+      q.y += p.y;
+      q.z += p.z;
+      q.w += p.w;
+    }
+    const float f[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
-      for (int k = 0; k < K; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], 16);
-    // (with at most 16 warps the upper half of the lanes holds zeros and takes the lower half's sum below)
+    for (int k = 0; k < K; ++k) v[k] = f[k];
 #pragma unroll
-    for (int off = 8; off > 0; off >>= 1)
-#pragma unroll
-      for (int k = 0; k < K; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], off);
-    if (nw <= 16)
-#pragma unroll
-      for (int k = 0; k < K; ++k) v[k] = __shfl_sync(0xffffffffu, v[k], lane & 15);
+    for (int i = K; i < 4; ++i) v[i % K] += f[i];
   }
 }
 
@@ -311,10 +313,9 @@ inline int ring_depth(size_t step, int ctas) {
   while (d > 1 && step * d * ctas > kRingBytes) --d;
   return d;
 }
-template <typename T, int U>
-constexpr int cta_threads() { return U == 2 ? 512 : 16384 / (4 * Vec<T>::E); }   // of rows of up to 16,384 values
-template <typename T, int U, int RB, bool RMS>
-__global__ void __launch_bounds__(cta_threads<T, U>())
+// MAXT, MINB: threads and resident CTAs the registers are shared out for.
+template <typename T, int U, int RB, bool RMS, int MAXT, int MINB>
+__global__ void __launch_bounds__(MAXT, MINB)
 norm_fwd_cta_kernel(const Rows R, const T* __restrict__ x, int64_t x_stride,
                                     const float* __restrict__ w, const float* __restrict__ b, float eps,
                                     T* __restrict__ y, float* __restrict__ mean, float* __restrict__ rstd, int depth) {
@@ -328,6 +329,8 @@ norm_fwd_cta_kernel(const Rows R, const T* __restrict__ x, int64_t x_stride,
   f32x2 wr[U * S::P], br[U * S::P];
   S::params(w, 1.f, t, T_row, R.V, wr);
   S::params(b, 0.f, t, T_row, R.V, br);
+  for (int i = t; i < 2 * kMaxWarps * RB; i += T_row) sm[i] = 0.f;
+  __syncthreads();
   const float inv_c = 1.0f / (float)R.C;
   const int64_t step = (int64_t)gridDim.x * RB;
   auto slot = [&](int st, int r, int u) { return ring + ((st * RB + r) * U + u) * T_row + t; };
@@ -360,13 +363,13 @@ norm_fwd_cta_kernel(const Rows R, const T* __restrict__ x, int64_t x_stride,
     if (!RMS) {
 #pragma unroll
       for (int r = 0; r < RB; ++r) S::mean_part(xv[r], mu[r]);
-      row_sum<0, RB>(mu, sm, buf);
+      row_sum<0, RB, MAXT>(mu, sm, buf);
 #pragma unroll
       for (int r = 0; r < RB; ++r) mu[r] *= inv_c;
     }
 #pragma unroll
     for (int r = 0; r < RB; ++r) S::var_part(xv[r], mu[r], have, q[r]);
-    row_sum<0, RB>(q, sm, buf);
+    row_sum<0, RB, MAXT>(q, sm, buf);
 #pragma unroll
     for (int r = 0; r < RB; ++r) {
       const int64_t row = base + r;
@@ -507,8 +510,7 @@ norm_bwd_kernel(const Rows R, const T* __restrict__ dy, const T* __restrict__ x,
     }
 }
 
-// Longer rows: a CTA per row with the forward's ring, of x and dy. MAXT, MINB:
-// threads and resident CTAs the registers are shared out for.
+// Longer rows: a CTA per row with the forward's ring, of x and dy.
 template <typename T, int U, bool RMS, int MAXT, int MINB>
 __global__ void __launch_bounds__(MAXT, MINB)
 norm_bwd_cta_kernel(const Rows R, const T* __restrict__ dy, const T* __restrict__ x, int64_t x_stride,
@@ -526,6 +528,8 @@ norm_bwd_cta_kernel(const Rows R, const T* __restrict__ dy, const T* __restrict_
   S::params(w, 1.f, t, T_row, R.V, wr);
 #pragma unroll
   for (int i = 0; i < U * S::P; ++i) dw[i] = db[i] = pair(0.f, 0.f);
+  for (int i = t; i < 2 * kMaxWarps * K; i += T_row) sm[i] = 0.f;
+  __syncthreads();
   const float inv_c = 1.0f / (float)R.C;
   auto slot = [&](int st, int which, int u) { return ring + ((st * 2 + which) * U + u) * T_row + t; };
   auto fetch = [&](int64_t row, int st) {
@@ -567,7 +571,7 @@ norm_bwd_cta_kernel(const Rows R, const T* __restrict__ dy, const T* __restrict_
     float s[K], sg;
     S::grad_part(xv, gv, mu, rs, wr, dw, db, h, g, s[0], sg);
     if (!RMS) s[K - 1] = sg;
-    row_sum<0, K>(s, sm, buf);
+    row_sum<0, K, MAXT>(s, sm, buf);
     const float mgx = s[0] * inv_c, mg = RMS ? 0.f : s[K - 1] * inv_c;
     uint4* dst = reinterpret_cast<uint4*>(dx + R.at(row, dx_stride)) + t;
 #pragma unroll
@@ -639,6 +643,8 @@ bool set_smem(const void* kern, size_t bytes) {
 
 template <typename T, bool RMS>
 struct Go {
+  template <int U>
+  static constexpr int longest() { return 16384 / (U * Vec<T>::E); }   // threads of a row of 16,384 values
   template <int L, int U, int RB>
   static bool fwd(const Rows& R, const void* x, int64_t xs, const float* w, const float* b, float eps, void* y,
                   float* mean, float* rstd, int sms, cudaStream_t st) {
@@ -649,14 +655,15 @@ struct Go {
                                                                                mean, rstd);
     return true;
   }
-  template <int U, int RB>
+  template <int U, int MAXT, int MINB>
   static bool fwd_cta(const Rows& R, const void* x, int64_t xs, const float* w, const float* b, float eps, void* y,
                       float* mean, float* rstd, int sms, cudaStream_t st) {
     const int threads = 32 * ((R.V + 32 * U - 1) / (32 * U));
+    constexpr int RB = U == 4 ? 1 : 2, kThreads = U == 4 ? longest<U>() : MAXT;
     const size_t step = (size_t)RB * U * threads * 16;
-    const int depth = ring_depth(step, U == 2 ? 2 : 1);   // two CTAs per SM where a thread has two vectors
+    const int depth = ring_depth(step, MINB);
     const size_t smem = step * depth;
-    auto kern = norm_fwd_cta_kernel<T, U, RB, RMS>;
+    auto kern = norm_fwd_cta_kernel<T, U, RB, RMS, kThreads, MINB>;
     if (!set_smem((const void*)kern, smem)) return false;
     int per = 0;
     if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kern, threads, smem) != cudaSuccess || per < 1) return false;
@@ -682,7 +689,7 @@ struct Go {
     const int threads = 32 * ((R.V + 32 * U - 1) / (32 * U));
     const size_t step = (size_t)2 * U * threads * 16;
     const int depth = ring_depth(step, MINB);
-    constexpr int kThreads = U == 4 ? cta_threads<T, U>() : MAXT;
+    constexpr int kThreads = U == 4 ? longest<U>() : MAXT;
     auto kern = norm_bwd_cta_kernel<T, U, RMS, kThreads, MINB>;
     if (!set_smem((const void*)kern, step * depth)) return false;
     kern<<<(unsigned)grid, threads, step * depth, st>>>(R, (const T*)dy, (const T*)x, xs, w, mean, rstd, (T*)dx, dxs,
@@ -725,7 +732,7 @@ sparsp_status_t launch_norm_fwd(const Dims& s, bool head, bool rms, const void* 
     else ok = rms ? Go<__nv_bfloat16, true>::CALL : Go<__nv_bfloat16, false>::CALL;      \
   } while (0)
 #define NORM_WARP(L, U, RB) NORM_TYPED(template fwd<L NORM_COMMA U NORM_COMMA RB>(R, x, x_stride, w, b, eps, y, mean, rstd, sms, st))
-#define NORM_CTA(U, MAXT, MINB) NORM_TYPED(template fwd_cta<U NORM_COMMA (U == 4 ? 1 : 2)>(R, x, x_stride, w, b, eps, y, mean, rstd, sms, st))
+#define NORM_CTA(U, MAXT, MINB) NORM_TYPED(template fwd_cta<U NORM_COMMA MAXT NORM_COMMA MINB>(R, x, x_stride, w, b, eps, y, mean, rstd, sms, st))
 #define NORM_COMMA ,
   NORM_ROWS(NORM_WARP, NORM_CTA);
 #undef NORM_WARP
