@@ -163,42 +163,38 @@ template <typename T, int U, bool RMS>
 struct Share {
   using X = Vec<T>;
   static constexpr int E = X::E, P = E / 2;   // values and pairs of a vector
-  static __device__ __forceinline__ void mean_part(const uint4 (&x)[U], float& s) {
+  static __device__ __forceinline__ void values(const uint4 (&x)[U], f32x2 (&f)[U * P]) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) X::unpack(x[u], f + u * P);
+  }
+  static __device__ __forceinline__ float mean_part(const f32x2 (&f)[U * P]) {
     f32x2 a = pair(0.f, 0.f);
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      f32x2 f[P];
-      X::unpack(x[u], f);
-#pragma unroll
-      for (int i = 0; i < P; ++i) a = add2(a, f[i]);
-    }
-    s = hsum(a);
+    for (int i = 0; i < U * P; ++i) a = add2(a, f[i]);
+    return hsum(a);
   }
-  // sum of (x - mu)^2 over the vectors that exist (a missing one holds zeros, not the mean)
-  static __device__ __forceinline__ void var_part(const uint4 (&x)[U], float mu, int have, float& s) {
+  // x - mu in place, and the sum of its square over the vectors that exist (a
+  // missing one held zeros, not the mean)
+  static __device__ __forceinline__ float var_part(f32x2 (&f)[U * P], float mu, int have) {
     f32x2 a = pair(0.f, 0.f);
     const f32x2 m = pair(-mu, -mu);
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      f32x2 f[P];
-      X::unpack(x[u], f);
+    for (int u = 0; u < U; ++u)
       if (RMS || u < have)
 #pragma unroll
-        for (int i = 0; i < P; ++i) {
-          const f32x2 c = RMS ? f[i] : add2(f[i], m);
-          a = fma2(c, c, a);
+        for (int i = u * P; i < (u + 1) * P; ++i) {
+          if (!RMS) f[i] = add2(f[i], m);
+          a = fma2(f[i], f[i], a);
         }
-    }
-    s = hsum(a);
+    return hsum(a);
   }
-  // (x - mu) rs w + b
-  static __device__ __forceinline__ uint4 out(const uint4& x, float mu, float rs, const f32x2* w, const f32x2* b) {
-    const f32x2 m = pair(-mu, -mu), r = pair(rs, rs);
-    f32x2 f[P];
-    X::unpack(x, f);
+  // (x - mu) rs w + b of one vector of x - mu
+  static __device__ __forceinline__ uint4 out(const f32x2* f, float rs, const f32x2* w, const f32x2* b) {
+    const f32x2 r = pair(rs, rs);
+    f32x2 y[P];
 #pragma unroll
-    for (int i = 0; i < P; ++i) f[i] = fma2(mul2(RMS ? f[i] : add2(f[i], m), r), w[i], b[i]);
-    return X::pack(f);
+    for (int i = 0; i < P; ++i) y[i] = fma2(mul2(f[i], r), w[i], b[i]);
+    return X::pack(y);
   }
   // column sums of dw and db, row sums of g xh and g (g = dy w, xh = x rs - mu rs),
   // and xh and g themselves for grad_out
@@ -273,18 +269,22 @@ norm_fwd_kernel(const Rows R, const T* __restrict__ x, int64_t x_stride, const f
 #pragma unroll
       for (int u = 0; u < U; ++u) xv[r][u] = row < R.rows && u < have ? __ldcs(src + u * L) : make_uint4(0, 0, 0, 0);
     }
+    f32x2 f[RB][U * S::P];
     float mu[RB], q[RB];
 #pragma unroll
-    for (int r = 0; r < RB; ++r) mu[r] = 0.f;
+    for (int r = 0; r < RB; ++r) {
+      S::values(xv[r], f[r]);
+      mu[r] = 0.f;
+    }
     if (!RMS) {
 #pragma unroll
-      for (int r = 0; r < RB; ++r) S::mean_part(xv[r], mu[r]);
+      for (int r = 0; r < RB; ++r) mu[r] = S::mean_part(f[r]);
       row_sum<L, RB>(mu, nullptr, buf);
 #pragma unroll
       for (int r = 0; r < RB; ++r) mu[r] *= inv_c;
     }
 #pragma unroll
-    for (int r = 0; r < RB; ++r) S::var_part(xv[r], mu[r], have, q[r]);
+    for (int r = 0; r < RB; ++r) q[r] = S::var_part(f[r], mu[r], have);
     row_sum<L, RB>(q, nullptr, buf);
 #pragma unroll
     for (int r = 0; r < RB; ++r) {
@@ -294,7 +294,7 @@ norm_fwd_kernel(const Rows R, const T* __restrict__ x, int64_t x_stride, const f
       uint4* dst = reinterpret_cast<uint4*>(y + row * R.C) + t;
 #pragma unroll
       for (int u = 0; u < U; ++u)
-        if (u < have) __stcs(dst + u * L, S::out(xv[r][u], mu[r], rs, wr + u * S::P, br + u * S::P));
+        if (u < have) __stcs(dst + u * L, S::out(f[r] + u * S::P, rs, wr + u * S::P, br + u * S::P));
       if (t == 0) {
         if (!RMS && mean != nullptr) mean[row] = mu[r];
         if (rstd != nullptr) rstd[row] = rs;
@@ -357,18 +357,22 @@ norm_fwd_cta_kernel(const Rows R, const T* __restrict__ x, int64_t x_stride,
 #pragma unroll
       for (int u = 0; u < U; ++u)
         xv[r][u] = base + r < R.rows && u < have ? *slot(st, r, u) : make_uint4(0, 0, 0, 0);
+    f32x2 f[RB][U * S::P];
     float mu[RB], q[RB];
 #pragma unroll
-    for (int r = 0; r < RB; ++r) mu[r] = 0.f;
+    for (int r = 0; r < RB; ++r) {
+      S::values(xv[r], f[r]);
+      mu[r] = 0.f;
+    }
     if (!RMS) {
 #pragma unroll
-      for (int r = 0; r < RB; ++r) S::mean_part(xv[r], mu[r]);
+      for (int r = 0; r < RB; ++r) mu[r] = S::mean_part(f[r]);
       row_sum<0, RB, MAXT>(mu, sm, buf);
 #pragma unroll
       for (int r = 0; r < RB; ++r) mu[r] *= inv_c;
     }
 #pragma unroll
-    for (int r = 0; r < RB; ++r) S::var_part(xv[r], mu[r], have, q[r]);
+    for (int r = 0; r < RB; ++r) q[r] = S::var_part(f[r], mu[r], have);
     row_sum<0, RB, MAXT>(q, sm, buf);
 #pragma unroll
     for (int r = 0; r < RB; ++r) {
@@ -378,7 +382,7 @@ norm_fwd_cta_kernel(const Rows R, const T* __restrict__ x, int64_t x_stride,
       uint4* dst = reinterpret_cast<uint4*>(y + row * R.C) + t;
 #pragma unroll
       for (int u = 0; u < U; ++u)
-        if (u < have) __stcs(dst + u * T_row, S::out(xv[r][u], mu[r], rs, wr + u * S::P, br + u * S::P));
+        if (u < have) __stcs(dst + u * T_row, S::out(f[r] + u * S::P, rs, wr + u * S::P, br + u * S::P));
       if (t == 0) {
         if (!RMS && mean != nullptr) mean[row] = mu[r];
         if (rstd != nullptr) rstd[row] = rs;
