@@ -169,8 +169,8 @@ def _ptr(t):
 
 
 def _stream(stream=None):
-    if stream is None:
-        stream = torch.cuda.current_stream()
+    if stream is None:   # the current stream's handle, without a Stream object
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     return stream.cuda_stream
 
 
@@ -187,37 +187,35 @@ def _empty(n_bytes: int, device) -> torch.Tensor:
     return torch.empty(max(int(n_bytes), 16), dtype=torch.uint8, device=device)
 
 
-def _want(name: str, t, dims, dtype, optional: bool = False):
-    """A tensor argument of the calls below: contiguous, on the current device,
-    of this shape and dtype (a plain address is passed through)."""
+def _refuse(name: str, t, what: str):
+    got = None if t is None else (tuple(t.shape), t.dtype, str(t.device), t.stride())
+    raise ValueError(f"{name}: expected {what} on the current CUDA device, got {got}")
+
+
+def _want(name: str, t, dims, dtype, dev: int, optional: bool = False):
+    """Address of a tensor argument of the calls below: contiguous, on device dev
+    (the current one), of this shape and dtype. A plain address is passed through."""
     if t is None and optional or isinstance(t, int):
         return t
-    if (t is None or tuple(t.shape) != tuple(dims) or t.dtype != dtype or not t.is_contiguous()
-            or t.device.index != torch.cuda.current_device()):
-        got = None if t is None else (tuple(t.shape), t.dtype, str(t.device), t.stride())
-        raise ValueError(f"{name}: expected a contiguous {tuple(dims)} {dtype} tensor on the current CUDA device, "
-                         f"got {got}")
-    return t
+    if t is None or t.shape != dims or t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous():
+        _refuse(name, t, f"a contiguous {tuple(dims)} {dtype} tensor")
+    return t.data_ptr()
 
 
-def _token_stride(shape: Shape, name: str, t) -> int:
-    """Elements between the tokens of a raster tensor [B, N, H, d] that may be a
-    slice of a wider one (heads and columns contiguous, batches of N tokens)."""
-    s, dims = shape, (shape.B, shape.N, shape.H, shape.d)
+def _token_stride(shape: Shape, name: str, t, dims, dtype, dev: int) -> tuple:
+    """(address, elements between tokens) of a raster tensor [B, N, H, d] that may be
+    a slice of a wider one (heads and columns contiguous, batches of N tokens)."""
     if isinstance(t, int):
-        return 0
-    ts = s.H * s.d
-    ok = (t is not None and tuple(t.shape) == dims and t.dtype == s.torch_dtype
-          and t.device.index == torch.cuda.current_device())
-    if ok:
+        return t, 0
+    if t is not None and t.shape == dims and t.dtype is dtype and t.get_device() == dev:
+        if t.is_contiguous():
+            return t.data_ptr(), 0
+        B, N, H, d = dims
         st = t.stride()
-        ts = st[1] if s.N > 1 else st[0] if s.B > 1 else ts
-        ok = st[3] == 1 and (s.H == 1 or st[2] == s.d) and (s.B == 1 or st[0] == s.N * ts) and ts >= s.H * s.d
-    if not ok:
-        got = None if t is None else (tuple(t.shape), t.dtype, str(t.device), t.stride())
-        raise ValueError(f"{name}: expected a raster {dims} {s.torch_dtype} tensor on the current CUDA device with "
-                         f"contiguous heads and one stride between tokens, got {got}")
-    return ts
+        ts = st[1] if N > 1 else st[0] if B > 1 else H * d
+        if st[3] == 1 and (H == 1 or st[2] == d) and (B == 1 or st[0] == N * ts) and ts >= H * d:
+            return t.data_ptr(), ts
+    _refuse(name, t, f"a raster {tuple(dims)} {dtype} tensor with contiguous heads and one stride between tokens")
 
 
 # ----------------------------------------------------------------- before step 1: token norm, rotary positions
@@ -237,23 +235,22 @@ def norm_fwd(shape: Shape, x, w=None, b=None, eps: float = 1e-6, rms: bool = Fal
     projection (one stride between tokens). w, b: float32 [H*d] or [d], or None.
     Returns (y, mean, rstd), the statistics float32 [B,N] ([B,N,H] with per_head);
     mean is None with rms."""
-    s = shape
-    xs = _token_stride(s, "x", x)
-    cols, stat = ((s.d,), (s.B, s.N, s.H)) if per_head else ((s.H * s.d,), (s.B, s.N))
+    dims = (shape.B, shape.N, shape.H, shape.d)
+    dt, f32, dev = shape.torch_dtype, torch.float32, torch.cuda.current_device()
+    px, xs = _token_stride(shape, "x", x, dims, dt, dev)
+    cols, stat = ((dims[3],), dims[:3]) if per_head else ((dims[2] * dims[3],), dims[:2])
     if out is None:
-        out = torch.empty((s.B, s.N, s.H, s.d), dtype=s.torch_dtype, device=x.device)
+        out = torch.empty(dims, dtype=dt, device=x.device)
     if rms:
         mean = None
     elif mean is None:
-        mean = torch.empty(stat, dtype=torch.float32, device=x.device)
+        mean = torch.empty(stat, dtype=f32, device=x.device)
     if rstd is None:
-        rstd = torch.empty(stat, dtype=torch.float32, device=x.device)
-    f32 = torch.float32
+        rstd = torch.empty(stat, dtype=f32, device=x.device)
     _check("sparsp_norm_fwd", lib().sparsp_norm_fwd(
-        _sref(s), _norm_flags(rms, per_head), _ptr(x), xs, _ptr(_want("w", w, cols, f32, True)),
-        _ptr(_want("b", b, cols, f32, True)), float(eps),
-        _ptr(_want("out", out, (s.B, s.N, s.H, s.d), s.torch_dtype)), _ptr(_want("mean", mean, stat, f32, True)),
-        _ptr(_want("rstd", rstd, stat, f32)), _stream(stream)))
+        _sref(shape), _norm_flags(rms, per_head), px, xs, _want("w", w, cols, f32, dev, True),
+        _want("b", b, cols, f32, dev, True), eps, _want("out", out, dims, dt, dev),
+        _want("mean", mean, stat, f32, dev, True), _want("rstd", rstd, stat, f32, dev), _stream(stream)))
     return out, mean, rstd
 
 
@@ -261,24 +258,24 @@ def norm_bwd(shape: Shape, dy, x, w, mean, rstd, rms: bool = False, per_head: bo
              ws=None, stream=None):
     """Gradients of norm_fwd from its x, mean (None with rms) and rstd: (dx, dw, db),
     db None with rms unless a buffer is given. dx may be a slice like x."""
-    s = shape
-    xs = _token_stride(s, "x", x)
-    cols, stat = ((s.d,), (s.B, s.N, s.H)) if per_head else ((s.H * s.d,), (s.B, s.N))
-    dims, f32 = (s.B, s.N, s.H, s.d), torch.float32
+    dims = (shape.B, shape.N, shape.H, shape.d)
+    dt, f32, dev = shape.torch_dtype, torch.float32, torch.cuda.current_device()
+    px, xs = _token_stride(shape, "x", x, dims, dt, dev)
+    cols, stat = ((dims[3],), dims[:3]) if per_head else ((dims[2] * dims[3],), dims[:2])
     if dx is None:
-        dx = torch.empty(dims, dtype=s.torch_dtype, device=x.device)
+        dx = torch.empty(dims, dtype=dt, device=x.device)
     if dw is None:
         dw = torch.empty(cols, dtype=f32, device=x.device)
     if db is None and not rms:
         db = torch.empty(cols, dtype=f32, device=x.device)
     if ws is None:
-        ws = _empty(norm_workspace_size(s, rms, per_head), x.device)
-    dxs = _token_stride(s, "dx", dx)
+        ws = _empty(norm_workspace_size(shape, rms, per_head), x.device)
+    pdx, dxs = _token_stride(shape, "dx", dx, dims, dt, dev)
     _check("sparsp_norm_bwd", lib().sparsp_norm_bwd(
-        _sref(s), _norm_flags(rms, per_head), _ptr(_want("dy", dy, dims, s.torch_dtype)), _ptr(x), xs,
-        _ptr(_want("w", w, cols, f32, True)), _ptr(None if rms else _want("mean", mean, stat, f32)),
-        _ptr(_want("rstd", rstd, stat, f32)), _ptr(dx), dxs, _ptr(_want("dw", dw, cols, f32, True)),
-        _ptr(_want("db", db, cols, f32, True)), _ptr(ws), ws.numel(), _stream(stream)))
+        _sref(shape), _norm_flags(rms, per_head), _want("dy", dy, dims, dt, dev), px, xs,
+        _want("w", w, cols, f32, dev, True), None if rms else _want("mean", mean, stat, f32, dev),
+        _want("rstd", rstd, stat, f32, dev), pdx, dxs, _want("dw", dw, cols, f32, dev),
+        _want("db", db, cols, f32, dev, True), _ptr(ws), ws.numel(), _stream(stream)))
     return dx, dw, db
 
 
@@ -322,21 +319,18 @@ def rope(shape: Shape, table: RopeTable, x, out=None, inverse: bool = False, in_
     be slices of wider ones (one stride between tokens)."""
     s = shape
     raster, blocked = (s.B, s.N, s.H, s.d), (s.B, s.H, s.N, s.d)
-    dt, i32 = s.torch_dtype, torch.int32
+    dt, dev = s.torch_dtype, torch.cuda.current_device()
     if out is None:
         out = torch.empty(blocked if out_blocked else raster, dtype=dt, device=x.device)
-    xs = 0 if in_blocked else _token_stride(s, "x", x)
-    os_ = 0 if out_blocked else _token_stride(s, "out", out)
-    if in_blocked:
-        _want("x", x, blocked, dt)
-    if out_blocked:
-        _want("out", out, blocked, dt)
+    px, xs = ((_want("x", x, blocked, dt, dev), 0) if in_blocked else _token_stride(s, "x", x, raster, dt, dev))
+    po, os_ = ((_want("out", out, blocked, dt, dev), 0) if out_blocked
+               else _token_stride(s, "out", out, raster, dt, dev))
     flags = ((ROPE_INVERSE if inverse else 0) | (ROPE_IN_BLOCKED if in_blocked else 0)
              | (ROPE_OUT_BLOCKED if out_blocked else 0))
     _check("sparsp_rope", lib().sparsp_rope(
-        _sref(s), ctypes.byref(table.axes), _ptr(table.table), _ptr(_want("pos", pos, (s.B, s.N, 3), i32, True)),
-        _ptr(x), xs, _ptr(out), os_, flags,
-        _ptr(_want("means", means, (s.B, s.H, s.nb, s.d), torch.float32, True)), _ptr(status), _stream(stream)))
+        _sref(s), ctypes.byref(table.axes), table.table.data_ptr(),
+        _want("pos", pos, (s.B, s.N, 3), torch.int32, dev, True), px, xs, po, os_, flags,
+        _want("means", means, (s.B, s.H, s.nb, s.d), torch.float32, dev, True), _ptr(status), _stream(stream)))
     return out
 
 
@@ -643,15 +637,15 @@ def mask_plan(shape: Shape, pos, lo, hi, plan: MaskPlan | None = None, stream=No
     (int32 [B,N], raster order): documents with pos = lo = number and hi = lo + 1,
     padding with pos = -1 and lo = hi = 0, frames with pos = frame and
     hi = max(frame + 1, prefix). It serves every layer and step with that mask."""
-    s, i32 = shape, torch.int32
-    for name, t in (("pos", pos), ("lo", lo), ("hi", hi)):
-        _want(name, t, (s.B, s.N), i32)
+    s, dev = shape, torch.cuda.current_device()
+    pos_, lo_, hi_ = (_want(name, t, (s.B, s.N), torch.int32, dev) for name, t in
+                      (("pos", pos), ("lo", lo), ("hi", hi)))
     if plan is None:
         plan = MaskPlan(_mask_dims(s), _empty(lib().sparsp_mask_plan_size(_sref(s)), pos.device))
     elif plan.dims != _mask_dims(s):
         raise ValueError(f"mask_plan: the plan is of shape {plan.dims}, not {_mask_dims(s)}")
-    _check("sparsp_mask_plan", lib().sparsp_mask_plan(_sref(s), _ptr(pos), _ptr(lo), _ptr(hi), _ptr(plan.plan),
-                                                      plan.plan.numel(), _stream(stream)))
+    _check("sparsp_mask_plan", lib().sparsp_mask_plan(_sref(s), pos_, lo_, hi_, _ptr(plan.plan), plan.plan.numel(),
+                                                      _stream(stream)))
     return plan
 
 
@@ -665,9 +659,8 @@ def _plan_ptr(shape: Shape, mask: MaskPlan | None):
 
 def mask_scores(shape: Shape, mask: MaskPlan, scores, stream=None) -> torch.Tensor:
     """scores [B,H,nb,nb] in place: MASKED_SCORE for block pairs that see nothing of each other."""
-    _want("scores", scores, (shape.B, shape.H, shape.nb, shape.nb), torch.float32)
-    _check("sparsp_mask_scores", lib().sparsp_mask_scores(_sref(shape), _plan_ptr(shape, mask), _ptr(scores),
-                                                          _stream(stream)))
+    at = _want("scores", scores, (shape.B, shape.H, shape.nb, shape.nb), torch.float32, torch.cuda.current_device())
+    _check("sparsp_mask_scores", lib().sparsp_mask_scores(_sref(shape), _plan_ptr(shape, mask), at, _stream(stream)))
     return scores
 
 
@@ -681,18 +674,20 @@ def attn_masked_fwd(shape: Shape, q, k, v, row_ptr, col_idx, scale: float = 0.0,
     """attn_fwd over the keys a token mask lets each query see, with the scores
     capped to cap * tanh(score / cap) when cap > 0. Returns (O, LSE); a query
     that sees nothing has O = 0, LSE = -inf."""
-    dev = q.device
+    B, N, H, d = shape.B, shape.N, shape.H, shape.d
+    raster, blocked, dt, dev = (B, N, H, d), (B, H, N, d), shape.torch_dtype, torch.cuda.current_device()
+    ind, outd = raster if flags & IN_RASTER else blocked, raster if flags & OUT_RASTER else blocked
     if o is None:
-        o = torch.empty((shape.B, shape.N, shape.H, shape.d) if flags & OUT_RASTER else
-                        (shape.B, shape.H, shape.N, shape.d), dtype=q.dtype, device=dev)
+        o = torch.empty(outd, dtype=dt, device=q.device)
     if lse is None:
-        lse = torch.empty((shape.B, shape.H, shape.N), dtype=torch.float32, device=dev)
+        lse = torch.empty((B, H, N), dtype=torch.float32, device=q.device)
     if ws is None:
-        ws = _empty(attn_masked_workspace_size(shape, False), dev)
+        ws = _empty(attn_masked_workspace_size(shape, False), q.device)
     _check("sparsp_attn_masked_fwd", lib().sparsp_attn_masked_fwd(
-        _sref(shape), _ptr(q), _ptr(k), _ptr(v), _ptr(row_ptr), _ptr(col_idx), float(scale), float(cap),
-        _plan_ptr(shape, mask), _ptr(o), _ptr(lse), _ptr(ws), ws.numel(), int(flags), _ptr(prof), _ptr(status),
-        _stream(stream)))
+        _sref(shape), _want("q", q, ind, dt, dev), _want("k", k, ind, dt, dev), _want("v", v, ind, dt, dev),
+        _want("row_ptr", row_ptr, (shape.rows + 1,), torch.int32, dev), _ptr(col_idx), scale, cap,
+        _plan_ptr(shape, mask), _want("o", o, outd, dt, dev), _want("lse", lse, (B, H, N), torch.float32, dev),
+        _ptr(ws), ws.numel(), int(flags), _ptr(prof), _ptr(status), _stream(stream)))
     return o, lse
 
 
@@ -700,17 +695,21 @@ def attn_masked_bwd(shape: Shape, q, k, v, o, lse, dout, row_ptr, col_idx, scale
                     mask: MaskPlan | None = None, dq=None, dk=None, dv=None, ws=None, flags: int = 0, prof=None,
                     status=None, stream=None):
     """Gradients of attn_masked_fwd, (dQ, dK, dV); layouts as attn_bwd."""
-    dev = q.device
-    dims = (shape.B, shape.N, shape.H, shape.d) if flags & OUT_RASTER else tuple(q.shape)
-    dq = torch.empty(dims, dtype=q.dtype, device=dev) if dq is None else dq
-    dk = torch.empty(dims, dtype=k.dtype, device=dev) if dk is None else dk
-    dv = torch.empty(dims, dtype=v.dtype, device=dev) if dv is None else dv
+    B, N, H, d = shape.B, shape.N, shape.H, shape.d
+    raster, blocked, dt, dev = (B, N, H, d), (B, H, N, d), shape.torch_dtype, torch.cuda.current_device()
+    outd = raster if flags & OUT_RASTER else blocked
+    dq = torch.empty(outd, dtype=dt, device=q.device) if dq is None else dq
+    dk = torch.empty(outd, dtype=dt, device=q.device) if dk is None else dk
+    dv = torch.empty(outd, dtype=dt, device=q.device) if dv is None else dv
     if ws is None:
-        ws = _empty(attn_masked_workspace_size(shape, True), dev)
+        ws = _empty(attn_masked_workspace_size(shape, True), q.device)
     _check("sparsp_attn_masked_bwd", lib().sparsp_attn_masked_bwd(
-        _sref(shape), _ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), _ptr(dout), _ptr(row_ptr), _ptr(col_idx),
-        float(scale), float(cap), _plan_ptr(shape, mask), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(ws), ws.numel(),
-        int(flags), _ptr(prof), _ptr(status), _stream(stream)))
+        _sref(shape), _want("q", q, blocked, dt, dev), _want("k", k, blocked, dt, dev),
+        _want("v", v, blocked, dt, dev), _want("o", o, outd, dt, dev),
+        _want("lse", lse, (B, H, N), torch.float32, dev), _want("dout", dout, blocked, dt, dev),
+        _want("row_ptr", row_ptr, (shape.rows + 1,), torch.int32, dev), _ptr(col_idx), scale, cap,
+        _plan_ptr(shape, mask), _want("dq", dq, outd, dt, dev), _want("dk", dk, outd, dt, dev),
+        _want("dv", dv, outd, dt, dev), _ptr(ws), ws.numel(), int(flags), _ptr(prof), _ptr(status), _stream(stream)))
     return dq, dk, dv
 
 
