@@ -71,6 +71,9 @@ struct AttnWs {
   // token masks only: the CSR of the block pairs that see something
   int32_t* seen_ptr;   // [rows+1]
   int32_t* seen_idx;   // [B*H*nb*nb]
+  // masked forward only: items for the general kernel, [rows] and [rows + 2]
+  int32_t* fix_items;
+  int32_t* fix_mark;   // marks, then count and pull counter
   size_t bytes;
 };
 
@@ -98,6 +101,8 @@ AttnWs attn_ws_layout(const Dims& s, bool backward, void* base, bool masked = fa
   if (masked) {
     w.seen_ptr = (int32_t*)take((rows + 1) * 4);
     w.seen_idx = (int32_t*)take(rows * (size_t)s.nb * 4);
+    w.fix_items = (int32_t*)take(rows * 4);
+    w.fix_mark = (int32_t*)take((rows + 2) * 4);
   }
   w.bytes = off;
   return w;
@@ -205,10 +210,13 @@ sparsp_status_t attn_fwd(const sparsp_shape_t* shape, const void* q, const void*
     return launch_attn_fwd_f32(s, (const float*)q, (const float*)k, (const float*)v, row_ptr,
                                col_idx, scale, (float*)o, lse, w.items, w.counter, prof, d_status,
                                st);
-  if (masked)
+  if (masked) {
+    const int64_t items = (int64_t)s.B * s.H * attn_fwd_tc_items_per_head(s);
+    const FixList fix{w.fix_items, w.fix_mark, w.fix_mark + items, w.fix_mark + items + 1};
     return launch_attn_fwd_masked(s, (const __nv_bfloat16*)q, (const __nv_bfloat16*)k, (const __nv_bfloat16*)v,
                                   row_ptr, col_idx, scale, cap, mask, (__nv_bfloat16*)o, lse, raster, in_raster,
-                                  w.items, w.counter, prof, d_status, st);
+                                  w.items, w.counter, fix, prof, d_status, st);
+  }
   if (tc)
     return launch_attn_fwd_tc(s, (const __nv_bfloat16*)q, (const __nv_bfloat16*)k,
                               (const __nv_bfloat16*)v, row_ptr, col_idx, scale,

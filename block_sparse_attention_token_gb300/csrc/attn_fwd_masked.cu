@@ -1,5 +1,6 @@
-// The tcgen05 forward with a token mask and, in a variant of its own, a score
-// cap (attn_fwd_tc.cuh).
+// The tcgen05 forward with a token mask and a score cap (attn_fwd_tc.cuh): the
+// kernel without a running maximum, then, where scores may leave its range, the
+// general one over the items it passed on (it returns at once when there are none).
 #include "attn_fwd_tc.cuh"
 
 namespace sparsp {
@@ -8,15 +9,26 @@ sparsp_status_t launch_attn_fwd_masked(const Dims& s, const __nv_bfloat16* q, co
                                        const __nv_bfloat16* v, const int32_t* row_ptr, const int32_t* col_idx,
                                        float scale, float cap, const MaskView& mask, __nv_bfloat16* o, float* lse,
                                        bool raster, bool in_raster, const int32_t* items, int32_t* counter,
-                                       uint64_t* prof, int32_t* d_status, cudaStream_t st) {
-  if (cap > kFixedCap)
-    return launch_fwd_mod<3>(s, q, k, v, row_ptr, col_idx, scale, o, lse, raster, in_raster, items, counter, prof,
-                             d_status, mask, cap, st);
-  if (cap > 0.f)
+                                       const FixList& fix, uint64_t* prof, int32_t* d_status, cudaStream_t st) {
+  if (cap > 0.f && cap <= kFixedCap)
     return launch_fwd_mod<2>(s, q, k, v, row_ptr, col_idx, scale, o, lse, raster, in_raster, items, counter, prof,
-                             d_status, mask, cap, st);
-  return launch_fwd_mod<1>(s, q, k, v, row_ptr, col_idx, scale, o, lse, raster, in_raster, items, counter, prof,
-                           d_status, mask, cap, st);
+                             d_status, mask, cap, FixList{}, st);
+  // the list: marks, then count and pull counter, in one stretch
+  const size_t n = (size_t)s.B * s.H * attn_fwd_tc_items_per_head(s);
+  if (cudaMemsetAsync(fix.mark, 0, (n + 2) * sizeof(int32_t), st) != cudaSuccess) return SPARSP_ERR_CUDA;
+  sparsp_status_t r;
+  if (cap > 0.f) {
+    r = launch_fwd_mod<2>(s, q, k, v, row_ptr, col_idx, scale, o, lse, raster, in_raster, items, counter, prof, d_status,
+                          mask, cap, fix, st);
+    if (r != SPARSP_OK) return r;
+    return launch_fwd_mod<3>(s, q, k, v, row_ptr, col_idx, scale, o, lse, raster, in_raster, fix.items, fix.counter, prof,
+                             d_status, mask, cap, fix, st);
+  }
+  r = launch_fwd_mod<1>(s, q, k, v, row_ptr, col_idx, scale, o, lse, raster, in_raster, items, counter, prof, d_status,
+                        mask, cap, fix, st);
+  if (r != SPARSP_OK) return r;
+  return launch_fwd_mod<4>(s, q, k, v, row_ptr, col_idx, scale, o, lse, raster, in_raster, fix.items, fix.counter, prof,
+                           d_status, mask, cap, fix, st);
 }
 
 }  // namespace sparsp

@@ -21,7 +21,7 @@ sparsp_status_t launch_attn_fwd_tc(const Dims& s, const __nv_bfloat16* q, const 
                                    float* lse, bool raster, bool in_raster, const int32_t* items,
                                    int32_t* counter, uint64_t* prof, int32_t* d_status, cudaStream_t st) {
   return launch_fwd_mod<0>(s, q, k, v, row_ptr, col_idx, scale, o, lse, raster, in_raster, items, counter, prof,
-                           d_status, MaskView{}, 0.f, st);
+                           d_status, MaskView{}, 0.f, FixList{}, st);
 }
 
 }  // namespace sparsp

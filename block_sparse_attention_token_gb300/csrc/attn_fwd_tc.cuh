@@ -52,11 +52,13 @@
 // SPARSP_ERR_TIMEOUT, all roles leave their loops, copies and MMAs in flight
 // are drained with a second bounded wait, and TMEM is released.
 //
-// MOD = 0 is attention over the selected blocks; MOD = 1 adds a token mask
-// (mask.cuh), MOD = 2 a score cap of at most kFixedCap beside it and MOD = 3 any
-// cap: y = cap tanh(scale s / cap) (cap.cuh). The producer tells with the item
-// which of its blocks the token mask cuts (by the blocks' ranges); in those each
-// row's visible columns come as bits, the others run as they do without a mask.
+// MOD = 0 is attention over the selected blocks. MOD = 1 adds a token mask
+// (mask.cuh) and MOD = 2 a score cap beside it, y = cap tanh(scale s / cap)
+// (cap.cuh), for scores in the range of a softmax without a maximum (FAST); MOD = 3
+// (cap) and 4 (none) are for any scores and do the items those pass on. The producer
+// tells with the item which of its blocks the token mask cuts (by the blocks'
+// ranges); in those each row's visible columns come as bits, the others run as
+// they do without a mask.
 #pragma once
 #include <type_traits>
 
@@ -93,11 +95,12 @@ struct Cfg {
   // a whole 128-column S row in registers (one pass per stage, S released as
   // soon as it is loaded) with the 200 registers the register split below
   // gives them.
-  static constexpr bool DUO = D == 64 && MOD_ != 2;
-  static constexpr int NSM = MOD_ == 2 ? 16 : 4;           // softmax warps
+  static constexpr bool FAST = MOD_ == 1 || MOD_ == 2;
+  static constexpr bool DUO = D == 64 && !FAST;
+  static constexpr int NSM = FAST ? 16 : 4;           // softmax warps
   // arrivals of the softmax warps at S_FREE, P_FULL and O_EMPTY: every thread, or with
   // MOD one lane of each warp concerned
-  static constexpr int kArrivals = MOD_ == 0 ? 32 * NSM : MOD_ == 2 ? 8 : 4;
+  static constexpr int kArrivals = MOD_ == 0 ? 32 * NSM : FAST ? 8 : 4;
   // MMA issuer warps: S and PV each get their own with d = 128; with DUO one
   // warp issues both streams (the softmax releases S(e-1) before it writes
   // P(e-1), so S(e) then PV(e-1) in one warp never wait on each other)
@@ -115,10 +118,10 @@ struct Cfg {
                 "register split of the two warpgroups");
   // K and V ring stages: 3 of each fit beside a d = 128 query tile; a DUO CTA
   // has half of the SM's shared memory for tiles of half the size: 3 K and 2 V
-  // (four with MOD 2 and d = 64, which has an SM's shared memory to itself; two V
+  // (four with FAST and d = 64, which has an SM's shared memory to itself; two V
   // stages with d = 128, whose row sums and cut bits need the room of the third)
-  static constexpr int NK = MOD_ == 2 && D == 64 ? 4 : 3;
-  static constexpr int NV = DUO || (MOD_ == 2 && D == 128) ? 2 : MOD_ == 2 ? 4 : 3;
+  static constexpr int NK = FAST && D == 64 ? 4 : 3;
+  static constexpr int NV = DUO || (FAST && D == 128) ? 2 : FAST ? 4 : 3;
   static constexpr int NSB = DUO ? 1 : 2, NPB = DUO ? 1 : 2;   // S and P buffers in TMEM
   static constexpr int NI = DUO || PAIR || MOD_ != 0 ? 2 : kNI;   // item ring slots
   static constexpr int kMinCtas = DUO ? 2 : 1;                  // CTAs per SM
@@ -147,16 +150,16 @@ struct Cfg {
   static constexpr uint32_t kMaskWords = !PAIR ? (MOD_ != 0 ? kMaxBlocks / 32 : 0)
                                                : (MASK_BYTES ? 8 * MAXW + 4 : (MOD_ != 0 ? 4 : 2) * MAXW + 1);
   static constexpr uint32_t kOffMask = kOffBits + kBitsBytes;
-  static constexpr uint32_t kOffEx = kOffMask + (NI * kMaskWords * 4 + 15) / 16 * 16;   // MOD 2: parts of the row sums
-  static constexpr uint32_t kOffMisc = kOffEx + (MOD_ == 2 ? 2048 : 0);
+  static constexpr uint32_t kOffEx = kOffMask + (NI * kMaskWords * 4 + 15) / 16 * 16;   // FAST: parts of the row sums
+  static constexpr uint32_t kOffMisc = kOffEx + (FAST ? 2048 : 0);
   static constexpr uint32_t kSmemBytes = kOffMisc + 16 + 1024;   // + alignment slack
   static_assert(kSmemBytes <= (DUO ? 115712u : 232448u), "shared memory");
 };
 constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr uint64_t kDrainNs = 200000000ull;
 constexpr float kRescaleThreshold = 8.0f;   // log2 units
-// Up to this cap exp(y) needs no reference: P <= 2^73, and with 2^19 keys and
-// values up to 2^35 the sums stay below 2^127; a row's smallest sum is 2^-73.
+// Up to this cap one reference c0 = cap log2(e) - 20 holds every score: P lies in
+// [2^-124.3, 2^20], so that sums of 2^19 terms and values up to 2^88 fit fp32.
 constexpr float kFixedCap = 50.0f;
 
 __device__ __forceinline__ bool wait_raw(uint32_t bar, uint32_t parity, uint64_t limit) {
@@ -219,6 +222,10 @@ struct Params {
   // MOD 2, 3: 2 scale log2(e) / cap, cap log2(e) and scale / cap
   float c1, cap2, inv_cap;
   NearCap near;
+  float c0;              // FAST: reference of every row, log2 units
+  int32_t* fix_items;    // FAST: items for the general kernel, or null; the general kernel: its items
+  int32_t* fix_count;
+  int32_t* fix_mark;     // [items] zeroed: is the item on the list
 };
 
 template <int BT, int D, int MOD>
@@ -242,6 +249,7 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint64_t t_start = globaltimer_ns();
   const int words = (p.nb + 31) >> 5;
+  if (MOD > 2 && p.fix_count != nullptr && *p.fix_count == 0) return;   // nothing was passed on
 
   if (threadIdx.x == 0) {
     mbar_init(bar(Q_FULL), 1);
@@ -289,6 +297,7 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
   const uint32_t tmem = *tmem_slot;
   const Guard g{abort_flag, p.d_status, kWaitNs};
   const int nb = p.nb, nbp = p.nbp;
+  const int64_t n_items = MOD > 2 && p.fix_count != nullptr ? *p.fix_count : p.n_items;
 
   if (warp >= C::NSM) {
   if constexpr (C::DUO) regs_decrease<C::kRegAux>();   // the whole second warpgroup
@@ -304,7 +313,7 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
       uint32_t* bmA = bits + ri * 2 * C::MAXW;
       uint32_t* bmB = bmA + C::MAXW;
       int32_t item = -1, len = -2, badbits = 0;
-      if (slot < p.n_items) {
+      if (slot < n_items) {
         item = p.items[slot];
         if constexpr (PAIR) {
           // the two rows as bitmaps in the ring slot; a bad row counts as empty
@@ -635,15 +644,18 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
     }
     __syncwarp();
   }
-  } else if constexpr (MOD == 2) {
-    // ------------------------------------------------------------ softmax + epilogue with a cap of at most kFixedCap
-    // Capped scores lie in [-cap, cap], so exp needs no reference: P = exp2(y) and
-    // the row sum stay far inside fp32 and bf16, and no maximum is taken, nothing is
-    // rescaled and stages do not depend on one another. Two groups of eight
-    // warps take the stages in turn (group g those of S and P buffer g), two warps
-    // per 32 rows with 64 columns each, so that the waits and loads of some run
-    // under the arithmetic of others. A warp goes through TMEM 32 columns at a
-    // time in a loop that is not unrolled: unrolled, its variants do not stay
+  } else if constexpr (C::FAST) {
+    // ------------------------------------------------------------ softmax + epilogue with a mask or a cap
+    // No running maximum: P = exp2(y - c0) with one constant c0 for every row. With a
+    // cap of at most kFixedCap the scores cannot leave the range of that; else
+    // c0 = 0 and an item with a row whose sum left [2^-80, 2^80], or whose O is not
+    // finite, goes on the list of items that the general kernel does after this
+    // one (scores of more than some 55 in magnitude: a softmax that is one key).
+    // So stages do not depend on one another and nothing is rescaled. Two groups of
+    // eight warps take the stages in turn (group g those of S and P buffer g),
+    // two warps per 32 rows with 64 columns each, so that the waits and loads of some
+    // run under the arithmetic of others. A warp goes through TMEM 32 columns at
+    // a time in a loop that is not unrolled: unrolled, its variants do not stay
     // in the instruction cache. At the end of an item the parts of the row sum
     // meet in shared memory and group 0 writes O and LSE while group 1 goes on.
     const int grp = warp >> 3, hh = (warp >> 2) & 1, rw = warp & 3, t = (int)(threadIdx.x & 127);
@@ -702,6 +714,7 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
       }
       UnionSeek seek(bits + ri * 2 * C::MAXW, bits + ri * 2 * C::MAXW + C::MAXW, PAIR ? words : 0);
       float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+      uint32_t any = 0u;   // this row has seen a key
       bool ok = true;
       for (int e = (grp ^ (int)(stages_before & 1u)); e < len; e += 2, ++turn) {
         // did the row block select this half's key block, does the mask cut it, and the
@@ -737,15 +750,8 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
           uint32_t s[32];
           tmem_ld32(tS + 32u * c, s);
           wait_ld();
-          float big[2] = {0.f, 0.f};
-#pragma unroll
-          for (int x = 0; x < 32; x += 2)
-            big[(x >> 1) & 1] = fmaxf(fmaxf(big[(x >> 1) & 1], fabsf(__uint_as_float(s[x]))),
-                                      fabsf(__uint_as_float(s[x + 1])));
-          // the largest score of the warp's chunk says which form of the cap holds
-          const float most = fmaxf(big[0], big[1]);
-          const bool near = __all_sync(0xffffffffu, most <= p.near.limit);
-          auto probs = [&](auto form_c, auto cut_c) {
+          any |= w;
+          auto probs = [&](auto form_c, auto cut_c) {   // form of the cap: near, within, any, none
             constexpr int FORM = decltype(form_c)::value;
             constexpr bool CUT = decltype(cut_c)::value;
 #pragma unroll
@@ -753,13 +759,15 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
               const float s0 = __uint_as_float(s[2 * x]), s1 = __uint_as_float(s[2 * x + 1]);
               float y0, y1;
               if constexpr (FORM == 0) {
-                near_cap_x2(p.near, s0, s1, y0, y1);
+                near_cap_x2(p.near, s0, s1, -p.c0, y0, y1);
               } else if constexpr (FORM == 1) {
                 tanh_poly_x2(s0, s1, p.inv_cap, y0, y1);
-                mul_x2(y0, y1, p.cap2, p.cap2, y0, y1);
+                fma_x2(y0, y1, p.cap2, -p.c0, y0, y1);
+              } else if constexpr (FORM == 2) {
+                y0 = cap_exp(s0 * p.c1, p.cap2) - p.c0;
+                y1 = cap_exp(s1 * p.c1, p.cap2) - p.c0;
               } else {
-                y0 = cap_exp(s0 * p.c1, p.cap2);
-                y1 = cap_exp(s1 * p.c1, p.cap2);
+                mul_x2(s0, s1, p.scale_log2, p.scale_log2, y0, y1);
               }
               float p0 = ex2f(y0), p1 = ex2f(y1);
               if constexpr (CUT) {
@@ -770,13 +778,26 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
               pk[x] = pack2(p0, p1);
             }
           };
-          if (near) {
-            if (cut) probs(std::integral_constant<int, 0>{}, std::true_type{});
-            else probs(std::integral_constant<int, 0>{}, std::false_type{});
-          } else if (__all_sync(0xffffffffu, most * p.inv_cap <= 1.f)) {
-            probs(std::integral_constant<int, 1>{}, std::true_type{});
+          using std::integral_constant;
+          if constexpr (MOD == 1) {
+            if (cut) probs(integral_constant<int, 3>{}, std::true_type{});
+            else probs(integral_constant<int, 3>{}, std::false_type{});
           } else {
-            probs(std::integral_constant<int, 2>{}, std::true_type{});
+            // the largest score of the warp's chunk says which form of the cap holds
+            float big[2] = {0.f, 0.f};
+#pragma unroll
+            for (int x = 0; x < 32; x += 2)
+              big[(x >> 1) & 1] = fmaxf(fmaxf(big[(x >> 1) & 1], fabsf(__uint_as_float(s[x]))),
+                                        fabsf(__uint_as_float(s[x + 1])));
+            const float most = fmaxf(big[0], big[1]);
+            if (__all_sync(0xffffffffu, most <= p.near.limit)) {
+              if (cut) probs(integral_constant<int, 0>{}, std::true_type{});
+              else probs(integral_constant<int, 0>{}, std::false_type{});
+            } else if (__all_sync(0xffffffffu, most * p.inv_cap <= 1.f)) {
+              probs(integral_constant<int, 1>{}, std::true_type{});
+            } else {
+              probs(integral_constant<int, 2>{}, std::true_type{});
+            }
           }
           tmem_st16(tP + 16u * c, pk);
         }
@@ -790,6 +811,7 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
       arrive(bar(I_EMPTY + ri));
       stages_before += (uint32_t)len;
       float l = (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+      if (any != 0u) l = fmaxf(l, 1.2e-38f);   // 0 is for a row that has seen no key
       if (!wait_warp(bar(EXCH + 4 + rw), (o_items & 1u) ^ 1u, g)) break;   // the last item's parts were read
       part[(2 * grp + hh) * 128 + t] = l;
       arrive(bar(EXCH + rw));
@@ -804,11 +826,21 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
       ++o_items;
       fence_after();
       const float inv = l > 0.f ? 1.0f / l : 0.f;   // 0: the row saw no key
+      // (NaN compares false: such a row goes to the general kernel as well)
+      bool good = p.fix_items == nullptr || l == 0.f || (l > 8.3e-25f && l < 1.2e24f);
 #pragma unroll 1
       for (int c = 0; c < D / 64; ++c) {
         uint32_t ov[32];
         tmem_ld32(t_row + C::kColO + hh * (D / 2) + c * 32u, ov);
         wait_ld();
+        if (p.fix_items != nullptr) {
+          float top[2] = {0.f, 0.f};   // NaN does not pass a maximum, but its row's l is NaN or its V is
+#pragma unroll
+          for (int x = 0; x < 32; x += 2)
+            top[(x >> 1) & 1] = fmaxf(fmaxf(top[(x >> 1) & 1], fabsf(__uint_as_float(ov[x]))),
+                                      fabsf(__uint_as_float(ov[x + 1])));
+          good = good && fmaxf(top[0], top[1]) < INFINITY;
+        }
         if (!stores) continue;
         uint32_t w[16];
 #pragma unroll
@@ -819,11 +851,15 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
       }
       fence_before();
       arrive(bar(O_EMPTY));
-      if (stores && hh == 0) p.lse[row] = l > 0.f ? log2f(l) * 0.69314718055994531f : -INFINITY;
+      if (stores && hh == 0) p.lse[row] = l > 0.f ? (p.c0 + log2f(l)) * 0.69314718055994531f : -INFINITY;
+      // one entry per item however many of its warps ask for it
+      if (p.fix_items != nullptr && __any_sync(0xffffffffu, stores && !good) && lane == 0 &&
+          atomicExch(&p.fix_mark[item], 1) == 0)
+        p.fix_items[atomicAdd(p.fix_count, 1)] = (int32_t)item;
     }
   } else if constexpr (MOD != 0) {
     if constexpr (C::DUO) regs_increase<C::kRegSoftmax>();
-    // ------------------------------------------------------------ softmax + epilogue with a mask, or a larger cap
+    // ------------------------------------------------------------ softmax + epilogue of any scores with a mask or a cap
     const uint32_t t_row = tmem + ((uint32_t)(warp * 32) << 16);
     uint32_t it_use = 0, s_use = 0, o_items = 0;
     uint64_t blocks_done = 0;
@@ -929,66 +965,7 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
       for (int e = 0; e < len; ++e) {
         const uint32_t b = s_use % C::NSB;
         const uint64_t gb = blocks_done + e;
-        // a stage whose scores all count as they are: the plain kernel's
-        auto stage = [&]() -> bool {
-          const bool h1 = PAIR ? has1 : true, h2 = PAIR ? has2 : true;
-          if (!wait_warp(bar(S_FULL + b), (s_use / C::NSB) & 1u, g)) return false;
-          fence_after();
-          uint32_t s[C::KR];
-          float cm[C::KR / 32];
-#pragma unroll
-          for (int c = 0; c < C::KR / 32; ++c)
-            cm[c] = tmem_ld32_max(t_row + C::kColS + b * 128u + c * 32u, s + 32 * c);
-          wait_ld();
-          fence_before();
-          arrive(bar(S_FREE + b));
-          ++s_use;
-          if (!h1) cm[0] = cm[1] = -INFINITY;
-          if (!h2) cm[2] = cm[3] = -INFINITY;
-          const float m_new = fmaxf(m, fmaxf(fmaxf(cm[0], cm[1]), fmaxf(cm[2], cm[3])) * sl2);
-          bool resc = false;
-          float f = 1.f;
-          if (__any_sync(0xffffffffu, m_new > m + kRescaleThreshold)) {
-            resc = e > 0;
-            f = ex2f(m - m_new);
-            m = m_new;
-          }
-          uint32_t pk[C::KR / 2];
-          float rs[8];
-#pragma unroll
-          for (int u = 0; u < 8; ++u) rs[u] = 0.f;
-#pragma unroll
-          for (int hh = 0; hh < 2; ++hh) {
-            if (hh == 0 ? h1 : h2) {
-#pragma unroll
-              for (int c = 32 * hh; c < 32 * hh + 32; ++c) {
-                float x0, x1;
-                fma_x2(__uint_as_float(s[2 * c]), __uint_as_float(s[2 * c + 1]), sl2, -m, x0, x1);
-                const float p0 = ex2f(x0), p1 = ex2f(x1);
-                add_x2(rs[2 * (c & 3)], rs[2 * (c & 3) + 1], p0, p1);
-                pk[c] = pack2(p0, p1);
-              }
-            } else {
-#pragma unroll
-              for (int c = 32 * hh; c < 32 * hh + 32; ++c) pk[c] = 0u;
-            }
-          }
-          if (gb >= (uint64_t)C::NPB) {   // P buffer b was last read by the PV of block g - NPB
-            if (!wait_warp(bar(PV_DONE + b), (uint32_t)(((gb - C::NPB) / C::NPB) & 1u), g)) return false;
-            fence_after();
-          }
-#pragma unroll
-          for (int c = 0; c < C::KR / 64; ++c) tmem_st32(t_row + C::kColP + b * 64u + 32u * c, pk + 32 * c);
-          if (resc) {
-            if (!rescale(gb, f)) return false;
-            l *= f;
-          }
-          l += ((rs[0] + rs[1]) + (rs[2] + rs[3])) + ((rs[4] + rs[5]) + (rs[6] + rs[7]));
-          return true;
-        };
-        // A stage the mask cuts for some row of the warp, or (MOD 3) one with a cap:
-        // half by half through TMEM in a loop that is not unrolled (unrolled, the
-        // variants of a stage do not stay in the instruction cache), against
+        // A stage goes half by half through TMEM in a loop that is not unrolled, against
         // the maximum of the stages before; when that is outgrown by more than the
         // threshold it starts over with the stage's own.
         auto stage_mod = [&]() -> bool {
@@ -1083,9 +1060,7 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
           l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
           return true;
         };
-        if constexpr (MOD == 3) ok = stage_mod();
-        else ok = cut1 || cut2 ? stage_mod() : stage();
-        if (!ok) break;
+        if (!(ok = stage_mod())) break;
         wait_st();
         fence_before();
         arrive(bar(P_FULL + b));
@@ -1325,7 +1300,7 @@ sparsp_status_t launch_fwd_mod(const Dims& s, const __nv_bfloat16* q, const __nv
                                const __nv_bfloat16* v, const int32_t* row_ptr, const int32_t* col_idx, float scale,
                                __nv_bfloat16* o, float* lse, bool raster, bool in_raster, const int32_t* items,
                                int32_t* counter, uint64_t* prof, int32_t* d_status, const MaskView& mask, float cap,
-                               cudaStream_t st) {
+                               const FixList& fix, cudaStream_t st) {
   const uint64_t rows = (uint64_t)s.B * s.H * s.N;
   CUtensorMap tq, tk, tv;
   if (in_raster) {
@@ -1343,9 +1318,10 @@ sparsp_status_t launch_fwd_mod(const Dims& s, const __nv_bfloat16* q, const __nv
   constexpr float kLog2e = 1.4426950408889634f;
   Params prm{row_ptr, col_idx, s.N, s.nb, nbp, (int64_t)s.B * s.H * nbp, (int64_t)rows, scale * kLog2e, o, lse,
              raster ? 1 : 0, raster_map(s), in_raster ? 1 : 0, raster_box(s), items, counter, prof, d_status,
-             mask, MOD >= 2 ? 2.f * scale * kLog2e / cap : 0.f, cap * kLog2e,
-             MOD >= 2 ? scale / cap : 0.f,
-             MOD == 2 ? near_cap(scale, cap) : NearCap{}};
+             mask, MOD == 2 || MOD == 3 ? 2.f * scale * kLog2e / cap : 0.f, cap * kLog2e,
+             MOD == 2 || MOD == 3 ? scale / cap : 0.f,
+             MOD == 2 ? near_cap(scale, cap) : NearCap{},
+             MOD == 2 && cap <= kFixedCap ? fmaxf(cap * kLog2e - 20.f, 0.f) : 0.f, fix.items, fix.count, fix.mark};
   if (s.Bt == 128 && s.d == 128) return go_fwd<128, 128, MOD>(s, tq, tk, tv, prm, st);
   if (s.Bt == 128 && s.d == 64) return go_fwd<128, 64, MOD>(s, tq, tk, tv, prm, st);
   if (s.Bt == 64 && s.d == 128) return go_fwd<64, 128, MOD>(s, tq, tk, tv, prm, st);

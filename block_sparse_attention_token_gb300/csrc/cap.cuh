@@ -33,14 +33,6 @@ __device__ constexpr float tanh_coef(int k) {
                   : 0.001041022245772183f;
 }
 
-__device__ __forceinline__ float cap_poly(float x) {
-  const float u = x * x;
-  float q = tanh_coef(6);
-#pragma unroll
-  for (int k = 5; k >= 0; --k) q = fmaf(q, u, tanh_coef(k));
-  return x * q;
-}
-
 // cap2 tanh by its definition, t = 2 x log2(e): 1 - 2 / (1 + exp(2 x)), for any x
 // (good to a few 2^-24 of the cap).
 __device__ __forceinline__ float cap_exp(float t, float cap2) {
@@ -57,14 +49,6 @@ __device__ __forceinline__ void tanh_poly_x2(float s0, float s1, float inv_cap, 
   for (int k = 4; k >= 0; --k) fma2_x2(q0, q1, u0, u1, tanh_coef(k), q0, q1);
   mul_x2(x0, x1, q0, q1, t0, t1);
 }
-// cap2 tanh + add of a pair of scores
-__device__ __forceinline__ void cap_poly_x2(float s0, float s1, float inv_cap, float cap2, float add, float& y0,
-                                            float& y1) {
-  float t0, t1;
-  tanh_poly_x2(s0, s1, inv_cap, t0, t1);
-  fma_x2(t0, t1, cap2, add, y0, y1);
-}
-
 // Where all |x| <= kNearCap a polynomial of degree 4 in s^2 does (the same fit, 1.7e-7
 // evaluated in fp32), with the powers of scale / cap and the factor cap2 folded into
 // its coefficients: six multiply-adds from the score to y. `limit` is the largest
@@ -106,14 +90,14 @@ __device__ __forceinline__ void near_tanh_x2(const NearCap& n, float s0, float s
   fma2_x2(q0, q1, u0, u1, n.c[0], q0, q1);
   mul_x2(s0, s1, q0, q1, t0, t1);
 }
-// y of a pair of scores
-__device__ __forceinline__ void near_cap_x2(const NearCap& n, float s0, float s1, float& y0, float& y1) {
+// y + add of a pair of scores
+__device__ __forceinline__ void near_cap_x2(const NearCap& n, float s0, float s1, float add, float& y0, float& y1) {
   float u0, u1, q0, q1;
   mul_x2(s0, s1, s0, s1, u0, u1);
   fma_x2(u0, u1, n.c[4], n.c[3], q0, q1);
 #pragma unroll
   for (int k = 2; k >= 0; --k) fma2_x2(q0, q1, u0, u1, n.c[k], q0, q1);
-  mul_x2(s0, s1, q0, q1, y0, y1);
+  fma2_x2(s0, s1, q0, q1, add, y0, y1);
 }
 
 }  // namespace tc

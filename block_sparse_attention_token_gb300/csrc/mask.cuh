@@ -99,12 +99,20 @@ sparsp_status_t launch_mask_scores(const Dims& s, const MaskView& m, float* scor
 sparsp_status_t launch_mask_csr(const Dims& s, const MaskView& m, const int32_t* row_ptr, const int32_t* col_idx,
                                 int32_t* out_ptr, int32_t* out_idx, int32_t* d_status, cudaStream_t st);
 
+// Items the fast forward kernels pass on to the general one: all zeroed before.
+struct FixList {
+  int32_t* items;     // [items]
+  int32_t* mark;      // [items]
+  int32_t* count;     // 1
+  int32_t* counter;   // 1: the general kernel's pull counter
+};
+
 // tcgen05 attention with a token mask (may be empty) and a score cap (0: none).
 sparsp_status_t launch_attn_fwd_masked(const Dims& s, const __nv_bfloat16* q, const __nv_bfloat16* k,
                                        const __nv_bfloat16* v, const int32_t* row_ptr, const int32_t* col_idx,
                                        float scale, float cap, const MaskView& mask, __nv_bfloat16* o, float* lse,
                                        bool raster, bool in_raster, const int32_t* items, int32_t* counter,
-                                       uint64_t* prof, int32_t* d_status, cudaStream_t st);
+                                       const FixList& fix, uint64_t* prof, int32_t* d_status, cudaStream_t st);
 sparsp_status_t launch_attn_bwd_masked(const Dims& s, int mode, const __nv_bfloat16* q, const __nv_bfloat16* k,
                                        const __nv_bfloat16* v, const __nv_bfloat16* dout, const float* lse2,
                                        const float* delta, const int32_t* ptr, const int32_t* idx, float scale,
