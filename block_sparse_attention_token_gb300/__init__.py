@@ -649,6 +649,26 @@ def mask_plan(shape: Shape, pos, lo, hi, plan: MaskPlan | None = None, stream=No
     return plan
 
 
+def document_mask(shape: Shape, ids):
+    """(pos, lo, hi) of mask_plan for documents packed into one grid: ids int32
+    [B, N], raster order; a token sees the tokens of its own number, and a token of a
+    negative number (padding) sees and is seen by nothing."""
+    live = ids >= 0
+    pos = torch.where(live, ids, -1).int()
+    return pos, torch.where(live, ids, 0).int(), torch.where(live, ids + 1, 0).int()
+
+
+def frame_mask(shape: Shape, prefix: int = 0, window: int | None = None, device="cuda"):
+    """(pos, lo, hi) of mask_plan for generation frame by frame: a token sees its own
+    frame and those before it (the last `window` frames of them, its own included),
+    and with no window also the first `prefix` frames."""
+    if window is not None and (prefix or window < 1):
+        raise ValueError("frame_mask: a window is at least one frame and takes no prefix")
+    t = (torch.arange(shape.N, device=device) // (shape.Y * shape.X)).expand(shape.B, shape.N)
+    lo = torch.zeros_like(t) if window is None else (t - window + 1).clamp(min=0)
+    return t.int().contiguous(), lo.int().contiguous(), (t + 1).clamp(min=prefix).int().contiguous()
+
+
 def _plan_ptr(shape: Shape, mask: MaskPlan | None):
     if mask is None:
         return None
@@ -736,5 +756,5 @@ def default_scale(d: int) -> float:
     return 1.0 / math.sqrt(d)
 
 
-from .pipeline import GraphedStep, Pipeline  # noqa: E402,F401
+from .pipeline import GraphedStep, Pipeline, QKNorm  # noqa: E402,F401
 from .streaming import HostPipeline  # noqa: E402,F401

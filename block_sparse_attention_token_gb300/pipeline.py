@@ -1,12 +1,17 @@
 """The whole hot path as one object with preallocated device buffers.
 
-forward(): reorder Q, K, V into tiles -> block scores -> Top-p/Top-k selection
+forward(): (optional) token norm and three-axis rotary positions of Q and K -> reorder
+Q, K, V into tiles (the rotation happens in that pass) -> block scores -> Top-p/Top-k selection
 -> (optional) head balancing over P virtual ranks and slack-aware augmentation
 of the CSR -> (optional) dependency-aware placement of blocks on the P
 partitions -> KV demand of P partitions (+ gather) -> block-sparse attention
 -> O in raster order (written there by attention itself where the tcgen05
 kernel runs, else by an inverse reorder). backward(): dO into tiles ->
-attention backward -> dQ, dK, dV in raster order (likewise). Every step is one
+attention backward -> dQ, dK, dV in raster order (likewise) -> (optional) inverse
+rotation and norm backward, with the gradients of the norm's weights. With a token
+mask, block pairs that see nothing of each other are masked before the selection,
+and attention runs over the tokens that the mask lets through; a score cap
+applies in attention alone. Every step is one
 or more libsparsp kernels on the current stream, except that by default the
 KV demand gather runs on a side
 stream beside attention (the caller's stream waits for both); nothing here
@@ -22,9 +27,25 @@ import torch
 
 from . import (EST_LOWRANK, EST_MEAN, PROF_SLOTS, Shape, attn_bwd, attn_fwd, attn_workspace_size, augment,
                augment_workspace_size, balance_heads, Balance, predictor_fit,
+               attn_masked_bwd, attn_masked_fwd, attn_masked_workspace_size, MaskPlan, mask_scores, norm_bwd, norm_fwd,
+               norm_workspace_size, rope as rope_turn, RopeTable,
                block_scores, block_scores_pooled, block_scores_workspace_size, kv_demand, kv_gather, lib, placement,
                placement_workspace_size, reorder, reorder_pool, select, select_workspace_size, DemandOut,
                OUT_RASTER, IN_RASTER, pool_means)
+
+
+@dataclasses.dataclass
+class QKNorm:
+    """Token norm of Q and of K in a Pipeline: layer norm, or RMS norm with rms, over
+    the H*d values of a token, or over each head's d values with per_head. Weights
+    and biases are float32 [H*d] or [d], or None; they are read at every forward()."""
+    q_weight: torch.Tensor | None = None
+    k_weight: torch.Tensor | None = None
+    q_bias: torch.Tensor | None = None
+    k_bias: torch.Tensor | None = None
+    eps: float = 1e-6
+    rms: bool = False
+    per_head: bool = False
 
 
 class Pipeline:
@@ -41,7 +62,12 @@ class Pipeline:
         bal = (1 if self.migrations is not None else 0) + (14 if self.augment else 0)
         # projection, two score products, gradient products, loss (partials, sum), weight gradients
         pred = 7 if self.predictor_lr is not None else 0
-        return 3 + scores + pred + 3 + bal + place + 4 + gather + lpt + 1 + (0 if self.raster_out else 1)
+        # norm of Q and K; with raster inputs the rotation is a pass of its own; masked scores, the masked CSR (count,
+        # scan, fill), and the general attention kernel over what the first one passes on
+        extra = (2 if self.norm is not None else 0) + (2 if self.rope is not None and self.raster_in else 0)
+        extra += (4 if self.mask is not None else 0)
+        extra += 1 if (self.mask is not None and not self.cap) or self.cap > 50 else 0
+        return 3 + scores + pred + 3 + bal + place + 4 + gather + lpt + 1 + (0 if self.raster_out else 1) + extra
 
     def kernels_per_backward(self) -> int:
         """reorder dO, rowdot, CSR transpose, schedule, dQ, schedule, dK + dV (one
@@ -49,18 +75,26 @@ class Pipeline:
         backward writes raster gradients)."""
         lpt = 2 if self.flags & 1 else 1
         kv = 2 if self.flags & 4 else 1
-        return 1 + 1 + 1 + lpt + 1 + lpt + kv + (0 if self.raster_out else 3)
+        if self.mask is not None or self.cap:
+            kv = 1
+        # the masked CSR; the inverse rotations (in place of two inverse reorders where there are any); norm backward
+        # (gradient, weights' sums) of Q and K
+        extra = (3 if self.mask is not None else 0) + (2 if self.rope is not None and self.raster_out else 0)
+        extra += 4 if self.norm is not None else 0
+        return 1 + 1 + 1 + lpt + 1 + lpt + kv + (0 if self.raster_out else 3) + extra
 
     def __init__(self, shape: Shape, estimator: str, top_p: float, k_floor: int, P: int, rank: int = 16,
                  gather: bool = True, flags: int = 0, backward: bool = False, device="cuda",
                  fused_estimation: bool = True, placement: bool = False, migrations: int | None = None,
                  augment: bool = False, predictor_lr: float | None = None, overlap_demand: bool = True,
-                 raster_inputs: bool = False):
+                 raster_inputs: bool = False, norm: QKNorm | None = None, rope: RopeTable | None = None,
+                 rope_pos: torch.Tensor | None = None, mask: MaskPlan | None = None, cap: float = 0.0):
         """overlap_demand: after the KV demand lists (bitmap, offsets, indices),
         run the demand gather on a low-priority side stream while attention runs
         on a high-priority one; the two only read the same K/V, and the
         gather's CTAs (no shared memory) fit beside the persistent attention
-        CTAs. forward() returns after both on the caller's stream. migrations: balance heads over P virtual ranks with at most this many
+        CTAs. forward() returns after both on the caller's stream. migrations: balance
+        heads over P virtual ranks with at most this many
         migrations (None: no balancing). augment: fill each rank's slack with
         extra blocks (on the balanced ranks, or the contiguous head split);
         attention then runs on the augmented CSR. predictor_lr: with the
@@ -70,7 +104,11 @@ class Pipeline:
         reorder pass; the tile means come from a pooling read of raster Q and
         K, and the demand gather and attention read the raster tensors
         themselves (each block one 5-D TMA box), so forward()'s inputs stay
-        in use until attention and the gather have finished."""
+        in use until attention and the gather have finished. norm: token norm of Q and
+        K first; backward() then also reads forward()'s q and k, and leaves the
+        weights' gradients in self.norm_grads. rope: three-axis rotary positions
+        of Q and K (rope_pos: int32 [B, N, 3] table positions, default the grid). mask: a
+        token mask; cap: a score cap; both need shapes of the tcgen05 kernels."""
         self.shape, self.top_p, self.k_floor, self.P, self.rank, self.flags = shape, top_p, k_floor, P, rank, flags
         self.est = EST_LOWRANK if estimator == "lowrank" else EST_MEAN
         self.fused = fused_estimation
@@ -79,6 +117,16 @@ class Pipeline:
         dev = torch.device(device)
         blocked = (s.B, s.H, s.N, s.d)
         self.raster_in = raster_inputs
+        self.norm, self.rope, self.rope_pos, self.mask, self.cap = norm, rope, rope_pos, mask, float(cap)
+        raster = (s.B, s.N, s.H, s.d)
+        self.qn = self.kn = self.qr = self.kr = None       # normed, and normed and turned, raster Q and K
+        if norm is not None:
+            self.qn, self.kn = (torch.empty(raster, dtype=dt, device=dev) for _ in range(2))
+            stat = raster[:3] if norm.per_head else raster[:2]
+            self.norm_stats = [(None if norm.rms else torch.empty(stat, dtype=torch.float32, device=dev),
+                                torch.empty(stat, dtype=torch.float32, device=dev)) for _ in range(2)]
+        if rope is not None and raster_inputs:
+            self.qr, self.kr = (torch.empty(raster, dtype=dt, device=dev) for _ in range(2))
         self.qb = self.kb = self.vb = None
         if not raster_inputs:
             self.qb, self.kb, self.vb = (torch.empty(blocked, dtype=dt, device=dev) for _ in range(3))
@@ -126,6 +174,12 @@ class Pipeline:
         # the stage after which forward()'s raster inputs are no longer read
         self.inputs_read_mark = ("overlap" if overlap_demand and gather else "attn_fwd") if raster_inputs \
             else "reorder"
+        masked = mask is not None or self.cap != 0.0
+        if masked and not fwd_raster:
+            raise ValueError("a token mask or a score cap needs a shape of the tcgen05 kernels")
+        self._qk_in = None   # forward()'s q and k (read by the norm's backward)
+        # the stage of backward() after which the step's raster inputs are no longer read
+        self.grad_inputs_read_mark = "reorder_dout" if norm is None else "norm_bwd"
         self._o_fwd = None   # the buffer forward() last wrote O to (read by backward() when raster)
         # block-order O (and gradients) only where attention does not write raster rows
         self.ob = None if self.raster_out else torch.empty(blocked, dtype=dt, device=dev)
@@ -153,7 +207,8 @@ class Pipeline:
         if placement:
             self.owner = torch.empty((s.B, s.nb), dtype=torch.int32, device=dev)
             self.ws_place = torch.empty(max(placement_workspace_size(s), 16), dtype=torch.uint8, device=dev)
-        self.ws_attn = torch.empty(max(attn_workspace_size(s, backward), 16), dtype=torch.uint8, device=dev)
+        n_ws = attn_masked_workspace_size(s, backward) if masked else attn_workspace_size(s, backward)
+        self.ws_attn = torch.empty(max(n_ws, 16), dtype=torch.uint8, device=dev)
         self.status = torch.zeros(1, dtype=torch.int32, device=dev)
         self.prof = torch.zeros(PROF_SLOTS, dtype=torch.int64, device=dev)
         if backward:
@@ -163,6 +218,21 @@ class Pipeline:
                 self.dqb, self.dkb, self.dvb = (torch.empty(blocked, dtype=dt, device=dev) for _ in range(3))
             self.dq, self.dk, self.dv = (torch.empty((s.B, s.N, s.H, s.d), dtype=dt, device=dev)
                                          for _ in range(3))
+            # gradients between attention and the inverse rotation, and between that and the norm
+            self._g_attn = [torch.empty(raster, dtype=dt, device=dev) for _ in range(2)] \
+                if self.raster_out and (norm is not None or rope is not None) else None
+            self._g_rope = [torch.empty(raster, dtype=dt, device=dev) for _ in range(2)] \
+                if norm is not None and (rope is not None or not self.raster_out) else None
+            self.norm_grads = None
+            if norm is not None:
+                cols = s.d if norm.per_head else s.H * s.d
+                mk = lambda: torch.empty(cols, dtype=torch.float32, device=dev)
+                # {"q_weight", "k_weight"[, "q_bias", "k_bias"]}: written by every backward()
+                self.norm_grads = {x: mk() for x in ("q_weight", "k_weight")}
+                if not norm.rms or norm.q_bias is not None or norm.k_bias is not None:
+                    self.norm_grads.update({x: mk() for x in ("q_bias", "k_bias")})
+                self.ws_norm = torch.empty(max(norm_workspace_size(s, norm.rms, norm.per_head), 16), dtype=torch.uint8,
+                                           device=dev)
 
     def forward(self, q, k, v, wq=None, wk=None, prof: bool = False, mark=None, out=None, before=None):
         """mark: optional callable(stage_name, stream=None) invoked after each
@@ -175,33 +245,42 @@ class Pipeline:
         s = self.shape
         mark = mark or (lambda name, stream=None: None)
         before = before or (lambda name: None)
-        if self.raster_in:   # the tile means alone: attention and the gather read the raster tensors
-            before("q")
-            pool_means(s, q, self.qmeans)
-            before("k")
-            pool_means(s, k, self.kmeans)
-            mark("reorder")
-            block_scores_pooled(s, self.qmeans, self.kmeans, self.est, wq, wk, self.rank, out=self.scores,
-                                ws=self.ws_pooled)
-        elif self.fused:   # the tile means come out of the reorder pass itself
-            before("q")
-            reorder_pool(s, q, self.qb, self.qmeans)
-            before("k")
-            reorder_pool(s, k, self.kb, self.kmeans)
+        def prepared(name, x, normed, stats, weight, bias, turned, blocked, means):
+            """Norm, rotation and tile order of Q or K, as far as this pipeline does
+            them; returns the tensor that attention reads."""
+            before(name)
+            if self.norm is not None:
+                n = self.norm
+                norm_fwd(s, x, weight, bias, n.eps, n.rms, n.per_head, out=normed, mean=stats[0], rstd=stats[1])
+                x = normed
+            means = means if self.fused else None
+            if self.rope is not None:
+                return rope_turn(s, self.rope, x, out=turned if self.raster_in else blocked,
+                                 out_blocked=not self.raster_in, pos=self.rope_pos, means=means, status=self.status)
+            if self.raster_in:   # the tile means alone: attention and the gather read the raster tensors
+                pool_means(s, x, means)
+                return x
+            if self.fused:       # the tile means come out of the reorder pass itself
+                reorder_pool(s, x, blocked, means)
+            else:
+                reorder(s, x, blocked)
+            return blocked
+
+        n, st = self.norm or QKNorm(), self.norm_stats if self.norm is not None else (None, None)
+        self._qk_in = (q, k)
+        aq = prepared("q", q, self.qn, st[0], n.q_weight, n.q_bias, self.qr, self.qb, self.qmeans)
+        ak = prepared("k", k, self.kn, st[1], n.k_weight, n.k_bias, self.kr, self.kb, self.kmeans)
+        if not self.raster_in:
             before("v")
             reorder(s, v, self.vb)
-            mark("reorder")
+        mark("reorder")
+        if self.fused:
             block_scores_pooled(s, self.qmeans, self.kmeans, self.est, wq, wk, self.rank, out=self.scores,
                                 ws=self.ws_pooled)
         else:
-            before("q")
-            reorder(s, q, self.qb)
-            before("k")
-            reorder(s, k, self.kb)
-            before("v")
-            reorder(s, v, self.vb)
-            mark("reorder")
             block_scores(s, self.qb, self.kb, self.est, wq, wk, self.rank, out=self.scores, ws=self.ws_scores)
+        if self.mask is not None:
+            mask_scores(s, self.mask, self.scores)
         mark("scores")
         if self.predictor_lr is not None:
             predictor_fit(s, self.qmeans, self.kmeans, wq, wk, self.predictor_lr, self.rank, self.predictor_loss,
@@ -224,11 +303,19 @@ class Pipeline:
         o = self.o if out is None else out
         # attention output: raster O directly, or block order and an inverse reorder
         o_attn, aflags = (o, self.flags | OUT_RASTER) if self.raster_out else (self.ob, self.flags)
+        av = self.vb
         if self.raster_in:
             before("v")
-            aq, ak, av, aflags = q, k, v, aflags | IN_RASTER
-        else:
-            aq, ak, av = self.qb, self.kb, self.vb
+            av, aflags = v, aflags | IN_RASTER
+
+        def attention(stream=None):
+            p = self.prof if prof else None
+            if self.mask is not None or self.cap:
+                attn_masked_fwd(s, aq, ak, av, rp, ci, 0.0, self.cap, self.mask, o_attn, self.lse, self.ws_attn,
+                                aflags, p, self.status, stream)
+            else:
+                attn_fwd(s, aq, ak, av, rp, ci, 0.0, o_attn, self.lse, self.ws_attn, aflags, p, self.status, stream)
+
         if self.overlap_demand and self.demand.kg is not None:
             # the lists (bitmap, offsets, indices) first, on this stream: they need a
             # little shared memory, which attention leaves none of; then the gather
@@ -244,8 +331,7 @@ class Pipeline:
             lo.wait_event(self._selected)
             with torch.cuda.stream(hi):   # enqueued first: the persistent CTAs take their SMs first
                 mark("attn_fwd:begin", hi)
-                attn_fwd(s, aq, ak, av, rp, ci, 0.0, o_attn, self.lse, self.ws_attn,
-                         aflags, self.prof if prof else None, self.status, stream=hi)
+                attention(hi)
                 mark("attn_fwd", hi)
             with torch.cuda.stream(lo):
                 mark("kv_gather:begin", lo)
@@ -263,8 +349,7 @@ class Pipeline:
                 kv_demand(s, self.P, rp, ci, self.kb, self.vb, out=self.demand, status=self.status,
                           owner=self.owner)
             mark("kv_demand")
-            attn_fwd(s, aq, ak, av, rp, ci, 0.0, o_attn, self.lse, self.ws_attn,
-                     aflags, self.prof if prof else None, self.status)
+            attention()
             mark("attn_fwd")
         if not self.raster_out:
             reorder(s, self.ob, o, inverse=True)
@@ -277,7 +362,8 @@ class Pipeline:
         before: optional callable("do") invoked just before dout is first read.
         With raster_out the backward reads O from the buffer the last forward()
         wrote it to, which must still hold it, and writes the gradients' raster
-        rows itself."""
+        rows itself. With a norm it reads forward()'s q and k, which must still hold
+        their values, and writes the weights' gradients to self.norm_grads."""
         s = self.shape
         mark = mark or (lambda name: None)
         if before is not None:   # e.g. to wait for dout's copy
@@ -286,20 +372,42 @@ class Pipeline:
         mark("reorder_dout")
         rp, ci = self.csr
         dq, dk, dv = (self.dq, self.dk, self.dv) if outs is None else outs
+        gq, gk = (dq, dk) if self.norm is None and self.rope is None else (self._g_attn or (None, None))
+        p = self.prof if prof else None
         if self.raster_out:
             if self._o_fwd is None:
                 raise RuntimeError("backward() needs a forward() first")
-            attn_bwd(s, self.qb, self.kb, self.vb, self._o_fwd, self.lse, self.dob, rp, ci, 0.0, dq, dk, dv,
-                     self.ws_attn, self.flags | OUT_RASTER, self.prof if prof else None, self.status)
+            args = (s, self.qb, self.kb, self.vb, self._o_fwd, self.lse, self.dob, rp, ci, 0.0)
+            rest = (gq, gk, dv, self.ws_attn, self.flags | OUT_RASTER, p, self.status)
+            if self.mask is not None or self.cap:
+                attn_masked_bwd(*args, self.cap, self.mask, *rest)
+            else:
+                attn_bwd(*args, *rest)
             mark("attn_bwd")
-            return dq, dk, dv
-        attn_bwd(s, self.qb, self.kb, self.vb, self.ob, self.lse, self.dob, rp, ci, 0.0,
-                 self.dqb, self.dkb, self.dvb, self.ws_attn, self.flags, self.prof if prof else None, self.status)
-        mark("attn_bwd")
-        reorder(s, self.dqb, dq, inverse=True)
-        reorder(s, self.dkb, dk, inverse=True)
-        reorder(s, self.dvb, dv, inverse=True)
-        mark("reorder_grads")
+        else:
+            attn_bwd(s, self.qb, self.kb, self.vb, self.ob, self.lse, self.dob, rp, ci, 0.0,
+                     self.dqb, self.dkb, self.dvb, self.ws_attn, self.flags, p, self.status)
+            mark("attn_bwd")
+            gq, gk = self.dqb, self.dkb
+        # dQ and dK back through the rotation (and to raster order), then through the norm
+        g_in = (gq, gk)
+        g_out = (dq, dk) if self.norm is None else (self._g_rope or g_in)
+        for g, to in zip(g_in, g_out):
+            if self.rope is not None:
+                rope_turn(s, self.rope, g, out=to, inverse=True, in_blocked=not self.raster_out, out_blocked=False,
+                          pos=self.rope_pos, status=self.status)
+            elif not self.raster_out:
+                reorder(s, g, to, inverse=True)
+        if not self.raster_out:
+            reorder(s, self.dvb, dv, inverse=True)
+            mark("reorder_grads")
+        if self.norm is not None:
+            n, grads = self.norm, self.norm_grads
+            for x, g, to, (mean, rstd), w, name in zip(self._qk_in, g_out, (dq, dk), self.norm_stats,
+                                                       (n.q_weight, n.k_weight), ("q", "k")):
+                norm_bwd(s, g, x, w, mean, rstd, n.rms, n.per_head, dx=to, dw=grads[name + "_weight"],
+                         db=grads.get(name + "_bias"), ws=self.ws_norm)
+            mark("norm_bwd")
         return dq, dk, dv
 
     def capture(self, q, k, v, wq=None, wk=None, dout=None) -> "GraphedStep":

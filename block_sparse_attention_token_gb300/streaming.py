@@ -87,7 +87,7 @@ class HostPipeline:
         cur.wait_event(self.out_free[b])                   # step n-2's results have left the device
 
         def mark(name, stream=None):
-            if name == "reorder_dout":                     # every raster input has been read
+            if name == self.pipe.grad_inputs_read_mark:    # every raster input has been read
                 self.in_free[b].record(cur)
 
         q, k, v, do = self.t_inp[b]
