@@ -62,7 +62,8 @@ rowdot_kernel(const __nv_bfloat16* __restrict__ o, const __nv_bfloat16* __restri
   for (int off = 4; off > 0; off >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, off);
   if (row < rows && sub == 0) {
     delta[row] = acc;
-    if (lse2 != nullptr) lse2[row] = lse[row] * kLog2e;   // -inf stays -inf
+    // a row that attended to nothing (-inf) gets +inf: exp2(y - inf) is then 0 for every key
+    if (lse2 != nullptr) lse2[row] = lse[row] == -INFINITY ? INFINITY : lse[row] * kLog2e;
   }
 }
 

@@ -61,8 +61,7 @@
 // MOD = 1 adds the forward's token mask and MOD = 2 its score cap beside it
 // (modes 0 and 3): dS gains the factor 1 - tanh^2, and tanh is the forward's
 // (cap.cuh). The producer tells with the item which of its blocks the token mask
-// cuts; there P is cleared by the bits of the columns a row sees (a query that
-// sees no key has LSE = -inf, and is cleared everywhere).
+// cuts; there P is cleared by the bits of the columns a row sees.
 #pragma once
 #include <type_traits>
 
@@ -270,6 +269,7 @@ attn_bwd_tc_kernel(const __grid_constant__ CUtensorMap ta1, const __grid_constan
           const bool okB = iA + 1 < nb ? list_bitmap(p.ptr, p.idx, nb, bh * nb + iA + 1, bmB, words, lane) : true;
           badbits = (okA ? 0 : 1) | (okB ? 0 : 2);
           if (badbits && lane == 0) report(p.d_status, SPARSP_ERR_DATA);
+          if (MOD != 0) badbits = 0;   // its bitmap is empty: it counts as an empty row
           const int u = union_count(bmA, bmB, words, lane);
           len = (badbits == 3) ? -1 : (u + 1) / 2;   // stages of two blocks
           if constexpr (MOD != 0) {
@@ -300,7 +300,7 @@ attn_bwd_tc_kernel(const __grid_constant__ CUtensorMap ta1, const __grid_constan
           bad = __any_sync(0xffffffffu, bad);
           if (bad) {
             if (lane == 0) report(p.d_status, SPARSP_ERR_DATA);
-            len = -1;
+            len = MOD != 0 ? 0 : -1;   // MOD: it counts as an empty row
           } else {
             len = b - a;
             if constexpr (MOD != 0) {

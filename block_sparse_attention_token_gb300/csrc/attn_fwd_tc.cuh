@@ -326,6 +326,7 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
                                        : true;
           badbits = (okA ? 0 : 1) | (okB ? 0 : 2);
           if (badbits && lane == 0) report(p.d_status, SPARSP_ERR_DATA);
+          if (MOD != 0) badbits = 0;   // its bitmap is empty: it counts as an empty row
           const int u = union_count(bmA, bmB, words, lane);
           len = (badbits == 3) ? -1 : (u + 1) / 2;   // stages of two key blocks
           if constexpr (MOD != 0) {
@@ -353,7 +354,7 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
           bad = __any_sync(0xffffffffu, bad);
           if (bad) {
             if (lane == 0) report(p.d_status, SPARSP_ERR_DATA);
-            len = -1;
+            len = MOD != 0 ? 0 : -1;   // MOD: it counts as an empty row
           } else {
             len = b - a;
             if constexpr (MOD != 0) {

@@ -579,12 +579,13 @@ SPARSP_API sparsp_status_t sparsp_mask_scores(const sparsp_shape_t* shape, const
  *   y = scale q.k, or cap tanh(scale q.k / cap) where cap > 0,
  *   O_q = sum_k softmax_k(y) v_k,   LSE_q = ln sum_k exp(y).
  * plan: of sparsp_mask_plan for this shape, or NULL (every key is seen). cap = 0:
- * no cap, else 2^-20 <= cap <= 2^20 (SPARSP_ERR_INVALID_ARG outside). A query that sees no key gives O = 0, LSE = -inf. Block pairs that
- * see nothing of each other are dropped before the work is ordered. Values in
- * keys that a query does not see must be finite (their weight is 0, and 0 times
- * infinity is not). A malformed row (an index outside [0, nb), more than nb
- * entries) sets SPARSP_ERR_DATA; with a plan it counts as empty, else it is
- * skipped.
+ * no cap, else 2^-20 <= cap <= 2^20 (SPARSP_ERR_INVALID_ARG outside). A query that
+ * sees no key gives O = 0, LSE = -inf. Block pairs that see nothing of each other
+ * are dropped before the work is ordered (unless the shape is so small that
+ * this would cost more). Values in keys that a query does not see must be finite
+ * (their weight is 0, and 0 times infinity is not). A malformed row (an index
+ * outside [0, nb), more than nb entries; with 64-token blocks an index given
+ * twice) sets SPARSP_ERR_DATA and counts as empty.
  * bf16 on the tcgen05 kernels (Bt and d in {64, 128}, nb <= 1024 when Bt = 64
  * and d = 128); elsewhere, and with SPARSP_KERNEL_PORTABLE,
  * SPARSP_ERR_UNSUPPORTED. The other options, scale, prof and layouts as in
@@ -602,7 +603,8 @@ SPARSP_API sparsp_status_t sparsp_attn_masked_fwd(const sparsp_shape_t* shape, c
  *   P = exp(y - LSE) on the keys seen, dS = P (dO V^T - D) (1 - tanh^2(scale q.k / cap))
  * (the last factor with a cap), dQ = scale dS K, dK = scale dS^T Q, dV = P^T dO.
  * Queries that see nothing and keys that nobody sees get zero gradients; all
- * values must be finite there too. dK and dV always come from one kernel
+ * values must be finite there too. A malformed row sets SPARSP_ERR_DATA; the
+ * gradients are then not defined. dK and dV always come from one kernel
  * (SPARSP_BWD_SPLIT_KV is ignored unless there is neither plan nor cap).
  * ws: at least sparsp_attn_masked_workspace_size(shape, 1) bytes.
  */

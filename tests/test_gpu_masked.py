@@ -294,21 +294,45 @@ def test_masked_keys_do_not_reach_the_scores():
     assert (g1[1][:, :, dead] == 0).all() and (g1[2][:, :, dead] == 0).all()
 
 
-def test_malformed_rows_are_reported():
-    s = sp.make_shape(1, 2, 6, 16, 24, 64, 2, 8, 8, "bf16")
+@pytest.mark.parametrize("dims", SHAPES[:5])
+@pytest.mark.parametrize("kind,cap", [("docs", 0.0), ("frames", 9.0), (None, 9.0)])
+@pytest.mark.parametrize("how", ["index", "length", "twice"])
+def test_malformed_rows_count_as_empty(dims, kind, cap, how):
+    s = sp.make_shape(*dims, "bf16")
     g = gen(17)
     q, k, v, do = inputs(s, g)
     rp, ci, chosen = csr(s, 0.7, g)
-    mask = masks(s, "docs", g)
-    plan = sp.mask_plan(s, *mask)
-    bad = ci.clone()
-    bad[int(rp[2])] = s.nb            # row 2 (every block): its first index out of range
+    mask = masks(s, kind or "all", g)
+    plan = sp.mask_plan(s, *mask) if kind else None
+    rp, ci, chosen = rp.clone(), ci.clone(), chosen.clone()
+    if how == "index":
+        ci[int(rp[2])] = s.nb             # row 2 (every block): its first index out of range
+        bad = 2
+    elif how == "twice":
+        if s.Bt != 64:
+            pytest.skip("128-token blocks attend to a block as often as it is listed")
+        ci[int(rp[2])] = ci[int(rp[2]) + 1]
+        bad = 2
+    else:
+        rp[2] = rp[3] + 1                 # row 2 ends before it begins; row 1 (empty) then holds row 2 and a block more
+        bad = 2
+        row1 = ci[int(rp[1]):int(rp[2])].long()
+        chosen[0, 1] = False
+        if int(rp[2] - rp[1]) <= s.nb and row1.unique().numel() == row1.numel():
+            chosen[0, 1, row1] = True
+        elif int(rp[2] - rp[1]) <= s.nb and s.Bt != 64:
+            pytest.skip("row 1 lists a block twice here")
+    chosen[0, bad] = False
     st = torch.zeros(1, dtype=torch.int32, device="cuda")
-    o, lse = sp.attn_masked_fwd(s, q, k, v, rp, bad, mask=plan, status=st)
+    scale = s.d ** -0.5
+    o, lse = (torch.full_like(q, 7.0), torch.full((s.B, s.H, s.N), 7.0, device="cuda"))
+    sp.attn_masked_fwd(s, q, k, v, rp, ci, cap=cap, mask=plan, status=st, o=o, lse=lse)
     assert int(st) == sp.DATA
-    chosen = chosen.clone()
-    chosen[0, 2] = False              # it counts as empty
-    check_forward(s, o, lse, reference(s, q, k, v, chosen, mask, s.d ** -0.5, 0.0), q, k, v, s.d ** -0.5, 0.0)
+    ref = reference(s, q, k, v, chosen, mask, scale, cap)
+    check_forward(s, o, lse, ref, q, k, v, scale, cap)
+    st.zero_()                            # the backward reports it; its gradients are not defined then
+    sp.attn_masked_bwd(s, q, k, v, o, lse, do, rp, ci, cap=cap, mask=plan, status=st)
+    assert int(st) == sp.DATA
 
 
 @pytest.mark.parametrize("dims", SHAPES[:6])
