@@ -82,8 +82,8 @@ constexpr uint32_t kStats = 1024;             // LSE*log2e [128] + D [128] of a 
 constexpr int HB = 64;   // columns of a half block
 enum Bar {
   A_FULL = 0, A_EMPTY, AT_FULL, C_FULL, C_EMPTY = C_FULL + kMaxNS, SD_FULL = C_EMPTY + kMaxNS,
-  X_FULL = SD_FULL + 2,
-  X_DONE = X_FULL + 2, ACC_FULL = X_DONE + 2, ACC_EMPTY, I_FULL, I_EMPTY = I_FULL + kNI,
+  X_FULL = SD_FULL + 3,
+  X_DONE = X_FULL + 3, ACC_FULL = X_DONE + 3, ACC_EMPTY, I_FULL, I_EMPTY = I_FULL + kNI,
   TEAR = I_EMPTY + kNI, TEAR2, NBAR
 };
 // Tile geometry, shared-memory layout and TMEM map for head dimension D
@@ -109,8 +109,13 @@ struct BCfg {
   static constexpr int NBOX = D / 64;
   static constexpr uint32_t kTile = TR * D * 2;
   static constexpr int kNS = D == 64 ? 4 : 2;   // column-tile stages
-  static constexpr uint32_t kColAcc = 256, kColAcc2 = 256 + D;
-  static constexpr uint32_t kColA1 = 384, kColA2 = 384 + D / 2;
+  // MOD and d = 64: three half buffers [0, 384), so that a half's S and dP are ready when
+  // the row warps come to it (the two of the other kernels each wait, in turn, for their
+  // S and dP, the row warps and the accumulate before the next); accumulators
+  // from 384, the row tiles in [448, 512) or, in mode 3, in shared memory
+  static constexpr int NBUF = MOD_ != 0 && D == 64 ? 3 : 2;
+  static constexpr uint32_t kColAcc = 128 * NBUF, kColAcc2 = kColAcc + D;
+  static constexpr uint32_t kColA1 = NBUF == 3 ? 448 : 384, kColA2 = kColA1 + D / 2;
   static constexpr uint32_t kOffA2 = kTile, kOffStage = 2 * kTile;
   static constexpr uint32_t kStageBytes = 2 * kTile + kStats;   // a multiple of 1024: tiles stay aligned
   static constexpr uint32_t kOffBar = kOffStage + kNS * kStageBytes;
@@ -184,7 +189,8 @@ attn_bwd_tc_kernel(const __grid_constant__ CUtensorMap ta1, const __grid_constan
   constexpr bool kHasDP = MODE != 2;
   // the item's row tiles as the A operand in TMEM; mode 3 with d = 128 has no
   // TMEM left beside its two accumulators and reads them from shared memory
-  constexpr bool kRowsInTmem = MODE != 3 || D == 64;
+  constexpr bool kRowsInTmem = MODE != 3 || (D == 64 && MOD == 0);
+  constexpr uint32_t NB = C::NBUF;   // half buffers
   constexpr uint32_t kTile = C::kTile, kStageBytes = C::kStageBytes;
   constexpr int kNS = C::kNS;
   extern __shared__ uint8_t smem_raw[];
@@ -210,7 +216,7 @@ attn_bwd_tc_kernel(const __grid_constant__ CUtensorMap ta1, const __grid_constan
       mbar_init(bar(C_FULL + s), 1);
       mbar_init(bar(C_EMPTY + s), 1);
     }
-    for (int b = 0; b < 2; ++b) {
+    for (int b = 0; b < C::NBUF; ++b) {
       mbar_init(bar(SD_FULL + b), 1);
       mbar_init(bar(X_FULL + b), C::kArrivalsX);
       mbar_init(bar(X_DONE + b), 1);
@@ -425,9 +431,9 @@ attn_bwd_tc_kernel(const __grid_constant__ CUtensorMap ta1, const __grid_constan
         if (!(ok = wait_warp(bar(C_FULL + st), (c_use / kNS) & 1u, g))) break;
         const uint32_t sb = stage(st);
         for (int h = 0; h < 2; ++h) {
-          const uint32_t b = hg & 1u;
-          // buffer b holds X of half hg - 2 until that half's accumulate MMA has completed
-          if (!(ok = wait_warp(bar(X_DONE + b), ((hg >> 1) & 1u) ^ 1u, g))) break;
+          const uint32_t b = hg % NB;
+          // buffer b holds X of half hg - NB until that half's accumulate MMA has completed
+          if (!(ok = wait_warp(bar(X_DONE + b), ((hg / NB) & 1u) ^ 1u, g))) break;
           fence_after();
           // rows [64h, 64h+64) of the column tile: 64 rows x 128 B = 8 KB into each box
           const uint32_t rows_h = (uint32_t)h * (HB * 128u);
@@ -506,8 +512,8 @@ attn_bwd_tc_kernel(const __grid_constant__ CUtensorMap ta1, const __grid_constan
         const uint32_t st = c_use % kNS;
         const uint32_t b3 = stage(st) + kB3;
         for (int h = 0; h < 2; ++h) {
-          const uint32_t b = hg & 1u;
-          if (!(ok = wait_warp(bar(X_FULL + b), (hg >> 1) & 1u, g))) break;
+          const uint32_t b = hg % NB;
+          if (!(ok = wait_warp(bar(X_FULL + b), (hg / NB) & 1u, g))) break;
           if (e == 0 && h == 0 && !(ok = wait_warp(bar(ACC_EMPTY), (acc_items & 1u) ^ 1u, g))) break;
           fence_after();
           if (elect_one()) {
@@ -553,14 +559,13 @@ attn_bwd_tc_kernel(const __grid_constant__ CUtensorMap ta1, const __grid_constan
     __syncwarp();
   } else if constexpr (MOD != 0) {
     // ------------------------------------------------------------ P / dS and epilogue with a mask or a cap
-    // Sixteen warps: eight per half block (half h is always half buffer h), two per
+    // Sixteen warps: eight per half block (in turn over the half buffers), two per
     // 32 rows with 32 columns each. The chains of a cap or a mask then have three
     // other warps of the scheduler to run beside, and the code of a half stays in the
     // instruction cache. A warp writes its X over its own S (and dP) columns.
     const int hf = warp >> 3, q = (warp >> 2) & 1, rw = warp & 3, t = (int)(threadIdx.x & 127);
     const int k4 = warp >> 2;                                       // this warp among the four of its rows
     const uint32_t t_row = tmem + ((uint32_t)(rw * 32) << 16);
-    const uint32_t tS = t_row + 128u * hf + 32u * q, tD = tS + HB;   // its columns of S and dP
     const float sl2 = p.sl2;
     uint32_t it_use = 0, stages = 0, acc_items = 0, a_use = 0;
     uint4* pending = nullptr;    // output row of the previous item, written once its accumulator is full
@@ -635,7 +640,8 @@ attn_bwd_tc_kernel(const __grid_constant__ CUtensorMap ta1, const __grid_constan
       if (kRowsInTmem) {
         // the item's row tiles -> TMEM (tile hf, box q); the A region is free once the
         // last S and dP of the previous item, its second half's, have completed
-        if (stages > 0 && !(ok = wait_warp(bar(SD_FULL + 1), (stages - 1u) & 1u, g))) break;
+        const uint32_t last = 2u * stages - 1u;   // counted over the CTA
+        if (stages > 0 && !(ok = wait_warp(bar(SD_FULL + last % NB), (last / NB) & 1u, g))) break;
         if (!(ok = wait_warp(bar(A_FULL), a_use & 1u, g))) break;
         ++a_use;
         fence_after();
@@ -706,7 +712,9 @@ attn_bwd_tc_kernel(const __grid_constant__ CUtensorMap ta1, const __grid_constan
           else see = key_bits(groups, ipos, __ldg(p.mask.lo + at), __ldg(p.mask.len + at));
           has = __any_sync(0xffffffffu, see != 0u);
         }
-        if (!(ok = wait_warp(bar(SD_FULL + hf), stages & 1u, g))) break;
+        const uint32_t hg = 2u * stages + (uint32_t)hf, b = hg % NB;
+        const uint32_t tS = t_row + 128u * b + 32u * q, tD = tS + HB;   // this warp's columns of S and dP
+        if (!(ok = wait_warp(bar(SD_FULL + b), (hg / NB) & 1u, g))) break;
         fence_after();
         {
           uint32_t xk[16], xd[16];
@@ -802,7 +810,7 @@ attn_bwd_tc_kernel(const __grid_constant__ CUtensorMap ta1, const __grid_constan
         }
         wait_st();
         fence_before();
-        arrive(bar(X_FULL + hf));
+        arrive(bar(X_FULL + b));
       }
       if (!ok) break;
       release();
