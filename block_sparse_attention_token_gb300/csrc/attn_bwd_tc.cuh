@@ -62,6 +62,11 @@
 // (modes 0 and 3): dS gains the factor 1 - tanh^2, and tanh is the forward's
 // (cap.cuh). The producer tells with the item which of its blocks the token mask
 // cuts; there P is cleared by the bits of the columns a row sees.
+// dQ sums dS K over a row in which dS sums to zero, so that the part all keys share
+// cancels and the rounding of dS to one bf16 weighs more than in dK and dV (relative
+// error 2.5e-3, of it 1.7e-3 the rounding of the result, against 2.35e-3): mode 0 keeps
+// dS as two bf16 parts and accumulates both (1.7e-3; 4% of the backward's time with
+// d = 64, 10% with d = 128). P and dS of mode 3 are one bf16, as in the forward.
 #pragma once
 #include <type_traits>
 
@@ -537,6 +542,11 @@ attn_bwd_tc_kernel(const __grid_constant__ CUtensorMap ta1, const __grid_constan
                 mma_ts(tmem + C::kColAcc, tmem + 128u * b + xcol(kk),
                        smem_desc(b3 + (uint32_t)(4 * h + kk) * 2048u, kBox, 1024, kSwizzle128B), idAcc,
                        acc | (kk > 0 ? 1u : 0u));
+              if (MOD != 0)   // the second part of dS
+#pragma unroll
+                for (int kk = 0; kk < HB / 16; ++kk)
+                  mma_ts(tmem + C::kColAcc, tmem + 128u * b + 16u + xcol(kk),
+                         smem_desc(b3 + (uint32_t)(4 * h + kk) * 2048u, kBox, 1024, kSwizzle128B), idAcc, 1u);
             }
             commit(bar(X_DONE + b));
             if (h == 1) commit(bar(C_EMPTY + st));   // last reader of this stage
@@ -779,9 +789,15 @@ attn_bwd_tc_kernel(const __grid_constant__ CUtensorMap ta1, const __grid_constan
                 xk[2 * x4 + 1] = pack2(pr[2], pr[3]);
                 xd[2 * x4] = pack2(ds[0], ds[1]);
                 xd[2 * x4 + 1] = pack2(ds[2], ds[3]);
-              } else {
-                xk[2 * x4] = pack2(ds[0], ds[1]);
-                xk[2 * x4 + 1] = pack2(ds[2], ds[3]);
+              } else {   // dS as the sum of two bf16
+#pragma unroll
+                for (int u = 0; u < 4; u += 2) {
+                  const uint32_t h = pack2(ds[u], ds[u + 1]);
+                  xk[2 * x4 + u / 2] = h;
+                  float r0, r1;
+                  sub_x2(ds[u], ds[u + 1], __uint_as_float(h << 16), __uint_as_float(h & 0xffff0000u), r0, r1);
+                  xd[2 * x4 + u / 2] = pack2(r0, r1);
+                }
               }
             }
           };
@@ -806,7 +822,7 @@ attn_bwd_tc_kernel(const __grid_constant__ CUtensorMap ta1, const __grid_constan
           }
           }
           tmem_st16(tS, xk);                  // over S columns read before
-          if (MODE == 3) tmem_st16(tD, xd);   // dS^T over dP^T
+          tmem_st16(MODE == 3 ? tD : tS + 16u, xd);   // dS^T over dP^T; the second part of dS beside the first
         }
         wait_st();
         fence_before();
