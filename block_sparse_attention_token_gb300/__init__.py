@@ -187,6 +187,15 @@ def _empty(n_bytes: int, device) -> torch.Tensor:
     return torch.empty(max(int(n_bytes), 16), dtype=torch.uint8, device=device)
 
 
+def _held(stream, *made):
+    """Tensors a call allocated on the current stream and uses on another: their
+    memory is not given away before that stream is done with them."""
+    if stream is not None:
+        for t in made:
+            if t is not None:
+                t.record_stream(stream)
+
+
 def _refuse(name: str, t, what: str):
     got = None if t is None else (tuple(t.shape), t.dtype, str(t.device), t.stride())
     raise ValueError(f"{name}: expected {what} on the current CUDA device, got {got}")
@@ -239,18 +248,20 @@ def norm_fwd(shape: Shape, x, w=None, b=None, eps: float = 1e-6, rms: bool = Fal
     dt, f32, dev = shape.torch_dtype, torch.float32, torch.cuda.current_device()
     px, xs = _token_stride(shape, "x", x, dims, dt, dev)
     cols, stat = ((dims[3],), dims[:3]) if per_head else ((dims[2] * dims[3],), dims[:2])
+    made = []
     if out is None:
-        out = torch.empty(dims, dtype=dt, device=x.device)
+        made.append(out := torch.empty(dims, dtype=dt, device=x.device))
     if rms:
         mean = None
     elif mean is None:
-        mean = torch.empty(stat, dtype=f32, device=x.device)
+        made.append(mean := torch.empty(stat, dtype=f32, device=x.device))
     if rstd is None:
-        rstd = torch.empty(stat, dtype=f32, device=x.device)
+        made.append(rstd := torch.empty(stat, dtype=f32, device=x.device))
     _check("sparsp_norm_fwd", lib().sparsp_norm_fwd(
         _sref(shape), _norm_flags(rms, per_head), px, xs, _want("w", w, cols, f32, dev, True),
         _want("b", b, cols, f32, dev, True), eps, _want("out", out, dims, dt, dev),
         _want("mean", mean, stat, f32, dev, True), _want("rstd", rstd, stat, f32, dev), _stream(stream)))
+    _held(stream, *made)
     return out, mean, rstd
 
 
@@ -262,20 +273,22 @@ def norm_bwd(shape: Shape, dy, x, w, mean, rstd, rms: bool = False, per_head: bo
     dt, f32, dev = shape.torch_dtype, torch.float32, torch.cuda.current_device()
     px, xs = _token_stride(shape, "x", x, dims, dt, dev)
     cols, stat = ((dims[3],), dims[:3]) if per_head else ((dims[2] * dims[3],), dims[:2])
+    made = []
     if dx is None:
-        dx = torch.empty(dims, dtype=dt, device=x.device)
+        made.append(dx := torch.empty(dims, dtype=dt, device=x.device))
     if dw is None:
-        dw = torch.empty(cols, dtype=f32, device=x.device)
+        made.append(dw := torch.empty(cols, dtype=f32, device=x.device))
     if db is None and not rms:
-        db = torch.empty(cols, dtype=f32, device=x.device)
+        made.append(db := torch.empty(cols, dtype=f32, device=x.device))
     if ws is None:
-        ws = _empty(norm_workspace_size(shape, rms, per_head), x.device)
+        made.append(ws := _empty(norm_workspace_size(shape, rms, per_head), x.device))
     pdx, dxs = _token_stride(shape, "dx", dx, dims, dt, dev)
     _check("sparsp_norm_bwd", lib().sparsp_norm_bwd(
         _sref(shape), _norm_flags(rms, per_head), _want("dy", dy, dims, dt, dev), px, xs,
         _want("w", w, cols, f32, dev, True), None if rms else _want("mean", mean, stat, f32, dev),
         _want("rstd", rstd, stat, f32, dev), pdx, dxs, _want("dw", dw, cols, f32, dev),
         _want("db", db, cols, f32, dev, True), _ptr(ws), ws.numel(), _stream(stream)))
+    _held(stream, *made)
     return dx, dw, db
 
 
@@ -306,6 +319,7 @@ def rope_table(shape: Shape, cols, theta: float = 10000.0, offset=(0.0, 0.0, 0.0
     _check("sparsp_rope_table", lib().sparsp_rope_table(
         ctypes.byref(axes), float(theta), ctypes.byref(d3(*offset)), ctypes.byref(d3(*scale)), _ptr(table),
         table.numel() * 4, _stream(stream)))
+    _held(stream, table)
     return RopeTable(axes, table)
 
 
@@ -320,7 +334,8 @@ def rope(shape: Shape, table: RopeTable, x, out=None, inverse: bool = False, in_
     s = shape
     raster, blocked = (s.B, s.N, s.H, s.d), (s.B, s.H, s.N, s.d)
     dt, dev = s.torch_dtype, torch.cuda.current_device()
-    if out is None:
+    made = out is None
+    if made:
         out = torch.empty(blocked if out_blocked else raster, dtype=dt, device=x.device)
     px, xs = ((_want("x", x, blocked, dt, dev), 0) if in_blocked else _token_stride(s, "x", x, raster, dt, dev))
     po, os_ = ((_want("out", out, blocked, dt, dev), 0) if out_blocked
@@ -331,6 +346,7 @@ def rope(shape: Shape, table: RopeTable, x, out=None, inverse: bool = False, in_
         _sref(s), ctypes.byref(table.axes), table.table.data_ptr(),
         _want("pos", pos, (s.B, s.N, 3), torch.int32, dev, True), px, xs, po, os_, flags,
         _want("means", means, (s.B, s.H, s.nb, s.d), torch.float32, dev, True), _ptr(status), _stream(stream)))
+    _held(stream, out if made else None)
     return out
 
 
@@ -640,12 +656,14 @@ def mask_plan(shape: Shape, pos, lo, hi, plan: MaskPlan | None = None, stream=No
     s, dev = shape, torch.cuda.current_device()
     pos_, lo_, hi_ = (_want(name, t, (s.B, s.N), torch.int32, dev) for name, t in
                       (("pos", pos), ("lo", lo), ("hi", hi)))
-    if plan is None:
+    made = plan is None
+    if made:
         plan = MaskPlan(_mask_dims(s), _empty(lib().sparsp_mask_plan_size(_sref(s)), pos.device))
     elif plan.dims != _mask_dims(s):
         raise ValueError(f"mask_plan: the plan is of shape {plan.dims}, not {_mask_dims(s)}")
     _check("sparsp_mask_plan", lib().sparsp_mask_plan(_sref(s), pos_, lo_, hi_, _ptr(plan.plan), plan.plan.numel(),
                                                       _stream(stream)))
+    _held(stream, plan.plan if made else None)
     return plan
 
 
@@ -697,17 +715,19 @@ def attn_masked_fwd(shape: Shape, q, k, v, row_ptr, col_idx, scale: float = 0.0,
     B, N, H, d = shape.B, shape.N, shape.H, shape.d
     raster, blocked, dt, dev = (B, N, H, d), (B, H, N, d), shape.torch_dtype, torch.cuda.current_device()
     ind, outd = raster if flags & IN_RASTER else blocked, raster if flags & OUT_RASTER else blocked
+    made = []
     if o is None:
-        o = torch.empty(outd, dtype=dt, device=q.device)
+        made.append(o := torch.empty(outd, dtype=dt, device=q.device))
     if lse is None:
-        lse = torch.empty((B, H, N), dtype=torch.float32, device=q.device)
+        made.append(lse := torch.empty((B, H, N), dtype=torch.float32, device=q.device))
     if ws is None:
-        ws = _empty(attn_masked_workspace_size(shape, False), q.device)
+        made.append(ws := _empty(attn_masked_workspace_size(shape, False), q.device))
     _check("sparsp_attn_masked_fwd", lib().sparsp_attn_masked_fwd(
         _sref(shape), _want("q", q, ind, dt, dev), _want("k", k, ind, dt, dev), _want("v", v, ind, dt, dev),
         _want("row_ptr", row_ptr, (shape.rows + 1,), torch.int32, dev), _ptr(col_idx), scale, cap,
         _plan_ptr(shape, mask), _want("o", o, outd, dt, dev), _want("lse", lse, (B, H, N), torch.float32, dev),
         _ptr(ws), ws.numel(), int(flags), _ptr(prof), _ptr(status), _stream(stream)))
+    _held(stream, *made)
     return o, lse
 
 
@@ -718,11 +738,15 @@ def attn_masked_bwd(shape: Shape, q, k, v, o, lse, dout, row_ptr, col_idx, scale
     B, N, H, d = shape.B, shape.N, shape.H, shape.d
     raster, blocked, dt, dev = (B, N, H, d), (B, H, N, d), shape.torch_dtype, torch.cuda.current_device()
     outd = raster if flags & OUT_RASTER else blocked
-    dq = torch.empty(outd, dtype=dt, device=q.device) if dq is None else dq
-    dk = torch.empty(outd, dtype=dt, device=q.device) if dk is None else dk
-    dv = torch.empty(outd, dtype=dt, device=q.device) if dv is None else dv
+    made = []
+    if dq is None:
+        made.append(dq := torch.empty(outd, dtype=dt, device=q.device))
+    if dk is None:
+        made.append(dk := torch.empty(outd, dtype=dt, device=q.device))
+    if dv is None:
+        made.append(dv := torch.empty(outd, dtype=dt, device=q.device))
     if ws is None:
-        ws = _empty(attn_masked_workspace_size(shape, True), q.device)
+        made.append(ws := _empty(attn_masked_workspace_size(shape, True), q.device))
     _check("sparsp_attn_masked_bwd", lib().sparsp_attn_masked_bwd(
         _sref(shape), _want("q", q, blocked, dt, dev), _want("k", k, blocked, dt, dev),
         _want("v", v, blocked, dt, dev), _want("o", o, outd, dt, dev),
@@ -730,6 +754,7 @@ def attn_masked_bwd(shape: Shape, q, k, v, o, lse, dout, row_ptr, col_idx, scale
         _want("row_ptr", row_ptr, (shape.rows + 1,), torch.int32, dev), _ptr(col_idx), scale, cap,
         _plan_ptr(shape, mask), _want("dq", dq, outd, dt, dev), _want("dk", dk, outd, dt, dev),
         _want("dv", dv, outd, dt, dev), _ptr(ws), ws.numel(), int(flags), _ptr(prof), _ptr(status), _stream(stream)))
+    _held(stream, *made)
     return dq, dk, dv
 
 

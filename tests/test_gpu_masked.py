@@ -369,6 +369,111 @@ def test_mask_scores(dims, kind):
     assert (k4 | ~chosen)[some].all()      # no masked pair is picked while a row has others
 
 
+# nb = 4,096 blocks: 262,144 tokens in 64-token blocks, 524,288 in 128-token ones (d = 64: rows of 64 MB and more)
+@pytest.mark.parametrize("dims", [(1, 1, 64, 64, 64, 64, 1, 8, 8), (1, 1, 64, 128, 64, 128, 2, 8, 8),
+                                  (1, 1, 64, 128, 64, 64, 2, 8, 8)])
+@pytest.mark.parametrize("cap", [0.0, 12.0])
+def test_longest_sequences(dims, cap):
+    """The largest number of blocks, on query and key blocks at both ends, at document borders and in between."""
+    s = sp.make_shape(*dims, "bf16")
+    g = gen(20)
+    q, k, v, do = inputs(s, g)
+    nb, bt = s.nb, s.Bt
+    mask = masks(s, "docs", g)
+    plan = sp.mask_plan(s, *mask)
+    # per row: the block itself, its neighbours and a few far ones; the same few are then in many lists
+    far = torch.randint(0, nb, (64,), generator=g, device="cuda")
+    own = torch.arange(nb, device="cuda")[:, None]
+    cols = torch.cat([own, (own + 1) % nb, (own * 7 + 13) % nb, far[torch.arange(nb, device="cuda")[:, None] % 64],
+                      far[(own // 64) % 64]], 1)
+    chosen = torch.zeros(nb, nb, dtype=torch.bool, device="cuda").scatter_(1, cols, True)
+    rp = torch.zeros(nb + 1, dtype=torch.int32, device="cuda")
+    rp[1:] = chosen.sum(1).cumsum(0)
+    ci = chosen.nonzero()[:, 1].int()
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    scale = s.d ** -0.5
+    o, lse = sp.attn_masked_fwd(s, q, k, v, rp, ci, scale, cap, plan, status=st)
+    grads = sp.attn_masked_bwd(s, q, k, v, o, lse, do, rp, ci, scale, cap, plan, status=st)
+    assert int(st) == 0
+    pos, lo, hi = (to_blocked(s, t)[0].view(nb, bt).long() for t in mask)
+    qb, kb, vb, ob, dob = (x.view(nb, bt, s.d).double() for x in (q, k, v, o, do))
+    lb = lse.view(nb, bt).double()
+
+    def pair(i, j):      # rows of blocks i against the keys of blocks j, in float64
+        t = scale * qb[i].flatten(0, 1) @ kb[j].flatten(0, 1).T
+        see = (lo[i].view(-1, 1) <= pos[j].view(1, -1)) & (pos[j].view(1, -1) < hi[i].view(-1, 1))
+        slope = 1.0
+        if cap > 0:
+            slope = 1 - torch.tanh(t / cap) ** 2
+            t = cap * torch.tanh(t / cap)
+        return t, see, slope
+
+    e = exp_error(s, q[:, :, :4096], k[:, :, :4096], scale, cap) * 2
+    rel = 2 * e + 2.0 ** -20 * (1 + cap)
+    for i in (0, 1, nb // 3, nb // 2 + 5, nb - 600, nb - 1):
+        j = chosen[i].nonzero()[:, 0]
+        t, see, slope = pair(torch.tensor([i], device="cuda"), j)
+        t = t.masked_fill(~see, -math.inf)
+        L = torch.logsumexp(t, -1)
+        dead = ~see.any(-1)
+        p = torch.exp(t - L[:, None]).masked_fill(~see, 0.0)
+        O, mass = p @ vb[j].flatten(0, 1), p @ vb[j].flatten(0, 1).abs()
+        close(ob[i], O, (U16 + rel) * mass * (1 + U16) + U16 * O.abs() + 1e-30, f"O {i}")
+        assert torch.isneginf(lb[i][dead]).all()
+        close(lb[i][~dead], L[~dead], rel + 4 * U32 * L[~dead].abs(), f"LSE {i}")
+        p = torch.exp(t - lb[i].masked_fill(dead, 0.0)[:, None]).masked_fill(~see, 0.0)
+        dp = dob[i] @ vb[j].flatten(0, 1).T
+        ds = p * (dp - (dob[i] * ob[i]).sum(-1, keepdim=True)) * slope
+        dq = scale * ds @ kb[j].flatten(0, 1)
+        tol = (U16 ** 2 + rel + 2.0 ** -12) * scale * ds.abs() @ kb[j].flatten(0, 1).abs()   # 2^-12: dP - D in fp32
+        close(grads[0].view(nb, bt, s.d)[i], dq, tol * (1 + U16) + U16 * dq.abs() + 1e-6, f"dQ {i}")
+    for j in (0, int(far[0]), nb // 3, nb - 1):
+        i = chosen[:, j].nonzero()[:, 0]
+        t, see, slope = pair(i, torch.tensor([j], device="cuda"))
+        Li = lb[i].flatten()[:, None]
+        p = torch.exp(t - torch.where(torch.isinf(Li), 0.0, Li)).masked_fill(~see, 0.0)
+        d_i = dob[i].flatten(0, 1)
+        dv = p.T @ d_i
+        close(grads[2].view(nb, bt, s.d)[j], dv, (U16 + rel) * (p.T @ d_i.abs()) * (1 + U16) + U16 * dv.abs() + 1e-30,
+              f"dV {j}")
+        ds = p * (d_i @ vb[j].T - (d_i * ob[i].flatten(0, 1)).sum(-1, keepdim=True)) * slope
+        dk = scale * ds.T @ qb[i].flatten(0, 1)
+        tol = (U16 + rel + 2.0 ** -12) * scale * ds.abs().T @ qb[i].flatten(0, 1).abs()
+        close(grads[1].view(nb, bt, s.d)[j], dk, tol * (1 + U16) + U16 * dk.abs() + 1e-6, f"dK {j}")
+
+
+def test_given_stream_and_a_workspace_in_turn():
+    """The stream argument (outputs and workspace made by the call), and one workspace for two captured steps that
+    run in turn."""
+    s = sp.make_shape(1, 2, 6, 16, 24, 64, 2, 8, 8, "bf16")
+    g = gen(27)
+    q, k, v, do = inputs(s, g)
+    rp, ci, _ = csr(s, 0.6, g)
+    plan = sp.mask_plan(s, *masks(s, "docs", g))
+    args = (s, q, k, v, rp, ci)
+    want = [[t.clone() for t in sp.attn_masked_fwd(*args, cap=cap, mask=plan)] for cap in (0.0, 80.0)]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    got = sp.attn_masked_fwd(*args, mask=plan, stream=side)
+    grads = sp.attn_masked_bwd(s, q, k, v, *got, do, rp, ci, mask=plan, stream=side)
+    torch.cuda.current_stream().wait_stream(side)
+    assert all(torch.equal(a, b) for a, b in zip(got, want[0]))
+    assert all(torch.isfinite(t).all() for t in grads)
+    ws = torch.empty(sp.attn_masked_workspace_size(s), dtype=torch.uint8, device="cuda")
+    graphs, outs = [], []
+    for cap in (0.0, 80.0):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            outs.append(sp.attn_masked_fwd(*args, cap=cap, mask=plan, ws=ws))
+        graphs.append(graph)
+    for _ in range(3):
+        for graph in graphs:
+            graph.replay()
+    torch.cuda.synchronize()
+    for o, w in zip(outs, want):
+        assert all(torch.equal(a, b) for a, b in zip(o, w))
+
+
 def test_other_stream_and_two_captured_graphs():
     """A call on a side stream, and two captured steps with workspaces of their own replayed in turn, give the same
     bits as eager calls; a captured step follows its inputs."""

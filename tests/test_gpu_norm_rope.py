@@ -183,6 +183,30 @@ def test_norm_special_rows():
     assert torch.isnan(y2[0, 2, 1]).all() and torch.isfinite(y2[0, 2, 0]).all()
 
 
+@pytest.mark.parametrize("per_head", [False, True])
+def test_norm_backward_with_some_gradients(per_head):
+    """dw and db are written only where asked for (through the C call: the binding always asks for dw)."""
+    import ctypes
+    s = sp.make_shape(1, 20, 4, 16, 16, 64, 4, 4, 4, "bf16")
+    g = gen(10)
+    x, dy = raster(s, g), raster(s, g).contiguous()
+    w = torch.rand(64 if per_head else 1280, generator=g, device="cuda")
+    _, mean, rstd = sp.norm_fwd(s, x, w, per_head=per_head)
+    want = sp.norm_bwd(s, dy, x, w, mean, rstd, per_head=per_head)
+    ws = torch.empty(sp.norm_workspace_size(s, per_head=per_head), dtype=torch.uint8, device="cuda")
+    stream = torch.cuda.current_stream().cuda_stream
+    for ask_w, ask_b in ((False, False), (True, False), (False, True)):
+        dx = torch.empty_like(dy)
+        dw, db = torch.full_like(w, 7.0), torch.full_like(w, 7.0)
+        code = sp.lib().sparsp_norm_bwd(
+            ctypes.byref(s), sp.NORM_HEAD if per_head else 0, dy.data_ptr(), x.data_ptr(), 0, w.data_ptr(),
+            mean.data_ptr(), rstd.data_ptr(), dx.data_ptr(), 0, dw.data_ptr() if ask_w else None,
+            db.data_ptr() if ask_b else None, ws.data_ptr() if ask_w or ask_b else None, ws.numel(), stream)
+        assert code == sp.OK and torch.equal(dx, want[0])
+        assert torch.equal(dw, want[1]) if ask_w else (dw == 7.0).all()
+        assert torch.equal(db, want[2]) if ask_b else (db == 7.0).all()
+
+
 def test_norm_no_weight_and_repeatable():
     s = sp.make_shape(2, 12, 4, 16, 16, 128, 2, 8, 8, "bf16")
     g = gen(5)
