@@ -187,17 +187,20 @@ def _empty(n_bytes: int, device) -> torch.Tensor:
     return torch.empty(max(int(n_bytes), 16), dtype=torch.uint8, device=device)
 
 
-def _held(stream, *made):
-    """Tensors a call allocated on the current stream and uses on another: their
-    memory is not given away before that stream is done with them."""
-    if stream is not None:
-        for t in made:
-            if t is not None:
-                t.record_stream(stream)
+def _new(stream, dims, dtype, device) -> torch.Tensor:
+    """A tensor that a call makes and uses on `stream`: of that stream's memory, so that
+    no earlier work on the current stream still uses it, and held for the current
+    stream, which reads it afterwards."""
+    if stream is None:
+        return torch.empty(dims, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(dims, dtype=dtype, device=device)
+    t.record_stream(torch.cuda.current_stream())
+    return t
 
 
 def _refuse(name: str, t, what: str):
-    got = None if t is None else (tuple(t.shape), t.dtype, str(t.device), t.stride())
+    got = (tuple(t.shape), t.dtype, str(t.device), t.stride()) if isinstance(t, torch.Tensor) else t
     raise ValueError(f"{name}: expected {what} on the current CUDA device, got {got}")
 
 
@@ -206,9 +209,26 @@ def _want(name: str, t, dims, dtype, dev: int, optional: bool = False):
     (the current one), of this shape and dtype. A plain address is passed through."""
     if t is None and optional or isinstance(t, int):
         return t
-    if t is None or t.shape != dims or t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous():
+    if (not isinstance(t, torch.Tensor) or t.shape != dims or t.dtype is not dtype or t.get_device() != dev
+            or not t.is_contiguous()):
         _refuse(name, t, f"a contiguous {tuple(dims)} {dtype} tensor")
     return t.data_ptr()
+
+
+def _buffer(name: str, t, dtype, dev: int, optional: bool = False):
+    """Address of a buffer of any length: contiguous, on device dev, of this dtype."""
+    if t is None and optional or isinstance(t, int):
+        return t
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous():
+        _refuse(name, t, f"a contiguous {dtype} tensor")
+    return t.data_ptr()
+
+
+def _space(ws, dev: int) -> tuple:
+    """(address, bytes) of a workspace tensor."""
+    if ws.get_device() != dev or not ws.is_contiguous():
+        _refuse("ws", ws, "a contiguous workspace")
+    return ws.data_ptr(), ws.numel() * ws.element_size()
 
 
 def _token_stride(shape: Shape, name: str, t, dims, dtype, dev: int) -> tuple:
@@ -248,20 +268,18 @@ def norm_fwd(shape: Shape, x, w=None, b=None, eps: float = 1e-6, rms: bool = Fal
     dt, f32, dev = shape.torch_dtype, torch.float32, torch.cuda.current_device()
     px, xs = _token_stride(shape, "x", x, dims, dt, dev)
     cols, stat = ((dims[3],), dims[:3]) if per_head else ((dims[2] * dims[3],), dims[:2])
-    made = []
     if out is None:
-        made.append(out := torch.empty(dims, dtype=dt, device=x.device))
+        out = _new(stream, dims, dt, x.device)
     if rms:
         mean = None
     elif mean is None:
-        made.append(mean := torch.empty(stat, dtype=f32, device=x.device))
+        mean = _new(stream, stat, f32, x.device)
     if rstd is None:
-        made.append(rstd := torch.empty(stat, dtype=f32, device=x.device))
+        rstd = _new(stream, stat, f32, x.device)
     _check("sparsp_norm_fwd", lib().sparsp_norm_fwd(
         _sref(shape), _norm_flags(rms, per_head), px, xs, _want("w", w, cols, f32, dev, True),
         _want("b", b, cols, f32, dev, True), eps, _want("out", out, dims, dt, dev),
         _want("mean", mean, stat, f32, dev, True), _want("rstd", rstd, stat, f32, dev), _stream(stream)))
-    _held(stream, *made)
     return out, mean, rstd
 
 
@@ -273,22 +291,20 @@ def norm_bwd(shape: Shape, dy, x, w, mean, rstd, rms: bool = False, per_head: bo
     dt, f32, dev = shape.torch_dtype, torch.float32, torch.cuda.current_device()
     px, xs = _token_stride(shape, "x", x, dims, dt, dev)
     cols, stat = ((dims[3],), dims[:3]) if per_head else ((dims[2] * dims[3],), dims[:2])
-    made = []
     if dx is None:
-        made.append(dx := torch.empty(dims, dtype=dt, device=x.device))
+        dx = _new(stream, dims, dt, x.device)
     if dw is None:
-        made.append(dw := torch.empty(cols, dtype=f32, device=x.device))
+        dw = _new(stream, cols, f32, x.device)
     if db is None and not rms:
-        made.append(db := torch.empty(cols, dtype=f32, device=x.device))
+        db = _new(stream, cols, f32, x.device)
     if ws is None:
-        made.append(ws := _empty(norm_workspace_size(shape, rms, per_head), x.device))
+        ws = _new(stream, max(norm_workspace_size(shape, rms, per_head), 16), torch.uint8, x.device)
     pdx, dxs = _token_stride(shape, "dx", dx, dims, dt, dev)
     _check("sparsp_norm_bwd", lib().sparsp_norm_bwd(
         _sref(shape), _norm_flags(rms, per_head), _want("dy", dy, dims, dt, dev), px, xs,
         _want("w", w, cols, f32, dev, True), None if rms else _want("mean", mean, stat, f32, dev),
         _want("rstd", rstd, stat, f32, dev), pdx, dxs, _want("dw", dw, cols, f32, dev),
-        _want("db", db, cols, f32, dev, True), _ptr(ws), ws.numel(), _stream(stream)))
-    _held(stream, *made)
+        _want("db", db, cols, f32, dev, True), *_space(ws, dev), _stream(stream)))
     return dx, dw, db
 
 
@@ -314,12 +330,11 @@ def rope_table(shape: Shape, cols, theta: float = 10000.0, offset=(0.0, 0.0, 0.0
                          f"{'paired by halves' if half else ''}")
     axes = RopeAxes((_I32 * 3)(*cols), (_I32 * 3)(*ext), int(half))
     n = lib().sparsp_rope_table_size(ctypes.byref(axes))
-    table = torch.empty(max(n // 4, 4), dtype=torch.float32, device=f"cuda:{torch.cuda.current_device()}")
+    table = _new(stream, max(n // 4, 4), torch.float32, f"cuda:{torch.cuda.current_device()}")
     d3 = ctypes.c_double * 3
     _check("sparsp_rope_table", lib().sparsp_rope_table(
         ctypes.byref(axes), float(theta), ctypes.byref(d3(*offset)), ctypes.byref(d3(*scale)), _ptr(table),
         table.numel() * 4, _stream(stream)))
-    _held(stream, table)
     return RopeTable(axes, table)
 
 
@@ -334,19 +349,18 @@ def rope(shape: Shape, table: RopeTable, x, out=None, inverse: bool = False, in_
     s = shape
     raster, blocked = (s.B, s.N, s.H, s.d), (s.B, s.H, s.N, s.d)
     dt, dev = s.torch_dtype, torch.cuda.current_device()
-    made = out is None
-    if made:
-        out = torch.empty(blocked if out_blocked else raster, dtype=dt, device=x.device)
+    if out is None:
+        out = _new(stream, blocked if out_blocked else raster, dt, x.device)
     px, xs = ((_want("x", x, blocked, dt, dev), 0) if in_blocked else _token_stride(s, "x", x, raster, dt, dev))
     po, os_ = ((_want("out", out, blocked, dt, dev), 0) if out_blocked
                else _token_stride(s, "out", out, raster, dt, dev))
     flags = ((ROPE_INVERSE if inverse else 0) | (ROPE_IN_BLOCKED if in_blocked else 0)
              | (ROPE_OUT_BLOCKED if out_blocked else 0))
     _check("sparsp_rope", lib().sparsp_rope(
-        _sref(s), ctypes.byref(table.axes), table.table.data_ptr(),
+        _sref(s), ctypes.byref(table.axes), _buffer("table", table.table, torch.float32, dev),
         _want("pos", pos, (s.B, s.N, 3), torch.int32, dev, True), px, xs, po, os_, flags,
-        _want("means", means, (s.B, s.H, s.nb, s.d), torch.float32, dev, True), _ptr(status), _stream(stream)))
-    _held(stream, out if made else None)
+        _want("means", means, (s.B, s.H, s.nb, s.d), torch.float32, dev, True),
+        _buffer("status", status, torch.int32, dev, True), _stream(stream)))
     return out
 
 
@@ -656,21 +670,20 @@ def mask_plan(shape: Shape, pos, lo, hi, plan: MaskPlan | None = None, stream=No
     s, dev = shape, torch.cuda.current_device()
     pos_, lo_, hi_ = (_want(name, t, (s.B, s.N), torch.int32, dev) for name, t in
                       (("pos", pos), ("lo", lo), ("hi", hi)))
-    made = plan is None
-    if made:
-        plan = MaskPlan(_mask_dims(s), _empty(lib().sparsp_mask_plan_size(_sref(s)), pos.device))
+    if plan is None:
+        plan = MaskPlan(_mask_dims(s), _new(stream, max(lib().sparsp_mask_plan_size(_sref(s)), 16), torch.uint8,
+                                            pos.device))
     elif plan.dims != _mask_dims(s):
         raise ValueError(f"mask_plan: the plan is of shape {plan.dims}, not {_mask_dims(s)}")
-    _check("sparsp_mask_plan", lib().sparsp_mask_plan(_sref(s), pos_, lo_, hi_, _ptr(plan.plan), plan.plan.numel(),
+    _check("sparsp_mask_plan", lib().sparsp_mask_plan(_sref(s), pos_, lo_, hi_, *_space(plan.plan, dev),
                                                       _stream(stream)))
-    _held(stream, plan.plan if made else None)
     return plan
 
 
 def document_mask(shape: Shape, ids):
     """(pos, lo, hi) of mask_plan for documents packed into one grid: ids int32
     [B, N], raster order; a token sees the tokens of its own number, and a token of a
-    negative number (padding) sees and is seen by nothing."""
+    negative number (padding) sees and is seen by nothing. Numbers are below 2^31 - 1."""
     live = ids >= 0
     pos = torch.where(live, ids, -1).int()
     return pos, torch.where(live, ids, 0).int(), torch.where(live, ids + 1, 0).int()
@@ -687,18 +700,20 @@ def frame_mask(shape: Shape, prefix: int = 0, window: int | None = None, device=
     return t.int().contiguous(), lo.int().contiguous(), (t + 1).clamp(min=prefix).int().contiguous()
 
 
-def _plan_ptr(shape: Shape, mask: MaskPlan | None):
+def _plan_ptr(shape: Shape, mask: MaskPlan | None, dev: int | None = None):
     if mask is None:
         return None
     if mask.dims != _mask_dims(shape):
         raise ValueError(f"the mask plan is of (B, T, Y, X, ta, tb, tc) {mask.dims}, not {_mask_dims(shape)}")
-    return mask.plan.data_ptr()
+    return mask.plan.data_ptr() if dev is None else _buffer("mask", mask.plan, torch.uint8, dev)
 
 
 def mask_scores(shape: Shape, mask: MaskPlan, scores, stream=None) -> torch.Tensor:
     """scores [B,H,nb,nb] in place: MASKED_SCORE for block pairs that see nothing of each other."""
-    at = _want("scores", scores, (shape.B, shape.H, shape.nb, shape.nb), torch.float32, torch.cuda.current_device())
-    _check("sparsp_mask_scores", lib().sparsp_mask_scores(_sref(shape), _plan_ptr(shape, mask), at, _stream(stream)))
+    dev = torch.cuda.current_device()
+    at = _want("scores", scores, (shape.B, shape.H, shape.nb, shape.nb), torch.float32, dev)
+    _check("sparsp_mask_scores", lib().sparsp_mask_scores(_sref(shape), _plan_ptr(shape, mask, dev), at,
+                                                          _stream(stream)))
     return scores
 
 
@@ -715,19 +730,19 @@ def attn_masked_fwd(shape: Shape, q, k, v, row_ptr, col_idx, scale: float = 0.0,
     B, N, H, d = shape.B, shape.N, shape.H, shape.d
     raster, blocked, dt, dev = (B, N, H, d), (B, H, N, d), shape.torch_dtype, torch.cuda.current_device()
     ind, outd = raster if flags & IN_RASTER else blocked, raster if flags & OUT_RASTER else blocked
-    made = []
     if o is None:
-        made.append(o := torch.empty(outd, dtype=dt, device=q.device))
+        o = _new(stream, outd, dt, q.device)
     if lse is None:
-        made.append(lse := torch.empty((B, H, N), dtype=torch.float32, device=q.device))
+        lse = _new(stream, (B, H, N), torch.float32, q.device)
     if ws is None:
-        made.append(ws := _empty(attn_masked_workspace_size(shape, False), q.device))
+        ws = _new(stream, max(attn_masked_workspace_size(shape, False), 16), torch.uint8, q.device)
     _check("sparsp_attn_masked_fwd", lib().sparsp_attn_masked_fwd(
         _sref(shape), _want("q", q, ind, dt, dev), _want("k", k, ind, dt, dev), _want("v", v, ind, dt, dev),
-        _want("row_ptr", row_ptr, (shape.rows + 1,), torch.int32, dev), _ptr(col_idx), scale, cap,
-        _plan_ptr(shape, mask), _want("o", o, outd, dt, dev), _want("lse", lse, (B, H, N), torch.float32, dev),
-        _ptr(ws), ws.numel(), int(flags), _ptr(prof), _ptr(status), _stream(stream)))
-    _held(stream, *made)
+        _want("row_ptr", row_ptr, (shape.rows + 1,), torch.int32, dev), _buffer("col_idx", col_idx, torch.int32, dev),
+        scale, cap, _plan_ptr(shape, mask, dev), _want("o", o, outd, dt, dev),
+        _want("lse", lse, (B, H, N), torch.float32, dev),
+        *_space(ws, dev), int(flags), _buffer("prof", prof, torch.int64, dev, True),
+        _buffer("status", status, torch.int32, dev, True), _stream(stream)))
     return o, lse
 
 
@@ -738,23 +753,18 @@ def attn_masked_bwd(shape: Shape, q, k, v, o, lse, dout, row_ptr, col_idx, scale
     B, N, H, d = shape.B, shape.N, shape.H, shape.d
     raster, blocked, dt, dev = (B, N, H, d), (B, H, N, d), shape.torch_dtype, torch.cuda.current_device()
     outd = raster if flags & OUT_RASTER else blocked
-    made = []
-    if dq is None:
-        made.append(dq := torch.empty(outd, dtype=dt, device=q.device))
-    if dk is None:
-        made.append(dk := torch.empty(outd, dtype=dt, device=q.device))
-    if dv is None:
-        made.append(dv := torch.empty(outd, dtype=dt, device=q.device))
+    dq, dk, dv = (_new(stream, outd, dt, q.device) if t is None else t for t in (dq, dk, dv))
     if ws is None:
-        made.append(ws := _empty(attn_masked_workspace_size(shape, True), q.device))
+        ws = _new(stream, max(attn_masked_workspace_size(shape, True), 16), torch.uint8, q.device)
     _check("sparsp_attn_masked_bwd", lib().sparsp_attn_masked_bwd(
         _sref(shape), _want("q", q, blocked, dt, dev), _want("k", k, blocked, dt, dev),
         _want("v", v, blocked, dt, dev), _want("o", o, outd, dt, dev),
         _want("lse", lse, (B, H, N), torch.float32, dev), _want("dout", dout, blocked, dt, dev),
-        _want("row_ptr", row_ptr, (shape.rows + 1,), torch.int32, dev), _ptr(col_idx), scale, cap,
-        _plan_ptr(shape, mask), _want("dq", dq, outd, dt, dev), _want("dk", dk, outd, dt, dev),
-        _want("dv", dv, outd, dt, dev), _ptr(ws), ws.numel(), int(flags), _ptr(prof), _ptr(status), _stream(stream)))
-    _held(stream, *made)
+        _want("row_ptr", row_ptr, (shape.rows + 1,), torch.int32, dev), _buffer("col_idx", col_idx, torch.int32, dev),
+        scale, cap, _plan_ptr(shape, mask, dev), _want("dq", dq, outd, dt, dev), _want("dk", dk, outd, dt, dev),
+        _want("dv", dv, outd, dt, dev), *_space(ws, dev), int(flags),
+        _buffer("prof", prof, torch.int64, dev, True), _buffer("status", status, torch.int32, dev, True),
+        _stream(stream)))
     return dq, dk, dv
 
 

@@ -153,8 +153,8 @@ bool cap_ok(float cap, float scale, int d) {
 }
 
 // Is it worth dropping the block pairs that see nothing of each other before the
-// work is ordered? The three launches cost about 14 us (1,024 tokens, 2 heads:
-// forward 46 us with them, 32 us without), a stage of the attention kernel that
+// work is ordered? The three launches cost about 10 us (1,024 tokens, 2 heads:
+// forward 44 us with them, 35 us without), a stage of the attention kernel that
 // turns out empty about 0.9 us: not where the busiest SM has few stages at all.
 bool drops_unseen(const Dims& s, int items_per_head) {
   const int sms = device_sm_count();

@@ -182,6 +182,7 @@ struct Params {
   // MOD == 2: 2 scale log2(e) / cap, cap log2(e) and scale / cap
   float c1, cap2, inv_cap;
   NearCap near;
+  int exp_cap;        // cap <= kExpCap
 };
 
 template <int MODE, int D, int BTB, int MOD>
@@ -736,7 +737,7 @@ attn_bwd_tc_kernel(const __grid_constant__ CUtensorMap ta1, const __grid_constan
           tmem_ld32(tS, sv);
           tmem_ld32(tD, dv);
           wait_ld();
-          auto operands = [&](auto form_c, auto cut_c) {   // form of the cap: none, near, within, any
+          auto operands = [&](auto form_c, auto cut_c) {   // form of the cap: none, near, within, any, any and large
             constexpr int FORM = decltype(form_c)::value;
             constexpr bool CUT = decltype(cut_c)::value;
 #pragma unroll
@@ -767,12 +768,18 @@ attn_bwd_tc_kernel(const __grid_constant__ CUtensorMap ta1, const __grid_constan
                   tanh_poly_x2(s0, s1, p.inv_cap, t0, t1);
                   fma_x2(t0, t1, p.cap2, -l2[u], -l2[u + 1], e0, e1);
                   fma2_x2(t0, t1, -t0, -t1, 1.f, c0, c1);
-                } else {
+                } else if constexpr (FORM == 3) {
                   const float r0 = rcpf(1.f + ex2f(s0 * p.c1)), r1 = rcpf(1.f + ex2f(s1 * p.c1));
                   e0 = fmaf(r0, -2.f * p.cap2, p.cap2) - l2[u];
                   e1 = fmaf(r1, -2.f * p.cap2, p.cap2) - l2[u + 1];
                   c0 = 4.f * r0 * (1.f - r0);
                   c1 = 4.f * r1 * (1.f - r1);
+                } else {
+                  t0 = tanh_any(s0 * p.inv_cap, s0 * p.c1);
+                  t1 = tanh_any(s1 * p.inv_cap, s1 * p.c1);
+                  fma_x2(t0, t1, p.cap2, -l2[u], -l2[u + 1], e0, e1);
+                  c0 = fmaf(-t0, t0, 1.f);   // near 1 - t0^2 = 0 off by 2^-23 in absolute terms
+                  c1 = fmaf(-t1, t1, 1.f);
                 }
                 pr[u] = ex2f(e0);
                 pr[u + 1] = ex2f(e1);
@@ -816,8 +823,10 @@ attn_bwd_tc_kernel(const __grid_constant__ CUtensorMap ta1, const __grid_constan
               else operands(integral_constant<int, 1>{}, std::false_type{});
             } else if (__all_sync(0xffffffffu, most * p.inv_cap <= 1.f)) {
               operands(integral_constant<int, 2>{}, std::true_type{});
-            } else {
+            } else if (p.exp_cap) {
               operands(integral_constant<int, 3>{}, std::true_type{});
+            } else {
+              operands(integral_constant<int, 4>{}, std::true_type{});
             }
           }
           }
@@ -1130,7 +1139,7 @@ sparsp_status_t launch_bwd_mod(const Dims& s, int mode, const __nv_bfloat16* q,
              mode == 2 ? 1.0f : scale, lse2, delta, out, out2, 1.0f, items, counter, prof, d_status,
              raster ? 1 : 0, raster_map(s), mask, MOD == 2 ? 2.f * scale * 1.4426950408889634f / cap : 0.f,
              cap * 1.4426950408889634f, MOD == 2 ? scale / cap : 0.f,
-             MOD == 2 ? near_cap_backward(scale, cap) : NearCap{}};
+             MOD == 2 ? near_cap_backward(scale, cap) : NearCap{}, cap <= kExpCap};
   if (s.Bt == 64) {
     if (s.d == 64) return launch_d<64, 64, MOD>(mode, m, s, prm, st);
     return launch_d<128, 64, MOD>(mode, m, s, prm, st);

@@ -158,9 +158,10 @@ struct Cfg {
 constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr uint64_t kDrainNs = 200000000ull;
 constexpr float kRescaleThreshold = 8.0f;   // log2 units
-// Up to this cap one reference c0 = cap log2(e) - 20 holds every score: P lies in
-// [2^-124.3, 2^20], so that sums of 2^19 terms and values up to 2^88 fit fp32.
-constexpr float kFixedCap = 50.0f;
+// Up to this cap one reference c0 = max(0, cap log2(e) - 20) holds every score: P lies
+// in [2^-37.8, 2^20], so that sums of 2^19 terms and their products with values from
+// 2^-88 to 2^88 stay normal fp32 numbers. Beyond it c0 = 0 and the rows are checked.
+constexpr float kFixedCap = 20.0f;
 
 __device__ __forceinline__ bool wait_raw(uint32_t bar, uint32_t parity, uint64_t limit) {
   const uint64_t t0 = globaltimer_ns();
@@ -222,6 +223,7 @@ struct Params {
   // MOD 2, 3: 2 scale log2(e) / cap, cap log2(e) and scale / cap
   float c1, cap2, inv_cap;
   NearCap near;
+  int exp_cap;           // cap <= kExpCap
   float c0;              // FAST: reference of every row, log2 units
   int32_t* fix_items;    // FAST: items for the general kernel, or null; the general kernel: its items
   int32_t* fix_count;
@@ -649,9 +651,9 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
     // ------------------------------------------------------------ softmax + epilogue with a mask or a cap
     // No running maximum: P = exp2(y - c0) with one constant c0 for every row. With a
     // cap of at most kFixedCap the scores cannot leave the range of that; else
-    // c0 = 0 and an item with a row whose sum left [2^-80, 2^80], or whose O is not
+    // c0 = 0 and an item with a row whose sum left [2^-60, 2^80], or whose O is not
     // finite, goes on the list of items that the general kernel does after this
-    // one (scores of more than some 55 in magnitude: a softmax that is one key).
+    // one (scores of more than 55, or all below -42: a softmax that is one key).
     // So stages do not depend on one another and nothing is rescaled. Two groups of
     // eight warps take the stages in turn (group g those of S and P buffer g),
     // two warps per 32 rows with 64 columns each, so that the waits and loads of some
@@ -752,7 +754,7 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
           tmem_ld32(tS + 32u * c, s);
           wait_ld();
           any |= w;
-          auto probs = [&](auto form_c, auto cut_c) {   // form of the cap: near, within, any, none
+          auto probs = [&](auto form_c, auto cut_c) {   // form of the cap: near, within, any, none, any and large
             constexpr int FORM = decltype(form_c)::value;
             constexpr bool CUT = decltype(cut_c)::value;
 #pragma unroll
@@ -767,6 +769,9 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
               } else if constexpr (FORM == 2) {
                 y0 = cap_exp(s0 * p.c1, p.cap2) - p.c0;
                 y1 = cap_exp(s1 * p.c1, p.cap2) - p.c0;
+              } else if constexpr (FORM == 4) {
+                y0 = fmaf(tanh_any(s0 * p.inv_cap, s0 * p.c1), p.cap2, -p.c0);
+                y1 = fmaf(tanh_any(s1 * p.inv_cap, s1 * p.c1), p.cap2, -p.c0);
               } else {
                 mul_x2(s0, s1, p.scale_log2, p.scale_log2, y0, y1);
               }
@@ -796,8 +801,10 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
               else probs(integral_constant<int, 0>{}, std::false_type{});
             } else if (__all_sync(0xffffffffu, most * p.inv_cap <= 1.f)) {
               probs(integral_constant<int, 1>{}, std::true_type{});
-            } else {
+            } else if (p.exp_cap) {
               probs(integral_constant<int, 2>{}, std::true_type{});
+            } else {
+              probs(integral_constant<int, 4>{}, std::true_type{});
             }
           }
           tmem_st16(tP + 16u * c, pk);
@@ -828,7 +835,7 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
       fence_after();
       const float inv = l > 0.f ? 1.0f / l : 0.f;   // 0: the row saw no key
       // (NaN compares false: such a row goes to the general kernel as well)
-      bool good = p.fix_items == nullptr || l == 0.f || (l > 8.3e-25f && l < 1.2e24f);
+      bool good = p.fix_items == nullptr || l == 0.f || (l > 8.7e-19f && l < 1.2e24f);
 #pragma unroll 1
       for (int c = 0; c < D / 64; ++c) {
         uint32_t ov[32];
@@ -1005,7 +1012,7 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
             }
             const float mx = fmaxf(mw[0], mw[1]);
             if (MOD != 3) return mx * sl2;
-            return mx == -INFINITY ? mx : cap_exp(mx * p.c1, p.cap2);
+            return mx == -INFINITY ? mx : tanh_any(mx * p.inv_cap, mx * p.c1) * p.cap2;
           };
           bool known = false, resc = false;
           float f = 1.f;
@@ -1041,8 +1048,8 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
               if constexpr (MOD != 3) {
                 fma_x2(s0, s1, sl2, -mr, x0, x1);
               } else {   // the cap would bring a masked score back
-                x0 = s0 == -INFINITY ? s0 : cap_exp(s0 * p.c1, p.cap2) - mr;
-                x1 = s1 == -INFINITY ? s1 : cap_exp(s1 * p.c1, p.cap2) - mr;
+                x0 = s0 == -INFINITY ? s0 : fmaf(tanh_any(s0 * p.inv_cap, s0 * p.c1), p.cap2, -mr);
+                x1 = s1 == -INFINITY ? s1 : fmaf(tanh_any(s1 * p.inv_cap, s1 * p.c1), p.cap2, -mr);
               }
               const float p0 = ex2f(x0), p1 = ex2f(x1);
               add_x2(sum[c & 1].x, sum[c & 1].y, p0, p1);
@@ -1321,7 +1328,7 @@ sparsp_status_t launch_fwd_mod(const Dims& s, const __nv_bfloat16* q, const __nv
              raster ? 1 : 0, raster_map(s), in_raster ? 1 : 0, raster_box(s), items, counter, prof, d_status,
              mask, MOD == 2 || MOD == 3 ? 2.f * scale * kLog2e / cap : 0.f, cap * kLog2e,
              MOD == 2 || MOD == 3 ? scale / cap : 0.f,
-             MOD == 2 ? near_cap(scale, cap) : NearCap{},
+             MOD == 2 ? near_cap(scale, cap) : NearCap{}, cap <= kExpCap,
              MOD == 2 && cap <= kFixedCap ? fmaxf(cap * kLog2e - 20.f, 0.f) : 0.f, fix.items, fix.count, fix.mark};
   if (s.Bt == 128 && s.d == 128) return go_fwd<128, 128, MOD>(s, tq, tk, tv, prm, st);
   if (s.Bt == 128 && s.d == 64) return go_fwd<128, 64, MOD>(s, tq, tk, tv, prm, st);

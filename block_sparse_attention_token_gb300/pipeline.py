@@ -63,10 +63,10 @@ class Pipeline:
         # projection, two score products, gradient products, loss (partials, sum), weight gradients
         pred = 7 if self.predictor_lr is not None else 0
         # norm of Q and K; with raster inputs the rotation is a pass of its own; masked scores, the masked CSR (count,
-        # scan, fill), and the general attention kernel over what the first one passes on
+        # scan, fill; left out for small shapes), and the general attention kernel over what the first one passes on
         extra = (2 if self.norm is not None else 0) + (2 if self.rope is not None and self.raster_in else 0)
         extra += (4 if self.mask is not None else 0)
-        extra += 1 if (self.mask is not None and not self.cap) or self.cap > 50 else 0
+        extra += 1 if (self.mask is not None and not self.cap) or self.cap > 20 else 0
         return 3 + scores + pred + 3 + bal + place + 4 + gather + lpt + 1 + (0 if self.raster_out else 1) + extra
 
     def kernels_per_backward(self) -> int:
@@ -267,7 +267,7 @@ class Pipeline:
             return blocked
 
         n, st = self.norm or QKNorm(), self.norm_stats if self.norm is not None else (None, None)
-        self._qk_in = (q, k)
+        self._qk_in = (q, k) if self.norm is not None else None
         aq = prepared("q", q, self.qn, st[0], n.q_weight, n.q_bias, self.qr, self.qb, self.qmeans)
         ak = prepared("k", k, self.kn, st[1], n.k_weight, n.k_bias, self.kr, self.kb, self.kmeans)
         if not self.raster_in:

@@ -31,7 +31,9 @@
  *    cache of the SM count and of the tensor-map encoder entry point.
  *    Calls are thread-safe.
  *  - Work is enqueued on `stream` (a cudaStream_t; NULL = legacy default).
- *  - All device pointers must be 16-byte aligned; tensors are contiguous.
+ *  - All device pointers must be 16-byte aligned; tensors are contiguous, but
+ *    for the raster tensors of sparsp_norm_* and sparsp_rope that take a stride
+ *    between tokens.
  *  - Shapes: d in {64, 128}; Bt = ta*tb*tc in {64, 128}; nb = N/Bt <= 4096
  *    (524,288 tokens in 128-token blocks) and B*H*nb*nb < 2^31 (int32 CSR
  *    offsets); dtype SPARSP_F32 or SPARSP_BF16 (bf16 inputs accumulate in
@@ -478,7 +480,8 @@ SPARSP_API sparsp_status_t sparsp_csr_transpose(const sparsp_shape_t* shape, con
  * w, b: float32 [C] or NULL (1 and 0). mean, rstd: float32 [B,N] ([B,N,H] with
  * HEAD) or NULL; RMS does not write mean. eps >= 0. Statistics and products
  * are fp32, y is rounded once. Strides are multiples of 16 bytes, at least
- * H*d. C <= 16384 (else SPARSP_ERR_UNSUPPORTED). y and x must not overlap.
+ * H*d. C <= 16384 (else SPARSP_ERR_UNSUPPORTED). The byte ranges of y and x,
+ * from their first value to their last, must not overlap.
  */
 enum {
   SPARSP_NORM_RMS = 1u << 0,
@@ -494,7 +497,7 @@ SPARSP_API sparsp_status_t sparsp_norm_fwd(const sparsp_shape_t* shape, uint32_t
  *   dw = sum over rows of dy xh,  db = sum over rows of dy.
  * dy: contiguous [B,N,H,d]; dx: [B,N,H,d] with dx_stride elements between
  * tokens (values between its tokens are left as they were); dw, db: float32 [C]
- * or NULL. dx must not overlap dy or x. ws: at least
+ * or NULL. The byte range of dx must not overlap that of dy or x. ws: at least
  * sparsp_norm_workspace_size(shape, flags) bytes when dw or db is given.
  * Sums over rows run in a fixed order: results are bitwise reproducible.
  */
@@ -537,7 +540,7 @@ SPARSP_API sparsp_status_t sparsp_rope_table(const sparsp_rope_t* rope, double t
  *            [0, extent) sets SPARSP_ERR_DATA; that axis' pairs are then not turned.
  *   means    NULL, or float32 [B,H,nb,d]: the tile means of the turned values before
  *            rounding, for sparsp_block_scores_pooled.
- * Products are fp32 and rounded once. in and out must not overlap.
+ * Products are fp32 and rounded once. The byte ranges of in and out must not overlap.
  */
 enum {
   SPARSP_ROPE_INVERSE = 1u << 0,
@@ -583,7 +586,8 @@ SPARSP_API sparsp_status_t sparsp_mask_scores(const sparsp_shape_t* shape, const
  * sees no key gives O = 0, LSE = -inf. Block pairs that see nothing of each other
  * are dropped before the work is ordered (unless the shape is so small that
  * this would cost more). Values in keys that a query does not see must be finite
- * (their weight is 0, and 0 times infinity is not). A malformed row (an index
+ * (their weight is 0, and 0 times infinity is not); with a cap of up to 20, |v| below
+ * 2^88. A malformed row (an index
  * outside [0, nb), more than nb entries; with 64-token blocks an index given
  * twice) sets SPARSP_ERR_DATA and counts as empty.
  * bf16 on the tcgen05 kernels (Bt and d in {64, 128}, nb <= 1024 when Bt = 64

@@ -276,6 +276,56 @@ def test_extreme_scores(dims, cap):
         check_backward(s, grads, ref, lse, o, do, q, k, v, 1.0, cap)
 
 
+@pytest.mark.parametrize("dims", SHAPES[:5])
+@pytest.mark.parametrize("cap", [0.0, 18.0, 20.0, 21.0, 50.0, 200.0])
+def test_scores_all_low_and_small_values(dims, cap):
+    """Every score of some rows is at -cap (or far below zero), of others at +cap, and the values are small or large:
+    the probabilities keep their precision whatever the reference of the exponentials."""
+    s = sp.make_shape(*dims, "bf16")
+    g = gen(31)
+    mask = masks(s, "docs", g)
+    plan = sp.mask_plan(s, *mask)
+    rp, ci, chosen = csr(s, 0.7, g)
+    q, k, v, do = inputs(s, g)
+    k = k.abs()
+    q[:, :, 1::3], q[:, :, 2::3] = -q[:, :, 1::3].abs(), q[:, :, 2::3].abs()
+    for small in (1e-9, 1e9):
+        o, lse = sp.attn_masked_fwd(s, q, k, (v * small).bfloat16(), rp, ci, 1.0, cap, plan)
+        v_ = (v * small).bfloat16()
+        ref = reference(s, q, k, v_, chosen, mask, 1.0, cap)
+        check_forward(s, o, lse, ref, q, k, v_, 1.0, cap)
+        grads = sp.attn_masked_bwd(s, q, k, v_, o, lse, do, rp, ci, 1.0, cap, plan)
+        check_backward(s, grads, ref, lse, o, do, q, k, v_, 1.0, cap)
+
+
+@pytest.mark.parametrize("dims", SHAPES[:5])
+@pytest.mark.parametrize("cap", [2048.0, 2.0 ** 20])
+@pytest.mark.parametrize("level", [8.0, 600.0])
+def test_large_caps_keep_the_scores(dims, cap, level):
+    """Under a cap that scores do not come near, they lose no more than the products' own rounding: here all of them
+    are about `level` with differences of a few units, in the range of the kernel without a maximum and out of it. The
+    cap adds to the exponent's error 2^-20 of the largest score, a polynomial's relative error, not 2^-20 of the cap."""
+    s = sp.make_shape(*dims, "bf16")
+    g = gen(32)
+    mask = masks(s, "docs", g)
+    plan = sp.mask_plan(s, *mask)
+    rp, ci, chosen = csr(s, 0.7, g)
+    q, k, v, do = inputs(s, g)
+    q, k = q * 0.25, k * 0.25
+    q[..., 0], k[..., 0] = math.sqrt(level), math.sqrt(level)
+    o, lse = sp.attn_masked_fwd(s, q, k, v, rp, ci, 1.0, cap, plan)
+    ref = reference(s, q, k, v, chosen, mask, 1.0, cap)
+    top = 2.0 * level                         # in place of the cap: exp_error's cap term
+    assert float(ref[0].masked_fill(~ref[1], 0.0).abs().amax()) < top
+    e = exp_error(s, q, k, 1.0, top)
+    rel = 2 * e + 2.0 ** -20
+    close(o, ref[4], (U16 + rel) * (ref[3] @ v.double().abs()) * (1 + U16) + U16 * ref[4].abs() + 1e-30, "O")
+    live = ref[1].any(-1)
+    close(lse[live], ref[5][live], rel + 4 * U32 * ref[5][live].abs(), "LSE")
+    grads = sp.attn_masked_bwd(s, q, k, v, o, lse, do, rp, ci, 1.0, cap, plan)
+    check_backward(s, grads, ref, lse, o, do, q, k, v, 1.0, top)
+
+
 def test_masked_keys_do_not_reach_the_scores():
     """A key that nobody sees may hold any finite values: the largest bf16 changes nothing."""
     s = sp.make_shape(1, 2, 6, 16, 24, 64, 2, 8, 8, "bf16")

@@ -99,3 +99,24 @@ def test_binding_refuses_another_shapes_plan():
     with pytest.raises(ValueError):
         sp._plan_ptr(other, plan)
     assert sp._plan_ptr(s, None) is None
+
+
+def test_the_binding_refuses_other_devices_and_types(lib):
+    """Every tensor of the calls is checked before the library sees it: a table, a plan, indices, a workspace or a
+    status word on another device than the current one."""
+    import torch
+    cpu = {"device": "cpu"}
+    with pytest.raises(ValueError, match="ws"):
+        sp._space(torch.empty(64, dtype=torch.uint8), 0)
+    with pytest.raises(ValueError, match="col_idx"):
+        sp._buffer("col_idx", torch.empty(4, dtype=torch.int64, **cpu), torch.int32, -1)
+    with pytest.raises(ValueError, match="col_idx"):
+        sp._buffer("col_idx", torch.empty(4, dtype=torch.int32, **cpu), torch.int32, 0)
+    with pytest.raises(ValueError, match="col_idx"):
+        sp._buffer("col_idx", torch.empty(4, 4, dtype=torch.int32, **cpu).t()[:2], torch.int32, -1)
+    with pytest.raises(ValueError, match="col_idx"):
+        sp._buffer("col_idx", None, torch.int32, 0)
+    assert sp._buffer("status", None, torch.int32, 0, True) is None
+    assert sp._buffer("status", FAKE, torch.int32, 0, True) == FAKE
+    with pytest.raises(ValueError, match="expected"):
+        sp._want("w", "text", (4,), torch.float32, 0)
