@@ -111,8 +111,11 @@ struct Cfg {
   // thread; the softmax warps rise to 200 and the other four drop to 56
   // (4 x 32 x 200 + 4 x 32 x 56 = 256 x 128)
   static constexpr int NIDLE = DUO ? 2 : 0;
-  static constexpr int THREADS = 32 * (NSM + 1 + NIS + NIDLE);   // + producer, issuer(s), idle
-  static constexpr int W_PROD = NSM, W_S = NSM + 1, W_PV = NSM + NIS;
+  // FAST: the loads have a warp of their own, so that the producer prepares the next
+  // item's lists and masks meanwhile
+  static constexpr int NLD = FAST ? 1 : 0;
+  static constexpr int THREADS = 32 * (NSM + 1 + NIS + NIDLE + NLD);   // + producer, issuer(s), idle, loader
+  static constexpr int W_PROD = NSM, W_S = NSM + 1, W_PV = NSM + NIS, W_LOAD = W_PV + NIDLE + 1;
   static constexpr uint32_t kRegSoftmax = 200, kRegAux = 56;
   static_assert(!DUO || (THREADS == 256 && NSM == 4 && 128 * (kRegSoftmax + kRegAux) == 256 * 128),
                 "register split of the two warpgroups");
@@ -275,7 +278,7 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
     mbar_init(bar(O_EMPTY), C::kArrivals);
     for (int r = 0; r < kNI; ++r) {
       mbar_init(bar(I_FULL + r), 1);
-      mbar_init(bar(I_EMPTY + r), C::NSM + C::NIS);
+      mbar_init(bar(I_EMPTY + r), C::NSM + C::NIS + C::NLD);
     }
     mbar_init(bar(TEAR), 1);
     mbar_init(bar(TEAR_PV), 1);
@@ -383,7 +386,7 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
       __syncwarp();
       ++it_fill;
       if (len == -2) break;
-      if (len <= 0) continue;
+      if (C::FAST || len <= 0) continue;
       const int64_t bh = item / nbp;
       const int i0 = PAIR ? 2 * (item % nbp) : item % nb;   // first query block of the item
       int32_t yq = (int32_t)(bh * p.N + (int64_t)i0 * BT);
@@ -475,6 +478,143 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
       for (uint32_t s = 0; s < C::NV; ++s)
         if (v_fill > s) wait_raw(bar(V_FULL + s), ((v_fill - 1 - s) / C::NV) & 1u, kDrainNs);
     }
+  } else if (C::FAST && warp == C::W_LOAD) {
+    // ------------------------------------------------------------ loader (FAST)
+    // K of the next stage, then V of the stage before it (and with an item's first V its
+    // Q), so that S is not held up by V's ring. The instructions of a stage are what
+    // bounds this warp (beside the softmax warps' loops they are seldom in the instruction
+    // cache): one thread, no collective steps, one copy per block, running parities, the
+    // next block's index read a stage early.
+    if (lane == 0) {
+      struct Stage {
+        int32_t r1, r2;      // its blocks' first rows, or the blocks with raster inputs
+        int32_t bh;
+        int32_t first;       // its item's first query block where it is the first stage, else -1
+        int32_t slot;        // its item's ring slot where it is the last stage, else -1
+      };
+      Stage now{0, 0, 0, -1, -1};   // the stage whose V is still to be loaded
+      bool some = false, end = false, ok = true;
+      uint32_t ks = 0, kp = 1, vs = 0, vp = 1, qp = 1, ri = 0, ip = 0;   // ring places and parities
+      uint32_t k_fill = 0, v_fill = 0, q_fill = 0;
+      int e = 0;
+      int32_t len = 0, y0 = 0, bh = 0, i0 = 0, j_next = 0;
+      const int32_t* list = p.col_idx;
+      UnionWalk walk(bits, bits, 0);
+      const int32_t unit = p.in_raster ? 1 : BT;
+      auto rows = [&](uint32_t tile, uint32_t b, const CUtensorMap* map, const Stage& t) {   // K or V of a stage
+        mbar_arrive_expect_tx(b, C::kKTile);
+        if (p.in_raster) {
+#pragma unroll 1
+          for (int h = 0; h < C::NBOX; ++h) {
+            const uint32_t dst = tile + h * C::kKBox;
+            const int4 c1 = p.rbox.at(t.bh, t.r1);
+            tma_load_5d(dst, map, b, 64 * h, c1.x, c1.y, c1.z, c1.w);
+            if (PAIR) {
+              const int4 c2 = p.rbox.at(t.bh, t.r2);
+              tma_load_5d(dst + C::kHalfBox, map, b, 64 * h, c2.x, c2.y, c2.z, c2.w);
+            }
+          }
+        } else if (PAIR && C::NBOX == 2) {   // the two blocks' rows alternate by 64-column box
+#pragma unroll
+          for (int h = 0; h < C::NBOX; ++h) {
+            tma_load_3d(tile + h * C::kKBox, map, b, 0, t.r1, h);
+            tma_load_3d(tile + h * C::kKBox + C::kHalfBox, map, b, 0, t.r2, h);
+          }
+        } else {                             // both boxes of d = 128 in one copy
+          tma_load_3d(tile, map, b, 0, t.r1, 0);
+          if (PAIR) tma_load_3d(tile + C::kHalfBox, map, b, 0, t.r2, 0);
+        }
+      };
+      for (;;) {
+        // the next item; one that is not ready is waited for only when nothing else is left to do
+        while (e >= len && !end) {
+          const uint32_t full = bar(I_FULL + ri);
+          if (some && !mbar_test_wait(full, ip)) break;
+          if (!(ok = wait(full, ip, g))) break;
+          const int32_t item = ring[ri].x;
+          len = ring[ri].y;
+          e = 0;
+          end = len == -2;
+          if (len > 0) {
+            bh = item / nbp;
+            i0 = item - bh * nbp;
+            if (PAIR) {
+              i0 *= 2;
+              walk = UnionWalk(bits + ri * 2 * C::MAXW, bits + ri * 2 * C::MAXW + C::MAXW, words);
+            } else {
+              list = p.col_idx + p.row_ptr[item];
+              j_next = *list;
+            }
+            y0 = p.in_raster ? 0 : (int32_t)(bh * p.N);
+          } else {
+            mbar_arrive(bar(I_EMPTY + ri));
+          }
+          if (++ri == C::NI) ri = 0, ip ^= 1u;
+        }
+        if (!ok) break;
+        const bool more = e < len;
+        Stage next{0, 0, bh, -1, -1};
+        if (more) {
+          int32_t j1, j2;
+          if constexpr (PAIR) {
+            j1 = walk.next();
+            j2 = walk.next();
+            if (j2 < 0) j2 = j1;   // a lone last block: loaded twice, its second half masked
+          } else {
+            j1 = j2 = j_next;
+            if (e + 1 < len) j_next = list[e + 1];
+          }
+          if (!dcheck(j1 >= 0 && j1 < nb && j2 >= 0 && j2 < nb, p.d_status)) j1 = j2 = 0;
+          next.r1 = y0 + j1 * unit;
+          next.r2 = y0 + j2 * unit;
+          if (e == 0) next.first = i0;
+          if (++e == len) next.slot = (int32_t)(ri == 0 ? C::NI - 1 : ri - 1);
+          if (!(ok = wait(bar(K_EMPTY + ks), kp, g))) break;
+          rows(sK + ks * C::kKTile, bar(K_FULL + ks), &tk, next);
+          ++k_fill;
+          if (++ks == C::NK) ks = 0, kp ^= 1u;
+        } else if (!some && end) {
+          break;
+        }
+        if (some) {
+          if (now.first >= 0) {
+            if (!(ok = wait(bar(Q_EMPTY), qp, g))) break;
+            mbar_arrive_expect_tx(bar(Q_FULL), C::kQTile);
+            if (p.in_raster) {   // the item's block(s), one 5-D box each
+#pragma unroll 1
+              for (int h = 0; h < C::NBOX; ++h) {
+                const int4 c = p.rbox.at(now.bh, now.first);
+                tma_load_5d(sQ + h * C::kQBox, &tq, bar(Q_FULL), 64 * h, c.x, c.y, c.z, c.w);
+                if (PAIR) {   // a head's last pair of an odd nb loads its first block twice (never stored)
+                  const int4 c2 = p.rbox.at(now.bh, now.first + 1 < nb ? now.first + 1 : now.first);
+                  tma_load_5d(sQ + h * C::kQBox + C::kHalfBox, &tq, bar(Q_FULL), 64 * h, c2.x, c2.y, c2.z, c2.w);
+                }
+              }
+            } else {
+              tma_load_3d(sQ, &tq, bar(Q_FULL), 0, (int32_t)(now.bh * p.N) + now.first * BT, 0);
+            }
+            qp ^= 1u;
+            ++q_fill;
+          }
+          if (!(ok = wait(bar(V_EMPTY + vs), vp, g))) break;
+          rows(sV + vs * C::kKTile, bar(V_FULL + vs), &tv, now);
+          ++v_fill;
+          if (++vs == C::NV) vs = 0, vp ^= 1u;
+          if (now.slot >= 0) mbar_arrive(bar(I_EMPTY + now.slot));   // the item's lists have been walked
+        }
+        some = more;
+        now = next;
+      }
+      if (*abort_flag) {
+        // drain copies still in flight before the shared memory goes away
+        if (q_fill) wait_raw(bar(Q_FULL), (q_fill - 1) & 1u, kDrainNs);
+        for (uint32_t s = 0; s < C::NK; ++s)
+          if (k_fill > s) wait_raw(bar(K_FULL + s), ((k_fill - 1 - s) / C::NK) & 1u, kDrainNs);
+        for (uint32_t s = 0; s < C::NV; ++s)
+          if (v_fill > s) wait_raw(bar(V_FULL + s), ((v_fill - 1 - s) / C::NV) & 1u, kDrainNs);
+      }
+    }
+    __syncwarp();
   } else if (C::DUO && warp == C::W_S) {
     // ------------------------------------------------------------ S and PV from one warp (DUO)
     // Per item: S(0), then S(e) before PV(e-1) for e = 1 .. len-1, then PV(len-1).
@@ -1314,6 +1454,12 @@ sparsp_status_t launch_fwd_mod(const Dims& s, const __nv_bfloat16* q, const __nv
   if (in_raster) {
     // raster inputs: one block per 5-D box (two boxes for a pair's query tile)
     if (!make_tmap_bf16_raster(&tq, q, s) || !make_tmap_bf16_raster(&tk, k, s) || !make_tmap_bf16_raster(&tv, v, s))
+      return SPARSP_ERR_CUDA;
+  } else if (MOD == 1 || MOD == 2) {   // the loader's: all columns of 128 query rows, or of one block
+    const uint32_t kv_boxes = s.Bt == 64 ? 1 : (uint32_t)s.d / 64;   // pairs' blocks alternate by column box
+    if (!make_tmap_bf16_boxes(&tq, q, rows, (uint64_t)s.d, 128, (uint32_t)s.d / 64) ||
+        !make_tmap_bf16_boxes(&tk, k, rows, (uint64_t)s.d, (uint32_t)s.Bt, kv_boxes) ||
+        !make_tmap_bf16_boxes(&tv, v, rows, (uint64_t)s.d, (uint32_t)s.Bt, kv_boxes))
       return SPARSP_ERR_CUDA;
   } else if (!make_tmap_bf16_rows(&tq, q, rows, (uint64_t)s.d, 128) ||   // Q boxes: the MMA's 128 rows
              !make_tmap_bf16_rows(&tk, k, rows, (uint64_t)s.d, (uint32_t)s.Bt) ||   // K, V: one block
