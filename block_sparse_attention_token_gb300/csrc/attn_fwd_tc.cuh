@@ -888,12 +888,17 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
 #pragma unroll
             for (int x = 0; x < 16; ++x) pk[x] = 0u;
             tmem_st16(tP + 16u * c, pk);
+            if (c == 1) arrive(bar(S_FREE + grp));
             continue;
           }
           uint32_t s[32];
           tmem_ld32(tS + 32u * c, s);
           wait_ld();
           any |= w;
+          if (c == 1) {   // the stage's scores are in registers: the next S may start
+            fence_before();
+            arrive(bar(S_FREE + grp));
+          }
           auto probs = [&](auto form_c, auto cut_c) {   // form of the cap: near, within, any, none, any and large
             constexpr int FORM = decltype(form_c)::value;
             constexpr bool CUT = decltype(cut_c)::value;
@@ -949,8 +954,6 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
           }
           tmem_st16(tP + 16u * c, pk);
         }
-        fence_before();
-        arrive(bar(S_FREE + grp));
         wait_st();
         fence_before();
         arrive(bar(P_FULL + grp));
