@@ -877,8 +877,15 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
           query_bits(groups, ilo, ilen, __ldg(kp), __ldg(kp + 32), lane, see0, see1);
         }
         if (!(ok = wait_warp(bar(S_FULL + grp), turn & 1u, g))) break;
-        if (turn > 0 && !(ok = wait_warp(bar(PV_DONE + grp), (turn - 1u) & 1u, g))) break;   // P buffer free again
+        // P's buffer is free when the PV of this group's last stage is done: waited for under the
+        // first exponentials, but with 64-token blocks, where a mask often leaves a warp's
+        // columns none, before them (8k clips 241 us against 257; 30k frames in 128-token
+        // blocks, capped, 6.54 ms against 5.88)
+        if (PAIR && turn > 0 && !(ok = wait_warp(bar(PV_DONE + grp), (turn - 1u) & 1u, g))) break;
         fence_after();
+        auto p_free = [&](int c) {
+          return PAIR || c > 0 || turn == 0 || wait_warp(bar(PV_DONE + grp), (turn - 1u) & 1u, g);
+        };
 #pragma unroll 1
         for (int c = 0; c < 2; ++c) {
           const uint32_t w = c == 0 ? see0 : see1;
@@ -887,6 +894,7 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
           if (!has || !__any_sync(0xffffffffu, w != 0u)) {
 #pragma unroll
             for (int x = 0; x < 16; ++x) pk[x] = 0u;
+            if (!(ok = p_free(c))) break;
             tmem_st16(tP + 16u * c, pk);
             if (c == 1) arrive(bar(S_FREE + grp));
             continue;
@@ -952,8 +960,10 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
               probs(integral_constant<int, 4>{}, std::true_type{});
             }
           }
+          if (!(ok = p_free(c))) break;
           tmem_st16(tP + 16u * c, pk);
         }
+        if (!ok) break;
         wait_st();
         fence_before();
         arrive(bar(P_FULL + grp));
