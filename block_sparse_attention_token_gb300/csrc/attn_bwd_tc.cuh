@@ -122,7 +122,13 @@ struct BCfg {
   static constexpr uint32_t kColAcc = 128 * NBUF, kColAcc2 = kColAcc + D;
   static constexpr uint32_t kColA1 = NBUF == 3 ? 448 : 384, kColA2 = kColA1 + D / 2;
   static constexpr uint32_t kOffA2 = kTile, kOffStage = 2 * kTile;
-  static constexpr uint32_t kStageBytes = 2 * kTile + kStats;   // a multiple of 1024: tiles stay aligned
+  // MOD and d = 64: the mask's part of a stage's columns, positions (mode 0) or the
+  // intervals' starts and lengths, comes with the stage (1 KB behind the statistics);
+  // read from global memory by the row warps instead, its latency is not hidden there
+  // (8k clips in 64-token blocks 760 us against 705, capped 924 against 876). With d = 128
+  // it is, behind longer MMAs (64k clips 14.6 ms against 14.9).
+  static constexpr bool STAGED = MOD_ != 0 && D == 64;
+  static constexpr uint32_t kStageBytes = 2 * kTile + kStats + (STAGED ? kStats : 0u);   // tiles stay aligned to 1024
   static constexpr uint32_t kOffBar = kOffStage + kNS * kStageBytes;
   static constexpr uint32_t kOffRing = kOffBar + 8 * NBAR;   // [kNI] int4: item, stages, bad-list bits
   // pairs: bitmap words of one list (up to 1,024 blocks with d = 128, kMaxBlocks with d = 64)
@@ -381,7 +387,14 @@ attn_bwd_tc_kernel(const __grid_constant__ CUtensorMap ta1, const __grid_constan
         if (!(ok = wait_warp(bar(C_EMPTY + st), ((c_fill / kNS) & 1u) ^ 1u, g))) break;
         if (lane == 0) {
           const uint32_t sb = stage(st);
-          mbar_arrive_expect_tx(bar(C_FULL + st), 2 * kTile + (MODE != 0 ? kStats : 0u));
+          // does the mask cut one of the blocks for one of the item's rows
+          const uint8_t* mk = masks + ri * (C::kMaskBytes + 16);
+          bool cut = false;
+          if (C::STAGED)
+            cut = PAIR ? ((mk[2 * e] | mk[2 * e + 1]) & 12u) != 0u
+                       : (reinterpret_cast<const uint32_t*>(mk)[e >> 5] >> (e & 31)) & 1u;
+          mbar_arrive_expect_tx(bar(C_FULL + st), 2 * kTile + (MODE != 0 ? kStats : 0u) +
+                                                      (cut ? (MODE == 0 ? 512u : 1024u) : 0u));
 #pragma unroll
           for (int h = 0; h < C::NBOX; ++h) {
             tma_load_2d(sb + h * kBox, &tb1, bar(C_FULL + st), 64 * h, yc);
@@ -400,6 +413,21 @@ attn_bwd_tc_kernel(const __grid_constant__ CUtensorMap ta1, const __grid_constan
             } else {
               bulk_load(sb + 2 * kTile, p.lse2 + yc64, 512, bar(C_FULL + st));
               bulk_load(sb + 2 * kTile + 512, p.delta + yc64, 512, bar(C_FULL + st));
+            }
+          }
+          if (cut) {   // the mask's part of one block, or of two side by side
+            const int64_t tok0 = bh / p.rm.H * p.N;
+            constexpr uint32_t kBytes = BTB * 4;
+#pragma unroll
+            for (int x = 0; x < (PAIR ? 2 : 1); ++x) {
+              const int64_t at = tok0 + (int64_t)(x ? c2 : c1) * BTB;
+              const uint32_t to = sb + 2 * kTile + kStats + x * kBytes;
+              if (MODE == 0) {
+                bulk_load(to, p.mask.pos + at, kBytes, bar(C_FULL + st));
+              } else {
+                bulk_load(to, p.mask.lo + at, kBytes, bar(C_FULL + st));
+                bulk_load(to + 512, p.mask.len + at, kBytes, bar(C_FULL + st));
+              }
             }
           }
         }
@@ -701,7 +729,7 @@ attn_bwd_tc_kernel(const __grid_constant__ CUtensorMap ta1, const __grid_constan
         groups.make(MODE == 0 ? ilo : (uint32_t)ipos, ilen, lane);
       }
       const uint8_t* mk = masks + ri * (C::kMaskBytes + 16);
-      UnionSeek seek(bits + ri * 2 * C::MAXW, bits + ri * 2 * C::MAXW + C::MAXW, PAIR ? words : 0);
+      UnionSeek seek(bits + ri * 2 * C::MAXW, bits + ri * 2 * C::MAXW + C::MAXW, PAIR && !C::STAGED ? words : 0);
       for (int e = 0; e < len; ++e, ++stages) {
         const uint32_t st = stages % kNS;
         const float4* stats = reinterpret_cast<const float4*>(gbase + C::kOffStage + st * kStageBytes + 2 * kTile);
@@ -717,10 +745,21 @@ attn_bwd_tc_kernel(const __grid_constant__ CUtensorMap ta1, const __grid_constan
         }
         uint32_t see = 0xffffffffu;
         if (cut) {
-          const int64_t j = PAIR ? seek.at(2 * e + hf) : __ldg(p.idx + p.ptr[item] + e);
-          const int64_t at = tok0 + j * BTB + (PAIR ? 0 : HB * hf) + 32 * q + lane;
-          if (MODE == 0) see = query_bits(groups, ilo, ilen, __ldg(p.mask.pos + at));
-          else see = key_bits(groups, ipos, __ldg(p.mask.lo + at), __ldg(p.mask.len + at));
+          int32_t x0;         // of this lane's column: position (mode 0), or start and length
+          uint32_t x1 = 0u;
+          if constexpr (C::STAGED) {
+            if (!(ok = wait_warp(bar(C_FULL + st), (stages / kNS) & 1u, g))) break;
+            const uint32_t* cols = reinterpret_cast<const uint32_t*>(stats + kStats / 16) + HB * hf + 32 * q + lane;
+            x0 = (int32_t)cols[0];
+            if (MODE != 0) x1 = cols[128];
+          } else {
+            const int64_t j = PAIR ? seek.at(2 * e + hf) : __ldg(p.idx + p.ptr[item] + e);
+            const int64_t at = tok0 + j * BTB + (PAIR ? 0 : HB * hf) + 32 * q + lane;
+            x0 = __ldg((MODE == 0 ? p.mask.pos : p.mask.lo) + at);
+            if (MODE != 0) x1 = __ldg(p.mask.len + at);
+          }
+          if (MODE == 0) see = query_bits(groups, ilo, ilen, x0);
+          else see = key_bits(groups, ipos, x0, x1);
           has = __any_sync(0xffffffffu, see != 0u);
         }
         const uint32_t hg = 2u * stages + (uint32_t)hf, b = hg % NB;
