@@ -16,7 +16,13 @@
 // several heads. All heads of a token turn alike, so a thread loads the (cos,
 // sin) of its tokens and columns once, keeps them in registers and sweeps the
 // heads; the 16-byte vectors of the next heads are on their way meanwhile, each
-// thread's into shared-memory slots of its own (cp.async).
+// thread's into shared-memory slots of its own (cp.async): without them 138 us for the
+// first case here. Measured, cold cache, against a copy's 6.67 TB/s (bf16):
+//   30,720 tokens, 40 heads of 128, raster to tile order with means: 111 us, 5.7 TB/s (0.86)
+//   65,536 tokens, 24 heads of 128, the inverse with given positions: 138 us, 5.8 TB/s (0.87)
+//   8,192 tokens, 12 heads of 64: 10.2 us, of which the launch is half
+// The rest is the ramp of CTAs that live for 8 heads only, and the read and write streams
+// of rows 10 KB apart.
 #include "common.cuh"
 #include "tc_helpers.cuh"
 
