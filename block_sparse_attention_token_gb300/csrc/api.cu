@@ -204,7 +204,14 @@ sparsp_status_t attn_fwd(const sparsp_shape_t* shape, const void* q, const void*
     col_idx = w.seen_idx;
   }
   const bool flat = (flags & SPARSP_SCHED_FLAT) != 0;
-  if (tc && attn_fwd_tc_items_per_head(s) != s.nb) {
+  // the general kernel's list of a masked call: marks, then count and pull counter, in one stretch
+  const int64_t masked_items = masked ? (int64_t)s.B * s.H * attn_fwd_tc_items_per_head(s) : 0;
+  if (masked && order_items_fits(s, attn_fwd_tc_items_per_head(s), plan != nullptr)) {
+    r = launch_order_items(s, attn_fwd_tc_items_per_head(s), row_ptr, w.items, w.counter, w.fix_mark,
+                           (int)masked_items + 2, st);
+  } else if (masked && cudaMemsetAsync(w.fix_mark, 0, (masked_items + 2) * sizeof(int32_t), st) != cudaSuccess) {
+    return SPARSP_ERR_CUDA;
+  } else if (tc && attn_fwd_tc_items_per_head(s) != s.nb) {
     // the tcgen05 kernel's items are pairs of query blocks: order the pairs,
     // each costing the sum of its two rows
     r = launch_pair_ptr(s, row_ptr, w.pair_ptr, st);
@@ -221,8 +228,7 @@ sparsp_status_t attn_fwd(const sparsp_shape_t* shape, const void* q, const void*
                                col_idx, scale, (float*)o, lse, w.items, w.counter, prof, d_status,
                                st);
   if (masked) {
-    const int64_t items = (int64_t)s.B * s.H * attn_fwd_tc_items_per_head(s);
-    const FixList fix{w.fix_items, w.fix_mark, w.fix_mark + items, w.fix_mark + items + 1};
+    const FixList fix{w.fix_items, w.fix_mark, w.fix_mark + masked_items, w.fix_mark + masked_items + 1};
     return launch_attn_fwd_masked(s, (const __nv_bfloat16*)q, (const __nv_bfloat16*)k, (const __nv_bfloat16*)v,
                                   row_ptr, col_idx, scale, cap, mask, (__nv_bfloat16*)o, lse, raster, in_raster,
                                   w.items, w.counter, fix, prof, d_status, st);
@@ -292,7 +298,10 @@ sparsp_status_t attn_bwd(const sparsp_shape_t* shape, const void* q, const void*
   const bool pairs = tc && attn_bwd_tc_items_per_head(s) != s.nb;
   Dims sp = s;
   sp.nb = pairs ? attn_bwd_tc_items_per_head(s) : s.nb;
-  if (pairs) {
+  const bool small = masked && order_items_fits(s, sp.nb, plan != nullptr);
+  if (small) {
+    r = launch_order_items(s, sp.nb, row_ptr, w.items, w.counter, nullptr, 0, st);
+  } else if (pairs) {
     r = launch_pair_ptr(s, row_ptr, w.pair_ptr, st);
     if (r != SPARSP_OK) return r;
     r = launch_lpt(sp, w.pair_ptr, flat, w.items, w.counter, w.hist, st, 2 * s.nb);
@@ -307,7 +316,9 @@ sparsp_status_t attn_bwd(const sparsp_shape_t* shape, const void* q, const void*
                : launch_attn_bwd_tc(s, 0, (cb)q, (cb)k, (cb)v, (cb)dout, w.lse2, w.delta, row_ptr, col_idx, scale,
                                     (__nv_bfloat16*)dq, nullptr, w.items, w.counter, prof, d_status, raster, st);
     if (r != SPARSP_OK) return r;
-    if (pairs) {   // pair_ptr is free again: the dQ kernel reads only its item list
+    if (small) {
+      r = launch_order_items(s, sp.nb, w.col_ptr, w.items2, w.counter + 1, nullptr, 0, st);
+    } else if (pairs) {   // pair_ptr is free again: the dQ kernel reads only its item list
       r = launch_pair_ptr(s, w.col_ptr, w.pair_ptr, st);
       if (r != SPARSP_OK) return r;
       r = launch_lpt(sp, w.pair_ptr, flat, w.items2, w.counter + 1, w.hist, st, 2 * s.nb);

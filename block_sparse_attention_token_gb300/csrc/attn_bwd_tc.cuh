@@ -602,7 +602,7 @@ attn_bwd_tc_kernel(const __grid_constant__ CUtensorMap ta1, const __grid_constan
     // 32 rows with 32 columns each. The chains of a cap or a mask then have three
     // other warps of the scheduler to run beside, and the code of a half stays in the
     // instruction cache. A warp writes its X over its own S (and dP) columns.
-    // Measured: 8,192 tokens, 12 heads of 64, clips: 705 us, with a cap 876 us (four warps
+    // Measured: 8,192 tokens, 12 heads of 64, clips: 698 us, with a cap 855 us (four warps
     // 1,600; the third half buffer of d = 64 took 943 to 872); 65,536 tokens, 24 heads of
     // 128, clips: 14.6 ms (without a mask 12.7 ms on the same blocks), the tensor pipe 57 to
     // 65% busy. What a half waits for is its round through S and dP, the row warps and the

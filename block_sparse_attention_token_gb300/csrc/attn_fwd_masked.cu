@@ -13,9 +13,6 @@ sparsp_status_t launch_attn_fwd_masked(const Dims& s, const __nv_bfloat16* q, co
   if (cap > 0.f && cap <= kFixedCap)
     return launch_fwd_mod<2>(s, q, k, v, row_ptr, col_idx, scale, o, lse, raster, in_raster, items, counter, prof,
                              d_status, mask, cap, FixList{}, st);
-  // the list: marks, then count and pull counter, in one stretch
-  const size_t n = (size_t)s.B * s.H * attn_fwd_tc_items_per_head(s);
-  if (cudaMemsetAsync(fix.mark, 0, (n + 2) * sizeof(int32_t), st) != cudaSuccess) return SPARSP_ERR_CUDA;
   sparsp_status_t r;
   if (cap > 0.f) {
     r = launch_fwd_mod<2>(s, q, k, v, row_ptr, col_idx, scale, o, lse, raster, in_raster, items, counter, prof, d_status,

@@ -806,8 +806,8 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
     // Measured: 65,536 tokens, 24 heads of 128, clips: 3.3 ms (the kernel without a mask
     // 3.25 ms on the same blocks), the tensor pipe issuing 70% of the time; 30,720
     // tokens, 40 heads of 128, frames and cap: 5.9 to 6.2 ms, the fp32 pipe 43% and the
-    // tensor pipe 49% busy; 8,192 tokens, 12 heads of 64, clips: 242 us, of it 30 us the other
-    // launches and 30 us the uneven ends of 768 items on 152 SMs; a stage takes there as
+    // tensor pipe 49% busy; 8,192 tokens, 12 heads of 64, clips: 230 us, of it 25 us the other
+    // launches and 25 us the uneven ends of 768 items on 152 SMs; a stage takes there as
     // long as its chain S, 64 columns per warp, P V. Four warps with a running maximum
     // took 381 us there.
     const int grp = warp >> 3, hh = (warp >> 2) & 1, rw = warp & 3, t = (int)(threadIdx.x & 127);

@@ -92,7 +92,87 @@ mask_csr_kernel(const MaskView m, int H, int nb, int64_t rows, const int32_t* __
   }
 }
 
+// The work order of a small problem in one CTA: items (rows, or pairs of rows of a
+// head) by their number of blocks, the longest first, equal ones in any order (the
+// results do not depend on it); the pull counter and `n_zero` further words are
+// cleared. A counting sort in shared memory; the lanes of a warp with equal costs count
+// together, as one counter hit by all items one by one takes longer than the sort
+// (ranks by comparing all pairs of 768 items: 15 us more).
+constexpr int kOrderThreads = 1024, kOrderMaxBlocks = 1024, kOrderItems = 4096;
+__global__ void __launch_bounds__(kOrderThreads)
+order_items_kernel(const int32_t* __restrict__ row_ptr, int nb, int per_head, int n, int32_t* __restrict__ items,
+                   int32_t* __restrict__ counter, int32_t* __restrict__ zero, int n_zero) {
+  __shared__ int32_t place[2 * kOrderMaxBlocks + 1];   // items per cost, then the next slot of each
+  __shared__ int32_t warp_sum[32];
+  const int t = threadIdx.x, lane = t & 31, top = 2 * nb, step = per_head == nb ? 1 : 2;
+  // adds the warp's items to their costs' counters; an item's place among them
+  auto take = [&](int item, int32_t& c) {
+    c = -1;
+    if (item < n) {
+      const int h = item / per_head, r = (item - h * per_head) * step;
+      c = row_ptr[(int64_t)h * nb + min(r + step, nb)] - row_ptr[(int64_t)h * nb + r];
+      c = min(max(c, 0), top);
+    }
+    const unsigned same = __match_any_sync(0xffffffffu, c);
+    const int lead = __ffs(same) - 1;
+    int32_t at = 0;
+    if (lane == lead && c >= 0) at = atomicAdd(&place[c], __popc(same));
+    return __shfl_sync(0xffffffffu, at, lead) + __popc(same & ((1u << lane) - 1u));
+  };
+  for (int c = t; c <= top; c += kOrderThreads) place[c] = 0;
+  for (int i = t; i < n_zero; i += kOrderThreads) zero[i] = 0;
+  if (t == 0) *counter = 0;
+  __syncthreads();
+  int32_t c;
+  for (int i = t; i - lane < n; i += kOrderThreads) take(i, c);
+  __syncthreads();
+  // items with a larger cost: each thread some costs from the top down, then over the threads
+  constexpr int kPer = (2 * kOrderMaxBlocks + kOrderThreads) / kOrderThreads;
+  int32_t mine[kPer], sum = 0;
+#pragma unroll
+  for (int u = 0; u < kPer; ++u) {
+    const int k = top - (t * kPer + u);
+    mine[u] = k >= 0 ? place[k] : 0;
+    sum += mine[u];
+  }
+  int32_t incl = sum;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const int32_t o = __shfl_up_sync(0xffffffffu, incl, off);
+    if (lane >= off) incl += o;
+  }
+  if (lane == 31) warp_sum[t >> 5] = incl;
+  __syncthreads();
+  int32_t run = incl - sum;
+  for (int w = 0; w < (t >> 5); ++w) run += warp_sum[w];
+#pragma unroll
+  for (int u = 0; u < kPer; ++u) {
+    const int k = top - (t * kPer + u);
+    if (k >= 0) place[k] = run;
+    run += mine[u];
+  }
+  __syncthreads();
+  for (int i = t; i - lane < n; i += kOrderThreads) {
+    const int32_t slot = take(i, c);
+    if (i < n) items[slot] = i;
+  }
+}
+
 }  // namespace
+
+bool order_items_fits(const Dims& s, int per_head, bool uneven) {
+  const int64_t n = (int64_t)s.B * s.H * per_head, kv_bytes = (int64_t)s.B * s.H * s.N * s.d * s.elem * 2;
+  if (s.nb > kOrderMaxBlocks || n > kOrderItems) return false;
+  return n <= device_sm_count() || (uneven && kv_bytes <= (int64_t)64 << 20);
+}
+
+sparsp_status_t launch_order_items(const Dims& s, int per_head, const int32_t* row_ptr, int32_t* items,
+                                   int32_t* counter, int32_t* zero, int n_zero, cudaStream_t st) {
+  order_items_kernel<<<1, kOrderThreads, 0, st>>>(row_ptr, s.nb, per_head, s.B * s.H * per_head, items, counter, zero,
+                                                  n_zero);
+  SPARSP_LAUNCH_CHECK();
+  return SPARSP_OK;
+}
 
 sparsp_status_t launch_mask_plan(const Dims& s, const int32_t* pos, const int32_t* lo, const int32_t* hi, void* plan,
                                  cudaStream_t st) {

@@ -63,7 +63,8 @@ class Pipeline:
         # projection, two score products, gradient products, loss (partials, sum), weight gradients
         pred = 7 if self.predictor_lr is not None else 0
         # norm of Q and K; with raster inputs the rotation is a pass of its own; masked scores, the masked CSR (count,
-        # scan, fill; left out for small shapes), and the general attention kernel over what the first one passes on
+        # scan, fill; left out for small shapes, as is a launch of the order in 64-token blocks), and the general
+        # attention kernel over what the first one passes on
         extra = (2 if self.norm is not None else 0) + (2 if self.rope is not None and self.raster_in else 0)
         extra += (4 if self.mask is not None else 0)
         extra += 1 if (self.mask is not None and not self.cap) or self.cap > 20 else 0

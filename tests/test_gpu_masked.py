@@ -492,6 +492,36 @@ def test_longest_sequences(dims, cap):
         close(grads[1].view(nb, bt, s.d)[j], dk, tol * (1 + U16) + U16 * dk.abs() + 1e-6, f"dK {j}")
 
 
+@pytest.mark.parametrize("dims", [(1, 64, 4, 32, 32, 64, 4, 4, 4), (2, 40, 4, 16, 24, 64, 2, 8, 8),
+                                  (1, 40, 5, 8, 24, 128, 1, 8, 8)])
+@pytest.mark.parametrize("cap", [0.0, 30.0])
+def test_many_heads(dims, cap):
+    """More items than the threads that order them (2,048 pairs), odd pairs and several batch elements: heads in every
+    place against 64 bits; one CTA that takes all items in turn gives the same bits."""
+    s = sp.make_shape(*dims, "bf16")
+    g = gen(33)
+    q, k, v, do = inputs(s, g)
+    rp, ci, chosen = csr(s, 0.5, g)
+    mask = masks(s, "docs", g)
+    plan = sp.mask_plan(s, *mask)
+    scale = sp.default_scale(s.d)
+    o, lse = sp.attn_masked_fwd(s, q, k, v, rp, ci, cap=cap, mask=plan)
+    grads = sp.attn_masked_bwd(s, q, k, v, o, lse, do, rp, ci, cap=cap, mask=plan)
+    one = sp.make_shape(1, 1, *dims[2:], "bf16")
+    for b, h in [(0, 0), (s.B - 1, s.H - 1), (s.B - 1, s.H // 2)]:
+        r = b * s.H + h
+        q1, k1, v1, do1, o1, *g1 = (t[b:b + 1, h:h + 1] for t in (q, k, v, do, o, *grads))
+        lse1 = lse[b:b + 1, h:h + 1]
+        ref = reference(one, q1, k1, v1, chosen[r:r + 1], tuple(t[b:b + 1] for t in mask), scale, cap)
+        check_forward(one, o1, lse1, ref, q1, k1, v1, scale, cap)
+        check_backward(one, g1, ref, lse1, o1, do1, q1, k1, v1, scale, cap)
+    for got, want in zip(sp.attn_masked_fwd(s, q, k, v, rp, ci, cap=cap, mask=plan, flags=sp.GRID_CAP(1)), (o, lse)):
+        assert torch.equal(got, want)
+    for got, want in zip(sp.attn_masked_bwd(s, q, k, v, o, lse, do, rp, ci, cap=cap, mask=plan, flags=sp.GRID_CAP(1)),
+                         grads):
+        assert torch.equal(got, want)
+
+
 def test_given_stream_and_a_workspace_in_turn():
     """The stream argument (outputs and workspace made by the call), and one workspace for two captured steps that
     run in turn."""
