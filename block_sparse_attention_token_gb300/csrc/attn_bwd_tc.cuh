@@ -779,7 +779,9 @@ attn_bwd_tc_kernel(const __grid_constant__ CUtensorMap ta1, const __grid_constan
             for (int x = 0; x < 16; ++x) xk[x] = xd[x] = 0u;
           } else {
           uint32_t sv[32], dv[32];
-          tmem_ld32(tS, sv);
+          float most = 0.f;   // the largest score of this row's chunk
+          if constexpr (MOD == 2) most = tmem_ld32_most(tS, sv);
+          else tmem_ld32(tS, sv);
           tmem_ld32(tD, dv);
           wait_ld();
           auto operands = [&](auto form_c, auto cut_c) {   // form of the cap: none, near, within, any, any and large
@@ -859,10 +861,6 @@ attn_bwd_tc_kernel(const __grid_constant__ CUtensorMap ta1, const __grid_constan
             else operands(integral_constant<int, 0>{}, std::false_type{});
           } else {
             // the largest score of the warp's chunk says which form of the cap holds
-            float most = 0.f;
-#pragma unroll
-            for (int x = 0; x < 32; x += 2)
-              most = fmaxf(fmaxf(most, fabsf(__uint_as_float(sv[x]))), fabsf(__uint_as_float(sv[x + 1])));
             if (__all_sync(0xffffffffu, most <= p.near.limit)) {
               if (cut) operands(integral_constant<int, 1>{}, std::true_type{});
               else operands(integral_constant<int, 1>{}, std::false_type{});

@@ -909,7 +909,9 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
             continue;
           }
           uint32_t s[32];
-          tmem_ld32(tS + 32u * c, s);
+          float most = 0.f;   // the largest score of this row's chunk
+          if constexpr (MOD == 2) most = tmem_ld32_most(tS + 32u * c, s);
+          else tmem_ld32(tS + 32u * c, s);
           wait_ld();
           any |= w;
           if (c == 1) {   // the stage's scores are in registers: the next S may start
@@ -952,12 +954,6 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
             else probs(integral_constant<int, 3>{}, std::false_type{});
           } else {
             // the largest score of the warp's chunk says which form of the cap holds
-            float big[2] = {0.f, 0.f};
-#pragma unroll
-            for (int x = 0; x < 32; x += 2)
-              big[(x >> 1) & 1] = fmaxf(fmaxf(big[(x >> 1) & 1], fabsf(__uint_as_float(s[x]))),
-                                        fabsf(__uint_as_float(s[x + 1])));
-            const float most = fmaxf(big[0], big[1]);
             if (__all_sync(0xffffffffu, most <= p.near.limit)) {
               if (cut) probs(integral_constant<int, 0>{}, std::true_type{});
               else probs(integral_constant<int, 0>{}, std::false_type{});
