@@ -281,11 +281,15 @@ attn_bwd_tc_kernel(const __grid_constant__ CUtensorMap ta1, const __grid_constan
           // the pair's two lists as bitmaps; a bad list counts as empty
           const int64_t bh = item / nbp;
           const int iA = 2 * (item % nbp);
-          for (int w = lane; w < 2 * C::MAXW; w += 32) bmA[w] = 0u;
-          __syncwarp();
-          const bool okA = list_bitmap(p.ptr, p.idx, nb, bh * nb + iA, bmA, words, lane);
-          const bool okB = iA + 1 < nb ? list_bitmap(p.ptr, p.idx, nb, bh * nb + iA + 1, bmB, words, lane) : true;
-          badbits = (okA ? 0 : 1) | (okB ? 0 : 2);
+          if constexpr (MOD != 0) {
+            badbits = pair_bitmaps(p.ptr, p.idx, nb, bh * nb + iA, iA + 1 < nb, bmA, bmB, words, lane);
+          } else {
+            for (int w = lane; w < 2 * C::MAXW; w += 32) bmA[w] = 0u;
+            __syncwarp();
+            const bool okA = list_bitmap(p.ptr, p.idx, nb, bh * nb + iA, bmA, words, lane);
+            const bool okB = iA + 1 < nb ? list_bitmap(p.ptr, p.idx, nb, bh * nb + iA + 1, bmB, words, lane) : true;
+            badbits = (okA ? 0 : 1) | (okB ? 0 : 2);
+          }
           if (badbits && lane == 0) report(p.d_status, SPARSP_ERR_DATA);
           if (MOD != 0) badbits = 0;   // its bitmap is empty: it counts as an empty row
           const int u = union_count(bmA, bmB, words, lane);
@@ -297,7 +301,7 @@ attn_bwd_tc_kernel(const __grid_constant__ CUtensorMap ta1, const __grid_constan
             const int2* other = MODE == 0 ? p.mask.krange : p.mask.qrange;
             const int2 ra = masked ? __ldg(own + blk0 + iA) : make_int2(0, 0);
             const int2 rb = masked && iA + 1 < nb ? __ldg(own + blk0 + iA + 1) : ra;
-            union_codes<true>(bmA, bmB, words, u, lane,
+            union_codes<true>(bmA, bmB, words, nb, u, lane,
                               reinterpret_cast<uint32_t*>(masks + ri * (C::kMaskBytes + 16)), [&](int c) -> uint32_t {
               if (!masked) return 0u;
               const int2 x = __ldg(other + blk0 + c);

@@ -326,12 +326,16 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
           // the two rows as bitmaps in the ring slot; a bad row counts as empty
           const int64_t bh = item / nbp;
           const int iA = 2 * (item % nbp);
-          for (int w = lane; w < 2 * C::MAXW; w += 32) bmA[w] = 0u;
-          __syncwarp();
-          const bool okA = list_bitmap(p.row_ptr, p.col_idx, nb, bh * nb + iA, bmA, words, lane);
-          const bool okB = iA + 1 < nb ? list_bitmap(p.row_ptr, p.col_idx, nb, bh * nb + iA + 1, bmB, words, lane)
-                                       : true;
-          badbits = (okA ? 0 : 1) | (okB ? 0 : 2);
+          if constexpr (MOD != 0) {
+            badbits = pair_bitmaps(p.row_ptr, p.col_idx, nb, bh * nb + iA, iA + 1 < nb, bmA, bmB, words, lane);
+          } else {
+            for (int w = lane; w < 2 * C::MAXW; w += 32) bmA[w] = 0u;
+            __syncwarp();
+            const bool okA = list_bitmap(p.row_ptr, p.col_idx, nb, bh * nb + iA, bmA, words, lane);
+            const bool okB = iA + 1 < nb ? list_bitmap(p.row_ptr, p.col_idx, nb, bh * nb + iA + 1, bmB, words, lane)
+                                         : true;
+            badbits = (okA ? 0 : 1) | (okB ? 0 : 2);
+          }
           if (badbits && lane == 0) report(p.d_status, SPARSP_ERR_DATA);
           if (MOD != 0) badbits = 0;   // its bitmap is empty: it counts as an empty row
           const int u = union_count(bmA, bmB, words, lane);
@@ -341,7 +345,7 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
             const bool masked = p.mask.pos != nullptr;
             const int2 qa = masked ? __ldg(p.mask.qrange + blk0 + iA) : make_int2(0, 0);
             const int2 qb = masked && iA + 1 < nb ? __ldg(p.mask.qrange + blk0 + iA + 1) : qa;
-            union_codes<false>(bmA, bmB, words, u, lane, masks + ri * C::kMaskWords, [&](int j) -> uint32_t {
+            union_codes<false>(bmA, bmB, words, nb, u, lane, masks + ri * C::kMaskWords, [&](int j) -> uint32_t {
               if (!masked) return 0u;
               const int2 k = __ldg(p.mask.krange + blk0 + j);
               return (all_seen(qa, k) ? 0u : 1u) | (all_seen(qb, k) ? 0u : 2u);

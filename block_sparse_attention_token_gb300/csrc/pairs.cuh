@@ -148,35 +148,83 @@ __device__ __forceinline__ void union_masks2(const uint32_t* a, const uint32_t* 
 // cut(j), whether the token mask cuts the pair of the first / second row block
 // with block j. BYTES: one byte per block (stage s = bytes 2s, 2s + 1), else one
 // nibble (stage s = byte s). mk holds 32 * words codes and one more, cleared
-// here; warp-collective.
+// here; warp-collective; cut is asked for every block.
 template <bool BYTES, typename Cut>
-__device__ __forceinline__ void union_codes(const uint32_t* a, const uint32_t* b, int words, int u, int lane,
+__device__ __forceinline__ void union_codes(const uint32_t* a, const uint32_t* b, int words, int nb, int u, int lane,
                                             uint32_t* mk, Cut cut) {
   const int nw = BYTES ? (u + 4) / 4 : (u + 8) / 8;
   for (int w = lane; w < nw; w += 32) mk[w] = 0u;
   __syncwarp();
+  // a lane per block, four words at a time: what cut reads comes in whole lines and side by side
   int base_rank = 0;
-  for (int w0 = 0; w0 < words; w0 += 32) {
-    const int w = w0 + lane;
-    const uint32_t x = w < words ? a[w] : 0u, y = w < words ? b[w] : 0u;
-    uint32_t un = x | y;
-    const int c = __popc(un);
-    int incl = c;
+  for (int w0 = 0; w0 < words; w0 += 4) {
+    uint32_t c[4];
 #pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-      const int t = __shfl_up_sync(0xffffffffu, incl, off);
-      if (lane >= off) incl += t;
+    for (int v = 0; v < 4; ++v) {
+      const int j = (w0 + v) * 32 + lane;
+      c[v] = j < nb ? cut(j) : 0u;
     }
-    int rk = base_rank + incl - c;
-    for (; un != 0u; un &= un - 1u, ++rk) {
-      const int bit = __ffs(un) - 1;
-      const uint32_t code = ((x >> bit) & 1u) | (((y >> bit) & 1u) << 1) | (cut(w * 32 + bit) << 2);
-      if (BYTES) reinterpret_cast<uint8_t*>(mk)[rk] = (uint8_t)code;
-      else atomicOr(&mk[rk >> 3], code << (4 * (rk & 7)));
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {
+      if (w0 + v >= words) break;
+      const uint32_t x = a[w0 + v], y = b[w0 + v], un = x | y;
+      if ((un >> lane) & 1u) {
+        const int rk = base_rank + __popc(un & ((1u << lane) - 1u));
+        const uint32_t code = ((x >> lane) & 1u) | (((y >> lane) & 1u) << 1) | (c[v] << 2);
+        if (BYTES) reinterpret_cast<uint8_t*>(mk)[rk] = (uint8_t)code;
+        else atomicOr(&mk[rk >> 3], code << (4 * (rk & 7)));
+      }
+      base_rank += __popc(un);
     }
-    base_rank += __shfl_sync(0xffffffffu, incl, 31);
   }
   __syncwarp();
+}
+
+// The two lists of a pair, rows r and (where there is one) r + 1, as list_bitmap makes
+// them, their loads side by side. Returns which of them are bad (bits 0 and 1). For a
+// pair of 128 blocks' lists this and union_codes took 15,000 cycles list by list and
+// word by word, most of them one load after another.
+__device__ __forceinline__ int pair_bitmaps(const int32_t* ptr, const int32_t* idx, int nb, int64_t r, bool two,
+                                            uint32_t* bmA, uint32_t* bmB, int words, int lane) {
+  for (int w = lane; w < words; w += 32) bmA[w] = bmB[w] = 0u;
+  __syncwarp();
+  const int32_t a = ptr[r], b = ptr[r + 1], c = two ? ptr[r + 2] : b;
+  bool badA = b < a || b - a > nb, badB = c < b || c - b > nb;
+  const int32_t e0 = badA ? b : a, e1 = badB ? b : c;
+  for (int32_t e = e0 + lane; e < e1; e += 128) {
+    int32_t j[4];
+#pragma unroll
+    for (int v = 0; v < 4; ++v) j[v] = e + 32 * v < e1 ? idx[e + 32 * v] : 0;
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {
+      const int32_t at = e + 32 * v;
+      if (at >= e1) break;
+      if (j[v] < 0 || j[v] >= nb) {
+        badA |= at < b;
+        badB |= at >= b;
+      } else {
+        atomicOr(&(at < b ? bmA : bmB)[j[v] >> 5], 1u << (j[v] & 31));
+      }
+    }
+  }
+  badA = __any_sync(0xffffffffu, badA);
+  badB = __any_sync(0xffffffffu, badB);
+  __syncwarp();
+  int nA = 0, nB = 0;
+  for (int w = lane; w < words; w += 32) {
+    nA += __popc(bmA[w]);
+    nB += __popc(bmB[w]);
+  }
+  badA |= __reduce_add_sync(0xffffffffu, nA) != b - a;   // an index listed twice
+  badB |= __reduce_add_sync(0xffffffffu, nB) != c - b;
+  if (badA || badB) {
+    for (int w = lane; w < words; w += 32) {
+      if (badA) bmA[w] = 0u;
+      if (badB) bmB[w] = 0u;
+    }
+    __syncwarp();
+  }
+  return (badA ? 1 : 0) | (badB ? 2 : 0);
 }
 
 // The block of a given rank in the union of two bitmaps, for ascending ranks.
