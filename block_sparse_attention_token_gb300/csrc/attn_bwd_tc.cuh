@@ -314,33 +314,31 @@ attn_bwd_tc_kernel(const __grid_constant__ CUtensorMap ta1, const __grid_constan
         } else {
           const int32_t a = p.ptr[item], b = p.ptr[item + 1];
           bool bad = (b < a) || (b - a > nb);
-          if (!bad)
-            for (int32_t e = a + lane; e < b; e += 32) {
-              const int32_t j = p.idx[e];
-              if (j < 0 || j >= nb) bad = true;
-            }
-          bad = __any_sync(0xffffffffu, bad);
+          if constexpr (MOD != 0) {
+            const int64_t blk0 = (int64_t)item / nb / p.rm.H * nb;
+            const bool masked = p.mask.pos != nullptr;
+            const int2 own = masked ? __ldg((MODE == 0 ? p.mask.qrange : p.mask.krange) + blk0 + item % nb)
+                                    : make_int2(0, 0);
+            if (!bad)
+              bad = list_cuts(p.idx + a, b - a, nb, lane,
+                              reinterpret_cast<uint32_t*>(masks + ri * (C::kMaskBytes + 16)), [&](int j) {
+                if (!masked) return false;
+                const int2 x = __ldg((MODE == 0 ? p.mask.krange : p.mask.qrange) + blk0 + j);
+                return !(MODE == 0 ? all_seen(own, x) : all_seen(x, own));
+              });
+          } else {
+            if (!bad)
+              for (int32_t e = a + lane; e < b; e += 32) {
+                const int32_t j = p.idx[e];
+                if (j < 0 || j >= nb) bad = true;
+              }
+            bad = __any_sync(0xffffffffu, bad);
+          }
           if (bad) {
             if (lane == 0) report(p.d_status, SPARSP_ERR_DATA);
             len = MOD != 0 ? 0 : -1;   // MOD: it counts as an empty row
           } else {
             len = b - a;
-            if constexpr (MOD != 0) {
-              const int64_t blk0 = (int64_t)item / nb / p.rm.H * nb;
-              const bool masked = p.mask.pos != nullptr;
-              const int2 own = masked ? __ldg((MODE == 0 ? p.mask.qrange : p.mask.krange) + blk0 + item % nb)
-                                      : make_int2(0, 0);
-              uint32_t* words_ = reinterpret_cast<uint32_t*>(masks + ri * (C::kMaskBytes + 16));
-              for (int32_t e = 0; e < len; e += 32) {
-                bool cut = masked && e + lane < len;
-                if (cut) {
-                  const int2 x = __ldg((MODE == 0 ? p.mask.krange : p.mask.qrange) + blk0 + p.idx[a + e + lane]);
-                  cut = !(MODE == 0 ? all_seen(own, x) : all_seen(x, own));
-                }
-                const uint32_t w = __ballot_sync(0xffffffffu, cut);
-                if (lane == 0) words_[e >> 5] = w;
-              }
-            }
           }
         }
       }

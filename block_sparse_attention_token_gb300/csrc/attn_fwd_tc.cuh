@@ -357,28 +357,26 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
         } else {
           const int32_t a = p.row_ptr[item], b = p.row_ptr[item + 1];
           bool bad = (b < a) || (b - a > nb);
-          if (!bad)
-            for (int32_t e = a + lane; e < b; e += 32) {
-              const int32_t j = p.col_idx[e];
-              if (j < 0 || j >= nb) bad = true;
-            }
-          bad = __any_sync(0xffffffffu, bad);
+          if constexpr (MOD != 0) {
+            const int64_t blk0 = (int64_t)item / nb / p.rm.H * nb;
+            const bool masked = p.mask.pos != nullptr;
+            const int2 q = masked ? __ldg(p.mask.qrange + blk0 + item % nb) : make_int2(0, 0);
+            if (!bad)
+              bad = list_cuts(p.col_idx + a, b - a, nb, lane, masks + ri * C::kMaskWords,
+                              [&](int j) { return masked && !all_seen(q, __ldg(p.mask.krange + blk0 + j)); });
+          } else {
+            if (!bad)
+              for (int32_t e = a + lane; e < b; e += 32) {
+                const int32_t j = p.col_idx[e];
+                if (j < 0 || j >= nb) bad = true;
+              }
+            bad = __any_sync(0xffffffffu, bad);
+          }
           if (bad) {
             if (lane == 0) report(p.d_status, SPARSP_ERR_DATA);
             len = MOD != 0 ? 0 : -1;   // MOD: it counts as an empty row
           } else {
             len = b - a;
-            if constexpr (MOD != 0) {
-              const int64_t blk0 = (int64_t)item / nb / p.rm.H * nb;
-              const bool masked = p.mask.pos != nullptr;
-              const int2 q = masked ? __ldg(p.mask.qrange + blk0 + item % nb) : make_int2(0, 0);
-              for (int32_t e = 0; e < len; e += 32) {
-                bool cut = masked && e + lane < len;
-                if (cut) cut = !all_seen(q, __ldg(p.mask.krange + blk0 + p.col_idx[a + e + lane]));
-                const uint32_t w = __ballot_sync(0xffffffffu, cut);
-                if (lane == 0) masks[ri * C::kMaskWords + (e >> 5)] = w;
-              }
-            }
           }
         }
       }

@@ -227,6 +227,31 @@ __device__ __forceinline__ int pair_bitmaps(const int32_t* ptr, const int32_t* i
   return (badA ? 1 : 0) | (badB ? 2 : 0);
 }
 
+// One list of `len` blocks at idx: is an index outside [0, nb), and a bit per block, does
+// the token mask cut it (cut(j); bits of mk). Warp-collective; four loads side by side.
+template <typename Cut>
+__device__ __forceinline__ bool list_cuts(const int32_t* idx, int32_t len, int nb, int lane, uint32_t* mk, Cut cut) {
+  bool bad = false;
+  for (int32_t e = 0; e < len; e += 128) {
+    int32_t j[4];
+    bool c[4];
+#pragma unroll
+    for (int v = 0; v < 4; ++v) j[v] = e + 32 * v + lane < len ? idx[e + 32 * v + lane] : 0;
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {
+      const bool in = j[v] >= 0 && j[v] < nb;
+      bad |= !in;
+      c[v] = in && e + 32 * v + lane < len && cut(j[v]);
+    }
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {
+      const uint32_t w = __ballot_sync(0xffffffffu, c[v]);
+      if (lane == 0 && e + 32 * v < len) mk[(e >> 5) + v] = w;
+    }
+  }
+  return __any_sync(0xffffffffu, bad);
+}
+
 // The block of a given rank in the union of two bitmaps, for ascending ranks.
 struct UnionSeek {
   const uint32_t* a;
