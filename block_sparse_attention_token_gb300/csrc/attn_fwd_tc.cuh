@@ -79,7 +79,10 @@ enum Bar {
   Q_FULL = 0, Q_EMPTY, K_FULL, K_EMPTY = K_FULL + kMaxStages, V_FULL = K_EMPTY + kMaxStages,
   V_EMPTY = V_FULL + kMaxStages, S_FULL = V_EMPTY + kMaxStages, S_FREE = S_FULL + 2, P_FULL = S_FREE + 2, PV_DONE = P_FULL + 2, O_FULL = PV_DONE + 2,
   O_EMPTY,
-  I_FULL, I_EMPTY = I_FULL + kNI, TEAR = I_EMPTY + kNI, TEAR_PV, EXCH, NBAR = EXCH + 8
+  I_FULL, I_EMPTY = I_FULL + kNI, TEAR = I_EMPTY + kNI, TEAR_PV, EXCH, NBAR = EXCH + 8,
+  // FAST: three buffers, each S and then P, in the places of S_FULL to PV_DONE and the one
+  // before (V's ring has less than kMaxStages stages there)
+  S3_FULL = S_FULL - 1, P3_FULL = S3_FULL + 3, PV3_DONE = P3_FULL + 3
 };
 // Tile geometry for blocks of BT tokens and head dimension D. The query tile
 // and a key/value stage are 128 rows each: one block, or two 64-token blocks
@@ -127,10 +130,14 @@ struct Cfg {
   // stages with d = 128, whose row sums and cut bits need the room of the third)
   static constexpr int NK = FAST && D == 64 ? 4 : 3;
   static constexpr int NV = DUO || (FAST && D == 128) ? 2 : FAST ? 4 : 3;
-  static constexpr int NSB = DUO ? 1 : 2, NPB = DUO ? 1 : 2;   // S and P buffers in TMEM
+  // S and P buffers in TMEM. FAST: three of 128 columns, P written over the S it is made
+  // of, so that S of the stage after next is ready when its softmax warps come to it
+  static constexpr int NSB = FAST ? 3 : DUO ? 1 : 2, NPB = NSB;
+  static constexpr int B_S = FAST ? S3_FULL : S_FULL, B_P = FAST ? P3_FULL : P_FULL;
+  static constexpr int B_PV = FAST ? PV3_DONE : PV_DONE;
   static constexpr int NI = DUO || PAIR || MOD_ != 0 ? 2 : kNI;   // item ring slots
   static constexpr int kMinCtas = DUO ? 2 : 1;                  // CTAs per SM
-  static constexpr uint32_t kColS = 0, kColO = DUO ? 128 : 256, kColP = DUO ? 192 : 384;
+  static constexpr uint32_t kColS = 0, kColO = FAST ? 384 : DUO ? 128 : 256, kColP = DUO ? 192 : 384;
   static constexpr uint32_t kTmemCols = DUO ? 256 : 512;
   // bitmap words of one CSR row in the item ring (pairs): up to kMaxBlocks
   // blocks, except for d = 128 whose tiles leave room for 1,024 blocks only
@@ -269,13 +276,22 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
       mbar_init(bar(V_FULL + s), 1);
       mbar_init(bar(V_EMPTY + s), 1);
     }
-    for (int b = 0; b < 2; ++b) {
-      mbar_init(bar(S_FULL + b), 1);
-      mbar_init(bar(S_FREE + b), C::kArrivals);
-      mbar_init(bar(P_FULL + b), C::kArrivals);
+    if (C::FAST) {
+      static_assert(!C::FAST || C::NV < kMaxStages, "barriers");
+      for (int b = 0; b < 3; ++b) {
+        mbar_init(bar(S3_FULL + b), 1);
+        mbar_init(bar(P3_FULL + b), C::kArrivals);
+        mbar_init(bar(PV3_DONE + b), 1);
+      }
+    } else {
+      for (int b = 0; b < 2; ++b) {
+        mbar_init(bar(S_FULL + b), 1);
+        mbar_init(bar(S_FREE + b), C::kArrivals);
+        mbar_init(bar(P_FULL + b), C::kArrivals);
+      }
+      mbar_init(bar(PV_DONE), 1);
+      mbar_init(bar(PV_DONE + 1), 1);
     }
-    mbar_init(bar(PV_DONE), 1);
-    mbar_init(bar(PV_DONE + 1), 1);
     mbar_init(bar(O_FULL), 1);
     mbar_init(bar(O_EMPTY), C::kArrivals);
     for (int r = 0; r < kNI; ++r) {
@@ -714,7 +730,8 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
       bool ok = true;
       for (int e = 0; e < len; ++e) {
         const uint32_t b = s_issue % C::NSB, ks = k_use % C::NK;
-        if (!(ok = wait_warp(bar(S_FREE + b), ((s_issue / C::NSB) & 1u) ^ 1u, g))) break;
+        // FAST: the buffer held P until its PV was done
+        if (!(ok = wait_warp(bar((C::FAST ? C::B_PV : S_FREE) + b), ((s_issue / C::NSB) & 1u) ^ 1u, g))) break;
         if (!(ok = wait_warp(bar(K_FULL + ks), (k_use / C::NK) & 1u, g))) break;
         fence_after();
         const uint32_t kb = sK + ks * C::kKTile;
@@ -727,7 +744,7 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
             mma_ss(tmem + C::kColS + b * 128u, smem_desc(sQ + offq, 16, 1024, kSwizzle128B),
                    smem_desc(kb + offk, 16, 1024, kSwizzle128B), idS, kk > 0 ? 1u : 0u);
           }
-          commit(bar(S_FULL + b));
+          commit(bar(C::B_S + b));
           commit(bar(K_EMPTY + ks));
           if (e + 1 == len) commit(bar(Q_EMPTY));   // every S of this item is issued
         }
@@ -762,18 +779,20 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
       for (int e = 0; e < len; ++e) {
         const uint32_t b = pv % C::NPB, vs = v_use % C::NV;
         if (!(ok = wait_warp(bar(V_FULL + vs), (v_use / C::NV) & 1u, g))) break;
-        if (!(ok = wait_warp(bar(P_FULL + b), (pv / C::NPB) & 1u, g))) break;
+        if (!(ok = wait_warp(bar(C::B_P + b), (pv / C::NPB) & 1u, g))) break;
         if (e == 0 && !(ok = wait_warp(bar(O_EMPTY), (o_items & 1u) ^ 1u, g))) break;
         fence_after();
         const uint32_t vb = sV + vs * C::kKTile;
         if (elect_one()) {
 #pragma unroll
           for (int kk = 0; kk < C::KR / 16; ++kk)
-            mma_ts(tmem + C::kColO, tmem + C::kColP + b * 64u + (uint32_t)kk * 8u,
+            mma_ts(tmem + C::kColO,
+                   C::FAST ? tmem + C::kColS + b * 128u + (uint32_t)(kk >> 2) * 64u + (uint32_t)(kk & 3) * 8u
+                           : tmem + C::kColP + b * 64u + (uint32_t)kk * 8u,
                    smem_desc(vb + (uint32_t)kk * 2048u, C::kKBox, 1024, kSwizzle128B), idO,
                    (e > 0 || kk > 0) ? 1u : 0u);
           commit(bar(V_EMPTY + vs));
-          commit(bar(PV_DONE + b));
+          commit(bar(C::B_PV + b));
           if (e + 1 == len) commit(bar(O_FULL));
         }
         __syncwarp();
@@ -799,9 +818,9 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
     // finite, goes on the list of items that the general kernel does after this
     // one (scores of more than 55, or all below -42: a softmax that is one key).
     // So stages do not depend on one another and nothing is rescaled. Two groups of
-    // eight warps take the stages in turn (group g those of S and P buffer g),
-    // two warps per 32 rows with 64 columns each, so that the waits and loads of some
-    // run under the arithmetic of others. A warp goes through TMEM 32 columns at
+    // eight warps take the stages in turn, two warps per 32 rows with 64 columns each, so
+    // that the waits and loads of some run under the arithmetic of others; three S / P
+    // buffers, so that neither group waits for its next S. A warp goes through TMEM 32 columns at
     // a time in a loop that is not unrolled: unrolled, its variants do not stay
     // in the instruction cache. At the end of an item the parts of the row sum
     // meet in shared memory and group 0 writes O and LSE while group 1 goes on.
@@ -815,10 +834,8 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
     const int grp = warp >> 3, hh = (warp >> 2) & 1, rw = warp & 3, t = (int)(threadIdx.x & 127);
     const uint32_t t_row = tmem + ((uint32_t)(rw * 32) << 16);
     float* part = reinterpret_cast<float*>(gbase + C::kOffEx);   // [4][128] parts of the row sums
-    uint32_t it_use = 0, turn = 0, o_items = 0;                  // turn: stages done by this group
-    uint32_t stages_before = 0;                                  // of this CTA
+    uint32_t it_use = 0, o_items = 0, stages_before = 0;         // stages of this CTA
     const int half = PAIR ? t >> 6 : 0;   // with pairs, rows 0-63 are query block 2p and rows 64-127 block 2p + 1
-    const uint32_t tS = t_row + C::kColS + grp * 128u + hh * 64u, tP = t_row + C::kColP + grp * 64u + hh * 32u;
     auto arrive = [&](uint32_t bar_) {   // for the whole warp
       __syncwarp();
       if (lane == 0) mbar_arrive(bar_);
@@ -870,7 +887,7 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
       float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
       uint32_t any = 0u;   // this row has seen a key
       bool ok = true;
-      for (int e = (grp ^ (int)(stages_before & 1u)); e < len; e += 2, ++turn) {
+      for (int e = (grp ^ (int)(stages_before & 1u)); e < len; e += 2) {
         // did the row block select this half's key block, does the mask cut it, and the
         // columns this row sees then
         bool has = true, cut;
@@ -887,16 +904,10 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
           const int32_t* kp = pos0 + j * BT + (PAIR ? 0 : 64 * hh);
           query_bits(groups, ilo, ilen, __ldg(kp), __ldg(kp + 32), lane, see0, see1);
         }
-        if (!(ok = wait_warp(bar(S_FULL + grp), turn & 1u, g))) break;
-        // P's buffer is free when the PV of this group's last stage is done: waited for under the
-        // first exponentials, but with 64-token blocks, where a mask often leaves a warp's
-        // columns none, before them (8k clips 241 us against 257; 30k frames in 128-token
-        // blocks, capped, 6.54 ms against 5.88)
-        if (PAIR && turn > 0 && !(ok = wait_warp(bar(PV_DONE + grp), (turn - 1u) & 1u, g))) break;
+        const uint32_t n = stages_before + (uint32_t)e, buf = n % 3u;   // stage of the CTA, its buffer
+        const uint32_t tS = t_row + C::kColS + buf * 128u + hh * 64u;   // this warp's scores, and its P over them
+        if (!(ok = wait_warp(bar(C::B_S + buf), (n / 3u) & 1u, g))) break;
         fence_after();
-        auto p_free = [&](int c) {
-          return PAIR || c > 0 || turn == 0 || wait_warp(bar(PV_DONE + grp), (turn - 1u) & 1u, g);
-        };
 #pragma unroll 1
         for (int c = 0; c < 2; ++c) {
           const uint32_t w = c == 0 ? see0 : see1;
@@ -905,9 +916,7 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
           if (!has || !__any_sync(0xffffffffu, w != 0u)) {
 #pragma unroll
             for (int x = 0; x < 16; ++x) pk[x] = 0u;
-            if (!(ok = p_free(c))) break;
-            tmem_st16(tP + 16u * c, pk);
-            if (c == 1) arrive(bar(S_FREE + grp));
+            tmem_st16(tS + 16u * c, pk);
             continue;
           }
           uint32_t s[32];
@@ -916,10 +925,6 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
           else tmem_ld32(tS + 32u * c, s);
           wait_ld();
           any |= w;
-          if (c == 1) {   // the stage's scores are in registers: the next S may start
-            fence_before();
-            arrive(bar(S_FREE + grp));
-          }
           auto probs = [&](auto form_c, auto cut_c) {   // form of the cap: near, within, any, none, any and large
             constexpr int FORM = decltype(form_c)::value;
             constexpr bool CUT = decltype(cut_c)::value;
@@ -967,13 +972,11 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
               probs(integral_constant<int, 4>{}, std::true_type{});
             }
           }
-          if (!(ok = p_free(c))) break;
-          tmem_st16(tP + 16u * c, pk);
+          tmem_st16(tS + 16u * c, pk);
         }
-        if (!ok) break;
         wait_st();
         fence_before();
-        arrive(bar(P_FULL + grp));
+        arrive(bar(C::B_P + buf));
       }
       if (!ok) break;
       arrive(bar(I_EMPTY + ri));
