@@ -604,12 +604,12 @@ attn_bwd_tc_kernel(const __grid_constant__ CUtensorMap ta1, const __grid_constan
     // 32 rows with 32 columns each. The chains of a cap or a mask then have three
     // other warps of the scheduler to run beside, and the code of a half stays in the
     // instruction cache. A warp writes its X over its own S (and dP) columns.
-    // Measured: 8,192 tokens, 12 heads of 64, clips: 698 us, with a cap 855 us (four warps
+    // Measured: 8,192 tokens, 12 heads of 64, clips: 640 us, with a cap 785 us (four warps
     // 1,600; the third half buffer of d = 64 took 943 to 872); 65,536 tokens, 24 heads of
     // 128, clips: 14.6 ms (without a mask 12.7 ms on the same blocks), the tensor pipe 57 to
     // 65% busy. What a half waits for is its round through S and dP, the row warps and the
     // accumulate, with two half buffers at d = 128 (TMEM holds no third) and three at 64.
-    // A loader warp beside the producer, as in the forward, was slower (15.0 ms, 900 us).
+    // A loader warp beside the producer, as in the forward, was slower (15.0 ms against 14.6, 900 us against 876).
     const int hf = warp >> 3, q = (warp >> 2) & 1, rw = warp & 3, t = (int)(threadIdx.x & 127);
     const int k4 = warp >> 2;                                       // this warp among the four of its rows
     const uint32_t t_row = tmem + ((uint32_t)(rw * 32) << 16);

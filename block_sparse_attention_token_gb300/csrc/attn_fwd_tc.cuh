@@ -48,7 +48,7 @@
 //              block, so the masks of a pair are warp-uniform.
 // TMEM (512 columns): S0 [0,128), S1 [128,256), O [256,384), P0 [384,448),
 // P1 [448,512); DUO (256 columns per CTA): S [0,128), O [128,192),
-// P [192,256). Every mbarrier wait is bounded (2 s); on expiry the CTA sets
+// P [192,256); FAST: three of S and then P [0,384), O [384,384+d). Every mbarrier wait is bounded (2 s); on expiry the CTA sets
 // SPARSP_ERR_TIMEOUT, all roles leave their loops, copies and MMAs in flight
 // are drained with a second bounded wait, and TMEM is released.
 //
@@ -824,13 +824,13 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
     // a time in a loop that is not unrolled: unrolled, its variants do not stay
     // in the instruction cache. At the end of an item the parts of the row sum
     // meet in shared memory and group 0 writes O and LSE while group 1 goes on.
-    // Measured: 65,536 tokens, 24 heads of 128, clips: 3.3 ms (the kernel without a mask
-    // 3.25 ms on the same blocks), the tensor pipe issuing 70% of the time; 30,720
-    // tokens, 40 heads of 128, frames and cap: 5.9 to 6.2 ms, the fp32 pipe 43% and the
-    // tensor pipe 49% busy; 8,192 tokens, 12 heads of 64, clips: 230 us, of it 25 us the other
-    // launches and 25 us the uneven ends of 768 items on 152 SMs; a stage takes there as
+    // Measured: 65,536 tokens, 24 heads of 128, clips: 3.35 ms (the kernel without a mask
+    // 3.27 ms on the same blocks), the tensor pipe issuing 70% of the time; 30,720
+    // tokens, 40 heads of 128, frames and cap: 5.5 to 5.8 ms, the fp32 pipe 48% and the
+    // tensor pipe 54% busy; 8,192 tokens, 12 heads of 64, clips: 211 us, of it 25 us the other
+    // launches and 20 us the uneven ends of 768 items on 152 SMs; a stage takes there as
     // long as its chain S, 64 columns per warp, P V. Four warps with a running maximum
-    // took 381 us there.
+    // took 381 us there, two S buffers and two of P 220.
     const int grp = warp >> 3, hh = (warp >> 2) & 1, rw = warp & 3, t = (int)(threadIdx.x & 127);
     const uint32_t t_row = tmem + ((uint32_t)(rw * 32) << 16);
     float* part = reinterpret_cast<float*>(gbase + C::kOffEx);   // [4][128] parts of the row sums
