@@ -206,10 +206,11 @@ sparsp_status_t attn_fwd(const sparsp_shape_t* shape, const void* q, const void*
   const bool flat = (flags & SPARSP_SCHED_FLAT) != 0;
   // the general kernel's list of a masked call: marks, then count and pull counter, in one stretch
   const int64_t masked_items = masked ? (int64_t)s.B * s.H * attn_fwd_tc_items_per_head(s) : 0;
+  const int64_t cleared = masked && !(cap > 0.f && cap <= kFixedCap) ? masked_items + 2 : 0;
   if (masked && order_items_fits(s, attn_fwd_tc_items_per_head(s), plan != nullptr)) {
     r = launch_order_items(s, attn_fwd_tc_items_per_head(s), row_ptr, w.items, w.counter, w.fix_mark,
-                           (int)masked_items + 2, st);
-  } else if (masked && cudaMemsetAsync(w.fix_mark, 0, (masked_items + 2) * sizeof(int32_t), st) != cudaSuccess) {
+                           (int)cleared, st);
+  } else if (cleared > 0 && cudaMemsetAsync(w.fix_mark, 0, cleared * sizeof(int32_t), st) != cudaSuccess) {
     return SPARSP_ERR_CUDA;
   } else if (tc && attn_fwd_tc_items_per_head(s) != s.nb) {
     // the tcgen05 kernel's items are pairs of query blocks: order the pairs,

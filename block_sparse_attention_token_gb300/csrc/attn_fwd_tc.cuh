@@ -48,8 +48,8 @@
 //              block, so the masks of a pair are warp-uniform.
 // TMEM (512 columns): S0 [0,128), S1 [128,256), O [256,384), P0 [384,448),
 // P1 [448,512); DUO (256 columns per CTA): S [0,128), O [128,192),
-// P [192,256); FAST: three of S and then P [0,384), O [384,384+d). Every mbarrier wait is bounded (2 s); on expiry the CTA sets
-// SPARSP_ERR_TIMEOUT, all roles leave their loops, copies and MMAs in flight
+// P [192,256); FAST: three of S and then P [0,384), O [384,384+d).
+// Every mbarrier wait is bounded (2 s); on expiry the CTA sets SPARSP_ERR_TIMEOUT, all roles leave their loops, copies and MMAs in flight
 // are drained with a second bounded wait, and TMEM is released.
 //
 // MOD = 0 is attention over the selected blocks. MOD = 1 adds a token mask
@@ -170,10 +170,6 @@ struct Cfg {
 constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr uint64_t kDrainNs = 200000000ull;
 constexpr float kRescaleThreshold = 8.0f;   // log2 units
-// Up to this cap one reference c0 = max(0, cap log2(e) - 20) holds every score: P lies
-// in [2^-37.8, 2^20], so that sums of 2^19 terms and their products with values from
-// 2^-88 to 2^88 stay normal fp32 numbers. Beyond it c0 = 0 and the rows are checked.
-constexpr float kFixedCap = 20.0f;
 
 __device__ __forceinline__ bool wait_raw(uint32_t bar, uint32_t parity, uint64_t limit) {
   const uint64_t t0 = globaltimer_ns();

@@ -110,6 +110,11 @@ bool order_items_fits(const Dims& s, int per_head, bool uneven);
 sparsp_status_t launch_order_items(const Dims& s, int per_head, const int32_t* row_ptr, int32_t* items,
                                    int32_t* counter, int32_t* zero, int n_zero, cudaStream_t st);
 
+// Up to this cap one reference c0 = max(0, cap log2(e) - 20) holds every score: P lies
+// in [2^-37.8, 2^20], so that sums of 2^19 terms and their products with values from
+// 2^-88 to 2^88 stay normal fp32 numbers. Beyond it c0 = 0 and the rows are checked.
+constexpr float kFixedCap = 20.0f;
+
 // Items the fast forward kernels pass on to the general one.
 struct FixList {
   int32_t* items;     // [items]
