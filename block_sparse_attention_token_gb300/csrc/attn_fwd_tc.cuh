@@ -978,7 +978,7 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
       arrive(bar(I_EMPTY + ri));
       stages_before += (uint32_t)len;
       float l = (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
-      if (any != 0u) l = fmaxf(l, 1.2e-38f);   // 0 is for a row that has seen no key
+      if (any != 0u && l < 1.2e-38f) l = 1.2e-38f;   // 0 is for a row that has seen no key; NaN stays NaN
       if (!wait_warp(bar(EXCH + 4 + rw), (o_items & 1u) ^ 1u, g)) break;   // the last item's parts were read
       part[(2 * grp + hh) * 128 + t] = l;
       arrive(bar(EXCH + rw));
@@ -1018,7 +1018,7 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
       }
       fence_before();
       arrive(bar(O_EMPTY));
-      if (stores && hh == 0) p.lse[row] = l > 0.f ? (p.c0 + log2f(l)) * 0.69314718055994531f : -INFINITY;
+      if (stores && hh == 0) p.lse[row] = l == 0.f ? -INFINITY : (p.c0 + log2f(l)) * 0.69314718055994531f;   // NaN of NaN
       // one entry per item however many of its warps ask for it
       if (p.fix_items != nullptr && __any_sync(0xffffffffu, stores && !good) && lane == 0 &&
           atomicExch(&p.fix_mark[item], 1) == 0)
@@ -1255,7 +1255,7 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
       }
       fence_before();
       arrive(bar(O_EMPTY));
-      if (stores) p.lse[row] = l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
+      if (stores) p.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;   // NaN of NaN
     }
   } else {
     if constexpr (C::DUO) regs_increase<C::kRegSoftmax>();

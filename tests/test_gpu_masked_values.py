@@ -1,0 +1,62 @@
+"""Masked and capped attention on values at the ends of their range: NaN and infinite inputs in keys and queries that
+count, sums that leave fp32's range, values so small or large that products do, in each range of the cap (none, up to
+20, where no score leaves the kernel's range, and beyond). Tolerances are those of test_gpu_masked."""
+import math
+
+import pytest
+import torch
+
+import block_sparse_attention_token_gb300 as sp
+from tests.test_gpu_masked import (U16, U32, check_backward, check_forward, close, csr, exp_error, gen, inputs, masks,
+                                   reference, to_blocked)
+
+pytestmark = [pytest.mark.gpu, pytest.mark.timeout(300)]
+
+# 128-token blocks with d = 128, and pairs of 64-token blocks with both head sizes
+DIMS = [(1, 2, 6, 16, 24, 128, 2, 8, 8), (2, 2, 4, 16, 12, 64, 4, 4, 4), (1, 2, 5, 8, 24, 128, 1, 8, 8)]
+CAPS = [0.0, 10.0, 50.0, 300.0]
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    import __graft_entry__
+    __graft_entry__.build()
+
+
+def setting(dims, seed, kind="docs"):
+    s = sp.make_shape(*dims, "bf16")
+    g = gen(seed)
+    mask = masks(s, kind, g)
+    rp, ci, chosen = csr(s, 0.6, g)
+    return s, g, mask, sp.mask_plan(s, *mask), rp, ci, chosen
+
+
+def check_beside(o, lse, ref, bad, v, rel, what):
+    """Rows in `bad` have neither a finite value nor a finite LSE; all others are those of the reference."""
+    assert (~torch.isfinite(o[bad])).all() and (~torch.isfinite(lse[bad])).all(), what
+    _, pick, _, p, O, L = ref
+    live, dead = pick.any(-1) & ~bad, ~pick.any(-1)
+    mass = (p[:, :, :, :].nan_to_num(0.0) @ v.double().abs())[live]
+    close(o[live], O[live], (U16 + rel) * mass * (1 + U16) + U16 * O[live].abs() + 1e-30, what + " O")
+    close(lse[live], L[live], rel + 4 * U32 * L[live].abs(), what + " LSE")
+    assert (o[dead] == 0).all() and torch.isneginf(lse[dead]).all()
+
+
+@pytest.mark.parametrize("dims", DIMS)
+@pytest.mark.parametrize("cap", CAPS)
+def test_nan_in_a_key_and_in_a_query(dims, cap):
+    """A row that sees a NaN score has NaN in O and in LSE, not a plausible LSE of its other keys; the others are as
+    they would be."""
+    s, g, mask, plan, rp, ci, chosen = setting(dims, 41)
+    q, k, v, _ = inputs(s, g)
+    scale = s.d ** -0.5
+    rel = 2 * exp_error(s, q, k, scale, cap) + 2.0 ** -20
+    for t, at in ((k, 5), (k, s.N // 2 + 70), (q, s.N // 3)):
+        q2, k2 = q.clone(), k.clone()
+        (q2 if t is q else k2)[:, :, at, 3] = math.nan
+        o, lse = sp.attn_masked_fwd(s, q2, k2, v, rp, ci, scale, cap, plan)
+        ref = reference(s, q2, k2, v, chosen, mask, scale, cap)
+        bad = (ref[0].isnan() & ref[1]).any(-1)
+        assert bad.any() and not bad.all()
+        assert o[bad].isnan().all() and lse[bad].isnan().all()
+        check_beside(o, lse, ref, bad, v, rel, f"NaN at {at}")
