@@ -184,6 +184,13 @@ __device__ __forceinline__ float ex2f(float x) {
   return y;
 }
 
+// The larger of two, NaN if either is
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float m;
+  asm("max.NaN.f32 %0, %1, %2;\n" : "=f"(m) : "f"(a), "f"(b));
+  return m;
+}
+
 // 32 columns of this thread's TMEM lane, and their maximum (sm_103 load with
 // reduction)
 __device__ __forceinline__ float tmem_ld32_max(uint32_t taddr, uint32_t* r) {
@@ -1001,12 +1008,14 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
         tmem_ld32(t_row + C::kColO + hh * (D / 2) + c * 32u, ov);
         wait_ld();
         if (p.fix_items != nullptr) {
-          float top[2] = {0.f, 0.f};   // NaN does not pass a maximum, but its row's l is NaN or its V is
+          // sums of products beyond fp32 of both signs are infinite here, not NaN (measured); a maximum
+          // that passes NaN on does not rest on that
+          float top[2] = {0.f, 0.f};
 #pragma unroll
           for (int x = 0; x < 32; x += 2)
-            top[(x >> 1) & 1] = fmaxf(fmaxf(top[(x >> 1) & 1], fabsf(__uint_as_float(ov[x]))),
-                                      fabsf(__uint_as_float(ov[x + 1])));
-          good = good && fmaxf(top[0], top[1]) < INFINITY;
+            top[(x >> 1) & 1] = max_nan(max_nan(top[(x >> 1) & 1], fabsf(__uint_as_float(ov[x]))),
+                                        fabsf(__uint_as_float(ov[x + 1])));
+          good = good && max_nan(top[0], top[1]) < INFINITY;
         }
         if (!stores) continue;
         uint32_t w[16];

@@ -60,3 +60,20 @@ def test_nan_in_a_key_and_in_a_query(dims, cap):
         assert bad.any() and not bad.all()
         assert o[bad].isnan().all() and lse[bad].isnan().all()
         check_beside(o, lse, ref, bad, v, rel, f"NaN at {at}")
+
+
+@pytest.mark.parametrize("dims", DIMS)
+@pytest.mark.parametrize("cap", [0.0, 60.0, 1000.0])
+@pytest.mark.parametrize("large", [2.0 ** 50, 2.0 ** 70])
+def test_products_beyond_fp32(dims, cap, large):
+    """Scores of about 45 with sums inside the range of the kernel without a maximum (its probabilities reach 2^65),
+    and values of both signs so large that the products leave fp32: every row is done again, none is NaN."""
+    s, g, mask, plan, rp, ci, chosen = setting(dims, 42)
+    q, k, v, _ = inputs(s, g, 0.05)
+    q[..., 0], k[..., 0] = math.sqrt(45.0 if cap in (0.0, 1000.0) else 58.0), math.sqrt(45.0 if cap in (0.0, 1000.0) else 58.0)
+    v = (v * large).bfloat16()
+    o, lse = sp.attn_masked_fwd(s, q, k, v, rp, ci, 1.0, cap, plan)
+    ref = reference(s, q, k, v, chosen, mask, 1.0, cap)
+    top = ref[5][torch.isfinite(ref[5])]
+    assert 40 < float(top.min()) and float(top.max()) < 55.4      # 2^80 is 55.45
+    check_forward(s, o, lse, ref, q, k, v, 1.0, cap)
