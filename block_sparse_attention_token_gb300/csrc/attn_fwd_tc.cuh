@@ -818,8 +818,8 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
     // No running maximum: P = exp2(y - c0) with one constant c0 for every row. With a
     // cap of at most kFixedCap the scores cannot leave the range of that; else
     // c0 = 0 and an item with a row whose sum left [2^-60, 2^80], or whose O is not
-    // finite, goes on the list of items that the general kernel does after this
-    // one (scores of more than 55, or all below -42: a softmax that is one key).
+    // finite or too small beside its sum, goes on the list of items that the general kernel
+    // does after this one (scores of more than 55, or all below -42: a softmax that is one key).
     // So stages do not depend on one another and nothing is rescaled. Two groups of
     // eight warps take the stages in turn, two warps per 32 rows with 64 columns each, so
     // that the waits and loads of some run under the arithmetic of others; three S / P
@@ -1015,7 +1015,11 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
           for (int x = 0; x < 32; x += 2)
             top[(x >> 1) & 1] = max_nan(max_nan(top[(x >> 1) & 1], fabsf(__uint_as_float(ov[x]))),
                                         fabsf(__uint_as_float(ov[x + 1])));
-          good = good && max_nan(top[0], top[1]) < INFINITY;
+          const float most = max_nan(top[0], top[1]);
+          // A small sum may belong to probabilities whose products with small values leave fp32 at
+          // the lower end: 2^19 products lost below 2^-126 are 2^-17 of a largest sum of 2^-90, and, with a
+          // row sum above 2^-20 (scores above -14), 2^-87 in O.
+          good = good && most < INFINITY && (l == 0.f || l > 9.6e-7f || most > 8.1e-28f);
         }
         if (!stores) continue;
         uint32_t w[16];

@@ -586,8 +586,9 @@ SPARSP_API sparsp_status_t sparsp_mask_scores(const sparsp_shape_t* shape, const
  * sees no key gives O = 0, LSE = -inf. Block pairs that see nothing of each other
  * are dropped before the work is ordered (unless the shape is so small that
  * this would cost more). Values in keys that a query does not see must be finite
- * (their weight is 0, and 0 times infinity is not); with a cap of up to 20, |v| below
- * 2^88. A malformed row (an index
+ * (their weight is 0, and 0 times infinity is not). With a cap of up to 20, |v| is
+ * below 2^88 and what is below 2^-88 may be lost; otherwise what is below 2^-87 of
+ * v or 2^-17 of a row's largest |O| may be. A malformed row (an index
  * outside [0, nb), more than nb entries; with 64-token blocks an index given
  * twice) sets SPARSP_ERR_DATA and counts as empty.
  * bf16 on the tcgen05 kernels (Bt and d in {64, 128}, nb <= 1024 when Bt = 64

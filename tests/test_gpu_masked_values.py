@@ -77,3 +77,23 @@ def test_products_beyond_fp32(dims, cap, large):
     top = ref[5][torch.isfinite(ref[5])]
     assert 40 < float(top.min()) and float(top.max()) < 55.4      # 2^80 is 55.45
     check_forward(s, o, lse, ref, q, k, v, 1.0, cap)
+
+
+@pytest.mark.parametrize("dims", DIMS)
+@pytest.mark.parametrize("cap", [0.0, 60.0])
+@pytest.mark.parametrize("small", [2.0 ** -60, 2.0 ** -80, 2.0 ** -95])
+def test_products_below_fp32(dims, cap, small):
+    """Scores of about -35 with sums inside the range of the kernel without a maximum, and values so small that the
+    products (2^-50 and less times the value) leave fp32: O is good to its own roundings all the same."""
+    s, g, mask, plan, rp, ci, chosen = setting(dims, 43)
+    q, k, v, _ = inputs(s, g, 0.05)
+    level = math.sqrt(35.0 if cap == 0 else 39.0)
+    q[..., 0], k[..., 0] = -level, level
+    v = (v * small).bfloat16()
+    o, lse = sp.attn_masked_fwd(s, q, k, v, rp, ci, 1.0, cap, plan)
+    ref = reference(s, q, k, v, chosen, mask, 1.0, cap)
+    seen = ref[5][torch.isfinite(ref[5])]
+    assert -41.5 < float(seen.min()) and float(seen.max()) < -14.0     # 2^-60 is -41.6
+    check_forward(s, o, lse, ref, q, k, v, 1.0, cap)
+    rel = 2 * exp_error(s, q, k, 1.0, cap) + 2.0 ** -20
+    close(o, ref[4], (U16 + rel) * (ref[3] @ v.double().abs()) * (1 + U16) + U16 * ref[4].abs(), "O without a floor")
