@@ -6,6 +6,8 @@
 // Which form holds is decided per warp and 32 columns by the largest score there.
 #pragma once
 
+#include <math.h>
+
 #include "tc_helpers.cuh"
 
 namespace sparsp {
@@ -67,7 +69,7 @@ __device__ __forceinline__ float tanh_any(float x, float t) {
 // Where all |x| <= kNearCap a polynomial of degree 4 in s^2 does (the same fit, 1.7e-7
 // evaluated in fp32), with the powers of scale / cap and the factor cap2 folded into
 // its coefficients: six multiply-adds from the score to y. `limit` is the largest
-// |s| it is for; 0 where the folded coefficients would leave fp32's range.
+// |s| it is for; all is 0 where the folded coefficients would leave fp32's range.
 constexpr float kNearCap = 0.6f;
 struct NearCap {
   float c[5];
@@ -80,14 +82,17 @@ inline NearCap near_cap(double scale, double cap) {
   const double t[5] = {0.9999999403953552, -0.33332309126853943, 0.13310173153877258, -0.05210147798061371,
                        0.01547542680054903};
   double f = cap * 1.4426950408889634 * a;
-  for (int k = 0; k < 5; ++k, f *= a * a) n.c[k] = (float)(t[k] * f);
+  for (int k = 0; k < 5; ++k, f *= a * a) {
+    n.c[k] = (float)(t[k] * f);
+    if (isinf(n.c[k])) return NearCap{};   // a chunk of zeros is within any limit, and 0 times infinity is not 0
+  }
   n.limit = (float)(kNearCap / a);
   return n;
 }
 // The backward rounds everything it makes of tanh to bf16: degree 3 (2.3e-6) will do
 // there, and tanh itself is what it needs twice (c[4] is not used). The error counts
 // times the score in the exponent, so that above a cap of 100 (where it could pass
-// 2e-4) the fit is that of |x| <= 0.25 (5e-9).
+// 2e-4) the fit is that of |x| <= 0.25 (5e-9). Its largest coefficient is 0.05 * 16384^7.
 inline NearCap near_cap_backward(double scale, double cap) {
   NearCap n{};
   const double a = scale / cap;

@@ -97,3 +97,21 @@ def test_products_below_fp32(dims, cap, small):
     check_forward(s, o, lse, ref, q, k, v, 1.0, cap)
     rel = 2 * exp_error(s, q, k, 1.0, cap) + 2.0 ** -20
     close(o, ref[4], (U16 + rel) * (ref[3] @ v.double().abs()) * (1 + U16) + U16 * ref[4].abs(), "O without a floor")
+
+
+@pytest.mark.parametrize("dims", DIMS)
+@pytest.mark.parametrize("scale,cap", [(3.27e6, 200.0), (3.27e6, 1000.0), (1e30, 2.0 ** 20), (2.0 ** -30, 2.0 ** -18)])
+def test_scales_far_from_the_cap(dims, scale, cap):
+    """scale / cap at the border where the polynomial's folded coefficients leave fp32 and beyond, queries small or
+    large in turn, keys of which each 32 hold two far below (their chunk takes another form of the cap, and the row's
+    sum stays in range) and keys that are all zeros: a score of 0 stays 0."""
+    s, g, mask, plan, rp, ci, chosen = setting(dims, 44)
+    q, k, v, do = inputs(s, g)
+    q = (q * (0.3 / scale)).bfloat16()
+    q[..., 0], k[:, :, 5::16, 0] = 1 / scale, -150.0
+    k[:, :, : s.Bt] = 0
+    o, lse = sp.attn_masked_fwd(s, q, k, v, rp, ci, scale, cap, plan)
+    ref = reference(s, q, k, v, chosen, mask, scale, cap)
+    check_forward(s, o, lse, ref, q, k, v, scale, cap)
+    grads = sp.attn_masked_bwd(s, q, k, v, o, lse, do, rp, ci, scale, cap, plan)
+    check_backward(s, grads, ref, lse, o, do, q, k, v, scale, cap)
