@@ -61,7 +61,7 @@
 // MOD = 1 adds the forward's token mask and MOD = 2 its score cap beside it
 // (modes 0 and 3): dS gains the factor 1 - tanh^2, and tanh is the forward's
 // (cap.cuh). The producer tells with the item which of its blocks the token mask
-// cuts; there P is cleared by the bits of the columns a row sees.
+// cuts; there P and dS are cleared by the bits of the columns a row sees.
 // dQ sums dS K over a row in which dS sums to zero, so that the part all keys share
 // cancels and the rounding of dS to one bf16 weighs more than in dK and dV (relative
 // error 2.5e-3, of it 1.7e-3 the rounding of the result, against 2.35e-3): mode 0 keeps
@@ -832,13 +832,13 @@ attn_bwd_tc_kernel(const __grid_constant__ CUtensorMap ta1, const __grid_constan
                 }
                 pr[u] = ex2f(e0);
                 pr[u + 1] = ex2f(e1);
-                if constexpr (CUT) {
-                  if (!((see >> x) & 1u)) pr[u] = 0.f;
-                  if (!((see >> (x + 1)) & 1u)) pr[u + 1] = 0.f;
-                }
                 sub_x2(__uint_as_float(dv[x]), __uint_as_float(dv[x + 1]), dd[u], dd[u + 1], t0, t1);
                 if (FORM != 0) mul_x2(t0, t1, c0, c1, t0, t1);
                 mul_x2(pr[u], pr[u + 1], t0, t1, ds[u], ds[u + 1]);
+                if constexpr (CUT) {   // dS too: with finite values that nobody sees S and dP may be infinite or NaN
+                  if (!((see >> x) & 1u)) pr[u] = ds[u] = 0.f;
+                  if (!((see >> (x + 1)) & 1u)) pr[u + 1] = ds[u + 1] = 0.f;
+                }
               }
               if (MODE == 3) {
                 xk[2 * x4] = pack2(pr[0], pr[1]);

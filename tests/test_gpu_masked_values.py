@@ -115,3 +115,33 @@ def test_scales_far_from_the_cap(dims, scale, cap):
     check_forward(s, o, lse, ref, q, k, v, scale, cap)
     grads = sp.attn_masked_bwd(s, q, k, v, o, lse, do, rp, ci, scale, cap, plan)
     check_backward(s, grads, ref, lse, o, do, q, k, v, scale, cap)
+
+
+@pytest.mark.parametrize("dims", DIMS)
+@pytest.mark.parametrize("cap", CAPS)
+def test_largest_values_that_nobody_sees(dims, cap):
+    """The largest bf16 in tokens that see nothing and that nobody sees (padding): their scores and dO V^T overflow, and
+    no result of the other tokens changes beyond its bounds (the form that a cap takes goes by the largest score
+    beside them); the gradients of the padding are zero."""
+    s, g, mask, plan, rp, ci, chosen = setting(dims, 45)
+    q, k, v, do = inputs(s, g)
+    scale = s.d ** -0.5
+    o, lse = sp.attn_masked_fwd(s, q, k, v, rp, ci, scale, cap, plan)
+    ref = reference(s, q, k, v, chosen, mask, scale, cap)
+    grads = sp.attn_masked_bwd(s, q, k, v, o, lse, do, rp, ci, scale, cap, plan)
+    pad = to_blocked(s, mask[0]) < 0
+    assert pad.any()
+    at = pad[:, None].expand(s.B, s.H, s.N)
+    largest = torch.finfo(torch.bfloat16).max
+    for i in range(4):
+        x = [t.clone() for t in (q, k, v, do)]
+        x[i][at] = largest * torch.randn(int(at.sum()), s.d, generator=g, device="cuda").sign().bfloat16()
+        o2, lse2 = sp.attn_masked_fwd(s, *x[:3], rp, ci, scale, cap, plan)
+        check_forward(s, o2, lse2, ref, q, k, v, scale, cap)
+        got = sp.attn_masked_bwd(s, *x[:3], o, lse, x[3], rp, ci, scale, cap, plan)
+        check_backward(s, got, ref, lse, o, do, q, k, v, scale, cap)
+        for t in got:
+            assert (t[at] == 0).all()
+        if cap == 0:
+            assert torch.equal(o2, o) and torch.equal(lse2, lse)
+            assert all(torch.equal(a, b) for a, b in zip(got, grads))
