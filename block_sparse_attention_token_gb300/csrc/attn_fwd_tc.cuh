@@ -1178,6 +1178,10 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
 #pragma unroll
             for (int c = 0; c < 64; c += 2) {
               const uint32_t w = c < 32 ? w0 : w1;
+              if (MOD == 3) {   // -inf stands for a masked score below; one that is seen is -cap
+                s[c] = __float_as_uint(max_nan(__uint_as_float(s[c]), -3.402823466e38f));
+                s[c + 1] = __float_as_uint(max_nan(__uint_as_float(s[c + 1]), -3.402823466e38f));
+              }
               if (!((w >> (c & 31)) & 1u)) s[c] = 0xff800000u;
               if (!((w >> ((c + 1) & 31)) & 1u)) s[c + 1] = 0xff800000u;
               mw[(c >> 1) & 1] = fmaxf(fmaxf(mw[(c >> 1) & 1], __uint_as_float(s[c])), __uint_as_float(s[c + 1]));

@@ -145,3 +145,51 @@ def test_largest_values_that_nobody_sees(dims, cap):
         if cap == 0:
             assert torch.equal(o2, o) and torch.equal(lse2, lse)
             assert all(torch.equal(a, b) for a, b in zip(got, grads))
+
+
+@pytest.mark.parametrize("dims", DIMS)
+@pytest.mark.parametrize("cap", CAPS)
+def test_infinite_scores(dims, cap):
+    """An infinite value in a key: scores of both signs of infinity by the queries' signs. A cap bounds them, +-cap as
+    the formula has it, also where a row sees nothing but -inf; without one a row that sees +inf is not finite,
+    and -inf is a weight of zero."""
+    s, g, mask, plan, rp, ci, chosen = setting(dims, 46)
+    q, k, v, _ = inputs(s, g)
+    scale = s.d ** -0.5
+    rel = 2 * exp_error(s, q, k, scale, cap) + 2.0 ** -20
+    q[..., 7] = torch.where(q[..., 7] < 0, -1.0, 1.0).bfloat16()
+    for at in (slice(5, 6), slice(0, s.N)):
+        k2 = k.clone()
+        k2[:, :, at, 7] = math.inf
+        o, lse = sp.attn_masked_fwd(s, q, k2, v, rp, ci, scale, cap, plan)
+        ref = reference(s, q, k2, v, chosen, mask, scale, cap)
+        t, pick = ref[0], ref[1]
+        if cap > 0:
+            assert torch.isfinite(t[pick]).all()
+            check_beside(o, lse, ref, torch.zeros_like(pick[..., 0]), v, rel, "capped")
+            continue
+        bad = (torch.isposinf(t) & pick).any(-1)
+        none = pick.any(-1) & (torch.isneginf(t) | ~pick).all(-1)     # nothing but -inf: LSE = -inf, O is not defined
+        assert bad.any() and torch.isneginf(lse[none]).all()
+        live = ref[1].any(-1) & ~none
+        p = torch.where(bad[..., None], 0.0, ref[3])
+        ref = (t, pick & live[..., None], ref[2], p, torch.where(live[..., None], p @ v.double(), 0.0), ref[5])
+        check_beside(torch.where(none[..., None], 0.0, o.float()), lse, ref, bad, v, rel, "uncapped")
+
+
+@pytest.mark.parametrize("cap", CAPS)
+def test_infinity_in_a_value(cap):
+    """An infinite value is infinite (or NaN) in its column of O for the rows that see its key, and nothing else: LSE
+    and the other columns are as they would be. (128-token blocks: a pair's other block has weights of zero there.)"""
+    s, g, mask, plan, rp, ci, chosen = setting(DIMS[0], 47, "all")
+    q, k, v, _ = inputs(s, g)
+    scale = s.d ** -0.5
+    ref = reference(s, q, k, v, chosen, mask, scale, cap)
+    v2 = v.clone()
+    v2[:, :, 5, 9] = math.inf
+    o, lse = sp.attn_masked_fwd(s, q, k, v2, rp, ci, scale, cap, plan)
+    sees = ref[1][..., 5]
+    assert sees.any() and not torch.isfinite(o[..., 9][sees]).any()
+    o = o.clone()
+    o[..., 9] = torch.where(sees, ref[4][..., 9].bfloat16(), o[..., 9])
+    check_forward(s, o, lse, ref, q, k, v, scale, cap)
