@@ -224,6 +224,19 @@ def _buffer(name: str, t, dtype, dev: int, optional: bool = False):
     return t.data_ptr()
 
 
+def _whole(shape: Shape, name: str, t, optional: bool = False):
+    """Refuses a Q-sized tensor of the reorder's layouts that is not one contiguous
+    piece of (at least) B*N*H*d values: those calls take its address alone."""
+    if t is None and optional or isinstance(t, int):
+        return
+    s = shape
+    n, size = s.B * s.N * s.H * s.d, 4 if s.dtype == F32 else 2
+    if not isinstance(t, torch.Tensor) or not t.is_contiguous() or t.numel() < n or t.element_size() != size:
+        got = (tuple(t.shape), t.dtype, t.stride()) if isinstance(t, torch.Tensor) else t
+        raise ValueError(f"{name}: expected a contiguous tensor of {s.B} x {s.N} x {s.H} x {s.d} {s.torch_dtype} values, "
+                         f"got {got}")
+
+
 def _space(ws, dev: int) -> tuple:
     """(address, bytes) of a workspace tensor."""
     if ws.get_device() != dev or not ws.is_contiguous():
@@ -369,6 +382,8 @@ def rope(shape: Shape, table: RopeTable, x, out=None, inverse: bool = False, in_
 def reorder(shape: Shape, x: torch.Tensor, out: torch.Tensor | None = None, inverse: bool = False,
             stream=None) -> torch.Tensor:
     """Raster [B,N,H,d] -> blocked [B,H,N,d] (or back with inverse=True)."""
+    _whole(shape, "x", x)
+    _whole(shape, "out", out, True)
     if out is None:
         dims = (shape.B, shape.N, shape.H, shape.d) if inverse else (shape.B, shape.H, shape.N, shape.d)
         out = torch.empty(dims, dtype=x.dtype, device=x.device)
@@ -397,6 +412,8 @@ def block_scores(shape: Shape, q, k, estimator=EST_MEAN, wq=None, wk=None, rank=
 def reorder_pool(shape: Shape, x: torch.Tensor, out: torch.Tensor | None = None,
                  means: torch.Tensor | None = None, stream=None):
     """Raster -> blocked, plus the fp32 tile means [B, H, nb, d] from the same pass."""
+    _whole(shape, "x", x)
+    _whole(shape, "out", out, True)
     if out is None:
         out = torch.empty((shape.B, shape.H, shape.N, shape.d), dtype=x.dtype, device=x.device)
     if means is None:
@@ -408,6 +425,7 @@ def reorder_pool(shape: Shape, x: torch.Tensor, out: torch.Tensor | None = None,
 
 def pool_means(shape: Shape, x: torch.Tensor, means: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """The fp32 tile means [B, H, nb, d] of raster x alone (no reordered copy)."""
+    _whole(shape, "x", x)
     if means is None:
         means = torch.empty((shape.B, shape.H, shape.nb, shape.d), dtype=torch.float32, device=x.device)
     _check("sparsp_reorder_pool", lib().sparsp_reorder_pool(_sref(shape), _ptr(x), None, _ptr(means),

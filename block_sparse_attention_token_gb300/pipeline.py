@@ -31,7 +31,7 @@ from . import (EST_LOWRANK, EST_MEAN, PROF_SLOTS, Shape, attn_bwd, attn_fwd, att
                norm_workspace_size, rope as rope_turn, RopeTable,
                block_scores, block_scores_pooled, block_scores_workspace_size, kv_demand, kv_gather, lib, placement,
                placement_workspace_size, reorder, reorder_pool, select, select_workspace_size, DemandOut,
-               OUT_RASTER, IN_RASTER, pool_means)
+               OUT_RASTER, IN_RASTER, pool_means, _whole)
 
 
 @dataclasses.dataclass
@@ -242,8 +242,12 @@ class Pipeline:
         their own streams, each preceded by a "<stage>:begin" mark, and the
         region they share by "overlap". out: optional raster output buffer
         (default: self.o). before: optional callable(name) invoked just before
-        input "q", "k" or "v" is first read (e.g. to wait for its copy)."""
+        input "q", "k" or "v" is first read (e.g. to wait for its copy). All are
+        contiguous raster tensors, but q and k that a norm or a rotation reads may be
+        slices of a wider one (one stride between tokens); ValueError otherwise."""
         s = self.shape
+        _whole(s, "v", v)
+        _whole(s, "out", out, True)
         mark = mark or (lambda name, stream=None: None)
         before = before or (lambda name: None)
         def prepared(name, x, normed, stats, weight, bias, turned, blocked, means):
@@ -364,8 +368,15 @@ class Pipeline:
         With raster_out the backward reads O from the buffer the last forward()
         wrote it to, which must still hold it, and writes the gradients' raster
         rows itself. With a norm it reads forward()'s q and k, which must still hold
-        their values, and writes the weights' gradients to self.norm_grads."""
+        their values, and writes the weights' gradients to self.norm_grads. dout and
+        outs are contiguous, but dQ and dK that a rotation or a norm writes may be
+        slices like forward()'s q and k."""
         s = self.shape
+        _whole(s, "dout", dout)
+        if outs is not None:
+            for name, t in zip(("dq", "dk", "dv"), outs):
+                if name == "dv" or self.rope is None and self.norm is None:
+                    _whole(s, name, t)
         mark = mark or (lambda name: None)
         if before is not None:   # e.g. to wait for dout's copy
             before("do")
