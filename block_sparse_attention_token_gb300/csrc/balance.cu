@@ -10,7 +10,8 @@
 //  aug_keys_kernel - one warp per CSR row: each unselected block's value
 //                    v = fl32(e_j / Z) (e_j = expf(S_j - max) in fp32, Z summed
 //                    in fp64), stored as the orderable key bits(v) + 1; selected
-//                    blocks get key 0. Also writes the row's base count. Rows
+//                    blocks and masked pairs (SPARSP_MASKED_SCORE) get key 0. Also
+//                    writes the row's base count. Rows
 //                    of ranks without slack get no keys (nothing is read there).
 //  aug_slack/count/hist/digit kernels - per (batch element, rank): slack =
 //                    L* - L_r; candidates and the 8-bit digit histograms of a
@@ -228,7 +229,7 @@ aug_keys_kernel(const float* __restrict__ scores, const int32_t* __restrict__ ro
     for (int n = c - cpre[w]; n > 0; --n) x &= x - 1u;   // drop the lower candidates of the word
     const int j = w * 32 + __ffs(x) - 1;
     const float v = (float)((double)expf(S[j] - m) / Z);
-    K[j] = __float_as_uint(v) + 1u;
+    K[j] = S[j] == SPARSP_MASKED_SCORE ? 0u : __float_as_uint(v) + 1u;   // attention would leave a masked pair out
   }
 }
 

@@ -347,7 +347,8 @@ SPARSP_API sparsp_status_t sparsp_balance_heads(const sparsp_shape_t* shape, int
  * unselected blocks (h, i, j) of largest value v = fl32(e_j / Z), where
  * e_j = exp(S_j - max_j S) in fp32 and Z = sum_j e_j in fp64 over the row of
  * scores (the mass selection assigns the block), ties by row (b*H + h)*nb + i
- * then j ascending. The critical load is unchanged.
+ * then j ascending. A block whose score is SPARSP_MASKED_SCORE
+ * (sparsp_mask_scores) is no candidate. The critical load is unchanged.
  *   scores       float32 [B, H, nb, nb]: the block scores selection ran on.
  *   row_ptr/col_idx: the selection's CSR (ascending rows).
  *   row_ptr_out  int32 [B*H*nb + 1], col_idx_out int32 [col_cap]: the augmented

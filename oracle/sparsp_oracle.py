@@ -665,6 +665,9 @@ def balance_heads(costs, P, max_migrations):
     return head_rank, moves
 
 
+MASKED_SCORE = np.float32(-1.0e30)   # the score of a pair of blocks that see nothing of each other
+
+
 def block_values(S) -> np.ndarray:
     """The value of every block of a row: its softmax mass, taken as selection
     takes it (e_j = exp(S_j - max) correctly rounded to float32, Z = sum e in
@@ -700,8 +703,9 @@ def augment(S, row_ptr, col_idx, B, H, nb, head_rank, P) -> Augmented:
     Its candidates are the unselected blocks (h, i, j) of the rows of its
     heads, valued by block_values; it takes the min(slack, #candidates) best,
     ordered by (value descending, row (b*H + h)*nb + i ascending, j ascending).
-    The critical path (L*) is unchanged. Returns the augmented CSR (rows stay
-    ascending) with per-rank counts.
+    A block whose score is MASKED_SCORE (nobody in the row sees it) is no
+    candidate. The critical path (L*) is unchanged. Returns the augmented CSR
+    (rows stay ascending) with per-rank counts.
     """
     V = block_values(S)
     rp = np.asarray(row_ptr, dtype=np.int64)
@@ -722,7 +726,7 @@ def augment(S, row_ptr, col_idx, B, H, nb, head_rank, P) -> Augmented:
                 for i in range(nb):
                     row = (b * H + h) * nb + i
                     for j in range(nb):
-                        if j not in rows[row]:
+                        if j not in rows[row] and S[row, j] != MASKED_SCORE:
                             cands.append((-float(V[row, j]), row, j))
             cands.sort()
             take = min(top - int(loads[r]), len(cands))
