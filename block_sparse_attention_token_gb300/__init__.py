@@ -30,6 +30,7 @@ KERNEL_PORTABLE = 2
 BWD_SPLIT_KV = 4
 OUT_RASTER = 8
 IN_RASTER = 16
+LISTS_SEEN = 32
 GRID_CAP_SHIFT = 16
 MASKED_SCORE = -1.0e30
 NORM_RMS, NORM_HEAD = 1, 2
@@ -130,6 +131,8 @@ _SIG = {
     "sparsp_mask_plan_size": (ctypes.c_size_t, [_P]),
     "sparsp_mask_plan": (_I32, [_P, _P, _P, _P, _P, ctypes.c_size_t, _P]),
     "sparsp_mask_scores": (_I32, [_P, _P, _P, _P]),
+    "sparsp_mask_csr": (_I32, [_P, _P, _P, _P, _P, _P, _P, _P]),
+    "sparsp_attn_masked_compacts": (_I32, [_P, _I32]),
     "sparsp_attn_masked_workspace_size": (ctypes.c_size_t, [_P, _I32]),
     "sparsp_attn_masked_fwd": (_I32, [_P, _P, _P, _P, _P, _P, ctypes.c_float, ctypes.c_float, _P, _P, _P, _P,
                                       ctypes.c_size_t, ctypes.c_uint32, _P, _P, _P]),
@@ -733,6 +736,30 @@ def mask_scores(shape: Shape, mask: MaskPlan, scores, stream=None) -> torch.Tens
     _check("sparsp_mask_scores", lib().sparsp_mask_scores(_sref(shape), _plan_ptr(shape, mask, dev), at,
                                                           _stream(stream)))
     return scores
+
+
+def mask_csr(shape: Shape, mask: MaskPlan, row_ptr, col_idx, row_ptr_out=None, col_idx_out=None, status=None,
+             stream=None):
+    """The rows of a CSR without the block pairs that see nothing of each other (what the
+    selection picks of them has no part in attention, and none in its demand or cost).
+    Returns (row_ptr_out, col_idx_out); col_idx_out holds at least B*H*nb*nb entries."""
+    s, i32, dev = shape, torch.int32, torch.cuda.current_device()
+    if row_ptr_out is None:
+        row_ptr_out = _new(stream, s.rows + 1, i32, row_ptr.device)
+    if col_idx_out is None:
+        col_idx_out = _new(stream, s.rows * s.nb, i32, row_ptr.device)
+    elif isinstance(col_idx_out, torch.Tensor) and col_idx_out.numel() < s.rows * s.nb:
+        raise ValueError(f"mask_csr: col_idx_out holds {col_idx_out.numel()} of up to {s.rows * s.nb} entries")
+    _check("sparsp_mask_csr", lib().sparsp_mask_csr(
+        _sref(s), _plan_ptr(s, mask, dev), _want("row_ptr", row_ptr, (s.rows + 1,), i32, dev),
+        _buffer("col_idx", col_idx, i32, dev), _want("row_ptr_out", row_ptr_out, (s.rows + 1,), i32, dev),
+        _buffer("col_idx_out", col_idx_out, i32, dev), _buffer("status", status, i32, dev, True), _stream(stream)))
+    return row_ptr_out, col_idx_out
+
+
+def attn_masked_compacts(shape: Shape, backward: bool = False) -> bool:
+    """Does masked attention of this shape run mask_csr on its lists itself (without LISTS_SEEN)?"""
+    return lib().sparsp_attn_masked_compacts(_sref(shape), int(backward)) != 0
 
 
 def attn_masked_workspace_size(shape: Shape, backward: bool = False) -> int:

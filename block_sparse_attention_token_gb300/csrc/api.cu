@@ -54,7 +54,7 @@ size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 
 // Every attention option bit; a call ignores the ones that do not concern it.
 constexpr uint32_t kKnownFlags = SPARSP_SCHED_FLAT | SPARSP_KERNEL_PORTABLE | SPARSP_BWD_SPLIT_KV |
-                                 SPARSP_OUT_RASTER | SPARSP_IN_RASTER | SPARSP_GRID_CAP_MASK;
+                                 SPARSP_OUT_RASTER | SPARSP_IN_RASTER | SPARSP_LISTS_SEEN | SPARSP_GRID_CAP_MASK;
 
 // Attention workspace layout: items, counter(s), then backward extras.
 struct AttnWs {
@@ -197,7 +197,7 @@ sparsp_status_t attn_fwd(const sparsp_shape_t* shape, const void* q, const void*
   masked = plan != nullptr || cap > 0.f;
   cudaStream_t st = (cudaStream_t)stream;
   const MaskView mask = mask_view(s, plan);
-  if (plan != nullptr && drops_unseen(s, attn_fwd_tc_items_per_head(s))) {
+  if (plan != nullptr && !(flags & SPARSP_LISTS_SEEN) && drops_unseen(s, attn_fwd_tc_items_per_head(s))) {
     r = launch_mask_csr(s, mask, row_ptr, col_idx, w.seen_ptr, w.seen_idx, d_status, st);
     if (r != SPARSP_OK) return r;
     row_ptr = w.seen_ptr;
@@ -284,7 +284,7 @@ sparsp_status_t attn_bwd(const sparsp_shape_t* shape, const void* q, const void*
   if (masked && !tc) return SPARSP_ERR_UNSUPPORTED;
   masked = plan != nullptr || cap > 0.f;
   const MaskView mask = mask_view(s, plan);
-  if (plan != nullptr && drops_unseen(s, attn_bwd_tc_items_per_head(s))) {
+  if (plan != nullptr && !(flags & SPARSP_LISTS_SEEN) && drops_unseen(s, attn_bwd_tc_items_per_head(s))) {
     r = launch_mask_csr(s, mask, row_ptr, col_idx, w.seen_ptr, w.seen_idx, d_status, st);
     if (r != SPARSP_OK) return r;
     row_ptr = w.seen_ptr;
@@ -766,6 +766,30 @@ sparsp_status_t sparsp_mask_scores(const sparsp_shape_t* shape, const void* plan
   CHECK_PTR(plan);
   CHECK_PTR(scores);
   return launch_mask_scores(s, mask_view(s, plan), scores, (cudaStream_t)stream);
+}
+
+sparsp_status_t sparsp_mask_csr(const sparsp_shape_t* shape, const void* plan, const int32_t* row_ptr,
+                                const int32_t* col_idx, int32_t* row_ptr_out, int32_t* col_idx_out, int32_t* d_status,
+                                sparsp_stream_t stream) {
+  Dims s;
+  sparsp_status_t r = check_shape(shape, &s);
+  if (r != SPARSP_OK) return r;
+  CHECK_PTR(plan);
+  CHECK_PTR(row_ptr);
+  CHECK_PTR(col_idx);
+  CHECK_PTR(row_ptr_out);
+  CHECK_PTR(col_idx_out);
+  CHECK_OPT_PTR(d_status);
+  const uintptr_t a = (uintptr_t)row_ptr, b = (uintptr_t)row_ptr_out, n = (uintptr_t)(s.rows() + 1) * sizeof(int32_t);
+  if ((a < b + n && b < a + n) || col_idx == col_idx_out) return SPARSP_ERR_INVALID_ARG;   // overlap
+  return launch_mask_csr(s, mask_view(s, plan), row_ptr, col_idx, row_ptr_out, col_idx_out, d_status,
+                         (cudaStream_t)stream);
+}
+
+int32_t sparsp_attn_masked_compacts(const sparsp_shape_t* shape, int32_t backward) {
+  Dims s;
+  if (check_shape(shape, &s) != SPARSP_OK) return 0;
+  return drops_unseen(s, backward ? attn_bwd_tc_items_per_head(s) : attn_fwd_tc_items_per_head(s)) ? 1 : 0;
 }
 
 size_t sparsp_attn_masked_workspace_size(const sparsp_shape_t* shape, int32_t backward) {

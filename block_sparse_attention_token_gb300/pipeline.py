@@ -9,8 +9,9 @@ partitions -> KV demand of P partitions (+ gather) -> block-sparse attention
 kernel runs, else by an inverse reorder). backward(): dO into tiles ->
 attention backward -> dQ, dK, dV in raster order (likewise) -> (optional) inverse
 rotation and norm backward, with the gradients of the norm's weights. With a token
-mask, block pairs that see nothing of each other are masked before the selection,
-and attention runs over the tokens that the mask lets through; a score cap
+mask, block pairs that see nothing of each other are masked before the selection and
+leave its lists after it (balancing, augmentation, placement and the KV demand count the
+others), and attention runs over the tokens that the mask lets through; a score cap
 applies in attention alone. Every step is one
 or more libsparsp kernels on the current stream, except that by default the
 KV demand gather runs on a side
@@ -27,7 +28,8 @@ import torch
 
 from . import (EST_LOWRANK, EST_MEAN, PROF_SLOTS, Shape, attn_bwd, attn_fwd, attn_workspace_size, augment,
                augment_workspace_size, balance_heads, Balance, predictor_fit,
-               attn_masked_bwd, attn_masked_fwd, attn_masked_workspace_size, MaskPlan, mask_scores, norm_bwd, norm_fwd,
+               attn_masked_bwd, attn_masked_compacts, attn_masked_fwd, attn_masked_workspace_size, LISTS_SEEN, MaskPlan,
+               mask_csr, mask_scores, norm_bwd, norm_fwd,
                norm_workspace_size, rope as rope_turn, RopeTable,
                block_scores, block_scores_pooled, block_scores_workspace_size, kv_demand, kv_gather, lib, placement,
                placement_workspace_size, reorder, reorder_pool, select, select_workspace_size, DemandOut,
@@ -203,7 +205,14 @@ class Pipeline:
             self.col_idx_aug = torch.empty(s.rows * s.nb, dtype=torch.int32, device=dev)
             self.added = torch.empty((s.B, P), dtype=torch.int64, device=dev)
             self.ws_aug = torch.empty(max(augment_workspace_size(s, P), 16), dtype=torch.uint8, device=dev)
-        self.csr = (self.row_ptr, self.col_idx)
+        self.csr = (self.row_ptr, self.col_idx)   # the lists attention runs on
+        self._lists_flag = 0
+        if mask is not None:
+            # the selected pairs that see something; attention runs on them where it would make
+            # the same lists itself
+            self.row_ptr_seen = torch.empty(s.rows + 1, dtype=torch.int32, device=dev)
+            self.col_idx_seen = torch.empty(s.rows * s.nb, dtype=torch.int32, device=dev)
+            self._attn_on_seen = attn_masked_compacts(s)
         self.owner = self.ws_place = None
         if placement:
             self.owner = torch.empty((s.B, s.nb), dtype=torch.int32, device=dev)
@@ -292,16 +301,21 @@ class Pipeline:
                           self.gwq, self.gwk, self.ws_pred)
             mark("predictor")
         select(s, self.scores, self.top_p, self.k_floor, self.row_ptr, self.col_idx, self.ws_sel, self.status)
-        mark("select")
         rp, ci = self.row_ptr, self.col_idx
+        self.csr, self._lists_flag = (rp, ci), 0
+        if self.mask is not None:
+            rp, ci = mask_csr(s, self.mask, rp, ci, self.row_ptr_seen, self.col_idx_seen, self.status)
+            if self._attn_on_seen or self.augment:
+                self.csr, self._lists_flag = (rp, ci), LISTS_SEEN
+        mark("select")
         if self.balance is not None:
-            balance_heads(s, self.P, self.row_ptr, self.migrations, out=self.balance)
+            balance_heads(s, self.P, rp, self.migrations, out=self.balance)
             mark("balance")
         if self.augment:
-            rp, ci, _ = augment(s, self.P, self.scores, self.row_ptr, self.col_idx, self.balance.head_rank,
+            rp, ci, _ = augment(s, self.P, self.scores, rp, ci, self.balance.head_rank,
                                 self.row_ptr_aug, self.col_idx_aug, self.added, self.ws_aug, self.status)
+            self.csr = (rp, ci)
             mark("augment")
-        self.csr = (rp, ci)
         if self.owner is not None:
             placement(s, self.P, rp, ci, self.owner, self.ws_place, self.status)
             mark("placement")
@@ -316,10 +330,10 @@ class Pipeline:
         def attention(stream=None):
             p = self.prof if prof else None
             if self.mask is not None or self.cap:
-                attn_masked_fwd(s, aq, ak, av, rp, ci, 0.0, self.cap, self.mask, o_attn, self.lse, self.ws_attn,
-                                aflags, p, self.status, stream)
+                attn_masked_fwd(s, aq, ak, av, *self.csr, 0.0, self.cap, self.mask, o_attn, self.lse, self.ws_attn,
+                                aflags | self._lists_flag, p, self.status, stream)
             else:
-                attn_fwd(s, aq, ak, av, rp, ci, 0.0, o_attn, self.lse, self.ws_attn, aflags, p, self.status, stream)
+                attn_fwd(s, aq, ak, av, *self.csr, 0.0, o_attn, self.lse, self.ws_attn, aflags, p, self.status, stream)
 
         if self.overlap_demand and self.demand.kg is not None:
             # the lists (bitmap, offsets, indices) first, on this stream: they need a
@@ -390,11 +404,11 @@ class Pipeline:
             if self._o_fwd is None:
                 raise RuntimeError("backward() needs a forward() first")
             args = (s, self.qb, self.kb, self.vb, self._o_fwd, self.lse, self.dob, rp, ci, 0.0)
-            rest = (gq, gk, dv, self.ws_attn, self.flags | OUT_RASTER, p, self.status)
             if self.mask is not None or self.cap:
-                attn_masked_bwd(*args, self.cap, self.mask, *rest)
+                attn_masked_bwd(*args, self.cap, self.mask, gq, gk, dv, self.ws_attn,
+                                self.flags | OUT_RASTER | self._lists_flag, p, self.status)
             else:
-                attn_bwd(*args, *rest)
+                attn_bwd(*args, gq, gk, dv, self.ws_attn, self.flags | OUT_RASTER, p, self.status)
             mark("attn_bwd")
         else:
             attn_bwd(s, self.qb, self.kb, self.vb, self.ob, self.lse, self.dob, rp, ci, 0.0,

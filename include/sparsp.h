@@ -118,7 +118,11 @@ enum {
    * as one 5-D tile (column, head, x, y, frame), so no reorder pass is needed.
    * Results are bitwise those of the block-ordered inputs. Only the tcgen05
    * kernel does this; elsewhere SPARSP_ERR_UNSUPPORTED. */
-  SPARSP_IN_RASTER = 1u << 4
+  SPARSP_IN_RASTER = 1u << 4,
+  /* Masked attention: row_ptr and col_idx come from sparsp_mask_csr with this
+   * plan (or are augmented from there without masked pairs), so that the call
+   * need not look for pairs that see nothing of each other itself. */
+  SPARSP_LISTS_SEEN = 1u << 5
 };
 /* Attention kernels: at most n persistent CTAs (1 <= n <= 4095) instead of
  * one per SM (times the kernel's occupancy), encoded in bits 16..27 of the
@@ -577,6 +581,22 @@ SPARSP_API sparsp_status_t sparsp_mask_plan(const sparsp_shape_t* shape, const i
 #define SPARSP_MASKED_SCORE (-1.0e30f)
 SPARSP_API sparsp_status_t sparsp_mask_scores(const sparsp_shape_t* shape, const void* plan, float* scores,
                                               sparsp_stream_t stream);
+/*
+ * The rows of a CSR without the pairs of blocks whose ranges show that none of
+ * the query tokens sees any of the keys, in their order: what balancing,
+ * augmentation, placement, the KV demand and attention have to do with a
+ * selection under this mask (sparsp_select picks such pairs where a row has no
+ * others, or fewer than its floor). row_ptr_out [B*H*nb + 1], col_idx_out
+ * [B*H*nb*nb]; neither may be the input's. A malformed row (an index outside
+ * [0, nb), more than nb entries) becomes empty and sets SPARSP_ERR_DATA.
+ */
+SPARSP_API sparsp_status_t sparsp_mask_csr(const sparsp_shape_t* shape, const void* plan, const int32_t* row_ptr,
+                                           const int32_t* col_idx, int32_t* row_ptr_out, int32_t* col_idx_out,
+                                           int32_t* d_status, sparsp_stream_t stream);
+/* 1 where masked attention of this shape takes such pairs out of its lists itself
+ * before the work is ordered (without SPARSP_LISTS_SEEN), 0 where it leaves them to
+ * the kernel, which skips what they hold: in shapes so small that this costs less. */
+SPARSP_API int32_t sparsp_attn_masked_compacts(const sparsp_shape_t* shape, int32_t backward);
 /*
  * sparsp_attn_fwd with a token mask and a cap on the scores: over the keys k of
  * the selected blocks that q sees,

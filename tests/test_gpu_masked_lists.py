@@ -69,3 +69,104 @@ def test_augment_leaves_masked_pairs(dims, P):
     assert host(added).tolist() == ref.added.tolist()
     V = np.where(S_ == orc.MASKED_SCORE, np.float32(0), orc.block_values(S_))
     compare_augmented(host(rp2), host(ci2), ref, host(rp), host(ci), V, host(hr), s.B, s.H, s.nb, P)
+
+
+@pytest.mark.parametrize("dims", DIMS)
+def test_mask_csr(dims):
+    """The rows' pairs that see something, in their order; a malformed row is empty and reported; attention on these
+    lists gives the bits of its own compaction."""
+    s = sp.make_shape(*dims, "bf16")
+    g = gen(52)
+    mask, meet = padded(s)
+    plan = sp.mask_plan(s, *mask)
+    chosen = torch.rand(s.B, s.H, s.nb, s.nb, generator=g, device="cuda") < 0.6
+    rp, ci = csr_of(chosen)
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    rp2, ci2 = sp.mask_csr(s, plan, rp, ci, status=st)
+    want = csr_of(chosen & meet[:, None])
+    n = int(rp2[-1])
+    assert int(st) == 0 and torch.equal(rp2, want[0]) and torch.equal(ci2[:n], want[1][:n])
+    # rows keep their own order
+    back = torch.cat([ci[int(a):int(b)].flip(0) for a, b in zip(rp[:-1], rp[1:])] + [ci[-4:]])
+    rp3, ci3 = sp.mask_csr(s, plan, rp, back)
+    assert torch.equal(rp3, rp2)
+    assert torch.equal(ci3[:n], torch.cat([ci2[int(a):int(b)].flip(0) for a, b in zip(rp2[:-1], rp2[1:])]))
+    q, k, v = (torch.randn(s.B, s.H, s.N, s.d, generator=g, device="cuda").bfloat16() for _ in range(3))
+    one = sp.attn_masked_fwd(s, q, k, v, rp2, ci2, mask=plan, flags=sp.LISTS_SEEN)
+    two = sp.attn_masked_fwd(s, q, k, v, rp2, ci2, mask=plan)
+    assert all(torch.equal(a, b) for a, b in zip(one, two))
+    grads = [sp.attn_masked_bwd(s, q, k, v, *one, v, rp2, ci2, mask=plan, flags=f) for f in (0, sp.LISTS_SEEN)]
+    assert all(torch.equal(a, b) for a, b in zip(*grads))
+    if sp.attn_masked_compacts(s):
+        two = sp.attn_masked_fwd(s, q, k, v, rp, ci, mask=plan)
+        assert all(torch.equal(a, b) for a, b in zip(one, two))
+    # malformed: an index out of range in row 3; row 5 longer than it may be, and row 4 if it then ends before it begins
+    bad = ci.clone()
+    bad[int(rp[3])] = s.nb
+    long = rp.clone()
+    long[5] = int(rp[6]) - s.nb - 1
+    if int(long[5]) < 0:
+        long[5] = 0
+    size = long[1:] - long[:-1]
+    for r, c, rows in ((rp, bad, [3]), (long, ci, ((size < 0) | (size > s.nb)).nonzero()[:, 0].tolist())):
+        assert rows
+        st.zero_()
+        rp4, ci4 = sp.mask_csr(s, plan, r, c, status=st)
+        assert int(st) == sp.DATA
+        for x in rows:
+            assert int(rp4[x]) == int(rp4[x + 1])
+        assert int(rp4[3] - rp4[2]) == int(rp2[3] - rp2[2])
+
+
+@pytest.mark.parametrize("dims", DIMS)
+@pytest.mark.parametrize("augmented", [False, True])
+def test_pipeline_counts_pairs_that_see_something(dims, augmented):
+    """Padding tiles, whose rows select as if all scores were equal, and a floor above what some rows see: neither the
+    heads' costs, nor augmentation, nor the demand of a partition holds a block for a query block that sees nothing
+    of it, and attention gives the same values."""
+    s = sp.make_shape(*dims, "bf16")
+    g = gen(53)
+    mask, meet = padded(s)
+    plan = sp.mask_plan(s, *mask)
+    q, k, v, do = (torch.randn(s.B, s.N, s.H, s.d, generator=g, device="cuda").bfloat16() for _ in range(4))
+    P, floor = 3, int(meet.sum(-1).amax())
+    kw = dict(migrations=2, augment=True) if augmented else {}
+    pipe = sp.Pipeline(s, "mean", 0.7, floor, P, mask=plan, backward=True, **kw)
+    o, lse = (t.clone() for t in pipe.forward(q, k, v))
+    grads = [t.clone() for t in pipe.backward(do)]
+    assert int(pipe.status) == 0
+    picked = chosen_of(s, pipe.row_ptr, pipe.col_idx)
+    assert (picked & ~meet[:, None]).any()          # the selection itself has such pairs
+    lists = picked & meet[:, None]
+    if augmented:
+        assert host(pipe.balance.loads)[:, 0].sum(-1).tolist() == lists.flatten(1).sum(1).tolist()
+        final = chosen_of(s, *pipe.csr)
+        assert (meet[:, None] | ~final).all() and (final | ~lists).all()
+        assert int(pipe.added.sum()) == int(final.sum()) - int(lists.sum())
+        lists = final
+    edges = [r * s.nb // P for r in range(P + 1)]
+    want = torch.stack([lists[:, :, a:b].any(2) for a, b in zip(edges, edges[1:])], 2).view(-1, s.nb)
+    dem = pipe.demand
+    n = int(dem.dem_ptr[-1])
+    got = torch.zeros_like(want)
+    got[torch.repeat_interleave(torch.arange(want.shape[0], device="cuda"),
+                                (dem.dem_ptr[1:] - dem.dem_ptr[:-1]).long()), dem.dem_idx[:n].long()] = True
+    assert torch.equal(got, want) and n == int(want.sum())
+    rows = got.nonzero()
+    kb = sp.reorder(s, k).view(s.B * s.H, s.nb, s.Bt, s.d)
+    assert torch.equal(dem.kg[:n], kb[rows[:, 0] // P, rows[:, 1]])
+    # the same values as attention on the selection (with what was added) under the mask
+    rp, ci = csr_of(lists)
+    ins = [sp.reorder(s, x) for x in (q, k, v, do)]
+    o2, lse2 = sp.attn_masked_fwd(s, *ins[:3], rp, ci, mask=plan, flags=sp.OUT_RASTER)
+    seen = torch.isfinite(lse2)
+    assert torch.equal(seen, torch.isfinite(lse))
+    assert torch.allclose(lse[seen], lse2[seen], rtol=0, atol=2e-6) and float((o.float() - o2.float()).norm() / o2.float().norm()) < 2.0 ** -8
+    g2 = sp.attn_masked_bwd(s, *ins[:3], o2, lse2, ins[3], rp, ci, mask=plan, flags=sp.OUT_RASTER)
+    for a, b in zip(grads, g2):
+        assert float((a.float() - b.float()).norm() / b.float().norm()) < 2.0 ** -7
+    # placement takes the same lists
+    if not augmented:
+        placed = sp.Pipeline(s, "mean", 0.7, floor, P, mask=plan, placement=True)
+        placed.forward(q, k, v)
+        assert torch.equal(placed.owner, sp.placement(s, P, rp, ci))
