@@ -133,6 +133,7 @@ _SIG = {
     "sparsp_mask_scores": (_I32, [_P, _P, _P, _P]),
     "sparsp_mask_csr": (_I32, [_P, _P, _P, _P, _P, _P, _P, _P]),
     "sparsp_attn_masked_compacts": (_I32, [_P, _I32]),
+    "sparsp_attn_launches": (_I32, [_P, _I32, _I32, ctypes.c_float, ctypes.c_uint32]),
     "sparsp_attn_masked_workspace_size": (ctypes.c_size_t, [_P, _I32]),
     "sparsp_attn_masked_fwd": (_I32, [_P, _P, _P, _P, _P, _P, ctypes.c_float, ctypes.c_float, _P, _P, _P, _P,
                                       ctypes.c_size_t, ctypes.c_uint32, _P, _P, _P]),
@@ -631,6 +632,11 @@ def csr_transpose(shape: Shape, row_ptr, col_idx, nnz_cap=None, status=None, str
         _sref(shape), _ptr(row_ptr), _ptr(col_idx), _ptr(col_ptr), _ptr(row_idx), _ptr(status),
         _stream(stream)))
     return col_ptr, row_idx
+
+
+def attn_launches(shape: Shape, backward: bool = False, plan: bool = False, cap: float = 0.0, flags: int = 0) -> int:
+    """The number of kernels that attention with these arguments launches."""
+    return lib().sparsp_attn_launches(_sref(shape), int(backward), int(plan), cap, int(flags))
 
 
 def attn_workspace_size(shape: Shape, backward: bool = False) -> int:

@@ -162,6 +162,33 @@ bool drops_unseen(const Dims& s, int items_per_head) {
   return sms <= 0 || per_sm * items_per_head > 16;
 }
 
+// What an attention call launches, decided in one place for the call and for
+// sparsp_attn_launches.
+struct AttnSteps {
+  bool tc;          // the tcgen05 kernels
+  bool masked;      // a token mask or a cap
+  bool compacts;    // three launches that drop the pairs that see nothing of each other
+  bool one_order;   // the work is ordered by one launch (order_items)
+  bool pairs;       // items are pairs of 64-token blocks, whose costs take a launch first
+  bool flat;        // SPARSP_SCHED_FLAT
+  bool twice;       // forward: the general kernel follows over the items passed on to it
+  int per_head;     // items per head
+  int order_launches() const { return one_order ? 1 : (pairs ? 1 : 0) + (flat ? 2 : 1); }
+};
+AttnSteps attn_steps(const Dims& s, uint32_t flags, bool plan, float cap, bool backward) {
+  AttnSteps a{};
+  a.tc = s.dtype == SPARSP_BF16 && !(flags & SPARSP_KERNEL_PORTABLE) &&
+         (backward ? attn_bwd_tc_supported(s) : attn_fwd_tc_supported(s));
+  a.masked = plan || cap > 0.f;
+  a.per_head = !a.tc ? s.nb : backward ? attn_bwd_tc_items_per_head(s) : attn_fwd_tc_items_per_head(s);
+  a.compacts = plan && !(flags & SPARSP_LISTS_SEEN) && drops_unseen(s, a.per_head);
+  a.one_order = a.masked && order_items_fits(s, a.per_head, plan);
+  a.pairs = a.per_head != s.nb;
+  a.flat = (flags & SPARSP_SCHED_FLAT) != 0;
+  a.twice = a.masked && !(cap > 0.f && cap <= kFixedCap);
+  return a;
+}
+
 // sparsp_attn_fwd, and sparsp_attn_masked_fwd with `masked`: both validate alike;
 // a masked call without plan and cap is the plain one.
 sparsp_status_t attn_fwd(const sparsp_shape_t* shape, const void* q, const void* k, const void* v,
@@ -189,36 +216,36 @@ sparsp_status_t attn_fwd(const sparsp_shape_t* shape, const void* q, const void*
   AttnWs w = attn_ws_layout(s, false, ws, masked);
   if (ws_bytes < w.bytes) return SPARSP_ERR_WORKSPACE;
   if (scale <= 0.f) scale = 1.0f / sqrtf((float)s.d);
-  const bool tc = s.dtype != SPARSP_F32 && !(flags & SPARSP_KERNEL_PORTABLE) && attn_fwd_tc_supported(s);
+  const AttnSteps steps = attn_steps(s, flags, plan != nullptr, cap, false);
+  const bool tc = steps.tc;
   const bool raster = (flags & SPARSP_OUT_RASTER) != 0;
   const bool in_raster = (flags & SPARSP_IN_RASTER) != 0;
   if ((raster || in_raster) && !tc) return SPARSP_ERR_UNSUPPORTED;   // only the tcgen05 kernel reads or writes raster rows
   if (masked && !tc) return SPARSP_ERR_UNSUPPORTED;
-  masked = plan != nullptr || cap > 0.f;
+  masked = steps.masked;
   cudaStream_t st = (cudaStream_t)stream;
   const MaskView mask = mask_view(s, plan);
-  if (plan != nullptr && !(flags & SPARSP_LISTS_SEEN) && drops_unseen(s, attn_fwd_tc_items_per_head(s))) {
+  if (steps.compacts) {
     r = launch_mask_csr(s, mask, row_ptr, col_idx, w.seen_ptr, w.seen_idx, d_status, st);
     if (r != SPARSP_OK) return r;
     row_ptr = w.seen_ptr;
     col_idx = w.seen_idx;
   }
-  const bool flat = (flags & SPARSP_SCHED_FLAT) != 0;
+  const bool flat = steps.flat;
   // the general kernel's list of a masked call: marks, then count and pull counter, in one stretch
-  const int64_t masked_items = masked ? (int64_t)s.B * s.H * attn_fwd_tc_items_per_head(s) : 0;
-  const int64_t cleared = masked && !(cap > 0.f && cap <= kFixedCap) ? masked_items + 2 : 0;
-  if (masked && order_items_fits(s, attn_fwd_tc_items_per_head(s), plan != nullptr)) {
-    r = launch_order_items(s, attn_fwd_tc_items_per_head(s), row_ptr, w.items, w.counter, w.fix_mark,
-                           (int)cleared, st);
+  const int64_t masked_items = masked ? (int64_t)s.B * s.H * steps.per_head : 0;
+  const int64_t cleared = steps.twice ? masked_items + 2 : 0;
+  if (steps.one_order) {
+    r = launch_order_items(s, steps.per_head, row_ptr, w.items, w.counter, w.fix_mark, (int)cleared, st);
   } else if (cleared > 0 && cudaMemsetAsync(w.fix_mark, 0, cleared * sizeof(int32_t), st) != cudaSuccess) {
     return SPARSP_ERR_CUDA;
-  } else if (tc && attn_fwd_tc_items_per_head(s) != s.nb) {
+  } else if (steps.pairs) {
     // the tcgen05 kernel's items are pairs of query blocks: order the pairs,
     // each costing the sum of its two rows
     r = launch_pair_ptr(s, row_ptr, w.pair_ptr, st);
     if (r != SPARSP_OK) return r;
     Dims sp = s;
-    sp.nb = attn_fwd_tc_items_per_head(s);
+    sp.nb = steps.per_head;
     r = launch_lpt(sp, w.pair_ptr, flat, w.items, w.counter, w.hist, st, 2 * s.nb);
   } else {
     r = launch_lpt(s, row_ptr, flat, w.items, w.counter, w.hist, st);
@@ -276,15 +303,15 @@ sparsp_status_t attn_bwd(const sparsp_shape_t* shape, const void* q, const void*
   if (ws_bytes < w.bytes) return SPARSP_ERR_WORKSPACE;
   if (scale <= 0.f) scale = 1.0f / sqrtf((float)s.d);
   cudaStream_t st = (cudaStream_t)stream;
-  const bool flat = (flags & SPARSP_SCHED_FLAT) != 0;
   typedef const __nv_bfloat16* cb;
-  const bool tc = !(flags & SPARSP_KERNEL_PORTABLE) && attn_bwd_tc_supported(s);
+  const AttnSteps steps = attn_steps(s, flags, plan != nullptr, cap, true);
+  const bool tc = steps.tc, flat = steps.flat;
   const bool raster = (flags & SPARSP_OUT_RASTER) != 0;
   if (raster && !tc) return SPARSP_ERR_UNSUPPORTED;   // only the tcgen05 kernels write raster rows
   if (masked && !tc) return SPARSP_ERR_UNSUPPORTED;
-  masked = plan != nullptr || cap > 0.f;
+  masked = steps.masked;
   const MaskView mask = mask_view(s, plan);
-  if (plan != nullptr && !(flags & SPARSP_LISTS_SEEN) && drops_unseen(s, attn_bwd_tc_items_per_head(s))) {
+  if (steps.compacts) {
     r = launch_mask_csr(s, mask, row_ptr, col_idx, w.seen_ptr, w.seen_idx, d_status, st);
     if (r != SPARSP_OK) return r;
     row_ptr = w.seen_ptr;
@@ -296,11 +323,10 @@ sparsp_status_t attn_bwd(const sparsp_shape_t* shape, const void* q, const void*
   if (r != SPARSP_OK) return r;
   // the tcgen05 kernels' items with 64-token blocks are pairs of blocks, each
   // costing the sum of its two lists (CSR rows for dQ, CSC columns for dK/dV)
-  const bool pairs = tc && attn_bwd_tc_items_per_head(s) != s.nb;
+  const bool pairs = steps.pairs;
   Dims sp = s;
-  sp.nb = pairs ? attn_bwd_tc_items_per_head(s) : s.nb;
-  const bool small = masked && order_items_fits(s, sp.nb, plan != nullptr);
-  if (small) {
+  sp.nb = steps.per_head;
+  if (steps.one_order) {
     r = launch_order_items(s, sp.nb, row_ptr, w.items, w.counter, nullptr, 0, st);
   } else if (pairs) {
     r = launch_pair_ptr(s, row_ptr, w.pair_ptr, st);
@@ -317,7 +343,7 @@ sparsp_status_t attn_bwd(const sparsp_shape_t* shape, const void* q, const void*
                : launch_attn_bwd_tc(s, 0, (cb)q, (cb)k, (cb)v, (cb)dout, w.lse2, w.delta, row_ptr, col_idx, scale,
                                     (__nv_bfloat16*)dq, nullptr, w.items, w.counter, prof, d_status, raster, st);
     if (r != SPARSP_OK) return r;
-    if (small) {
+    if (steps.one_order) {
       r = launch_order_items(s, sp.nb, w.col_ptr, w.items2, w.counter + 1, nullptr, 0, st);
     } else if (pairs) {   // pair_ptr is free again: the dQ kernel reads only its item list
       r = launch_pair_ptr(s, w.col_ptr, w.pair_ptr, st);
@@ -712,6 +738,17 @@ sparsp_status_t sparsp_csr_transpose(const sparsp_shape_t* shape, const int32_t*
   CHECK_OPT_PTR(d_status);
   return launch_csr_transpose(s, row_ptr, col_idx, col_ptr, row_idx, d_status,
                               (cudaStream_t)stream);
+}
+
+int32_t sparsp_attn_launches(const sparsp_shape_t* shape, int32_t backward, int32_t plan, float cap, uint32_t flags) {
+  Dims s;
+  if (check_shape(shape, &s) != SPARSP_OK || !cap_ok(cap, 0.f, s.d) || (flags & ~kKnownFlags)) return 0;
+  const AttnSteps a = attn_steps(s, flags, plan != 0, cap, backward != 0);
+  if (a.masked && !a.tc) return 0;
+  const int lists = a.compacts ? 3 : 0;
+  if (!backward) return lists + a.order_launches() + (a.twice ? 2 : 1);
+  // row dot and CSR transpose; an order before each of dQ and dK, dV
+  return lists + 2 + 2 * a.order_launches() + 1 + (a.tc && !a.masked && (flags & SPARSP_BWD_SPLIT_KV) ? 2 : 1);
 }
 
 size_t sparsp_attn_workspace_size(const sparsp_shape_t* shape, int32_t backward) {

@@ -26,11 +26,10 @@ import dataclasses
 
 import torch
 
-from . import (EST_LOWRANK, EST_MEAN, PROF_SLOTS, Shape, attn_bwd, attn_fwd, attn_workspace_size, augment,
+from . import (EST_LOWRANK, EST_MEAN, PROF_SLOTS, Shape, attn_bwd, attn_fwd, attn_launches, attn_workspace_size, augment,
                augment_workspace_size, balance_heads, Balance, predictor_fit,
                attn_masked_bwd, attn_masked_compacts, attn_masked_fwd, attn_masked_workspace_size, LISTS_SEEN, MaskPlan,
-               mask_csr, mask_scores, norm_bwd, norm_fwd,
-               norm_workspace_size, rope as rope_turn, RopeTable,
+               mask_csr, mask_scores, norm_bwd, norm_fwd, norm_workspace_size, rope as rope_turn, RopeTable,
                block_scores, block_scores_pooled, block_scores_workspace_size, kv_demand, kv_gather, lib, placement,
                placement_workspace_size, reorder, reorder_pool, select, select_workspace_size, DemandOut,
                OUT_RASTER, IN_RASTER, pool_means, _whole)
@@ -51,40 +50,36 @@ class QKNorm:
 
 
 class Pipeline:
+    def _attn_flags(self) -> int:
+        seen = self.mask is not None and (self._attn_on_seen or self.augment)
+        return self.flags | (OUT_RASTER if self.raster_out else 0) | (LISTS_SEEN if seen else 0)
+
     def kernels_per_forward(self) -> int:
-        """Kernels forward() launches: reorder x3, pool + product, select x3 (count,
+        """Kernels forward() launches: norm of Q and K (2) when there is one, reorder x3
+        (the rotation is in that pass; with raster inputs a rotation or pooling pass over Q and K
+        each), pool + product, masked scores (1) and lists (3) under a mask, select x3 (count,
         scan, fill), predictor fitting x7 when enabled, balancing (1) and augmentation x14 (keys, slack, four
         histogram + digit passes, row counts, ties, scan, fill) when enabled, placement x2 (affinity, greedy) when
-        enabled, demand x5 (counter reset, bitmap, scan, list, gather), schedule (1, or 2 in
-        flat order) + attention, inverse reorder (none when attention writes raster O)."""
-        lpt = 2 if self.flags & 1 else 1
+        enabled, demand x5 (counter reset, bitmap, scan, list, gather), attention with the order of its
+        work (attn_launches), inverse reorder (none when attention writes raster O)."""
         gather = 1 if self.demand.kg is not None else 0
         scores = (2 if self.est == EST_LOWRANK else 1) if self.fused else 2
         place = 2 if self.owner is not None else 0
         bal = (1 if self.migrations is not None else 0) + (14 if self.augment else 0)
         # projection, two score products, gradient products, loss (partials, sum), weight gradients
         pred = 7 if self.predictor_lr is not None else 0
-        # norm of Q and K; with raster inputs the rotation is a pass of its own; masked scores, the masked CSR (count,
-        # scan, fill; left out for small shapes, as is a launch of the order in 64-token blocks), and the general
-        # attention kernel over what the first one passes on
-        extra = (2 if self.norm is not None else 0) + (2 if self.rope is not None and self.raster_in else 0)
-        extra += (4 if self.mask is not None else 0)
-        extra += 1 if (self.mask is not None and not self.cap) or self.cap > 20 else 0
-        return 3 + scores + pred + 3 + bal + place + 4 + gather + lpt + 1 + (0 if self.raster_out else 1) + extra
+        tiles = (2 if self.norm is not None else 0) + (2 if self.raster_in else 3)
+        masked = 4 if self.mask is not None else 0
+        attn = attn_launches(self.shape, False, self.mask is not None, self.cap, self._attn_flags())
+        return tiles + scores + masked + pred + 3 + bal + place + 4 + gather + attn + (0 if self.raster_out else 1)
 
     def kernels_per_backward(self) -> int:
-        """reorder dO, rowdot, CSR transpose, schedule, dQ, schedule, dK + dV (one
-        kernel, two with BWD_SPLIT_KV), 3 inverse reorders (none when the
-        backward writes raster gradients)."""
-        lpt = 2 if self.flags & 1 else 1
-        kv = 2 if self.flags & 4 else 1
-        if self.mask is not None or self.cap:
-            kv = 1
-        # the masked CSR; the inverse rotations (in place of two inverse reorders where there are any); norm backward
-        # (gradient, weights' sums) of Q and K
-        extra = (3 if self.mask is not None else 0) + (2 if self.rope is not None and self.raster_out else 0)
-        extra += 4 if self.norm is not None else 0
-        return 1 + 1 + 1 + lpt + 1 + lpt + kv + (0 if self.raster_out else 3) + extra
+        """Reorder of dO, attention (attn_launches), an inverse rotation or reorder of dQ and dK
+        each (no reorder when the backward writes raster gradients) and an inverse reorder of dV
+        (likewise), norm backward (gradient, weights' sums) of Q and K."""
+        attn = attn_launches(self.shape, True, self.mask is not None, self.cap, self._attn_flags())
+        back = (2 if self.rope is not None or not self.raster_out else 0) + (0 if self.raster_out else 1)
+        return 1 + attn + back + (4 if self.norm is not None else 0)
 
     def __init__(self, shape: Shape, estimator: str, top_p: float, k_floor: int, P: int, rank: int = 16,
                  gather: bool = True, flags: int = 0, backward: bool = False, device="cuda",

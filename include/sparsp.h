@@ -463,6 +463,14 @@ SPARSP_API sparsp_status_t sparsp_attn_bwd(const sparsp_shape_t* shape, const vo
                                 sparsp_stream_t stream);
 
 /*
+ * The number of kernels that an attention call with these arguments launches
+ * (plan: is there a token mask; plain calls: 0, and cap 0). 0 for arguments that
+ * the call refuses.
+ */
+SPARSP_API int32_t sparsp_attn_launches(const sparsp_shape_t* shape, int32_t backward, int32_t plan, float cap,
+                                        uint32_t flags);
+
+/*
  * Transpose of the per-head CSR (used by the backward): for each key block j
  * of head (b,h), the query blocks that selected it, ascending.
  * col_ptr int32 [B*H*nb+1]; row_idx int32 (capacity = nnz of the CSR).
