@@ -107,6 +107,15 @@ lpt_place_kernel(const int32_t* __restrict__ row_ptr, const int32_t* __restrict_
 
 constexpr int kBitmapMaxBlocks = 1024;
 
+// A row that ends before it begins, or is longer than it can be: it is reported and not
+// read, as it may begin or end anywhere. A head with such a row may list more
+// entries than it has room for: the lists are written up to where the head's rows end.
+__device__ __forceinline__ bool bad_row(int32_t a, int32_t b, int nb) { return b < a || (int64_t)b - a > nb; }
+__device__ __forceinline__ int64_t list_limit(int32_t head_end, int BH, int nb) {
+  const int64_t all = (int64_t)BH * nb * nb;
+  return head_end < all ? head_end : all;
+}
+
 // CSR -> CSC per head beyond kBitmapMaxBlocks blocks. Rows are visited in
 // order, one row per step, so each key block's list of query blocks comes out
 // ascending.
@@ -119,13 +128,26 @@ csr_transpose_kernel(const int32_t* __restrict__ row_ptr, const int32_t* __restr
   __shared__ int32_t warp_tot[32];
   const int bh = blockIdx.x;
   const int64_t r0 = (int64_t)bh * nb;
-  for (int j = threadIdx.x; j < nb; j += blockDim.x) cnt[j] = 0;
-  __syncthreads();
+  bool bad = false;
+  for (int j = threadIdx.x; j < nb; j += blockDim.x) {
+    cnt[j] = 0;
+    bad |= bad_row(row_ptr[r0 + j], row_ptr[r0 + j + 1], nb);
+  }
+  const bool any_bad = __syncthreads_or(bad);
   const int32_t e0 = row_ptr[r0], e1 = row_ptr[r0 + nb];
-  for (int32_t e = e0 + threadIdx.x; e < e1; e += blockDim.x) {
-    const int32_t j = col_idx[e];
-    if (j >= 0 && j < nb) atomicAdd(&cnt[j], 1);
-    else report(d_status, SPARSP_ERR_DATA);
+  auto count = [&](int32_t a, int32_t b) {
+    for (int32_t e = a + (int32_t)threadIdx.x; e < b; e += blockDim.x) {
+      const int32_t j = col_idx[e];
+      if (j >= 0 && j < nb) atomicAdd(&cnt[j], 1);
+      else report(d_status, SPARSP_ERR_DATA);
+    }
+  };
+  if (!any_bad) {
+    count(e0, e1);
+  } else {
+    if (threadIdx.x == 0) report(d_status, SPARSP_ERR_DATA);
+    for (int i = 0; i < nb; ++i)
+      if (!bad_row(row_ptr[r0 + i], row_ptr[r0 + i + 1], nb)) count(row_ptr[r0 + i], row_ptr[r0 + i + 1]);
   }
   __syncthreads();
   // exclusive scan of cnt[0..nb): thread t takes the kPer entries from kPer*t
@@ -166,13 +188,15 @@ csr_transpose_kernel(const int32_t* __restrict__ row_ptr, const int32_t* __restr
   }
   if (bh == BH - 1 && threadIdx.x == 0) col_ptr[(int64_t)BH * nb] = row_ptr[(int64_t)BH * nb];
   __syncthreads();
+  const int64_t limit = list_limit(e1, BH, nb);
   for (int i = 0; i < nb; ++i) {
     const int32_t a = row_ptr[r0 + i], b = row_ptr[r0 + i + 1];
-    for (int32_t e = a + threadIdx.x; e < b; e += blockDim.x) {
+    if (any_bad && bad_row(a, b, nb)) continue;
+    for (int32_t e = a + (int32_t)threadIdx.x; e < b; e += blockDim.x) {
       const int32_t jj = col_idx[e];
       if (jj >= 0 && jj < nb) {
         const int32_t pos = atomicAdd(&cursor[jj], 1);   // distinct jj within a row
-        if (dcheck(pos >= e0 && pos < e1, d_status)) row_idx[pos] = i;
+        if (pos >= 0 && pos < limit) row_idx[pos] = i;
       }
     }
     __syncthreads();
@@ -201,7 +225,7 @@ csr_transpose_bitmap_kernel(const int32_t* __restrict__ row_ptr, const int32_t* 
   // one warp per row: its bits and the column counts
   for (int i = warp; i < nb; i += nwarps) {
     const int32_t a = row_ptr[r0 + i], b = row_ptr[r0 + i + 1];
-    bool bad = b < a;
+    bool bad = bad_row(a, b, nb);
     for (int32_t e = a + lane; e < b && !bad; e += 32) {
       const int32_t j = col_idx[e];
       if (j < 0 || j >= nb) {
@@ -248,12 +272,12 @@ csr_transpose_bitmap_kernel(const int32_t* __restrict__ row_ptr, const int32_t* 
   if (bh == BH - 1 && threadIdx.x == 0) col_ptr[(int64_t)BH * nb] = row_ptr[(int64_t)BH * nb];
   // column j, down the rows
   if (j < nb) {
-    const int32_t end = pos + v;
+    const int64_t limit = list_limit(row_ptr[r0 + nb], BH, nb);
     const uint32_t bit = 1u << (j & 31);
     const uint32_t* col = bm + (j >> 5);
     for (int i = 0; i < nb; ++i)
       if (col[i * W] & bit) {
-        if (dcheck(pos < end, d_status)) row_idx[pos] = i;
+        if (pos >= 0 && pos < limit) row_idx[pos] = i;
         ++pos;
       }
   }

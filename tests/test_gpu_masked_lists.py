@@ -170,3 +170,34 @@ def test_pipeline_counts_pairs_that_see_something(dims, augmented):
         placed = sp.Pipeline(s, "mean", 0.7, floor, P, mask=plan, placement=True)
         placed.forward(q, k, v)
         assert torch.equal(placed.owner, sp.placement(s, P, rp, ci))
+
+
+@pytest.mark.parametrize("dims", [(2, 2, 6, 16, 24, 64, 2, 8, 8), (2, 1, 32, 48, 48, 64, 4, 4, 4)])
+def test_transpose_leaves_out_rows_that_are_too_long(dims):
+    """A row that claims more entries than there are blocks (all of them readable here) is reported and not read: its
+    head's other rows and the other heads come out as without it."""
+    s = sp.make_shape(*dims, "bf16")
+    g = gen(54)
+    chosen = torch.rand(s.B, s.H, s.nb, s.nb, generator=g, device="cuda") < (0.5 if s.nb < 100 else 0.02)
+    chosen[..., 0] = True
+    rp, ci = csr_of(chosen)
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    cp, ri = sp.csr_transpose(s, rp, ci, status=st)
+    assert int(st) == 0 and torch.equal(chosen_of(s, cp, ri).transpose(-1, -2), chosen)
+    n, last = int(rp[-1]), s.rows - 1
+    long = rp.clone()
+    long[last] = n - s.nb - 1          # the last row of the last head is now too long, the row before it ends too early
+    ci = torch.cat([ci, ci])
+    size = long[1:] - long[:-1]
+    gone = (size < 0) | (size > s.nb)
+    assert gone[last]
+    want = chosen.view(s.rows, s.nb) & ~gone[:, None]
+    for r in (~gone & (long[1:] != rp[1:])).nonzero()[:, 0].tolist():      # a row cut short keeps its first entries
+        want[r, ci[int(long[r + 1]):int(rp[r + 1])].long()] = False
+    cp, ri = sp.csr_transpose(s, long, ci, status=st)
+    assert int(st) == sp.DATA
+    cp_, ri_, want_ = cp.tolist(), ri.cpu(), want.view(s.B * s.H, s.nb, s.nb).cpu()
+    for c in range(s.rows):
+        h, j = divmod(c, s.nb)
+        rows = want_[h, :, j].nonzero()[:, 0]
+        assert torch.equal(ri_[cp_[c]:cp_[c] + len(rows)].long(), rows), (h, j)
