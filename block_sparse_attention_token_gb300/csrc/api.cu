@@ -153,13 +153,18 @@ bool cap_ok(float cap, float scale, int d) {
 }
 
 // Is it worth dropping the block pairs that see nothing of each other before the
-// work is ordered? The three launches cost about 10 us (1,024 tokens, 2 heads:
-// forward 44 us with them, 35 us without), a stage of the attention kernel that
-// turns out empty about 0.9 us: not where the busiest SM has few stages at all.
+// work is ordered? The three launches cost 12 us; a stage of the attention kernel that turns
+// out empty costs it little. By the stages of the busiest SM, if every block were
+// selected: up to 128 of them lists without regard to the mask (60% of all blocks, three
+// documents) take the forward 5 to 14 us longer with the launches (1 to 16 heads, 1,024 to
+// 4,096 tokens: 27 -> 40 us ... 98 -> 111; backward 64 -> 76 ... 306 -> 318, but 182 -> 155 with
+// 128-token blocks and 64 stages), from 384 on such lists gain (8,192 tokens, 12 heads: forward
+// 212 -> 183 and 186 -> 129 us, backward 708 -> 575 and 774 -> 466) and lists selected by masked
+// scores lose the 12 us (145 -> 157).
 bool drops_unseen(const Dims& s, int items_per_head) {
   const int sms = device_sm_count();
   const int64_t items = (int64_t)s.B * s.H * items_per_head, per_sm = (items + sms - 1) / (sms > 0 ? sms : 1);
-  return sms <= 0 || per_sm * items_per_head > 16;
+  return sms <= 0 || per_sm * items_per_head > 128;
 }
 
 // What an attention call launches, decided in one place for the call and for

@@ -103,9 +103,12 @@ sparsp_status_t launch_mask_csr(const Dims& s, const MaskView& m, const int32_t*
 // place of the pairs' costs, the order and a memset, for problems of one wave (1,024
 // tokens, 2 heads: forward 33 -> 30 us, backward 68 -> 61 us), and for lists a mask
 // makes uneven whose K and V stay in L2 (64 MB at most), so that heads need not be taken
-// one after the other (8,192 tokens in 64-token blocks, 12 heads, clips: forward 242 -> 230
-// us, capped 322 -> 302, backward 705 -> 698; without a mask, lists of about one
-// length, capped, 335 us head by head against 345).
+// one after the other. Head by head against this order, clips of 8,192 tokens: 24 MB of K and
+// V forward 226 -> 216 us, backward 689 -> 672; 48 MB 423 -> 409 and 1,406 -> 1,399 (d = 128: 195
+// -> 177, 730 -> 683); 64 MB 240 -> 217, 914 -> 855. Beyond, the two are near each other or this
+// one loses: 96 MB 323 -> 310 us with 24 heads, 367 -> 371 with 12 longer ones, 128 MB 1,834
+// -> 1,871, 192 MB 2,314 -> 2,566. Without a mask (lists of about one length, capped) it gains
+// or loses as much: 24 MB 280 -> 291 us, 64 MB 362 -> 341, backward 1,226 -> 1,247 at 48 MB.
 bool order_items_fits(const Dims& s, int per_head, bool uneven);
 sparsp_status_t launch_order_items(const Dims& s, int per_head, const int32_t* row_ptr, int32_t* items,
                                    int32_t* counter, int32_t* zero, int n_zero, cudaStream_t st);

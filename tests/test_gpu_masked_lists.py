@@ -7,7 +7,7 @@ import torch
 import block_sparse_attention_token_gb300 as sp
 from oracle import sparsp_oracle as orc
 from tests.gpu_helpers import compare_augmented, host
-from tests.test_gpu_masked import gen, masks, to_blocked
+from tests.test_gpu_masked import check_backward, check_forward, csr, gen, inputs, masks, reference, to_blocked
 
 pytestmark = [pytest.mark.gpu, pytest.mark.timeout(300)]
 
@@ -201,3 +201,37 @@ def test_transpose_leaves_out_rows_that_are_too_long(dims):
         h, j = divmod(c, s.nb)
         rows = want_[h, :, j].nonzero()[:, 0]
         assert torch.equal(ri_[cp_[c]:cp_[c] + len(rows)].long(), rows), (h, j)
+
+
+@pytest.mark.parametrize("dims", [(1, 64, 4, 32, 32, 64, 4, 4, 4), (1, 40, 4, 32, 32, 128, 2, 8, 8)])
+@pytest.mark.parametrize("cap", [0.0, 9.0])
+def test_malformed_rows_where_attention_compacts(dims, cap):
+    """Shapes whose lists masked attention compacts itself: malformed rows are reported and count as empty, the others
+    give the values of the formula, and the same bits as their own compaction handed in."""
+    s, one = sp.make_shape(*dims, "bf16"), sp.make_shape(1, 1, *dims[2:], "bf16")
+    assert sp.attn_masked_compacts(s) and sp.attn_masked_compacts(s, True) and not sp.attn_masked_compacts(one)
+    g = gen(55)
+    q, k, v, do = inputs(s, g)
+    rp, ci, chosen = csr(s, 0.5, g)
+    mask, meet = padded(s)
+    plan = sp.mask_plan(s, *mask)
+    ci, chosen = ci.clone(), chosen.clone()
+    rows = [2, 5 * s.nb + 2, (s.H - 1) * s.nb + 2]       # rows that list every block
+    for r, j in zip(rows, (s.nb, -1, 1 << 30)):
+        ci[int(rp[r]) + 1] = j
+        chosen[r // s.nb, r % s.nb] = False
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    o, lse = sp.attn_masked_fwd(s, q, k, v, rp, ci, cap=cap, mask=plan, status=st)
+    assert int(st) == sp.DATA
+    st.zero_()
+    grads = sp.attn_masked_bwd(s, q, k, v, o, lse, do, rp, ci, cap=cap, mask=plan, status=st)
+    assert int(st) == sp.DATA
+    scale = sp.default_scale(s.d)
+    for h in (0, 5, s.H // 2, s.H - 1):
+        q1, k1, v1, do1, o1, *g1 = (t[:, h:h + 1] for t in (q, k, v, do, o, *grads))
+        ref = reference(one, q1, k1, v1, chosen[h:h + 1], mask, scale, cap)
+        check_forward(one, o1, lse[:, h:h + 1], ref, q1, k1, v1, scale, cap)
+        check_backward(one, g1, ref, lse[:, h:h + 1], o1, do1, q1, k1, v1, scale, cap)
+    rp2, ci2 = sp.mask_csr(s, plan, rp, ci)
+    o2, lse2 = sp.attn_masked_fwd(s, q, k, v, rp2, ci2, cap=cap, mask=plan, flags=sp.LISTS_SEEN)
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
