@@ -604,10 +604,11 @@ attn_bwd_tc_kernel(const __grid_constant__ CUtensorMap ta1, const __grid_constan
     // 32 rows with 32 columns each. The chains of a cap or a mask then have three
     // other warps of the scheduler to run beside, and the code of a half stays in the
     // instruction cache. A warp writes its X over its own S (and dP) columns.
-    // Measured: 8,192 tokens, 12 heads of 64, clips: 640 us, with a cap 785 us (four warps
+    // Measured: 8,192 tokens, 12 heads of 64, clips: 640 us, with a cap 800 us (four warps
     // 1,600; the third half buffer of d = 64 took 943 to 872); 65,536 tokens, 24 heads of
-    // 128, clips: 14.6 ms (without a mask 12.7 ms on the same blocks), the tensor pipe 57 to
-    // 65% busy. What a half waits for is its round through S and dP, the row warps and the
+    // 128, clips: 14.6 ms (without a mask 12.7 ms on the same blocks; with a cap 17.0), the tensor pipe
+    // 57 to 65% busy. Nineteen warps leave 96 registers a thread: mode 3 spills 96 to 144 bytes, mode
+    // 0 8 to 76. Scores beyond the cap: 8k clips 1,015 us. What a half waits for is its round through S and dP, the row warps and the
     // accumulate, with two half buffers at d = 128 (TMEM holds no third) and three at 64.
     // A loader warp beside the producer, as in the forward, was slower (15.0 ms against 14.6, 900 us against 876).
     const int hf = warp >> 3, q = (warp >> 2) & 1, rw = warp & 3, t = (int)(threadIdx.x & 127);

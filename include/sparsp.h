@@ -612,9 +612,13 @@ SPARSP_API int32_t sparsp_attn_masked_compacts(const sparsp_shape_t* shape, int3
  *   O_q = sum_k softmax_k(y) v_k,   LSE_q = ln sum_k exp(y).
  * plan: of sparsp_mask_plan for this shape, or NULL (every key is seen). cap = 0:
  * no cap, else 2^-20 <= cap <= 2^20 (SPARSP_ERR_INVALID_ARG outside). A query that
- * sees no key gives O = 0, LSE = -inf. Block pairs that see nothing of each other
+ * sees no key gives O = 0, LSE = -inf; one that sees a score of NaN, or without a cap
+ * one of +inf, gives NaN in both. Block pairs that see nothing of each other
  * are dropped before the work is ordered (unless the shape is so small that
- * this would cost more). Values in keys that a query does not see must be finite
+ * this would cost more). Without a cap, or with one above 20, a block (a pair of 64-token
+ * blocks) with a row whose sum of exponentials leaves [2^-60, 2^80] is done again by a second kernel,
+ * so that a row's last bits may depend on the other rows of its block; the same inputs
+ * give the same bits. Values in keys that a query does not see must be finite
  * (their weight is 0, and 0 times infinity is not). With a cap of up to 20, |v| is
  * below 2^88 and what is below 2^-88 may be lost; otherwise what is below 2^-87 of
  * v or 2^-17 of a row's largest |O| may be. A malformed row (an index
@@ -623,7 +627,9 @@ SPARSP_API int32_t sparsp_attn_masked_compacts(const sparsp_shape_t* shape, int3
  * bf16 on the tcgen05 kernels (Bt and d in {64, 128}, nb <= 1024 when Bt = 64
  * and d = 128); elsewhere, and with SPARSP_KERNEL_PORTABLE,
  * SPARSP_ERR_UNSUPPORTED. The other options, scale, prof and layouts as in
- * sparsp_attn_fwd; with neither plan nor cap the two give the same bits.
+ * sparsp_attn_fwd (small problems, and uneven ones whose K and V stay in L2, are ordered
+ * over all heads with or without SPARSP_SCHED_FLAT); with neither plan nor cap the two
+ * give the same bits.
  * ws: at least sparsp_attn_masked_workspace_size(shape, 0) bytes.
  */
 SPARSP_API size_t sparsp_attn_masked_workspace_size(const sparsp_shape_t* shape, int32_t backward);
