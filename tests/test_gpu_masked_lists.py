@@ -57,7 +57,8 @@ def test_augment_leaves_masked_pairs(dims, P):
     plan = sp.mask_plan(s, *mask)
     assert not meet.any(-1).all()
     S = sp.mask_scores(s, plan, torch.randn(s.B, s.H, s.nb, s.nb, generator=g, device="cuda"))
-    chosen = (torch.rand(S.shape, generator=g, device="cuda") < torch.linspace(0.1, 0.9, s.H, device="cuda").view(1, -1, 1, 1))
+    density = torch.linspace(0.1, 0.9, s.H, device="cuda").view(1, -1, 1, 1)
+    chosen = torch.rand(S.shape, generator=g, device="cuda") < density
     rp, ci = csr_of(chosen & meet[:, None])
     hr = (torch.arange(s.H) * P // s.H).int().expand(s.B, s.H).contiguous().cuda()
     st = torch.zeros(1, dtype=torch.int32, device="cuda")
@@ -161,10 +162,11 @@ def test_pipeline_counts_pairs_that_see_something(dims, augmented):
     o2, lse2 = sp.attn_masked_fwd(s, *ins[:3], rp, ci, mask=plan, flags=sp.OUT_RASTER)
     seen = torch.isfinite(lse2)
     assert torch.equal(seen, torch.isfinite(lse))
-    assert torch.allclose(lse[seen], lse2[seen], rtol=0, atol=2e-6) and float((o.float() - o2.float()).norm() / o2.float().norm()) < 2.0 ** -8
+    # the order of the sums alone differs: fp32 in LSE, a rounding of P and of the result (P, dS and the result) each
+    apart = lambda a, b: float((a.float() - b.float()).norm() / b.float().norm())
+    assert torch.allclose(lse[seen], lse2[seen], rtol=0, atol=2e-6) and apart(o, o2) < 2.0 ** -8
     g2 = sp.attn_masked_bwd(s, *ins[:3], o2, lse2, ins[3], rp, ci, mask=plan, flags=sp.OUT_RASTER)
-    for a, b in zip(grads, g2):
-        assert float((a.float() - b.float()).norm() / b.float().norm()) < 2.0 ** -7
+    assert all(apart(a, b) < 2.0 ** -7 for a, b in zip(grads, g2))
     # placement takes the same lists
     if not augmented:
         placed = sp.Pipeline(s, "mean", 0.7, floor, P, mask=plan, placement=True)

@@ -70,7 +70,8 @@ def test_products_beyond_fp32(dims, cap, large):
     and values of both signs so large that the products leave fp32: every row is done again, none is NaN."""
     s, g, mask, plan, rp, ci, chosen = setting(dims, 42)
     q, k, v, _ = inputs(s, g, 0.05)
-    q[..., 0], k[..., 0] = math.sqrt(45.0 if cap in (0.0, 1000.0) else 58.0), math.sqrt(45.0 if cap in (0.0, 1000.0) else 58.0)
+    level = math.sqrt(58.0 if cap == 60.0 else 45.0)      # 60 tanh(58 / 60) is 44.8
+    q[..., 0], k[..., 0] = level, level
     v = (v * large).bfloat16()
     o, lse = sp.attn_masked_fwd(s, q, k, v, rp, ci, 1.0, cap, plan)
     ref = reference(s, q, k, v, chosen, mask, 1.0, cap)
