@@ -35,6 +35,7 @@ GRID_CAP_SHIFT = 16
 MASKED_SCORE = -1.0e30
 NORM_RMS, NORM_HEAD = 1, 2
 ROPE_INVERSE, ROPE_IN_BLOCKED, ROPE_OUT_BLOCKED = 1, 2, 4
+NORM_ROPE_RMS, NORM_ROPE_BLOCKED = 1, 2
 
 
 def GRID_CAP(n: int) -> int:
@@ -128,6 +129,10 @@ _SIG = {
     "sparsp_rope_table_size": (ctypes.c_size_t, [_P]),
     "sparsp_rope_table": (_I32, [_P, ctypes.c_double, _P, _P, _P, ctypes.c_size_t, _P]),
     "sparsp_rope": (_I32, [_P, _P, _P, _P, _P, ctypes.c_int64, _P, ctypes.c_int64, ctypes.c_uint32, _P, _P, _P]),
+    "sparsp_norm_rope_workspace_size": (ctypes.c_size_t, [_P, _I32]),
+    "sparsp_norm_rope_fwd": (_I32, [_P, ctypes.c_uint32, ctypes.c_float, _P, _P, _P, _P, _P, _P, _P]),
+    "sparsp_norm_rope_bwd": (_I32, [_P, ctypes.c_uint32, ctypes.c_float, _P, _P, _P, _P, _P, _P, ctypes.c_size_t, _P,
+                                    _P]),
     "sparsp_mask_plan_size": (ctypes.c_size_t, [_P]),
     "sparsp_mask_plan": (_I32, [_P, _P, _P, _P, _P, ctypes.c_size_t, _P]),
     "sparsp_mask_scores": (_I32, [_P, _P, _P, _P]),
@@ -379,6 +384,100 @@ def rope(shape: Shape, table: RopeTable, x, out=None, inverse: bool = False, in_
         _want("means", means, (s.B, s.H, s.nb, s.d), torch.float32, dev, True),
         _buffer("status", status, torch.int32, dev, True), _stream(stream)))
     return out
+
+
+class NormRope(ctypes.Structure):
+    _fields_ = [("heads", _I32), ("x", _P), ("x_stride", ctypes.c_int64), ("dy", _P), ("dy_stride", ctypes.c_int64),
+                ("w", _P), ("b", _P), ("out", _P), ("out_stride", ctypes.c_int64), ("means", _P), ("dw", _P), ("db", _P)]
+
+
+def norm_rope_workspace_size(shape: Shape, heads_k: int = 0) -> int:
+    return lib().sparsp_norm_rope_workspace_size(_sref(shape), int(heads_k))
+
+
+def _head_dims(shape: Shape, name: str, t) -> tuple:
+    if not isinstance(t, torch.Tensor) or t.dim() != 4:
+        _refuse(name, t, "a raster [B, N, heads, d] tensor")
+    return shape.B, shape.N, t.shape[2], shape.d
+
+
+def norm_rope_fwd(shape: Shape, table: RopeTable, q, k=None, q_weight=None, k_weight=None, q_bias=None, k_bias=None,
+                  eps: float = 1e-6, rms: bool = False, pos=None, q_out=None, k_out=None, out_blocked: bool = True,
+                  q_means=None, k_means=None, status=None, stream=None):
+    """norm_fwd(per_head=True) and rope of Q and K in one pass, with one rounding; returns
+    (q_out, k_out). q [B,N,H,d] and k [B,N,Hk,d] (or None) are raster and may be slices of a
+    fused projection; the results are in tile order, or with out_blocked=False raster,
+    and may then be slices too. Weights and biases: float32 [d] or None. Without tile
+    order and means the shape's tile does not count (make_shape(1, H, tokens, 1, 1, d, 1, 1,
+    1, dtype) with pos for the new tokens of many requests)."""
+    s, dt, f32, dev = shape, shape.torch_dtype, torch.float32, torch.cuda.current_device()
+    parts, outs = [], []
+    for n, x, w, b, out, means in (("q", q, q_weight, q_bias, q_out, q_means), ("k", k, k_weight, k_bias, k_out, k_means)):
+        if x is None:
+            parts.append(None)
+            outs.append(None)
+            continue
+        raster = _head_dims(s, n, x)
+        blocked = (raster[0], raster[2], raster[1], raster[3])
+        px, xs = _token_stride(s, n, x, raster, dt, dev)
+        if out is None:
+            out = _new(stream, blocked if out_blocked else raster, dt, x.device)
+        po, os_ = ((_want(n + "_out", out, blocked, dt, dev), 0) if out_blocked
+                   else _token_stride(s, n + "_out", out, raster, dt, dev))
+        pm = None if means is None else _want(n + "_means", means, (s.B, raster[2], s.nb, s.d), f32, dev)
+        parts.append(NormRope(raster[2], px, xs, None, 0, _want(n + "_weight", w, (s.d,), f32, dev, True),
+                              _want(n + "_bias", b, (s.d,), f32, dev, True), po, os_, pm, None, None))
+        outs.append(out)
+    flags = (NORM_ROPE_RMS if rms else 0) | (NORM_ROPE_BLOCKED if out_blocked else 0)
+    _check("sparsp_norm_rope_fwd", lib().sparsp_norm_rope_fwd(
+        _sref(s), flags, eps, ctypes.byref(table.axes), _buffer("table", table.table, f32, dev),
+        _want("pos", pos, (s.B, s.N, 3), torch.int32, dev, True), ctypes.byref(parts[0]),
+        None if parts[1] is None else ctypes.byref(parts[1]), _buffer("status", status, torch.int32, dev, True),
+        _stream(stream)))
+    return outs[0], outs[1]
+
+
+def norm_rope_bwd(shape: Shape, table: RopeTable, dy_q, dy_k, q, k=None, q_weight=None, k_weight=None,
+                  eps: float = 1e-6, rms: bool = False, pos=None, in_blocked: bool = False, dq=None, dk=None, dw=None,
+                  db=None, ws=None, status=None, stream=None):
+    """Gradients of norm_rope_fwd from its q and k: (dq, dk, [dw of q, of k], [db of q, of k]).
+    dy_q, dy_k: gradients of its results, raster (slices too) or with in_blocked in tile
+    order. dq and dk are raster and may be slices of one tensor. db is None with rms
+    unless buffers are given; entries of k are None without it."""
+    s, dt, f32, dev = shape, shape.torch_dtype, torch.float32, torch.cuda.current_device()
+    parts, dxs, dws, dbs = [], [], [], []
+    for i, (n, x, dy, w, dx) in enumerate((("q", q, dy_q, q_weight, dq), ("k", k, dy_k, k_weight, dk))):
+        if x is None:
+            for made in (parts, dxs, dws, dbs):
+                made.append(None)
+            continue
+        raster = _head_dims(s, n, x)
+        blocked = (raster[0], raster[2], raster[1], raster[3])
+        px, xs = _token_stride(s, n, x, raster, dt, dev)
+        py, ys = ((_want("dy_" + n, dy, blocked, dt, dev), 0) if in_blocked
+                  else _token_stride(s, "dy_" + n, dy, raster, dt, dev))
+        if dx is None:
+            dx = _new(stream, raster, dt, x.device)
+        po, os_ = _token_stride(s, "d" + n, dx, raster, dt, dev)
+        gw = _new(stream, (s.d,), f32, x.device) if dw is None or dw[i] is None else dw[i]
+        gb = None if db is None else db[i]
+        if gb is None and not rms:
+            gb = _new(stream, (s.d,), f32, x.device)
+        parts.append(NormRope(raster[2], px, xs, py, ys, _want(n + "_weight", w, (s.d,), f32, dev, True), None, po, os_,
+                              None, _want("dw", gw, (s.d,), f32, dev), _want("db", gb, (s.d,), f32, dev, True)))
+        dxs.append(dx)
+        dws.append(gw)
+        dbs.append(gb)
+    if ws is None:
+        heads_k = 0 if k is None else parts[1].heads
+        ws = _new(stream, max(norm_rope_workspace_size(s, heads_k), 16), torch.uint8, q.device)
+    flags = (NORM_ROPE_RMS if rms else 0) | (NORM_ROPE_BLOCKED if in_blocked else 0)
+    _check("sparsp_norm_rope_bwd", lib().sparsp_norm_rope_bwd(
+        _sref(s), flags, eps, ctypes.byref(table.axes), _buffer("table", table.table, f32, dev),
+        _want("pos", pos, (s.B, s.N, 3), torch.int32, dev, True), ctypes.byref(parts[0]),
+        None if parts[1] is None else ctypes.byref(parts[1]), *_space(ws, dev),
+        _buffer("status", status, torch.int32, dev, True), _stream(stream)))
+    return dxs[0], dxs[1], dws, dbs
 
 
 # ----------------------------------------------------------------- step 1

@@ -2,14 +2,12 @@
 // call, so host errors leave outputs untouched) and dispatch to launchers.
 #include <math.h>
 
-#include "common.cuh"
+#include "api.cuh"
 #include "mask.cuh"
 
 using namespace sparsp;
 
 namespace {
-
-bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
 
 // Validates the shape and fills Dims. Accepts d in {64,128}, Bt in {64,128},
 // nb <= kMaxBlocks, B*H <= 65535.
@@ -38,19 +36,6 @@ sparsp_status_t check_shape(const sparsp_shape_t* sh, Dims* s) {
   s->elem = sh->dtype == SPARSP_F32 ? 4 : 2;
   return SPARSP_OK;
 }
-
-#define CHECK_PTR(p)                                   \
-  do {                                                 \
-    if ((p) == nullptr) return SPARSP_ERR_INVALID_ARG; \
-    if (!aligned16(p)) return SPARSP_ERR_ALIGN;        \
-  } while (0)
-
-#define CHECK_OPT_PTR(p)                                        \
-  do {                                                          \
-    if ((p) != nullptr && !aligned16(p)) return SPARSP_ERR_ALIGN; \
-  } while (0)
-
-size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 
 // Every attention option bit; a call ignores the ones that do not concern it.
 constexpr uint32_t kKnownFlags = SPARSP_SCHED_FLAT | SPARSP_KERNEL_PORTABLE | SPARSP_BWD_SPLIT_KV |
@@ -141,6 +126,106 @@ sparsp_status_t check_rope(const sparsp_rope_t* r) {
   for (int ax = 0; ax < 3; ++ax)
     if (r->cols[ax] < 0 || r->cols[ax] % 2 || r->cols[ax] > 128 || r->extent[ax] < 1) return SPARSP_ERR_SHAPE;
   if (rope_table_entries(*r) > INT32_MAX) return SPARSP_ERR_UNSUPPORTED;
+  return SPARSP_OK;
+}
+
+// The shape of norm and rotation in one pass: its tile counts only with tile order or
+// tile means, else any number of tokens is taken.
+sparsp_status_t check_rows(const sparsp_shape_t* sh, bool tiles, Dims* s) {
+  if (sh == nullptr) return SPARSP_ERR_INVALID_ARG;
+  if (tiles) return check_shape(sh, s);
+  if (sh->B <= 0 || sh->H <= 0 || sh->T <= 0 || sh->Y <= 0 || sh->X <= 0) return SPARSP_ERR_SHAPE;
+  if ((sh->dtype != SPARSP_F32 && sh->dtype != SPARSP_BF16) || (sh->d != 64 && sh->d != 128)) return SPARSP_ERR_UNSUPPORTED;
+  if ((int64_t)sh->B * sh->H > 65535) return SPARSP_ERR_UNSUPPORTED;
+  int64_t n = (int64_t)sh->T * sh->Y;   // below 2^62
+  if (n > INT32_MAX || (n *= sh->X) > INT32_MAX || n * sh->B > INT32_MAX) return SPARSP_ERR_UNSUPPORTED;
+  *s = Dims{};
+  s->B = sh->B; s->H = sh->H; s->T = sh->T; s->Y = sh->Y; s->X = sh->X; s->d = sh->d;
+  s->dtype = sh->dtype;
+  s->N = n;
+  s->ta = s->tb = s->tc = s->Bt = 1;
+  s->nT = s->T; s->nY = s->Y; s->nX = s->X;
+  s->nb = (int)n;
+  s->elem = sh->dtype == SPARSP_F32 ? 4 : 2;
+  return SPARSP_OK;
+}
+
+// The bytes that a tensor of `heads` heads takes up, from its first value to its last.
+struct Span {
+  const uint8_t* p;
+  int64_t stride, row, bytes;
+  bool meets(const Span& o) const { return p < o.p + o.bytes && o.p < p + bytes; }
+  // do two outputs share a value? Slices of one wider tensor lie side by side in each row.
+  bool clashes(const Span& o) const {
+    if (!meets(o)) return false;
+    if (stride != o.stride) return true;
+    const int64_t at = ((o.p - p) % stride + stride) % stride;
+    return at < row || at + o.row > stride;
+  }
+};
+// fills in a stride of 0 and checks it (tile order: none), and gives the span
+sparsp_status_t span_of(const Dims& s, int heads, const void* p, int64_t* stride, bool blocked, Span* out) {
+  Dims t = s;
+  t.H = heads;
+  if (blocked) *stride = 0;
+  const sparsp_status_t r = check_stride(t, stride);
+  if (r != SPARSP_OK) return r;
+  const int64_t row = (int64_t)heads * s.d * s.elem, rows = (int64_t)s.B * s.N;
+  *out = Span{(const uint8_t*)p, *stride * s.elem, row, (rows - 1) * *stride * s.elem + row};
+  return SPARSP_OK;
+}
+
+// Arguments that norm and rotation in one pass share, forward and backward; q and k
+// are made complete copies. k->heads = 0: q alone.
+sparsp_status_t check_norm_rope(const sparsp_shape_t* shape, uint32_t flags, float eps, const sparsp_rope_t* rope,
+                                const float* table, const int32_t* pos, const sparsp_norm_rope_t* q,
+                                const sparsp_norm_rope_t* k, bool backward, bool* tiles, Dims* s, sparsp_norm_rope_t* tq,
+                                sparsp_norm_rope_t* tk) {
+  if (q == nullptr) return SPARSP_ERR_INVALID_ARG;
+  *tq = *q;
+  *tk = k != nullptr ? *k : sparsp_norm_rope_t{};
+  const bool blocked = (flags & SPARSP_NORM_ROPE_BLOCKED) != 0;
+  *tiles = blocked || (!backward && (tq->means != nullptr || tk->means != nullptr));
+  sparsp_status_t r = check_rows(shape, *tiles, s);
+  if (r != SPARSP_OK) return r;
+  if (flags & ~(SPARSP_NORM_ROPE_RMS | SPARSP_NORM_ROPE_BLOCKED)) return SPARSP_ERR_INVALID_ARG;
+  if (!(eps >= 0.f) || isinf(eps)) return SPARSP_ERR_INVALID_ARG;
+  r = check_rope(rope);
+  if (r != SPARSP_OK) return r;
+  const int turned = rope->cols[0] + rope->cols[1] + rope->cols[2];
+  if (turned > s->d || (rope->half && turned != s->d)) return SPARSP_ERR_SHAPE;
+  const int grid[3] = {s->T, s->Y, s->X};
+  if (pos == nullptr)
+    for (int ax = 0; ax < 3; ++ax)
+      if (rope->cols[ax] > 0 && rope->extent[ax] < grid[ax]) return SPARSP_ERR_SHAPE;
+  CHECK_PTR(table);
+  CHECK_OPT_PTR(pos);
+  if (tq->heads != s->H || tk->heads < 0 || (k != nullptr && tk->heads == 0)) return SPARSP_ERR_SHAPE;
+  if ((int64_t)s->B * tk->heads > 65535) return SPARSP_ERR_UNSUPPORTED;
+  Span in[4], out[2];
+  int n_in = 0, n_out = 0;
+  for (sparsp_norm_rope_t* t : {tq, tk}) {
+    if (t->heads == 0) continue;
+    CHECK_PTR(t->x);
+    CHECK_PTR(t->out);
+    CHECK_OPT_PTR(t->w);
+    if (backward) {
+      CHECK_PTR(t->dy);
+      CHECK_OPT_PTR(t->dw);
+      CHECK_OPT_PTR(t->db);
+    } else {
+      CHECK_OPT_PTR(t->b);
+      CHECK_OPT_PTR(t->means);
+    }
+    r = span_of(*s, t->heads, t->x, &t->x_stride, false, &in[n_in++]);
+    if (r == SPARSP_OK && backward) r = span_of(*s, t->heads, t->dy, &t->dy_stride, blocked, &in[n_in++]);
+    if (r == SPARSP_OK) r = span_of(*s, t->heads, t->out, &t->out_stride, !backward && blocked, &out[n_out++]);
+    if (r != SPARSP_OK) return r;
+  }
+  for (int o = 0; o < n_out; ++o)
+    for (int i = 0; i < n_in; ++i)
+      if (out[o].meets(in[i])) return SPARSP_ERR_INVALID_ARG;
+  if (n_out == 2 && out[0].clashes(out[1])) return SPARSP_ERR_INVALID_ARG;
   return SPARSP_OK;
 }
 
@@ -961,6 +1046,43 @@ sparsp_status_t sparsp_rope(const sparsp_shape_t* shape, const sparsp_rope_t* ro
   if (overlap(s, in, in_stride, out, out_stride)) return SPARSP_ERR_INVALID_ARG;
   return launch_rope(s, *rope, table, pos, in, in_stride, in_blocked, out, out_stride, out_blocked,
                      (flags & SPARSP_ROPE_INVERSE) != 0, means, d_status, (cudaStream_t)stream);
+}
+
+size_t sparsp_norm_rope_workspace_size(const sparsp_shape_t* shape, int32_t heads_k) {
+  Dims s;
+  if (check_rows(shape, false, &s) != SPARSP_OK || heads_k < 0 || (int64_t)s.B * heads_k > 65535) return 0;
+  return norm_rope_ws(s, heads_k);
+}
+
+sparsp_status_t sparsp_norm_rope_fwd(const sparsp_shape_t* shape, uint32_t flags, float eps, const sparsp_rope_t* rope,
+                                     const float* table, const int32_t* pos, const sparsp_norm_rope_t* q,
+                                     const sparsp_norm_rope_t* k, int32_t* d_status, sparsp_stream_t stream) {
+  Dims s;
+  sparsp_norm_rope_t tq, tk;
+  bool tiles;
+  const sparsp_status_t r = check_norm_rope(shape, flags, eps, rope, table, pos, q, k, false, &tiles, &s, &tq, &tk);
+  if (r != SPARSP_OK) return r;
+  CHECK_OPT_PTR(d_status);
+  return launch_norm_rope_fwd(s, tiles, *rope, table, pos, (flags & SPARSP_NORM_ROPE_RMS) != 0, eps,
+                              (flags & SPARSP_NORM_ROPE_BLOCKED) != 0, tq, tk, d_status, (cudaStream_t)stream);
+}
+
+sparsp_status_t sparsp_norm_rope_bwd(const sparsp_shape_t* shape, uint32_t flags, float eps, const sparsp_rope_t* rope,
+                                     const float* table, const int32_t* pos, const sparsp_norm_rope_t* q,
+                                     const sparsp_norm_rope_t* k, void* ws, size_t ws_bytes, int32_t* d_status,
+                                     sparsp_stream_t stream) {
+  Dims s;
+  sparsp_norm_rope_t tq, tk;
+  bool tiles;
+  const sparsp_status_t r = check_norm_rope(shape, flags, eps, rope, table, pos, q, k, true, &tiles, &s, &tq, &tk);
+  if (r != SPARSP_OK) return r;
+  CHECK_OPT_PTR(d_status);
+  if (tq.dw != nullptr || tq.db != nullptr || tk.dw != nullptr || tk.db != nullptr) {
+    CHECK_PTR(ws);
+    if (ws_bytes < norm_rope_ws(s, tk.heads)) return SPARSP_ERR_WORKSPACE;
+  }
+  return launch_norm_rope_bwd(s, tiles, *rope, table, pos, (flags & SPARSP_NORM_ROPE_RMS) != 0, eps,
+                              (flags & SPARSP_NORM_ROPE_BLOCKED) != 0, tq, tk, ws, d_status, (cudaStream_t)stream);
 }
 
 }  // extern "C"

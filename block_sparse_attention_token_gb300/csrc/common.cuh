@@ -170,6 +170,18 @@ sparsp_status_t launch_rope(const Dims& s, const sparsp_rope_t& r, const float* 
                             const void* in, int64_t in_stride, bool in_blocked, void* out, int64_t out_stride,
                             bool out_blocked, bool inverse, float* means, int32_t* d_status, cudaStream_t st);
 
+// Norm of every head's row with rotary positions; `tiles`: the tile order or tile
+// means are used, else the shape's tile is not looked at.
+size_t norm_rope_ws(const Dims& s, int heads_k);
+sparsp_status_t launch_norm_rope_fwd(const Dims& s, bool tiles, const sparsp_rope_t& r, const float* table,
+                                     const int32_t* pos, bool rms, float eps, bool out_blocked,
+                                     const sparsp_norm_rope_t& q, const sparsp_norm_rope_t& k, int32_t* d_status,
+                                     cudaStream_t st);
+sparsp_status_t launch_norm_rope_bwd(const Dims& s, bool tiles, const sparsp_rope_t& r, const float* table,
+                                     const int32_t* pos, bool rms, float eps, bool in_blocked,
+                                     const sparsp_norm_rope_t& q, const sparsp_norm_rope_t& k, void* ws,
+                                     int32_t* d_status, cudaStream_t st);
+
 size_t lpt_ws(const Dims& s);
 // cmax: the largest item cost the flat order distinguishes (0 = nb).
 sparsp_status_t launch_lpt(const Dims& s, const int32_t* row_ptr, bool flat, int32_t* items,

@@ -23,60 +23,14 @@
 //   8,192 tokens, 12 heads of 64: 10.2 us, of which the launch is half
 // The rest is the ramp of CTAs that live for 8 heads only, and the read and write streams
 // of rows 10 KB apart.
-#include "common.cuh"
-#include "tc_helpers.cuh"
+#include "rows.cuh"
 
 namespace sparsp {
 namespace {
 
-struct RopeArgs {
-  int cols[3];          // columns per axis
-  int extent[3];        // table rows per axis
-  int base[3];          // first table entry per axis
-  const float2* table;
-  const int32_t* pos;   // [B, N, 3] or null: grid coordinates
-  float sign;           // -1: inverse
-};
-
 struct Side {           // one tensor: raster rows `stride` elements apart per token, or tile order
   int64_t stride;
   int blocked;
-};
-
-template <typename T>
-struct Row16;
-template <>
-struct Row16<__nv_bfloat16> {
-  static constexpr int E = 8;
-  static __device__ __forceinline__ void unpack(const uint4& v, float* f) {
-    const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&v);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const float2 t = __bfloat1622float2(h[e]);
-      f[2 * e] = t.x;
-      f[2 * e + 1] = t.y;
-    }
-  }
-  static __device__ __forceinline__ uint4 pack(const float* f) {
-    uint4 v;
-    __nv_bfloat162* h = reinterpret_cast<__nv_bfloat162*>(&v);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) h[e] = __floats2bfloat162_rn(f[2 * e], f[2 * e + 1]);
-    return v;
-  }
-};
-template <>
-struct Row16<float> {
-  static constexpr int E = 4;
-  static __device__ __forceinline__ void unpack(const uint4& v, float* f) {
-    f[0] = __uint_as_float(v.x);
-    f[1] = __uint_as_float(v.y);
-    f[2] = __uint_as_float(v.z);
-    f[3] = __uint_as_float(v.w);
-  }
-  static __device__ __forceinline__ uint4 pack(const float* f) {
-    return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
-  }
 };
 
 template <typename T, int D, int BT, bool HALF>
@@ -92,13 +46,6 @@ struct RopeCfg {
 };
 
 constexpr int kDepth = 3;   // heads in flight per CTA (three tiles: up to 96 KB with bf16, two CTAs per SM)
-
-__device__ __forceinline__ void copy_async16(void* dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(tc::smem_u32(dst)), "l"(src) : "memory");
-}
-__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;\n" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;\n" ::"n"(N) : "memory"); }
 
 template <typename T, int D, int BT, bool HALF, bool POOL>
 __global__ void __launch_bounds__(RopeCfg<T, D, BT, HALF>::THREADS)
@@ -238,20 +185,6 @@ rope_table_kernel(const RopeArgs a, double theta, double off0, double off1, doub
   table[e] = make_float2((float)c, (float)s);
 }
 
-RopeArgs args_of(const sparsp_rope_t& r, const float* table) {
-  RopeArgs a{};
-  int64_t at = 0;
-  for (int ax = 0; ax < 3; ++ax) {
-    a.cols[ax] = r.cols[ax];
-    a.extent[ax] = r.extent[ax];
-    a.base[ax] = (int)at;
-    at += (int64_t)r.extent[ax] * (r.cols[ax] / 2);
-  }
-  a.table = reinterpret_cast<const float2*>(table);
-  a.sign = 1.f;
-  return a;
-}
-
 template <typename T, int D, int BT, bool HALF>
 bool go(const Dims& s, const void* in, const Side& si, void* out, const Side& so, const RopeArgs& a, float* means,
         int32_t* d_status, cudaStream_t st) {
@@ -289,7 +222,7 @@ int64_t rope_table_entries(const sparsp_rope_t& r) {
 
 sparsp_status_t launch_rope_table(const sparsp_rope_t& r, double theta, const double* offset, const double* scale,
                                   float* table, cudaStream_t st) {
-  const RopeArgs a = args_of(r, nullptr);
+  const RopeArgs a = rope_args(r, nullptr);
   const int64_t total = rope_table_entries(r);
   if (total == 0) return SPARSP_OK;
   rope_table_kernel<<<(unsigned)((total + 255) / 256), 256, 0, st>>>(a, theta, offset[0], offset[1], offset[2],
@@ -302,7 +235,7 @@ sparsp_status_t launch_rope_table(const sparsp_rope_t& r, double theta, const do
 sparsp_status_t launch_rope(const Dims& s, const sparsp_rope_t& r, const float* table, const int32_t* pos,
                             const void* in, int64_t in_stride, bool in_blocked, void* out, int64_t out_stride,
                             bool out_blocked, bool inverse, float* means, int32_t* d_status, cudaStream_t st) {
-  RopeArgs a = args_of(r, table);
+  RopeArgs a = rope_args(r, table);
   a.pos = pos;
   a.sign = inverse ? -1.f : 1.f;
   const Side si{in_stride, in_blocked}, so{out_stride, out_blocked};

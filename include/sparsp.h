@@ -566,6 +566,57 @@ SPARSP_API sparsp_status_t sparsp_rope(const sparsp_shape_t* shape, const sparsp
                                        sparsp_stream_t stream);
 
 /*
+ * The norm of every head's row and the rotary positions in one pass over Q and K:
+ *   y = R(w xh + b),  xh = (x - mean) rstd  (sparsp_norm_fwd with SPARSP_NORM_HEAD,
+ *   then sparsp_rope, with one rounding; SPARSP_NORM_ROPE_RMS: mean = 0).
+ * x: raster [B,N,heads,d] with x_stride elements between tokens (0: heads*d), out:
+ * raster with out_stride, or with SPARSP_NORM_ROPE_BLOCKED tile order [B,heads,N,d];
+ * w, b: float32 [d] or NULL (1 and 0), the same for every head; means: NULL or float32
+ * [B,heads,nb,d], the tile means of y before rounding. heads may differ between q and
+ * k; q->heads = shape->H; k NULL: q alone. The shape's tile counts only with tile order
+ * or means; without them any number of tokens up to 2^31 - 1 is taken (T = tokens, Y =
+ * X = 1), e.g. the new tokens of many requests, with their positions in pos. rope,
+ * table, pos and d_status as in sparsp_rope, eps and strides as in sparsp_norm_fwd.
+ * The byte range of neither out may overlap that of an input; the two outs may be
+ * slices of one wider tensor.
+ */
+typedef struct {
+  int32_t heads;
+  const void* x;
+  int64_t x_stride;
+  const void* dy;       /* backward: gradient of y, raster, or tile order with BLOCKED */
+  int64_t dy_stride;
+  const float* w;
+  const float* b;       /* forward */
+  void* out;            /* y, or in the backward dx (raster) */
+  int64_t out_stride;
+  float* means;         /* forward */
+  float* dw;            /* backward: float32 [d] or NULL */
+  float* db;
+} sparsp_norm_rope_t;
+enum {
+  SPARSP_NORM_ROPE_RMS = 1u << 0,
+  SPARSP_NORM_ROPE_BLOCKED = 1u << 1
+};
+SPARSP_API sparsp_status_t sparsp_norm_rope_fwd(const sparsp_shape_t* shape, uint32_t flags, float eps,
+                                                const sparsp_rope_t* rope, const float* table, const int32_t* pos,
+                                                const sparsp_norm_rope_t* q, const sparsp_norm_rope_t* k,
+                                                int32_t* d_status, sparsp_stream_t stream);
+/*
+ * Its backward, from x alone (the statistics are taken again): with g = R^T dy, gw = g w,
+ *   dx = rstd (gw - mean_d(gw) - xh mean_d(gw xh))   (without mean_d(gw) for RMS),
+ *   dw = sum over rows and heads of g xh,  db = sum over rows and heads of g.
+ * ws: at least sparsp_norm_rope_workspace_size() bytes (heads_k: k's heads, 0 without
+ * k) when a dw or db is given. Sums run in a fixed order: results are bitwise
+ * reproducible.
+ */
+SPARSP_API size_t sparsp_norm_rope_workspace_size(const sparsp_shape_t* shape, int32_t heads_k);
+SPARSP_API sparsp_status_t sparsp_norm_rope_bwd(const sparsp_shape_t* shape, uint32_t flags, float eps,
+                                                const sparsp_rope_t* rope, const float* table, const int32_t* pos,
+                                                const sparsp_norm_rope_t* q, const sparsp_norm_rope_t* k, void* ws,
+                                                size_t ws_bytes, int32_t* d_status, sparsp_stream_t stream);
+
+/*
  * Token masks. Query token n sees key token m (of its batch element) where
  *   lo[n] <= pos[m] < hi[n];      hi <= lo: n sees nothing.
  * pos, lo, hi: int32 [B,N], raster order, any int32 values. Documents: pos = lo
