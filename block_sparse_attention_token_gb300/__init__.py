@@ -36,6 +36,7 @@ MASKED_SCORE = -1.0e30
 NORM_RMS, NORM_HEAD = 1, 2
 ROPE_INVERSE, ROPE_IN_BLOCKED, ROPE_OUT_BLOCKED = 1, 2, 4
 NORM_ROPE_RMS, NORM_ROPE_BLOCKED = 1, 2
+CACHE_CAUSAL = 1
 
 
 def GRID_CAP(n: int) -> int:
@@ -144,6 +145,13 @@ _SIG = {
                                       ctypes.c_size_t, ctypes.c_uint32, _P, _P, _P]),
     "sparsp_attn_masked_bwd": (_I32, [_P, _P, _P, _P, _P, _P, _P, _P, _P, ctypes.c_float, ctypes.c_float, _P, _P, _P,
                                       _P, _P, ctypes.c_size_t, ctypes.c_uint32, _P, _P, _P]),
+    "sparsp_cache_extend": (_I32, [_P, _I32, _I32, _P, _P, _P, _I32, _P, _P, _P, _P, _P, ctypes.c_int64, _P, _P, _P]),
+    "sparsp_cache_write": (_I32, [_P, _I32, _P, ctypes.c_int64, ctypes.c_int64, _P, ctypes.c_int64, ctypes.c_int64, _P,
+                                  ctypes.c_int64, _P, _P, _P, _P, _P, _P]),
+    "sparsp_attn_cache_workspace_size": (ctypes.c_size_t, [_P, _I32, _I32, ctypes.c_int64, _I32, _I32]),
+    "sparsp_attn_cache_fwd": (_I32, [_P, _I32, _I32, _P, ctypes.c_int64, _P, ctypes.c_int64, _I32, _P, _P, _I32, _P, _P,
+                                     _P, _P, _P, _P, ctypes.c_int64, ctypes.c_float, ctypes.c_uint32, _P, _P, _P,
+                                     ctypes.c_size_t, _P, _P]),
     "sparsp_diag_umma_tile": (_I32, [_P, _P, _P, _I32, _I32, _I32, _P, _P]),
     "sparsp_diag_wait_timeout": (_I32, [ctypes.c_uint64, _P, _P]),
 }
@@ -941,5 +949,7 @@ def default_scale(d: int) -> float:
     return 1.0 / math.sqrt(d)
 
 
+from .cache import (CachePool, CacheShape, attn_cache_fwd, attn_cache_workspace_size, block_pool,  # noqa: E402,F401
+                    cache_extend, cache_write)
 from .pipeline import GraphedStep, Pipeline, QKNorm  # noqa: E402,F401
 from .streaming import HostPipeline  # noqa: E402,F401

@@ -1,0 +1,507 @@
+// Attention over a cache of keys and values in 8 bits, found through block tables, for
+// packed queries of many requests.
+//
+//   O = sum_j softmax_j(scale ks_j q.K_j) vs_j V_j, K and V the e4m3 codes, ks and vs the
+// scales of their block and key head. The products run on the codes: an e4m3 code is
+// exact in 16 bits, ks multiplies a score and vs a sum over one block's keys in fp32.
+//
+// Few queries: bound by the cache's bytes. A warp holds the scores transposed, S^T = K Q^T
+// (16 keys by 8 query rows: heads that share a key head, and new tokens, side by side), so that
+// few rows fill a matrix instruction; O^T = V^T P^T. The codes go from global memory into
+// registers in the operands' own layout: the columns of the head are permuted alike in Q and
+// K, and the rows of V^T are columns that a lane has loaded anyway, so no shared memory is
+// needed. Work is counted in units of 64 keys over all requests and key heads and dealt out
+// evenly: a CTA takes a range of units, and an item (request, key head, 8 or 16 rows) that
+// spans several CTAs leaves partial sums that a second kernel joins in order.
+#include <cuda_fp16.h>
+
+#include "cache.cuh"
+
+namespace sparsp {
+namespace {
+
+constexpr int kWarps = 4;
+constexpr int kThreads = kWarps * 32;
+constexpr int kGrid = 152 * 3;     // CTAs that share the work (the workspace depends on it)
+constexpr int kMinUnits = 2;       // units that are worth a CTA
+constexpr float kPScale = 2048.f;  // P is at most 16 and is held as 2^11 P in f16: 2^-35 is not lost
+
+// Where the units of a range lie. Entries are requests (every block is seen, all key heads
+// alike) or request and key head (lists).
+struct Entry {
+  int b, hk, n, len, s0, groups, units;   // hk: of lists; n: new tokens; units of one item
+  int64_t weight;
+};
+
+template <int RT>   // query rows of an item
+struct Walk {
+  const CacheAttn& a;
+  __device__ __forceinline__ int entries() const { return a.row_ptr != nullptr ? a.B * a.c.heads : a.B; }
+  __device__ __forceinline__ Entry at(int e, bool tell) const {
+    Entry x;
+    x.hk = a.row_ptr != nullptr ? e % a.c.heads : 0;
+    x.b = a.row_ptr != nullptr ? e / a.c.heads : e;
+    x.s0 = a.start[x.b];
+    const int s1 = a.start[x.b + 1];
+    x.n = s1 - x.s0;
+    x.len = a.len[x.b];
+    if (x.s0 < 0 || s1 < x.s0 || s1 > a.tokens || x.n > a.max_add) {
+      if (tell) report(a.d_status, SPARSP_ERR_DATA);
+      x.n = 0;
+    }
+    if (x.len < 0 || x.len > (int64_t)a.max_blocks * a.c.bt) {
+      if (tell) report(a.d_status, SPARSP_ERR_DATA);
+      x.len = 0;
+    }
+    x.groups = (int)(((int64_t)x.n * a.group + RT - 1) / RT);
+    if (a.row_ptr != nullptr) {
+      const int64_t p0 = a.row_ptr[e], p1 = a.row_ptr[e + 1];
+      int64_t count = p1 - p0;
+      if (p0 < 0 || count < 0 || count > a.max_blocks || p1 > a.col_cap) {
+        if (tell) report(a.d_status, SPARSP_ERR_DATA);
+        count = 0;
+      }
+      x.units = (int)count * (a.c.bt / kUnit);
+    } else {
+      x.units = (x.len + kUnit - 1) / kUnit;
+    }
+    // an item without keys still has its rows to write: one unit, empty
+    x.weight = (int64_t)x.groups * max(1, x.units) * (a.row_ptr != nullptr ? 1 : a.c.heads);
+    return x;
+  }
+};
+
+// What the joining kernel needs to know of a CTA's last item where it goes on in others.
+struct Open {
+  int b, hk, row0, rows, s0, last, slot, pad;   // last: the CTA of its last unit; slot: of this CTA's part
+};
+
+struct Parts {
+  Open* open;      // [kGrid]
+  float* sum;      // [2 kGrid][RT][D]
+  float2* ml;      // [2 kGrid][RT] maximum (base 2) and sum
+};
+
+__device__ __forceinline__ uint32_t f16x2_of_e4m3(uint32_t two) {   // the low two bytes
+  uint32_t r;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;\n" : "=r"(r) : "h"((uint16_t)two));
+  return r;
+}
+__device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                    uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t transposed(uint32_t v) {
+  uint32_t r;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;\n" : "=r"(r) : "r"(v));
+  return r;
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ float exp2_fast(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(r) : "f"(x));
+  return r;
+}
+
+// One warp's 16 keys of a unit, as loaded.
+template <int D>
+struct Keys {
+  uint4 k[2][D / 64];                          // rows g and g + 8
+  uint32_t v[4][D / 32];                       // tokens 2t, 2t+1, 2t+8, 2t+9; columns D/8 g ...
+  float ks, vs;
+  int first;                                   // position of the warp's first key
+  int valid;                                   // of the 16, how many exist
+};
+
+template <int D, int NT>
+__global__ void __launch_bounds__(kThreads)
+attn_cache_kernel(const CacheAttn a, const Parts parts) {
+  constexpr int RT = 8 * NT, SEG = D / 64, VW = D / 32;
+  const Walk<RT> walk{a};
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
+  __shared__ int64_t s_scan[kThreads];
+  __shared__ int64_t s_begin[3];               // first entry, its unit offset, total
+  __shared__ __align__(16) __half s_q[RT][D + 8];
+  __shared__ float s_factor[RT];
+  __shared__ float s_m[kWarps][RT], s_l[kWarps][RT];
+  __shared__ float s_o[kWarps][RT][D + 2];
+  asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
+
+  // ---- this CTA's range of units
+  const int entries = walk.entries(), per = (entries + kThreads - 1) / kThreads;
+  const int e0 = min(entries, (int)threadIdx.x * per), e1 = min(entries, e0 + per);
+  int64_t mine = 0;
+  for (int e = e0; e < e1; ++e) mine += walk.at(e, blockIdx.x == 0).weight;
+  s_scan[threadIdx.x] = mine;
+  __syncthreads();
+  int64_t below = 0, total = 0;
+  for (int i = 0; i < kThreads; ++i) {
+    if (i < threadIdx.x) below += s_scan[i];
+    total += s_scan[i];
+  }
+  const int64_t ctas = min((int64_t)gridDim.x, max((int64_t)1, (total + kMinUnits - 1) / kMinUnits)), cta = blockIdx.x;
+  const int64_t begin = cta * total / ctas, end = cta < ctas ? (cta + 1) * total / ctas : begin;
+  if (threadIdx.x == 0) parts.open[cta].last = -1;
+  if (cta >= ctas || begin >= end) return;      // the same for the whole CTA
+  if (below <= begin && begin < below + mine) {
+    int64_t at = below;
+    int e = e0;
+    for (;; ++e) {
+      const int64_t w = walk.at(e, false).weight;
+      if (begin < at + w) break;
+      at += w;
+    }
+    s_begin[0] = e;
+    s_begin[1] = begin - at;
+  }
+  __syncthreads();
+  int entry = (int)s_begin[0];
+  int64_t offset = s_begin[1], unit_at = begin;
+  Entry x = walk.at(entry, false);
+
+  while (unit_at < end) {
+    while (offset >= x.weight) {               // entries without queries weigh nothing
+      offset -= x.weight;
+      x = walk.at(++entry, false);
+    }
+    // ---- an item, and this CTA's piece [u0, u1) of it
+    const int units = max(1, x.units);
+    const int item = (int)(offset / units), u0 = (int)(offset - (int64_t)item * units);
+    const int u1 = (int)min((int64_t)units, u0 + (end - unit_at));
+    const int hk = a.row_ptr != nullptr ? x.hk : item / x.groups, group = a.row_ptr != nullptr ? item : item % x.groups;
+    const int row0 = group * RT, rows = min(RT, x.n * a.group - row0);
+    const int32_t* table = a.table + (int64_t)x.b * a.max_blocks;
+    const int32_t* list = a.row_ptr != nullptr ? a.col_idx + a.row_ptr[entry] : nullptr;
+
+    // ---- Q: f16 under a power of two per row
+    for (int r = warp * (32 / (D / 8)) + lane / (D / 8); r < RT; r += kWarps * (32 / (D / 8))) {
+      const int c = lane % (D / 8);
+      float f[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) f[i] = 0.f;
+      if (r < rows) {
+        const int tok = (row0 + r) / a.group, h = hk * a.group + (row0 + r) % a.group;
+        const uint4 w = __ldg(reinterpret_cast<const uint4*>(a.q + (int64_t)(x.s0 + tok) * a.q_token + (int64_t)h * D) + c);
+        const uint32_t p[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          f[2 * i] = __uint_as_float(p[i] << 16);
+          f[2 * i + 1] = __uint_as_float(p[i] & 0xffff0000u);
+        }
+      }
+      float most = 0.f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) most = fabsf(f[i]) < INFINITY ? fmaxf(most, fabsf(f[i])) : most;
+#pragma unroll
+      for (int o = D / 16; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+      // 2^14 <= most * 2^-e < 2^15 (bf16's 8 bits stay whole down to 2^-32 of the row's largest)
+      int e = (int)(__float_as_uint(most) >> 23) - 127 - 14;
+      e = max(-100, min(100, e));
+      const float down = __uint_as_float((uint32_t)(127 - e) << 23);
+      uint4 w;
+      w.x = pack_f16(f[0] * down, f[1] * down);
+      w.y = pack_f16(f[2] * down, f[3] * down);
+      w.z = pack_f16(f[4] * down, f[5] * down);
+      w.w = pack_f16(f[6] * down, f[7] * down);
+      *reinterpret_cast<uint4*>(&s_q[r][c * 8]) = w;
+      if (c == 0) s_factor[r] = __uint_as_float((uint32_t)(127 + e) << 23) * a.scale_log2;
+    }
+    __syncthreads();
+    uint32_t qf[NT][D / 16][2];
+    float factor[NT][2];
+    int last[NT][2];                            // the last key position that a row sees
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+#pragma unroll
+      for (int s = 0; s < D / 16; ++s) {
+        const uint2 w = *reinterpret_cast<const uint2*>(&s_q[j * 8 + g][64 * (s / 4) + 16 * t + 4 * (s % 4)]);
+        qf[j][s][0] = w.x;
+        qf[j][s][1] = w.y;
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int r = j * 8 + 2 * t + i;
+        factor[j][i] = s_factor[r];
+        last[j][i] = a.causal ? x.len - x.n + (row0 + r) / a.group : INT32_MAX;
+      }
+    }
+    float m[NT][2], l[NT][2], o[NT][D / 16][4];
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+      m[j][0] = m[j][1] = -INFINITY;
+      l[j][0] = l[j][1] = 0.f;
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i) o[j][i][0] = o[j][i][1] = o[j][i][2] = o[j][i][3] = 0.f;
+    }
+
+    auto load = [&](int u, Keys<D>& w) {
+      const int per_block = a.c.bt / kUnit;
+      int j = u / per_block, at = u % per_block * kUnit + warp * 16;
+      w.valid = 0;
+      if (u < u1 && u < x.units) {
+        if (list != nullptr) {
+          j = list[j];
+          if (j < 0 || (int64_t)j * a.c.bt >= x.len) {
+            report(a.d_status, SPARSP_ERR_DATA);
+            j = -1;
+          }
+        }
+        if (j >= 0) {
+          const int page = table[j];
+          if (page < 0 || page >= a.c.blocks) {
+            report(a.d_status, SPARSP_ERR_DATA);
+          } else {
+            const int64_t block = (int64_t)page * a.c.heads + hk;
+            w.first = j * a.c.bt + at;
+            w.valid = max(0, min(16, x.len - w.first));
+            w.ks = __ldg(a.ks + block);
+            w.vs = __ldg(a.vs + block);
+            const uint8_t* kb = a.kc + (block * a.c.bt + at) * D;
+            const uint8_t* vb = a.vc + (block * a.c.bt + at) * D;
+#pragma unroll
+            for (int r = 0; r < 2; ++r)
+#pragma unroll
+              for (int s = 0; s < SEG; ++s)
+                w.k[r][s] = g + 8 * r < w.valid
+                                ? __ldg(reinterpret_cast<const uint4*>(kb + (g + 8 * r) * D + 64 * s + 16 * t))
+                                : make_uint4(0, 0, 0, 0);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int tok = 2 * t + (i & 1) + 8 * (i >> 1);
+              const uint8_t* p = vb + tok * D + D / 8 * g;
+              if (VW == 4) {
+                const uint4 q = tok < w.valid ? __ldg(reinterpret_cast<const uint4*>(p)) : make_uint4(0, 0, 0, 0);
+                w.v[i][0] = q.x;
+                w.v[i][1] = q.y;
+                w.v[i][VW - 2] = q.z;
+                w.v[i][VW - 1] = q.w;
+              } else {
+                const uint2 q = tok < w.valid ? __ldg(reinterpret_cast<const uint2*>(p)) : make_uint2(0, 0);
+                w.v[i][0] = q.x;
+                w.v[i][1] = q.y;
+              }
+            }
+          }
+        }
+      }
+    };
+
+    auto step = [&](const Keys<D>& w) {
+      float c[NT][4];
+#pragma unroll
+      for (int j = 0; j < NT; ++j) c[j][0] = c[j][1] = c[j][2] = c[j][3] = 0.f;
+#pragma unroll
+      for (int s = 0; s < D / 16; ++s) {
+        const uint4& ka = w.k[0][s / 4];
+        const uint4& kb = w.k[1][s / 4];
+        const uint32_t wa = s % 4 == 0 ? ka.x : s % 4 == 1 ? ka.y : s % 4 == 2 ? ka.z : ka.w;
+        const uint32_t wb = s % 4 == 0 ? kb.x : s % 4 == 1 ? kb.y : s % 4 == 2 ? kb.z : kb.w;
+        const uint32_t a0 = f16x2_of_e4m3(wa), a1 = f16x2_of_e4m3(wb), a2 = f16x2_of_e4m3(wa >> 16),
+                       a3 = f16x2_of_e4m3(wb >> 16);
+#pragma unroll
+        for (int j = 0; j < NT; ++j) mma(c[j], a0, a1, a2, a3, qf[j][s][0], qf[j][s][1]);
+      }
+      uint32_t p[NT][2];
+      float corr[NT][2];
+      bool moved = false;
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const float f = factor[j][i] * w.ks;
+          c[j][i] = g < w.valid && w.first + g <= last[j][i] ? c[j][i] * f : -INFINITY;
+          c[j][2 + i] = g + 8 < w.valid && w.first + g + 8 <= last[j][i] ? c[j][2 + i] * f : -INFINITY;
+          // the maximum follows when a score passes it by more than 2^4
+          moved |= fmaxf(c[j][i], c[j][2 + i]) > m[j][i] + 4.f;
+          corr[j][i] = 1.f;
+        }
+      if (__any_sync(0xffffffffu, moved)) {
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            float top = fmaxf(m[j][i], fmaxf(c[j][i], c[j][2 + i]));
+#pragma unroll
+            for (int off = 4; off < 32; off <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+            if (top > m[j][i] + 4.f) {                 // by itself: not by what other rows hold
+              corr[j][i] = exp2_fast(m[j][i] - top);   // 0 for the first
+              l[j][i] *= corr[j][i];
+              m[j][i] = top;
+            }
+          }
+      }
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        float e[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          e[i] = c[j][i] == -INFINITY ? 0.f : exp2_fast(c[j][i] - m[j][i & 1]);
+          l[j][i & 1] += e[i];
+        }
+        p[j][0] = transposed(pack_f16(e[0] * kPScale, e[1] * kPScale));
+        p[j][1] = transposed(pack_f16(e[2] * kPScale, e[3] * kPScale));
+      }
+      const float vf = w.vs * (1.0f / kPScale);
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i) {
+        const uint32_t sel = i & 1 ? 0x7362 : 0x5140;
+        const uint32_t lo = __byte_perm(w.v[0][i / 2], w.v[1][i / 2], sel);
+        const uint32_t hi = __byte_perm(w.v[2][i / 2], w.v[3][i / 2], sel);
+        const uint32_t a0 = f16x2_of_e4m3(lo), a1 = f16x2_of_e4m3(lo >> 16), a2 = f16x2_of_e4m3(hi),
+                       a3 = f16x2_of_e4m3(hi >> 16);
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+          float d[4] = {0.f, 0.f, 0.f, 0.f};
+          mma(d, a0, a1, a2, a3, p[j][0], p[j][1]);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) o[j][i][k] = o[j][i][k] * corr[j][k & 1] + d[k] * vf;
+        }
+      }
+    };
+
+    Keys<D> w[2];
+    load(u0, w[0]);
+    for (int u = u0; u < u1; u += 2) {
+      load(u + 1, w[1]);
+      if (w[0].valid > 0) step(w[0]);
+      load(u + 2, w[0]);
+      if (w[1].valid > 0) step(w[1]);
+    }
+
+    // ---- join the warps
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+#pragma unroll
+        for (int off = 4; off < 32; off <<= 1) l[j][i] += __shfl_xor_sync(0xffffffffu, l[j][i], off);
+        if (g == 0) {
+          s_m[warp][j * 8 + 2 * t + i] = m[j][i];
+          s_l[warp][j * 8 + 2 * t + i] = l[j][i];
+        }
+      }
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          s_o[warp][j * 8 + 2 * t + (k & 1)][D / 8 * g + 2 * i + (k >> 1)] = o[j][i][k];
+    __syncthreads();
+    const bool whole = u0 == 0 && u1 == units;
+    const int slot = 2 * (int)cta + (unit_at == begin ? 0 : 1);
+    for (int i = threadIdx.x; i < rows * D; i += kThreads) {
+      const int r = i / D, c = i % D;
+      float top = s_m[0][r], sum = 0.f, all = 0.f;
+#pragma unroll
+      for (int q = 1; q < kWarps; ++q) top = fmaxf(top, s_m[q][r]);
+#pragma unroll
+      for (int q = 0; q < kWarps; ++q) {
+        const float f = s_m[q][r] == -INFINITY ? 0.f : exp2_fast(s_m[q][r] - top);
+        // a warp that saw nothing has sums of zero; one whose scores were NaN has NaN
+        sum += s_l[q][r] == 0.f ? 0.f : f == 0.f && s_m[q][r] == -INFINITY ? s_l[q][r] : f * s_l[q][r];
+        all += s_l[q][r] == 0.f ? 0.f : f == 0.f && s_m[q][r] == -INFINITY ? s_o[q][r][c] : f * s_o[q][r][c];
+      }
+      if (whole) {
+        const int tok = x.s0 + (row0 + r) / a.group, h = hk * a.group + (row0 + r) % a.group;
+        a.o[((int64_t)tok * a.H + h) * D + c] = __float2bfloat16(sum == 0.f ? 0.f : all / sum);
+        if (c == 0) a.lse[(int64_t)tok * a.H + h] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
+      } else {
+        parts.sum[((int64_t)slot * RT + r) * D + c] = all;
+        if (c == 0) parts.ml[(int64_t)slot * RT + r] = make_float2(top, sum);
+      }
+    }
+    if (!whole && u0 == 0 && threadIdx.x == 0) {
+      const int64_t stop = unit_at + units - 1;          // the item's last unit
+      parts.open[cta] = Open{x.b, hk, row0, rows, x.s0, (int)(((stop + 1) * ctas - 1) / total), slot, 0};
+    }
+    __syncthreads();
+    unit_at += u1 - u0;
+    offset += u1 - u0;
+  }
+}
+
+// CTA c joins the parts of the item that starts in CTA c of the kernel above and goes on in
+// others, in their order: a warp per row.
+template <int D, int NT>
+__global__ void __launch_bounds__(256)
+attn_cache_join_kernel(const CacheAttn a, const Parts parts) {
+  constexpr int RT = 8 * NT, W = D / 32;
+  asm volatile("griddepcontrol.wait;\n" ::: "memory");
+  const Open it = parts.open[blockIdx.x];
+  if (it.last < 0) return;
+  const int lane = threadIdx.x & 31;
+  const int count = it.last - (int)blockIdx.x + 1;
+  auto slot_of = [&](int i) { return i == 0 ? it.slot : 2 * ((int)blockIdx.x + i); };
+  for (int r = threadIdx.x >> 5; r < it.rows; r += 8) {
+    float top = -INFINITY, sum = 0.f, all[W];
+#pragma unroll
+    for (int k = 0; k < W; ++k) all[k] = 0.f;
+    for (int i = lane; i < count; i += 32) top = fmaxf(top, parts.ml[(int64_t)slot_of(i) * RT + r].x);
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+#pragma unroll 4
+    for (int i = 0; i < count; ++i) {
+      const float2 ml = parts.ml[(int64_t)slot_of(i) * RT + r];
+      const float f = ml.x == -INFINITY ? (ml.y == 0.f ? 0.f : 1.f) : exp2_fast(ml.x - top);
+      sum += ml.y * f;
+#pragma unroll
+      for (int k = 0; k < W; ++k) all[k] += f * parts.sum[((int64_t)slot_of(i) * RT + r) * D + lane + 32 * k];
+    }
+    const int tok = it.s0 + (it.row0 + r) / a.group, h = it.hk * a.group + (it.row0 + r) % a.group;
+#pragma unroll
+    for (int k = 0; k < W; ++k)
+      a.o[((int64_t)tok * a.H + h) * D + lane + 32 * k] = __float2bfloat16(sum == 0.f ? 0.f : all[k] / sum);
+    if (lane == 0) a.lse[(int64_t)tok * a.H + h] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
+  }
+}
+
+int rows_of(int group, int max_add) { return (int64_t)group * max_add <= 8 ? 8 : 16; }
+
+size_t align(size_t n) { return (n + 255) & ~(size_t)255; }
+
+template <int D, int NT>
+sparsp_status_t go(const CacheAttn& a, void* ws, cudaStream_t st) {
+  constexpr int RT = 8 * NT;
+  Parts p;
+  uint8_t* at = (uint8_t*)ws;
+  p.open = (Open*)at;
+  at += align(kGrid * sizeof(Open));
+  p.ml = (float2*)at;
+  at += align((size_t)2 * kGrid * RT * sizeof(float2));
+  p.sum = (float*)at;
+  attn_cache_kernel<D, NT><<<kGrid, kThreads, 0, st>>>(a, p);
+  SPARSP_LAUNCH_CHECK();
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(kGrid);
+  cfg.blockDim = dim3(256);
+  cfg.stream = st;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, attn_cache_join_kernel<D, NT>, a, p) != cudaSuccess) return SPARSP_ERR_CUDA;
+  SPARSP_LAUNCH_CHECK();
+  return SPARSP_OK;
+}
+
+}  // namespace
+
+size_t attn_cache_ws(const CacheDims& c, int group, int max_add) {
+  const size_t rt = rows_of(group, max_add);
+  return align(kGrid * sizeof(Open)) + align(2 * kGrid * rt * sizeof(float2)) + 2 * kGrid * rt * c.d * sizeof(float);
+}
+
+sparsp_status_t launch_attn_cache(const CacheAttn& a, void* ws, cudaStream_t st) {
+  const bool small = rows_of(a.group, a.max_add) == 8;
+  if (a.c.d == 64) return small ? go<64, 1>(a, ws, st) : go<64, 2>(a, ws, st);
+  return small ? go<128, 1>(a, ws, st) : go<128, 2>(a, ws, st);
+}
+
+}  // namespace sparsp

@@ -1,0 +1,350 @@
+// Upkeep of a cache of keys and values in 8 bits: the tables and slots of a step from
+// the requests' lengths, and the write of its new keys and values.
+//
+// Tables. Request b holds len tokens in ceil(len / bt) blocks and gets add more:
+//   need_b = ceil((len + add) / bt) - ceil(len / bt) blocks, handed out from a list in
+// the order of the requests, so that one scan over the requests gives every request its
+// place in the list and its place among the packed new tokens. One cluster of CTAs does
+// it in one launch: each scans all requests for itself (thousands at most, in registers), and
+// barriers of the cluster stand between what is read and what may be written over it.
+//
+// Write. A value is held as x = s c, c of e4m3 and s the scale of its block and head:
+//   s = 2^e, the smallest e >= -100 with max |x| <= 448 2^e.
+// A power of two costs no bit of a floating-point code, makes x / s exact, so that a code is
+// one rounding of x and the same for every way of computing it, and lets a block that
+// grows be brought to a larger scale with no error but the codes' own subnormals. A run
+// of new tokens in one block is one pass: its values wait in registers for their
+// maximum. Bound by HBM.
+#include <cooperative_groups.h>
+#include <cuda_fp8.h>
+
+#include "cache.cuh"
+#include "rows.cuh"
+
+namespace cg = cooperative_groups;
+
+namespace sparsp {
+namespace {
+
+constexpr int kExtendThreads = 1024;
+constexpr int kExtendCluster = 8;
+
+// The sums over the CTA's threads below this one, and of all, of two numbers.
+__device__ __forceinline__ void scan2(int64_t (&v)[2], int64_t (&total)[2], int64_t (*sm)[2]) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int64_t in[2] = {v[0], v[1]};
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1)
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int64_t t = __shfl_up_sync(0xffffffffu, in[k], off);
+      if (lane >= off) in[k] += t;
+    }
+  if (lane == 31)
+#pragma unroll
+    for (int k = 0; k < 2; ++k) sm[warp][k] = in[k];
+  __syncthreads();
+  int64_t below[2] = {0, 0};
+  total[0] = total[1] = 0;
+  for (int w = 0; w < kExtendThreads / 32; ++w)
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      if (w < warp) below[k] += sm[w][k];
+      total[k] += sm[w][k];
+    }
+#pragma unroll
+  for (int k = 0; k < 2; ++k) v[k] = below[k] + in[k] - v[k];
+}
+
+__global__ void __launch_bounds__(kExtendThreads)
+cache_extend_kernel(const CacheDims c, const CacheExtend a, int32_t* d_status) {
+  cg::cluster_group cluster = cg::this_cluster();
+  const int rank = cluster.block_rank(), ranks = cluster.num_blocks();
+  extern __shared__ int32_t sm_req[];
+  int32_t* s_start = sm_req;                     // [B] first packed token
+  int32_t* s_len = sm_req + a.B;                 // [B] tokens held before, -1: gets no slots
+  int32_t* s_place = sm_req + 2 * a.B;           // [B] place in the list of free blocks
+  __shared__ int64_t s_scan[kExtendThreads / 32][2];
+  __shared__ int32_t s_given;
+  const int bt = c.bt, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t room = (int64_t)a.max_blocks * bt;
+  int used = a.used != nullptr ? *a.used : 0;
+  if (used < 0 || used > a.n_free) {             // no such place in the list: nothing to hand out
+    report(d_status, SPARSP_ERR_DATA);
+    used = a.n_free;
+  }
+  if (threadIdx.x == 0) s_given = 0;
+  const int per = (a.B + kExtendThreads - 1) / kExtendThreads;
+  const int b0 = min(a.B, (int)threadIdx.x * per), b1 = min(a.B, b0 + per);
+  auto blocks_of = [&](int64_t n) { return (int)((n + bt - 1) / bt); };
+  // A request's length, new tokens and new blocks; one that makes no sense brings nothing.
+  auto sizes = [&](int b, int& len, int& add, int& need) {
+    len = a.len[b];
+    add = a.add[b];
+    const bool ok = len >= 0 && add >= 0 && (int64_t)len + add <= room;
+    if (!ok) {
+      report(d_status, SPARSP_ERR_DATA);
+      add = 0;
+    }
+    need = ok ? blocks_of((int64_t)len + add) - blocks_of(len) : 0;
+    return ok;
+  };
+  int64_t v[2] = {0, 0}, total[2];
+  for (int b = b0; b < b1; ++b) {
+    int len, add, need;
+    sizes(b, len, add, need);
+    v[0] += add;
+    v[1] += need;
+  }
+  scan2(v, total, s_scan);
+  int given = 0;
+  for (int b = b0; b < b1; ++b) {
+    int len, add, need;
+    const bool ok = sizes(b, len, add, need);
+    // whoever finds too few blocks waits, and so does everyone behind who needs one
+    const bool in = ok && v[0] + add <= a.tokens && (need == 0 || v[1] + need <= a.n_free - used);
+    if (ok && !in) report(d_status, SPARSP_ERR_CAPACITY);
+    s_start[b] = (int)min(v[0], (int64_t)INT32_MAX);
+    s_len[b] = in ? len : -1;
+    s_place[b] = used + (in ? (int)v[1] : 0);
+    if (in) given += need;
+    v[0] += add;
+    v[1] += need;
+  }
+  if (given > 0) atomicAdd(&s_given, given);
+  cluster.sync();                                // every CTA has read len and used
+  if (rank == 0) {
+    for (int b = b0; b < b1; ++b) {
+      const int len = s_len[b];
+      a.start[b] = s_start[b];
+      a.len_out[b] = len >= 0 ? len + a.add[b] : a.len[b];
+    }
+    if (threadIdx.x == 0) {
+      a.start[a.B] = (int)min(total[0], (int64_t)INT32_MAX);
+      if (a.used_out != nullptr) *a.used_out = used + s_given;
+    }
+  }
+  // the blocks handed out: a warp takes a request
+  for (int b = rank * (kExtendThreads / 32) + warp; b < a.B; b += ranks * (kExtendThreads / 32)) {
+    const int len = s_len[b];
+    if (len < 0) continue;
+    const int have = blocks_of(len), need = blocks_of((int64_t)len + a.add[b]) - have;
+    for (int i = lane; i < need; i += 32) {
+      int id = a.free_blocks[s_place[b] + i];
+      if (id < 0 || id >= c.blocks) {
+        report(d_status, SPARSP_ERR_DATA);
+        id = -1;
+      }
+      a.table[(int64_t)b * a.max_blocks + have + i] = id;
+    }
+  }
+  cluster.sync();                                // the table is whole
+  // slots: four packed tokens to a thread, the first one's request by bisection
+  for (int64_t t0 = (int64_t)(rank * kExtendThreads + threadIdx.x) * 4; t0 < a.tokens;
+       t0 += (int64_t)ranks * kExtendThreads * 4) {
+    int lo = 0, hi = a.B;                        // the last request that starts at or before t0
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (s_start[mid] <= t0) lo = mid;
+      else hi = mid;
+    }
+    int slot[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int64_t t = t0 + i;
+      slot[i] = -1;
+      if (t >= total[0] || t >= a.tokens) continue;
+      while (lo + 1 < a.B && s_start[lo + 1] <= t) ++lo;
+      const int len = s_len[lo];
+      if (len < 0) continue;
+      const int p = len + (int)(t - s_start[lo]);
+      const int id = __ldcg(a.table + (int64_t)lo * a.max_blocks + p / bt);
+      if (id < 0 || id >= c.blocks) report(d_status, SPARSP_ERR_DATA);
+      else slot[i] = id * bt + p % bt;
+    }
+    if (t0 + 4 <= a.tokens) {
+      *reinterpret_cast<int4*>(a.slots + t0) = make_int4(slot[0], slot[1], slot[2], slot[3]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (t0 + i < a.tokens) a.slots[t0 + i] = slot[i];
+    }
+  }
+}
+
+// Two fp32 values as e4m3 codes, lo in the low byte (round to nearest even, at most +-448).
+__device__ __forceinline__ uint32_t e4m3_pair(float lo, float hi) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;\n" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ float2 e4m3_values(uint32_t pair) {
+  uint32_t h;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;\n" : "=r"(h) : "h"((uint16_t)pair));
+  return __half22float2(*reinterpret_cast<__half2*>(&h));
+}
+
+// The scale of values of up to `most` (finite, not negative): 448 = 1.75 * 2^8.
+__device__ __forceinline__ float scale_of(float most) {
+  const uint32_t u = __float_as_uint(most);
+  int e = (int)(u >> 23) - 127 - 8 + ((u & 0x7fffffu) > 0x600000u ? 1 : 0);
+  return __uint_as_float((uint32_t)(max(e, -100) + 127) << 23);
+}
+
+constexpr int kWriteThreads = 256;
+constexpr int kGranule = 64;      // most packed tokens that one CTA looks for runs in
+
+// CTA (granule of packed tokens, head, K or V). A run is new tokens in a row whose slots
+// are next to each other in one block; it belongs to the granule it starts in.
+template <typename T, int D, int BT>
+__global__ void __launch_bounds__(kWriteThreads)
+cache_write_kernel(const CacheDims c, const CacheWrite a, int granule, int32_t* d_status) {
+  using X = Row16<T>;
+  constexpr int E = X::E, LPR = D / E, kRows = kWriteThreads / LPR, U = BT / kRows;   // lanes per row, rows a sweep
+  static_assert(U * kRows == BT, "rows of a block");
+  __shared__ uint64_t s_heads;      // the granule's tokens that start a run
+  __shared__ int s_count;
+  __shared__ float s_most[kWriteThreads / 32];
+  const int h = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const bool is_v = blockIdx.z != 0;
+  const T* x = static_cast<const T*>(is_v ? a.v : a.k) + (int64_t)h * (is_v ? a.v_head : a.k_head);
+  const int64_t stride = is_v ? a.v_token : a.k_token;
+  uint8_t* codes = is_v ? a.vc : a.kc;
+  float* scales = is_v ? a.vs : a.ks;
+  const int64_t capacity = (int64_t)c.blocks * BT;
+  const int64_t t0 = (int64_t)blockIdx.x * granule;
+  if (threadIdx.x == 0) s_heads = 0;
+  __syncthreads();
+  if (threadIdx.x < granule && t0 + threadIdx.x < a.tokens) {
+    const int64_t t = t0 + threadIdx.x;
+    const int slot = a.slots[t];
+    if (slot >= capacity) report(d_status, SPARSP_ERR_DATA);
+    else if (slot >= 0 && (t == 0 || slot % BT == 0 || a.slots[t - 1] != slot - 1))
+      atomicOr((unsigned long long*)&s_heads, 1ull << threadIdx.x);
+  }
+  __syncthreads();
+  const int c0 = threadIdx.x % LPR, r0 = threadIdx.x / LPR;
+  for (uint64_t heads = s_heads; heads != 0; heads &= heads - 1) {
+    const int64_t first = t0 + __ffsll((long long)heads) - 1;
+    const int slot = a.slots[first], block = slot / BT, off = slot % BT;
+    // how many tokens follow in the same block
+    if (threadIdx.x == 0) s_count = BT - off;
+    __syncthreads();
+    if (threadIdx.x > 0 && threadIdx.x < BT - off &&
+        (first + threadIdx.x >= a.tokens || a.slots[first + threadIdx.x] != slot + (int)threadIdx.x))
+      atomicMin(&s_count, (int)threadIdx.x);
+    __syncthreads();
+    const int count = s_count;
+    uint4 w[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (r0 + u * kRows < count)
+        w[u] = __ldg(reinterpret_cast<const uint4*>(x + (first + r0 + u * kRows) * stride) + c0);
+    float* scale_at = scales + (int64_t)block * c.heads + h;
+    const float old = off > 0 ? *scale_at : 0.f;
+    float most = 0.f;
+    bool finite = true;
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (r0 + u * kRows < count) {
+        float f[E];
+        X::unpack(w[u], f);
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          const float m = fabsf(f[e]);
+          if (m < INFINITY) most = fmaxf(most, m);
+          else finite = false;
+        }
+      }
+    if (!finite) report(d_status, SPARSP_ERR_DATA);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+    if (lane == 0) s_most[warp] = most;
+    __syncthreads();                              // also: every thread has read the old scale
+#pragma unroll
+    for (int i = 0; i < kWriteThreads / 32; ++i) most = fmaxf(most, s_most[i]);
+    float scale = scale_of(most);
+    const bool kept = off > 0 && old > 0.f && old < INFINITY;
+    if (off > 0 && !kept) report(d_status, SPARSP_ERR_DATA);   // codes without a scale: left as they are
+    if (kept && old >= scale) scale = old;
+    if (threadIdx.x == 0) *scale_at = scale;
+    const bool exact = (__float_as_uint(scale) & 0x7fffffu) == 0;   // a scale of this call's: its inverse is exact
+    const float inverse = 1.0f / scale;
+    uint8_t* base = codes + ((int64_t)block * c.heads + h) * BT * D;
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (r0 + u * kRows < count) {
+        float f[E];
+        X::unpack(w[u], f);
+        uint32_t code[E / 4];
+#pragma unroll
+        for (int e = 0; e < E; ++e)   // what is not finite is held as NaN
+          f[e] = fabsf(f[e]) < INFINITY ? (exact ? f[e] * inverse : f[e] / scale) : NAN;
+#pragma unroll
+        for (int e = 0; e < E / 4; ++e)
+          code[e] = e4m3_pair(f[4 * e], f[4 * e + 1]) | e4m3_pair(f[4 * e + 2], f[4 * e + 3]) << 16;
+        uint8_t* to = base + (int64_t)(off + r0 + u * kRows) * D + c0 * E;
+        if (E == 8) *reinterpret_cast<uint2*>(to) = make_uint2(code[0], code[E / 4 - 1]);
+        else *reinterpret_cast<uint32_t*>(to) = code[0];
+      }
+    if (kept && scale > old) {                    // older tokens of the block, brought to the larger scale
+      const float ratio = old / scale;
+      for (int i = threadIdx.x; i < off * D / 4; i += kWriteThreads) {
+        uint32_t& word = reinterpret_cast<uint32_t*>(base)[i];
+        const float2 lo = e4m3_values(word & 0xffffu), hi = e4m3_values(word >> 16);
+        word = e4m3_pair(lo.x * ratio, lo.y * ratio) | e4m3_pair(hi.x * ratio, hi.y * ratio) << 16;
+      }
+    }
+    __syncthreads();                              // s_count and s_most are written again
+  }
+}
+
+template <typename T, int D, int BT>
+void go_write(const CacheDims& c, const CacheWrite& a, int32_t* d_status, cudaStream_t st) {
+  // granules as large as still leave about sixteen CTAs per SM
+  int granule = kGranule;
+  while (granule > 1 && (int64_t)((a.tokens + granule - 1) / granule) * c.heads * 2 < 152 * 16) granule /= 2;
+  const dim3 grid((unsigned)((a.tokens + granule - 1) / granule), (unsigned)c.heads, 2);
+  cache_write_kernel<T, D, BT><<<grid, kWriteThreads, 0, st>>>(c, a, granule, d_status);
+}
+
+template <typename T>
+void go_write_shape(const CacheDims& c, const CacheWrite& a, int32_t* d_status, cudaStream_t st) {
+  if (c.d == 64 && c.bt == 64) go_write<T, 64, 64>(c, a, d_status, st);
+  else if (c.d == 64) go_write<T, 64, 128>(c, a, d_status, st);
+  else if (c.bt == 64) go_write<T, 128, 64>(c, a, d_status, st);
+  else go_write<T, 128, 128>(c, a, d_status, st);
+}
+
+}  // namespace
+
+sparsp_status_t launch_cache_extend(const CacheDims& c, const CacheExtend& a, int32_t* d_status, cudaStream_t st) {
+  const size_t smem = (size_t)a.B * 3 * sizeof(int32_t);
+  if (cudaFuncSetAttribute(cache_extend_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+    return SPARSP_ERR_CUDA;
+  const int ctas = a.tokens <= 4 * kExtendThreads && a.B <= kExtendThreads ? 1 : kExtendCluster;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(ctas);
+  cfg.blockDim = dim3(kExtendThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim = {(unsigned)ctas, 1, 1};
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, cache_extend_kernel, c, a, d_status) != cudaSuccess) return SPARSP_ERR_CUDA;
+  SPARSP_LAUNCH_CHECK();
+  return SPARSP_OK;
+}
+
+sparsp_status_t launch_cache_write(const CacheDims& c, int dtype, const CacheWrite& a, int32_t* d_status,
+                                   cudaStream_t st) {
+  if (a.tokens == 0) return SPARSP_OK;
+  if (dtype == SPARSP_F32) go_write_shape<float>(c, a, d_status, st);
+  else go_write_shape<__nv_bfloat16>(c, a, d_status, st);
+  SPARSP_LAUNCH_CHECK();
+  return SPARSP_OK;
+}
+
+}  // namespace sparsp

@@ -27,7 +27,7 @@ struct Cfg {
   static constexpr int NP = NE / 2;                            // pairs of a unit
   static constexpr int UPR = D / NE;                           // units (lanes) per row
   static constexpr int VECS = GR * D / E;                      // vectors of a granule
-  static constexpr int THREADS = VECS > 2048 ? VECS / 8 : 256; // at most 8 vectors a thread
+  static constexpr int THREADS = VECS >= 2048 ? 512 : 256;      // 4 to 8 vectors a thread
   static constexpr int U = GR * UPR / THREADS;                 // units (rows) per thread
   static constexpr int kRowStep = THREADS / UPR;
   static_assert(UPR <= 32 && THREADS % UPR == 0 && U >= 1 && U * THREADS == GR * UPR, "granule split");

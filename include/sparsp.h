@@ -706,6 +706,97 @@ SPARSP_API sparsp_status_t sparsp_attn_masked_bwd(const sparsp_shape_t* shape, c
                                                   void* ws, size_t ws_bytes, uint32_t flags, uint64_t* prof,
                                                   int32_t* d_status, sparsp_stream_t stream);
 
+/*
+ * A cache of keys and values in 8 bits, for generation: new tokens attend to what
+ * earlier steps have left (frame by frame, or one token of each of many requests).
+ * Pools of `blocks` blocks of bt tokens, [blocks, heads, bt, d] codes of e4m3 (sign,
+ * 4 bits of exponent, 3 of mantissa, no infinities) for K and for V, with float32
+ * scales [blocks, heads] each: a value is code * scale. heads: key/value heads. d and bt
+ * in {64, 128}, blocks * bt < 2^31, heads <= 65535.
+ * Request b holds len[b] tokens; token p of it sits in block table[b * max_blocks + p / bt]
+ * at p % bt. Slot of a token: block * bt + p % bt. B <= 16384, max_blocks * bt < 2^31.
+ */
+typedef struct {
+  int32_t blocks, heads, d, bt;
+} sparsp_cache_t;
+
+/*
+ * Tables and slots of a step, from the requests' lengths: request b holds len[b] tokens and
+ * gets add[b] new ones. The ceil((len+add)/bt) - ceil(len/bt) blocks it needs are taken, in
+ * the order of the requests, from free_blocks[used ...] (int32 [n_free], 4-byte aligned; used:
+ * device word or NULL, 0) and entered into table [B, max_blocks] (its other entries stay).
+ *   len_out  int32 [B]: len + add (may be len itself).
+ *   start    int32 [B+1]: the first of each request's new tokens in the packed order, and
+ *            their number.
+ *   slots    int32 [tokens]: slot of every packed new token; -1 past the last one.
+ *   used_out device word or NULL: used + the blocks handed out (may be used itself).
+ * A request whose need is not covered, or whose tokens do not fit in `tokens`, sets
+ * SPARSP_ERR_CAPACITY and waits, and so does every later one that needs a block (or
+ * brings tokens past the end): len_out = len, slots -1, no blocks; its tokens keep their
+ * place in the packed order. A request with a negative len or add, or more than
+ * max_blocks * bt tokens, sets SPARSP_ERR_DATA and brings nothing; a block number
+ * outside [0, blocks) sets SPARSP_ERR_DATA and gives slots of -1.
+ */
+SPARSP_API sparsp_status_t sparsp_cache_extend(const sparsp_cache_t* cache, int32_t B, int32_t max_blocks,
+                                               const int32_t* len, const int32_t* add, const int32_t* free_blocks,
+                                               int32_t n_free, const int32_t* used, int32_t* table, int32_t* len_out,
+                                               int32_t* start, int32_t* slots, int64_t tokens, int32_t* used_out,
+                                               int32_t* d_status, sparsp_stream_t stream);
+/*
+ * New keys and values into the pools (kc, ks; vc, vs). k, v: rows of `heads` heads of
+ * dtype (SPARSP_F32 or SPARSP_BF16), k_stride elements between tokens and k_head between
+ * heads (0: heads*d and d; tile order [heads, N, d]: d and N*d); likewise v. Token i goes to
+ * slots[i]; a negative slot is left out, one past the pool sets SPARSP_ERR_DATA.
+ * Tokens in a row whose slots are next to each other in one block are a run. Its block's scale,
+ * per head, becomes the smallest power of two, at least 2^-100, under which the run's
+ * magnitudes are at most 448; where the run starts inside the block, the larger of that
+ * and the block's old scale, and the tokens before it are rounded again to the larger scale.
+ * Codes are rounded to nearest, ties to even. A NaN or infinity is held as NaN, does not
+ * count for the scale, and sets SPARSP_ERR_DATA. A block may have only one run in a call
+ * (as slots of sparsp_cache_extend have); with two its contents are not defined. Where a
+ * run starts inside a block whose scale is not positive and finite, SPARSP_ERR_DATA is
+ * set and the tokens before it are left as they are.
+ */
+SPARSP_API sparsp_status_t sparsp_cache_write(const sparsp_cache_t* cache, int32_t dtype, const void* k,
+                                              int64_t k_stride, int64_t k_head, const void* v, int64_t v_stride,
+                                              int64_t v_head, const int32_t* slots, int64_t tokens, void* kc,
+                                              float* ks, void* vc, float* vs, int32_t* d_status,
+                                              sparsp_stream_t stream);
+/*
+ * Attention of new tokens over that cache. q: packed rows [tokens, H, d] of bf16, q_stride
+ * elements between tokens (0: H*d); request b has rows start[b] .. start[b+1]-1, at most
+ * max_add of them, which are the last of its len[b] tokens. H is a multiple of the cache's
+ * heads; query head h reads key head h / (H / heads). Over the keys it sees,
+ *   O_q = sum_k softmax_k(scale q.k) v_k,  LSE_q = ln sum_k exp(scale q.k),
+ * k and v the values that the codes stand for; scale <= 0 means 1/sqrt(d).
+ *   SPARSP_CACHE_CAUSAL  row i of n sees the tokens up to its own, len - n + i; else all len.
+ *   row_ptr, col_idx     NULL, or a CSR of key blocks: row b * heads + hk lists the distinct
+ *                        blocks j (tokens j*bt ...) that request b's rows see under key
+ *                        head hk; col_cap: entries of col_idx.
+ * o: bf16 [tokens, H, d], lse: float32 [tokens, H]. A row that sees no key gives O = 0,
+ * LSE = -inf; one that sees a score of NaN or +inf gives NaN in both. Rows outside every
+ * request are left as they were. Values of keys that a row does not see must not be NaN
+ * (tokens past len may hold anything). Products are exact or in fp32; the softmax's weights
+ * are rounded to 11 bits.
+ * Sums are taken in an order that depends on the lengths alone: the same call gives the same bits.
+ * SPARSP_ERR_DATA on the device: rows outside [0, tokens] or more than max_add of them (the
+ * request's are left out), a length outside [0, max_blocks * bt] (counts as 0), a CSR row that is
+ * malformed (counts as empty), an entry of it without tokens or a block outside the pool
+ * (its keys are left out).
+ * ws: at least sparsp_attn_cache_workspace_size() bytes.
+ */
+enum { SPARSP_CACHE_CAUSAL = 1u << 0 };
+SPARSP_API size_t sparsp_attn_cache_workspace_size(const sparsp_cache_t* cache, int32_t B, int32_t H, int64_t tokens,
+                                                   int32_t max_add, int32_t max_blocks);
+SPARSP_API sparsp_status_t sparsp_attn_cache_fwd(const sparsp_cache_t* cache, int32_t B, int32_t H, const void* q,
+                                                 int64_t q_stride, const int32_t* start, int64_t tokens,
+                                                 int32_t max_add, const int32_t* len, const int32_t* table,
+                                                 int32_t max_blocks, const void* kc, const float* ks, const void* vc,
+                                                 const float* vs, const int32_t* row_ptr, const int32_t* col_idx,
+                                                 int64_t col_cap, float scale, uint32_t flags, void* o, float* lse,
+                                                 void* ws, size_t ws_bytes, int32_t* d_status,
+                                                 sparsp_stream_t stream);
+
 /* Number of SMs of the current device (cached), or -1 on error. */
 SPARSP_API int32_t sparsp_device_sm_count(void);
 
