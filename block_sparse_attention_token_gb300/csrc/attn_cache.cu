@@ -9,20 +9,23 @@
 // (16 keys by 8 query rows: heads that share a key head, and new tokens, side by side), so that
 // few rows fill a matrix instruction; O^T = V^T P^T. The codes go from global memory into
 // registers in the operands' own layout: the columns of the head are permuted alike in Q and
-// K, and the rows of V^T are columns that a lane has loaded anyway, so no shared memory is
-// needed. Work is counted in units of 64 keys over all requests and key heads and dealt out
+// K, and the rows of V^T are columns that a lane has loaded anyway, so that a lane needs only
+// what it loads itself; it does so some stages ahead, into shared-memory slots of its own. Work is counted in units of 64 keys over all requests and key heads and dealt out
 // evenly: a CTA takes a range of units, and an item (request, key head, 8 or 16 rows) that
 // spans several CTAs leaves partial sums that a second kernel joins in order.
 #include <cuda_fp16.h>
 
 #include "cache.cuh"
+#include "rows.cuh"
 
 namespace sparsp {
 namespace {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
-constexpr int kGrid = 152 * 3;     // CTAs that share the work (the workspace depends on it)
+constexpr int kGrid = 152 * 3;     // CTAs that share the work, at most (the workspace depends on it)
+// CTAs per SM: two rows' accumulators of 128 columns do not fit the registers of three.
+constexpr int ctas_per_sm(int d, int nt) { return d == 128 && nt == 2 ? 2 : 3; }
 constexpr int kMinUnits = 2;       // units that are worth a CTA
 constexpr float kPScale = 2048.f;  // P is at most 16 and is held as 2^11 P in f16: 2^-35 is not lost
 
@@ -108,28 +111,61 @@ __device__ __forceinline__ float exp2_fast(float x) {
   return r;
 }
 
-// One warp's 16 keys of a unit, as loaded.
+// Writes four columns of a finished row, and its LSE.
 template <int D>
-struct Keys {
-  uint4 k[2][D / 64];                          // rows g and g + 8
-  uint32_t v[4][D / 32];                       // tokens 2t, 2t+1, 2t+8, 2t+9; columns D/8 g ...
-  float ks, vs;
-  int first;                                   // position of the warp's first key
-  int valid;                                   // of the 16, how many exist
+__device__ __forceinline__ void finish(const CacheAttn& a, int s0, int hk, int row, int c, float top, float sum,
+                                       const float4& all) {
+  const int64_t at = (int64_t)(s0 + row / a.group) * a.H + hk * a.group + row % a.group;
+  const float f = sum == 0.f ? 0.f : 1.0f / sum;
+  const __nv_bfloat162 lo = __floats2bfloat162_rn(all.x * f, all.y * f), hi = __floats2bfloat162_rn(all.z * f, all.w * f);
+  *reinterpret_cast<uint2*>(a.o + at * D + c) =
+      make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+  if (c == 0) a.lse[at] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
+}
+
+// A warp's ring of 16-key stages: every lane reads back only what it copied itself, so no
+// barrier stands between a copy and its use.
+constexpr int kStages = 4;
+template <int D>
+struct Stage {
+  uint4 k[2][D / 64][32];            // rows g and g + 8 of the stage, columns 64 s + 16 t
+  uint4 v[D / 32][32];               // tokens 2t, 2t+1, 2t+8, 2t+9, columns D/8 g (D = 64: two of them in 16 bytes)
+  float ks[32], vs[32];
 };
 
+__device__ __forceinline__ void copy16(void* dst, const void* src, bool there) {   // zeros where it is not
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(tc::smem_u32(dst)), "l"(src), "r"(there ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void copy8(void* dst, const void* src, bool there) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;\n" ::"r"(tc::smem_u32(dst)), "l"(src), "r"(there ? 8 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void copy4(void* dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;\n" ::"r"(tc::smem_u32(dst)), "l"(src) : "memory");
+}
+
 template <int D, int NT>
-__global__ void __launch_bounds__(kThreads)
+constexpr int attn_smem() {
+  constexpr int ring = kWarps * kStages * (int)sizeof(Stage<D>);
+  constexpr int sums = kWarps * 8 * NT * (D + 4) * 4;    // the warps' sums, over the ring
+  return ring > sums ? ring : sums;
+}
+
+template <int D, int NT>
+__global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT))
 attn_cache_kernel(const CacheAttn a, const Parts parts) {
-  constexpr int RT = 8 * NT, SEG = D / 64, VW = D / 32;
+  constexpr int RT = 8 * NT, SEG = D / 64;
   const Walk<RT> walk{a};
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
-  __shared__ int64_t s_scan[kThreads];
-  __shared__ int64_t s_begin[3];               // first entry, its unit offset, total
+  extern __shared__ __align__(16) uint8_t smem[];
+  Stage<D>* ring = reinterpret_cast<Stage<D>*>(smem) + warp * kStages;
+  float (*s_o)[RT][D + 4] = reinterpret_cast<float (*)[RT][D + 4]>(smem);
+  __shared__ int64_t s_scan[kWarps];
+  __shared__ int64_t s_begin[2];               // first entry, its unit offset
   __shared__ __align__(16) __half s_q[RT][D + 8];
   __shared__ float s_factor[RT];
   __shared__ float s_m[kWarps][RT], s_l[kWarps][RT];
-  __shared__ float s_o[kWarps][RT][D + 2];
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
 
   // ---- this CTA's range of units
@@ -137,11 +173,19 @@ attn_cache_kernel(const CacheAttn a, const Parts parts) {
   const int e0 = min(entries, (int)threadIdx.x * per), e1 = min(entries, e0 + per);
   int64_t mine = 0;
   for (int e = e0; e < e1; ++e) mine += walk.at(e, blockIdx.x == 0).weight;
-  s_scan[threadIdx.x] = mine;
+  int64_t below = mine;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const int64_t v = __shfl_up_sync(0xffffffffu, below, off);
+    if (lane >= off) below += v;
+  }
+  if (lane == 31) s_scan[warp] = below;
+  below -= mine;
   __syncthreads();
-  int64_t below = 0, total = 0;
-  for (int i = 0; i < kThreads; ++i) {
-    if (i < threadIdx.x) below += s_scan[i];
+  int64_t total = 0;
+#pragma unroll
+  for (int i = 0; i < kWarps; ++i) {
+    if (i < warp) below += s_scan[i];
     total += s_scan[i];
   }
   const int64_t ctas = min((int64_t)gridDim.x, max((int64_t)1, (total + kMinUnits - 1) / kMinUnits)), cta = blockIdx.x;
@@ -177,6 +221,66 @@ attn_cache_kernel(const CacheAttn a, const Parts parts) {
     const int row0 = group * RT, rows = min(RT, x.n * a.group - row0);
     const int32_t* table = a.table + (int64_t)x.b * a.max_blocks;
     const int32_t* list = a.row_ptr != nullptr ? a.col_idx + a.row_ptr[entry] : nullptr;
+    const int per_block = a.c.bt / kUnit, stop = min(u1, x.units);
+
+    // The key block of unit u and its place in the pool, looked up ahead of the copies: the list
+    // two units ahead, the table one.
+    auto block_of = [&](int u) -> int {        // -1: none
+      if (u >= stop) return -1;
+      const int j = u / per_block;
+      return list != nullptr ? __ldg(list + j) : j;
+    };
+    auto page_of = [&](int u, int j) -> int {  // -1: none
+      if (u >= stop) return -1;
+      if (j < 0 || (int64_t)j * a.c.bt >= x.len) {
+        report(a.d_status, SPARSP_ERR_DATA);
+        return -1;
+      }
+      return __ldg(table + j);
+    };
+    // Copies the warp's 16 keys of unit u into a stage; returns how many exist.
+    auto fetch = [&](int u, int j, int page, Stage<D>& st) -> int {
+      int valid = 0;
+      if (u < stop && j >= 0 && (int64_t)j * a.c.bt < x.len) {
+        if (page < 0 || page >= a.c.blocks) {
+          report(a.d_status, SPARSP_ERR_DATA);
+        } else {
+          const int at = u % per_block * kUnit + warp * 16;
+          valid = max(0, min(16, x.len - (j * a.c.bt + at)));
+          const int64_t block = (int64_t)page * a.c.heads + hk;
+          const uint8_t* kb = a.kc + (block * a.c.bt + at) * D + g * D + 16 * t;
+          const uint8_t* vb = a.vc + (block * a.c.bt + at) * D + 2 * t * D + D / 8 * g;
+          copy4(&st.ks[lane], a.ks + block);
+          copy4(&st.vs[lane], a.vs + block);
+#pragma unroll
+          for (int r = 0; r < 2; ++r)
+#pragma unroll
+            for (int s = 0; s < SEG; ++s) copy16(&st.k[r][s][lane], kb + 8 * r * D + 64 * s, g + 8 * r < valid);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int tok = (i & 1) + 8 * (i >> 1);
+            const bool there = 2 * t + tok < valid;
+            if (D == 128) copy16(&st.v[i % (D / 32)][lane], vb + tok * D, there);
+            else copy8(reinterpret_cast<uint2*>(&st.v[i / 2][lane]) + (i & 1), vb + tok * D, there);
+          }
+        }
+      }
+      copy_commit();
+      return valid;
+    };
+    int first[kStages], valid[kStages];        // position of the warp's first key, and how many exist, by stage
+    int block1 = block_of(u0), page1 = page_of(u0, block1), block2 = block_of(u0 + 1);
+    auto ahead = [&](int u, int& at, int& n, Stage<D>& st) {   // unit u into a stage; u rises by one from call to call
+      const int page2 = page_of(u + 1, block2);
+      const int block3 = block_of(u + 2);
+      at = block1 * a.c.bt + u % per_block * kUnit + warp * 16;
+      n = fetch(u, block1, page1, st);
+      block1 = block2;
+      page1 = page2;
+      block2 = block3;
+    };
+#pragma unroll
+    for (int s = 0; s < kStages - 1; ++s) ahead(u0 + s, first[s], valid[s], ring[s]);
 
     // ---- Q: f16 under a power of two per row
     for (int r = warp * (32 / (D / 8)) + lane / (D / 8); r < RT; r += kWarps * (32 / (D / 8))) {
@@ -239,102 +343,57 @@ attn_cache_kernel(const CacheAttn a, const Parts parts) {
       for (int i = 0; i < D / 16; ++i) o[j][i][0] = o[j][i][1] = o[j][i][2] = o[j][i][3] = 0.f;
     }
 
-    auto load = [&](int u, Keys<D>& w) {
-      const int per_block = a.c.bt / kUnit;
-      int j = u / per_block, at = u % per_block * kUnit + warp * 16;
-      w.valid = 0;
-      if (u < u1 && u < x.units) {
-        if (list != nullptr) {
-          j = list[j];
-          if (j < 0 || (int64_t)j * a.c.bt >= x.len) {
-            report(a.d_status, SPARSP_ERR_DATA);
-            j = -1;
-          }
-        }
-        if (j >= 0) {
-          const int page = table[j];
-          if (page < 0 || page >= a.c.blocks) {
-            report(a.d_status, SPARSP_ERR_DATA);
-          } else {
-            const int64_t block = (int64_t)page * a.c.heads + hk;
-            w.first = j * a.c.bt + at;
-            w.valid = max(0, min(16, x.len - w.first));
-            w.ks = __ldg(a.ks + block);
-            w.vs = __ldg(a.vs + block);
-            const uint8_t* kb = a.kc + (block * a.c.bt + at) * D;
-            const uint8_t* vb = a.vc + (block * a.c.bt + at) * D;
-#pragma unroll
-            for (int r = 0; r < 2; ++r)
-#pragma unroll
-              for (int s = 0; s < SEG; ++s)
-                w.k[r][s] = g + 8 * r < w.valid
-                                ? __ldg(reinterpret_cast<const uint4*>(kb + (g + 8 * r) * D + 64 * s + 16 * t))
-                                : make_uint4(0, 0, 0, 0);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int tok = 2 * t + (i & 1) + 8 * (i >> 1);
-              const uint8_t* p = vb + tok * D + D / 8 * g;
-              if (VW == 4) {
-                const uint4 q = tok < w.valid ? __ldg(reinterpret_cast<const uint4*>(p)) : make_uint4(0, 0, 0, 0);
-                w.v[i][0] = q.x;
-                w.v[i][1] = q.y;
-                w.v[i][VW - 2] = q.z;
-                w.v[i][VW - 1] = q.w;
-              } else {
-                const uint2 q = tok < w.valid ? __ldg(reinterpret_cast<const uint2*>(p)) : make_uint2(0, 0);
-                w.v[i][0] = q.x;
-                w.v[i][1] = q.y;
-              }
-            }
-          }
-        }
-      }
-    };
-
-    auto step = [&](const Keys<D>& w) {
+    auto step = [&](const Stage<D>& st, int at, int n) {
       float c[NT][4];
 #pragma unroll
       for (int j = 0; j < NT; ++j) c[j][0] = c[j][1] = c[j][2] = c[j][3] = 0.f;
 #pragma unroll
-      for (int s = 0; s < D / 16; ++s) {
-        const uint4& ka = w.k[0][s / 4];
-        const uint4& kb = w.k[1][s / 4];
-        const uint32_t wa = s % 4 == 0 ? ka.x : s % 4 == 1 ? ka.y : s % 4 == 2 ? ka.z : ka.w;
-        const uint32_t wb = s % 4 == 0 ? kb.x : s % 4 == 1 ? kb.y : s % 4 == 2 ? kb.z : kb.w;
-        const uint32_t a0 = f16x2_of_e4m3(wa), a1 = f16x2_of_e4m3(wb), a2 = f16x2_of_e4m3(wa >> 16),
-                       a3 = f16x2_of_e4m3(wb >> 16);
+      for (int s4 = 0; s4 < SEG; ++s4) {
+        const uint4 ka = st.k[0][s4][lane], kb = st.k[1][s4][lane];
+        const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w}, wb[4] = {kb.x, kb.y, kb.z, kb.w};
 #pragma unroll
-        for (int j = 0; j < NT; ++j) mma(c[j], a0, a1, a2, a3, qf[j][s][0], qf[j][s][1]);
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t a0 = f16x2_of_e4m3(wa[i]), a1 = f16x2_of_e4m3(wb[i]), a2 = f16x2_of_e4m3(wa[i] >> 16),
+                         a3 = f16x2_of_e4m3(wb[i] >> 16);
+#pragma unroll
+          for (int j = 0; j < NT; ++j) mma(c[j], a0, a1, a2, a3, qf[j][s4 * 4 + i][0], qf[j][s4 * 4 + i][1]);
+        }
       }
-      uint32_t p[NT][2];
-      float corr[NT][2];
+      const float ks = st.ks[lane], vf = st.vs[lane] * (1.0f / kPScale);
       bool moved = false;
 #pragma unroll
       for (int j = 0; j < NT; ++j)
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          const float f = factor[j][i] * w.ks;
-          c[j][i] = g < w.valid && w.first + g <= last[j][i] ? c[j][i] * f : -INFINITY;
-          c[j][2 + i] = g + 8 < w.valid && w.first + g + 8 <= last[j][i] ? c[j][2 + i] * f : -INFINITY;
+          const float f = factor[j][i] * ks;
+          c[j][i] = g < n && at + g <= last[j][i] ? c[j][i] * f : -INFINITY;
+          c[j][2 + i] = g + 8 < n && at + g + 8 <= last[j][i] ? c[j][2 + i] * f : -INFINITY;
           // the maximum follows when a score passes it by more than 2^4
           moved |= fmaxf(c[j][i], c[j][2 + i]) > m[j][i] + 4.f;
-          corr[j][i] = 1.f;
         }
       if (__any_sync(0xffffffffu, moved)) {
 #pragma unroll
-        for (int j = 0; j < NT; ++j)
+        for (int j = 0; j < NT; ++j) {
+          float corr[2];
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             float top = fmaxf(m[j][i], fmaxf(c[j][i], c[j][2 + i]));
 #pragma unroll
             for (int off = 4; off < 32; off <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+            corr[i] = 1.f;
             if (top > m[j][i] + 4.f) {                 // by itself: not by what other rows hold
-              corr[j][i] = exp2_fast(m[j][i] - top);   // 0 for the first
-              l[j][i] *= corr[j][i];
+              corr[i] = exp2_fast(m[j][i] - top);      // 0 for the first
+              l[j][i] *= corr[i];
               m[j][i] = top;
             }
           }
+#pragma unroll
+          for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) o[j][i][k] *= corr[k & 1];
+        }
       }
+      uint32_t p[NT][2];
 #pragma unroll
       for (int j = 0; j < NT; ++j) {
         float e[4];
@@ -346,12 +405,31 @@ attn_cache_kernel(const CacheAttn a, const Parts parts) {
         p[j][0] = transposed(pack_f16(e[0] * kPScale, e[1] * kPScale));
         p[j][1] = transposed(pack_f16(e[2] * kPScale, e[3] * kPScale));
       }
-      const float vf = w.vs * (1.0f / kPScale);
+      uint32_t v[4][D / 32];
+      if (D == 128) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint4 w = st.v[i % (D / 32)][lane];
+          v[i][0] = w.x;
+          v[i][1] = w.y;
+          v[i][D / 32 - 2] = w.z;
+          v[i][D / 32 - 1] = w.w;
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const uint4 w = st.v[i][lane];
+          v[2 * i][0] = w.x;
+          v[2 * i][1] = w.y;
+          v[2 * i + 1][0] = w.z;
+          v[2 * i + 1][1] = w.w;
+        }
+      }
 #pragma unroll
       for (int i = 0; i < D / 16; ++i) {
         const uint32_t sel = i & 1 ? 0x7362 : 0x5140;
-        const uint32_t lo = __byte_perm(w.v[0][i / 2], w.v[1][i / 2], sel);
-        const uint32_t hi = __byte_perm(w.v[2][i / 2], w.v[3][i / 2], sel);
+        const uint32_t lo = __byte_perm(v[0][i / 2], v[1][i / 2], sel);
+        const uint32_t hi = __byte_perm(v[2][i / 2], v[3][i / 2], sel);
         const uint32_t a0 = f16x2_of_e4m3(lo), a1 = f16x2_of_e4m3(lo >> 16), a2 = f16x2_of_e4m3(hi),
                        a3 = f16x2_of_e4m3(hi >> 16);
 #pragma unroll
@@ -359,19 +437,22 @@ attn_cache_kernel(const CacheAttn a, const Parts parts) {
           float d[4] = {0.f, 0.f, 0.f, 0.f};
           mma(d, a0, a1, a2, a3, p[j][0], p[j][1]);
 #pragma unroll
-          for (int k = 0; k < 4; ++k) o[j][i][k] = o[j][i][k] * corr[j][k & 1] + d[k] * vf;
+          for (int k = 0; k < 4; ++k) o[j][i][k] = fmaf(d[k], vf, o[j][i][k]);
         }
       }
     };
 
-    Keys<D> w[2];
-    load(u0, w[0]);
-    for (int u = u0; u < u1; u += 2) {
-      load(u + 1, w[1]);
-      if (w[0].valid > 0) step(w[0]);
-      load(u + 2, w[0]);
-      if (w[1].valid > 0) step(w[1]);
+    for (int u = u0; u < u1; u += kStages) {
+#pragma unroll
+      for (int s = 0; s < kStages; ++s) {
+        constexpr int kAhead = kStages - 1;
+        const int next = (s + kAhead) % kStages;
+        ahead(u + s + kAhead, first[next], valid[next], ring[next]);
+        copy_wait<kAhead>();
+        if (valid[s] > 0) step(ring[s], first[s], valid[s]);
+      }
     }
+    copy_wait<0>();
 
     // ---- join the warps
 #pragma unroll
@@ -385,40 +466,46 @@ attn_cache_kernel(const CacheAttn a, const Parts parts) {
           s_l[warp][j * 8 + 2 * t + i] = l[j][i];
         }
       }
+    __syncthreads();                            // the rings are done with
 #pragma unroll
     for (int j = 0; j < NT; ++j)
 #pragma unroll
       for (int i = 0; i < D / 16; ++i)
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          s_o[warp][j * 8 + 2 * t + (k & 1)][D / 8 * g + 2 * i + (k >> 1)] = o[j][i][k];
+        for (int k = 0; k < 2; ++k)
+          *reinterpret_cast<float2*>(&s_o[warp][j * 8 + 2 * t + k][D / 8 * g + 2 * i]) =
+              make_float2(o[j][i][k], o[j][i][k + 2]);
     __syncthreads();
     const bool whole = u0 == 0 && u1 == units;
     const int slot = 2 * (int)cta + (unit_at == begin ? 0 : 1);
-    for (int i = threadIdx.x; i < rows * D; i += kThreads) {
-      const int r = i / D, c = i % D;
-      float top = s_m[0][r], sum = 0.f, all = 0.f;
+    for (int i = threadIdx.x; i < rows * (D / 4); i += kThreads) {
+      const int r = i / (D / 4), c = i % (D / 4) * 4;
+      float top = s_m[0][r], sum = 0.f;
+      float4 all = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
       for (int q = 1; q < kWarps; ++q) top = fmaxf(top, s_m[q][r]);
 #pragma unroll
       for (int q = 0; q < kWarps; ++q) {
-        const float f = s_m[q][r] == -INFINITY ? 0.f : exp2_fast(s_m[q][r] - top);
-        // a warp that saw nothing has sums of zero; one whose scores were NaN has NaN
-        sum += s_l[q][r] == 0.f ? 0.f : f == 0.f && s_m[q][r] == -INFINITY ? s_l[q][r] : f * s_l[q][r];
-        all += s_l[q][r] == 0.f ? 0.f : f == 0.f && s_m[q][r] == -INFINITY ? s_o[q][r][c] : f * s_o[q][r][c];
+        // a warp that saw nothing has a sum of 0; one that saw only NaN has no maximum, but a sum
+        if (s_l[q][r] == 0.f) continue;
+        const float f = s_m[q][r] == -INFINITY ? 1.f : exp2_fast(s_m[q][r] - top);
+        const float4 w = *reinterpret_cast<const float4*>(&s_o[q][r][c]);
+        sum = fmaf(f, s_l[q][r], sum);
+        all.x = fmaf(f, w.x, all.x);
+        all.y = fmaf(f, w.y, all.y);
+        all.z = fmaf(f, w.z, all.z);
+        all.w = fmaf(f, w.w, all.w);
       }
       if (whole) {
-        const int tok = x.s0 + (row0 + r) / a.group, h = hk * a.group + (row0 + r) % a.group;
-        a.o[((int64_t)tok * a.H + h) * D + c] = __float2bfloat16(sum == 0.f ? 0.f : all / sum);
-        if (c == 0) a.lse[(int64_t)tok * a.H + h] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
+        finish<D>(a, x.s0, hk, row0 + r, c, top, sum, all);
       } else {
-        parts.sum[((int64_t)slot * RT + r) * D + c] = all;
+        *reinterpret_cast<float4*>(parts.sum + ((int64_t)slot * RT + r) * D + c) = all;
         if (c == 0) parts.ml[(int64_t)slot * RT + r] = make_float2(top, sum);
       }
     }
     if (!whole && u0 == 0 && threadIdx.x == 0) {
-      const int64_t stop = unit_at + units - 1;          // the item's last unit
-      parts.open[cta] = Open{x.b, hk, row0, rows, x.s0, (int)(((stop + 1) * ctas - 1) / total), slot, 0};
+      const int64_t end_unit = unit_at + units - 1;      // the item's last unit
+      parts.open[cta] = Open{x.b, hk, row0, rows, x.s0, (int)(((end_unit + 1) * ctas - 1) / total), slot, 0};
     }
     __syncthreads();
     unit_at += u1 - u0;
@@ -427,38 +514,59 @@ attn_cache_kernel(const CacheAttn a, const Parts parts) {
 }
 
 // CTA c joins the parts of the item that starts in CTA c of the kernel above and goes on in
-// others, in their order: a warp per row.
+// others: warps take every eighth part of a row, then their sums are joined in order.
 template <int D, int NT>
 __global__ void __launch_bounds__(256)
 attn_cache_join_kernel(const CacheAttn a, const Parts parts) {
-  constexpr int RT = 8 * NT, W = D / 32;
+  constexpr int RT = 8 * NT, W = 8, L = D / 4;           // L lanes hold a row
+  __shared__ float s_top[W], s_sum[W];
+  __shared__ float4 s_all[W][L];
   asm volatile("griddepcontrol.wait;\n" ::: "memory");
   const Open it = parts.open[blockIdx.x];
-  if (it.last < 0) return;
-  const int lane = threadIdx.x & 31;
+  const int r = blockIdx.y;
+  if (it.last < 0 || r >= it.rows) return;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int count = it.last - (int)blockIdx.x + 1;
-  auto slot_of = [&](int i) { return i == 0 ? it.slot : 2 * ((int)blockIdx.x + i); };
-  for (int r = threadIdx.x >> 5; r < it.rows; r += 8) {
-    float top = -INFINITY, sum = 0.f, all[W];
+  auto slot_of = [&](int i) { return (int64_t)(i == 0 ? it.slot : 2 * ((int)blockIdx.x + i)); };
+  float top = -INFINITY;
+  for (int i = threadIdx.x; i < count; i += 256) top = fmaxf(top, parts.ml[slot_of(i) * RT + r].x);
 #pragma unroll
-    for (int k = 0; k < W; ++k) all[k] = 0.f;
-    for (int i = lane; i < count; i += 32) top = fmaxf(top, parts.ml[(int64_t)slot_of(i) * RT + r].x);
+  for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+  if (lane == 0) s_top[warp] = top;
+  __syncthreads();
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+  for (int i = 0; i < W; ++i) top = fmaxf(top, s_top[i]);
+  float sum = 0.f;
+  float4 all = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-    for (int i = 0; i < count; ++i) {
-      const float2 ml = parts.ml[(int64_t)slot_of(i) * RT + r];
-      const float f = ml.x == -INFINITY ? (ml.y == 0.f ? 0.f : 1.f) : exp2_fast(ml.x - top);
-      sum += ml.y * f;
-#pragma unroll
-      for (int k = 0; k < W; ++k) all[k] += f * parts.sum[((int64_t)slot_of(i) * RT + r) * D + lane + 32 * k];
+  for (int i = warp; i < count; i += W) {
+    const float2 ml = parts.ml[slot_of(i) * RT + r];
+    const float f = ml.y == 0.f ? 0.f : ml.x == -INFINITY ? 1.f : exp2_fast(ml.x - top);
+    sum = fmaf(f, ml.y, sum);
+    if (lane < L) {
+      const float4 w = *reinterpret_cast<const float4*>(parts.sum + (slot_of(i) * RT + r) * D + 4 * lane);
+      all.x = fmaf(f, w.x, all.x);
+      all.y = fmaf(f, w.y, all.y);
+      all.z = fmaf(f, w.z, all.z);
+      all.w = fmaf(f, w.w, all.w);
     }
-    const int tok = it.s0 + (it.row0 + r) / a.group, h = it.hk * a.group + (it.row0 + r) % a.group;
-#pragma unroll
-    for (int k = 0; k < W; ++k)
-      a.o[((int64_t)tok * a.H + h) * D + lane + 32 * k] = __float2bfloat16(sum == 0.f ? 0.f : all[k] / sum);
-    if (lane == 0) a.lse[(int64_t)tok * a.H + h] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
   }
+  if (lane == 0) s_sum[warp] = sum;
+  if (lane < L) s_all[warp][lane] = all;
+  __syncthreads();
+  if (threadIdx.x >= L) return;
+  sum = 0.f;
+  all = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+  for (int i = 0; i < W; ++i) {
+    const float4 w = s_all[i][threadIdx.x];
+    sum += s_sum[i];
+    all.x += w.x;
+    all.y += w.y;
+    all.z += w.z;
+    all.w += w.w;
+  }
+  finish<D>(a, it.s0, it.hk, it.row0 + r, 4 * threadIdx.x, top, sum, all);
 }
 
 int rows_of(int group, int max_add) { return (int64_t)group * max_add <= 8 ? 8 : 16; }
@@ -475,10 +583,13 @@ sparsp_status_t go(const CacheAttn& a, void* ws, cudaStream_t st) {
   p.ml = (float2*)at;
   at += align((size_t)2 * kGrid * RT * sizeof(float2));
   p.sum = (float*)at;
-  attn_cache_kernel<D, NT><<<kGrid, kThreads, 0, st>>>(a, p);
+  constexpr int smem = attn_smem<D, NT>();
+  if (cudaFuncSetAttribute(attn_cache_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+    return SPARSP_ERR_CUDA;
+  attn_cache_kernel<D, NT><<<152 * ctas_per_sm(D, NT), kThreads, smem, st>>>(a, p);
   SPARSP_LAUNCH_CHECK();
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(kGrid);
+  cfg.gridDim = dim3(152 * ctas_per_sm(D, NT), RT);
   cfg.blockDim = dim3(256);
   cfg.stream = st;
   cudaLaunchAttribute attr{};

@@ -16,7 +16,9 @@
 // of new tokens in one block is one pass: its values wait in registers for their
 // maximum. Bound by HBM.
 #include <cooperative_groups.h>
-#include <cuda_fp8.h>
+#include <cuda_fp16.h>
+
+#include <type_traits>
 
 #include "cache.cuh"
 #include "rows.cuh"
@@ -184,126 +186,183 @@ __device__ __forceinline__ float2 e4m3_values(uint32_t pair) {
   return __half22float2(*reinterpret_cast<__half2*>(&h));
 }
 
-// The scale of values of up to `most` (finite, not negative): 448 = 1.75 * 2^8.
-__device__ __forceinline__ float scale_of(float most) {
-  const uint32_t u = __float_as_uint(most);
-  int e = (int)(u >> 23) - 127 - 8 + ((u & 0x7fffffu) > 0x600000u ? 1 : 0);
+// The scale of values of up to `most` (finite, not negative; as bits): 448 = 1.75 * 2^8.
+__device__ __forceinline__ float scale_of(uint32_t most) {
+  const int e = (int)(most >> 23) - 127 - 8 + ((most & 0x7fffffu) > 0x600000u ? 1 : 0);
+  return __uint_as_float((uint32_t)(max(e, -100) + 127) << 23);
+}
+// The smallest power of two from 2^-100 on that is not below a scale (0 < x <= 2^120).
+__device__ __forceinline__ float power_above(float x) {
+  const uint32_t u = __float_as_uint(x);
+  const int e = (int)(u >> 23) - 127 + ((u & 0x7fffffu) != 0 ? 1 : 0);
   return __uint_as_float((uint32_t)(max(e, -100) + 127) << 23);
 }
 
+constexpr uint32_t kInf = 0x7f800000u;   // magnitudes as bits: from here on not finite
+
+// 16 bytes of new values: their largest magnitude (as fp32 bits; as they come, or of the
+// finite ones), and their codes under 1 / scale.
+template <typename T>
+struct Fresh;
+template <>
+struct Fresh<__nv_bfloat16> {
+  static constexpr int E = 8;
+  static __device__ __forceinline__ uint32_t most(const uint4& v) {
+    const uint32_t m = __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu),
+                                __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu));
+    return max(m << 16, m & 0xffff0000u);
+  }
+  static __device__ __forceinline__ void values(const uint4& v, float* f) { Row16<__nv_bfloat16>::unpack(v, f); }
+};
+template <>
+struct Fresh<float> {
+  static constexpr int E = 4;
+  static __device__ __forceinline__ uint32_t most(const uint4& v) {
+    return max(max(v.x & 0x7fffffffu, v.y & 0x7fffffffu), max(v.z & 0x7fffffffu, v.w & 0x7fffffffu));
+  }
+  static __device__ __forceinline__ void values(const uint4& v, float* f) { Row16<float>::unpack(v, f); }
+};
+template <typename T>
+__device__ __forceinline__ uint32_t finite_most(const uint4& v) {
+  float f[Fresh<T>::E];
+  Fresh<T>::values(v, f);
+  uint32_t m = 0;
+#pragma unroll
+  for (int e = 0; e < Fresh<T>::E; ++e) {
+    const uint32_t u = __float_as_uint(f[e]) & 0x7fffffffu;
+    if (u < kInf) m = max(m, u);
+  }
+  return m;
+}
+template <typename T>
+__device__ __forceinline__ void store_codes(uint8_t* to, const uint4& v, float inverse, bool finite) {
+  constexpr int E = Fresh<T>::E;
+  float f[E];
+  Fresh<T>::values(v, f);
+  if (!finite)   // what is not finite is held as NaN
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+      if (!(fabsf(f[e]) < INFINITY)) f[e] = NAN;
+  uint32_t code[E / 4];
+#pragma unroll
+  for (int e = 0; e < E / 4; ++e)
+    code[e] = e4m3_pair(f[4 * e] * inverse, f[4 * e + 1] * inverse) |
+              e4m3_pair(f[4 * e + 2] * inverse, f[4 * e + 3] * inverse) << 16;
+  if (E == 8) *reinterpret_cast<uint2*>(to) = make_uint2(code[0], code[E / 4 - 1]);
+  else *reinterpret_cast<uint32_t*>(to) = code[0];
+}
+
 constexpr int kWriteThreads = 256;
-constexpr int kGranule = 64;      // most packed tokens that one CTA looks for runs in
+constexpr int kGranule = 128;     // most packed tokens that one CTA looks for runs in
+constexpr int kShortRun = 4;      // tokens of a run that one warp takes by itself
 
 // CTA (granule of packed tokens, head, K or V). A run is new tokens in a row whose slots
-// are next to each other in one block; it belongs to the granule it starts in.
+// are next to each other in one block; it belongs to the granule it starts in. A short run is a
+// warp's, a longer one the CTA's. Every warp finds the runs for itself.
 template <typename T, int D, int BT>
 __global__ void __launch_bounds__(kWriteThreads)
 cache_write_kernel(const CacheDims c, const CacheWrite a, int granule, int32_t* d_status) {
-  using X = Row16<T>;
-  constexpr int E = X::E, LPR = D / E, kRows = kWriteThreads / LPR, U = BT / kRows;   // lanes per row, rows a sweep
-  static_assert(U * kRows == BT, "rows of a block");
-  __shared__ uint64_t s_heads;      // the granule's tokens that start a run
-  __shared__ int s_count;
-  __shared__ float s_most[kWriteThreads / 32];
+  constexpr int E = Fresh<T>::E, LPR = D / E;        // lanes per row
+  __shared__ uint32_t s_most[2][kWriteThreads / 32];
   const int h = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const bool is_v = blockIdx.z != 0;
   const T* x = static_cast<const T*>(is_v ? a.v : a.k) + (int64_t)h * (is_v ? a.v_head : a.k_head);
   const int64_t stride = is_v ? a.v_token : a.k_token;
   uint8_t* codes = is_v ? a.vc : a.kc;
   float* scales = is_v ? a.vs : a.ks;
-  const int64_t capacity = (int64_t)c.blocks * BT;
-  const int64_t t0 = (int64_t)blockIdx.x * granule;
-  if (threadIdx.x == 0) s_heads = 0;
-  __syncthreads();
-  if (threadIdx.x < granule && t0 + threadIdx.x < a.tokens) {
-    const int64_t t = t0 + threadIdx.x;
-    const int slot = a.slots[t];
-    if (slot >= capacity) report(d_status, SPARSP_ERR_DATA);
-    else if (slot >= 0 && (t == 0 || slot % BT == 0 || a.slots[t - 1] != slot - 1))
-      atomicOr((unsigned long long*)&s_heads, 1ull << threadIdx.x);
-  }
-  __syncthreads();
-  const int c0 = threadIdx.x % LPR, r0 = threadIdx.x / LPR;
-  for (uint64_t heads = s_heads; heads != 0; heads &= heads - 1) {
-    const int64_t first = t0 + __ffsll((long long)heads) - 1;
-    const int slot = a.slots[first], block = slot / BT, off = slot % BT;
-    // how many tokens follow in the same block
-    if (threadIdx.x == 0) s_count = BT - off;
-    __syncthreads();
-    if (threadIdx.x > 0 && threadIdx.x < BT - off &&
-        (first + threadIdx.x >= a.tokens || a.slots[first + threadIdx.x] != slot + (int)threadIdx.x))
-      atomicMin(&s_count, (int)threadIdx.x);
-    __syncthreads();
-    const int count = s_count;
+  const int64_t capacity = (int64_t)c.blocks * BT, t0 = (int64_t)blockIdx.x * granule;
+  int turn = 0, buf = 0;
+
+  // One run of `count` tokens from packed token `first` on; t of `threads` threads take part.
+  auto run = [&](int64_t first, int slot, int count, int t, auto threads, auto sweeps, auto reduce) {
+    constexpr int kRows = decltype(threads)::value / LPR, U = decltype(sweeps)::value;
+    const int c0 = t % LPR, r0 = t / LPR, block = slot / BT, off = slot % BT;
+    const T* from = x + first * stride + c0 * E;
     uint4 w[U];
 #pragma unroll
     for (int u = 0; u < U; ++u)
-      if (r0 + u * kRows < count)
-        w[u] = __ldg(reinterpret_cast<const uint4*>(x + (first + r0 + u * kRows) * stride) + c0);
+      if (r0 + u * kRows < count) w[u] = __ldg(reinterpret_cast<const uint4*>(from + (r0 + u * kRows) * stride));
     float* scale_at = scales + (int64_t)block * c.heads + h;
     const float old = off > 0 ? *scale_at : 0.f;
-    float most = 0.f;
-    bool finite = true;
+    uint32_t most = 0;
 #pragma unroll
     for (int u = 0; u < U; ++u)
-      if (r0 + u * kRows < count) {
-        float f[E];
-        X::unpack(w[u], f);
+      if (r0 + u * kRows < count) most = max(most, Fresh<T>::most(w[u]));
+    most = reduce(most);                             // also: every thread has read the old scale
+    const bool finite = most < kInf;
+    if (!finite) {
+      if (t == 0) report(d_status, SPARSP_ERR_DATA);
+      most = 0;
 #pragma unroll
-        for (int e = 0; e < E; ++e) {
-          const float m = fabsf(f[e]);
-          if (m < INFINITY) most = fmaxf(most, m);
-          else finite = false;
-        }
-      }
-    if (!finite) report(d_status, SPARSP_ERR_DATA);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
-    if (lane == 0) s_most[warp] = most;
-    __syncthreads();                              // also: every thread has read the old scale
-#pragma unroll
-    for (int i = 0; i < kWriteThreads / 32; ++i) most = fmaxf(most, s_most[i]);
+      for (int u = 0; u < U; ++u)
+        if (r0 + u * kRows < count) most = max(most, finite_most<T>(w[u]));
+      most = reduce(most);
+    }
     float scale = scale_of(most);
-    const bool kept = off > 0 && old > 0.f && old < INFINITY;
-    if (off > 0 && !kept) report(d_status, SPARSP_ERR_DATA);   // codes without a scale: left as they are
-    if (kept && old >= scale) scale = old;
-    if (threadIdx.x == 0) *scale_at = scale;
-    const bool exact = (__float_as_uint(scale) & 0x7fffffu) == 0;   // a scale of this call's: its inverse is exact
-    const float inverse = 1.0f / scale;
+    const bool kept = old > 0.f && old <= 0x1p120f;  // of older tokens (never of off == 0)
+    if (off > 0 && !kept && t == 0) report(d_status, SPARSP_ERR_DATA);   // codes without a scale stay as they are
+    if (kept) scale = fmaxf(scale, power_above(old));
+    if (t == 0) *scale_at = scale;
+    const float inverse = __uint_as_float((254u << 23) - __float_as_uint(scale));   // of a power of two
     uint8_t* base = codes + ((int64_t)block * c.heads + h) * BT * D;
 #pragma unroll
     for (int u = 0; u < U; ++u)
-      if (r0 + u * kRows < count) {
-        float f[E];
-        X::unpack(w[u], f);
-        uint32_t code[E / 4];
-#pragma unroll
-        for (int e = 0; e < E; ++e)   // what is not finite is held as NaN
-          f[e] = fabsf(f[e]) < INFINITY ? (exact ? f[e] * inverse : f[e] / scale) : NAN;
-#pragma unroll
-        for (int e = 0; e < E / 4; ++e)
-          code[e] = e4m3_pair(f[4 * e], f[4 * e + 1]) | e4m3_pair(f[4 * e + 2], f[4 * e + 3]) << 16;
-        uint8_t* to = base + (int64_t)(off + r0 + u * kRows) * D + c0 * E;
-        if (E == 8) *reinterpret_cast<uint2*>(to) = make_uint2(code[0], code[E / 4 - 1]);
-        else *reinterpret_cast<uint32_t*>(to) = code[0];
-      }
-    if (kept && scale > old) {                    // older tokens of the block, brought to the larger scale
-      const float ratio = old / scale;
-      for (int i = threadIdx.x; i < off * D / 4; i += kWriteThreads) {
+      if (r0 + u * kRows < count)
+        store_codes<T>(base + (int64_t)(off + r0 + u * kRows) * D + c0 * E, w[u], inverse, finite);
+    if (kept && scale != old) {                      // older tokens, brought to the larger scale
+      const float ratio = old * inverse;
+      for (int i = t; i < off * D / 4; i += decltype(threads)::value) {
         uint32_t& word = reinterpret_cast<uint32_t*>(base)[i];
         const float2 lo = e4m3_values(word & 0xffffu), hi = e4m3_values(word >> 16);
         word = e4m3_pair(lo.x * ratio, lo.y * ratio) | e4m3_pair(hi.x * ratio, hi.y * ratio) << 16;
       }
     }
-    __syncthreads();                              // s_count and s_most are written again
+  };
+
+  for (int g0 = 0; g0 < granule; g0 += 32) {
+    const int64_t t = t0 + g0 + lane;
+    bool head = false;
+    if (g0 + lane < granule && t < a.tokens) {
+      const int slot = a.slots[t];
+      if (slot >= capacity) report(d_status, SPARSP_ERR_DATA);
+      else head = slot >= 0 && (t == 0 || slot % BT == 0 || a.slots[t - 1] != slot - 1);
+    }
+    for (uint32_t heads = __ballot_sync(0xffffffffu, head); heads != 0; heads &= heads - 1) {
+      const int64_t first = t0 + g0 + __ffs(heads) - 1;
+      const int slot = a.slots[first], room = BT - slot % BT;
+      int count = 0;                                 // tokens that follow one another in the block
+      for (int i = 0; i < room; i += 32) {
+        const int r = i + lane;
+        const uint32_t on = __ballot_sync(0xffffffffu, r < room && first + r < a.tokens && a.slots[first + r] == slot + r);
+        count += on == 0xffffffffu ? 32 : __ffs(~on) - 1;
+        if (on != 0xffffffffu) break;
+      }
+      if (count <= kShortRun) {
+        if (turn++ % (kWriteThreads / 32) == warp)
+          run(first, slot, count, lane, std::integral_constant<int, 32>{},
+              std::integral_constant<int, kShortRun * LPR / 32>{},
+              [](uint32_t v) { return __reduce_max_sync(0xffffffffu, v); });
+      } else {
+        run(first, slot, count, (int)threadIdx.x, std::integral_constant<int, kWriteThreads>{},
+            std::integral_constant<int, BT * LPR / kWriteThreads>{}, [&](uint32_t v) {
+              v = __reduce_max_sync(0xffffffffu, v);
+              if (lane == 0) s_most[buf][warp] = v;
+              __syncthreads();                       // the buffers alternate: one barrier is enough
+#pragma unroll
+              for (int i = 0; i < kWriteThreads / 32; ++i) v = max(v, s_most[buf][i]);
+              buf ^= 1;
+              return v;
+            });
+      }
+    }
   }
 }
 
 template <typename T, int D, int BT>
 void go_write(const CacheDims& c, const CacheWrite& a, int32_t* d_status, cudaStream_t st) {
-  // granules as large as still leave about sixteen CTAs per SM
+  // granules as large as still leave three CTAs per SM
   int granule = kGranule;
-  while (granule > 1 && (int64_t)((a.tokens + granule - 1) / granule) * c.heads * 2 < 152 * 16) granule /= 2;
+  while (granule > 8 && (int64_t)((a.tokens + granule - 1) / granule) * c.heads * 2 < 152 * 3) granule /= 2;
   const dim3 grid((unsigned)((a.tokens + granule - 1) / granule), (unsigned)c.heads, 2);
   cache_write_kernel<T, D, BT><<<grid, kWriteThreads, 0, st>>>(c, a, granule, d_status);
 }

@@ -30,47 +30,13 @@
 // threads, whose registers do not hold the backward's sums: it spills 288 to 372 bytes a
 // thread and takes about twice the bytes' time (fp32, 30,720 rows of 5,120: 641 us, floor 283;
 // bf16, rows of 12,288: 687, floor 340).
-#include "common.cuh"
-#include "tc_helpers.cuh"
+#include "rows.cuh"
 
 namespace sparsp {
 namespace {
 
 constexpr int kWarpThreads = 256;   // CTA of the shuffle kernels
 constexpr int kMaxWarps = 32;
-
-// Two fp32 values in one 64-bit register pair, for the packed fp32 instructions:
-// held as one operand from load to store, so that no moves are spent on pairing.
-typedef unsigned long long f32x2;
-__device__ __forceinline__ f32x2 pair(float a, float b) {
-  f32x2 r;
-  asm("mov.b64 %0, {%1, %2};\n" : "=l"(r) : "f"(a), "f"(b));
-  return r;
-}
-__device__ __forceinline__ float2 both(f32x2 v) {
-  float2 r;
-  asm("mov.b64 {%0, %1}, %2;\n" : "=f"(r.x), "=f"(r.y) : "l"(v));
-  return r;
-}
-__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
-  f32x2 r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;\n" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
-  f32x2 r;
-  asm("mul.rn.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
-  f32x2 r;
-  asm("add.rn.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ float hsum(f32x2 v) {
-  const float2 t = both(v);
-  return t.x + t.y;
-}
 
 // 16 bytes of a row as fp32 pairs and back.
 template <typename T>
@@ -123,14 +89,8 @@ struct Rows {
   }
 };
 
-__device__ __forceinline__ void copy_async16(void* dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(tc::smem_u32(dst)), "l"(src) : "memory");
-}
-__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;\n" ::: "memory"); }
 // Until at most n of this thread's copy groups are in flight (n < 4).
-template <int N>
-__device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;\n" ::"n"(N) : "memory"); }
-__device__ __forceinline__ void copy_wait(int n) {
+__device__ __forceinline__ void copy_wait_for(int n) {
   if (n == 3) copy_wait<3>();
   else if (n == 2) copy_wait<2>();
   else if (n == 1) copy_wait<1>();
@@ -366,7 +326,7 @@ norm_fwd_cta_kernel(const Rows R, const T* __restrict__ x, int64_t x_stride,
   int st = 0;
   for (int64_t base = first; base < R.rows; base += step, st = st + 1 == depth ? 0 : st + 1) {
     fetch(base + (depth - 1) * step, st == 0 ? depth - 1 : st - 1);   // the slots of the step before
-    copy_wait(depth - 1);
+    copy_wait_for(depth - 1);
     uint4 xv[RB][U];
 #pragma unroll
     for (int r = 0; r < RB; ++r)
@@ -575,7 +535,7 @@ norm_bwd_cta_kernel(const Rows R, const T* __restrict__ dy, const T* __restrict_
   }
   for (int64_t row = blockIdx.x; row < R.rows; row += step, st = st + 1 == depth ? 0 : st + 1) {
     fetch(row + (depth - 1) * step, st == 0 ? depth - 1 : st - 1);
-    copy_wait(depth - 1);
+    copy_wait_for(depth - 1);
     const float mu = mu_n, rs = rs_n;
     if (row + step < R.rows) {
       mu_n = RMS ? 0.f : mean[row + step];

@@ -25,6 +25,7 @@ struct Cfg {
   static constexpr int NV = HALF ? 2 : 1;                      // vectors of a unit
   static constexpr int NE = NV * E;                            // values of a unit
   static constexpr int NP = NE / 2;                            // pairs of a unit
+  static constexpr int P2 = Unit<T, HALF>::P2;                 // the same, two to a packed operand
   static constexpr int UPR = D / NE;                           // units (lanes) per row
   static constexpr int VECS = GR * D / E;                      // vectors of a granule
   static constexpr int THREADS = VECS >= 2048 ? 512 : 256;      // 4 to 8 vectors a thread
@@ -112,16 +113,56 @@ __device__ __forceinline__ float2 turn_of(const RopeArgs& a, const int4& tk, int
   return make_float2(v.x, v.y * a.sign);
 }
 
-template <bool HALF, int E, int NP>
-__device__ __forceinline__ void turn(float* f, const float2* cs) {
+// (x, y) -> (x c - y s, x s + y c), two pairs at a time.
+template <int P2>
+__device__ __forceinline__ void turn(f32x2* x, f32x2* y, const f32x2* c, const f32x2* s) {
 #pragma unroll
-  for (int k = 0; k < NP; ++k) {
-    float& x = f[HALF ? k : 2 * k];
-    float& y = f[HALF ? E + k : 2 * k + 1];
-    const float r = x * cs[k].x - y * cs[k].y;
-    y = x * cs[k].y + y * cs[k].x;
-    x = r;
+  for (int i = 0; i < P2; ++i) {
+    const f32x2 r = fma2(x[i], c[i], mul2(y[i], s[i] ^ 0x8000000080000000ull));
+    y[i] = fma2(y[i], c[i], mul2(x[i], s[i]));
+    x[i] = r;
   }
+}
+
+// The columns of pair i of unit column c0.
+template <int D, int E, bool HALF>
+__device__ __forceinline__ int col_x(int c0, int i) { return c0 * E + (HALF ? i : 2 * i); }
+template <int D, int E, bool HALF>
+__device__ __forceinline__ int col_y(int c0, int i) { return HALF ? c0 * E + i + D / 2 : c0 * E + 2 * i + 1; }
+
+// A parameter vector's values at a lane's columns.
+template <int D, int E, bool HALF, int P2>
+__device__ __forceinline__ void params(const float* p, float none, int c0, f32x2* x, f32x2* y) {
+#pragma unroll
+  for (int i = 0; i < P2; ++i) {
+    float v[4] = {none, none, none, none};
+    if (p != nullptr) {
+      v[0] = __ldg(p + col_x<D, E, HALF>(c0, 2 * i));
+      v[1] = __ldg(p + col_x<D, E, HALF>(c0, 2 * i + 1));
+      v[2] = __ldg(p + col_y<D, E, HALF>(c0, 2 * i));
+      v[3] = __ldg(p + col_y<D, E, HALF>(c0, 2 * i + 1));
+    }
+    x[i] = pair(v[0], v[1]);
+    y[i] = pair(v[2], v[3]);
+  }
+}
+
+template <int P2>
+__device__ __forceinline__ float sum_of(const f32x2* x, const f32x2* y) {
+  f32x2 a = add2(x[0], y[0]);
+#pragma unroll
+  for (int i = 1; i < P2; ++i) a = add2(a, add2(x[i], y[i]));
+  return hsum(a);
+}
+template <int P2>   // sum of a b over both halves of the pairs
+__device__ __forceinline__ float dot_of(const f32x2* ax, const f32x2* ay, const f32x2* bx, const f32x2* by) {
+  f32x2 a = mul2(ax[0], bx[0]), b = mul2(ay[0], by[0]);
+#pragma unroll
+  for (int i = 1; i < P2; ++i) {
+    a = fma2(ax[i], bx[i], a);
+    b = fma2(ay[i], by[i], b);
+  }
+  return hsum(add2(a, b));
 }
 
 // Sums over the UPR lanes that share a row.
@@ -135,16 +176,16 @@ __device__ __forceinline__ void row_sum(float (&v)[K]) {
 
 constexpr int kDepth = 3;   // heads in flight per CTA
 
-template <typename T, int D, int GR, bool HALF, bool POOL>
+// BIAS: there may be one (a layer norm, or an RMS norm with a bias).
+template <typename T, int D, int GR, bool HALF, bool POOL, bool BIAS>
 __global__ void __launch_bounds__(Cfg<T, D, GR, HALF>::THREADS)
 norm_rope_fwd_kernel(const Fwd q, const Fwd k, const Tokens tk, const RopeArgs a, bool rms, float eps, bool out_blocked,
                      int heads_per_cta, int32_t* d_status) {
   using C = Cfg<T, D, GR, HALF>;
-  using X = Row16<T>;
-  constexpr int E = C::E, NE = C::NE;
+  using X = Unit<T, HALF>;
+  constexpr int E = C::E, P2 = C::P2;
   __shared__ int4 tok[GR];
-  constexpr int kPart = C::THREADS / 32 * C::UPR;
-  __shared__ float part[POOL ? 2 : 1][POOL ? kPart : 1][POOL ? NE + 1 : 1];
+  __shared__ float part[POOL ? 2 : 1][POOL ? C::THREADS / 32 : 1][POOL ? D : 1];   // per warp, its columns' sums
   extern __shared__ uint4 ring[];   // [min(kDepth, heads)][U][NV][THREADS]
   const bool is_q = blockIdx.y < q.groups;
   const Fwd& t = is_q ? q : k;
@@ -154,22 +195,22 @@ norm_rope_fwd_kernel(const Fwd q, const Fwd k, const Tokens tk, const RopeArgs a
   locate<GR, C::THREADS>(tok, tk, a, d_status);
   __syncthreads();
   const int c0 = threadIdx.x % C::UPR, o0 = threadIdx.x / C::UPR;   // this thread's unit column, its first row
-  float2 cs[C::U][C::NP];
-  int64_t flat[C::U];
+  f32x2 cos[C::U][P2], sin[C::U][P2];
+  int flat[C::U];
 #pragma unroll
   for (int u = 0; u < C::U; ++u) {
     const int4 w = tok[o0 + u * C::kRowStep];
     flat[u] = w.x;
 #pragma unroll
-    for (int i = 0; i < C::NP; ++i) cs[u][i] = turn_of(a, w, c0 * C::NP + i);
+    for (int i = 0; i < P2; ++i) {
+      const float2 p = turn_of(a, w, c0 * C::NP + 2 * i), q = turn_of(a, w, c0 * C::NP + 2 * i + 1);
+      cos[u][i] = pair(p.x, q.x);
+      sin[u][i] = pair(p.y, q.y);
+    }
   }
-  float w[NE], b[NE];
-#pragma unroll
-  for (int e = 0; e < NE; ++e) {
-    const int c = c0 * E + (e / E) * (D / 2) + e % E;
-    w[e] = t.w != nullptr ? __ldg(t.w + c) : 1.f;
-    b[e] = t.b != nullptr ? __ldg(t.b + c) : 0.f;
-  }
+  f32x2 wx[P2], wy[P2], bx[P2], by[P2];
+  params<D, E, HALF, P2>(t.w, 1.f, c0, wx, wy);
+  if (BIAS) params<D, E, HALF, P2>(t.b, 0.f, c0, bx, by);
   // rows of tile order: those of head h of this granule's batch element start at blocked0(h)
   const int64_t N = tk.rm.N;
   const int64_t at = (int64_t)blockIdx.x * GR, batch = at / N, row0 = at - batch * N;
@@ -191,59 +232,74 @@ norm_rope_fwd_kernel(const Fwd q, const Fwd k, const Tokens tk, const RopeArgs a
   for (int h = h0; h < h1; ++h, st = st + 1 == kDepth ? 0 : st + 1) {
     fetch(h + kDepth - 1, st == 0 ? kDepth - 1 : st - 1);   // the slots of the head before
     copy_wait<kDepth - 1>();
-    float acc[NE];
+    f32x2 ax[P2], ay[P2];
 #pragma unroll
-    for (int e = 0; e < NE; ++e) acc[e] = 0.f;
+    for (int i = 0; i < P2; ++i) ax[i] = ay[i] = 0;   // two zeros
 #pragma unroll
     for (int u = 0; u < C::U; ++u) {
-      float f[NE];
+      f32x2 x[P2], y[P2];
+      uint4 v16[C::NV];
 #pragma unroll
-      for (int v = 0; v < C::NV; ++v) X::unpack(*place(st, u, v), f + v * E);
-      if (!rms) {
-        float m[1] = {0.f};
-#pragma unroll
-        for (int e = 0; e < NE; ++e) m[0] += f[e];
+      for (int v = 0; v < C::NV; ++v) v16[v] = *place(st, u, v);
+      X::unpack(v16, x, y);
+      if (BIAS && !rms) {
+        float m[1] = {sum_of<P2>(x, y)};
         row_sum<C::UPR>(m);
+        const f32x2 mean = pair(m[0] * (-1.0f / D), m[0] * (-1.0f / D));
 #pragma unroll
-        for (int e = 0; e < NE; ++e) f[e] -= m[0] * (1.0f / D);
+        for (int i = 0; i < P2; ++i) {
+          x[i] = add2(x[i], mean);
+          y[i] = add2(y[i], mean);
+        }
       }
-      float s[1] = {0.f};
-#pragma unroll
-      for (int e = 0; e < NE; ++e) s[0] += f[e] * f[e];
+      float s[1] = {dot_of<P2>(x, y, x, y)};
       row_sum<C::UPR>(s);
-      const float rstd = 1.0f / sqrtf(s[0] * (1.0f / D) + eps);
+      const float rstd = inv_sqrt(s[0] * (1.0f / D) + eps);
+      const f32x2 r2 = pair(rstd, rstd);
 #pragma unroll
-      for (int e = 0; e < NE; ++e) f[e] = f[e] * rstd * w[e] + b[e];
-      turn<HALF, E, C::NP>(f, cs[u]);
+      for (int i = 0; i < P2; ++i) {
+        x[i] = BIAS ? fma2(mul2(x[i], r2), wx[i], bx[i]) : mul2(mul2(x[i], r2), wx[i]);
+        y[i] = BIAS ? fma2(mul2(y[i], r2), wy[i], by[i]) : mul2(mul2(y[i], r2), wy[i]);
+      }
+      turn<P2>(x, y, cos[u], sin[u]);
       if (POOL)
 #pragma unroll
-        for (int e = 0; e < NE; ++e) acc[e] += f[e];
+        for (int i = 0; i < P2; ++i) {
+          ax[i] = add2(ax[i], x[i]);
+          ay[i] = add2(ay[i], y[i]);
+        }
       if (flat[u] >= 0) {
         T* dst = out + (out_blocked ? ((batch * t.heads + h) * N + row0 + o0 + u * C::kRowStep) * D
                                     : flat[u] * t.out_stride + (int64_t)h * D);
+        X::pack(x, y, v16);
 #pragma unroll
-        for (int v = 0; v < C::NV; ++v)
-          __stcs(reinterpret_cast<uint4*>(dst + c0 * E + v * (D / 2)), X::pack(f + v * E));
+        for (int v = 0; v < C::NV; ++v) __stcs(reinterpret_cast<uint4*>(dst + c0 * E + v * (D / 2)), v16[v]);
       }
     }
     // the means of the fp32 values: summed per thread, over the lanes that share its
     // columns, then over the warps in order
     if constexpr (POOL) {
       if (t.means == nullptr) continue;   // the same for the whole CTA
-      float (*sum)[NE + 1] = part[(h - h0) & 1];   // the other one may still be read
+      float (*sum)[D] = part[(h - h0) & 1];          // the other one may still be read
 #pragma unroll
-      for (int off = 16; off >= C::UPR; off >>= 1)
+      for (int i = 0; i < C::NP; ++i) {
+        const float2 px = both(ax[i / 2]), py = both(ay[i / 2]);
+        float vx = i & 1 ? px.y : px.x, vy = i & 1 ? py.y : py.x;
 #pragma unroll
-        for (int e = 0; e < NE; ++e) acc[e] += __shfl_xor_sync(0xffffffffu, acc[e], off);
-      if ((threadIdx.x & 31) < C::UPR)
-#pragma unroll
-        for (int e = 0; e < NE; ++e) sum[(threadIdx.x >> 5) * C::UPR + c0][e] = acc[e];
+        for (int off = 16; off >= C::UPR; off >>= 1) {
+          vx += __shfl_xor_sync(0xffffffffu, vx, off);
+          vy += __shfl_xor_sync(0xffffffffu, vy, off);
+        }
+        if ((threadIdx.x & 31) < C::UPR) {
+          sum[threadIdx.x >> 5][col_x<D, E, HALF>(c0, i)] = vx;
+          sum[threadIdx.x >> 5][col_y<D, E, HALF>(c0, i)] = vy;
+        }
+      }
       __syncthreads();
       for (int c = threadIdx.x; c < D; c += C::THREADS) {
-        const int v = HALF ? c / (D / 2) : 0, cc = HALF ? c % (D / 2) : c;
         float s = 0.f;
 #pragma unroll
-        for (int g = 0; g < C::THREADS / 32; ++g) s += sum[g * C::UPR + cc / E][v * E + cc % E];
+        for (int g = 0; g < C::THREADS / 32; ++g) s += sum[g][c];
         t.means[((batch * t.heads + h) * (N / GR) + row0 / GR) * D + c] = s * (1.0f / (float)GR);
       }
     }
@@ -252,13 +308,13 @@ norm_rope_fwd_kernel(const Fwd q, const Fwd k, const Tokens tk, const RopeArgs a
 }
 
 // Each CTA leaves its columns' sums in part [CTA of q, then of k][dw, db][D].
-template <typename T, int D, int GR, bool HALF>
+template <typename T, int D, int GR, bool HALF, bool RMS>
 __global__ void __launch_bounds__(Cfg<T, D, GR, HALF>::THREADS)
-norm_rope_bwd_kernel(const Bwd q, const Bwd k, const Tokens tk, const RopeArgs a, bool rms, float eps, bool in_blocked,
+norm_rope_bwd_kernel(const Bwd q, const Bwd k, const Tokens tk, const RopeArgs a, float eps, bool in_blocked,
                      int heads_per_cta, float* __restrict__ part, int32_t* d_status) {
   using C = Cfg<T, D, GR, HALF>;
-  using X = Row16<T>;
-  constexpr int E = C::E, NE = C::NE;
+  using X = Unit<T, HALF>;
+  constexpr int E = C::E, P2 = C::P2;
   __shared__ int4 tok[GR];
   extern __shared__ uint4 ring[];   // [min(kDepth, heads)][x, dy][U][NV][THREADS]
   const bool is_q = blockIdx.y < q.groups;
@@ -271,21 +327,23 @@ norm_rope_bwd_kernel(const Bwd q, const Bwd k, const Tokens tk, const RopeArgs a
   locate<GR, C::THREADS>(tok, tk, a, d_status);
   __syncthreads();
   const int c0 = threadIdx.x % C::UPR, o0 = threadIdx.x / C::UPR;
-  float2 cs[C::U][C::NP];
-  int64_t flat[C::U];
+  f32x2 cos[C::U][P2], sin[C::U][P2];
+  int flat[C::U];
 #pragma unroll
   for (int u = 0; u < C::U; ++u) {
     const int4 w = tok[o0 + u * C::kRowStep];
     flat[u] = w.x;
 #pragma unroll
-    for (int i = 0; i < C::NP; ++i) cs[u][i] = turn_of(a, w, c0 * C::NP + i);
+    for (int i = 0; i < P2; ++i) {
+      const float2 p = turn_of(a, w, c0 * C::NP + 2 * i), q = turn_of(a, w, c0 * C::NP + 2 * i + 1);
+      cos[u][i] = pair(p.x, q.x);
+      sin[u][i] = pair(p.y, q.y);
+    }
   }
-  float w[NE], dw[NE], db[NE];
+  f32x2 wx[P2], wy[P2], dwx[P2], dwy[P2], dbx[P2], dby[P2];
+  params<D, E, HALF, P2>(t.w, 1.f, c0, wx, wy);
 #pragma unroll
-  for (int e = 0; e < NE; ++e) {
-    w[e] = t.w != nullptr ? __ldg(t.w + c0 * E + (e / E) * (D / 2) + e % E) : 1.f;
-    dw[e] = db[e] = 0.f;
-  }
+  for (int i = 0; i < P2; ++i) dwx[i] = dwy[i] = dbx[i] = dby[i] = 0;   // two zeros
   const int64_t N = tk.rm.N;
   const int64_t at = (int64_t)blockIdx.x * GR, batch = at / N, row0 = at - batch * N;
   auto place = [&](int st, int which, int u, int v) {
@@ -316,67 +374,84 @@ norm_rope_bwd_kernel(const Bwd q, const Bwd k, const Tokens tk, const RopeArgs a
 #pragma unroll
     for (int u = 0; u < C::U; ++u) {
       const bool live = flat[u] >= 0;
-      float f[NE], g[NE];
+      f32x2 fx[P2], fy[P2], gx[P2], gy[P2];
+      uint4 v16[C::NV];
 #pragma unroll
-      for (int v = 0; v < C::NV; ++v) {
-        X::unpack(*place(st, 0, u, v), f + v * E);
-        X::unpack(*place(st, 1, u, v), g + v * E);
-      }
-      turn<HALF, E, C::NP>(g, cs[u]);
-      if (!rms) {
-        float m[1] = {0.f};
+      for (int v = 0; v < C::NV; ++v) v16[v] = *place(st, 1, u, v);
+      X::unpack(v16, gx, gy);
 #pragma unroll
-        for (int e = 0; e < NE; ++e) m[0] += f[e];
+      for (int v = 0; v < C::NV; ++v) v16[v] = *place(st, 0, u, v);
+      X::unpack(v16, fx, fy);
+      turn<P2>(gx, gy, cos[u], sin[u]);
+      if (!RMS) {
+        float m[1] = {sum_of<P2>(fx, fy)};
         row_sum<C::UPR>(m);
+        const f32x2 mean = pair(m[0] * (-1.0f / D), m[0] * (-1.0f / D));
 #pragma unroll
-        for (int e = 0; e < NE; ++e) f[e] -= m[0] * (1.0f / D);
-      }
-      float s[3] = {0.f, 0.f, 0.f};   // (x - mean)^2, gw (x - mean), gw
-#pragma unroll
-      for (int e = 0; e < NE; ++e) {
-        const float gw = g[e] * w[e];
-        s[0] += f[e] * f[e];
-        s[1] += gw * f[e];
-        s[2] += gw;
-      }
-      row_sum<C::UPR>(s);
-      const float rstd = 1.0f / sqrtf(s[0] * (1.0f / D) + eps);
-      const float m1 = s[1] * rstd * (1.0f / D), m2 = rms ? 0.f : s[2] * (1.0f / D);
-      float r[NE];
-#pragma unroll
-      for (int e = 0; e < NE; ++e) {
-        const float xh = f[e] * rstd;
-        r[e] = rstd * (g[e] * w[e] - m2 - xh * m1);
-        if (live) {
-          dw[e] += g[e] * xh;
-          db[e] += g[e];
+        for (int i = 0; i < P2; ++i) {
+          fx[i] = add2(fx[i], mean);
+          fy[i] = add2(fy[i], mean);
         }
+      }
+      f32x2 ux[P2], uy[P2];                       // gw
+#pragma unroll
+      for (int i = 0; i < P2; ++i) {
+        ux[i] = mul2(gx[i], wx[i]);
+        uy[i] = mul2(gy[i], wy[i]);
+      }
+      float s[RMS ? 2 : 3] = {dot_of<P2>(fx, fy, fx, fy), dot_of<P2>(ux, uy, fx, fy)};
+      if (!RMS) s[RMS ? 0 : 2] = sum_of<P2>(ux, uy);
+      row_sum<C::UPR>(s);
+      const float rstd = inv_sqrt(s[0] * (1.0f / D) + eps);
+      // dx = rstd gw - (x - mean) rstd^2 mean(gw xh) - rstd mean(gw); xh = (x - mean) rstd
+      const float m1 = -s[1] * rstd * (1.0f / D), m2 = RMS ? 0.f : -s[RMS ? 0 : 2] * (1.0f / D);
+      const f32x2 r2 = pair(rstd, rstd), n1 = pair(m1, m1), n2 = pair(m2, m2);
+#pragma unroll
+      for (int i = 0; i < P2; ++i) {
+        fx[i] = mul2(fx[i], r2);
+        fy[i] = mul2(fy[i], r2);
+        if (live) {
+          dwx[i] = fma2(gx[i], fx[i], dwx[i]);
+          dwy[i] = fma2(gy[i], fy[i], dwy[i]);
+          dbx[i] = add2(dbx[i], gx[i]);
+          dby[i] = add2(dby[i], gy[i]);
+        }
+        if (!RMS) {
+          ux[i] = add2(ux[i], n2);
+          uy[i] = add2(uy[i], n2);
+        }
+        ux[i] = mul2(fma2(fx[i], n1, ux[i]), r2);
+        uy[i] = mul2(fma2(fy[i], n1, uy[i]), r2);
       }
       if (live) {
         T* dst = dx + flat[u] * t.dx_stride + (int64_t)h * D + c0 * E;
+        X::pack(ux, uy, v16);
 #pragma unroll
-        for (int v = 0; v < C::NV; ++v) __stcs(reinterpret_cast<uint4*>(dst + v * (D / 2)), X::pack(r + v * E));
+        for (int v = 0; v < C::NV; ++v) __stcs(reinterpret_cast<uint4*>(dst + v * (D / 2)), v16[v]);
       }
     }
   }
   copy_wait<0>();
   if (t.dw == nullptr && t.db == nullptr) return;
   // over the lanes of a warp that share columns, then over the warps in order
-#pragma unroll
-  for (int off = 16; off >= C::UPR; off >>= 1)
-#pragma unroll
-    for (int e = 0; e < NE; ++e) {
-      dw[e] += __shfl_xor_sync(0xffffffffu, dw[e], off);
-      db[e] += __shfl_xor_sync(0xffffffffu, db[e], off);
-    }
   float* sum = reinterpret_cast<float*>(ring);   // [warps][dw, db][D]
   __syncthreads();                               // every thread's slots are done with
-  if ((threadIdx.x & 31) < C::UPR)
 #pragma unroll
-    for (int e = 0; e < NE; ++e) {
-      const int c = c0 * E + (e / E) * (D / 2) + e % E;
-      sum[(threadIdx.x >> 5) * 2 * D + c] = dw[e];
-      sum[(threadIdx.x >> 5) * 2 * D + D + c] = db[e];
+  for (int i = 0; i < C::NP; ++i)
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const float2 px = both(k ? dbx[i / 2] : dwx[i / 2]), py = both(k ? dby[i / 2] : dwy[i / 2]);
+      float vx = i & 1 ? px.y : px.x, vy = i & 1 ? py.y : py.x;
+#pragma unroll
+      for (int off = 16; off >= C::UPR; off >>= 1) {
+        vx += __shfl_xor_sync(0xffffffffu, vx, off);
+        vy += __shfl_xor_sync(0xffffffffu, vy, off);
+      }
+      if ((threadIdx.x & 31) < C::UPR) {
+        float* to = sum + ((threadIdx.x >> 5) * 2 + k) * D;
+        to[col_x<D, E, HALF>(c0, i)] = vx;
+        to[col_y<D, E, HALF>(c0, i)] = vy;
+      }
     }
   __syncthreads();
   float* mine = part + ((is_q ? 0 : (int64_t)gridDim.x * q.groups) + (int64_t)blockIdx.x * t.groups + group) * 2 * D;
@@ -434,7 +509,8 @@ bool go_fwd(const Dims& s, const RopeArgs& a, Fwd q, Fwd k, const Tokens& tk, bo
   q.groups = (q.heads + hpc - 1) / hpc;
   k.groups = (k.heads + hpc - 1) / hpc;
   const size_t smem = (size_t)(hpc < kDepth ? hpc : kDepth) * C::VECS * 16;
-  auto kern = norm_rope_fwd_kernel<T, D, GR, HALF, POOL>;
+  const bool bias = !rms || q.b != nullptr || k.b != nullptr;
+  auto kern = bias ? norm_rope_fwd_kernel<T, D, GR, HALF, POOL, true> : norm_rope_fwd_kernel<T, D, GR, HALF, POOL, false>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) return false;
   kern<<<dim3((unsigned)granules, (unsigned)(q.groups + k.groups)), C::THREADS, smem, st>>>(q, k, tk, a, rms, eps, out_blocked,
                                                                                            hpc, d_status);
@@ -463,10 +539,10 @@ bool go_bwd(const Dims& s, const RopeArgs& a, Bwd q, Bwd k, const Tokens& tk, bo
   size_t smem = (size_t)(hpc < kDepth ? hpc : kDepth) * 2 * C::VECS * 16;
   const size_t sums = (size_t)C::THREADS / 32 * 2 * D * 4;
   if (smem < sums) smem = sums;
-  auto kern = norm_rope_bwd_kernel<T, D, GR, HALF>;
+  auto kern = rms ? norm_rope_bwd_kernel<T, D, GR, HALF, true> : norm_rope_bwd_kernel<T, D, GR, HALF, false>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) return false;
-  kern<<<dim3((unsigned)granules, (unsigned)(q.groups + k.groups)), C::THREADS, smem, st>>>(q, k, tk, a, rms, eps, in_blocked,
-                                                                                           hpc, part, d_status);
+  kern<<<dim3((unsigned)granules, (unsigned)(q.groups + k.groups)), C::THREADS, smem, st>>>(q, k, tk, a, eps, in_blocked, hpc,
+                                                                                           part, d_status);
   if (q.dw != nullptr || q.db != nullptr || k.dw != nullptr || k.db != nullptr)
     norm_rope_sum_kernel<D><<<dim3(2 * D / 32, k.heads > 0 ? 2 : 1), 1024, 0, st>>>(part, granules * q.groups,
                                                                                    granules * k.groups, q, k);

@@ -749,13 +749,13 @@ SPARSP_API sparsp_status_t sparsp_cache_extend(const sparsp_cache_t* cache, int3
  * slots[i]; a negative slot is left out, one past the pool sets SPARSP_ERR_DATA.
  * Tokens in a row whose slots are next to each other in one block are a run. Its block's scale,
  * per head, becomes the smallest power of two, at least 2^-100, under which the run's
- * magnitudes are at most 448; where the run starts inside the block, the larger of that
- * and the block's old scale, and the tokens before it are rounded again to the larger scale.
+ * magnitudes are at most 448; where the run starts inside the block, also not below the
+ * block's old scale, and the tokens before it are rounded again if the scale has grown.
  * Codes are rounded to nearest, ties to even. A NaN or infinity is held as NaN, does not
  * count for the scale, and sets SPARSP_ERR_DATA. A block may have only one run in a call
  * (as slots of sparsp_cache_extend have); with two its contents are not defined. Where a
- * run starts inside a block whose scale is not positive and finite, SPARSP_ERR_DATA is
- * set and the tokens before it are left as they are.
+ * run starts inside a block whose scale is not positive and at most 2^120, SPARSP_ERR_DATA
+ * is set, the old scale does not count and the tokens before the run are left as they are.
  */
 SPARSP_API sparsp_status_t sparsp_cache_write(const sparsp_cache_t* cache, int32_t dtype, const void* k,
                                               int64_t k_stride, int64_t k_head, const void* v, int64_t v_stride,
