@@ -80,7 +80,13 @@ sparsp_status_t sparsp_cache_extend(const sparsp_cache_t* cache, int32_t B, int3
   if (tokens > 0) CHECK_PTR(slots);
   CHECK_OPT_PTR(used_out);
   CHECK_OPT_PTR(d_status);
-  if (len_out == add || start == len || start == add || start == len_out) return SPARSP_ERR_INVALID_ARG;
+  const size_t n = (size_t)B * sizeof(int32_t);
+  auto meets = [](const void* p, size_t np, const void* q, size_t nq) {
+    return (const uint8_t*)p < (const uint8_t*)q + nq && (const uint8_t*)q < (const uint8_t*)p + np;
+  };
+  if ((len_out != len && meets(len_out, n, len, n)) || meets(len_out, n, add, n) || meets(start, n + 4, len, n) ||
+      meets(start, n + 4, add, n) || meets(start, n + 4, len_out, n))
+    return SPARSP_ERR_INVALID_ARG;
   CacheExtend a{B, max_blocks, n_free, (int)tokens, len, add, free_blocks, used, table, len_out, start, slots, used_out};
   return launch_cache_extend(c, a, d_status, (cudaStream_t)stream);
 }

@@ -26,7 +26,8 @@ constexpr int kThreads = kWarps * 32;
 constexpr int kGrid = 152 * 3;     // CTAs that share the work, at most (the workspace depends on it)
 // CTAs per SM: two rows' accumulators of 128 columns do not fit the registers of three.
 constexpr int ctas_per_sm(int d, int nt) { return d == 128 && nt == 2 ? 2 : 3; }
-constexpr int kMinUnits = 2;       // units that are worth a CTA
+constexpr int kItemCost = 4;       // units that an item's own work (its look-ups, queries, join) counts as
+constexpr int kMinUnits = 6;       // units, an item's own among them, that are worth a CTA
 constexpr float kPScale = 2048.f;  // P is at most 16 and is held as 2^11 P in f16: 2^-35 is not lost
 
 // Where the units of a range lie. Entries are requests (every block is seen, all key heads
@@ -69,20 +70,20 @@ struct Walk {
       x.units = (x.len + kUnit - 1) / kUnit;
     }
     // an item without keys still has its rows to write: one unit, empty
-    x.weight = (int64_t)x.groups * max(1, x.units) * (a.row_ptr != nullptr ? 1 : a.c.heads);
+    x.weight = (int64_t)x.groups * (kItemCost + max(1, x.units)) * (a.row_ptr != nullptr ? 1 : a.c.heads);
     return x;
   }
 };
 
 // What the joining kernel needs to know of a CTA's last item where it goes on in others.
 struct Open {
-  int b, hk, row0, rows, s0, last, slot, pad;   // last: the CTA of its last unit; slot: of this CTA's part
+  int b, hk, row0, rows, s0, last;   // last: the CTA of its last unit
 };
 
 struct Parts {
   Open* open;      // [kGrid]
   float* sum;      // [2 kGrid][RT][D]
-  float2* ml;      // [2 kGrid][RT] maximum (base 2) and sum
+  float2* ml;      // [2 kGrid][RT] maximum (base 2) and sum; a CTA's parts: an item that goes on, one that starts
 };
 
 __device__ __forceinline__ uint32_t f16x2_of_e4m3(uint32_t two) {   // the low two bytes
@@ -214,9 +215,15 @@ attn_cache_kernel(const CacheAttn a, const Parts parts) {
       x = walk.at(++entry, false);
     }
     // ---- an item, and this CTA's piece [u0, u1) of it
-    const int units = max(1, x.units);
-    const int item = (int)(offset / units), u0 = (int)(offset - (int64_t)item * units);
-    const int u1 = (int)min((int64_t)units, u0 + (end - unit_at));
+    // (its first kItemCost units stand for its own work and go with the first of its keys)
+    const int units = max(1, x.units), size = kItemCost + units;
+    const int item = (int)(offset / size), at0 = (int)(offset - (int64_t)item * size);
+    const int at1 = (int)min((int64_t)size, at0 + (end - unit_at));
+    const int64_t item_at = unit_at - at0;
+    const int u0 = max(0, at0 - kItemCost), u1 = at1 - kItemCost;
+    unit_at += at1 - at0;
+    offset += at1 - at0;
+    if (u1 <= u0) continue;
     const int hk = a.row_ptr != nullptr ? x.hk : item / x.groups, group = a.row_ptr != nullptr ? item : item % x.groups;
     const int row0 = group * RT, rows = min(RT, x.n * a.group - row0);
     const int32_t* table = a.table + (int64_t)x.b * a.max_blocks;
@@ -477,7 +484,7 @@ attn_cache_kernel(const CacheAttn a, const Parts parts) {
               make_float2(o[j][i][k], o[j][i][k + 2]);
     __syncthreads();
     const bool whole = u0 == 0 && u1 == units;
-    const int slot = 2 * (int)cta + (unit_at == begin ? 0 : 1);
+    const int slot = 2 * (int)cta + (u0 > 0 ? 0 : 1);     // a piece that goes on is the CTA's first
     for (int i = threadIdx.x; i < rows * (D / 4); i += kThreads) {
       const int r = i / (D / 4), c = i % (D / 4) * 4;
       float top = s_m[0][r], sum = 0.f;
@@ -504,12 +511,9 @@ attn_cache_kernel(const CacheAttn a, const Parts parts) {
       }
     }
     if (!whole && u0 == 0 && threadIdx.x == 0) {
-      const int64_t end_unit = unit_at + units - 1;      // the item's last unit
-      parts.open[cta] = Open{x.b, hk, row0, rows, x.s0, (int)(((end_unit + 1) * ctas - 1) / total), slot, 0};
+      parts.open[cta] = Open{x.b, hk, row0, rows, x.s0, (int)(((item_at + size) * ctas - 1) / total)};
     }
     __syncthreads();
-    unit_at += u1 - u0;
-    offset += u1 - u0;
   }
 }
 
@@ -527,7 +531,7 @@ attn_cache_join_kernel(const CacheAttn a, const Parts parts) {
   if (it.last < 0 || r >= it.rows) return;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int count = it.last - (int)blockIdx.x + 1;
-  auto slot_of = [&](int i) { return (int64_t)(i == 0 ? it.slot : 2 * ((int)blockIdx.x + i)); };
+  auto slot_of = [&](int i) { return (int64_t)(2 * ((int)blockIdx.x + i) + (i == 0 ? 1 : 0)); };
   float top = -INFINITY;
   for (int i = threadIdx.x; i < count; i += 256) top = fmaxf(top, parts.ml[slot_of(i) * RT + r].x);
 #pragma unroll

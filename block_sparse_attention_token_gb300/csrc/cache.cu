@@ -4,9 +4,12 @@
 // Tables. Request b holds len tokens in ceil(len / bt) blocks and gets add more:
 //   need_b = ceil((len + add) / bt) - ceil(len / bt) blocks, handed out from a list in
 // the order of the requests, so that one scan over the requests gives every request its
-// place in the list and its place among the packed new tokens. One cluster of CTAs does
-// it in one launch: each scans all requests for itself (thousands at most, in registers), and
-// barriers of the cluster stand between what is read and what may be written over it.
+// place in the list and its place among the packed new tokens. Every CTA scans all requests
+// for itself (thousands at most, a few to a thread) and then enters its share of the blocks and
+// of the slots, so that no CTA waits for another: the page of a new token comes from the
+// list if its block is new, else from a table entry that no one writes. What a call may overwrite
+// of its own input (the lengths, the place in the list) is written by the one CTA of a small
+// call after its reads, else by a second launch.
 //
 // Write. A value is held as x = s c, c of e4m3 and s the scale of its block and head:
 //   s = 2^e, the smallest e >= -100 with max |x| <= 448 2^e.
@@ -15,7 +18,6 @@
 // grows be brought to a larger scale with no error but the codes' own subnormals. A run
 // of new tokens in one block is one pass: its values wait in registers for their
 // maximum. Bound by HBM.
-#include <cooperative_groups.h>
 #include <cuda_fp16.h>
 
 #include <type_traits>
@@ -23,13 +25,11 @@
 #include "cache.cuh"
 #include "rows.cuh"
 
-namespace cg = cooperative_groups;
-
 namespace sparsp {
 namespace {
 
 constexpr int kExtendThreads = 1024;
-constexpr int kExtendCluster = 8;
+enum { kExtendLists = 1, kExtendState = 2 };   // what a launch writes: table, start and slots; lengths and place
 
 // The sums over the CTA's threads below this one, and of all, of two numbers.
 __device__ __forceinline__ void scan2(int64_t (&v)[2], int64_t (&total)[2], int64_t (*sm)[2]) {
@@ -59,9 +59,8 @@ __device__ __forceinline__ void scan2(int64_t (&v)[2], int64_t (&total)[2], int6
 }
 
 __global__ void __launch_bounds__(kExtendThreads)
-cache_extend_kernel(const CacheDims c, const CacheExtend a, int32_t* d_status) {
-  cg::cluster_group cluster = cg::this_cluster();
-  const int rank = cluster.block_rank(), ranks = cluster.num_blocks();
+cache_extend_kernel(const CacheDims c, const CacheExtend a, int what, int32_t* d_status) {
+  const int rank = blockIdx.x, ranks = gridDim.x;
   extern __shared__ int32_t sm_req[];
   int32_t* s_start = sm_req;                     // [B] first packed token
   int32_t* s_len = sm_req + a.B;                 // [B] tokens held before, -1: gets no slots
@@ -114,33 +113,33 @@ cache_extend_kernel(const CacheDims c, const CacheExtend a, int32_t* d_status) {
     v[1] += need;
   }
   if (given > 0) atomicAdd(&s_given, given);
-  cluster.sync();                                // every CTA has read len and used
-  if (rank == 0) {
+  __syncthreads();                               // all of len and used has been read
+  if (rank == 0 && (what & kExtendState)) {
     for (int b = b0; b < b1; ++b) {
       const int len = s_len[b];
-      a.start[b] = s_start[b];
       a.len_out[b] = len >= 0 ? len + a.add[b] : a.len[b];
     }
-    if (threadIdx.x == 0) {
-      a.start[a.B] = (int)min(total[0], (int64_t)INT32_MAX);
-      if (a.used_out != nullptr) *a.used_out = used + s_given;
-    }
+    if (threadIdx.x == 0 && a.used_out != nullptr) *a.used_out = used + s_given;
   }
+  if (!(what & kExtendLists)) return;
+  if (rank == 0) {
+    for (int b = b0; b < b1; ++b) a.start[b] = s_start[b];
+    if (threadIdx.x == 0) a.start[a.B] = (int)min(total[0], (int64_t)INT32_MAX);
+  }
+  // a block from the list (-1: none)
+  auto handed = [&](int at) {
+    const int id = a.free_blocks[at];
+    if (id >= 0 && id < c.blocks) return id;
+    report(d_status, SPARSP_ERR_DATA);
+    return -1;
+  };
   // the blocks handed out: a warp takes a request
   for (int b = rank * (kExtendThreads / 32) + warp; b < a.B; b += ranks * (kExtendThreads / 32)) {
     const int len = s_len[b];
     if (len < 0) continue;
     const int have = blocks_of(len), need = blocks_of((int64_t)len + a.add[b]) - have;
-    for (int i = lane; i < need; i += 32) {
-      int id = a.free_blocks[s_place[b] + i];
-      if (id < 0 || id >= c.blocks) {
-        report(d_status, SPARSP_ERR_DATA);
-        id = -1;
-      }
-      a.table[(int64_t)b * a.max_blocks + have + i] = id;
-    }
+    for (int i = lane; i < need; i += 32) a.table[(int64_t)b * a.max_blocks + have + i] = handed(s_place[b] + i);
   }
-  cluster.sync();                                // the table is whole
   // slots: four packed tokens to a thread, the first one's request by bisection
   for (int64_t t0 = (int64_t)(rank * kExtendThreads + threadIdx.x) * 4; t0 < a.tokens;
        t0 += (int64_t)ranks * kExtendThreads * 4) {
@@ -150,7 +149,7 @@ cache_extend_kernel(const CacheDims c, const CacheExtend a, int32_t* d_status) {
       if (s_start[mid] <= t0) lo = mid;
       else hi = mid;
     }
-    int slot[4];
+    int slot[4], page = -1, page_b = -1, page_j = -1;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int64_t t = t0 + i;
@@ -159,10 +158,17 @@ cache_extend_kernel(const CacheDims c, const CacheExtend a, int32_t* d_status) {
       while (lo + 1 < a.B && s_start[lo + 1] <= t) ++lo;
       const int len = s_len[lo];
       if (len < 0) continue;
-      const int p = len + (int)(t - s_start[lo]);
-      const int id = __ldcg(a.table + (int64_t)lo * a.max_blocks + p / bt);
-      if (id < 0 || id >= c.blocks) report(d_status, SPARSP_ERR_DATA);
-      else slot[i] = id * bt + p % bt;
+      const int p = len + (int)(t - s_start[lo]), j = p / bt, have = blocks_of(len);
+      if (j != page_j || lo != page_b) {
+        page = j >= have ? handed(s_place[lo] + j - have) : a.table[(int64_t)lo * a.max_blocks + j];
+        page_j = j;
+        page_b = lo;
+        if (page < 0 || page >= c.blocks) {
+          report(d_status, SPARSP_ERR_DATA);
+          page = -1;
+        }
+      }
+      if (page >= 0) slot[i] = page * bt + p % bt;
     }
     if (t0 + 4 <= a.tokens) {
       *reinterpret_cast<int4*>(a.slots + t0) = make_int4(slot[0], slot[1], slot[2], slot[3]);
@@ -260,7 +266,7 @@ constexpr int kShortRun = 4;      // tokens of a run that one warp takes by itse
 // are next to each other in one block; it belongs to the granule it starts in. A short run is a
 // warp's, a longer one the CTA's. Every warp finds the runs for itself.
 template <typename T, int D, int BT>
-__global__ void __launch_bounds__(kWriteThreads)
+__global__ void __launch_bounds__(kWriteThreads, sizeof(T) * D * BT <= 32768 ? 4 : 2)
 cache_write_kernel(const CacheDims c, const CacheWrite a, int granule, int32_t* d_status) {
   constexpr int E = Fresh<T>::E, LPR = D / E;        // lanes per row
   __shared__ uint32_t s_most[2][kWriteThreads / 32];
@@ -381,18 +387,16 @@ sparsp_status_t launch_cache_extend(const CacheDims& c, const CacheExtend& a, in
   const size_t smem = (size_t)a.B * 3 * sizeof(int32_t);
   if (cudaFuncSetAttribute(cache_extend_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
     return SPARSP_ERR_CUDA;
-  const int ctas = a.tokens <= 4 * kExtendThreads && a.B <= kExtendThreads ? 1 : kExtendCluster;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(ctas);
-  cfg.blockDim = dim3(kExtendThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim = {(unsigned)ctas, 1, 1};
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, cache_extend_kernel, c, a, d_status) != cudaSuccess) return SPARSP_ERR_CUDA;
+  // one CTA where a thread has at most four requests and eight tokens, else enough for four tokens a thread
+  const int64_t share = (int64_t)4 * kExtendThreads;
+  const int ctas = a.tokens <= 2 * share && a.B <= share ? 1 : (int)min((int64_t)152, max((int64_t)8, a.tokens / share));
+  const bool over = a.len_out == a.len || (a.used != nullptr && a.used_out == a.used);
+  if (ctas > 1 && over) {
+    cache_extend_kernel<<<ctas, kExtendThreads, smem, st>>>(c, a, kExtendLists, d_status);
+    cache_extend_kernel<<<1, kExtendThreads, smem, st>>>(c, a, kExtendState, nullptr);
+  } else {
+    cache_extend_kernel<<<ctas, kExtendThreads, smem, st>>>(c, a, kExtendLists | kExtendState, d_status);
+  }
   SPARSP_LAUNCH_CHECK();
   return SPARSP_OK;
 }

@@ -778,7 +778,8 @@ SPARSP_API sparsp_status_t sparsp_cache_write(const sparsp_cache_t* cache, int32
  * request are left as they were. Values of keys that a row does not see must not be NaN
  * (tokens past len may hold anything). Products are exact or in fp32; the softmax's weights
  * are rounded to 11 bits.
- * Sums are taken in an order that depends on the lengths alone: the same call gives the same bits.
+ * Sums are taken in an order that depends on the lengths (and lists) of the whole call: the
+ * same call gives the same bits, but a row's last bits may depend on the other requests.
  * SPARSP_ERR_DATA on the device: rows outside [0, tokens] or more than max_add of them (the
  * request's are left out), a length outside [0, max_blocks * bt] (counts as 0), a CSR row that is
  * malformed (counts as empty), an entry of it without tokens or a block outside the pool

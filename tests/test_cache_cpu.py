@@ -48,7 +48,7 @@ def extend(lib, cache=cache(), B=3, max_blocks=4, ln=at(0), add=at(1), free=at(2
     (dict(free=None), sp.INVALID_ARG), (dict(free=FAKE + 2), sp.ALIGN), (dict(table=None), sp.INVALID_ARG), (dict(len_out=None), sp.INVALID_ARG),
     (dict(start=None), sp.INVALID_ARG), (dict(slots=None), sp.INVALID_ARG), (dict(slots=FAKE + 4), sp.ALIGN),
     (dict(used=FAKE + 4), sp.ALIGN), (dict(used_out=FAKE + 8), sp.ALIGN), (dict(table=FAKE + 4), sp.ALIGN),
-    (dict(len_out=at(1)), sp.INVALID_ARG), (dict(start=at(0)), sp.INVALID_ARG), (dict(start=at(4)), sp.INVALID_ARG),
+    (dict(len_out=at(1)), sp.INVALID_ARG), (dict(B=100, len_out=at(0) + 64), sp.INVALID_ARG), (dict(start=at(0)), sp.INVALID_ARG), (dict(start=at(4)), sp.INVALID_ARG),
 ])
 def test_extend_refuses(lib, kw, code):
     assert extend(lib, **kw) == code

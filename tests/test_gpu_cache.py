@@ -473,6 +473,10 @@ def test_attn_bad_data():
     pool, table, start, ln, q = check_attn(lengths, add, 2, 2, 64, 64, True)
     want = sp.attn_cache_fwd(pool, q, start, ln, table, 2)
 
+    # the work is dealt out by the lengths of the whole call, so that the others' rows may be summed in
+    # another order: two results, each within 2^-8 |o| + (2^-11 + delta) max |v| of the same value
+    near = lambda x, y: torch.allclose(x.float(), y.float(), atol=2.0 ** -6, rtol=2.0 ** -7)
+
     def call(start=start, ln=ln, table=table, max_add=2, **kw):
         o, lse = torch.full_like(want[0], 5.0), torch.full_like(want[1], 5.0)
         status = word()
@@ -489,17 +493,16 @@ def test_attn_bad_data():
         row_ptr, col = csr(seen)
         o2, lse2, st2 = call(row_ptr=row_ptr, col_idx=col)
         assert st2 == 0
-        assert torch.allclose(o[1:3].float(), o2[1:3].float(), atol=2.0 ** -6, rtol=2.0 ** -7)
-        assert torch.equal(o[0], want[0][0]) and torch.equal(o[3], want[0][3])
+        assert near(o[1:3], o2[1:3]) and near(o[0], want[0][0]) and near(o[3], want[0][3])
     for bad_len in (-1, 2 ** 31 - 1, table.shape[1] * 64 + 1):        # a bad length counts as 0
         o, lse, st = call(ln=i32([100, bad_len, 300]))
         assert st == sp.DATA and (o[1:3] == 0).all() and torch.isinf(lse[1:3]).all()
-        assert torch.equal(o[3], want[0][3])
+        assert near(o[3], want[0][3])
     for s in ([0, 1, 3, 2 ** 31 - 1], [0, 1, 4, 3], [-1, 1, 3, 4], [0, 1, 3, 1000]):   # rows that are none: left out
         o, lse, st = call(start=i32(s))
         assert st == sp.DATA and torch.equal(o[4:], torch.full_like(o[4:], 5.0))
     o, lse, st = call(max_add=1)                                      # more rows than announced
-    assert st == sp.DATA and (o[1:3] == 5).all() and torch.equal(o[3], want[0][3])
+    assert st == sp.DATA and (o[1:3] == 5).all() and near(o[3], want[0][3])
     seen = [torch.ones(2, -(-n // 64), dtype=torch.bool, device="cuda") for n in lengths]
     row_ptr, col = csr(seen)
     for at, v in ((3, 4), (4, -1), (5, 2 ** 31 - 1)):                 # blocks without tokens: left out
@@ -507,12 +510,12 @@ def test_attn_bad_data():
         c[at] = v
         o, lse, st = call(row_ptr=row_ptr, col_idx=c)
         assert st == sp.DATA and torch.isfinite(o.float()).all()
-        assert torch.equal(o[3], want[0][3])
+        assert near(o[3], want[0][3])
     for at, v in ((2, 0), (2, 2 ** 31 - 1), (6, 1000), (3, -4)):      # rows of lists that make no sense: empty
         r = row_ptr.clone()
         r[at] = v
         o, lse, st = call(row_ptr=r, col_idx=col)
-        assert st == sp.DATA and torch.isfinite(o.float()).all() and torch.equal(o[0, :2], want[0][0, :2])
+        assert st == sp.DATA and torch.isfinite(o.float()).all() and near(o[0, :2], want[0][0, :2])
 
 
 def test_attn_stream_capture_and_two_graphs():
