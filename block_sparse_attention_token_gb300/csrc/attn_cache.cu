@@ -13,9 +13,7 @@
 // what it loads itself; it does so some stages ahead, into shared-memory slots of its own. Work is counted in units of 64 keys over all requests and key heads and dealt out
 // evenly: a CTA takes a range of units, and an item (request, key head, 8 or 16 rows) that
 // spans several CTAs leaves partial sums that a second kernel joins in order.
-#include <cuda_fp16.h>
-
-#include "cache.cuh"
+#include "cache_items.cuh"
 #include "rows.cuh"
 
 namespace sparsp {
@@ -30,67 +28,19 @@ constexpr int kItemCost = 4;       // units that an item's own work (its look-up
 constexpr int kMinUnits = 6;       // units, an item's own among them, that are worth a CTA
 constexpr float kPScale = 2048.f;  // P is at most 16 and is held as 2^11 P in f16: 2^-35 is not lost
 
-// Where the units of a range lie. Entries are requests (every block is seen, all key heads
-// alike) or request and key head (lists).
-struct Entry {
-  int b, hk, n, len, s0, groups, units;   // hk: of lists; n: new tokens; units of one item
-  int64_t weight;
-};
-
 template <int RT>   // query rows of an item
 struct Walk {
   const CacheAttn& a;
-  __device__ __forceinline__ int entries() const { return a.row_ptr != nullptr ? a.B * a.c.heads : a.B; }
   __device__ __forceinline__ Entry at(int e, bool tell) const {
-    Entry x;
-    x.hk = a.row_ptr != nullptr ? e % a.c.heads : 0;
-    x.b = a.row_ptr != nullptr ? e / a.c.heads : e;
-    x.s0 = a.start[x.b];
-    const int s1 = a.start[x.b + 1];
-    x.n = s1 - x.s0;
-    x.len = a.len[x.b];
-    if (x.s0 < 0 || s1 < x.s0 || s1 > a.tokens || x.n > a.max_add) {
-      if (tell) report(a.d_status, SPARSP_ERR_DATA);
-      x.n = 0;
-    }
-    if (x.len < 0 || x.len > (int64_t)a.max_blocks * a.c.bt) {
-      if (tell) report(a.d_status, SPARSP_ERR_DATA);
-      x.len = 0;
-    }
+    Entry x = entry_at(a, e, tell);
+    if (a.few > 0 && (int64_t)x.n * a.group > a.few) x.n = 0;   // the other kernel's
     x.groups = (int)(((int64_t)x.n * a.group + RT - 1) / RT);
-    if (a.row_ptr != nullptr) {
-      const int64_t p0 = a.row_ptr[e], p1 = a.row_ptr[e + 1];
-      int64_t count = p1 - p0;
-      if (p0 < 0 || count < 0 || count > a.max_blocks || p1 > a.col_cap) {
-        if (tell) report(a.d_status, SPARSP_ERR_DATA);
-        count = 0;
-      }
-      x.units = (int)count * (a.c.bt / kUnit);
-    } else {
-      x.units = (x.len + kUnit - 1) / kUnit;
-    }
     // an item without keys still has its rows to write: one unit, empty
     x.weight = (int64_t)x.groups * (kItemCost + max(1, x.units)) * (a.row_ptr != nullptr ? 1 : a.c.heads);
     return x;
   }
 };
 
-// What the joining kernel needs to know of a CTA's last item where it goes on in others.
-struct Open {
-  int b, hk, row0, rows, s0, last;   // last: the CTA of its last unit
-};
-
-struct Parts {
-  Open* open;      // [kGrid]
-  float* sum;      // [2 kGrid][RT][D]
-  float2* ml;      // [2 kGrid][RT] maximum (base 2) and sum; a CTA's parts: an item that goes on, one that starts
-};
-
-__device__ __forceinline__ uint32_t f16x2_of_e4m3(uint32_t two) {   // the low two bytes
-  uint32_t r;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;\n" : "=r"(r) : "h"((uint16_t)two));
-  return r;
-}
 __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                     uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
@@ -102,28 +52,6 @@ __device__ __forceinline__ uint32_t transposed(uint32_t v) {
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;\n" : "=r"(r) : "r"(v));
   return r;
 }
-__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
-  const __half2 h = __floats2half2_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
-__device__ __forceinline__ float exp2_fast(float x) {
-  float r;
-  asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(r) : "f"(x));
-  return r;
-}
-
-// Writes four columns of a finished row, and its LSE.
-template <int D>
-__device__ __forceinline__ void finish(const CacheAttn& a, int s0, int hk, int row, int c, float top, float sum,
-                                       const float4& all) {
-  const int64_t at = (int64_t)(s0 + row / a.group) * a.H + hk * a.group + row % a.group;
-  const float f = sum == 0.f ? 0.f : 1.0f / sum;
-  const __nv_bfloat162 lo = __floats2bfloat162_rn(all.x * f, all.y * f), hi = __floats2bfloat162_rn(all.z * f, all.w * f);
-  *reinterpret_cast<uint2*>(a.o + at * D + c) =
-      make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
-  if (c == 0) a.lse[at] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
-}
-
 // A warp's ring of 16-key stages: every lane reads back only what it copied itself, so no
 // barrier stands between a copy and its use.
 constexpr int kStages = 4;
@@ -170,25 +98,12 @@ attn_cache_kernel(const CacheAttn a, const Parts parts) {
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
 
   // ---- this CTA's range of units
-  const int entries = walk.entries(), per = (entries + kThreads - 1) / kThreads;
+  const int entries = entries_of(a), per = (entries + kThreads - 1) / kThreads;
   const int e0 = min(entries, (int)threadIdx.x * per), e1 = min(entries, e0 + per);
   int64_t mine = 0;
   for (int e = e0; e < e1; ++e) mine += walk.at(e, blockIdx.x == 0).weight;
-  int64_t below = mine;
-#pragma unroll
-  for (int off = 1; off < 32; off <<= 1) {
-    const int64_t v = __shfl_up_sync(0xffffffffu, below, off);
-    if (lane >= off) below += v;
-  }
-  if (lane == 31) s_scan[warp] = below;
-  below -= mine;
-  __syncthreads();
-  int64_t total = 0;
-#pragma unroll
-  for (int i = 0; i < kWarps; ++i) {
-    if (i < warp) below += s_scan[i];
-    total += s_scan[i];
-  }
+  int64_t total;
+  const int64_t below = scan_below<kWarps>(mine, s_scan, &total);
   const int64_t ctas = min((int64_t)gridDim.x, max((int64_t)1, (total + kMinUnits - 1) / kMinUnits)), cta = blockIdx.x;
   const int64_t begin = cta * total / ctas, end = cta < ctas ? (cta + 1) * total / ctas : begin;
   if (threadIdx.x == 0) parts.open[cta].last = -1;
@@ -573,50 +488,47 @@ attn_cache_join_kernel(const CacheAttn a, const Parts parts) {
   finish<D>(a, it.s0, it.hk, it.row0 + r, 4 * threadIdx.x, top, sum, all);
 }
 
+// Query rows of an item here: 8 where no request has more.
 int rows_of(int group, int max_add) { return (int64_t)group * max_add <= 8 ? 8 : 16; }
-
-size_t align(size_t n) { return (n + 255) & ~(size_t)255; }
 
 template <int D, int NT>
 sparsp_status_t go(const CacheAttn& a, void* ws, cudaStream_t st) {
-  constexpr int RT = 8 * NT;
-  Parts p;
-  uint8_t* at = (uint8_t*)ws;
-  p.open = (Open*)at;
-  at += align(kGrid * sizeof(Open));
-  p.ml = (float2*)at;
-  at += align((size_t)2 * kGrid * RT * sizeof(float2));
-  p.sum = (float*)at;
+  const Parts p = parts_of(ws, kGrid, 8 * NT);
   constexpr int smem = attn_smem<D, NT>();
+  const int ctas = 152 * ctas_per_sm(D, NT);
   if (cudaFuncSetAttribute(attn_cache_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
     return SPARSP_ERR_CUDA;
-  attn_cache_kernel<D, NT><<<152 * ctas_per_sm(D, NT), kThreads, smem, st>>>(a, p);
+  attn_cache_kernel<D, NT><<<ctas, kThreads, smem, st>>>(a, p);
   SPARSP_LAUNCH_CHECK();
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(152 * ctas_per_sm(D, NT), RT);
-  cfg.blockDim = dim3(256);
-  cfg.stream = st;
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, attn_cache_join_kernel<D, NT>, a, p) != cudaSuccess) return SPARSP_ERR_CUDA;
-  SPARSP_LAUNCH_CHECK();
-  return SPARSP_OK;
+  return launch_after(attn_cache_join_kernel<D, NT>, dim3(ctas, 8 * NT), 256, st, a, p);
 }
+
+// Requests with up to kFew rows (tokens times heads that share a key head) are this file's
+// kernel's, the others those of attn_cache_tc.cu. Where the packed rows leave room for no request
+// shorter than the longest, that one takes all, and a launch is saved.
+constexpr int kFew = 16;
+bool many(int group, int max_add) { return (int64_t)group * max_add > kFew; }
 
 }  // namespace
 
 size_t attn_cache_ws(const CacheDims& c, int group, int max_add) {
-  const size_t rt = rows_of(group, max_add);
-  return align(kGrid * sizeof(Open)) + align(2 * kGrid * rt * sizeof(float2)) + 2 * kGrid * rt * c.d * sizeof(float);
+  const size_t few = parts_bytes(kGrid, rows_of(group, max_add), c.d);
+  return many(group, max_add) ? parts_align(few) + attn_cache_tc_ws(c) : few;
 }
 
-sparsp_status_t launch_attn_cache(const CacheAttn& a, void* ws, cudaStream_t st) {
-  const bool small = rows_of(a.group, a.max_add) == 8;
-  if (a.c.d == 64) return small ? go<64, 1>(a, ws, st) : go<64, 2>(a, ws, st);
-  return small ? go<128, 1>(a, ws, st) : go<128, 2>(a, ws, st);
+sparsp_status_t launch_attn_cache(const CacheAttn& args, void* ws, cudaStream_t st) {
+  CacheAttn a = args;
+  const int rows = rows_of(a.group, a.max_add);
+  a.few = 0;
+  if (many(a.group, a.max_add)) {
+    const bool all = (int64_t)a.B * a.max_add <= a.tokens;
+    a.few = all ? 0 : kFew;
+    const sparsp_status_t r =
+        launch_attn_cache_tc(a, (uint8_t*)ws + parts_align(parts_bytes(kGrid, rows, a.c.d)), st);
+    if (r != SPARSP_OK || all) return r;
+  }
+  if (a.c.d == 64) return rows == 8 ? go<64, 1>(a, ws, st) : go<64, 2>(a, ws, st);
+  return rows == 8 ? go<128, 1>(a, ws, st) : go<128, 2>(a, ws, st);
 }
 
 }  // namespace sparsp

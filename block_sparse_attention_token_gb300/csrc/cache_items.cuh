@@ -1,0 +1,145 @@
+// What the kernels of attention over the cache share: the items that work is dealt out by,
+// the partial sums of items that several CTAs share, and 8-bit arithmetic.
+#pragma once
+
+#include <cuda_fp16.h>
+
+#include "cache.cuh"
+
+namespace sparsp {
+
+// Entries are requests (every block is seen, all key heads alike), or with lists request and
+// key head.
+struct Entry {
+  int b, hk, n, len, s0;        // n: new tokens, s0: the first one's row; hk: with lists
+  int units;                    // of 64 keys
+  int groups;                   // of rows: the kernel's own count, as are
+  int64_t per_head, weight;
+};
+__device__ __forceinline__ int entries_of(const CacheAttn& a) { return a.row_ptr != nullptr ? a.B * a.c.heads : a.B; }
+// What cannot be right is reported (with tell) and counts as nothing: rows, keys or list.
+__device__ __forceinline__ Entry entry_at(const CacheAttn& a, int e, bool tell) {
+  Entry x;
+  x.hk = a.row_ptr != nullptr ? e % a.c.heads : 0;
+  x.b = a.row_ptr != nullptr ? e / a.c.heads : e;
+  x.s0 = a.start[x.b];
+  const int s1 = a.start[x.b + 1];
+  x.n = (int)max((int64_t)-1, (int64_t)s1 - x.s0);
+  x.len = a.len[x.b];
+  if (x.s0 < 0 || x.n < 0 || s1 > a.tokens || x.n > a.max_add) {
+    if (tell) report(a.d_status, SPARSP_ERR_DATA);
+    x.n = 0;
+  }
+  if (x.len < 0 || x.len > (int64_t)a.max_blocks * a.c.bt) {
+    if (tell) report(a.d_status, SPARSP_ERR_DATA);
+    x.len = 0;
+  }
+  if (a.row_ptr != nullptr) {
+    const int64_t p0 = a.row_ptr[e], p1 = a.row_ptr[e + 1];
+    int64_t count = p1 - p0;
+    if (p0 < 0 || count < 0 || count > a.max_blocks || p1 > a.col_cap) {
+      if (tell) report(a.d_status, SPARSP_ERR_DATA);
+      count = 0;
+    }
+    x.units = (int)count * (a.c.bt / kUnit);
+  } else {
+    x.units = (x.len + kUnit - 1) / kUnit;
+  }
+  x.groups = 0;
+  x.per_head = x.weight = 0;
+  return x;
+}
+
+// The sum over the CTA's threads below this one, and over all of its WARPS warps.
+template <int WARPS>
+__device__ __forceinline__ int64_t scan_below(int64_t mine, int64_t* sm, int64_t* total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int64_t below = mine;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const int64_t v = __shfl_up_sync(0xffffffffu, below, off);
+    if (lane >= off) below += v;
+  }
+  if (lane == 31) sm[warp] = below;
+  below -= mine;
+  __syncthreads();
+  int64_t all = 0;
+#pragma unroll
+  for (int i = 0; i < WARPS; ++i) {
+    if (i < warp) below += sm[i];
+    all += sm[i];
+  }
+  *total = all;
+  return below;
+}
+
+// What the joining kernel needs to know of the item that starts in a CTA and goes on in others.
+struct Open {
+  int b, hk, row0, rows, s0, last;   // last: the CTA of its last unit; -1: there is none
+};
+struct Parts {
+  Open* open;      // [ctas]
+  float2* ml;      // [2 ctas][rows] reference (base 2) and sum; a CTA's parts: an item that goes on, one that starts
+  float* sum;      // [2 ctas][rows][d]
+};
+inline size_t parts_align(size_t n) { return (n + 255) & ~(size_t)255; }
+inline size_t parts_bytes(int ctas, int rows, int d) {
+  return parts_align(ctas * sizeof(Open)) + parts_align((size_t)2 * ctas * rows * sizeof(float2)) +
+         (size_t)2 * ctas * rows * d * sizeof(float);
+}
+inline Parts parts_of(void* ws, int ctas, int rows) {
+  uint8_t* at = (uint8_t*)ws;
+  Parts p;
+  p.open = (Open*)at;
+  at += parts_align(ctas * sizeof(Open));
+  p.ml = (float2*)at;
+  at += parts_align((size_t)2 * ctas * rows * sizeof(float2));
+  p.sum = (float*)at;
+  return p;
+}
+
+// Launches a kernel that may begin before the last one ends and waits for it itself.
+template <typename Kernel>
+sparsp_status_t launch_after(Kernel kern, dim3 grid, int threads, cudaStream_t st, const CacheAttn& a, const Parts& p) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.stream = st;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, kern, a, p) != cudaSuccess) return SPARSP_ERR_CUDA;
+  SPARSP_LAUNCH_CHECK();
+  return SPARSP_OK;
+}
+
+__device__ __forceinline__ uint32_t f16x2_of_e4m3(uint32_t two) {   // the low two bytes
+  uint32_t r;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;\n" : "=r"(r) : "h"((uint16_t)two));
+  return r;
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ float exp2_fast(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(r) : "f"(x));
+  return r;
+}
+
+// Writes four columns of a finished row, and its LSE.
+template <int D>
+__device__ __forceinline__ void finish(const CacheAttn& a, int s0, int hk, int row, int c, float top, float sum,
+                                       const float4& all) {
+  const int64_t at = (int64_t)(s0 + row / a.group) * a.H + hk * a.group + row % a.group;
+  const float f = sum == 0.f ? 0.f : 1.0f / sum;
+  const __nv_bfloat162 lo = __floats2bfloat162_rn(all.x * f, all.y * f), hi = __floats2bfloat162_rn(all.z * f, all.w * f);
+  *reinterpret_cast<uint2*>(a.o + at * D + c) =
+      make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+  if (c == 0) a.lse[at] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
+}
+
+}  // namespace sparsp

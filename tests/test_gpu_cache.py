@@ -6,7 +6,8 @@ rounding of the value. Attention, with y the base-e scores and p = exp(y - max):
 the products of the scores are exact, their fp32 sums (at most 128 terms, rounded or cut)
 are off by at most d 2^-23 sum |q k| scale, a score's scaling and exponential by a few 2^-22
 of |y| + 1: `delta` in a weight's relative error. A weight is rounded to 11 bits (2^-11) or
-lost below 2^-35 of its row's largest; sums over keys are fp32 with at most 2^-24 per key
+lost below 2^-35 of its row's largest; with more than 16 rows of a request to a key head, queries lose what
+is below 2^-18 of their row's largest value (`split`: d of them); sums over keys are fp32 with at most 2^-24 per key
 in a row of additions, LONG keys at most here. The result is rounded to bf16 (2^-8)."""
 import pytest
 import torch
@@ -335,6 +336,9 @@ def attn_ref(q, keys, add, lengths, scale, causal, bt, chosen=None):
         l = p.sum(-1, keepdim=True)
         safe = torch.where(l > 0, l, 1.0)
         delta = d * 2.0 ** -23 * mag + 2.0 ** -19 * (1 + mag)
+        if n * G > 16 and total:
+            split = qb.abs().amax(-1, keepdim=True) * k.abs().sum(-1).amax(-1)[:, None, None] * 2.0 ** -18
+            delta = delta + split * abs(scale)
         spread = (p @ v.abs()) / safe
         o = p @ v / safe
         lost = total * 2.0 ** -35 * (v.abs().amax() if total else 0.0)
@@ -426,10 +430,11 @@ def test_attn_whole_frames(d, bt, causal):
     check_attn([513], [200], 3, 1, d, bt, causal, density=0.5)
 
 
-def test_attn_wide_scales():
+@pytest.mark.parametrize("add", [[2, 1], [90, 1], [33, 128]])
+@pytest.mark.parametrize("d,bt", [(128, 64), (64, 128)])
+def test_attn_wide_scales(add, d, bt):
     """Values whose scales lie far apart from block to block, rows of large and tiny queries."""
-    d, bt, heads = 128, 64, 2
-    lengths, add = [260, 128], [2, 1]
+    heads, lengths = 2, [260, 128]
     pool, table, _ = filled(lengths, heads, d, bt)
     g = gen(11)
     for s in (pool.k_scale, pool.v_scale):
@@ -439,45 +444,50 @@ def test_attn_wide_scales():
         page = table[b, : -(-n // bt)].long()
         keys.append(tuple((values(c)[page] * s.double()[page][..., None, None]).transpose(0, 1).flatten(1, 2)[:, :n]
                           for c, s in ((pool.k, pool.k_scale), (pool.v, pool.v_scale))))
-    q = torch.randn(3, 4, d, generator=g, device="cuda")
+    q = torch.randn(sum(add), 4, d, generator=g, device="cuda")
     q[0] *= 1e-6
     q[1] *= 50.0
     q[2, 0] = 0.0
     q[2, 1, ::2] *= 2.0 ** -16      # half the columns far below the others
     q = q.bfloat16()
-    o, lse = sp.attn_cache_fwd(pool, q, i32([0, 2, 3]), i32(lengths), table, 2)
+    o, lse = sp.attn_cache_fwd(pool, q, i32([0] + add).cumsum(0).int(), i32(lengths), table, max(add))
     O, L, to, tl = attn_ref(q, keys, add, lengths, d ** -0.5, True, bt)
     assert ((o.double() - O).abs() <= to).all() and ((lse.double() - L).abs() <= tl).all()
 
 
-def test_attn_not_finite():
+@pytest.mark.parametrize("add", [[1, 2, 1], [1, 80, 1], [90, 5, 33]])
+def test_attn_not_finite(add):
     """NaN and infinities in a row's own query, or in a key that it sees, give NaN there and only there."""
-    lengths, add = [100, 90, 100], [1, 2, 1]
+    lengths, n = [100, 90, 100], sum(add)
     pool, table, start, ln, q = check_attn(lengths, add, 1, 4, 64, 64, True)
-    clean, lc = sp.attn_cache_fwd(pool, q, start, ln, table, 2)
+    clean, lc = sp.attn_cache_fwd(pool, q, start, ln, table, max(add))
     bad = q.clone()
-    bad[1, 2, 5], bad[2, 0, 7] = float("nan"), float("inf")
-    o, lse = sp.attn_cache_fwd(pool, bad, start, ln, table, 2)
-    hit = torch.zeros(4, 4, dtype=torch.bool, device="cuda")
-    hit[1, 2] = hit[2, 0] = True
-    assert torch.isnan(o[:4][hit]).all() and torch.isnan(lse[:4][hit]).all()
-    assert torch.equal(o[:4][~hit], clean[:4][~hit]) and torch.equal(lse[:4][~hit], lc[:4][~hit])
-    pool.k.view(torch.uint8)[table[2, 1], 0, 3, 9] = 0x7f      # a key of the last request
-    o, lse = sp.attn_cache_fwd(pool, q, start, ln, table, 2)
-    assert torch.isnan(o[3]).all() and torch.isnan(lse[3]).all()
-    assert torch.equal(o[:3], clean[:3]) and torch.equal(lse[:3], lc[:3])
+    bad[1, 2, 5], bad[2, 0, 7], bad[n - 1, 3, 0] = float("nan"), float("inf"), -float("inf")
+    o, lse = sp.attn_cache_fwd(pool, bad, start, ln, table, max(add))
+    hit = torch.zeros(n, 4, dtype=torch.bool, device="cuda")
+    hit[1, 2] = hit[2, 0] = hit[n - 1, 3] = True
+    assert torch.isnan(o[:n][hit]).all() and torch.isnan(lse[:n][hit]).all()
+    assert torch.equal(o[:n][~hit], clean[:n][~hit]) and torch.equal(lse[:n][~hit], lc[:n][~hit])
+    pool.k.view(torch.uint8)[table[2, 0], 0, 3, 9] = 0x7f      # a key of the last request
+    o, lse = sp.attn_cache_fwd(pool, q, start, ln, table, max(add))
+    mine = slice(n - add[2], n)
+    assert torch.isnan(o[mine]).all() and torch.isnan(lse[mine]).all()
+    assert torch.equal(o[: n - add[2]], clean[: n - add[2]]) and torch.equal(lse[: n - add[2]], lc[: n - add[2]])
 
 
-def test_attn_bad_data():
-    lengths, add = [100, 200, 300], [1, 2, 1]
+@pytest.mark.parametrize("add", [[1, 2, 1], [1, 70, 1], [20, 2, 300]])
+def test_attn_bad_data(add):
+    lengths, n, most = [100, 200, 300], sum(add), max(add)
+    one, two, three = slice(0, add[0]), slice(add[0], add[0] + add[1]), slice(add[0] + add[1], n)
+    s1, s2 = add[0], add[0] + add[1]
     pool, table, start, ln, q = check_attn(lengths, add, 2, 2, 64, 64, True)
-    want = sp.attn_cache_fwd(pool, q, start, ln, table, 2)
+    want = sp.attn_cache_fwd(pool, q, start, ln, table, most)
 
     # the work is dealt out by the lengths of the whole call, so that the others' rows may be summed in
     # another order: two results, each within 2^-8 |o| + (2^-11 + delta) max |v| of the same value
     near = lambda x, y: torch.allclose(x.float(), y.float(), atol=2.0 ** -6, rtol=2.0 ** -7)
 
-    def call(start=start, ln=ln, table=table, max_add=2, **kw):
+    def call(start=start, ln=ln, table=table, max_add=most, **kw):
         o, lse = torch.full_like(want[0], 5.0), torch.full_like(want[1], 5.0)
         status = word()
         sp.attn_cache_fwd(pool, q, start, ln, table, max_add, o=o, lse=lse, status=status, **kw)
@@ -493,16 +503,18 @@ def test_attn_bad_data():
         row_ptr, col = csr(seen)
         o2, lse2, st2 = call(row_ptr=row_ptr, col_idx=col)
         assert st2 == 0
-        assert near(o[1:3], o2[1:3]) and near(o[0], want[0][0]) and near(o[3], want[0][3])
+        assert near(o[two], o2[two]) and near(o[one], want[0][one]) and near(o[three], want[0][three])
     for bad_len in (-1, 2 ** 31 - 1, table.shape[1] * 64 + 1):        # a bad length counts as 0
         o, lse, st = call(ln=i32([100, bad_len, 300]))
-        assert st == sp.DATA and (o[1:3] == 0).all() and torch.isinf(lse[1:3]).all()
-        assert near(o[3], want[0][3])
-    for s in ([0, 1, 3, 2 ** 31 - 1], [0, 1, 4, 3], [-1, 1, 3, 4], [0, 1, 3, 1000]):   # rows that are none: left out
+        assert st == sp.DATA and (o[two] == 0).all() and torch.isinf(lse[two]).all()
+        assert near(o[three], want[0][three])
+    for s in ([0, s1, s2, 2 ** 31 - 1], [0, s1, n, s2], [-1, s1, s2, n], [0, s1, s2, 1000], [-2 ** 31, s1, s2, n]):   # rows that are none: left out
         o, lse, st = call(start=i32(s))
-        assert st == sp.DATA and torch.equal(o[4:], torch.full_like(o[4:], 5.0))
-    o, lse, st = call(max_add=1)                                      # more rows than announced
-    assert st == sp.DATA and (o[1:3] == 5).all() and near(o[3], want[0][3])
+        assert st == sp.DATA and torch.equal(o[n:], torch.full_like(o[n:], 5.0))
+    o, lse, st = call(max_add=most - 1)                               # more rows than announced
+    over = [p for p, a in zip((one, two, three), add) if a == most][0]
+    assert st == sp.DATA and (o[over] == 5).all()
+    assert all(near(o[p], want[0][p]) for p in (one, two, three) if p is not over)
     seen = [torch.ones(2, -(-n // 64), dtype=torch.bool, device="cuda") for n in lengths]
     row_ptr, col = csr(seen)
     for at, v in ((3, 4), (4, -1), (5, 2 ** 31 - 1)):                 # blocks without tokens: left out
@@ -510,12 +522,12 @@ def test_attn_bad_data():
         c[at] = v
         o, lse, st = call(row_ptr=row_ptr, col_idx=c)
         assert st == sp.DATA and torch.isfinite(o.float()).all()
-        assert near(o[3], want[0][3])
+        assert near(o[three], want[0][three])
     for at, v in ((2, 0), (2, 2 ** 31 - 1), (6, 1000), (3, -4)):      # rows of lists that make no sense: empty
         r = row_ptr.clone()
         r[at] = v
         o, lse, st = call(row_ptr=r, col_idx=col)
-        assert st == sp.DATA and torch.isfinite(o.float()).all() and near(o[0, :2], want[0][0, :2])
+        assert st == sp.DATA and torch.isfinite(o.float()).all() and near(o[one, :2], want[0][one, :2])
 
 
 def test_attn_stream_capture_and_two_graphs():
