@@ -19,14 +19,16 @@
 // keep the tensor cores busy, and both read the same K and V from shared memory. Work is counted in
 // stages of 128 keys over all items (request, key head, 256 rows) and dealt out evenly;
 // an item in several CTAs leaves partial sums that a second kernel joins in order.
-//   warps 0-3, 4-7: softmax and epilogue of tiles 0 and 1, a row per thread (= TMEM lane).
-//              At an item's start they also split its queries into shared memory.
-//   warps 8-11: widen V, zeros past a request's last token (what lies there may be anything).
-//   warp 12: producer: items, look-ups of lists and tables (32 at a time, a batch ahead),
+//   warps 0-7, 8-15: softmax and epilogue of tiles 0 and 1, two threads to a row (= TMEM lane), one for
+//              each half of a stage's keys (and of the columns of Q and O); the two exchange their
+//              largest score. At an item's start they also split its queries into shared memory.
+//   warps 16-19: widen V, zeros past a request's last token (what lies there may be anything).
+//   warp 20: producer: items, look-ups of lists and tables (32 at a time, a batch ahead),
 //              K by TMA boxes of 64 keys, V by bulk copies.
-//   warp 13: issues S of both tiles (A = q1, q2, B = K, K-major, from shared memory).
-//   warp 14: issues O += P V (A = P in TMEM, written over the S it is made of, B = V MN-major).
-// TMEM (512 columns): S and then P of the tiles [0, 256), O [256, 512).
+//   warp 21: issues S of both tiles (A = q1, q2, B = K, K-major, from shared memory).
+//   warp 22: issues O += P V (A = P in TMEM, written over the S it is made of, B = V MN-major).
+// TMEM (512 columns): S and then P of the tiles [0, 256) (P of a half stage over the scores it is
+// made of), O [256, 512).
 // Every mbarrier wait is bounded (2 s); on expiry the CTA sets SPARSP_ERR_TIMEOUT, all roles
 // leave their loops, copies and MMAs in flight are drained with a second bounded wait, and
 // TMEM is released.
@@ -46,6 +48,8 @@ constexpr int kMinStages = 10;     // stages, an item's own among them, that are
 constexpr float kShift = 11.f, kMoves = 4.f;   // P is held as 2^11 times what it is against R
 constexpr int kNK = 3, kNV = 2, kNW = 2, kNInfo = 8, kNItems = 2;
 constexpr uint64_t kWaitNs = 2000000000ull, kDrainNs = 200000000ull;
+
+constexpr int kSoftmax = 16, W_WIDEN = kSoftmax, W_PROD = W_WIDEN + 4, W_S = W_PROD + 1, W_PV = W_PROD + 2;   // warps
 
 enum Bars {
   K_FULL, K_EMPTY = K_FULL + kNK, V_FULL = K_EMPTY + kNK, V_EMPTY = V_FULL + kNV, W_FULL = V_EMPTY + kNV,
@@ -67,15 +71,16 @@ struct Info {
 
 template <int D>
 struct Cfg {
-  static constexpr int THREADS = 512;
-  static constexpr uint32_t kRegSoftmax = 200, kRegAux = 56;
-  static_assert(256 * (kRegSoftmax + kRegAux) == THREADS * 128, "register split of the four warpgroups");
+  static constexpr int THREADS = 768;
+  static constexpr uint32_t kRegSoftmax = 88, kRegAux = 64;
+  static_assert(512 * kRegSoftmax + 256 * kRegAux == THREADS * 80, "register split of the six warpgroups");
   static constexpr uint32_t kQ = kTileRows * D, kK = kStageKeys * D, kV = kStageKeys * D;      // bytes: q1 or q2, K, V
   static constexpr uint32_t kW = kStageKeys * D * 2, kWBox = kStageKeys * 128;                 // V in f16, 64 columns of it
   static constexpr uint32_t kOffK = 4 * kQ, kOffV = kOffK + kNK * kK, kOffW = kOffV + kNV * kV;
   static constexpr uint32_t kOffBar = kOffW + kNW * kW, kOffInfo = kOffBar + 8 * NBAR;
   static constexpr uint32_t kOffPiece = kOffInfo + kNInfo * (uint32_t)sizeof(Info);
-  static constexpr uint32_t kOffMisc = kOffPiece + kNItems * (uint32_t)sizeof(Piece);
+  static constexpr uint32_t kOffEx = kOffPiece + kNItems * (uint32_t)sizeof(Piece);   // [2][tile][half][row] floats
+  static constexpr uint32_t kOffMisc = kOffEx + 2 * 2 * 2 * kTileRows * 4;
   static constexpr uint32_t kSmem = kOffMisc + 64 + 1024;   // + alignment slack
   static_assert(kSmem <= 232448, "shared memory");
   // K-major rows of D bytes: 128-byte swizzle, or with D = 64 the 64-byte one
@@ -173,7 +178,7 @@ attn_cache_tc_kernel(const __grid_constant__ CUtensorMap tk, const CacheAttn a, 
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gbase + C::kOffMisc);
   volatile int32_t* abort_flag = reinterpret_cast<volatile int32_t*>(gbase + C::kOffMisc + 4);
   int64_t* s_begin = reinterpret_cast<int64_t*>(gbase + C::kOffMisc + 16);   // first entry, its offset
-  __shared__ int64_t s_scan[16];
+  __shared__ int64_t s_scan[C::THREADS / 32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
 
@@ -183,7 +188,7 @@ attn_cache_tc_kernel(const __grid_constant__ CUtensorMap tk, const CacheAttn a, 
   const int n0 = min(entries, (int)threadIdx.x * per), n1 = min(entries, n0 + per);
   int64_t mine = 0;
   for (int e = n0; e < n1; ++e) mine += walk.at(e, blockIdx.x == 0).weight;
-  int64_t total, below = scan_below<16>(mine, s_scan, &total);
+  int64_t total, below = scan_below<C::THREADS / 32>(mine, s_scan, &total);
   const int64_t ctas = min((int64_t)gridDim.x, max((int64_t)1, (total + kMinStages - 1) / kMinStages)), cta = blockIdx.x;
   const int64_t begin = cta * total / ctas, end = cta < ctas ? (cta + 1) * total / ctas : begin;
   if (threadIdx.x == 0) parts.open[cta].last = -1;
@@ -211,18 +216,18 @@ attn_cache_tc_kernel(const __grid_constant__ CUtensorMap tk, const CacheAttn a, 
     init(W_EMPTY, kNW, 1);
     init(INFO, kNInfo, 1);
     init(I_FULL, kNItems, 1);
-    init(I_EMPTY, kNItems, 14);   // softmax, widening and issuing warps
-    init(Q_FULL, 2, 4);
+    init(I_EMPTY, kNItems, kSoftmax + 6);   // softmax, widening and issuing warps
+    init(Q_FULL, 2, 8);
     init(S_FULL, 2, 1);
-    init(P_FULL, 2, 4);
+    init(P_FULL, 2, 8);
     init(PV_DONE, 2, 1);
-    init(O_EMPTY, 2, 4);
+    init(O_EMPTY, 2, 8);
     init(TEAR, 2, 1);
     *abort_flag = 0;
     fence_barrier_init();
   }
-  if (warp == 12 && lane == 0) prefetch_tmap(&tk);
-  if (warp == 13) {
+  if (warp == W_PROD && lane == 0) prefetch_tmap(&tk);
+  if (warp == W_S) {
     tmem_alloc(smem_u32(tmem_slot), 512);
     tmem_relinquish();
   }
@@ -246,9 +251,9 @@ attn_cache_tc_kernel(const __grid_constant__ CUtensorMap tk, const CacheAttn a, 
   };
   auto tiles_of = [&](const Piece& x) { return x.rows > kTileRows ? 2 : 1; };
 
-  if (warp >= 8) {
+  if (warp >= kSoftmax) {
     regs_decrease<C::kRegAux>();
-    if (warp == 12) {
+    if (warp == W_PROD) {
       // ------------------------------------------------------------ producer
       uint32_t it_fill = 0, k_fill = 0, v_fill = 0, n_info = 0;
       int entry = (int)s_begin[0];
@@ -387,7 +392,7 @@ attn_cache_tc_kernel(const __grid_constant__ CUtensorMap tk, const CacheAttn a, 
           if (v_fill > i) wait_raw(bar(V_FULL + (v_fill - 1 - i) % kNV), ((v_fill - 1 - i) / kNV) & 1u, kDrainNs);
       }
       __syncwarp();
-    } else if (warp == 13) {
+    } else if (warp == W_S) {
       // ------------------------------------------------------------ S = Q K^T issuer
       uint32_t k_use = 0, n_q[2] = {0, 0}, n_s[2] = {0, 0};
       bool issued = false, ok = true;
@@ -426,7 +431,7 @@ attn_cache_tc_kernel(const __grid_constant__ CUtensorMap tk, const CacheAttn a, 
         wait_raw(bar(TEAR), 0, kDrainNs);
       }
       __syncwarp();
-    } else if (warp == 14) {
+    } else if (warp == W_PV) {
       // ------------------------------------------------------------ O += P V issuer
       uint32_t w_use = 0, n_p[2] = {0, 0}, n_o[2] = {0, 0};
       bool issued = false, ok = true;
@@ -443,7 +448,7 @@ attn_cache_tc_kernel(const __grid_constant__ CUtensorMap tk, const CacheAttn a, 
             if (elect_one()) {
 #pragma unroll
               for (int kk = 0; kk < kStageKeys / 16; ++kk)
-                mma_ts(col_o(t), col_s(t) + 8u * kk, smem_desc(sW + ws * C::kW + 2048u * kk, C::kWBox, 1024, kSwizzle128B),
+                mma_ts(col_o(t), col_s(t) + 64u * (kk >> 2) + 8u * (kk & 3), smem_desc(sW + ws * C::kW + 2048u * kk, C::kWBox, 1024, kSwizzle128B),
                        idesc(D, 1), e > x.e0 || kk > 0 ? 1u : 0u);
               commit(bar(PV_DONE + t));
               if (t + 1 == tiles) commit(bar(W_EMPTY + ws));
@@ -461,10 +466,10 @@ attn_cache_tc_kernel(const __grid_constant__ CUtensorMap tk, const CacheAttn a, 
         wait_raw(bar(TEAR_PV), 0, kDrainNs);
       }
       __syncwarp();
-    } else if (warp < 12) {
+    } else if (warp < W_PROD) {
       // ------------------------------------------------------------ V to f16
       constexpr int CH = D / 16;                // 16-code vectors of a row
-      const int id = threadIdx.x - 256;
+      const int id = threadIdx.x - 32 * W_WIDEN;
       uint32_t n = 0;
       bool ok = true;
       Piece x;
@@ -513,13 +518,29 @@ attn_cache_tc_kernel(const __grid_constant__ CUtensorMap tk, const CacheAttn a, 
   } else {
     regs_increase<C::kRegSoftmax>();
     // -------------------------------------------------------------- softmax + epilogue of tile t
-    const int t = warp >> 2, r = threadIdx.x & 127;   // its row of the tile = TMEM lane
+    const int t = warp >> 3, half = (warp >> 2) & 1, r = (warp & 3) * 32 + lane;   // r: row of the tile = TMEM lane
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t t_s = col_s(t) + lanes, t_o = col_o(t) + lanes;
-    uint32_t n_info = 0, n_s = 0;
+    const uint32_t t_s = col_s(t) + lanes + 64u * half, t_o = col_o(t) + lanes + (uint32_t)half * (D / 2);
+    const int pair_bar = 1 + t * 4 + (warp & 3);   // named barrier of the two warps that share rows
+    float* ex = reinterpret_cast<float*>(gbase + C::kOffEx) + t * 2 * kTileRows + r;
+    uint32_t n_info = 0, n_s = 0, n_ex = 0;
     bool ok = true;
+    // The row's other half: gives its value for this one's. The two warps take every step together: a
+    // warp that has given up says so here (NaN with these bits), and both leave after it.
+    constexpr uint32_t kGone = 0x7fc0dead;
+    auto exchange = [&](float mine, float& theirs) -> bool {
+      float* at = ex + (n_ex++ & 1u) * 4 * kTileRows;   // the other buffer may still be read
+      at[half * kTileRows] = ok ? mine : __uint_as_float(kGone);
+      asm volatile("bar.sync %0, 64;\n" ::"r"(pair_bar) : "memory");
+      theirs = at[(half ^ 1) * kTileRows];
+      ok = ok && !__any_sync(0xffffffffu, __float_as_uint(theirs) == kGone);
+      return ok;
+    };
     Piece x;
-    while (ok && next_piece(x)) {
+    for (;;) {
+      float theirs;
+      ok = ok && next_piece(x);
+      if (!exchange(0.f, theirs)) break;
       if (t >= tiles_of(x)) {
         n_info += (uint32_t)(x.e1 - x.e0);
         continue;
@@ -531,14 +552,14 @@ attn_cache_tc_kernel(const __grid_constant__ CUtensorMap tk, const CacheAttn a, 
       // piece is done: its scores have been read)
       float factor = 0.f;
       {
-        uint4 w[D / 8];
+        const __nv_bfloat16* from = a.q + (int64_t)(x.s0 + tok) * a.q_token + (int64_t)h * D + half * (D / 2);
+        uint4 w[D / 16];
 #pragma unroll
-        for (int c = 0; c < D / 8; ++c)
-          w[c] = live ? __ldg(reinterpret_cast<const uint4*>(a.q + (int64_t)(x.s0 + tok) * a.q_token + (int64_t)h * D) + c)
-                      : make_uint4(0, 0, 0, 0);
+        for (int c = 0; c < D / 16; ++c)
+          w[c] = live ? __ldg(reinterpret_cast<const uint4*>(from) + c) : make_uint4(0, 0, 0, 0);
         uint32_t most = 0;                       // of the finite ones, as bf16 bits
 #pragma unroll
-        for (int c = 0; c < D / 8; ++c) {
+        for (int c = 0; c < D / 16; ++c) {
           const uint32_t p[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
@@ -547,14 +568,16 @@ attn_cache_tc_kernel(const __grid_constant__ CUtensorMap tk, const CacheAttn a, 
             if (hi < 0x7f80u) most = max(most, hi);
           }
         }
+        exchange(__uint_as_float(most), theirs);
+        most = max(most, __float_as_uint(theirs));
         // 224 < most * 2^-e <= 448
-        int ex = (int)(most >> 7) - 127 - 8 + ((most & 0x7fu) > 0x60u ? 1 : 0);
-        ex = max(-100, min(120, ex));
-        const float down = __uint_as_float((uint32_t)(127 - ex) << 23);
-        factor = __uint_as_float((uint32_t)(127 + ex) << 23) * a.scale_log2;
+        int e2 = (int)(most >> 7) - 127 - 8 + ((most & 0x7fu) > 0x60u ? 1 : 0);
+        e2 = max(-100, min(120, e2));
+        const float down = __uint_as_float((uint32_t)(127 - e2) << 23);
+        factor = __uint_as_float((uint32_t)(127 + e2) << 23) * a.scale_log2;
         uint8_t* q1 = gbase + (uint32_t)(2 * t) * C::kQ;
 #pragma unroll
-        for (int c = 0; c < D / 16; ++c) {
+        for (int c = 0; c < D / 32; ++c) {
           const uint32_t p[8] = {w[2 * c].x,     w[2 * c].y,     w[2 * c].z,     w[2 * c].w,
                                  w[2 * c + 1].x, w[2 * c + 1].y, w[2 * c + 1].z, w[2 * c + 1].w};
           uint32_t hi4[4], lo4[4];
@@ -574,54 +597,48 @@ attn_cache_tc_kernel(const __grid_constant__ CUtensorMap tk, const CacheAttn a, 
               lo4[i / 2] = small;
             }
           }
-          *reinterpret_cast<uint4*>(q1 + C::at(r, c)) = make_uint4(hi4[0], hi4[1], hi4[2], hi4[3]);
-          *reinterpret_cast<uint4*>(q1 + C::kQ + C::at(r, c)) = make_uint4(lo4[0], lo4[1], lo4[2], lo4[3]);
+          const uint32_t to = C::at(r, half * (D / 32) + c);
+          *reinterpret_cast<uint4*>(q1 + to) = make_uint4(hi4[0], hi4[1], hi4[2], hi4[3]);
+          *reinterpret_cast<uint4*>(q1 + C::kQ + to) = make_uint4(lo4[0], lo4[1], lo4[2], lo4[3]);
         }
         fence_async_shared();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(Q_FULL + t));
       }
       const int last = a.causal ? x.len - x.n + tok : INT32_MAX;   // the last key that the row sees
-      float ref = -INFINITY, l = 0.f;            // R, and l times 2^11
+      float ref = -INFINITY, l = 0.f;            // R; l times 2^11, of this half's keys
       for (int e = x.e0; e < x.e1; ++e) {
         const uint32_t is = n_info % kNInfo;
-        if (!(ok = wait_warp(bar(INFO + is), (n_info / kNInfo) & 1u, g))) break;
+        ok = ok && wait_warp(bar(INFO + is), (n_info / kNInfo) & 1u, g);
         ++n_info;
-        int see[2];
-        float c[2], lv[2], inv[2];
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const int pos = infos[is].pos[k];
-          see[k] = min(infos[is].valid[k], last - pos < 63 ? last - pos + 1 : 64);
-          c[k] = factor * infos[is].ks[k];
-          lv[k] = infos[is].lv[k];
-          inv[k] = infos[is].inv[k];
-        }
-        const bool cut = __any_sync(0xffffffffu, see[0] < 64 || see[1] < 64);
-        if (!(ok = wait_warp(bar(S_FULL + t), n_s & 1u, g))) break;
+        const int pos = infos[is].pos[half];
+        const int see = min(infos[is].valid[half], last - pos < 63 ? last - pos + 1 : 64);
+        const float c = factor * infos[is].ks[half], lv = infos[is].lv[half], inv = infos[is].inv[half];
+        const bool cut = __any_sync(0xffffffffu, see < 64);
+        ok = ok && wait_warp(bar(S_FULL + t), n_s & 1u, g);
         ++n_s;
         fence_after();
-        uint32_t s[kStageKeys];
-        float cm[4];
+        // the scores are read twice, for their maximum and for P: registers hold 32 of them at a time
+        uint32_t s[32];
+        float cm;
+        if (!cut) {
+          cm = tmem_ld32_max(t_s, s);
+          cm = fmaxf(cm, tmem_ld32_max(t_s + 32u, s));
+          wait_ld();
+        } else {
+          cm = -INFINITY;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) cm[i] = tmem_ld32_max(t_s + 32u * i, s + 32 * i);
-        wait_ld();
-        if (cut) {
+          for (int q = 0; q < 2; ++q) {
+            tmem_ld32(t_s + 32u * q, s);
+            wait_ld();
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            float mx = -INFINITY;
-#pragma unroll
-            for (int k = 0; k < 32; ++k) {
-              if ((i & 1) * 32 + k >= see[i >> 1]) s[32 * i + k] = 0xff800000u;
-              mx = fmaxf(mx, __uint_as_float(s[32 * i + k]));
-            }
-            cm[i] = mx;
+            for (int k = 0; k < 32; ++k) cm = 32 * q + k < see ? fmaxf(cm, __uint_as_float(s[k])) : cm;
           }
         }
         // a half without keys says nothing (its product with a scale might)
-        const float top0 = see[0] > 0 ? fmaf(fmaxf(cm[0], cm[1]), c[0], lv[0]) : -INFINITY;
-        const float top1 = see[1] > 0 ? fmaf(fmaxf(cm[2], cm[3]), c[1], lv[1]) : -INFINITY;
-        const float top = fmaxf(top0, top1);
+        float top = see > 0 ? fmaf(cm, c, lv) : -INFINITY;
+        if (!exchange(top, theirs)) break;
+        top = fmaxf(top, theirs);
         float f = 1.f;
         const bool moves = top > ref + kMoves;   // by itself: not by what other rows hold
         if (moves) {
@@ -629,29 +646,33 @@ attn_cache_tc_kernel(const __grid_constant__ CUtensorMap tk, const CacheAttn a, 
           ref = top;
           l *= f;
         }
-        const float against = ref == -INFINITY ? 0.f : ref;
-        float sum[2];
+        const float off = lv + kShift - (ref == -INFINITY ? 0.f : ref);
+        float rs[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const float off = lv[k] + kShift - against;
-          uint32_t pk[32];
-          float rs[4] = {0.f, 0.f, 0.f, 0.f};
+        for (int q = 0; q < 2; ++q) {
+          tmem_ld32(t_s + 32u * q, s);
+          wait_ld();
+          if (cut) {
 #pragma unroll
-          for (int i = 0; i < 32; ++i) {
+            for (int k = 0; k < 32; ++k)
+              if (32 * q + k >= see) s[k] = 0xff800000u;
+          }
+          uint32_t pk[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
             float x0, x1;
-            fma_x2(__uint_as_float(s[64 * k + 2 * i]), __uint_as_float(s[64 * k + 2 * i + 1]), c[k], off, x0, x1);
+            fma_x2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1]), c, off, x0, x1);
             const float p0 = exp2_fast(x0), p1 = exp2_fast(x1);
             add_x2(rs[2 * (i & 1)], rs[2 * (i & 1) + 1], p0, p1);
             pk[i] = pack_f16(p0, p1);
           }
-          tmem_st32(t_s + 32u * k, pk);
-          sum[k] = (rs[0] + rs[1]) + (rs[2] + rs[3]);
+          tmem_st16(t_s + 16u * q, pk);          // over scores of this half that have been read
         }
-        l = fmaf(sum[0], inv[0], fmaf(sum[1], inv[1], l));
+        l = fmaf((rs[0] + rs[1]) + (rs[2] + rs[3]), inv, l);
         // O follows the reference now that the scores are no longer held
         if (e > x.e0 && __any_sync(0xffffffffu, moves)) {   // PV of the last stage is done: S came after it
 #pragma unroll
-          for (int i = 0; i < D / 32; ++i) {
+          for (int i = 0; i < D / 64; ++i) {
             uint32_t ov[32];
             tmem_ld32(t_o + 32u * i, ov);
             wait_ld();
@@ -665,15 +686,16 @@ attn_cache_tc_kernel(const __grid_constant__ CUtensorMap tk, const CacheAttn a, 
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(P_FULL + t));
       }
-      if (!ok) break;
-      // ---- the end of a piece: O from TMEM
-      if (!(ok = wait_warp(bar(PV_DONE + t), (n_s - 1) & 1u, g))) break;
+      // ---- the end of a piece: the row's whole sum, and half of O from TMEM
+      ok = ok && wait_warp(bar(PV_DONE + t), (n_s - 1) & 1u, g);
+      if (!exchange(l, theirs)) break;
+      l = half ? theirs + l : l + theirs;
       fence_after();
-      const float none = l == 0.f ? 0.f : 1.f, scale = x.part < 0 ? (l == 0.f ? 0.f : 1.0f / l) : none;
+      const float scale = l == 0.f ? 0.f : x.part < 0 ? 1.0f / l : 1.f;
       const int64_t at = (int64_t)(x.s0 + tok) * a.H + h;
-      float* sums = parts.sum + ((int64_t)max(x.part, 0) * kItemRows + t * kTileRows + r) * D;
+      float* sums = parts.sum + ((int64_t)max(x.part, 0) * kItemRows + t * kTileRows + r) * D + half * (D / 2);
 #pragma unroll
-      for (int i = 0; i < D / 32; ++i) {
+      for (int i = 0; i < D / 64; ++i) {
         uint32_t ov[32];
         tmem_ld32(t_o + 32u * i, ov);
         wait_ld();
@@ -681,7 +703,7 @@ attn_cache_tc_kernel(const __grid_constant__ CUtensorMap tk, const CacheAttn a, 
 #pragma unroll
         for (int k = 0; k < 32; ++k) ov[k] = l == 0.f ? 0u : __float_as_uint(__uint_as_float(ov[k]) * scale);
         if (x.part < 0) {
-          uint4* to = reinterpret_cast<uint4*>(a.o + at * D + 32 * i);
+          uint4* to = reinterpret_cast<uint4*>(a.o + at * D + half * (D / 2) + 32 * i);
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             uint32_t w[4];
@@ -702,7 +724,7 @@ attn_cache_tc_kernel(const __grid_constant__ CUtensorMap tk, const CacheAttn a, 
       fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(O_EMPTY + t));
-      if (live) {
+      if (live && half == 0) {
         if (x.part < 0) a.lse[at] = l == 0.f ? -INFINITY : (ref - kShift + log2f(l)) * 0.6931471805599453f;
         else parts.ml[(int64_t)x.part * kItemRows + t * kTileRows + r] = make_float2(ref - kShift, l);
       }
@@ -712,7 +734,7 @@ attn_cache_tc_kernel(const __grid_constant__ CUtensorMap tk, const CacheAttn a, 
   fence_before();
   __syncthreads();
   fence_after();
-  if (warp == 13) tmem_dealloc(tmem, 512);
+  if (warp == W_S) tmem_dealloc(tmem, 512);
 }
 
 // The join of what items in several CTAs have left: CTA (c, rows of the item that starts in CTA c),
