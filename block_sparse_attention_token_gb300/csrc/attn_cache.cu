@@ -7,11 +7,11 @@
 //
 // Few queries: bound by the cache's bytes. A warp holds the scores transposed, S^T = K Q^T
 // (16 keys by 8 query rows: heads that share a key head, and new tokens, side by side), so that
-// few rows fill a matrix instruction; O^T = V^T P^T. The codes go from global memory into
+// few rows fill a matrix instruction; O^T = V^T P^T. The codes go from shared memory into
 // registers in the operands' own layout: the columns of the head are permuted alike in Q and
-// K, and the rows of V^T are columns that a lane has loaded anyway, so that a lane needs only
-// what it loads itself; it does so some stages ahead, into shared-memory slots of its own. Work is counted in units of 64 keys over all requests and key heads and dealt out
-// evenly: a CTA takes a range of units, and an item (request, key head, 8 or 16 rows) that
+// K, and the rows of V^T are columns of vectors that a lane reads anyway. Every warp has a ring of
+// stages of its own, filled by TMA. Work is counted in units of 64 keys over all requests
+// and key heads and dealt out evenly: a CTA takes a range of units, and an item (request, key head, 8 or 16 rows) that
 // spans several CTAs leaves partial sums that a second kernel joins in order.
 #include "cache_items.cuh"
 #include "rows.cuh"
@@ -22,8 +22,9 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kGrid = 152 * 3;     // CTAs that share the work, at most (the workspace depends on it)
-// CTAs per SM: two rows' accumulators of 128 columns do not fit the registers of three.
+// CTAs per SM: what the accumulators of 8 or 16 rows leave registers for.
 constexpr int ctas_per_sm(int d, int nt) { return d == 128 && nt == 2 ? 2 : 3; }
+constexpr int kWideUnits = 16;     // units of a piece from which on a warp takes whole units
 constexpr int kItemCost = 4;       // units that an item's own work (its look-ups, queries, join) counts as
 constexpr int kMinUnits = 6;       // units, an item's own among them, that are worth a CTA
 constexpr float kPScale = 2048.f;  // P is at most 16 and is held as 2^11 P in f16: 2^-35 is not lost
@@ -52,43 +53,63 @@ __device__ __forceinline__ uint32_t transposed(uint32_t v) {
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;\n" : "=r"(r) : "r"(v));
   return r;
 }
-// A warp's ring of 16-key stages: every lane reads back only what it copied itself, so no
-// barrier stands between a copy and its use.
-constexpr int kStages = 4;
+// A warp's ring of 16-key stages, filled by TMA (swizzled by the length of a row, so that the reads
+// below meet no bank twice) and waited for on a barrier per stage.
+constexpr int kStages = 3;
+constexpr uint64_t kWaitNs = 2000000000ull;
 template <int D>
 struct Stage {
-  uint4 k[2][D / 64][32];            // rows g and g + 8 of the stage, columns 64 s + 16 t
-  uint4 v[D / 32][32];               // tokens 2t, 2t+1, 2t+8, 2t+9, columns D/8 g (D = 64: two of them in 16 bytes)
-  float ks[32], vs[32];
+  uint8_t k[16 * D], v[16 * D];
 };
+// Where a lane (g, t) finds its vectors of a stage. K: rows g and g + 8; D = 128: 16-byte vectors 2t and 2t + 1,
+// D = 64: vector t. V: rows 2t, 2t + 1 (and 8 further), columns D/8 g ...
+template <int D>
+__device__ __forceinline__ int at_k(int g, int t, int s) {
+  return D == 128 ? g * 128 + (((2 * t + s) ^ g) << 4) : g * 64 + ((t ^ (g >> 1)) << 4);
+}
+template <int D>
+__device__ __forceinline__ int at_v(int g, int t, int i) {
+  const int r = 2 * t + i;
+  return D == 128 ? r * 128 + ((g ^ r) << 4) : r * 64 + (((g >> 1) ^ t) << 4) + (g & 1) * 8;
+}
 
-__device__ __forceinline__ void copy16(void* dst, const void* src, bool there) {   // zeros where it is not
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(tc::smem_u32(dst)), "l"(src), "r"(there ? 16 : 0)
-               : "memory");
-}
-__device__ __forceinline__ void copy8(void* dst, const void* src, bool there) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;\n" ::"r"(tc::smem_u32(dst)), "l"(src), "r"(there ? 8 : 0)
-               : "memory");
-}
-__device__ __forceinline__ void copy4(void* dst, const void* src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;\n" ::"r"(tc::smem_u32(dst)), "l"(src) : "memory");
+// Waits for a phase, at most kWaitNs; the whole warp gets the same answer.
+__device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity) {
+  bool ok = tc::mbar_try_wait(bar, parity);
+  if (!ok) {
+    const uint64_t t0 = globaltimer_ns();
+    do ok = tc::mbar_try_wait(bar, parity);
+    while (!ok && globaltimer_ns() - t0 < kWaitNs);
+  }
+  return __all_sync(0xffffffffu, ok);
 }
 
 template <int D, int NT>
 constexpr int attn_smem() {
   constexpr int ring = kWarps * kStages * (int)sizeof(Stage<D>);
   constexpr int sums = kWarps * 8 * NT * (D + 4) * 4;    // the warps' sums, over the ring
-  return ring > sums ? ring : sums;
+  return (ring > sums ? ring : sums) + 1024;               // + alignment slack
 }
 
 template <int D, int NT>
 __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT))
-attn_cache_kernel(const CacheAttn a, const Parts parts) {
+attn_cache_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v, const CacheAttn a,
+                  const Parts parts) {
   constexpr int RT = 8 * NT, SEG = D / 64;
   const Walk<RT> walk{a};
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
-  extern __shared__ __align__(16) uint8_t smem[];
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + (-tc::smem_u32(smem_raw) & 1023u);   // swizzle atoms
   Stage<D>* ring = reinterpret_cast<Stage<D>*>(smem) + warp * kStages;
+  __shared__ uint64_t s_full[kWarps][kStages];
+  auto full = [&](int st) { return tc::smem_u32(&s_full[warp][st]); };
+  uint32_t phases = 0;                         // of the stages' barriers
+  bool late = false;                           // a wait has expired: nothing more is copied or waited for
+  if (lane == 0) {
+    for (int i = 0; i < kStages; ++i) tc::mbar_init(full(i), 1);
+    tc::fence_barrier_init();
+  }
+  __syncwarp();
   float (*s_o)[RT][D + 4] = reinterpret_cast<float (*)[RT][D + 4]>(smem);
   __shared__ int64_t s_scan[kWarps];
   __shared__ int64_t s_begin[2];               // first entry, its unit offset
@@ -143,66 +164,70 @@ attn_cache_kernel(const CacheAttn a, const Parts parts) {
     const int row0 = group * RT, rows = min(RT, x.n * a.group - row0);
     const int32_t* table = a.table + (int64_t)x.b * a.max_blocks;
     const int32_t* list = a.row_ptr != nullptr ? a.col_idx + a.row_ptr[entry] : nullptr;
-    const int per_block = a.c.bt / kUnit, stop = min(u1, x.units);
+    const int shift = a.c.bt == kUnit ? 0 : 1, stop = min(u1, x.units);   // units per block, log2
+    // A warp's steps of 16 keys: in a long piece the four of every fourth unit, so that a look-up serves
+    // four steps; in a short one a quarter of every unit, so that all warps have work.
+    const bool wide = u1 - u0 >= kWideUnits;
+    const int first_unit = wide ? u0 + warp : u0, stride = wide ? 4 : 1;
+    const int steps = wide ? max(0, u1 - first_unit + 3) / 4 * 4 : u1 - u0;
 
-    // The key block of unit u and its place in the pool, looked up ahead of the copies: the list
-    // two units ahead, the table one.
+    // The key block of a unit and its place in the pool, looked up ahead of the copies: the list
+    // two units of this warp ahead, the table one.
     auto block_of = [&](int u) -> int {        // -1: none
       if (u >= stop) return -1;
-      const int j = u / per_block;
-      return list != nullptr ? __ldg(list + j) : j;
+      return list != nullptr ? __ldg(list + (u >> shift)) : u >> shift;
     };
     auto page_of = [&](int u, int j) -> int {  // -1: none
       if (u >= stop) return -1;
-      if (j < 0 || (int64_t)j * a.c.bt >= x.len) {
+      if (j < 0 || ((int64_t)j << shift) * kUnit >= x.len) {
         report(a.d_status, SPARSP_ERR_DATA);
         return -1;
       }
       return __ldg(table + j);
     };
-    // Copies the warp's 16 keys of unit u into a stage; returns how many exist.
-    auto fetch = [&](int u, int j, int page, Stage<D>& st) -> int {
-      int valid = 0;
-      if (u < stop && j >= 0 && (int64_t)j * a.c.bt < x.len) {
-        if (page < 0 || page >= a.c.blocks) {
+    int unit = first_unit;                     // the next one to be copied
+    int block1 = block_of(unit), page1 = page_of(unit, block1), block2 = block_of(unit + stride);
+    int pos = 0, exist = 0;                    // of the unit being copied: its first key, how many there are
+    int row = 0, page = 0;                     // its place in the pool
+    int first[kStages], valid[kStages];        // position of a stage's first key, and how many exist
+    float ks[kStages], vs[kStages];
+    // Copies step i into stage st; i rises by one from call to call.
+    auto ahead = [&](int i, int st) {
+      if (i < steps && (!wide || (i & 3) == 0)) {
+        const int in_block = (unit & ((1 << shift) - 1)) * kUnit;
+        exist = 0;
+        if (page1 >= 0 && page1 < a.c.blocks) {
+          pos = (block1 << shift) * kUnit + in_block;
+          exist = min(kUnit, x.len - pos);
+          row = hk * a.c.bt + in_block;
+          page = page1;
+        } else if (unit < stop) {
           report(a.d_status, SPARSP_ERR_DATA);
-        } else {
-          const int at = u % per_block * kUnit + warp * 16;
-          valid = max(0, min(16, x.len - (j * a.c.bt + at)));
+        }
+        block1 = block2;
+        page1 = page_of(unit + stride, block1);
+        block2 = block_of(unit + 2 * stride);
+        unit += stride;
+      }
+      valid[st] = 0;
+      if (i < steps) {
+        const int q = 16 * (wide ? i & 3 : warp);
+        first[st] = pos + q;
+        valid[st] = max(0, min(16, exist - q));
+        if (valid[st] > 0) {
           const int64_t block = (int64_t)page * a.c.heads + hk;
-          const uint8_t* kb = a.kc + (block * a.c.bt + at) * D + g * D + 16 * t;
-          const uint8_t* vb = a.vc + (block * a.c.bt + at) * D + 2 * t * D + D / 8 * g;
-          copy4(&st.ks[lane], a.ks + block);
-          copy4(&st.vs[lane], a.vs + block);
-#pragma unroll
-          for (int r = 0; r < 2; ++r)
-#pragma unroll
-            for (int s = 0; s < SEG; ++s) copy16(&st.k[r][s][lane], kb + 8 * r * D + 64 * s, g + 8 * r < valid);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int tok = (i & 1) + 8 * (i >> 1);
-            const bool there = 2 * t + tok < valid;
-            if (D == 128) copy16(&st.v[i % (D / 32)][lane], vb + tok * D, there);
-            else copy8(reinterpret_cast<uint2*>(&st.v[i / 2][lane]) + (i & 1), vb + tok * D, there);
+          ks[st] = __ldg(a.ks + block);
+          vs[st] = __ldg(a.vs + block);
+          if (lane == 0 && !late) {
+            tc::mbar_arrive_expect_tx(full(st), (uint32_t)sizeof(Stage<D>));
+            tc::tma_load_3d(tc::smem_u32(ring[st].k), &map_k, full(st), 0, row + q, page);
+            tc::tma_load_3d(tc::smem_u32(ring[st].v), &map_v, full(st), 0, row + q, page);
           }
         }
       }
-      copy_commit();
-      return valid;
-    };
-    int first[kStages], valid[kStages];        // position of the warp's first key, and how many exist, by stage
-    int block1 = block_of(u0), page1 = page_of(u0, block1), block2 = block_of(u0 + 1);
-    auto ahead = [&](int u, int& at, int& n, Stage<D>& st) {   // unit u into a stage; u rises by one from call to call
-      const int page2 = page_of(u + 1, block2);
-      const int block3 = block_of(u + 2);
-      at = block1 * a.c.bt + u % per_block * kUnit + warp * 16;
-      n = fetch(u, block1, page1, st);
-      block1 = block2;
-      page1 = page2;
-      block2 = block3;
     };
 #pragma unroll
-    for (int s = 0; s < kStages - 1; ++s) ahead(u0 + s, first[s], valid[s], ring[s]);
+    for (int s = 0; s < kStages - 1; ++s) ahead(s, s);
 
     // ---- Q: f16 under a power of two per row
     for (int r = warp * (32 / (D / 8)) + lane / (D / 8); r < RT; r += kWarps * (32 / (D / 8))) {
@@ -245,7 +270,7 @@ attn_cache_kernel(const CacheAttn a, const Parts parts) {
     for (int j = 0; j < NT; ++j) {
 #pragma unroll
       for (int s = 0; s < D / 16; ++s) {
-        const uint2 w = *reinterpret_cast<const uint2*>(&s_q[j * 8 + g][64 * (s / 4) + 16 * t + 4 * (s % 4)]);
+        const uint2 w = *reinterpret_cast<const uint2*>(&s_q[j * 8 + g][(D == 128 ? 32 * t + 16 * (s / 4) : 16 * t) + 4 * (s % 4)]);
         qf[j][s][0] = w.x;
         qf[j][s][1] = w.y;
       }
@@ -265,23 +290,30 @@ attn_cache_kernel(const CacheAttn a, const Parts parts) {
       for (int i = 0; i < D / 16; ++i) o[j][i][0] = o[j][i][1] = o[j][i][2] = o[j][i][3] = 0.f;
     }
 
-    auto step = [&](const Stage<D>& st, int at, int n) {
-      float c[NT][4];
+    auto step = [&](const Stage<D>& st, int at, int n, float ks, float vs) {
+      float c[NT][4], c2[NT][4];                // two sums, so that products need not wait for one another
 #pragma unroll
-      for (int j = 0; j < NT; ++j) c[j][0] = c[j][1] = c[j][2] = c[j][3] = 0.f;
+      for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) c[j][i] = c2[j][i] = 0.f;
 #pragma unroll
       for (int s4 = 0; s4 < SEG; ++s4) {
-        const uint4 ka = st.k[0][s4][lane], kb = st.k[1][s4][lane];
+        const uint8_t* p = st.k + at_k<D>(g, t, s4);
+        const uint4 ka = *reinterpret_cast<const uint4*>(p), kb = *reinterpret_cast<const uint4*>(p + 8 * D);
         const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w}, wb[4] = {kb.x, kb.y, kb.z, kb.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const uint32_t a0 = f16x2_of_e4m3(wa[i]), a1 = f16x2_of_e4m3(wb[i]), a2 = f16x2_of_e4m3(wa[i] >> 16),
                          a3 = f16x2_of_e4m3(wb[i] >> 16);
 #pragma unroll
-          for (int j = 0; j < NT; ++j) mma(c[j], a0, a1, a2, a3, qf[j][s4 * 4 + i][0], qf[j][s4 * 4 + i][1]);
+          for (int j = 0; j < NT; ++j) mma(i & 1 ? c2[j] : c[j], a0, a1, a2, a3, qf[j][s4 * 4 + i][0], qf[j][s4 * 4 + i][1]);
         }
       }
-      const float ks = st.ks[lane], vf = st.vs[lane] * (1.0f / kPScale);
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) c[j][i] += c2[j][i];
+      const float vf = vs * (1.0f / kPScale);
       bool moved = false;
 #pragma unroll
       for (int j = 0; j < NT; ++j)
@@ -327,26 +359,28 @@ attn_cache_kernel(const CacheAttn a, const Parts parts) {
         p[j][0] = transposed(pack_f16(e[0] * kPScale, e[1] * kPScale));
         p[j][1] = transposed(pack_f16(e[2] * kPScale, e[3] * kPScale));
       }
-      uint32_t v[4][D / 32];
-      if (D == 128) {
+      uint32_t v[4][D / 32];                     // tokens 2t, 2t + 1, 2t + 8, 2t + 9
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint4 w = st.v[i % (D / 32)][lane];
+      for (int i = 0; i < 4; ++i) {
+        const uint8_t* p = st.v + at_v<D>(g, t, i & 1) + (i >> 1) * 8 * D;
+        if (D == 128) {
+          const uint4 w = *reinterpret_cast<const uint4*>(p);
           v[i][0] = w.x;
           v[i][1] = w.y;
           v[i][D / 32 - 2] = w.z;
           v[i][D / 32 - 1] = w.w;
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const uint4 w = st.v[i][lane];
-          v[2 * i][0] = w.x;
-          v[2 * i][1] = w.y;
-          v[2 * i + 1][0] = w.z;
-          v[2 * i + 1][1] = w.w;
+        } else {
+          const uint2 w = *reinterpret_cast<const uint2*>(p);
+          v[i][0] = w.x;
+          v[i][1] = w.y;
         }
       }
+      if (n < 16)                                // what lies past the last token may be anything
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (2 * t + (i & 1) + 8 * (i >> 1) >= n)
+#pragma unroll
+            for (int k = 0; k < D / 32; ++k) v[i][k] = 0;
 #pragma unroll
       for (int i = 0; i < D / 16; ++i) {
         const uint32_t sel = i & 1 ? 0x7362 : 0x5140;
@@ -364,17 +398,21 @@ attn_cache_kernel(const CacheAttn a, const Parts parts) {
       }
     };
 
-    for (int u = u0; u < u1; u += kStages) {
+    for (int i = 0; i < steps; i += kStages) {
 #pragma unroll
       for (int s = 0; s < kStages; ++s) {
-        constexpr int kAhead = kStages - 1;
-        const int next = (s + kAhead) % kStages;
-        ahead(u + s + kAhead, first[next], valid[next], ring[next]);
-        copy_wait<kAhead>();
-        if (valid[s] > 0) step(ring[s], first[s], valid[s]);
+        ahead(i + s + kStages - 1, (s + kStages - 1) % kStages);
+        if (i + s < steps && valid[s] > 0) {
+          if (!late && !wait_for(full(s), (phases >> s) & 1u)) {
+            late = true;
+            report(a.d_status, SPARSP_ERR_TIMEOUT);
+          }
+          phases ^= 1u << s;
+          step(ring[s], first[s], valid[s], ks[s], vs[s]);
+          __syncwarp();                          // before the stage is filled again
+        }
       }
     }
-    copy_wait<0>();
 
     // ---- join the warps
 #pragma unroll
@@ -428,6 +466,7 @@ attn_cache_kernel(const CacheAttn a, const Parts parts) {
     if (!whole && u0 == 0 && threadIdx.x == 0) {
       parts.open[cta] = Open{x.b, hk, row0, rows, x.s0, (int)(((item_at + size) * ctas - 1) / total)};
     }
+    asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");   // the sums, before the rings are filled again
     __syncthreads();
   }
 }
@@ -498,7 +537,11 @@ sparsp_status_t go(const CacheAttn& a, void* ws, cudaStream_t st) {
   const int ctas = 152 * ctas_per_sm(D, NT);
   if (cudaFuncSetAttribute(attn_cache_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
     return SPARSP_ERR_CUDA;
-  attn_cache_kernel<D, NT><<<ctas, kThreads, smem, st>>>(a, p);
+  CUtensorMap map_k, map_v;
+  if (!make_tmap_codes(&map_k, a.kc, (uint64_t)D, (uint64_t)a.c.heads * a.c.bt, (uint64_t)a.c.blocks, 16) ||
+      !make_tmap_codes(&map_v, a.vc, (uint64_t)D, (uint64_t)a.c.heads * a.c.bt, (uint64_t)a.c.blocks, 16))
+    return SPARSP_ERR_CUDA;
+  attn_cache_kernel<D, NT><<<ctas, kThreads, smem, st>>>(map_k, map_v, a, p);
   SPARSP_LAUNCH_CHECK();
   return launch_after(attn_cache_join_kernel<D, NT>, dim3(ctas, 8 * NT), 256, st, a, p);
 }
