@@ -258,50 +258,59 @@ __device__ __forceinline__ void store_codes(uint8_t* to, const uint4& v, float i
   else *reinterpret_cast<uint32_t*>(to) = code[0];
 }
 
-constexpr int kWriteThreads = 256;
 constexpr int kGranule = 128;     // most packed tokens that one CTA looks for runs in
+constexpr int kWriteCtas = 456;   // CTAs that a call is split into where it can be
 constexpr int kShortRun = 4;      // tokens of a run that one warp takes by itself
+constexpr int kWriteDepth = 2;    // blocks' parts in flight per CTA
 
-// CTA (granule of packed tokens, head, K or V). A run is new tokens in a row whose slots
-// are next to each other in one block; it belongs to the granule it starts in. A short run is a
-// warp's, a longer one the CTA's. Every warp finds the runs for itself.
+// Threads of a CTA: at most eight vectors of a whole block to each.
 template <typename T, int D, int BT>
-__global__ void __launch_bounds__(kWriteThreads, sizeof(T) * D * BT <= 32768 ? 4 : 2)
-cache_write_kernel(const CacheDims c, const CacheWrite a, int granule, int32_t* d_status) {
+constexpr int write_threads() { return sizeof(T) * D * BT <= 32768 ? 256 : 512; }
+
+// CTA (granule of packed tokens, some heads). A run is new tokens in a row whose slots are next to
+// each other in one block; it belongs to the granule it starts in. A short run is a warp's,
+// a longer one the CTA's, which takes K and V of its heads one after the other while the
+// next ones are on their way into shared memory, each thread's into slots of its own. Every warp
+// finds the runs for itself.
+template <typename T, int D, int BT>
+__global__ void __launch_bounds__(write_threads<T, D, BT>(), sizeof(T) * D * BT <= 32768 ? 3 : 1)
+cache_write_kernel(const CacheDims c, const CacheWrite a, int granule, int heads, int32_t* d_status) {
+  constexpr int kWriteThreads = write_threads<T, D, BT>();
   constexpr int E = Fresh<T>::E, LPR = D / E;        // lanes per row
+  constexpr int kRows = kWriteThreads / LPR, U = BT / kRows;
+  extern __shared__ uint4 ring[];                    // [kWriteDepth][U][threads]
   __shared__ uint32_t s_most[2][kWriteThreads / 32];
-  const int h = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const bool is_v = blockIdx.z != 0;
-  const T* x = static_cast<const T*>(is_v ? a.v : a.k) + (int64_t)h * (is_v ? a.v_head : a.k_head);
-  const int64_t stride = is_v ? a.v_token : a.k_token;
-  uint8_t* codes = is_v ? a.vc : a.kc;
-  float* scales = is_v ? a.vs : a.ks;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int h0 = blockIdx.y * heads, tasks = 2 * (min(c.heads, h0 + heads) - h0);   // K and V of a head in turn
   const int64_t capacity = (int64_t)c.blocks * BT, t0 = (int64_t)blockIdx.x * granule;
   int turn = 0, buf = 0;
 
-  // One run of `count` tokens from packed token `first` on; t of `threads` threads take part.
-  auto run = [&](int64_t first, int slot, int count, int t, auto threads, auto sweeps, auto reduce) {
-    constexpr int kRows = decltype(threads)::value / LPR, U = decltype(sweeps)::value;
+  // Where a task's new values of packed token `first` start.
+  auto source = [&](int task, int64_t first) {
+    const int h = h0 + (task >> 1);
+    return task & 1 ? static_cast<const T*>(a.v) + first * a.v_token + h * a.v_head
+                    : static_cast<const T*>(a.k) + first * a.k_token + h * a.k_head;
+  };
+  // The part of a run that thread t of kThreads holds in w: row t / LPR + u kThreads / LPR, vector t % LPR.
+  auto hold = [&](int task, int slot, int count, int t, const auto& w, auto threads, auto reduce) {
+    constexpr int kPer = decltype(threads)::value / LPR, kU = sizeof(w) / sizeof(uint4);
     const int c0 = t % LPR, r0 = t / LPR, block = slot / BT, off = slot % BT;
-    const T* from = x + first * stride + c0 * E;
-    uint4 w[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (r0 + u * kRows < count) w[u] = __ldg(reinterpret_cast<const uint4*>(from + (r0 + u * kRows) * stride));
-    float* scale_at = scales + (int64_t)block * c.heads + h;
+    const int64_t at = (int64_t)block * c.heads + h0 + (task >> 1);
+    float* scale_at = (task & 1 ? a.vs : a.ks) + at;
+    uint8_t* base = (task & 1 ? a.vc : a.kc) + at * BT * D;
     const float old = off > 0 ? *scale_at : 0.f;
     uint32_t most = 0;
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (r0 + u * kRows < count) most = max(most, Fresh<T>::most(w[u]));
+    for (int u = 0; u < kU; ++u)
+      if (r0 + u * kPer < count) most = max(most, Fresh<T>::most(w[u]));
     most = reduce(most);                             // also: every thread has read the old scale
     const bool finite = most < kInf;
     if (!finite) {
       if (t == 0) report(d_status, SPARSP_ERR_DATA);
       most = 0;
 #pragma unroll
-      for (int u = 0; u < U; ++u)
-        if (r0 + u * kRows < count) most = max(most, finite_most<T>(w[u]));
+      for (int u = 0; u < kU; ++u)
+        if (r0 + u * kPer < count) most = max(most, finite_most<T>(w[u]));
       most = reduce(most);
     }
     float scale = scale_of(most);
@@ -310,11 +319,10 @@ cache_write_kernel(const CacheDims c, const CacheWrite a, int granule, int32_t* 
     if (kept) scale = fmaxf(scale, power_above(old));
     if (t == 0) *scale_at = scale;
     const float inverse = __uint_as_float((254u << 23) - __float_as_uint(scale));   // of a power of two
-    uint8_t* base = codes + ((int64_t)block * c.heads + h) * BT * D;
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (r0 + u * kRows < count)
-        store_codes<T>(base + (int64_t)(off + r0 + u * kRows) * D + c0 * E, w[u], inverse, finite);
+    for (int u = 0; u < kU; ++u)
+      if (r0 + u * kPer < count)
+        store_codes<T>(base + (off + r0 + u * kPer) * D + c0 * E, w[u], inverse, finite);
     if (kept && scale != old) {                      // older tokens, brought to the larger scale
       const float ratio = old * inverse;
       for (int i = t; i < off * D / 4; i += decltype(threads)::value) {
@@ -333,8 +341,8 @@ cache_write_kernel(const CacheDims c, const CacheWrite a, int granule, int32_t* 
       if (slot >= capacity) report(d_status, SPARSP_ERR_DATA);
       else head = slot >= 0 && (t == 0 || slot % BT == 0 || a.slots[t - 1] != slot - 1);
     }
-    for (uint32_t heads = __ballot_sync(0xffffffffu, head); heads != 0; heads &= heads - 1) {
-      const int64_t first = t0 + g0 + __ffs(heads) - 1;
+    for (uint32_t starts = __ballot_sync(0xffffffffu, head); starts != 0; starts &= starts - 1) {
+      const int64_t first = t0 + g0 + __ffs(starts) - 1;
       const int slot = a.slots[first], room = BT - slot % BT;
       int count = 0;                                 // tokens that follow one another in the block
       for (int i = 0; i < room; i += 32) {
@@ -344,41 +352,76 @@ cache_write_kernel(const CacheDims c, const CacheWrite a, int granule, int32_t* 
         if (on != 0xffffffffu) break;
       }
       if (count <= kShortRun) {
-        if (turn++ % (kWriteThreads / 32) == warp)
-          run(first, slot, count, lane, std::integral_constant<int, 32>{},
-              std::integral_constant<int, kShortRun * LPR / 32>{},
-              [](uint32_t v) { return __reduce_max_sync(0xffffffffu, v); });
-      } else {
-        run(first, slot, count, (int)threadIdx.x, std::integral_constant<int, kWriteThreads>{},
-            std::integral_constant<int, BT * LPR / kWriteThreads>{}, [&](uint32_t v) {
-              v = __reduce_max_sync(0xffffffffu, v);
-              if (lane == 0) s_most[buf][warp] = v;
-              __syncthreads();                       // the buffers alternate: one barrier is enough
+        constexpr int kU = kShortRun * LPR / 32;
+        for (int task = 0; task < tasks; ++task) {
+          if (turn++ % (kWriteThreads / 32) != warp) continue;
+          const int64_t stride = task & 1 ? a.v_token : a.k_token;
+          const T* from = source(task, first) + lane % LPR * E;
+          uint4 w[kU];
 #pragma unroll
-              for (int i = 0; i < kWriteThreads / 32; ++i) v = max(v, s_most[buf][i]);
-              buf ^= 1;
-              return v;
-            });
+          for (int u = 0; u < kU; ++u)
+            if (lane / LPR + u * (32 / LPR) < count)
+              w[u] = __ldg(reinterpret_cast<const uint4*>(from + (lane / LPR + u * (32 / LPR)) * stride));
+          hold(task, slot, count, lane, w, std::integral_constant<int, 32>{},
+               [](uint32_t v) { return __reduce_max_sync(0xffffffffu, v); });
+        }
+      } else {
+        auto place = [&](int st, int u) { return ring + (st * U + u) * kWriteThreads + threadIdx.x; };
+        auto fetch = [&](int task) {
+          if (task < tasks) {
+            const int64_t stride = task & 1 ? a.v_token : a.k_token;
+            const int r0 = threadIdx.x / LPR;
+            const T* from = source(task, first) + r0 * stride + threadIdx.x % LPR * E;
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+              if (r0 + u * kRows < count) copy_async16(place(task % kWriteDepth, u), from + u * kRows * stride);
+          }
+          copy_commit();
+        };
+        for (int i = 0; i < kWriteDepth - 1; ++i) fetch(i);
+        for (int task = 0; task < tasks; ++task) {
+          fetch(task + kWriteDepth - 1);
+          copy_wait<kWriteDepth - 1>();
+          uint4 w[U];
+#pragma unroll
+          for (int u = 0; u < U; ++u) w[u] = *place(task % kWriteDepth, u);
+          hold(task, slot, count, (int)threadIdx.x, w, std::integral_constant<int, kWriteThreads>{}, [&](uint32_t v) {
+            v = __reduce_max_sync(0xffffffffu, v);
+            if (lane == 0) s_most[buf][warp] = v;
+            __syncthreads();                         // the buffers alternate: one barrier is enough
+#pragma unroll
+            for (int i = 0; i < kWriteThreads / 32; ++i) v = max(v, s_most[buf][i]);
+            buf ^= 1;
+            return v;
+          });
+        }
+        copy_wait<0>();
       }
     }
   }
 }
 
 template <typename T, int D, int BT>
-void go_write(const CacheDims& c, const CacheWrite& a, int32_t* d_status, cudaStream_t st) {
-  // granules as large as still leave three CTAs per SM
-  int granule = kGranule;
-  while (granule > 8 && (int64_t)((a.tokens + granule - 1) / granule) * c.heads * 2 < 152 * 3) granule /= 2;
-  const dim3 grid((unsigned)((a.tokens + granule - 1) / granule), (unsigned)c.heads, 2);
-  cache_write_kernel<T, D, BT><<<grid, kWriteThreads, 0, st>>>(c, a, granule, d_status);
+bool go_write(const CacheDims& c, const CacheWrite& a, int32_t* d_status, cudaStream_t st) {
+  // granules and groups of heads as large as still leave three CTAs per SM
+  int granule = kGranule, heads = 8;
+  auto ctas = [&] { return (int64_t)((a.tokens + granule - 1) / granule) * ((c.heads + heads - 1) / heads); };
+  while (heads > 1 && ctas() < kWriteCtas) heads /= 2;
+  while (granule > 4 && ctas() < kWriteCtas) granule /= 2;
+  const size_t smem = (size_t)kWriteDepth * BT * D * sizeof(T);
+  auto kern = cache_write_kernel<T, D, BT>;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) return false;
+  const dim3 grid((unsigned)((a.tokens + granule - 1) / granule), (unsigned)((c.heads + heads - 1) / heads));
+  kern<<<grid, write_threads<T, D, BT>(), smem, st>>>(c, a, granule, heads, d_status);
+  return true;
 }
 
 template <typename T>
-void go_write_shape(const CacheDims& c, const CacheWrite& a, int32_t* d_status, cudaStream_t st) {
-  if (c.d == 64 && c.bt == 64) go_write<T, 64, 64>(c, a, d_status, st);
-  else if (c.d == 64) go_write<T, 64, 128>(c, a, d_status, st);
-  else if (c.bt == 64) go_write<T, 128, 64>(c, a, d_status, st);
-  else go_write<T, 128, 128>(c, a, d_status, st);
+bool go_write_shape(const CacheDims& c, const CacheWrite& a, int32_t* d_status, cudaStream_t st) {
+  if (c.d == 64 && c.bt == 64) return go_write<T, 64, 64>(c, a, d_status, st);
+  if (c.d == 64) return go_write<T, 64, 128>(c, a, d_status, st);
+  if (c.bt == 64) return go_write<T, 128, 64>(c, a, d_status, st);
+  return go_write<T, 128, 128>(c, a, d_status, st);
 }
 
 }  // namespace
@@ -404,8 +447,9 @@ sparsp_status_t launch_cache_extend(const CacheDims& c, const CacheExtend& a, in
 sparsp_status_t launch_cache_write(const CacheDims& c, int dtype, const CacheWrite& a, int32_t* d_status,
                                    cudaStream_t st) {
   if (a.tokens == 0) return SPARSP_OK;
-  if (dtype == SPARSP_F32) go_write_shape<float>(c, a, d_status, st);
-  else go_write_shape<__nv_bfloat16>(c, a, d_status, st);
+  if (!(dtype == SPARSP_F32 ? go_write_shape<float>(c, a, d_status, st)
+                            : go_write_shape<__nv_bfloat16>(c, a, d_status, st)))
+    return SPARSP_ERR_CUDA;
   SPARSP_LAUNCH_CHECK();
   return SPARSP_OK;
 }
