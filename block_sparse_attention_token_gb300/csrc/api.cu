@@ -170,6 +170,7 @@ sparsp_status_t span_of(const Dims& s, int heads, const void* p, int64_t* stride
   if (blocked) *stride = 0;
   const sparsp_status_t r = check_stride(t, stride);
   if (r != SPARSP_OK) return r;
+  if (*stride * s.elem > UINT32_MAX) return SPARSP_ERR_UNSUPPORTED;
   const int64_t row = (int64_t)heads * s.d * s.elem, rows = (int64_t)s.B * s.N;
   *out = Span{(const uint8_t*)p, *stride * s.elem, row, (rows - 1) * *stride * s.elem + row};
   return SPARSP_OK;

@@ -43,41 +43,43 @@ struct Tokens {
   int bt;           // tokens per tile
 };
 
+// Strides are bytes between tokens (raster); below 2^32, so that an address is one multiply-add.
 struct Fwd {
   const void* in;
-  int64_t in_stride;
+  uint32_t in_stride;
   void* out;
-  int64_t out_stride;
+  uint32_t out_stride;
   const float *w, *b;
   float* means;
   int heads, groups;
 };
 struct Bwd {
   const void *dy, *x;
-  int64_t dy_stride, x_stride;
+  uint32_t dy_stride, x_stride;
   void* dx;
-  int64_t dx_stride;
+  uint32_t dx_stride;
   const float* w;
   float *dw, *db;
   int heads, groups;
 };
 
-// tok[o]: flat raster token (b * N + n, -1 past the end) and its table row per axis (-1: not turned).
-template <int GR, int THREADS>
-__device__ __forceinline__ void locate(int4* tok, const Tokens& t, const RopeArgs& a, int32_t* d_status) {
+// tok[o] of tokens blockIdx.x * count ..: flat raster token (b * N + n, -1 past the end) and its table row
+// per axis (-1: not turned). In tile order count divides a tile's tokens.
+template <int THREADS>
+__device__ __forceinline__ void locate(int4* tok, int count, const Tokens& t, const RopeArgs& a, int32_t* d_status) {
   const RasterMap& rm = t.rm;
-  for (int o = threadIdx.x; o < GR; o += THREADS) {
+  for (int o = threadIdx.x; o < count; o += THREADS) {
     int64_t flat;
     int p[3];
     if (t.linear) {
-      flat = (int64_t)blockIdx.x * GR + o;
+      flat = (int64_t)blockIdx.x * count + o;
       const int n = (int)(flat % rm.N);
       p[0] = n / (rm.Y * rm.X);
       p[1] = n / rm.X % rm.Y;
       p[2] = n % rm.X;
     } else {
-      const int per = t.bt / GR, nb = (int)(rm.N / t.bt), tile = blockIdx.x / per;
-      const int j = tile % nb, oo = (int)(blockIdx.x % per) * GR + o;
+      const int per = t.bt / count, nb = (int)(rm.N / t.bt), tile = blockIdx.x / per;
+      const int j = tile % nb, oo = (int)(blockIdx.x % per) * count + o;
       const int bx = j % rm.nX, by = (j / rm.nX) % rm.nY, bt = j / (rm.nX * rm.nY);
       const int tbc = rm.tb * rm.tc, it = oo / tbc, rem = oo - it * tbc, iy = rem / rm.tc, ix = rem - iy * rm.tc;
       p[0] = bt * rm.ta + it;
@@ -118,7 +120,7 @@ template <int P2>
 __device__ __forceinline__ void turn(f32x2* x, f32x2* y, const f32x2* c, const f32x2* s) {
 #pragma unroll
   for (int i = 0; i < P2; ++i) {
-    const f32x2 r = fma2(x[i], c[i], mul2(y[i], s[i] ^ 0x8000000080000000ull));
+    const f32x2 r = sub2(mul2(x[i], c[i]), mul2(y[i], s[i]));
     y[i] = fma2(y[i], c[i], mul2(x[i], s[i]));
     x[i] = r;
   }
@@ -165,6 +167,12 @@ __device__ __forceinline__ float dot_of(const f32x2* ax, const f32x2* ay, const 
   return hsum(add2(a, b));
 }
 
+// Vector at `base` of a raster token.
+template <typename P>
+__device__ __forceinline__ P at_token(P base, int flat, uint32_t stride) {
+  return base + (uint64_t)(uint32_t)flat * stride;
+}
+
 // Sums over the UPR lanes that share a row.
 template <int UPR, int K>
 __device__ __forceinline__ void row_sum(float (&v)[K]) {
@@ -176,141 +184,168 @@ __device__ __forceinline__ void row_sum(float (&v)[K]) {
 
 constexpr int kDepth = 3;   // heads in flight per CTA
 
-// BIAS: there may be one (a layer norm, or an RMS norm with a bias).
-template <typename T, int D, int GR, bool HALF, bool POOL, bool BIAS>
-__global__ void __launch_bounds__(Cfg<T, D, GR, HALF>::THREADS)
-norm_rope_fwd_kernel(const Fwd q, const Fwd k, const Tokens tk, const RopeArgs a, bool rms, float eps, bool out_blocked,
+// BIAS: there may be one (a layer norm, or an RMS norm with a bias). POOL: a CTA takes a whole
+// tile, granule after granule, and leaves its means: each warp keeps its columns' sums of every
+// head in shared memory, so that they are joined once, at the end.
+template <typename T, int D, int GR, bool HALF, bool POOL, bool BIAS, bool BLOCKED>
+__global__ void __launch_bounds__(Cfg<T, D, GR, HALF>::THREADS, Cfg<T, D, GR, HALF>::THREADS == 256 ? 2 : 1)
+norm_rope_fwd_kernel(const Fwd q, const Fwd k, const Tokens tk, const RopeArgs a, bool rms, float eps,
                      int heads_per_cta, int32_t* d_status) {
   using C = Cfg<T, D, GR, HALF>;
   using X = Unit<T, HALF>;
-  constexpr int E = C::E, P2 = C::P2;
-  __shared__ int4 tok[GR];
-  __shared__ float part[POOL ? 2 : 1][POOL ? C::THREADS / 32 : 1][POOL ? D : 1];   // per warp, its columns' sums
-  extern __shared__ uint4 ring[];   // [min(kDepth, heads)][U][NV][THREADS]
+  constexpr int E = C::E, P2 = C::P2, kWarps = C::THREADS / 32;
+  __shared__ int4 tok[POOL ? 128 : GR];
+  extern __shared__ uint4 ring[];   // [min(kDepth, steps)][U][NV][THREADS], then with POOL [heads][warps][D] floats
   const bool is_q = blockIdx.y < q.groups;
   const Fwd& t = is_q ? q : k;
-  const int h0 = (is_q ? blockIdx.y : blockIdx.y - q.groups) * heads_per_cta, h1 = min(t.heads, h0 + heads_per_cta);
-  const T* in = static_cast<const T*>(t.in);
-  T* out = static_cast<T*>(t.out);
-  locate<GR, C::THREADS>(tok, tk, a, d_status);
+  const int h0 = (is_q ? blockIdx.y : blockIdx.y - q.groups) * heads_per_cta, heads = min(t.heads - h0, heads_per_cta);
+  const int parts = POOL ? tk.bt / GR : 1, steps = parts * heads;   // a step: a granule of a head
+  float* sums = reinterpret_cast<float*>(ring + (size_t)kDepth * C::VECS);
+  locate<C::THREADS>(tok, parts * GR, tk, a, d_status);
   __syncthreads();
-  const int c0 = threadIdx.x % C::UPR, o0 = threadIdx.x / C::UPR;   // this thread's unit column, its first row
-  f32x2 cos[C::U][P2], sin[C::U][P2];
-  int flat[C::U];
-#pragma unroll
-  for (int u = 0; u < C::U; ++u) {
-    const int4 w = tok[o0 + u * C::kRowStep];
-    flat[u] = w.x;
-#pragma unroll
-    for (int i = 0; i < P2; ++i) {
-      const float2 p = turn_of(a, w, c0 * C::NP + 2 * i), q = turn_of(a, w, c0 * C::NP + 2 * i + 1);
-      cos[u][i] = pair(p.x, q.x);
-      sin[u][i] = pair(p.y, q.y);
-    }
-  }
+  const int c0 = threadIdx.x % C::UPR, o0 = threadIdx.x / C::UPR, warp = threadIdx.x >> 5;   // c0: unit column, o0: first row
   f32x2 wx[P2], wy[P2], bx[P2], by[P2];
   params<D, E, HALF, P2>(t.w, 1.f, c0, wx, wy);
   if (BIAS) params<D, E, HALF, P2>(t.b, 0.f, c0, bx, by);
-  // rows of tile order: those of head h of this granule's batch element start at blocked0(h)
+  // rows of tile order: those of head h of this CTA's batch element start at (batch * heads + h) * N + row0
   const int64_t N = tk.rm.N;
-  const int64_t at = (int64_t)blockIdx.x * GR, batch = at / N, row0 = at - batch * N;
+  const int64_t at = (int64_t)blockIdx.x * parts * GR, batch = at / N, row0 = at - batch * N;
   auto place = [&](int st, int u, int v) { return ring + ((st * C::U + u) * C::NV + v) * C::THREADS + threadIdx.x; };
-  auto fetch = [&](int h, int st) {
-    if (h < h1) {
+  const uint8_t* in0 = static_cast<const uint8_t*>(t.in) + ((int64_t)h0 * D + c0 * E) * sizeof(T);
+  const uint8_t* in = in0;                       // of the next fetch
+  int f_head = 0, f_part = 0, f_step = 0;        // of the next fetch
+  auto fetch = [&]() {
+    if (f_step < steps) {
+      const int st = f_step % kDepth;
 #pragma unroll
-      for (int u = 0; u < C::U; ++u)
-        if (flat[u] >= 0) {
-          const T* src = in + flat[u] * t.in_stride + (int64_t)h * D + c0 * E;
+      for (int u = 0; u < C::U; ++u) {
+        const int flat = tok[f_part * GR + o0 + u * C::kRowStep].x;
+        if (POOL || flat >= 0) {                 // a tile is whole
+          const uint8_t* src = at_token(in, flat, t.in_stride);
 #pragma unroll
-          for (int v = 0; v < C::NV; ++v) copy_async16(place(st, u, v), src + v * (D / 2));
+          for (int v = 0; v < C::NV; ++v) copy_async16(place(st, u, v), src + v * (D / 2) * sizeof(T));
         }
+      }
+      in += D * sizeof(T);
+      ++f_step;
+      if (++f_head == heads) {
+        f_head = 0;
+        ++f_part;
+        in = in0;
+      }
     }
     copy_commit();
   };
-  for (int s = 0; s < kDepth - 1; ++s) fetch(h0 + s, s);
+  for (int s = 0; s < kDepth - 1; ++s) fetch();
   int st = 0;
-  for (int h = h0; h < h1; ++h, st = st + 1 == kDepth ? 0 : st + 1) {
-    fetch(h + kDepth - 1, st == 0 ? kDepth - 1 : st - 1);   // the slots of the head before
-    copy_wait<kDepth - 1>();
-    f32x2 ax[P2], ay[P2];
-#pragma unroll
-    for (int i = 0; i < P2; ++i) ax[i] = ay[i] = 0;   // two zeros
+  for (int part = 0; part < parts; ++part) {
+    f32x2 cos[C::U][P2], sin[C::U][P2];
+    int flat[C::U];
 #pragma unroll
     for (int u = 0; u < C::U; ++u) {
-      f32x2 x[P2], y[P2];
-      uint4 v16[C::NV];
-#pragma unroll
-      for (int v = 0; v < C::NV; ++v) v16[v] = *place(st, u, v);
-      X::unpack(v16, x, y);
-      if (BIAS && !rms) {
-        float m[1] = {sum_of<P2>(x, y)};
-        row_sum<C::UPR>(m);
-        const f32x2 mean = pair(m[0] * (-1.0f / D), m[0] * (-1.0f / D));
-#pragma unroll
-        for (int i = 0; i < P2; ++i) {
-          x[i] = add2(x[i], mean);
-          y[i] = add2(y[i], mean);
-        }
-      }
-      float s[1] = {dot_of<P2>(x, y, x, y)};
-      row_sum<C::UPR>(s);
-      const float rstd = inv_sqrt(s[0] * (1.0f / D) + eps);
-      const f32x2 r2 = pair(rstd, rstd);
+      const int4 w = tok[part * GR + o0 + u * C::kRowStep];
+      flat[u] = w.x;
 #pragma unroll
       for (int i = 0; i < P2; ++i) {
-        x[i] = BIAS ? fma2(mul2(x[i], r2), wx[i], bx[i]) : mul2(mul2(x[i], r2), wx[i]);
-        y[i] = BIAS ? fma2(mul2(y[i], r2), wy[i], by[i]) : mul2(mul2(y[i], r2), wy[i]);
-      }
-      turn<P2>(x, y, cos[u], sin[u]);
-      if (POOL)
-#pragma unroll
-        for (int i = 0; i < P2; ++i) {
-          ax[i] = add2(ax[i], x[i]);
-          ay[i] = add2(ay[i], y[i]);
-        }
-      if (flat[u] >= 0) {
-        T* dst = out + (out_blocked ? ((batch * t.heads + h) * N + row0 + o0 + u * C::kRowStep) * D
-                                    : flat[u] * t.out_stride + (int64_t)h * D);
-        X::pack(x, y, v16);
-#pragma unroll
-        for (int v = 0; v < C::NV; ++v) __stcs(reinterpret_cast<uint4*>(dst + c0 * E + v * (D / 2)), v16[v]);
+        const float2 p = turn_of(a, w, c0 * C::NP + 2 * i), q2 = turn_of(a, w, c0 * C::NP + 2 * i + 1);
+        cos[u][i] = pair(p.x, q2.x);
+        sin[u][i] = pair(p.y, q2.y);
       }
     }
-    // the means of the fp32 values: summed per thread, over the lanes that share its
-    // columns, then over the warps in order
-    if constexpr (POOL) {
-      if (t.means == nullptr) continue;   // the same for the whole CTA
-      float (*sum)[D] = part[(h - h0) & 1];          // the other one may still be read
+    uint8_t* out = static_cast<uint8_t*>(t.out) +
+                   (BLOCKED ? ((batch * t.heads + h0) * N + row0 + part * GR + o0) * D + c0 * E
+                            : (int64_t)h0 * D + c0 * E) * sizeof(T);
+    const int64_t out_step = (BLOCKED ? N * D : (int64_t)D) * sizeof(T);
+    for (int h = 0; h < heads; ++h, st = st + 1 == kDepth ? 0 : st + 1) {
+      fetch();                                   // into the slots of the step before
+      copy_wait<kDepth - 1>();
+      f32x2 ax[P2], ay[P2];
 #pragma unroll
-      for (int i = 0; i < C::NP; ++i) {
-        const float2 px = both(ax[i / 2]), py = both(ay[i / 2]);
-        float vx = i & 1 ? px.y : px.x, vy = i & 1 ? py.y : py.x;
+      for (int i = 0; i < P2; ++i) ax[i] = ay[i] = 0;   // two zeros
 #pragma unroll
-        for (int off = 16; off >= C::UPR; off >>= 1) {
-          vx += __shfl_xor_sync(0xffffffffu, vx, off);
-          vy += __shfl_xor_sync(0xffffffffu, vy, off);
+      for (int u = 0; u < C::U; ++u) {
+        f32x2 x[P2], y[P2];
+        uint4 v16[C::NV];
+#pragma unroll
+        for (int v = 0; v < C::NV; ++v) v16[v] = *place(st, u, v);
+        X::unpack(v16, x, y);
+        if (BIAS && !rms) {
+          float m[1] = {sum_of<P2>(x, y)};
+          row_sum<C::UPR>(m);
+          const f32x2 mean = pair(m[0] * (-1.0f / D), m[0] * (-1.0f / D));
+#pragma unroll
+          for (int i = 0; i < P2; ++i) {
+            x[i] = add2(x[i], mean);
+            y[i] = add2(y[i], mean);
+          }
         }
-        if ((threadIdx.x & 31) < C::UPR) {
-          sum[threadIdx.x >> 5][col_x<D, E, HALF>(c0, i)] = vx;
-          sum[threadIdx.x >> 5][col_y<D, E, HALF>(c0, i)] = vy;
+        float s[1] = {dot_of<P2>(x, y, x, y)};
+        row_sum<C::UPR>(s);
+        const float rstd = inv_sqrt(s[0] * (1.0f / D) + eps);
+        const f32x2 r2 = pair(rstd, rstd);
+#pragma unroll
+        for (int i = 0; i < P2; ++i) {
+          x[i] = BIAS ? fma2(mul2(x[i], r2), wx[i], bx[i]) : mul2(mul2(x[i], r2), wx[i]);
+          y[i] = BIAS ? fma2(mul2(y[i], r2), wy[i], by[i]) : mul2(mul2(y[i], r2), wy[i]);
+        }
+        turn<P2>(x, y, cos[u], sin[u]);
+        if (POOL)
+#pragma unroll
+          for (int i = 0; i < P2; ++i) {
+            ax[i] = add2(ax[i], x[i]);
+            ay[i] = add2(ay[i], y[i]);
+          }
+        if (POOL || flat[u] >= 0) {
+          uint8_t* dst = BLOCKED ? out + u * C::kRowStep * D * sizeof(T) : at_token(out, flat[u], t.out_stride);
+          X::pack(x, y, v16);
+#pragma unroll
+          for (int v = 0; v < C::NV; ++v) __stcs(reinterpret_cast<uint4*>(dst + v * (D / 2) * sizeof(T)), v16[v]);
         }
       }
-      __syncthreads();
-      for (int c = threadIdx.x; c < D; c += C::THREADS) {
-        float s = 0.f;
+      out += out_step;
+      // the sums of the fp32 values: per thread, then over the lanes that share its columns, then over granules
+      if constexpr (POOL) {
+        if (t.means != nullptr) {                // the same for the whole CTA
+          float* mine = sums + (h * kWarps + warp) * D;
 #pragma unroll
-        for (int g = 0; g < C::THREADS / 32; ++g) s += sum[g][c];
-        t.means[((batch * t.heads + h) * (N / GR) + row0 / GR) * D + c] = s * (1.0f / (float)GR);
+          for (int i = 0; i < C::NP; ++i) {
+            const float2 px = both(ax[i / 2]), py = both(ay[i / 2]);
+            float vx = i & 1 ? px.y : px.x, vy = i & 1 ? py.y : py.x;
+#pragma unroll
+            for (int off = 16; off >= C::UPR; off >>= 1) {
+              vx += __shfl_xor_sync(0xffffffffu, vx, off);
+              vy += __shfl_xor_sync(0xffffffffu, vy, off);
+            }
+            if ((threadIdx.x & 31) < C::UPR) {
+              float& sx = mine[col_x<D, E, HALF>(c0, i)];
+              float& sy = mine[col_y<D, E, HALF>(c0, i)];
+              sx = part == 0 ? vx : sx + vx;
+              sy = part == 0 ? vy : sy + vy;
+            }
+          }
+        }
       }
     }
   }
   copy_wait<0>();
+  if constexpr (POOL) {
+    if (t.means == nullptr) return;
+    __syncthreads();
+    float* to = t.means + ((batch * t.heads + h0) * (N / tk.bt) + row0 / tk.bt) * D;
+    for (int i = threadIdx.x; i < heads * D; i += C::THREADS) {
+      const int h = i / D, c = i % D;
+      float s = 0.f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) s += sums[(h * kWarps + w) * D + c];   // the warps in order
+      to[(int64_t)h * (N / tk.bt) * D + c] = s * (1.0f / (float)tk.bt);
+    }
+  }
 }
 
 // Each CTA leaves its columns' sums in part [CTA of q, then of k][dw, db][D].
-template <typename T, int D, int GR, bool HALF, bool RMS>
-__global__ void __launch_bounds__(Cfg<T, D, GR, HALF>::THREADS)
-norm_rope_bwd_kernel(const Bwd q, const Bwd k, const Tokens tk, const RopeArgs a, float eps, bool in_blocked,
+template <typename T, int D, int GR, bool HALF, bool RMS, bool BLOCKED>
+__global__ void __launch_bounds__(Cfg<T, D, GR, HALF>::THREADS, !HALF && Cfg<T, D, GR, HALF>::THREADS == 256 ? 2 : 1)
+norm_rope_bwd_kernel(const Bwd q, const Bwd k, const Tokens tk, const RopeArgs a, float eps,
                      int heads_per_cta, float* __restrict__ part, int32_t* d_status) {
   using C = Cfg<T, D, GR, HALF>;
   using X = Unit<T, HALF>;
@@ -321,10 +356,7 @@ norm_rope_bwd_kernel(const Bwd q, const Bwd k, const Tokens tk, const RopeArgs a
   const Bwd& t = is_q ? q : k;
   const int group = is_q ? blockIdx.y : blockIdx.y - q.groups;
   const int h0 = group * heads_per_cta, h1 = min(t.heads, h0 + heads_per_cta);
-  const T* x = static_cast<const T*>(t.x);
-  const T* dy = static_cast<const T*>(t.dy);
-  T* dx = static_cast<T*>(t.dx);
-  locate<GR, C::THREADS>(tok, tk, a, d_status);
+  locate<C::THREADS>(tok, GR, tk, a, d_status);
   __syncthreads();
   const int c0 = threadIdx.x % C::UPR, o0 = threadIdx.x / C::UPR;
   f32x2 cos[C::U][P2], sin[C::U][P2];
@@ -349,20 +381,27 @@ norm_rope_bwd_kernel(const Bwd q, const Bwd k, const Tokens tk, const RopeArgs a
   auto place = [&](int st, int which, int u, int v) {
     return ring + (((st * 2 + which) * C::U + u) * C::NV + v) * C::THREADS + threadIdx.x;
   };
+  const int64_t col0 = ((int64_t)h0 * D + c0 * E) * sizeof(T);
+  const uint8_t* x = static_cast<const uint8_t*>(t.x) + col0;                                     // of the next fetch
+  const uint8_t* dy = static_cast<const uint8_t*>(t.dy) +
+                      (BLOCKED ? (((batch * t.heads + h0) * N + row0 + o0) * D + c0 * E) * (int64_t)sizeof(T) : col0);
+  const int64_t dy_step = (BLOCKED ? N * D : (int64_t)D) * sizeof(T);
+  uint8_t* dx = static_cast<uint8_t*>(t.dx) + col0;                                               // of the next store
   auto fetch = [&](int h, int st) {
     if (h < h1) {
 #pragma unroll
       for (int u = 0; u < C::U; ++u)
         if (flat[u] >= 0) {
-          const T* sx = x + flat[u] * t.x_stride + (int64_t)h * D + c0 * E;
-          const T* sy = dy + (in_blocked ? ((batch * t.heads + h) * N + row0 + o0 + u * C::kRowStep) * D
-                                         : flat[u] * t.dy_stride + (int64_t)h * D) + c0 * E;
+          const uint8_t* sx = at_token(x, flat[u], t.x_stride);
+          const uint8_t* sy = BLOCKED ? dy + u * C::kRowStep * D * sizeof(T) : at_token(dy, flat[u], t.dy_stride);
 #pragma unroll
           for (int v = 0; v < C::NV; ++v) {
-            copy_async16(place(st, 0, u, v), sx + v * (D / 2));
-            copy_async16(place(st, 1, u, v), sy + v * (D / 2));
+            copy_async16(place(st, 0, u, v), sx + v * (D / 2) * sizeof(T));
+            copy_async16(place(st, 1, u, v), sy + v * (D / 2) * sizeof(T));
           }
         }
+      x += D * sizeof(T);
+      dy += dy_step;
     }
     copy_commit();
   };
@@ -424,12 +463,13 @@ norm_rope_bwd_kernel(const Bwd q, const Bwd k, const Tokens tk, const RopeArgs a
         uy[i] = mul2(fma2(fy[i], n1, uy[i]), r2);
       }
       if (live) {
-        T* dst = dx + flat[u] * t.dx_stride + (int64_t)h * D + c0 * E;
+        uint8_t* dst = at_token(dx, flat[u], t.dx_stride);
         X::pack(ux, uy, v16);
 #pragma unroll
-        for (int v = 0; v < C::NV; ++v) __stcs(reinterpret_cast<uint4*>(dst + v * (D / 2)), v16[v]);
+        for (int v = 0; v < C::NV; ++v) __stcs(reinterpret_cast<uint4*>(dst + v * (D / 2) * sizeof(T)), v16[v]);
       }
     }
+    dx += D * sizeof(T);
   }
   copy_wait<0>();
   if (t.dw == nullptr && t.db == nullptr) return;
@@ -500,31 +540,35 @@ constexpr int granule() { return sizeof(T) == 4 ? 32 : 64; }
 
 int64_t granules_of(const Dims& s, int gr) { return ((int64_t)s.B * s.N + gr - 1) / gr; }
 
-template <typename T, int D, int GR, bool HALF, bool POOL>
+template <typename T, int D, bool HALF, bool POOL>
 bool go_fwd(const Dims& s, const RopeArgs& a, Fwd q, Fwd k, const Tokens& tk, bool rms, float eps, bool out_blocked,
             int32_t* d_status, cudaStream_t st) {
+  constexpr int GR = granule<T>();
   using C = Cfg<T, D, GR, HALF>;
-  const int64_t granules = granules_of(s, GR);
+  const int64_t granules = granules_of(s, POOL ? s.Bt : GR);
   const int hpc = heads_per_cta(granules, q.heads + k.heads);
   q.groups = (q.heads + hpc - 1) / hpc;
   k.groups = (k.heads + hpc - 1) / hpc;
-  const size_t smem = (size_t)(hpc < kDepth ? hpc : kDepth) * C::VECS * 16;
+  const int steps = hpc * (POOL ? s.Bt / GR : 1);
+  const size_t smem = POOL ? (size_t)kDepth * C::VECS * 16 + (size_t)hpc * C::THREADS / 32 * D * sizeof(float)
+                           : (size_t)(steps < kDepth ? steps : kDepth) * C::VECS * 16;
   const bool bias = !rms || q.b != nullptr || k.b != nullptr;
-  auto kern = bias ? norm_rope_fwd_kernel<T, D, GR, HALF, POOL, true> : norm_rope_fwd_kernel<T, D, GR, HALF, POOL, false>;
+  auto kern = out_blocked ? (bias ? norm_rope_fwd_kernel<T, D, GR, HALF, POOL, true, true>
+                                  : norm_rope_fwd_kernel<T, D, GR, HALF, POOL, false, true>)
+                          : (bias ? norm_rope_fwd_kernel<T, D, GR, HALF, POOL, true, false>
+                                  : norm_rope_fwd_kernel<T, D, GR, HALF, POOL, false, false>);
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) return false;
-  kern<<<dim3((unsigned)granules, (unsigned)(q.groups + k.groups)), C::THREADS, smem, st>>>(q, k, tk, a, rms, eps, out_blocked,
-                                                                                           hpc, d_status);
+  kern<<<dim3((unsigned)granules, (unsigned)(q.groups + k.groups)), C::THREADS, smem, st>>>(q, k, tk, a, rms, eps, hpc,
+                                                                                           d_status);
   return true;
 }
 
 template <typename T, int D, bool HALF>
-bool go_fwd_granule(const Dims& s, const RopeArgs& a, const Fwd& q, const Fwd& k, const Tokens& tk, bool rms, float eps,
-                    bool out_blocked, int32_t* d_status, cudaStream_t st) {
-  if (q.means != nullptr || k.means != nullptr) {   // means take a whole tile
-    if (s.Bt == 64) return go_fwd<T, D, 64, HALF, true>(s, a, q, k, tk, rms, eps, out_blocked, d_status, st);
-    return go_fwd<T, D, 128, HALF, true>(s, a, q, k, tk, rms, eps, out_blocked, d_status, st);
-  }
-  return go_fwd<T, D, granule<T>(), HALF, false>(s, a, q, k, tk, rms, eps, out_blocked, d_status, st);
+bool go_fwd_pool(const Dims& s, const RopeArgs& a, const Fwd& q, const Fwd& k, const Tokens& tk, bool rms, float eps,
+                 bool out_blocked, int32_t* d_status, cudaStream_t st) {
+  if (q.means != nullptr || k.means != nullptr)
+    return go_fwd<T, D, HALF, true>(s, a, q, k, tk, rms, eps, out_blocked, d_status, st);
+  return go_fwd<T, D, HALF, false>(s, a, q, k, tk, rms, eps, out_blocked, d_status, st);
 }
 
 template <typename T, int D, bool HALF>
@@ -539,9 +583,12 @@ bool go_bwd(const Dims& s, const RopeArgs& a, Bwd q, Bwd k, const Tokens& tk, bo
   size_t smem = (size_t)(hpc < kDepth ? hpc : kDepth) * 2 * C::VECS * 16;
   const size_t sums = (size_t)C::THREADS / 32 * 2 * D * 4;
   if (smem < sums) smem = sums;
-  auto kern = rms ? norm_rope_bwd_kernel<T, D, GR, HALF, true> : norm_rope_bwd_kernel<T, D, GR, HALF, false>;
+  auto kern = in_blocked ? (rms ? norm_rope_bwd_kernel<T, D, GR, HALF, true, true>
+                                : norm_rope_bwd_kernel<T, D, GR, HALF, false, true>)
+                         : (rms ? norm_rope_bwd_kernel<T, D, GR, HALF, true, false>
+                                : norm_rope_bwd_kernel<T, D, GR, HALF, false, false>);
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) return false;
-  kern<<<dim3((unsigned)granules, (unsigned)(q.groups + k.groups)), C::THREADS, smem, st>>>(q, k, tk, a, eps, in_blocked, hpc,
+  kern<<<dim3((unsigned)granules, (unsigned)(q.groups + k.groups)), C::THREADS, smem, st>>>(q, k, tk, a, eps, hpc,
                                                                                            part, d_status);
   if (q.dw != nullptr || q.db != nullptr || k.dw != nullptr || k.db != nullptr)
     norm_rope_sum_kernel<D><<<dim3(2 * D / 32, k.heads > 0 ? 2 : 1), 1024, 0, st>>>(part, granules * q.groups,
@@ -572,15 +619,16 @@ sparsp_status_t launch_norm_rope_fwd(const Dims& s, bool tiles, const sparsp_rop
                                      cudaStream_t st) {
   RopeArgs a = rope_args(r, table);
   a.pos = pos;
-  auto part = [](const sparsp_norm_rope_t& t) {
-    return Fwd{t.x, t.x_stride, t.out, t.out_stride, t.w, t.b, t.means, t.heads, 0};
+  const int64_t e = s.elem;
+  auto part = [e](const sparsp_norm_rope_t& t) {
+    return Fwd{t.x, (uint32_t)(t.x_stride * e), t.out, (uint32_t)(t.out_stride * e), t.w, t.b, t.means, t.heads, 0};
   };
   const Tokens tk = tokens_of(s, tiles);
   const Fwd fq = part(q), fk = part(k);
   bool ok;
 #define SPARSP_GO(T, D)                                                                             \
-  ok = r.half ? go_fwd_granule<T, D, true>(s, a, fq, fk, tk, rms, eps, out_blocked, d_status, st)   \
-              : go_fwd_granule<T, D, false>(s, a, fq, fk, tk, rms, eps, out_blocked, d_status, st)
+  ok = r.half ? go_fwd_pool<T, D, true>(s, a, fq, fk, tk, rms, eps, out_blocked, d_status, st)   \
+              : go_fwd_pool<T, D, false>(s, a, fq, fk, tk, rms, eps, out_blocked, d_status, st)
   if (s.dtype == SPARSP_F32 && s.d == 64) SPARSP_GO(float, 64);
   else if (s.dtype == SPARSP_F32) SPARSP_GO(float, 128);
   else if (s.d == 64) SPARSP_GO(__nv_bfloat16, 64);
@@ -598,8 +646,10 @@ sparsp_status_t launch_norm_rope_bwd(const Dims& s, bool tiles, const sparsp_rop
   RopeArgs a = rope_args(r, table);
   a.pos = pos;
   a.sign = -1.f;
-  auto part = [](const sparsp_norm_rope_t& t) {
-    return Bwd{t.dy, t.x, t.dy_stride, t.x_stride, t.out, t.out_stride, t.w, t.dw, t.db, t.heads, 0};
+  const int64_t e = s.elem;
+  auto part = [e](const sparsp_norm_rope_t& t) {
+    return Bwd{t.dy, t.x, (uint32_t)(t.dy_stride * e), (uint32_t)(t.x_stride * e), t.out, (uint32_t)(t.out_stride * e),
+               t.w, t.dw, t.db, t.heads, 0};
   };
   const Tokens tk = tokens_of(s, tiles);
   const Bwd bq = part(q), bk = part(k);

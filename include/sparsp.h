@@ -576,7 +576,8 @@ SPARSP_API sparsp_status_t sparsp_rope(const sparsp_shape_t* shape, const sparsp
  * k; q->heads = shape->H; k NULL: q alone. The shape's tile counts only with tile order
  * or means; without them any number of tokens up to 2^31 - 1 is taken (T = tokens, Y =
  * X = 1), e.g. the new tokens of many requests, with their positions in pos. rope,
- * table, pos and d_status as in sparsp_rope, eps and strides as in sparsp_norm_fwd.
+ * table, pos and d_status as in sparsp_rope, eps and strides as in sparsp_norm_fwd (strides
+ * below 2^32 bytes, else SPARSP_ERR_UNSUPPORTED).
  * The byte range of neither out may overlap that of an input; the two outs may be
  * slices of one wider tensor.
  */

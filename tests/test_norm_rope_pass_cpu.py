@@ -59,6 +59,7 @@ def call(lib, name="fwd", s=None, flags=0, eps=1e-6, rope=None, table=FAKE - 409
     (dict(k=part(1, x=FAKE + 8)), sp.ALIGN), (dict(k=part(1, w=FAKE + 8)), sp.ALIGN),
     (dict(q=part(0, x_stride=64)), sp.SHAPE), (dict(q=part(0, x_stride=132)), sp.ALIGN),
     (dict(q=part(0, out_stride=-128)), sp.SHAPE), (dict(k=part(1, out_stride=1 << 61)), sp.SHAPE),
+    (dict(q=part(0, x_stride=1 << 31)), sp.UNSUPPORTED),
     (dict(q=part(0, out=FAKE)), sp.INVALID_ARG),                                      # in place
     (dict(k=part(1, out=FAKE + 1024)), sp.INVALID_ARG),                               # k's result over q
     (dict(k=part(1, out=FAKE + 2 * GAP)), sp.INVALID_ARG),                            # both results in one place
