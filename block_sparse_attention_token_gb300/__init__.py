@@ -224,6 +224,9 @@ def _refuse(name: str, t, what: str):
 def _want(name: str, t, dims, dtype, dev: int, optional: bool = False):
     """Address of a tensor argument of the calls below: contiguous, on device dev
     (the current one), of this shape and dtype. A plain address is passed through."""
+    if (t.__class__ is torch.Tensor and t.dtype is dtype and t.shape == dims and t.get_device() == dev
+            and t.is_contiguous()):
+        return t.data_ptr()
     if t is None and optional or isinstance(t, int):
         return t
     if (not isinstance(t, torch.Tensor) or t.shape != dims or t.dtype is not dtype or t.get_device() != dev

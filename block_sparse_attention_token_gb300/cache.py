@@ -84,12 +84,13 @@ def cache_extend(shape: CacheShape, length, add, free, table, tokens: int, used=
 def _rows(name: str, t, heads: int, d: int, dev: int, n: int | None = None) -> tuple:
     """(address, elements between tokens, between heads) of rows [tokens, heads, d] whose
     columns are contiguous."""
-    if (not isinstance(t, torch.Tensor) or t.dim() != 3 or tuple(t.shape[1:]) != (heads, d) or t.get_device() != dev
-            or n is not None and t.shape[0] != n or t.numel() and t.stride(2) != 1):
+    if not isinstance(t, torch.Tensor) or t.dim() != 3 or t.get_device() != dev:
+        _refuse(name, t, f"a [tokens, {heads}, {d}] tensor")
+    shape, st = t.shape, t.stride()
+    if shape[1] != heads or shape[2] != d or n is not None and shape[0] != n or shape[0] and st[2] != 1:
         _refuse(name, t, f"a [tokens, {heads}, {d}] tensor with contiguous columns")
     # a stride over a single token or head says nothing
-    ts, hs = t.stride(0) if t.shape[0] > 1 else 0, t.stride(1) if heads > 1 else 0
-    return t.data_ptr(), ts, hs
+    return t.data_ptr(), st[0] if shape[0] > 1 else 0, st[1] if heads > 1 else 0
 
 
 def cache_write(pool: CachePool, k, v, slots, status=None, stream=None) -> None:

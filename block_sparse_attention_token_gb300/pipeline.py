@@ -29,7 +29,8 @@ import torch
 from . import (EST_LOWRANK, EST_MEAN, PROF_SLOTS, Shape, attn_bwd, attn_fwd, attn_launches, attn_workspace_size, augment,
                augment_workspace_size, balance_heads, Balance, predictor_fit,
                attn_masked_bwd, attn_masked_compacts, attn_masked_fwd, attn_masked_workspace_size, LISTS_SEEN, MaskPlan,
-               mask_csr, mask_scores, norm_bwd, norm_fwd, norm_workspace_size, rope as rope_turn, RopeTable,
+               mask_csr, mask_scores, norm_bwd, norm_fwd, norm_rope_bwd, norm_rope_fwd, norm_rope_workspace_size,
+               norm_workspace_size, rope as rope_turn, RopeTable,
                block_scores, block_scores_pooled, block_scores_workspace_size, kv_demand, kv_gather, lib, placement,
                placement_workspace_size, reorder, reorder_pool, select, select_workspace_size, DemandOut,
                OUT_RASTER, IN_RASTER, pool_means, _whole)
@@ -39,7 +40,9 @@ from . import (EST_LOWRANK, EST_MEAN, PROF_SLOTS, Shape, attn_bwd, attn_fwd, att
 class QKNorm:
     """Token norm of Q and of K in a Pipeline: layer norm, or RMS norm with rms, over
     the H*d values of a token, or over each head's d values with per_head. Weights
-    and biases are float32 [H*d] or [d], or None; they are read at every forward()."""
+    and biases are float32 [H*d] or [d], or None; they are read at every forward(). one_pass
+    (with per_head and a rotation): norm and rotation of Q and K in one kernel, rounded once
+    and not between the two."""
     q_weight: torch.Tensor | None = None
     k_weight: torch.Tensor | None = None
     q_bias: torch.Tensor | None = None
@@ -47,6 +50,7 @@ class QKNorm:
     eps: float = 1e-6
     rms: bool = False
     per_head: bool = False
+    one_pass: bool = False
 
 
 class Pipeline:
@@ -55,7 +59,7 @@ class Pipeline:
         return self.flags | (OUT_RASTER if self.raster_out else 0) | (LISTS_SEEN if seen else 0)
 
     def kernels_per_forward(self) -> int:
-        """Kernels forward() launches: norm of Q and K (2) when there is one, reorder x3
+        """Kernels forward() launches: norm of Q and K (2, or 1 with the rotation in one pass) when there is one, reorder x3
         (the rotation is in that pass; with raster inputs a rotation or pooling pass over Q and K
         each), pool + product, masked scores (1) and lists (3) under a mask, select x3 (count,
         scan, fill), predictor fitting x7 when enabled, balancing (1) and augmentation x14 (keys, slack, four
@@ -69,6 +73,8 @@ class Pipeline:
         # projection, two score products, gradient products, loss (partials, sum), weight gradients
         pred = 7 if self.predictor_lr is not None else 0
         tiles = (2 if self.norm is not None else 0) + (2 if self.raster_in else 3)
+        if self.one_pass:
+            tiles = 1 + (0 if self.raster_in else 1)
         masked = 4 if self.mask is not None else 0
         attn = attn_launches(self.shape, False, self.mask is not None, self.cap, self._attn_flags())
         return tiles + scores + masked + pred + 3 + bal + place + 4 + gather + attn + (0 if self.raster_out else 1)
@@ -78,6 +84,8 @@ class Pipeline:
         each (no reorder when the backward writes raster gradients) and an inverse reorder of dV
         (likewise), norm backward (gradient, weights' sums) of Q and K."""
         attn = attn_launches(self.shape, True, self.mask is not None, self.cap, self._attn_flags())
+        if self.one_pass:   # gradient and weights' sums of Q and K, reorder of dV
+            return 1 + attn + 2 + (0 if self.raster_out else 1)
         back = (2 if self.rope is not None or not self.raster_out else 0) + (0 if self.raster_out else 1)
         return 1 + attn + back + (4 if self.norm is not None else 0)
 
@@ -117,8 +125,11 @@ class Pipeline:
         self.raster_in = raster_inputs
         self.norm, self.rope, self.rope_pos, self.mask, self.cap = norm, rope, rope_pos, mask, float(cap)
         raster = (s.B, s.N, s.H, s.d)
+        self.one_pass = norm is not None and norm.one_pass
+        if self.one_pass and (not norm.per_head or rope is None):
+            raise ValueError("norm and rotation in one pass need a norm per head and a rotation")
         self.qn = self.kn = self.qr = self.kr = None       # normed, and normed and turned, raster Q and K
-        if norm is not None:
+        if norm is not None and not self.one_pass:
             self.qn, self.kn = (torch.empty(raster, dtype=dt, device=dev) for _ in range(2))
             stat = raster[:3] if norm.per_head else raster[:2]
             self.norm_stats = [(None if norm.rms else torch.empty(stat, dtype=torch.float32, device=dev),
@@ -227,7 +238,7 @@ class Pipeline:
             self._g_attn = [torch.empty(raster, dtype=dt, device=dev) for _ in range(2)] \
                 if self.raster_out and (norm is not None or rope is not None) else None
             self._g_rope = [torch.empty(raster, dtype=dt, device=dev) for _ in range(2)] \
-                if norm is not None and (rope is not None or not self.raster_out) else None
+                if norm is not None and not self.one_pass and (rope is not None or not self.raster_out) else None
             self.norm_grads = None
             if norm is not None:
                 cols = s.d if norm.per_head else s.H * s.d
@@ -236,8 +247,8 @@ class Pipeline:
                 self.norm_grads = {x: mk() for x in ("q_weight", "k_weight")}
                 if not norm.rms or norm.q_bias is not None or norm.k_bias is not None:
                     self.norm_grads.update({x: mk() for x in ("q_bias", "k_bias")})
-                self.ws_norm = torch.empty(max(norm_workspace_size(s, norm.rms, norm.per_head), 16), dtype=torch.uint8,
-                                           device=dev)
+                n_ws = norm_rope_workspace_size(s, s.H) if self.one_pass else norm_workspace_size(s, norm.rms, norm.per_head)
+                self.ws_norm = torch.empty(max(n_ws, 16), dtype=torch.uint8, device=dev)
 
     def forward(self, q, k, v, wq=None, wk=None, prof: bool = False, mark=None, out=None, before=None):
         """mark: optional callable(stage_name, stream=None) invoked after each
@@ -275,10 +286,18 @@ class Pipeline:
                 reorder(s, x, blocked)
             return blocked
 
-        n, st = self.norm or QKNorm(), self.norm_stats if self.norm is not None else (None, None)
         self._qk_in = (q, k) if self.norm is not None else None
-        aq = prepared("q", q, self.qn, st[0], n.q_weight, n.q_bias, self.qr, self.qb, self.qmeans)
-        ak = prepared("k", k, self.kn, st[1], n.k_weight, n.k_bias, self.kr, self.kb, self.kmeans)
+        if self.one_pass:
+            n, tiles = self.norm, not self.raster_in
+            before("q")
+            before("k")
+            aq, ak = norm_rope_fwd(s, self.rope, q, k, n.q_weight, n.k_weight, n.q_bias, n.k_bias, n.eps, n.rms,
+                                   self.rope_pos, self.qb if tiles else self.qr, self.kb if tiles else self.kr, tiles,
+                                   self.qmeans if self.fused else None, self.kmeans if self.fused else None, self.status)
+        else:
+            n, st = self.norm or QKNorm(), self.norm_stats if self.norm is not None else (None, None)
+            aq = prepared("q", q, self.qn, st[0], n.q_weight, n.q_bias, self.qr, self.qb, self.qmeans)
+            ak = prepared("k", k, self.kn, st[1], n.k_weight, n.k_bias, self.kr, self.kb, self.kmeans)
         if not self.raster_in:
             before("v")
             reorder(s, v, self.vb)
@@ -411,6 +430,17 @@ class Pipeline:
             mark("attn_bwd")
             gq, gk = self.dqb, self.dkb
         # dQ and dK back through the rotation (and to raster order), then through the norm
+        if self.one_pass:
+            n, grads = self.norm, self.norm_grads
+            names = ("q", "k")
+            norm_rope_bwd(s, self.rope, gq, gk, *self._qk_in, n.q_weight, n.k_weight, n.eps, n.rms, self.rope_pos,
+                          not self.raster_out, dq, dk, [grads[x + "_weight"] for x in names],
+                          [grads.get(x + "_bias") for x in names], self.ws_norm, self.status)
+            if not self.raster_out:
+                reorder(s, self.dvb, dv, inverse=True)
+                mark("reorder_grads")
+            mark("norm_bwd")
+            return dq, dk, dv
         g_in = (gq, gk)
         g_out = (dq, dk) if self.norm is None else (self._g_rope or g_in)
         for g, to in zip(g_in, g_out):
