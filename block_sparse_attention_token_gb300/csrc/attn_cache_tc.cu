@@ -14,24 +14,25 @@
 // so that blocks of any scales add up in one accumulator; P is at most 2^15 (R follows when
 // it is passed by more than 2^4) and not below 2^-24 f16 has nothing to add.
 //
-// A CTA per SM works on 256 query rows (heads that share a key head, and tokens, side by
-// side) as two tiles of 128: while the softmax of one tile runs, the products of the other
-// keep the tensor cores busy, and both read the same K and V from shared memory. Work is counted in
+// Two SMs work on 256 query rows (heads that share a key head, and tokens, side by side) as one
+// cluster of two CTAs with paired products (cta_group::2): each has 128 of the rows in its tensor memory, and
+// each loads one half of K's keys and of V's columns, so that every byte of the cache is loaded and widened once
+// for 256 rows, and shared memory is read half as often as with a tile to each SM. Work is counted in
 // stages of 128 keys over all items (request, key head, 256 rows) and dealt out evenly;
-// an item in several CTAs leaves partial sums that a second kernel joins in order.
-//   warps 0-7, 8-15: softmax and epilogue of tiles 0 and 1, two threads to a row (= TMEM lane), one for
-//              each half of a stage's keys (and of the columns of Q and O); the two exchange their
-//              largest score. At an item's start they also split its queries into shared memory.
-//   warps 16-19: widen V, zeros past a request's last token (what lies there may be anything).
-//   warp 20: producer: items, look-ups of lists and tables (32 at a time, a batch ahead),
-//              K by TMA boxes of 64 keys, V by bulk copies.
-//   warp 21: issues S of both tiles (A = q1, q2, B = K, K-major, from shared memory).
-//   warp 22: issues O += P V (A = P in TMEM, written over the S it is made of, B = V MN-major).
-// TMEM (512 columns): S and then P of the tiles [0, 256) (P of a half stage over the scores it is
-// made of), O [256, 512).
-// Every mbarrier wait is bounded (2 s); on expiry the CTA sets SPARSP_ERR_TIMEOUT, all roles
+// an item in several clusters leaves partial sums that a second kernel joins in order.
+//   warps 0-7: softmax and epilogue of the CTA's rows, two threads to a row (= TMEM lane), one for each
+//              half of a stage's keys (and of the columns of Q and O); the two exchange their largest
+//              score. At an item's start they also split its queries into shared memory.
+//   warps 8-11: widen V, zeros past a request's last token (what lies there may be anything).
+//   warp 12: producer: items, look-ups of lists and tables (32 at a time, a batch ahead), and TMA: 64 keys
+//              of K, half of the columns of V.
+//   warp 13, first CTA: issues S of both (A = q1, q2, B = K, K-major, from shared memory).
+//   warp 14, first CTA: issues O += P V (A = P in TMEM, B = V MN-major).
+// TMEM (512 columns): S of two stages [0, 256), O [256, 256 + d), P of two stages [384, 512).
+// The first CTA's barriers count what its products wait for in both CTAs (remote arrivals); its commits
+// reach both. Every mbarrier wait is bounded (2 s); on expiry the CTA sets SPARSP_ERR_TIMEOUT, all roles
 // leave their loops, copies and MMAs in flight are drained with a second bounded wait, and
-// TMEM is released.
+// TMEM is released when both CTAs are done.
 #include <cuda_fp16.h>
 
 #include "cache_items.cuh"
@@ -44,18 +45,18 @@ using namespace tc;
 
 constexpr int kTileRows = 128, kItemRows = 2 * kTileRows, kStageKeys = 128;
 constexpr int kItemCost = 6;       // stages that an item's own work counts as
-constexpr int kMinStages = 10;     // stages, an item's own among them, that are worth a CTA
+constexpr int kMinStages = 10;     // stages, an item's own among them, that are worth a cluster
 constexpr float kShift = 11.f, kMoves = 4.f;   // P is held as 2^11 times what it is against R
-constexpr int kNK = 3, kNV = 2, kNW = 2, kNInfo = 8, kNItems = 2;
+constexpr int kNK = 6, kNV = 4, kNW = 3, kNInfo = 16, kNItems = 2;
 constexpr uint64_t kWaitNs = 2000000000ull, kDrainNs = 200000000ull;
+constexpr int kSoftmax = 8, W_WIDEN = kSoftmax, W_PROD = W_WIDEN + 4, W_S = W_PROD + 1, W_PV = W_PROD + 2;   // warps
 
-constexpr int kSoftmax = 16, W_WIDEN = kSoftmax, W_PROD = W_WIDEN + 4, W_S = W_PROD + 1, W_PV = W_PROD + 2;   // warps
-
+// First CTA: K_FULL, W_FULL, Q_FULL, S_FREE, P_FULL and O_EMPTY count both CTAs.
 enum Bars {
   K_FULL, K_EMPTY = K_FULL + kNK, V_FULL = K_EMPTY + kNK, V_EMPTY = V_FULL + kNV, W_FULL = V_EMPTY + kNV,
   W_EMPTY = W_FULL + kNW, INFO = W_EMPTY + kNW, I_FULL = INFO + kNInfo, I_EMPTY = I_FULL + kNItems,
-  Q_FULL = I_EMPTY + kNItems, S_FULL = Q_FULL + 2, P_FULL = S_FULL + 2, PV_DONE = P_FULL + 2, O_EMPTY = PV_DONE + 2,
-  TEAR = O_EMPTY + 2, TEAR_PV, NBAR
+  Q_FULL = I_EMPTY + kNItems, S_FULL, S_FREE = S_FULL + 2, P_FULL = S_FREE + 2, PV_DONE = P_FULL + 2,
+  O_EMPTY = PV_DONE + 2, TEAR, TEAR_PV, NBAR
 };
 
 // A piece of an item: stages [e0, e1) of it. e1 < 0: no more.
@@ -71,19 +72,19 @@ struct Info {
 
 template <int D>
 struct Cfg {
-  static constexpr int THREADS = 768;
-  static constexpr uint32_t kRegSoftmax = 88, kRegAux = 64;
-  static_assert(512 * kRegSoftmax + 256 * kRegAux == THREADS * 80, "register split of the six warpgroups");
-  static constexpr uint32_t kQ = kTileRows * D, kK = kStageKeys * D, kV = kStageKeys * D;      // bytes: q1 or q2, K, V
-  static constexpr uint32_t kW = kStageKeys * D * 2, kWBox = kStageKeys * 128;                 // V in f16, 64 columns of it
-  static constexpr uint32_t kOffK = 4 * kQ, kOffV = kOffK + kNK * kK, kOffW = kOffV + kNV * kV;
+  static constexpr int THREADS = 512;
+  static constexpr uint32_t kRegSoftmax = 176, kRegAux = 80;
+  static_assert(256 * (kRegSoftmax + kRegAux) == THREADS * 128, "register split of the four warpgroups");
+  // bytes: q1 or q2; half of a stage's K; half of its V's columns, raw and in f16
+  static constexpr uint32_t kQ = kTileRows * D, kK = kUnit * D, kV = kStageKeys * D / 2, kW = kStageKeys * D;
+  static constexpr uint32_t kOffK = 2 * kQ, kOffV = kOffK + kNK * kK, kOffW = kOffV + kNV * kV;
   static constexpr uint32_t kOffBar = kOffW + kNW * kW, kOffInfo = kOffBar + 8 * NBAR;
   static constexpr uint32_t kOffPiece = kOffInfo + kNInfo * (uint32_t)sizeof(Info);
-  static constexpr uint32_t kOffEx = kOffPiece + kNItems * (uint32_t)sizeof(Piece);   // [2][tile][half][row] floats
-  static constexpr uint32_t kOffMisc = kOffEx + 2 * 2 * 2 * kTileRows * 4;
+  static constexpr uint32_t kOffEx = kOffPiece + kNItems * (uint32_t)sizeof(Piece);   // [2][half][row] floats
+  static constexpr uint32_t kOffMisc = kOffEx + 2 * 2 * kTileRows * 4;
   static constexpr uint32_t kSmem = kOffMisc + 64 + 1024;   // + alignment slack
-  static_assert(kSmem <= 232448, "shared memory");
-  // K-major rows of D bytes: 128-byte swizzle, or with D = 64 the 64-byte one
+  static_assert(kSmem <= 232448 && kOffMisc % 8 == 0, "shared memory");
+  // K-major rows of D bytes, and V's rows of D / 2 columns in f16: 128-byte swizzle, or with D = 64 the 64-byte one
   static constexpr uint32_t kSwz = D == 128 ? kSwizzle128B : 4u, kAtom = 8 * D;
   // the 16-byte vector c of row r
   static __device__ __forceinline__ uint32_t at(int r, int c) {
@@ -91,16 +92,83 @@ struct Cfg {
   }
 };
 
-// Instruction descriptors: f32 += e4m3 e4m3, both K-major; f32 += f16 f16, B MN-major.
+// Instruction descriptors of 256 rows: f32 += e4m3 e4m3, both K-major; f32 += f16 f16, B MN-major.
 __host__ __device__ constexpr uint32_t idesc(int N, int b_mn) {
-  return (1u << 4) | ((uint32_t)b_mn << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
+  return (1u << 4) | ((uint32_t)b_mn << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(256 >> 4) << 24);
 }
 
+// Products of the pair: A, B and D lie at the same addresses in both CTAs.
 __device__ __forceinline__ void mma_8bit(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t id, uint32_t accumulate) {
   asm volatile(
       "{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
-      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
+      "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
       "l"(a_desc), "l"(b_desc), "r"(id), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void mma_f16(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t id, uint32_t accumulate) {
+  asm volatile(
+      "{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(id), "r"(accumulate)
+      : "memory");
+}
+// Arrives on the barrier at this address in both CTAs (one: in this one) when all earlier products of this
+// thread are done.
+__device__ __forceinline__ void commit_both(uint32_t bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n" ::"r"(bar),
+      "h"((uint16_t)3)
+      : "memory");
+}
+__device__ __forceinline__ void commit_one(uint32_t bar) {
+  asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];\n" ::"r"(bar) : "memory");
+}
+// The address of this CTA's shared memory as the first CTA has it.
+__device__ __forceinline__ uint32_t in_first(uint32_t addr) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, 0;\n" : "=r"(r) : "r"(addr));
+  return r;
+}
+__device__ __forceinline__ void arrive_cluster(uint32_t cluster_bar) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];\n" ::"r"(cluster_bar) : "memory");
+}
+__device__ __forceinline__ bool try_wait_cluster(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n.reg .pred p;\nmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\nselp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+// As wait_warp, for barriers that the other CTA arrives on.
+__device__ __forceinline__ bool wait_pair(uint32_t bar, uint32_t parity, const Guard& g) {
+  bool ok = try_wait_cluster(bar, parity);
+  if (!ok) {
+    const uint64_t t0 = globaltimer_ns();
+    for (uint32_t it = 1; !ok; ++it) {
+      ok = try_wait_cluster(bar, parity);
+      if (!ok && (it & 63u) == 0) {
+        if (*g.abort) break;
+        if (globaltimer_ns() - t0 > g.limit_ns) {
+          *g.abort = 1;
+          report(g.d_status, SPARSP_ERR_TIMEOUT);
+          break;
+        }
+      }
+    }
+  }
+  return __all_sync(0xffffffffu, ok);
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;\n" ::: "memory");
+}
+// A TMA box into this CTA's shared memory whose bytes count on a barrier of either CTA.
+__device__ __forceinline__ void tma_pair(uint32_t dst, const CUtensorMap* map, uint32_t cluster_bar, int x, int y, int z) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], "
+      "[%2];\n" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(cluster_bar), "r"(x), "r"(y), "r"(z)
       : "memory");
 }
 __device__ __forceinline__ void fence_async_shared() { asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory"); }
@@ -165,8 +233,9 @@ struct Walk {
 };
 
 template <int D>
-__global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
-attn_cache_tc_kernel(const __grid_constant__ CUtensorMap tk, const CacheAttn a, const Parts parts) {
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<D>::THREADS, 1)
+attn_cache_tc_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv, const CacheAttn a,
+                     const Parts parts) {
   using C = Cfg<D>;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
@@ -179,20 +248,21 @@ attn_cache_tc_kernel(const __grid_constant__ CUtensorMap tk, const CacheAttn a, 
   volatile int32_t* abort_flag = reinterpret_cast<volatile int32_t*>(gbase + C::kOffMisc + 4);
   int64_t* s_begin = reinterpret_cast<int64_t*>(gbase + C::kOffMisc + 16);   // first entry, its offset
   __shared__ int64_t s_scan[C::THREADS / 32];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, rank = (int)(blockIdx.x & 1u);
+  auto lead = [&](int i) -> uint32_t { return in_first(bar(i)); };   // the first CTA's
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
 
-  // ---- this CTA's range of stages
+  // ---- this cluster's range of stages
   const Walk walk{a};
   const int entries = entries_of(a), per = (entries + C::THREADS - 1) / C::THREADS;
   const int n0 = min(entries, (int)threadIdx.x * per), n1 = min(entries, n0 + per);
   int64_t mine = 0;
   for (int e = n0; e < n1; ++e) mine += walk.at(e, blockIdx.x == 0).weight;
   int64_t total, below = scan_below<C::THREADS / 32>(mine, s_scan, &total);
-  const int64_t ctas = min((int64_t)gridDim.x, max((int64_t)1, (total + kMinStages - 1) / kMinStages)), cta = blockIdx.x;
+  const int64_t ctas = min((int64_t)gridDim.x / 2, max((int64_t)1, (total + kMinStages - 1) / kMinStages)), cta = blockIdx.x / 2;
   const int64_t begin = cta * total / ctas, end = cta < ctas ? (cta + 1) * total / ctas : begin;
-  if (threadIdx.x == 0) parts.open[cta].last = -1;
-  if (cta >= ctas || begin >= end) return;      // the same for the whole CTA
+  if (threadIdx.x == 0 && rank == 0) parts.open[cta].last = -1;
+  if (cta >= ctas || begin >= end) return;      // the same for the whole cluster
   if (below <= begin && begin < below + mine) {
     int64_t at = below;
     int e = n0;
@@ -212,32 +282,38 @@ attn_cache_tc_kernel(const __grid_constant__ CUtensorMap tk, const CacheAttn a, 
     init(K_EMPTY, kNK, 1);
     init(V_FULL, kNV, 1);
     init(V_EMPTY, kNV, 4);
-    init(W_FULL, kNW, 4);
+    init(W_FULL, kNW, 2 * 4);
     init(W_EMPTY, kNW, 1);
     init(INFO, kNInfo, 1);
     init(I_FULL, kNItems, 1);
-    init(I_EMPTY, kNItems, kSoftmax + 6);   // softmax, widening and issuing warps
-    init(Q_FULL, 2, 8);
+    init(I_EMPTY, kNItems, kSoftmax + 4 + (rank == 0 ? 2 : 0));   // softmax, widening and issuing warps
+    init(Q_FULL, 1, 2 * kSoftmax);
     init(S_FULL, 2, 1);
-    init(P_FULL, 2, 8);
+    init(S_FREE, 2, 2 * kSoftmax);
+    init(P_FULL, 2, 2 * kSoftmax);
     init(PV_DONE, 2, 1);
-    init(O_EMPTY, 2, 8);
+    init(O_EMPTY, 1, 2 * kSoftmax);
     init(TEAR, 2, 1);
     *abort_flag = 0;
     fence_barrier_init();
   }
-  if (warp == W_PROD && lane == 0) prefetch_tmap(&tk);
+  if (warp == W_PROD && lane == 0) {
+    prefetch_tmap(&tk);
+    prefetch_tmap(&tv);
+  }
   if (warp == W_S) {
-    tmem_alloc(smem_u32(tmem_slot), 512);
-    tmem_relinquish();
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;\n" ::"r"(smem_u32(tmem_slot)) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;\n" ::: "memory");
   }
   fence_before();
   __syncthreads();
+  cluster_sync();                               // the barriers of both CTAs are ready
   fence_after();
   const uint32_t tmem = *tmem_slot;
   const Guard g{abort_flag, a.d_status, kWaitNs};
-  auto col_s = [&](int t) { return tmem + (uint32_t)t * 128u; };
-  auto col_o = [&](int t) { return tmem + 256u + (uint32_t)t * 128u; };
+  const uint32_t col_o = tmem + 256u;
+  auto col_s = [&](uint32_t b) { return tmem + b * 128u; };
+  auto col_p = [&](uint32_t b) { return tmem + 384u + b * 64u; };
   // The next piece from the ring; false at the end or on abort. The slot is given back at once.
   uint32_t it_use = 0;
   auto next_piece = [&](Piece& x) -> bool {
@@ -249,7 +325,6 @@ attn_cache_tc_kernel(const __grid_constant__ CUtensorMap tk, const CacheAttn a, 
     ++it_use;
     return x.e1 >= 0;
   };
-  auto tiles_of = [&](const Piece& x) { return x.rows > kTileRows ? 2 : 1; };
 
   if (warp >= kSoftmax) {
     regs_decrease<C::kRegAux>();
@@ -303,7 +378,7 @@ attn_cache_tc_kernel(const __grid_constant__ CUtensorMap tk, const CacheAttn a, 
         const int row0 = group * kItemRows, rows = min(kItemRows, x.n * a.group - row0);
         const bool whole = e0 == 0 && at1 == size;
         const int slot = 2 * (int)cta + (e0 > 0 ? 0 : 1);     // a piece that goes on is the CTA's first
-        if (!whole && e0 == 0 && lane == 0)
+        if (!whole && e0 == 0 && lane == 0 && rank == 0)
           parts.open[cta] = Open{x.b, hk, row0, rows, x.s0, (int)(((item_at + size) * ctas - 1) / total)};
         if (!(ok = publish(Piece{x.s0, hk, row0, rows, x.n, x.len, e0, e1, whole ? -1 : slot}))) break;
 
@@ -361,23 +436,21 @@ attn_cache_tc_kernel(const __grid_constant__ CUtensorMap tk, const CacheAttn a, 
           const int v0 = __shfl_sync(0xffffffffu, now.valid, i), v1 = __shfl_sync(0xffffffffu, now.valid, i + 1);
           const int p0 = __shfl_sync(0xffffffffu, now.page, i), p1 = __shfl_sync(0xffffffffu, now.page, i + 1);
           const int q0 = __shfl_sync(0xffffffffu, now.pos, i) % a.c.bt, q1 = __shfl_sync(0xffffffffu, now.pos, i + 1) % a.c.bt;
-          const uint32_t bytes = ((v0 > 0 ? 1u : 0u) + (v1 > 0 ? 1u : 0u)) * (uint32_t)(kUnit * D);
+          const uint32_t halves = (v0 > 0 ? 1u : 0u) + (v1 > 0 ? 1u : 0u);
           const uint32_t ks = k_fill % kNK, vs = v_fill % kNV;
           if (!(ok = wait_warp(bar(K_EMPTY + ks), ((k_fill / kNK) & 1u) ^ 1u, g))) break;
-          if (lane == 0) {
-            mbar_arrive_expect_tx(bar(K_FULL + ks), bytes);
-            if (v0 > 0) tma_load_3d(sK + ks * C::kK, &tk, bar(K_FULL + ks), 0, hk * a.c.bt + q0, p0);
-            if (v1 > 0) tma_load_3d(sK + ks * C::kK + kUnit * D, &tk, bar(K_FULL + ks), 0, hk * a.c.bt + q1, p1);
+          if (lane == 0) {                      // this CTA's half of the keys
+            if (rank == 0) mbar_arrive_expect_tx(bar(K_FULL + ks), halves * (uint32_t)(kUnit * D));
+            if ((rank == 0 ? v0 : v1) > 0)
+              tma_pair(sK + ks * C::kK, &tk, lead(K_FULL + ks), 0, hk * a.c.bt + (rank == 0 ? q0 : q1), rank == 0 ? p0 : p1);
           }
           __syncwarp();
           ++k_fill;
           if (!(ok = wait_warp(bar(V_EMPTY + vs), ((v_fill / kNV) & 1u) ^ 1u, g))) break;
-          if (lane == 0) {
-            mbar_arrive_expect_tx(bar(V_FULL + vs), bytes);
-            const uint8_t* from = a.vc + (int64_t)hk * a.c.bt * D;
-            const int64_t page = (int64_t)a.c.heads * a.c.bt * D;
-            if (v0 > 0) bulk_load(sV + vs * C::kV, from + p0 * page + q0 * D, kUnit * D, bar(V_FULL + vs));
-            if (v1 > 0) bulk_load(sV + vs * C::kV + kUnit * D, from + p1 * page + q1 * D, kUnit * D, bar(V_FULL + vs));
+          if (lane == 0) {                      // this CTA's half of the columns
+            mbar_arrive_expect_tx(bar(V_FULL + vs), halves * (uint32_t)(kUnit * D / 2));
+            if (v0 > 0) tma_load_3d(sV + vs * C::kV, &tv, bar(V_FULL + vs), rank * (D / 2), hk * a.c.bt + q0, p0);
+            if (v1 > 0) tma_load_3d(sV + vs * C::kV + kUnit * D / 2, &tv, bar(V_FULL + vs), rank * (D / 2), hk * a.c.bt + q1, p1);
           }
           __syncwarp();
           ++v_fill;
@@ -386,89 +459,78 @@ attn_cache_tc_kernel(const __grid_constant__ CUtensorMap tk, const CacheAttn a, 
       if (ok) publish(Piece{0, 0, 0, 0, 0, 0, 0, -1, 0});
       if (*abort_flag) {
         // copies in flight end before the CTA does
-        for (uint32_t i = 0; i < kNK; ++i)
+        for (uint32_t i = 0; rank == 0 && i < kNK; ++i)
           if (k_fill > i) wait_raw(bar(K_FULL + (k_fill - 1 - i) % kNK), ((k_fill - 1 - i) / kNK) & 1u, kDrainNs);
         for (uint32_t i = 0; i < kNV; ++i)
           if (v_fill > i) wait_raw(bar(V_FULL + (v_fill - 1 - i) % kNV), ((v_fill - 1 - i) / kNV) & 1u, kDrainNs);
       }
       __syncwarp();
-    } else if (warp == W_S) {
+    } else if (warp == W_S && rank == 0) {
       // ------------------------------------------------------------ S = Q K^T issuer
-      uint32_t k_use = 0, n_q[2] = {0, 0}, n_s[2] = {0, 0};
+      uint32_t n = 0, n_q = 0;
       bool issued = false, ok = true;
       Piece x;
       while (ok && next_piece(x)) {
-        const int tiles = tiles_of(x);
-        for (int t = 0; t < tiles && ok; ++t) ok = wait_warp(bar(Q_FULL + t), n_q[t]++ & 1u, g);
-        for (int e = x.e0; e < x.e1 && ok; ++e) {
-          const uint32_t ks = k_use % kNK;
-          if (!(ok = wait_warp(bar(K_FULL + ks), (k_use / kNK) & 1u, g))) break;
-          for (int t = 0; t < tiles; ++t) {
-            // the buffer held P until its PV was done
-            if (!(ok = wait_warp(bar(PV_DONE + t), (n_s[t] & 1u) ^ 1u, g))) break;
-            fence_after();
-            if (elect_one()) {
+        if (!(ok = wait_pair(bar(Q_FULL), n_q++ & 1u, g))) break;
+        for (int e = x.e0; e < x.e1; ++e, ++n) {
+          const uint32_t ks = n % kNK, b = n & 1u;
+          if (!(ok = wait_pair(bar(K_FULL + ks), (n / kNK) & 1u, g))) break;
+          if (!(ok = wait_pair(bar(S_FREE + b), ((n >> 1) & 1u) ^ 1u, g))) break;
+          fence_after();
+          if (elect_one()) {
 #pragma unroll
-              for (int q = 0; q < 2; ++q)
+            for (int q = 0; q < 2; ++q)
 #pragma unroll
-                for (int kk = 0; kk < D / 32; ++kk)
-                  mma_8bit(col_s(t), smem_desc(sQ + (uint32_t)(2 * t + q) * C::kQ + 32u * kk, 16, C::kAtom, C::kSwz),
-                           smem_desc(sK + ks * C::kK + 32u * kk, 16, C::kAtom, C::kSwz), idesc(kStageKeys, 0),
-                           q > 0 || kk > 0 ? 1u : 0u);
-              commit(bar(S_FULL + t));
-              if (t + 1 == tiles) commit(bar(K_EMPTY + ks));
-            }
-            __syncwarp();
-            ++n_s[t];
-            issued = true;
+              for (int kk = 0; kk < D / 32; ++kk)
+                mma_8bit(col_s(b), smem_desc(sQ + (uint32_t)q * C::kQ + 32u * kk, 16, C::kAtom, C::kSwz),
+                         smem_desc(sK + ks * C::kK + 32u * kk, 16, C::kAtom, C::kSwz), idesc(kStageKeys, 0),
+                         q > 0 || kk > 0 ? 1u : 0u);
+            commit_both(bar(S_FULL + b));
+            commit_both(bar(K_EMPTY + ks));
           }
-          ++k_use;
+          __syncwarp();
+          issued = true;
         }
       }
       if (*abort_flag && issued) {
-        if (elect_one()) commit(bar(TEAR));
+        if (elect_one()) commit_one(bar(TEAR));
         __syncwarp();
         wait_raw(bar(TEAR), 0, kDrainNs);
       }
       __syncwarp();
-    } else if (warp == W_PV) {
+    } else if (warp == W_PV && rank == 0) {
       // ------------------------------------------------------------ O += P V issuer
-      uint32_t w_use = 0, n_p[2] = {0, 0}, n_o[2] = {0, 0};
+      uint32_t n = 0, n_o = 0;
       bool issued = false, ok = true;
       Piece x;
       while (ok && next_piece(x)) {
-        const int tiles = tiles_of(x);
-        for (int e = x.e0; e < x.e1 && ok; ++e) {
-          const uint32_t ws = w_use % kNW;
-          if (!(ok = wait_warp(bar(W_FULL + ws), (w_use / kNW) & 1u, g))) break;
-          for (int t = 0; t < tiles; ++t) {
-            if (!(ok = wait_warp(bar(P_FULL + t), n_p[t] & 1u, g))) break;
-            if (e == x.e0 && !(ok = wait_warp(bar(O_EMPTY + t), (n_o[t]++ & 1u) ^ 1u, g))) break;
-            fence_after();
-            if (elect_one()) {
+        for (int e = x.e0; e < x.e1; ++e, ++n) {
+          const uint32_t ws = n % kNW, b = n & 1u;
+          if (!(ok = wait_pair(bar(W_FULL + ws), (n / kNW) & 1u, g))) break;
+          if (!(ok = wait_pair(bar(P_FULL + b), (n >> 1) & 1u, g))) break;
+          if (e == x.e0 && !(ok = wait_pair(bar(O_EMPTY), (n_o++ & 1u) ^ 1u, g))) break;
+          fence_after();
+          if (elect_one()) {
 #pragma unroll
-              for (int kk = 0; kk < kStageKeys / 16; ++kk)
-                mma_ts(col_o(t), col_s(t) + 64u * (kk >> 2) + 8u * (kk & 3), smem_desc(sW + ws * C::kW + 2048u * kk, C::kWBox, 1024, kSwizzle128B),
-                       idesc(D, 1), e > x.e0 || kk > 0 ? 1u : 0u);
-              commit(bar(PV_DONE + t));
-              if (t + 1 == tiles) commit(bar(W_EMPTY + ws));
-            }
-            __syncwarp();
-            ++n_p[t];
-            issued = true;
+            for (int kk = 0; kk < kStageKeys / 16; ++kk)
+              mma_f16(col_o, col_p(b) + 8u * kk, smem_desc(sW + ws * C::kW + 16u * D * kk, 16, C::kAtom, C::kSwz), idesc(D, 1),
+                      e > x.e0 || kk > 0 ? 1u : 0u);
+            commit_both(bar(PV_DONE + b));
+            commit_both(bar(W_EMPTY + ws));
           }
-          ++w_use;
+          __syncwarp();
+          issued = true;
         }
       }
       if (*abort_flag && issued) {
-        if (elect_one()) commit(bar(TEAR_PV));
+        if (elect_one()) commit_one(bar(TEAR_PV));
         __syncwarp();
         wait_raw(bar(TEAR_PV), 0, kDrainNs);
       }
       __syncwarp();
     } else if (warp < W_PROD) {
       // ------------------------------------------------------------ V to f16
-      constexpr int CH = D / 16;                // 16-code vectors of a row
+      constexpr int CH = D / 32;                // 16-code vectors of this CTA's half of a row
       const int id = threadIdx.x - 32 * W_WIDEN;
       uint32_t n = 0;
       bool ok = true;
@@ -484,7 +546,7 @@ attn_cache_tc_kernel(const __grid_constant__ CUtensorMap tk, const CacheAttn a, 
           uint8_t* to = gbase + C::kOffW + ws * C::kW;
 #pragma unroll
           for (int i = 0; i < kStageKeys * CH / 128; ++i) {
-            const int v = id + 128 * i, r = v / CH, c = v % CH;   // row, and its columns 16 c ..
+            const int v = id + 128 * i, r = v / CH, c = v % CH;   // row, and columns 16 c .. of the half
             uint4 w = from[v];
             if ((r & 63) >= (r < 64 ? valid0 : valid1)) w = make_uint4(0, 0, 0, 0);
             const uint32_t in[4] = {w.x, w.y, w.z, w.w};
@@ -494,21 +556,15 @@ attn_cache_tc_kernel(const __grid_constant__ CUtensorMap tk, const CacheAttn a, 
               out[2 * k] = f16x2_of_e4m3(in[k]);
               out[2 * k + 1] = f16x2_of_e4m3(in[k] >> 16);
             }
-            // two vectors of 8 columns; the other one first in the second box, for the banks' sake
-            uint8_t* row = to + (c >> 2) * C::kWBox + r * 128;
-            const int c0 = 2 * (c & 3), swap = (c >> 2) & 1;
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              const int h = k ^ swap;
-              *reinterpret_cast<uint4*>(row + (((c0 + h) ^ (r & 7)) << 4)) =
-                  h ? make_uint4(out[4], out[5], out[6], out[7]) : make_uint4(out[0], out[1], out[2], out[3]);
-            }
+            for (int k = 0; k < 2; ++k)         // a row of D / 2 values in f16 has D bytes, as one of K has
+              *reinterpret_cast<uint4*>(to + C::at(r, 2 * c + k)) = make_uint4(out[4 * k], out[4 * k + 1], out[4 * k + 2], out[4 * k + 3]);
           }
           fence_async_shared();
           __syncwarp();
           if (lane == 0) {
             mbar_arrive(bar(V_EMPTY + vs));
-            mbar_arrive(bar(W_FULL + ws));
+            arrive_cluster(lead(W_FULL + ws));
           }
           ++n;
         }
@@ -517,19 +573,20 @@ attn_cache_tc_kernel(const __grid_constant__ CUtensorMap tk, const CacheAttn a, 
     }
   } else {
     regs_increase<C::kRegSoftmax>();
-    // -------------------------------------------------------------- softmax + epilogue of tile t
-    const int t = warp >> 3, half = (warp >> 2) & 1, r = (warp & 3) * 32 + lane;   // r: row of the tile = TMEM lane
+    // -------------------------------------------------------------- softmax + epilogue of this CTA's rows
+    const int half = (warp >> 2) & 1, r = (warp & 3) * 32 + lane;   // r: row of the CTA = TMEM lane
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t t_s = col_s(t) + lanes + 64u * half, t_o = col_o(t) + lanes + (uint32_t)half * (D / 2);
-    const int pair_bar = 1 + t * 4 + (warp & 3);   // named barrier of the two warps that share rows
-    float* ex = reinterpret_cast<float*>(gbase + C::kOffEx) + t * 2 * kTileRows + r;
-    uint32_t n_info = 0, n_s = 0, n_ex = 0;
+    const uint32_t t_o = col_o + lanes + (uint32_t)half * (D / 2);
+    const int pair_bar = 1 + (warp & 3);         // named barrier of the two warps that share rows
+    float* ex = reinterpret_cast<float*>(gbase + C::kOffEx) + r;
+    const uint32_t s_free = lead(S_FREE), p_full = lead(P_FULL);
+    uint32_t n = 0, n_ex = 0;                    // stages, exchanges
     bool ok = true;
     // The row's other half: gives its value for this one's. The two warps take every step together: a
     // warp that has given up says so here (NaN with these bits), and both leave after it.
     constexpr uint32_t kGone = 0x7fc0dead;
     auto exchange = [&](float mine, float& theirs) -> bool {
-      float* at = ex + (n_ex++ & 1u) * 4 * kTileRows;   // the other buffer may still be read
+      float* at = ex + (n_ex++ & 1u) * 2 * kTileRows;   // the other buffer may still be read
       at[half * kTileRows] = ok ? mine : __uint_as_float(kGone);
       asm volatile("bar.sync %0, 64;\n" ::"r"(pair_bar) : "memory");
       theirs = at[(half ^ 1) * kTileRows];
@@ -541,12 +598,8 @@ attn_cache_tc_kernel(const __grid_constant__ CUtensorMap tk, const CacheAttn a, 
       float theirs;
       ok = ok && next_piece(x);
       if (!exchange(0.f, theirs)) break;
-      if (t >= tiles_of(x)) {
-        n_info += (uint32_t)(x.e1 - x.e0);
-        continue;
-      }
-      const int row = x.row0 + t * kTileRows + r;
-      const bool live = t * kTileRows + r < x.rows;
+      const int row = x.row0 + rank * kTileRows + r;
+      const bool live = rank * kTileRows + r < x.rows;
       const int tok = row / a.group, h = x.hk * a.group + row % a.group;
       // ---- the row's queries as two e4m3 values each, under a power of two (every S of the last
       // piece is done: its scores have been read)
@@ -575,7 +628,7 @@ attn_cache_tc_kernel(const __grid_constant__ CUtensorMap tk, const CacheAttn a, 
         e2 = max(-100, min(120, e2));
         const float down = __uint_as_float((uint32_t)(127 - e2) << 23);
         factor = __uint_as_float((uint32_t)(127 + e2) << 23) * a.scale_log2;
-        uint8_t* q1 = gbase + (uint32_t)(2 * t) * C::kQ;
+        uint8_t* q1 = gbase;
 #pragma unroll
         for (int c = 0; c < D / 32; ++c) {
           const uint32_t p[8] = {w[2 * c].x,     w[2 * c].y,     w[2 * c].z,     w[2 * c].w,
@@ -603,40 +656,48 @@ attn_cache_tc_kernel(const __grid_constant__ CUtensorMap tk, const CacheAttn a, 
         }
         fence_async_shared();
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar(Q_FULL + t));
+        if (lane == 0) arrive_cluster(lead(Q_FULL));
       }
       const int last = a.causal ? x.len - x.n + tok : INT32_MAX;   // the last key that the row sees
       float ref = -INFINITY, l = 0.f;            // R; l times 2^11, of this half's keys
-      for (int e = x.e0; e < x.e1; ++e) {
-        const uint32_t is = n_info % kNInfo;
-        ok = ok && wait_warp(bar(INFO + is), (n_info / kNInfo) & 1u, g);
-        ++n_info;
+      // what the row sees of a stage's half, and its scales: fetched while the last stage's scores come
+      int see;
+      float c, lv, inv;
+      auto facts = [&](uint32_t n) {
+        const uint32_t is = n % kNInfo;
+        ok = ok && wait_warp(bar(INFO + is), (n / kNInfo) & 1u, g);
         const int pos = infos[is].pos[half];
-        const int see = min(infos[is].valid[half], last - pos < 63 ? last - pos + 1 : 64);
-        const float c = factor * infos[is].ks[half], lv = infos[is].lv[half], inv = infos[is].inv[half];
-        const bool cut = __any_sync(0xffffffffu, see < 64);
-        ok = ok && wait_warp(bar(S_FULL + t), n_s & 1u, g);
-        ++n_s;
+        see = min(infos[is].valid[half], last - pos < 63 ? last - pos + 1 : 64);
+        c = factor * infos[is].ks[half];
+        lv = infos[is].lv[half];
+        inv = infos[is].inv[half];
+      };
+      facts(n);
+      for (int e = x.e0; e < x.e1; ++e, ++n) {
+        const uint32_t b = n & 1u;
+        ok = ok && wait_warp(bar(S_FULL + b), (n >> 1) & 1u, g);
         fence_after();
-        // the scores are read twice, for their maximum and for P: registers hold 32 of them at a time
-        uint32_t s[32];
-        float cm;
-        if (!cut) {
-          cm = tmem_ld32_max(t_s, s);
-          cm = fmaxf(cm, tmem_ld32_max(t_s + 32u, s));
-          wait_ld();
-        } else {
+        uint32_t s[64];
+        float cm = tmem_ld32_max(col_s(b) + lanes + 64u * half, s);
+        cm = fmaxf(cm, tmem_ld32_max(col_s(b) + lanes + 64u * half + 32u, s + 32));
+        const int see0 = see;
+        const float c0 = c, lv0 = lv, inv0 = inv;
+        const bool cut = __any_sync(0xffffffffu, see0 < 64);
+        if (e + 1 < x.e1) facts(n + 1);
+        wait_ld();
+        fence_before();
+        __syncwarp();
+        if (lane == 0) arrive_cluster(s_free + 8u * b);
+        if (cut) {
           cm = -INFINITY;
 #pragma unroll
-          for (int q = 0; q < 2; ++q) {
-            tmem_ld32(t_s + 32u * q, s);
-            wait_ld();
-#pragma unroll
-            for (int k = 0; k < 32; ++k) cm = 32 * q + k < see ? fmaxf(cm, __uint_as_float(s[k])) : cm;
+          for (int i = 0; i < 64; ++i) {
+            if (i >= see0) s[i] = 0xff800000u;
+            cm = fmaxf(cm, __uint_as_float(s[i]));
           }
         }
         // a half without keys says nothing (its product with a scale might)
-        float top = see > 0 ? fmaf(cm, c, lv) : -INFINITY;
+        float top = see0 > 0 ? fmaf(cm, c0, lv0) : -INFINITY;
         if (!exchange(top, theirs)) break;
         top = fmaxf(top, theirs);
         float f = 1.f;
@@ -646,54 +707,48 @@ attn_cache_tc_kernel(const __grid_constant__ CUtensorMap tk, const CacheAttn a, 
           ref = top;
           l *= f;
         }
-        const float off = lv + kShift - (ref == -INFINITY ? 0.f : ref);
+        const float off = lv0 + kShift - (ref == -INFINITY ? 0.f : ref);
         float rs[4] = {0.f, 0.f, 0.f, 0.f};
+        uint32_t pk[32];
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          tmem_ld32(t_s + 32u * q, s);
-          wait_ld();
-          if (cut) {
-#pragma unroll
-            for (int k = 0; k < 32; ++k)
-              if (32 * q + k >= see) s[k] = 0xff800000u;
-          }
-          uint32_t pk[16];
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            float x0, x1;
-            fma_x2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1]), c, off, x0, x1);
-            const float p0 = exp2_fast(x0), p1 = exp2_fast(x1);
-            add_x2(rs[2 * (i & 1)], rs[2 * (i & 1) + 1], p0, p1);
-            pk[i] = pack_f16(p0, p1);
-          }
-          tmem_st16(t_s + 16u * q, pk);          // over scores of this half that have been read
+        for (int i = 0; i < 32; ++i) {
+          float x0, x1;
+          fma_x2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1]), c0, off, x0, x1);
+          const float p0 = exp2_fast(x0), p1 = exp2_fast(x1);
+          add_x2(rs[2 * (i & 1)], rs[2 * (i & 1) + 1], p0, p1);
+          pk[i] = pack_f16(p0, p1);
         }
-        l = fmaf((rs[0] + rs[1]) + (rs[2] + rs[3]), inv, l);
-        // O follows the reference now that the scores are no longer held
-        if (e > x.e0 && __any_sync(0xffffffffu, moves)) {   // PV of the last stage is done: S came after it
+        l = fmaf((rs[0] + rs[1]) + (rs[2] + rs[3]), inv0, l);
+        // P buffer b was last read by the PV of two stages ago
+        if (n >= 2) ok = ok && wait_warp(bar(PV_DONE + b), ((n - 2) >> 1) & 1u, g);
+        fence_after();
+        tmem_st32(col_p(b) + lanes + 32u * half, pk);
+        if (e > x.e0 && __any_sync(0xffffffffu, moves)) {   // O follows the reference, after the PV of the last stage
+          ok = ok && wait_warp(bar(PV_DONE + (b ^ 1u)), ((n - 1) >> 1) & 1u, g);
+          fence_after();
 #pragma unroll
           for (int i = 0; i < D / 64; ++i) {
             uint32_t ov[32];
             tmem_ld32(t_o + 32u * i, ov);
             wait_ld();
 #pragma unroll
-            for (int k = 0; k < 32; ++k) ov[k] = __float_as_uint(__uint_as_float(ov[k]) * f);
+            for (int q = 0; q < 32; ++q) ov[q] = __float_as_uint(__uint_as_float(ov[q]) * f);
             tmem_st32(t_o + 32u * i, ov);
           }
         }
         wait_st();
         fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar(P_FULL + t));
+        if (lane == 0) arrive_cluster(p_full + 8u * b);
       }
       // ---- the end of a piece: the row's whole sum, and half of O from TMEM
-      ok = ok && wait_warp(bar(PV_DONE + t), (n_s - 1) & 1u, g);
+      ok = ok && wait_warp(bar(PV_DONE + ((n - 1) & 1u)), ((n - 1) >> 1) & 1u, g);
       if (!exchange(l, theirs)) break;
       l = half ? theirs + l : l + theirs;
       fence_after();
       const float scale = l == 0.f ? 0.f : x.part < 0 ? 1.0f / l : 1.f;
       const int64_t at = (int64_t)(x.s0 + tok) * a.H + h;
-      float* sums = parts.sum + ((int64_t)max(x.part, 0) * kItemRows + t * kTileRows + r) * D + half * (D / 2);
+      float* sums = parts.sum + ((int64_t)max(x.part, 0) * kItemRows + rank * kTileRows + r) * D + half * (D / 2);
 #pragma unroll
       for (int i = 0; i < D / 64; ++i) {
         uint32_t ov[32];
@@ -723,18 +778,20 @@ attn_cache_tc_kernel(const __grid_constant__ CUtensorMap tk, const CacheAttn a, 
       }
       fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(bar(O_EMPTY + t));
+      if (lane == 0) arrive_cluster(lead(O_EMPTY));
       if (live && half == 0) {
         if (x.part < 0) a.lse[at] = l == 0.f ? -INFINITY : (ref - kShift + log2f(l)) * 0.6931471805599453f;
-        else parts.ml[(int64_t)x.part * kItemRows + t * kTileRows + r] = make_float2(ref - kShift, l);
+        else parts.ml[(int64_t)x.part * kItemRows + rank * kTileRows + r] = make_float2(ref - kShift, l);
       }
     }
   }
 
   fence_before();
   __syncthreads();
+  cluster_sync();                               // neither reads the other's memory any more
   fence_after();
-  if (warp == W_S) tmem_dealloc(tmem, 512);
+  if (warp == W_S)
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;\n" ::"r"(tmem) : "memory");
 }
 
 // The join of what items in several CTAs have left: CTA (c, rows of the item that starts in CTA c),
@@ -772,18 +829,20 @@ attn_cache_tc_join_kernel(const CacheAttn a, const Parts parts) {
   }
 }
 
-constexpr int kGrid = 152;
+constexpr int kGrid = 76;           // clusters
 
 template <int D>
 sparsp_status_t go(const CacheAttn& a, void* ws, cudaStream_t st) {
-  CUtensorMap tk;
-  if (!make_tmap_codes(&tk, a.kc, (uint64_t)D, (uint64_t)a.c.heads * a.c.bt, (uint64_t)a.c.blocks, kUnit))
+  CUtensorMap tk, tv;
+  const uint64_t rows = (uint64_t)a.c.heads * a.c.bt, blocks = (uint64_t)a.c.blocks;
+  if (!make_tmap_codes(&tk, a.kc, (uint64_t)D, rows, blocks, kUnit) ||
+      !make_tmap_codes(&tv, a.vc, (uint64_t)D, rows, blocks, kUnit, D / 2))
     return SPARSP_ERR_CUDA;
   const Parts p = parts_of(ws, kGrid, kItemRows);
   constexpr int smem = Cfg<D>::kSmem;
   if (cudaFuncSetAttribute(attn_cache_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
     return SPARSP_ERR_CUDA;
-  attn_cache_tc_kernel<D><<<kGrid, Cfg<D>::THREADS, smem, st>>>(tk, a, p);
+  attn_cache_tc_kernel<D><<<2 * kGrid, Cfg<D>::THREADS, smem, st>>>(tk, tv, a, p);
   SPARSP_LAUNCH_CHECK();
   return launch_after(attn_cache_tc_join_kernel<D>, dim3(kGrid, kItemRows / kJoinRows), 256, st, a, p);
 }

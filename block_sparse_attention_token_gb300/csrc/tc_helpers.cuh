@@ -335,8 +335,10 @@ bool make_tmap_bf16_boxes(CUtensorMap* map, const void* base, uint64_t rows, uin
                           uint32_t boxes);
 
 // Host side: tensor map of [blocks, rows, cols] bytes (cols 64 or 128) with a box of all
-// columns x box_rows rows and a swizzle of a row's length.
-bool make_tmap_codes(CUtensorMap* map, const void* base, uint64_t cols, uint64_t rows, uint64_t blocks, uint32_t box_rows);
+// columns x box_rows rows and a swizzle of a row's length; or with box_cols of the columns
+// (a multiple of 16) and none.
+bool make_tmap_codes(CUtensorMap* map, const void* base, uint64_t cols, uint64_t rows, uint64_t blocks, uint32_t box_rows,
+                     uint32_t box_cols = 0);
 
 // Host side: tensor map of a raster [B, N, H, d] bf16 tensor (N = T*Y*X) as 5-D
 // (column, head, x, y, b*T + t) with a box of 64 columns x one head x one tile

@@ -40,15 +40,17 @@ bool make_tmap_bf16_rows(CUtensorMap* map, const void* base, uint64_t rows, uint
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-bool make_tmap_codes(CUtensorMap* map, const void* base, uint64_t cols, uint64_t rows, uint64_t blocks, uint32_t box_rows) {
+bool make_tmap_codes(CUtensorMap* map, const void* base, uint64_t cols, uint64_t rows, uint64_t blocks, uint32_t box_rows,
+                     uint32_t box_cols) {
   EncodeTiled enc = encoder();
   if (enc == nullptr) return false;
   const cuuint64_t dims[3] = {cols, rows, blocks};
   const cuuint64_t strides[2] = {cols, cols * rows};
-  const cuuint32_t box[3] = {(cuuint32_t)cols, box_rows, 1};
+  const cuuint32_t box[3] = {box_cols != 0 ? box_cols : (cuuint32_t)cols, box_rows, 1};
   const cuuint32_t estr[3] = {1, 1, 1};
   return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box, estr,
-             CU_TENSOR_MAP_INTERLEAVE_NONE, cols == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+             CU_TENSOR_MAP_INTERLEAVE_NONE,
+             box_cols != 0 ? CU_TENSOR_MAP_SWIZZLE_NONE : cols == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
