@@ -20,9 +20,10 @@
 // for 256 rows, and shared memory is read half as often as with a tile to each SM. Work is counted in
 // stages of 128 keys over all items (request, key head, 256 rows) and dealt out evenly;
 // an item in several clusters leaves partial sums that a second kernel joins in order.
-//   warps 0-7: softmax and epilogue of the CTA's rows, two threads to a row (= TMEM lane), one for each
-//              half of a stage's keys (and of the columns of Q and O); the two exchange their largest
-//              score. At an item's start they also split its queries into shared memory.
+//   warps 0-7: softmax and epilogue of the CTA's rows, two threads to a row (= TMEM lane): one for the even
+//              stages and one for the odd, which pass the row's reference from stage to stage, so that one loads
+//              scores while the other takes exponentials. Each has half of the columns of Q, which they
+//              split into shared memory at an item's start, and of O.
 //   warps 8-11: widen V, zeros past a request's last token (what lies there may be anything).
 //   warp 12: producer: items, look-ups of lists and tables (32 at a time, a batch ahead), and TMA: 64 keys
 //              of K, half of the columns of V.
@@ -47,7 +48,7 @@ constexpr int kTileRows = 128, kItemRows = 2 * kTileRows, kStageKeys = 128;
 constexpr int kItemCost = 6;       // stages that an item's own work counts as
 constexpr int kMinStages = 10;     // stages, an item's own among them, that are worth a cluster
 constexpr float kShift = 11.f, kMoves = 4.f;   // P is held as 2^11 times what it is against R
-constexpr int kNK = 6, kNV = 4, kNW = 3, kNInfo = 16, kNItems = 2;
+constexpr int kNK = 6, kNV = 4, kNW = 3, kNInfo = 8, kNItems = 2;
 constexpr uint64_t kWaitNs = 2000000000ull, kDrainNs = 200000000ull;
 constexpr int kSoftmax = 8, W_WIDEN = kSoftmax, W_PROD = W_WIDEN + 4, W_S = W_PROD + 1, W_PV = W_PROD + 2;   // warps
 
@@ -63,11 +64,15 @@ enum Bars {
 struct Piece {
   int s0, hk, row0, rows, n, len, e0, e1, part;   // part: -1: the whole item, else the slot of its sums
 };
-// A stage's two halves of 64 keys: position of the first key, how many exist, scale of K, log2
-// and inverse of the scale of V.
-struct Info {
-  int pos[2], valid[2];
-  float ks[2], lv[2], inv[2];
+// What is to be known of half a stage (64 keys): position of the first, how many exist, scale of K, log2 and inverse
+// of the scale of V. The producer leaves them by batches of 16 stages of a piece.
+struct alignas(16) Info {
+  int pos, valid;
+  float ks, lv, inv;
+};
+constexpr int kBatch = 16;
+struct Batch {
+  Info half[kBatch][2];
 };
 
 template <int D>
@@ -78,10 +83,11 @@ struct Cfg {
   // bytes: q1 or q2; half of a stage's K; half of its V's columns, raw and in f16
   static constexpr uint32_t kQ = kTileRows * D, kK = kUnit * D, kV = kStageKeys * D / 2, kW = kStageKeys * D;
   static constexpr uint32_t kOffK = 2 * kQ, kOffV = kOffK + kNK * kK, kOffW = kOffV + kNV * kV;
-  static constexpr uint32_t kOffBar = kOffW + kNW * kW, kOffInfo = kOffBar + 8 * NBAR;
-  static constexpr uint32_t kOffPiece = kOffInfo + kNInfo * (uint32_t)sizeof(Info);
+  static constexpr uint32_t kOffInfo = kOffW + kNW * kW, kOffBar = kOffInfo + kNInfo * (uint32_t)sizeof(Batch);
+  static constexpr uint32_t kOffPiece = kOffBar + 8 * NBAR;
   static constexpr uint32_t kOffEx = kOffPiece + kNItems * (uint32_t)sizeof(Piece);   // [2][half][row] floats
-  static constexpr uint32_t kOffMisc = kOffEx + 2 * 2 * kTileRows * 4;
+  static constexpr uint32_t kOffRef = kOffEx + 2 * 2 * kTileRows * 4;                 // [row] floats
+  static constexpr uint32_t kOffMisc = kOffRef + kTileRows * 4;
   static constexpr uint32_t kSmem = kOffMisc + 64 + 1024;   // + alignment slack
   static_assert(kSmem <= 232448 && kOffMisc % 8 == 0, "shared memory");
   // K-major rows of D bytes, and V's rows of D / 2 columns in f16: 128-byte swizzle, or with D = 64 the 64-byte one
@@ -242,7 +248,7 @@ attn_cache_tc_kernel(const __grid_constant__ CUtensorMap tk, const __grid_consta
   uint8_t* gbase = smem_raw + (base - raw);
   const uint32_t sQ = base, sK = base + C::kOffK, sV = base + C::kOffV, sW = base + C::kOffW;
   auto bar = [&](int i) -> uint32_t { return base + C::kOffBar + 8u * (uint32_t)i; };
-  Info* infos = reinterpret_cast<Info*>(gbase + C::kOffInfo);
+  Batch* infos = reinterpret_cast<Batch*>(gbase + C::kOffInfo);
   Piece* pieces = reinterpret_cast<Piece*>(gbase + C::kOffPiece);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gbase + C::kOffMisc);
   volatile int32_t* abort_flag = reinterpret_cast<volatile int32_t*>(gbase + C::kOffMisc + 4);
@@ -289,8 +295,8 @@ attn_cache_tc_kernel(const __grid_constant__ CUtensorMap tk, const __grid_consta
     init(I_EMPTY, kNItems, kSoftmax + 4 + (rank == 0 ? 2 : 0));   // softmax, widening and issuing warps
     init(Q_FULL, 1, 2 * kSoftmax);
     init(S_FULL, 2, 1);
-    init(S_FREE, 2, 2 * kSoftmax);
-    init(P_FULL, 2, 2 * kSoftmax);
+    init(S_FREE, 2, kSoftmax);    // a stage is four warps' in each CTA
+    init(P_FULL, 2, kSoftmax);
     init(PV_DONE, 2, 1);
     init(O_EMPTY, 1, 2 * kSoftmax);
     init(TEAR, 2, 1);
@@ -330,7 +336,7 @@ attn_cache_tc_kernel(const __grid_constant__ CUtensorMap tk, const __grid_consta
     regs_decrease<C::kRegAux>();
     if (warp == W_PROD) {
       // ------------------------------------------------------------ producer
-      uint32_t it_fill = 0, k_fill = 0, v_fill = 0, n_info = 0;
+      uint32_t it_fill = 0, k_fill = 0, v_fill = 0, n_batch = 0;
       int entry = (int)s_begin[0];
       int64_t offset = s_begin[1], unit_at = begin;
       Entry x = walk.at(entry, false);
@@ -386,11 +392,11 @@ attn_cache_tc_kernel(const __grid_constant__ CUtensorMap tk, const __grid_consta
         const int32_t* table = a.table + (int64_t)x.b * a.max_blocks;
         const int32_t* list = a.row_ptr != nullptr ? a.col_idx + a.row_ptr[entry] : nullptr;
         struct Half {
-          int pos, valid, page;
-          float ks, vs;
+          Info info;
+          int page, row;
         };
         auto look = [&](int u) -> Half {
-          Half h{0, 0, 0, 1.f, 1.f};
+          Half h{{0, 0, 1.f, 0.f, 1.f}, 0, 0};
           if (u >= 2 * e1 || u >= x.units) return h;
           int j = u / per_block;
           if (list != nullptr) j = __ldg(list + j);
@@ -404,11 +410,12 @@ attn_cache_tc_kernel(const __grid_constant__ CUtensorMap tk, const __grid_consta
             return h;
           }
           const int64_t block = (int64_t)page * a.c.heads + hk;
-          h.pos = j * a.c.bt + u % per_block * kUnit;
-          h.valid = max(0, min(kUnit, x.len - h.pos));
+          const int in_block = u % per_block * kUnit;
+          const float vs = fmaxf(__ldg(a.vs + block), 0x1p-120f);
           h.page = page;
-          h.ks = __ldg(a.ks + block);
-          h.vs = fmaxf(__ldg(a.vs + block), 0x1p-120f);
+          h.row = hk * a.c.bt + in_block;
+          h.info = Info{j * a.c.bt + in_block, max(0, min(kUnit, x.len - j * a.c.bt - in_block)), __ldg(a.ks + block), log2f(vs),
+                        1.0f / vs};
           return h;
         };
         Half now, ahead = look(2 * e0 + lane);
@@ -417,40 +424,29 @@ attn_cache_tc_kernel(const __grid_constant__ CUtensorMap tk, const __grid_consta
           if (i == 0) {
             now = ahead;
             ahead = look(2 * e + 32 + lane);
+            const uint32_t is = n_batch++ % kNInfo;
+            infos[is].half[lane >> 1][lane & 1] = now.info;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(INFO + is));
           }
-          // the stage's facts
-          const uint32_t is = n_info % kNInfo;
-          const float lv = log2f(now.vs), inv = 1.0f / now.vs;
-          if (lane == i || lane == i + 1) {
-            Info& f = infos[is];
-            const int h = lane - i;
-            f.pos[h] = now.pos;
-            f.valid[h] = now.valid;
-            f.ks[h] = now.ks;
-            f.lv[h] = lv;
-            f.inv[h] = inv;
-          }
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bar(INFO + is));
-          ++n_info;
-          const int v0 = __shfl_sync(0xffffffffu, now.valid, i), v1 = __shfl_sync(0xffffffffu, now.valid, i + 1);
+          const int v0 = __shfl_sync(0xffffffffu, now.info.valid, i), v1 = __shfl_sync(0xffffffffu, now.info.valid, i + 1);
           const int p0 = __shfl_sync(0xffffffffu, now.page, i), p1 = __shfl_sync(0xffffffffu, now.page, i + 1);
-          const int q0 = __shfl_sync(0xffffffffu, now.pos, i) % a.c.bt, q1 = __shfl_sync(0xffffffffu, now.pos, i + 1) % a.c.bt;
+          const int r0 = __shfl_sync(0xffffffffu, now.row, i), r1 = __shfl_sync(0xffffffffu, now.row, i + 1);
           const uint32_t halves = (v0 > 0 ? 1u : 0u) + (v1 > 0 ? 1u : 0u);
           const uint32_t ks = k_fill % kNK, vs = v_fill % kNV;
           if (!(ok = wait_warp(bar(K_EMPTY + ks), ((k_fill / kNK) & 1u) ^ 1u, g))) break;
           if (lane == 0) {                      // this CTA's half of the keys
             if (rank == 0) mbar_arrive_expect_tx(bar(K_FULL + ks), halves * (uint32_t)(kUnit * D));
             if ((rank == 0 ? v0 : v1) > 0)
-              tma_pair(sK + ks * C::kK, &tk, lead(K_FULL + ks), 0, hk * a.c.bt + (rank == 0 ? q0 : q1), rank == 0 ? p0 : p1);
+              tma_pair(sK + ks * C::kK, &tk, lead(K_FULL + ks), 0, rank == 0 ? r0 : r1, rank == 0 ? p0 : p1);
           }
           __syncwarp();
           ++k_fill;
           if (!(ok = wait_warp(bar(V_EMPTY + vs), ((v_fill / kNV) & 1u) ^ 1u, g))) break;
           if (lane == 0) {                      // this CTA's half of the columns
             mbar_arrive_expect_tx(bar(V_FULL + vs), halves * (uint32_t)(kUnit * D / 2));
-            if (v0 > 0) tma_load_3d(sV + vs * C::kV, &tv, bar(V_FULL + vs), rank * (D / 2), hk * a.c.bt + q0, p0);
-            if (v1 > 0) tma_load_3d(sV + vs * C::kV + kUnit * D / 2, &tv, bar(V_FULL + vs), rank * (D / 2), hk * a.c.bt + q1, p1);
+            if (v0 > 0) tma_load_3d(sV + vs * C::kV, &tv, bar(V_FULL + vs), rank * (D / 2), r0, p0);
+            if (v1 > 0) tma_load_3d(sV + vs * C::kV + kUnit * D / 2, &tv, bar(V_FULL + vs), rank * (D / 2), r1, p1);
           }
           __syncwarp();
           ++v_fill;
@@ -532,14 +528,18 @@ attn_cache_tc_kernel(const __grid_constant__ CUtensorMap tk, const __grid_consta
       // ------------------------------------------------------------ V to f16
       constexpr int CH = D / 32;                // 16-code vectors of this CTA's half of a row
       const int id = threadIdx.x - 32 * W_WIDEN;
-      uint32_t n = 0;
+      uint32_t n = 0, n_batch = 0;
       bool ok = true;
       Piece x;
       while (ok && next_piece(x)) {
         for (int e = x.e0; e < x.e1; ++e) {
-          const uint32_t vs = n % kNV, ws = n % kNW, is = n % kNInfo;
-          if (!(ok = wait_warp(bar(INFO + is), (n / kNInfo) & 1u, g))) break;
-          const int valid0 = infos[is].valid[0], valid1 = infos[is].valid[1];
+          const uint32_t vs = n % kNV, ws = n % kNW;
+          if ((e - x.e0) % kBatch == 0) {
+            if (!(ok = wait_warp(bar(INFO + n_batch % kNInfo), (n_batch / kNInfo) & 1u, g))) break;
+            ++n_batch;
+          }
+          const Info* half = infos[(n_batch - 1) % kNInfo].half[(e - x.e0) % kBatch];
+          const int valid0 = half[0].valid, valid1 = half[1].valid;
           if (!(ok = wait_warp(bar(V_FULL + vs), (n / kNV) & 1u, g))) break;
           if (!(ok = wait_warp(bar(W_EMPTY + ws), ((n / kNW) & 1u) ^ 1u, g))) break;
           const uint4* from = reinterpret_cast<const uint4*>(gbase + C::kOffV + vs * C::kV);
@@ -576,14 +576,16 @@ attn_cache_tc_kernel(const __grid_constant__ CUtensorMap tk, const __grid_consta
     // -------------------------------------------------------------- softmax + epilogue of this CTA's rows
     const int half = (warp >> 2) & 1, r = (warp & 3) * 32 + lane;   // r: row of the CTA = TMEM lane
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t t_o = col_o + lanes + (uint32_t)half * (D / 2);
-    const int pair_bar = 1 + (warp & 3);         // named barrier of the two warps that share rows
+    const uint32_t t_s = col_s(half) + lanes, t_p = col_p(half) + lanes;   // stage n is that of the half n & 1
+    // named barriers of the two warps that share rows: of both, and of the references of even and of odd stages
+    const int pair_bar = 1 + (warp & 3), ref_bar = 5 + (warp & 3);
     float* ex = reinterpret_cast<float*>(gbase + C::kOffEx) + r;
-    const uint32_t s_free = lead(S_FREE), p_full = lead(P_FULL);
-    uint32_t n = 0, n_ex = 0;                    // stages, exchanges
+    volatile float* ref_at = reinterpret_cast<volatile float*>(gbase + C::kOffRef) + r;
+    const uint32_t s_free = lead(S_FREE + half), p_full = lead(P_FULL + half);
+    uint32_t n = 0, n_ex = 0, n_batch = 0;       // stages, exchanges, batches of facts
     bool ok = true;
-    // The row's other half: gives its value for this one's. The two warps take every step together: a
-    // warp that has given up says so here (NaN with these bits), and both leave after it.
+    // The row's other thread: gives its value for this one's. A warp that has given up says so here, or with the
+    // reference (NaN with these bits); both leave after this.
     constexpr uint32_t kGone = 0x7fc0dead;
     auto exchange = [&](float mine, float& theirs) -> bool {
       float* at = ex + (n_ex++ & 1u) * 2 * kTileRows;   // the other buffer may still be read
@@ -659,93 +661,131 @@ attn_cache_tc_kernel(const __grid_constant__ CUtensorMap tk, const __grid_consta
         if (lane == 0) arrive_cluster(lead(Q_FULL));
       }
       const int last = a.causal ? x.len - x.n + tok : INT32_MAX;   // the last key that the row sees
-      float ref = -INFINITY, l = 0.f;            // R; l times 2^11, of this half's keys
-      // what the row sees of a stage's half, and its scales: fetched while the last stage's scores come
-      int see;
-      float c, lv, inv;
+      float ref = -INFINITY, l = 0.f;            // R; l times 2^11, of this thread's stages
+      // what the row sees of a stage's halves, and their scales: fetched while the scores of the stage before come
+      int see[2];
+      float c[2], lv[2], inv[2];
+      const uint32_t begin_n = n, end_n = n + (uint32_t)(x.e1 - x.e0);
+      int known = -1;                            // batches of this piece that are there
       auto facts = [&](uint32_t n) {
-        const uint32_t is = n % kNInfo;
-        ok = ok && wait_warp(bar(INFO + is), (n / kNInfo) & 1u, g);
-        const int pos = infos[is].pos[half];
-        see = min(infos[is].valid[half], last - pos < 63 ? last - pos + 1 : 64);
-        c = factor * infos[is].ks[half];
-        lv = infos[is].lv[half];
-        inv = infos[is].inv[half];
+        const int j = (int)(n - begin_n), batch = j / kBatch;
+        const uint32_t is = (n_batch + batch) % kNInfo;
+        if (batch > known) {
+          ok = ok && wait_warp(bar(INFO + is), ((n_batch + batch) / kNInfo) & 1u, g);
+          known = batch;
+        }
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const Info& f = infos[is].half[j % kBatch][k];
+          const int4 w = *reinterpret_cast<const int4*>(&f);
+          see[k] = min(w.y, last - w.x < 63 ? last - w.x + 1 : 64);
+          c[k] = factor * __int_as_float(w.z);
+          lv[k] = __int_as_float(w.w);
+          inv[k] = f.inv;
+        }
       };
-      facts(n);
-      for (int e = x.e0; e < x.e1; ++e, ++n) {
-        const uint32_t b = n & 1u;
-        ok = ok && wait_warp(bar(S_FULL + b), (n >> 1) & 1u, g);
+      if ((n & 1u) != (uint32_t)half) ++n;
+      if (n < end_n) facts(n);
+      for (; n < end_n; n += 2) {
+        ok = ok && wait_warp(bar(S_FULL + half), (n >> 1) & 1u, g);
         fence_after();
-        uint32_t s[64];
-        float cm = tmem_ld32_max(col_s(b) + lanes + 64u * half, s);
-        cm = fmaxf(cm, tmem_ld32_max(col_s(b) + lanes + 64u * half + 32u, s + 32));
-        const int see0 = see;
-        const float c0 = c, lv0 = lv, inv0 = inv;
-        const bool cut = __any_sync(0xffffffffu, see0 < 64);
-        if (e + 1 < x.e1) facts(n + 1);
+        uint32_t s[kStageKeys];
+        float cm[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) cm[i] = tmem_ld32_max(t_s + 32u * i, s + 32 * i);
         wait_ld();
         fence_before();
         __syncwarp();
-        if (lane == 0) arrive_cluster(s_free + 8u * b);
-        if (cut) {
-          cm = -INFINITY;
+        if (lane == 0) arrive_cluster(s_free);
+        if (__any_sync(0xffffffffu, see[0] < 64 || see[1] < 64)) {
 #pragma unroll
-          for (int i = 0; i < 64; ++i) {
-            if (i >= see0) s[i] = 0xff800000u;
-            cm = fmaxf(cm, __uint_as_float(s[i]));
+          for (int i = 0; i < 4; ++i) {
+            cm[i] = -INFINITY;
+#pragma unroll
+            for (int k = 0; k < 32; ++k) {
+              if ((i & 1) * 32 + k >= see[i >> 1]) s[32 * i + k] = 0xff800000u;
+              cm[i] = fmaxf(cm[i], __uint_as_float(s[32 * i + k]));
+            }
           }
         }
         // a half without keys says nothing (its product with a scale might)
-        float top = see0 > 0 ? fmaf(cm, c0, lv0) : -INFINITY;
-        if (!exchange(top, theirs)) break;
-        top = fmaxf(top, theirs);
-        float f = 1.f;
-        const bool moves = top > ref + kMoves;   // by itself: not by what other rows hold
-        if (moves) {
-          f = exp2_fast(ref - top);              // 0 for the first
-          ref = top;
-          l *= f;
+        const float top = fmaxf(see[0] > 0 ? fmaf(fmaxf(cm[0], cm[1]), c[0], lv[0]) : -INFINITY,
+                                see[1] > 0 ? fmaf(fmaxf(cm[2], cm[3]), c[1], lv[1]) : -INFINITY);
+        // the reference after the stage before, and this stage's for the one after
+        float was = -INFINITY;
+        if (n > 0) {
+          asm volatile("bar.sync %0, 64;\n" ::"r"(ref_bar + 4 * (half ^ 1)) : "memory");
+          const float got = *ref_at;
+          ok = ok && !__any_sync(0xffffffffu, __float_as_uint(got) == kGone);
+          if (n > begin_n) was = got;
         }
-        const float off = lv0 + kShift - (ref == -INFINITY ? 0.f : ref);
-        float rs[4] = {0.f, 0.f, 0.f, 0.f};
-        uint32_t pk[32];
-#pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          float x0, x1;
-          fma_x2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1]), c0, off, x0, x1);
-          const float p0 = exp2_fast(x0), p1 = exp2_fast(x1);
-          add_x2(rs[2 * (i & 1)], rs[2 * (i & 1) + 1], p0, p1);
-          pk[i] = pack_f16(p0, p1);
-        }
-        l = fmaf((rs[0] + rs[1]) + (rs[2] + rs[3]), inv0, l);
-        // P buffer b was last read by the PV of two stages ago
-        if (n >= 2) ok = ok && wait_warp(bar(PV_DONE + b), ((n - 2) >> 1) & 1u, g);
+        const bool moves = top > was + kMoves;   // by itself: not by what other rows hold
+        const float now = moves ? top : was;
+        __syncwarp();
+        *ref_at = ok ? now : __uint_as_float(kGone);
+        asm volatile("bar.arrive %0, 64;\n" ::"r"(ref_bar + 4 * half) : "memory");
+        if (!ok) break;
+        const float f = moves ? exp2_fast(was - now) : 1.f;   // 0 for the first
+        if (now != ref) l *= exp2_fast(ref - now);            // from where this thread left it
+        ref = now;
+        const float against = ref == -INFINITY ? 0.f : ref;
+        // P's buffer was last read by the PV of two stages ago
+        if (n >= 2) ok = ok && wait_warp(bar(PV_DONE + half), ((n - 2) >> 1) & 1u, g);
         fence_after();
-        tmem_st32(col_p(b) + lanes + 32u * half, pk);
-        if (e > x.e0 && __any_sync(0xffffffffu, moves)) {   // O follows the reference, after the PV of the last stage
-          ok = ok && wait_warp(bar(PV_DONE + (b ^ 1u)), ((n - 1) >> 1) & 1u, g);
+        float sum[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const float off = lv[k] + kShift - against;
+          float rs[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            uint32_t pk[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              float x0, x1;
+              fma_x2(__uint_as_float(s[64 * k + 32 * q + 2 * i]), __uint_as_float(s[64 * k + 32 * q + 2 * i + 1]), c[k], off, x0,
+                     x1);
+              const float p0 = exp2_fast(x0), p1 = exp2_fast(x1);
+              add_x2(rs[2 * (i & 1)], rs[2 * (i & 1) + 1], p0, p1);
+              pk[i] = pack_f16(p0, p1);
+            }
+            tmem_st16(t_p + 32u * k + 16u * q, pk);
+          }
+          sum[k] = (rs[0] + rs[1]) + (rs[2] + rs[3]);
+        }
+        l = fmaf(sum[0], inv[0], fmaf(sum[1], inv[1], l));
+        if (n > begin_n && __any_sync(0xffffffffu, moves)) {   // O follows the reference, after the PV of the last stage
+          ok = ok && wait_warp(bar(PV_DONE + (half ^ 1)), ((n - 1) >> 1) & 1u, g);
           fence_after();
 #pragma unroll
-          for (int i = 0; i < D / 64; ++i) {
+          for (int i = 0; i < D / 32; ++i) {
             uint32_t ov[32];
-            tmem_ld32(t_o + 32u * i, ov);
+            tmem_ld32(col_o + lanes + 32u * i, ov);
             wait_ld();
 #pragma unroll
             for (int q = 0; q < 32; ++q) ov[q] = __float_as_uint(__uint_as_float(ov[q]) * f);
-            tmem_st32(t_o + 32u * i, ov);
+            tmem_st32(col_o + lanes + 32u * i, ov);
           }
         }
         wait_st();
         fence_before();
         __syncwarp();
-        if (lane == 0) arrive_cluster(p_full + 8u * b);
+        if (lane == 0) arrive_cluster(p_full);
+        if (n + 2 < end_n) facts(n + 2);
       }
-      // ---- the end of a piece: the row's whole sum, and half of O from TMEM
+      n = end_n;
+      n_batch += (uint32_t)(x.e1 - x.e0 + kBatch - 1) / kBatch;
+      // ---- the end of a piece: the row's reference and whole sum, and half of O from TMEM
       ok = ok && wait_warp(bar(PV_DONE + ((n - 1) & 1u)), ((n - 1) >> 1) & 1u, g);
+      if (!exchange(ref, theirs)) break;
+      // the thread of the last stage has the reference that holds
+      const float final_ref = ((n - 1) & 1u) == (uint32_t)half ? ref : theirs;
+      if (final_ref != ref) l *= exp2_fast(ref - final_ref);
+      ref = final_ref;
       if (!exchange(l, theirs)) break;
       l = half ? theirs + l : l + theirs;
       fence_after();
+      const uint32_t t_o = col_o + lanes + (uint32_t)half * (D / 2);
       const float scale = l == 0.f ? 0.f : x.part < 0 ? 1.0f / l : 1.f;
       const int64_t at = (int64_t)(x.s0 + tok) * a.H + h;
       float* sums = parts.sum + ((int64_t)max(x.part, 0) * kItemRows + rank * kTileRows + r) * D + half * (D / 2);
