@@ -25,8 +25,10 @@ constexpr int kGrid = 152 * 3;     // CTAs that share the work, at most (the wor
 // CTAs per SM: what the accumulators of 8 or 16 rows leave registers for.
 constexpr int ctas_per_sm(int d, int nt) { return d == 128 && nt == 2 ? 2 : 3; }
 constexpr int kWideUnits = 16;     // units of a piece from which on a warp takes whole units
-constexpr int kItemCost = 4;       // units that an item's own work (its look-ups, queries, join) counts as
-constexpr int kMinUnits = 6;       // units, an item's own among them, that are worth a CTA
+// Units that an item's own work (its look-ups, queries, join) counts as: 16 uneven requests of 40 heads, d = 64, take
+// 99 us at 2, 71 at 4, 69 at 6, 71 at 8, 73 at 12; 256 requests of at most 256 keys 32, 33, 34, 34 from 4 on.
+constexpr int kItemCost = 6;
+constexpr int kMinUnits = kItemCost + 2;   // units, an item's own among them, that are worth a CTA
 constexpr float kPScale = 2048.f;  // P is at most 16 and is held as 2^11 P in f16: 2^-35 is not lost
 
 template <int RT>   // query rows of an item
@@ -104,7 +106,7 @@ attn_cache_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
   __shared__ uint64_t s_full[kWarps][kStages];
   auto full = [&](int st) { return tc::smem_u32(&s_full[warp][st]); };
   uint32_t phases = 0;                         // of the stages' barriers
-  bool late = false;                           // a wait has expired: nothing more is copied or waited for
+  bool late = false;                           // a wait has expired: nothing more is copied, what is on its way is waited for
   if (lane == 0) {
     for (int i = 0; i < kStages; ++i) tc::mbar_init(full(i), 1);
     tc::fence_barrier_init();
@@ -213,12 +215,12 @@ attn_cache_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
       if (i < steps) {
         const int q = 16 * (wide ? i & 3 : warp);
         first[st] = pos + q;
-        valid[st] = max(0, min(16, exist - q));
+        valid[st] = late ? 0 : max(0, min(16, exist - q));
         if (valid[st] > 0) {
           const int64_t block = (int64_t)page * a.c.heads + hk;
           ks[st] = __ldg(a.ks + block);
           vs[st] = __ldg(a.vs + block);
-          if (lane == 0 && !late) {
+          if (lane == 0) {
             tc::mbar_arrive_expect_tx(full(st), (uint32_t)sizeof(Stage<D>));
             tc::tma_load_3d(tc::smem_u32(ring[st].k), &map_k, full(st), 0, row + q, page);
             tc::tma_load_3d(tc::smem_u32(ring[st].v), &map_v, full(st), 0, row + q, page);
@@ -291,6 +293,8 @@ attn_cache_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
     }
 
     auto step = [&](const Stage<D>& st, int at, int n, float ks, float vs) {
+      // vs goes into the weights, and out of their sum again: one fma less for every element of O
+      const float lv = __log2f(fmaxf(vs, 0x1p-120f)), inv = exp2_fast(-lv);
       float c[NT][4], c2[NT][4];                // two sums, so that products need not wait for one another
 #pragma unroll
       for (int j = 0; j < NT; ++j)
@@ -313,15 +317,14 @@ attn_cache_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
       for (int j = 0; j < NT; ++j)
 #pragma unroll
         for (int i = 0; i < 4; ++i) c[j][i] += c2[j][i];
-      const float vf = vs * (1.0f / kPScale);
       bool moved = false;
 #pragma unroll
       for (int j = 0; j < NT; ++j)
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const float f = factor[j][i] * ks;
-          c[j][i] = g < n && at + g <= last[j][i] ? c[j][i] * f : -INFINITY;
-          c[j][2 + i] = g + 8 < n && at + g + 8 <= last[j][i] ? c[j][2 + i] * f : -INFINITY;
+          c[j][i] = g < n && at + g <= last[j][i] ? fmaf(c[j][i], f, lv) : -INFINITY;
+          c[j][2 + i] = g + 8 < n && at + g + 8 <= last[j][i] ? fmaf(c[j][2 + i], f, lv) : -INFINITY;
           // the maximum follows when a score passes it by more than 2^4
           moved |= fmaxf(c[j][i], c[j][2 + i]) > m[j][i] + 4.f;
         }
@@ -354,8 +357,9 @@ attn_cache_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           e[i] = c[j][i] == -INFINITY ? 0.f : exp2_fast(c[j][i] - m[j][i & 1]);
-          l[j][i & 1] += e[i];
         }
+        l[j][0] = fmaf(e[0] + e[2], inv, l[j][0]);
+        l[j][1] = fmaf(e[1] + e[3], inv, l[j][1]);
         p[j][0] = transposed(pack_f16(e[0] * kPScale, e[1] * kPScale));
         p[j][1] = transposed(pack_f16(e[2] * kPScale, e[3] * kPScale));
       }
@@ -389,12 +393,7 @@ attn_cache_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
         const uint32_t a0 = f16x2_of_e4m3(lo), a1 = f16x2_of_e4m3(lo >> 16), a2 = f16x2_of_e4m3(hi),
                        a3 = f16x2_of_e4m3(hi >> 16);
 #pragma unroll
-        for (int j = 0; j < NT; ++j) {
-          float d[4] = {0.f, 0.f, 0.f, 0.f};
-          mma(d, a0, a1, a2, a3, p[j][0], p[j][1]);
-#pragma unroll
-          for (int k = 0; k < 4; ++k) o[j][i][k] = fmaf(d[k], vf, o[j][i][k]);
-        }
+        for (int j = 0; j < NT; ++j) mma(o[j][i], a0, a1, a2, a3, p[j][0], p[j][1]);
       }
     };
 
@@ -403,7 +402,7 @@ attn_cache_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
       for (int s = 0; s < kStages; ++s) {
         ahead(i + s + kStages - 1, (s + kStages - 1) % kStages);
         if (i + s < steps && valid[s] > 0) {
-          if (!late && !wait_for(full(s), (phases >> s) & 1u)) {
+          if (!wait_for(full(s), (phases >> s) & 1u)) {
             late = true;
             report(a.d_status, SPARSP_ERR_TIMEOUT);
           }
@@ -434,7 +433,7 @@ attn_cache_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
 #pragma unroll
         for (int k = 0; k < 2; ++k)
           *reinterpret_cast<float2*>(&s_o[warp][j * 8 + 2 * t + k][D / 8 * g + 2 * i]) =
-              make_float2(o[j][i][k], o[j][i][k + 2]);
+              make_float2(o[j][i][k] * (1.f / kPScale), o[j][i][k + 2] * (1.f / kPScale));
     __syncthreads();
     const bool whole = u0 == 0 && u1 == units;
     const int slot = 2 * (int)cta + (u0 > 0 ? 0 : 1);     // a piece that goes on is the CTA's first
