@@ -29,7 +29,7 @@
 //              of K, half of the columns of V.
 //   warp 13, first CTA: issues S of both (A = q1, q2, B = K, K-major, from shared memory).
 //   warp 14, first CTA: issues O += P V (A = P in TMEM, B = V MN-major).
-// TMEM (512 columns): S of two stages [0, 256), O [256, 256 + d), P of two stages [384, 512).
+// TMEM (512 columns): S of three stages, and in its place P, [0, 384), O [384, 384 + d).
 // The first CTA's barriers count what its products wait for in both CTAs (remote arrivals); its commits
 // reach both. Every mbarrier wait is bounded (2 s); on expiry the CTA sets SPARSP_ERR_TIMEOUT, all roles
 // leave their loops, copies and MMAs in flight are drained with a second bounded wait, and
@@ -48,16 +48,16 @@ constexpr int kTileRows = 128, kItemRows = 2 * kTileRows, kStageKeys = 128;
 constexpr int kItemCost = 6;       // stages that an item's own work counts as
 constexpr int kMinStages = 10;     // stages, an item's own among them, that are worth a cluster
 constexpr float kShift = 11.f, kMoves = 4.f;   // P is held as 2^11 times what it is against R
-constexpr int kNK = 6, kNV = 4, kNW = 3, kNInfo = 8, kNItems = 2;
+constexpr int kNK = 6, kNV = 4, kNW = 3, kNInfo = 8, kNItems = 2, kNS = 3;
 constexpr uint64_t kWaitNs = 2000000000ull, kDrainNs = 200000000ull;
 constexpr int kSoftmax = 8, W_WIDEN = kSoftmax, W_PROD = W_WIDEN + 4, W_S = W_PROD + 1, W_PV = W_PROD + 2;   // warps
 
-// First CTA: K_FULL, W_FULL, Q_FULL, S_FREE, P_FULL and O_EMPTY count both CTAs.
+// First CTA: K_FULL, W_FULL, Q_FULL, P_FULL and O_EMPTY count both CTAs.
 enum Bars {
   K_FULL, K_EMPTY = K_FULL + kNK, V_FULL = K_EMPTY + kNK, V_EMPTY = V_FULL + kNV, W_FULL = V_EMPTY + kNV,
   W_EMPTY = W_FULL + kNW, INFO = W_EMPTY + kNW, I_FULL = INFO + kNInfo, I_EMPTY = I_FULL + kNItems,
-  Q_FULL = I_EMPTY + kNItems, S_FULL, S_FREE = S_FULL + 2, P_FULL = S_FREE + 2, PV_DONE = P_FULL + 2,
-  O_EMPTY = PV_DONE + 2, TEAR, TEAR_PV, NBAR
+  Q_FULL = I_EMPTY + kNItems, S_FULL, P_FULL = S_FULL + kNS, PV_DONE = P_FULL + kNS, O_EMPTY = PV_DONE + kNS,
+  TEAR, TEAR_PV, NBAR
 };
 
 // A piece of an item: stages [e0, e1) of it. e1 < 0: no more.
@@ -294,10 +294,9 @@ attn_cache_tc_kernel(const __grid_constant__ CUtensorMap tk, const __grid_consta
     init(I_FULL, kNItems, 1);
     init(I_EMPTY, kNItems, kSoftmax + 4 + (rank == 0 ? 2 : 0));   // softmax, widening and issuing warps
     init(Q_FULL, 1, 2 * kSoftmax);
-    init(S_FULL, 2, 1);
-    init(S_FREE, 2, kSoftmax);    // a stage is four warps' in each CTA
-    init(P_FULL, 2, kSoftmax);
-    init(PV_DONE, 2, 1);
+    init(S_FULL, kNS, 1);
+    init(P_FULL, kNS, kSoftmax);  // a stage is four warps' in each CTA
+    init(PV_DONE, kNS, 1);
     init(O_EMPTY, 1, 2 * kSoftmax);
     init(TEAR, 2, 1);
     *abort_flag = 0;
@@ -317,9 +316,8 @@ attn_cache_tc_kernel(const __grid_constant__ CUtensorMap tk, const __grid_consta
   fence_after();
   const uint32_t tmem = *tmem_slot;
   const Guard g{abort_flag, a.d_status, kWaitNs};
-  const uint32_t col_o = tmem + 256u;
-  auto col_s = [&](uint32_t b) { return tmem + b * 128u; };
-  auto col_p = [&](uint32_t b) { return tmem + 384u + b * 64u; };
+  const uint32_t col_o = tmem + 384u;
+  auto col_s = [&](uint32_t b) { return tmem + b * 128u; };   // S, and then P in the first 64 columns
   // The next piece from the ring; false at the end or on abort. The slot is given back at once.
   uint32_t it_use = 0;
   auto next_piece = [&](Piece& x) -> bool {
@@ -469,9 +467,9 @@ attn_cache_tc_kernel(const __grid_constant__ CUtensorMap tk, const __grid_consta
       while (ok && next_piece(x)) {
         if (!(ok = wait_pair(bar(Q_FULL), n_q++ & 1u, g))) break;
         for (int e = x.e0; e < x.e1; ++e, ++n) {
-          const uint32_t ks = n % kNK, b = n & 1u;
+          const uint32_t ks = n % kNK, b = n % kNS;
           if (!(ok = wait_pair(bar(K_FULL + ks), (n / kNK) & 1u, g))) break;
-          if (!(ok = wait_pair(bar(S_FREE + b), ((n >> 1) & 1u) ^ 1u, g))) break;
+          if (!(ok = wait_warp(bar(PV_DONE + b), ((n / kNS) & 1u) ^ 1u, g))) break;
           fence_after();
           if (elect_one()) {
 #pragma unroll
@@ -501,15 +499,15 @@ attn_cache_tc_kernel(const __grid_constant__ CUtensorMap tk, const __grid_consta
       Piece x;
       while (ok && next_piece(x)) {
         for (int e = x.e0; e < x.e1; ++e, ++n) {
-          const uint32_t ws = n % kNW, b = n & 1u;
+          const uint32_t ws = n % kNW, b = n % kNS;
           if (!(ok = wait_pair(bar(W_FULL + ws), (n / kNW) & 1u, g))) break;
-          if (!(ok = wait_pair(bar(P_FULL + b), (n >> 1) & 1u, g))) break;
+          if (!(ok = wait_pair(bar(P_FULL + b), (n / kNS) & 1u, g))) break;
           if (e == x.e0 && !(ok = wait_pair(bar(O_EMPTY), (n_o++ & 1u) ^ 1u, g))) break;
           fence_after();
           if (elect_one()) {
 #pragma unroll
             for (int kk = 0; kk < kStageKeys / 16; ++kk)
-              mma_f16(col_o, col_p(b) + 8u * kk, smem_desc(sW + ws * C::kW + 16u * D * kk, 16, C::kAtom, C::kSwz), idesc(D, 1),
+              mma_f16(col_o, col_s(b) + 8u * kk, smem_desc(sW + ws * C::kW + 16u * D * kk, 16, C::kAtom, C::kSwz), idesc(D, 1),
                       e > x.e0 || kk > 0 ? 1u : 0u);
             commit_both(bar(PV_DONE + b));
             commit_both(bar(W_EMPTY + ws));
@@ -576,12 +574,11 @@ attn_cache_tc_kernel(const __grid_constant__ CUtensorMap tk, const __grid_consta
     // -------------------------------------------------------------- softmax + epilogue of this CTA's rows
     const int half = (warp >> 2) & 1, r = (warp & 3) * 32 + lane;   // r: row of the CTA = TMEM lane
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t t_s = col_s(half) + lanes, t_p = col_p(half) + lanes;   // stage n is that of the half n & 1
     // named barriers of the two warps that share rows: of both, and of the references of even and of odd stages
     const int pair_bar = 1 + (warp & 3), ref_bar = 5 + (warp & 3);
     float* ex = reinterpret_cast<float*>(gbase + C::kOffEx) + r;
     volatile float* ref_at = reinterpret_cast<volatile float*>(gbase + C::kOffRef) + r;
-    const uint32_t s_free = lead(S_FREE + half), p_full = lead(P_FULL + half);
+    const uint32_t p_full = lead(P_FULL);
     uint32_t n = 0, n_ex = 0, n_batch = 0;       // stages, exchanges, batches of facts
     bool ok = true;
     // The row's other thread: gives its value for this one's. A warp that has given up says so here, or with the
@@ -687,16 +684,14 @@ attn_cache_tc_kernel(const __grid_constant__ CUtensorMap tk, const __grid_consta
       if ((n & 1u) != (uint32_t)half) ++n;
       if (n < end_n) facts(n);
       for (; n < end_n; n += 2) {
-        ok = ok && wait_warp(bar(S_FULL + half), (n >> 1) & 1u, g);
+        const uint32_t sb = n % kNS, t_s = col_s(sb) + lanes;
+        ok = ok && wait_warp(bar(S_FULL + sb), (n / kNS) & 1u, g);
         fence_after();
         uint32_t s[kStageKeys];
         float cm[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) cm[i] = tmem_ld32_max(t_s + 32u * i, s + 32 * i);
         wait_ld();
-        fence_before();
-        __syncwarp();
-        if (lane == 0) arrive_cluster(s_free);
         if (__any_sync(0xffffffffu, see[0] < 64 || see[1] < 64)) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
@@ -729,9 +724,6 @@ attn_cache_tc_kernel(const __grid_constant__ CUtensorMap tk, const __grid_consta
         if (now != ref) l *= exp2_fast(ref - now);            // from where this thread left it
         ref = now;
         const float against = ref == -INFINITY ? 0.f : ref;
-        // P's buffer was last read by the PV of two stages ago
-        if (n >= 2) ok = ok && wait_warp(bar(PV_DONE + half), ((n - 2) >> 1) & 1u, g);
-        fence_after();
         float sum[2];
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
@@ -749,13 +741,13 @@ attn_cache_tc_kernel(const __grid_constant__ CUtensorMap tk, const __grid_consta
               add_x2(rs[2 * (i & 1)], rs[2 * (i & 1) + 1], p0, p1);
               pk[i] = pack_f16(p0, p1);
             }
-            tmem_st16(t_p + 32u * k + 16u * q, pk);
+            tmem_st16(t_s + 32u * k + 16u * q, pk);
           }
           sum[k] = (rs[0] + rs[1]) + (rs[2] + rs[3]);
         }
         l = fmaf(sum[0], inv[0], fmaf(sum[1], inv[1], l));
         if (n > begin_n && __any_sync(0xffffffffu, moves)) {   // O follows the reference, after the PV of the last stage
-          ok = ok && wait_warp(bar(PV_DONE + (half ^ 1)), ((n - 1) >> 1) & 1u, g);
+          ok = ok && wait_warp(bar(PV_DONE + (n - 1) % kNS), ((n - 1) / kNS) & 1u, g);
           fence_after();
 #pragma unroll
           for (int i = 0; i < D / 32; ++i) {
@@ -770,13 +762,13 @@ attn_cache_tc_kernel(const __grid_constant__ CUtensorMap tk, const __grid_consta
         wait_st();
         fence_before();
         __syncwarp();
-        if (lane == 0) arrive_cluster(p_full);
+        if (lane == 0) arrive_cluster(p_full + 8u * sb);
         if (n + 2 < end_n) facts(n + 2);
       }
       n = end_n;
       n_batch += (uint32_t)(x.e1 - x.e0 + kBatch - 1) / kBatch;
       // ---- the end of a piece: the row's reference and whole sum, and half of O from TMEM
-      ok = ok && wait_warp(bar(PV_DONE + ((n - 1) & 1u)), ((n - 1) >> 1) & 1u, g);
+      ok = ok && wait_warp(bar(PV_DONE + (n - 1) % kNS), ((n - 1) / kNS) & 1u, g);
       if (!exchange(ref, theirs)) break;
       // the thread of the last stage has the reference that holds
       const float final_ref = ((n - 1) & 1u) == (uint32_t)half ? ref : theirs;
