@@ -684,6 +684,16 @@ attn_cache_tc_kernel(const __grid_constant__ CUtensorMap tk, const __grid_consta
       if ((n & 1u) != (uint32_t)half) ++n;
       if (n < end_n) facts(n);
       for (; n < end_n; n += 2) {
+        // What needs shared memory comes while S does: beside the products' reads every access takes hundreds of
+        // cycles. The reference after the stage before:
+        float was = -INFINITY;
+        if (n > 0) {
+          asm volatile("bar.sync %0, 64;\n" ::"r"(ref_bar + 4 * (half ^ 1)) : "memory");
+          const float got = *ref_at;
+          ok = ok && !__any_sync(0xffffffffu, __float_as_uint(got) == kGone);
+          if (n > begin_n) was = got;
+        }
+        const bool cut = __any_sync(0xffffffffu, see[0] < 64 || see[1] < 64);
         const uint32_t sb = n % kNS, t_s = col_s(sb) + lanes;
         ok = ok && wait_warp(bar(S_FULL + sb), (n / kNS) & 1u, g);
         fence_after();
@@ -692,7 +702,7 @@ attn_cache_tc_kernel(const __grid_constant__ CUtensorMap tk, const __grid_consta
 #pragma unroll
         for (int i = 0; i < 4; ++i) cm[i] = tmem_ld32_max(t_s + 32u * i, s + 32 * i);
         wait_ld();
-        if (__any_sync(0xffffffffu, see[0] < 64 || see[1] < 64)) {
+        if (cut) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             cm[i] = -INFINITY;
@@ -706,14 +716,7 @@ attn_cache_tc_kernel(const __grid_constant__ CUtensorMap tk, const __grid_consta
         // a half without keys says nothing (its product with a scale might)
         const float top = fmaxf(see[0] > 0 ? fmaf(fmaxf(cm[0], cm[1]), c[0], lv[0]) : -INFINITY,
                                 see[1] > 0 ? fmaf(fmaxf(cm[2], cm[3]), c[1], lv[1]) : -INFINITY);
-        // the reference after the stage before, and this stage's for the one after
-        float was = -INFINITY;
-        if (n > 0) {
-          asm volatile("bar.sync %0, 64;\n" ::"r"(ref_bar + 4 * (half ^ 1)) : "memory");
-          const float got = *ref_at;
-          ok = ok && !__any_sync(0xffffffffu, __float_as_uint(got) == kGone);
-          if (n > begin_n) was = got;
-        }
+        // this stage's reference, for the one after
         const bool moves = top > was + kMoves;   // by itself: not by what other rows hold
         const float now = moves ? top : was;
         __syncwarp();
