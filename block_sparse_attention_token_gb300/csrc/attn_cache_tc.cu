@@ -14,6 +14,15 @@
 // so that blocks of any scales add up in one accumulator; P is at most 2^15 (R follows when
 // it is passed by more than 2^4) and not below 2^-24 f16 has nothing to add.
 //
+// Measured: 1,536 queries x 30,720 keys x 40 heads of d = 128 take 630 us when they come alone (0.81 of the bf16
+// peak for the two products, 0.73 back to back under the power cap), d = 64 525 us, 4 prompts of 4,096 tokens x 32
+// heads 442 us. Counted in cycles, a stage of 128 keys is 1,570 (d = 64: 1,290) where its products take 1,090
+// (545): a row's thread spends 3,140 on each second stage, 950 of them on 128 exponentials and their sum, 200 on
+// handing P over, 300 each on reading what it has to know of the keys and on waiting for the other thread's
+// reference, 470 on waiting for S (d = 64: 230). No pipe is full (tensor 0.70, exponentials 0.33); what bounds it
+// is the round S - exponentials - P V, of which three fit tensor memory. What it gained from: pairs of SMs (846 ->
+// 725), a look-up for 16 stages at a time instead of every stage (718 -> 661), P in S's place (661 -> 651).
+//
 // Two SMs work on 256 query rows (heads that share a key head, and tokens, side by side) as one
 // cluster of two CTAs with paired products (cta_group::2): each has 128 of the rows in its tensor memory, and
 // each loads one half of K's keys and of V's columns, so that every byte of the cache is loaded and widened once
@@ -45,10 +54,13 @@ namespace {
 using namespace tc;
 
 constexpr int kTileRows = 128, kItemRows = 2 * kTileRows, kStageKeys = 128;
-constexpr int kItemCost = 6;       // stages that an item's own work counts as
+constexpr int kItemCost = 6;       // stages that an item's own work (queries, epilogue, join) counts as: 9,000 cycles
 constexpr int kMinStages = 10;     // stages, an item's own among them, that are worth a cluster
 constexpr float kShift = 11.f, kMoves = 4.f;   // P is held as 2^11 times what it is against R
-constexpr int kNK = 6, kNV = 4, kNW = 3, kNInfo = 8, kNItems = 2, kNS = 3;
+constexpr int kNK = 6, kNV = 4, kNW = 3, kNItems = 2, kNS = 3;
+// Batches of facts in the ring. Nobody hands one back: K's ring lets the producer run at most ten stages ahead of
+// any reader, and kNItems keeps those in three pieces, so that no more than five batches are in use.
+constexpr int kNInfo = 8;
 constexpr uint64_t kWaitNs = 2000000000ull, kDrainNs = 200000000ull;
 constexpr int kSoftmax = 8, W_WIDEN = kSoftmax, W_PROD = W_WIDEN + 4, W_S = W_PROD + 1, W_PV = W_PROD + 2;   // warps
 
@@ -659,7 +671,7 @@ attn_cache_tc_kernel(const __grid_constant__ CUtensorMap tk, const __grid_consta
       }
       const int last = a.causal ? x.len - x.n + tok : INT32_MAX;   // the last key that the row sees
       float ref = -INFINITY, l = 0.f;            // R; l times 2^11, of this thread's stages
-      // what the row sees of a stage's halves, and their scales: fetched while the scores of the stage before come
+      // what the row sees of a stage's halves, and their scales
       int see[2];
       float c[2], lv[2], inv[2];
       const uint32_t begin_n = n, end_n = n + (uint32_t)(x.e1 - x.e0);
@@ -682,17 +694,17 @@ attn_cache_tc_kernel(const __grid_constant__ CUtensorMap tk, const __grid_consta
         }
       };
       if ((n & 1u) != (uint32_t)half) ++n;
-      if (n < end_n) facts(n);
       for (; n < end_n; n += 2) {
-        // What needs shared memory comes while S does: beside the products' reads every access takes hundreds of
-        // cycles. The reference after the stage before:
+        // What needs shared memory comes while S does, as beside the products' reads every access takes hundreds of
+        // cycles (651 -> 629 us): the reference after the stage before, and what is known of the keys.
         float was = -INFINITY;
         if (n > 0) {
           asm volatile("bar.sync %0, 64;\n" ::"r"(ref_bar + 4 * (half ^ 1)) : "memory");
-          const float got = *ref_at;
-          ok = ok && !__any_sync(0xffffffffu, __float_as_uint(got) == kGone);
-          if (n > begin_n) was = got;
+          was = *ref_at;
         }
+        facts(n);
+        ok = ok && !__any_sync(0xffffffffu, __float_as_uint(was) == kGone);
+        if (n == begin_n) was = -INFINITY;
         const bool cut = __any_sync(0xffffffffu, see[0] < 64 || see[1] < 64);
         const uint32_t sb = n % kNS, t_s = col_s(sb) + lanes;
         ok = ok && wait_warp(bar(S_FULL + sb), (n / kNS) & 1u, g);
@@ -719,7 +731,6 @@ attn_cache_tc_kernel(const __grid_constant__ CUtensorMap tk, const __grid_consta
         // this stage's reference, for the one after
         const bool moves = top > was + kMoves;   // by itself: not by what other rows hold
         const float now = moves ? top : was;
-        __syncwarp();
         *ref_at = ok ? now : __uint_as_float(kGone);
         asm volatile("bar.arrive %0, 64;\n" ::"r"(ref_bar + 4 * half) : "memory");
         if (!ok) break;
@@ -766,7 +777,6 @@ attn_cache_tc_kernel(const __grid_constant__ CUtensorMap tk, const __grid_consta
         fence_before();
         __syncwarp();
         if (lane == 0) arrive_cluster(p_full + 8u * sb);
-        if (n + 2 < end_n) facts(n + 2);
       }
       n = end_n;
       n_batch += (uint32_t)(x.e1 - x.e0 + kBatch - 1) / kBatch;
