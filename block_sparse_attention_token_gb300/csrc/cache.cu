@@ -17,7 +17,10 @@
 // one rounding of x and the same for every way of computing it, and lets a block that
 // grows be brought to a larger scale with no error but the codes' own subnormals. A run
 // of new tokens in one block is one pass: its values wait in registers for their
-// maximum. Bound by HBM.
+// maximum. Bound by HBM: 30,720 tokens x 40 heads of 128 take 153 us, 0.91 of a copy's rate
+// (K and V of several heads to a CTA, the next ones on their way meanwhile; with one task to a CTA 199). 256 runs of
+// one token take 7 us on the device, a chain of four dependent loads; tables of 4,096 requests 14 us, 5 of
+// them the scan, of 64 requests 8.
 #include <cuda_fp16.h>
 
 #include <type_traits>
@@ -324,11 +327,21 @@ cache_write_kernel(const CacheDims c, const CacheWrite a, int granule, int heads
       if (r0 + u * kPer < count)
         store_codes<T>(base + (off + r0 + u * kPer) * D + c0 * E, w[u], inverse, finite);
     if (kept && scale != old) {                      // older tokens, brought to the larger scale
+      // eight (four) words at a time, as a warp may have 127 rows to bring along: 256 runs of one token with cold caches
+      // took 43 us word by word, not 19
+      constexpr int kStep = decltype(threads)::value, kAt = kStep == 32 ? 8 : 4;
       const float ratio = old * inverse;
-      for (int i = t; i < off * D / 4; i += decltype(threads)::value) {
-        uint32_t& word = reinterpret_cast<uint32_t*>(base)[i];
-        const float2 lo = e4m3_values(word & 0xffffu), hi = e4m3_values(word >> 16);
-        word = e4m3_pair(lo.x * ratio, lo.y * ratio) | e4m3_pair(hi.x * ratio, hi.y * ratio) << 16;
+      uint32_t* codes = reinterpret_cast<uint32_t*>(base) + t;
+      for (int n = off * D / 4 - t; n > 0; n -= kAt * kStep, codes += kAt * kStep) {
+        uint32_t held[kAt];
+#pragma unroll
+        for (int k = 0; k < kAt; ++k) held[k] = k * kStep < n ? codes[k * kStep] : 0;
+#pragma unroll
+        for (int k = 0; k < kAt; ++k) {
+          const float2 lo = e4m3_values(held[k] & 0xffffu), hi = e4m3_values(held[k] >> 16);
+          if (k * kStep < n)
+            codes[k * kStep] = e4m3_pair(lo.x * ratio, lo.y * ratio) | e4m3_pair(hi.x * ratio, hi.y * ratio) << 16;
+        }
       }
     }
   };
