@@ -12,7 +12,11 @@
 // K, and the rows of V^T are columns of vectors that a lane reads anyway. Every warp has a ring of
 // stages of its own, filled by TMA. Work is counted in units of 64 keys over all requests
 // and key heads and dealt out evenly: a CTA takes a range of units, and an item (request, key head, 8 or 16 rows) that
-// spans several CTAs leaves partial sums that a second kernel joins in order.
+// spans several CTAs leaves partial sums that a second kernel joins in order. vs goes into the weights and out of
+// their sum again (P = 2^(y + log2 vs - m), l = sum P / vs), so that the products of all blocks add up in place.
+// Measured (32 heads over 8, d = 128): 64 uneven requests of up to 32,768 tokens 80 us (0.82 of a copy's rate); 8 x 4
+// rows over a tenth of 131,072 keys 55 us (0.57; 20 us of it fixed: scan and look-ups at the latency of a cold cache,
+// the warps' join, the second kernel); one request of 1,024 keys 11 us on the device.
 #include "cache_items.cuh"
 #include "rows.cuh"
 
@@ -22,9 +26,12 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kGrid = 152 * 3;     // CTAs that share the work, at most (the workspace depends on it)
-// CTAs per SM: what the accumulators of 8 or 16 rows leave registers for.
+// CTAs per SM: what the accumulators of 8 or 16 rows leave registers for (three with 16 rows and d = 128 spill 260
+// bytes a thread: 75 us in the place of 67 for the sparse lists above).
 constexpr int ctas_per_sm(int d, int nt) { return d == 128 && nt == 2 ? 2 : 3; }
-constexpr int kWideUnits = 16;     // units of a piece from which on a warp takes whole units
+// Units of a piece from which on a warp takes whole units: at 8, 16, 32 one request of 1,024 keys takes 16.4, 15.4,
+// 15.5 us, 16 uneven requests 70.8, 70.2, 72.8.
+constexpr int kWideUnits = 16;
 // Units that an item's own work (its look-ups, queries, join) counts as: 16 uneven requests of 40 heads, d = 64, take
 // 99 us at 2, 71 at 4, 69 at 6, 71 at 8, 73 at 12; 256 requests of at most 256 keys 32, 33, 34, 34 from 4 on.
 constexpr int kItemCost = 6;
@@ -57,7 +64,7 @@ __device__ __forceinline__ uint32_t transposed(uint32_t v) {
 }
 // A warp's ring of 16-key stages, filled by TMA (swizzled by the length of a row, so that the reads
 // below meet no bank twice) and waited for on a barrier per stage.
-constexpr int kStages = 3;
+constexpr int kStages = 3;         // 3, 4, 5, 6: 59.9, 60.7, 62.5, 63.6 us for the sparse lists above
 constexpr uint64_t kWaitNs = 2000000000ull;
 template <int D>
 struct Stage {
@@ -548,7 +555,9 @@ sparsp_status_t go(const CacheAttn& a, void* ws, cudaStream_t st) {
 // Requests with up to kFew rows (tokens times heads that share a key head) are this file's
 // kernel's, the others those of attn_cache_tc.cu. Where the packed rows leave room for no request
 // shorter than the longest, that one takes all, and a launch is saved.
-constexpr int kFew = 16;
+// 32 requests of 8,192 keys, 8 key heads of 128, with 16, 32, 64, 128 rows: here 116, 156, 247, 424 us (rows beyond 16 read
+// the cache again), there 312, 181, 206, 223.
+constexpr int kFew = 32;
 bool many(int group, int max_add) { return (int64_t)group * max_add > kFew; }
 
 }  // namespace
