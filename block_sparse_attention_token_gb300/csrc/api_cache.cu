@@ -43,6 +43,15 @@ sparsp_status_t check_pools(const void* kc, const float* ks, const void* vc, con
   return SPARSP_OK;
 }
 
+// Words of 32 bits that an argument takes up.
+struct Words {
+  const void* p;
+  int64_t n;
+  bool meets(const Words& o) const {
+    return n > 0 && o.n > 0 && (const uint8_t*)p < (const uint8_t*)o.p + 4 * o.n && (const uint8_t*)o.p < (const uint8_t*)p + 4 * n;
+  }
+};
+
 sparsp_status_t check_attn(const sparsp_cache_t* cache, int32_t B, int32_t H, int64_t tokens, int32_t max_add,
                            int32_t max_blocks, CacheDims* c) {
   sparsp_status_t r = check_cache(cache, c);
@@ -80,13 +89,17 @@ sparsp_status_t sparsp_cache_extend(const sparsp_cache_t* cache, int32_t B, int3
   if (tokens > 0) CHECK_PTR(slots);
   CHECK_OPT_PTR(used_out);
   CHECK_OPT_PTR(d_status);
-  const size_t n = (size_t)B * sizeof(int32_t);
-  auto meets = [](const void* p, size_t np, const void* q, size_t nq) {
-    return (const uint8_t*)p < (const uint8_t*)q + nq && (const uint8_t*)q < (const uint8_t*)p + np;
-  };
-  if ((len_out != len && meets(len_out, n, len, n)) || meets(len_out, n, add, n) || meets(start, n + 4, len, n) ||
-      meets(start, n + 4, add, n) || meets(start, n + 4, len_out, n))
-    return SPARSP_ERR_INVALID_ARG;
+  // len_out may be len and used_out used; nothing else that is written may be read or written elsewhere
+  const Words in[] = {{len, B}, {add, B}, {free_blocks, n_free}, {used, used != nullptr}};
+  const Words out[] = {{len_out, B}, {used_out, used_out != nullptr}, {start, (int64_t)B + 1}, {slots, tokens},
+                       {table, (int64_t)B * max_blocks}};
+  for (int o = 0; o < 5; ++o) {
+    for (const Words& i : in)
+      if (out[o].meets(i) && !(out[o].p == i.p && (out[o].p == len_out ? i.p == len : out[o].p == used_out && i.p == used)))
+        return SPARSP_ERR_INVALID_ARG;
+    for (int other = 0; other < o; ++other)
+      if (out[o].meets(out[other])) return SPARSP_ERR_INVALID_ARG;
+  }
   CacheExtend a{B, max_blocks, n_free, (int)tokens, len, add, free_blocks, used, table, len_out, start, slots, used_out};
   return launch_cache_extend(c, a, d_status, (cudaStream_t)stream);
 }
@@ -155,8 +168,9 @@ sparsp_status_t sparsp_attn_cache_fwd(const sparsp_cache_t* cache, int32_t B, in
   CHECK_PTR(ws);
   if (ws_bytes < attn_cache_ws(a.c, H / a.c.heads, max_add)) return SPARSP_ERR_WORKSPACE;
   if (tokens == 0) return SPARSP_OK;
-  const uint8_t *pq = (const uint8_t*)q, *po = (const uint8_t*)o;
-  if (pq < po + tokens * row * 2 && po < pq + ((tokens - 1) * q_stride + row) * 2) return SPARSP_ERR_INVALID_ARG;
+  // (row is even)
+  const Words wq{q, ((tokens - 1) * q_stride + row) / 2}, wo{o, tokens * row / 2}, wl{lse, tokens * H};
+  if (wq.meets(wo) || wq.meets(wl) || wo.meets(wl)) return SPARSP_ERR_INVALID_ARG;
   a.B = B;
   a.H = H;
   a.group = H / a.c.heads;

@@ -731,6 +731,7 @@ typedef struct {
  *            their number.
  *   slots    int32 [tokens]: slot of every packed new token; -1 past the last one.
  *   used_out device word or NULL: used + the blocks handed out (may be used itself).
+ * Otherwise nothing that is written may overlap what is read or written elsewhere.
  * A request whose need is not covered, or whose tokens do not fit in `tokens`, sets
  * SPARSP_ERR_CAPACITY and waits, and so does every later one that needs a block (or
  * brings tokens past the end): len_out = len, slots -1, no blocks; its tokens keep their
@@ -777,15 +778,18 @@ SPARSP_API sparsp_status_t sparsp_cache_write(const sparsp_cache_t* cache, int32
  * o: bf16 [tokens, H, d], lse: float32 [tokens, H]. A row that sees no key gives O = 0,
  * LSE = -inf; one that sees a score of NaN or +inf gives NaN in both. Rows outside every
  * request are left as they were. Values of keys that a row does not see must not be NaN
- * (tokens past len may hold anything). Products are exact or in fp32; the softmax's weights
- * are rounded to 11 bits.
+ * (tokens past len may hold anything), and scales of V must be positive and finite (as sparsp_cache_write
+ * leaves them; below 2^-120 they count as that). Products are exact and summed in fp32; the softmax's weights
+ * are rounded to 11 bits. Of a request with more than 32 rows per key head (its tokens * H / heads), or of
+ * every request where B * max_add <= tokens and max_add * H / heads > 32, a query loses what is below 2^-18 of its
+ * largest value in magnitude.
  * Sums are taken in an order that depends on the lengths (and lists) of the whole call: the
  * same call gives the same bits, but a row's last bits may depend on the other requests.
  * SPARSP_ERR_DATA on the device: rows outside [0, tokens] or more than max_add of them (the
  * request's are left out), a length outside [0, max_blocks * bt] (counts as 0), a CSR row that is
  * malformed (counts as empty), an entry of it without tokens or a block outside the pool
  * (its keys are left out).
- * ws: at least sparsp_attn_cache_workspace_size() bytes.
+ * ws: at least sparsp_attn_cache_workspace_size() bytes. o and lse may not overlap q or each other.
  */
 enum { SPARSP_CACHE_CAUSAL = 1u << 0 };
 SPARSP_API size_t sparsp_attn_cache_workspace_size(const sparsp_cache_t* cache, int32_t B, int32_t H, int64_t tokens,

@@ -49,6 +49,9 @@ def extend(lib, cache=cache(), B=3, max_blocks=4, ln=at(0), add=at(1), free=at(2
     (dict(start=None), sp.INVALID_ARG), (dict(slots=None), sp.INVALID_ARG), (dict(slots=FAKE + 4), sp.ALIGN),
     (dict(used=FAKE + 4), sp.ALIGN), (dict(used_out=FAKE + 8), sp.ALIGN), (dict(table=FAKE + 4), sp.ALIGN),
     (dict(len_out=at(1)), sp.INVALID_ARG), (dict(B=100, len_out=at(0) + 64), sp.INVALID_ARG), (dict(start=at(0)), sp.INVALID_ARG), (dict(start=at(4)), sp.INVALID_ARG),
+    (dict(slots=at(3)), sp.INVALID_ARG), (dict(B=7, slots=at(5) + 16), sp.INVALID_ARG), (dict(used_out=at(1)), sp.INVALID_ARG),
+    (dict(table=at(2)), sp.INVALID_ARG), (dict(used=at(7), used_out=at(7), len_out=at(7)), sp.INVALID_ARG),
+    (dict(used=at(7), used_out=at(8), start=at(7)), sp.INVALID_ARG),
 ])
 def test_extend_refuses(lib, kw, code):
     assert extend(lib, **kw) == code
@@ -92,6 +95,7 @@ def attn(lib, cache=cache(), B=3, H=4, q=at(0), qs=0, start=at(1), tokens=5, max
     (dict(scale=float("nan")), sp.INVALID_ARG), (dict(scale=float("inf")), sp.INVALID_ARG), (dict(flags=2), sp.INVALID_ARG),
     (dict(ws=None), sp.INVALID_ARG), (dict(ws_bytes=100), sp.WORKSPACE), (dict(o=at(0)), sp.INVALID_ARG),
     (dict(o=at(0) + 512), sp.INVALID_ARG), (dict(qs=1024, o=at(0) + 8192), sp.INVALID_ARG),
+    (dict(lse=at(0) + 256), sp.INVALID_ARG), (dict(o=at(5), lse=at(5) + 64), sp.INVALID_ARG),
     (dict(tokens=0, q=None, o=None, lse=None), sp.OK),     # nothing to do, nothing launched
 ])
 def test_attn_refuses(lib, kw, code):

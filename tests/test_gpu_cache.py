@@ -6,7 +6,7 @@ rounding of the value. Attention, with y the base-e scores and p = exp(y - max):
 the products of the scores are exact, their fp32 sums (at most 128 terms, rounded or cut)
 are off by at most d 2^-23 sum |q k| scale, a score's scaling and exponential by a few 2^-22
 of |y| + 1: `delta` in a weight's relative error. A weight is rounded to 11 bits (2^-11) or
-lost below 2^-35 of its row's largest; with more than 16 rows of a request to a key head, queries lose what
+lost below 2^-35 of its row's largest; with more than 32 rows of a request to a key head, queries lose what
 is below 2^-18 of their row's largest value (`split`: d of them); sums over keys are fp32 with at most 2^-24 per key
 in a row of additions, LONG keys at most here. The result is rounded to bf16 (2^-8)."""
 import pytest
@@ -336,7 +336,7 @@ def attn_ref(q, keys, add, lengths, scale, causal, bt, chosen=None):
         l = p.sum(-1, keepdim=True)
         safe = torch.where(l > 0, l, 1.0)
         delta = d * 2.0 ** -23 * mag + 2.0 ** -19 * (1 + mag)
-        if n * G > 16 and total:
+        if n * G > 32 and total:
             split = qb.abs().amax(-1, keepdim=True) * k.abs().sum(-1).amax(-1)[:, None, None] * 2.0 ** -18
             delta = delta + split * abs(scale)
         spread = (p @ v.abs()) / safe
@@ -556,6 +556,66 @@ def test_attn_stream_capture_and_two_graphs():
         for scale, (o, lse) in zip((0.0, 0.5), outs):
             ref = sp.attn_cache_fwd(pool, q, start, ln, table, 1, scale)
             assert torch.equal(o, ref[0]) and torch.equal(lse, ref[1])
+
+
+def test_attn_many_rows_stream_and_two_graphs():
+    """As above, for requests of many rows and of few in one call, the two graphs on streams of their own."""
+    lengths, add = [1000, 300, 64], [150, 1, 40]
+    pool, table, start, ln, q = check_attn(lengths, add, 2, 2, 128, 64, True, behind=0)
+    graphs, outs, sides = [], [], [torch.cuda.Stream() for _ in range(2)]
+    for scale in (0.0, 0.5):
+        o, lse = torch.empty(191, 4, 128, dtype=torch.bfloat16, device="cuda"), torch.empty(191, 4, device="cuda")
+        ws = torch.empty(sp.attn_cache_workspace_size(pool.shape, 3, 4, 191, 150, table.shape[1]), dtype=torch.uint8, device="cuda")
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            sp.attn_cache_fwd(pool, q, start, ln, table, 150, scale, o=o, lse=lse, ws=ws)
+        graphs.append(graph)
+        outs.append((o, lse, ws))
+    for lengths in ([1000, 300, 64], [151, 299, 40], [777, 65, 63]):
+        ln.copy_(i32(lengths))
+        for side, graph in zip(sides, graphs):
+            side.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(side):
+                graph.replay()
+                graph.replay()
+        for side in sides:
+            torch.cuda.current_stream().wait_stream(side)
+        for scale, (o, lse, _) in zip((0.0, 0.5), outs):
+            ref = sp.attn_cache_fwd(pool, q, start, ln, table, 150, scale)
+            assert torch.equal(o, ref[0]) and torch.equal(lse, ref[1])
+
+
+@pytest.mark.parametrize("add", [1, 100])
+def test_far_offsets(add):
+    """A pool of more than 2^32 bytes of codes: the same as a small one whose blocks hold the same."""
+    n, heads, d, bt, g = 300, 30, 128, 128, gen(8)
+    k, v = (torch.randn(n, heads, d, generator=g, device="cuda") for _ in range(2))
+    q = torch.randn(add, heads, d, generator=g, device="cuda").bfloat16()
+    results, codes = [], []
+    for blocks, page in ((9000, [8999, 3, 8998]), (3, [2, 0, 1])):
+        pool, table = sp.block_pool(blocks, heads, d, bt), i32([page])
+        slots = (table[0].long()[:, None] * bt + torch.arange(bt, device="cuda")).flatten()[:n].int()
+        sp.cache_write(pool, k, v, slots)
+        codes.append([t.view(torch.uint8)[page] for t in (pool.k, pool.v)] + [t[page] for t in (pool.k_scale, pool.v_scale)])
+        results.append(sp.attn_cache_fwd(pool, q, i32([0, add]), i32([n]), table, add))
+        del pool
+    for a, b in zip(codes[0] + list(results[0]), codes[1] + list(results[1])):
+        assert torch.equal(a, b)
+    assert 9000 * heads * d * bt > 2 ** 32
+
+
+def test_no_tokens():
+    """A step in which nothing is new."""
+    pool, status = fresh_pool(4, 2, 64, 64), word()
+    before = [t.clone() for t in (pool.k.view(torch.uint8), pool.k_scale, pool.v.view(torch.uint8), pool.v_scale)]
+    ln, start, slots, used = sp.cache_extend(pool.shape, i32([5, 0]), i32([0, 0]), i32([]), i32([[1], [2]]), 0, status=status)
+    assert ln.tolist() == [5, 0] and start.tolist() == [0, 0, 0] and slots.numel() == 0 and int(used) == 0
+    x = torch.empty(0, 2, 64, device="cuda")
+    sp.cache_write(pool, x, x, slots, status=status)
+    o, lse = sp.attn_cache_fwd(pool, x.bfloat16(), start, ln, i32([[1], [2]]), 1, status=status)
+    assert o.shape == (0, 2, 64) and lse.shape == (0, 2) and int(status) == 0
+    for a, b in zip(before, (pool.k.view(torch.uint8), pool.k_scale, pool.v.view(torch.uint8), pool.v_scale)):
+        assert torch.equal(a, b)
 
 
 # ------------------------------------------------------------------- as they are used together
