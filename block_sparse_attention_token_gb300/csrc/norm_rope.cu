@@ -14,6 +14,11 @@
 // (UPR), so its sums are shuffles; a thread keeps the (cos, sin) of its tokens and
 // columns, and its columns of w and b, in registers and sweeps the heads, whose vectors are
 // copied into shared-memory slots of its own some heads ahead (cp.async).
+// Measured at 30,720 tokens and 40 + 40 heads of 128 in bf16 (of a copy's rate): forward 200 us (0.93),
+// with tile means 230 (0.81: a tile's means are joined over the warps at its end, through
+// shared memory), backward 307 (0.91); backward of 8,192 tokens and 12 + 12 heads of 64 in fp32 35 us (0.63: short
+// CTAs, and 5 us the sum of their parts); 64 tokens 5 us on the device. Norm and rotation
+// one after the other take 435 us forward, without means.
 #include "rows.cuh"
 
 namespace sparsp {
@@ -182,7 +187,9 @@ __device__ __forceinline__ void row_sum(float (&v)[K]) {
     for (int k = 0; k < K; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], off);
 }
 
-constexpr int kDepth = 3;   // heads in flight per CTA
+// Heads in flight per CTA: forward with means / backward take 238 / 312 us at 2, 233 / 308 at 3, 241 / 395 at 4 (one
+// CTA per SM).
+constexpr int kDepth = 3;
 
 // BIAS: there may be one (a layer norm, or an RMS norm with a bias). POOL: a CTA takes a whole
 // tile, granule after granule, and leaves its means: each warp keeps its columns' sums of every
@@ -535,6 +542,7 @@ int heads_per_cta(int64_t granules, int heads) {
   return (int)(h < 1 ? 1 : h > 8 ? 8 : h);
 }
 
+// Tokens of a granule: with 128 in bf16 forward / backward take 240 / 315 us, not 233 / 308; 64 in fp32 change nothing.
 template <typename T>
 constexpr int granule() { return sizeof(T) == 4 ? 32 : 64; }
 
