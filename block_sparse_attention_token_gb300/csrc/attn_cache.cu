@@ -470,7 +470,7 @@ attn_cache_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
       }
     }
     if (!whole && u0 == 0 && threadIdx.x == 0) {
-      parts.open[cta] = Open{x.b, hk, row0, rows, x.s0, (int)(((item_at + size) * ctas - 1) / total)};
+      parts.open[cta] = Open{hk, row0, rows, x.s0, (int)(((item_at + size) * ctas - 1) / total)};
     }
     asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");   // the sums, before the rings are filled again
     __syncthreads();

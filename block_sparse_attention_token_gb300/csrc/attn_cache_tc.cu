@@ -395,7 +395,7 @@ attn_cache_tc_kernel(const __grid_constant__ CUtensorMap tk, const __grid_consta
         const bool whole = e0 == 0 && at1 == size;
         const int slot = 2 * (int)cta + (e0 > 0 ? 0 : 1);     // a piece that goes on is the CTA's first
         if (!whole && e0 == 0 && lane == 0 && rank == 0)
-          parts.open[cta] = Open{x.b, hk, row0, rows, x.s0, (int)(((item_at + size) * ctas - 1) / total)};
+          parts.open[cta] = Open{hk, row0, rows, x.s0, (int)(((item_at + size) * ctas - 1) / total)};
         if (!(ok = publish(Piece{x.s0, hk, row0, rows, x.n, x.len, e0, e1, whole ? -1 : slot}))) break;
 
         // look-ups: lane i takes the half stage (64 keys) u0 + i of a batch of 32

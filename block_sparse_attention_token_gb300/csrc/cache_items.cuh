@@ -75,7 +75,7 @@ __device__ __forceinline__ int64_t scan_below(int64_t mine, int64_t* sm, int64_t
 
 // What the joining kernel needs to know of the item that starts in a CTA and goes on in others.
 struct Open {
-  int b, hk, row0, rows, s0, last;   // last: the CTA of its last unit; -1: there is none
+  int hk, row0, rows, s0, last;   // last: the CTA of its last unit; -1: there is none
 };
 struct Parts {
   Open* open;      // [ctas]
