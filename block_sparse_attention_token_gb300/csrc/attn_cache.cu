@@ -553,8 +553,8 @@ sparsp_status_t go(const CacheAttn& a, void* ws, cudaStream_t st) {
 }
 
 // Requests with up to kFew rows (tokens times heads that share a key head) are this file's
-// kernel's, the others those of attn_cache_tc.cu. Where the packed rows leave room for no request
-// shorter than the longest, that one takes all, and a launch is saved.
+// kernel's, the others those of attn_cache_tc.cu. Only the device knows the requests, so where there may be both
+// both are launched (the one without work takes 8 us); a single request is taken at its word, max_add.
 // 32 requests of 8,192 keys, 8 key heads of 128, with 16, 32, 64, 128 rows: here 116, 156, 247, 424 us (rows beyond 16 read
 // the cache again), there 312, 181, 206, 223.
 constexpr int kFew = 32;
@@ -572,7 +572,7 @@ sparsp_status_t launch_attn_cache(const CacheAttn& args, void* ws, cudaStream_t 
   const int rows = rows_of(a.group, a.max_add);
   a.few = 0;
   if (many(a.group, a.max_add)) {
-    const bool all = (int64_t)a.B * a.max_add <= a.tokens;
+    const bool all = a.B == 1;
     a.few = all ? 0 : kFew;
     const sparsp_status_t r =
         launch_attn_cache_tc(a, (uint8_t*)ws + parts_align(parts_bytes(kGrid, rows, a.c.d)), st);

@@ -48,7 +48,7 @@ struct CacheAttn {
   __nv_bfloat16* o;          // [tokens, H, d]
   float* lse;                // [tokens, H]
   int32_t* d_status;
-  int few;                   // rows of a request up to which it is the kernel's for few rows (0: every one)
+  int few;                   // rows of a request up to which it is the kernel's for few rows (0: it takes every one)
 };
 // Few rows of a request, and the dispatch; many rows.
 size_t attn_cache_ws(const CacheDims& c, int group, int max_add);

@@ -98,23 +98,6 @@ inline Parts parts_of(void* ws, int ctas, int rows) {
   return p;
 }
 
-// Launches a kernel that may begin before the last one ends and waits for it itself.
-template <typename Kernel>
-sparsp_status_t launch_after(Kernel kern, dim3 grid, int threads, cudaStream_t st, const CacheAttn& a, const Parts& p) {
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(threads);
-  cfg.stream = st;
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, kern, a, p) != cudaSuccess) return SPARSP_ERR_CUDA;
-  SPARSP_LAUNCH_CHECK();
-  return SPARSP_OK;
-}
-
 __device__ __forceinline__ uint32_t f16x2_of_e4m3(uint32_t two) {   // the low two bytes
   uint32_t r;
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;\n" : "=r"(r) : "h"((uint16_t)two));

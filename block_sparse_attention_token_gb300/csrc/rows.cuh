@@ -198,4 +198,21 @@ struct Unit<float, true> {
   }
 };
 
+// Launches a kernel that may begin before the one before it ends, and waits for it itself.
+template <typename... Params, typename... Args>
+sparsp_status_t launch_after(void (*kern)(Params...), dim3 grid, int threads, cudaStream_t st, const Args&... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.stream = st;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, kern, args...) != cudaSuccess) return SPARSP_ERR_CUDA;
+  SPARSP_LAUNCH_CHECK();
+  return SPARSP_OK;
+}
+
 }  // namespace sparsp

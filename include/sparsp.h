@@ -780,9 +780,8 @@ SPARSP_API sparsp_status_t sparsp_cache_write(const sparsp_cache_t* cache, int32
  * request are left as they were. Values of keys that a row does not see must not be NaN
  * (tokens past len may hold anything), and scales of V must be positive and finite (as sparsp_cache_write
  * leaves them; below 2^-120 they count as that). Products are exact and summed in fp32; the softmax's weights
- * are rounded to 11 bits. Of a request with more than 32 rows per key head (its tokens * H / heads), or of
- * every request where B * max_add <= tokens and max_add * H / heads > 32, a query loses what is below 2^-18 of its
- * largest value in magnitude.
+ * are rounded to 11 bits. Of a request with more than 32 rows per key head (its tokens * H / heads;
+ * with B = 1, max_add * H / heads), a query loses what is below 2^-18 of its largest value in magnitude.
  * Sums are taken in an order that depends on the lengths (and lists) of the whole call: the
  * same call gives the same bits, but a row's last bits may depend on the other requests.
  * SPARSP_ERR_DATA on the device: rows outside [0, tokens] or more than max_add of them (the
