@@ -15,8 +15,8 @@
 // columns, and its columns of w and b, in registers and sweeps the heads, whose vectors are
 // copied into shared-memory slots of its own some heads ahead (cp.async).
 // Measured at 30,720 tokens and 40 + 40 heads of 128 in bf16 (of a copy's rate): forward 200 us (0.93),
-// with tile means 230 (0.81: a tile's means are joined over the warps at its end, through
-// shared memory), backward 307 (0.91); backward of 8,192 tokens and 12 + 12 heads of 64 in fp32 35 us (0.63: short
+// with tile means 227 (0.82: a tile's means are joined over the warps at its end, through
+// shared memory), backward 304 (0.91); backward of 8,192 tokens and 12 + 12 heads of 64 in fp32 35 us (0.63: short
 // CTAs, and 5 us the sum of their parts); 64 tokens 5 us on the device. Norm and rotation
 // one after the other take 435 us forward, without means.
 #include "rows.cuh"
@@ -315,19 +315,19 @@ norm_rope_fwd_kernel(const Fwd q, const Fwd k, const Tokens tk, const RopeArgs a
         if (t.means != nullptr) {                // the same for the whole CTA
           float* mine = sums + (h * kWarps + warp) * D;
 #pragma unroll
-          for (int i = 0; i < C::NP; ++i) {
+          for (int i = 0; i < C::NP; i += 2) {   // two pairs of columns: four neighbours, or HALF two and two
             const float2 px = both(ax[i / 2]), py = both(ay[i / 2]);
-            float vx = i & 1 ? px.y : px.x, vy = i & 1 ? py.y : py.x;
+            float v[4] = {px.x, HALF ? px.y : py.x, HALF ? py.x : px.y, py.y};
 #pragma unroll
-            for (int off = 16; off >= C::UPR; off >>= 1) {
-              vx += __shfl_xor_sync(0xffffffffu, vx, off);
-              vy += __shfl_xor_sync(0xffffffffu, vy, off);
-            }
+            for (int off = 16; off >= C::UPR; off >>= 1)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) v[e] += __shfl_xor_sync(0xffffffffu, v[e], off);
             if ((threadIdx.x & 31) < C::UPR) {
-              float& sx = mine[col_x<D, E, HALF>(c0, i)];
-              float& sy = mine[col_y<D, E, HALF>(c0, i)];
-              sx = part == 0 ? vx : sx + vx;
-              sy = part == 0 ? vy : sy + vy;
+              float2* lo = reinterpret_cast<float2*>(mine + col_x<D, E, HALF>(c0, i));
+              float2* hi = reinterpret_cast<float2*>(HALF ? mine + col_y<D, E, HALF>(c0, i) : mine + col_x<D, E, HALF>(c0, i + 1));
+              const float2 was = part == 0 ? make_float2(0.f, 0.f) : *lo, then = part == 0 ? make_float2(0.f, 0.f) : *hi;
+              *lo = make_float2(was.x + v[0], was.y + v[1]);
+              *hi = make_float2(then.x + v[2], then.y + v[3]);
             }
           }
         }
