@@ -227,10 +227,10 @@ struct Walk {
     if (a.row_ptr != nullptr) return (x.units + 1) / 2;
     int keys = x.len;
     if (a.causal) {   // up to the last row's token
-      const int tok = min(x.n, ((group + 1) * kItemRows - 1) / a.group + 1) - 1;
+      const int tok = (int)min((uint32_t)x.n, ((uint32_t)(group + 1) * kItemRows - 1) / (uint32_t)a.group + 1) - 1;
       keys = max(0, min(keys, x.len - x.n + tok + 1));
     }
-    return (keys + kStageKeys - 1) / kStageKeys;
+    return (int)(((uint32_t)keys + kStageKeys - 1) / kStageKeys);   // keys may be 2^31 - 64
   }
   // of one item; an item without keys still has its rows to write: one stage, empty
   __device__ __forceinline__ int size(const Entry& x, int group) const { return kItemCost + max(1, stages(x, group)); }
