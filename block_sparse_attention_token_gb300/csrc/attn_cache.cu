@@ -329,7 +329,7 @@ attn_cache_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
       for (int j = 0; j < NT; ++j)
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          const float f = factor[j][i] * ks;
+          const float f = score_factor(factor[j][i], ks);
           c[j][i] = g < n && at + g <= last[j][i] ? fmaf(c[j][i], f, lv) : -INFINITY;
           c[j][2 + i] = g + 8 < n && at + g + 8 <= last[j][i] ? fmaf(c[j][2 + i], f, lv) : -INFINITY;
           // the maximum follows when a score passes it by more than 2^4

@@ -688,7 +688,7 @@ attn_cache_tc_kernel(const __grid_constant__ CUtensorMap tk, const __grid_consta
           const Info& f = infos[is].half[j % kBatch][k];
           const int4 w = *reinterpret_cast<const int4*>(&f);
           see[k] = min(w.y, last - w.x < 63 ? last - w.x + 1 : 64);
-          c[k] = factor * __int_as_float(w.z);
+          c[k] = see[k] > 0 ? score_factor(factor, __int_as_float(w.z)) : 1.f;   // what is hidden says nothing
           lv[k] = __int_as_float(w.w);
           inv[k] = f.inv;
         }

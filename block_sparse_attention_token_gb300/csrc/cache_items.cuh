@@ -3,6 +3,7 @@
 #pragma once
 
 #include <cuda_fp16.h>
+#include <float.h>
 
 #include "cache.cuh"
 
@@ -111,6 +112,15 @@ __device__ __forceinline__ float exp2_fast(float x) {
   float r;
   asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(r) : "f"(x));
   return r;
+}
+
+// What a product of codes is a score by: the row's factor times the keys' scale, but a normal number (or NaN).
+// Rows of zeros and blocks of zeros have the least factors there are, whose product is 0 in fp32: 0 times the -inf of
+// a hidden key would be NaN. At 2^-126 a product of codes (below 2^32) still is a score of 0, and a
+// product of 0 stays one at the other end.
+__device__ __forceinline__ float score_factor(float row, float ks) {
+  const float f = row * ks;
+  return f < FLT_MIN ? FLT_MIN : f > FLT_MAX ? FLT_MAX : f;
 }
 
 // Writes four columns of a finished row, and its LSE.
