@@ -12,8 +12,8 @@
 // K, and the rows of V^T are columns of vectors that a lane reads anyway. Every warp has a ring of
 // stages of its own, filled by TMA. Work is counted in units of 64 keys over all requests
 // and key heads and dealt out evenly: a CTA takes a range of units, and an item (request, key head, 8 or 16 rows) that
-// spans several CTAs leaves partial sums that a second kernel joins in order. vs goes into the weights and out of
-// their sum again (P = 2^(y + log2 vs - m), l = sum P / vs), so that the products of all blocks add up in place.
+// spans several CTAs leaves partial results that a second kernel joins in order. vs goes into the weights and out of
+// their sum again (cache_items.cuh), so that the products of all blocks add up in place.
 // Measured (32 heads over 8, d = 128): 64 uneven requests of up to 32,768 tokens 80 us (0.82 of a copy's rate); 8 x 4
 // rows over a tenth of 131,072 keys 55 us (0.57; 20 us of it fixed: scan and look-ups at the latency of a cold cache,
 // the warps' join, the second kernel); one request of 1,024 keys 11 us on the device.
@@ -124,7 +124,7 @@ attn_cache_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
   __shared__ int64_t s_begin[2];               // first entry, its unit offset
   __shared__ __align__(16) __half s_q[RT][D + 8];
   __shared__ float s_factor[RT];
-  __shared__ float s_m[kWarps][RT], s_l[kWarps][RT];
+  __shared__ float s_m[kWarps][RT], s_l[kWarps][RT], s_lu[kWarps];
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
 
   // ---- this CTA's range of units
@@ -290,7 +290,7 @@ attn_cache_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
         last[j][i] = a.causal ? x.len - x.n + (row0 + r) / a.group : INT32_MAX;
       }
     }
-    float m[NT][2], l[NT][2], o[NT][D / 16][4];
+    float m[NT][2], l[NT][2], o[NT][D / 16][4], lu = -INFINITY;   // lu: log2 u, of this warp
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
       m[j][0] = m[j][1] = -INFINITY;
@@ -300,8 +300,12 @@ attn_cache_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
     }
 
     auto step = [&](const Stage<D>& st, int at, int n, float ks, float vs) {
-      // vs goes into the weights, and out of their sum again: one fma less for every element of O
-      const float lv = __log2f(fmaxf(vs, 0x1p-120f)), inv = exp2_fast(-lv);
+      // vs / u goes into the weights, and out of their sum again: one fma less for every element of O
+      const float lvs = __log2f(fmaxf(vs, kLeastScale)), up = lvs - lu;   // (the same for the whole warp)
+      const bool rises = !(up <= kAbove), sinks = up < -kBelow;
+      if (rises) lu = lvs;
+      const float lv = rises || sinks ? 0.f : up, inv = exp2_fast(-lv);
+      const int nv = sinks ? 0 : n;             // how many have values
       float c[NT][4], c2[NT][4];                // two sums, so that products need not wait for one another
 #pragma unroll
       for (int j = 0; j < NT; ++j)
@@ -324,18 +328,19 @@ attn_cache_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
       for (int j = 0; j < NT; ++j)
 #pragma unroll
         for (int i = 0; i < 4; ++i) c[j][i] += c2[j][i];
-      bool moved = false;
+      bool moved = rises;
 #pragma unroll
       for (int j = 0; j < NT; ++j)
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          const float f = score_factor(factor[j][i], ks);
+          const float f = score_factor<false>(factor[j][i], ks);
           c[j][i] = g < n && at + g <= last[j][i] ? fmaf(c[j][i], f, lv) : -INFINITY;
           c[j][2 + i] = g + 8 < n && at + g + 8 <= last[j][i] ? fmaf(c[j][2 + i], f, lv) : -INFINITY;
           // the maximum follows when a score passes it by more than 2^4
           moved |= fmaxf(c[j][i], c[j][2 + i]) > m[j][i] + 4.f;
         }
       if (__any_sync(0xffffffffu, moved)) {
+        const float down = rises ? exp2_fast(-up) : 1.f;     // 0 for the first
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
           float corr[2];
@@ -350,6 +355,7 @@ attn_cache_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
               l[j][i] *= corr[i];
               m[j][i] = top;
             }
+            corr[i] *= down;
           }
 #pragma unroll
           for (int i = 0; i < D / 16; ++i)
@@ -386,10 +392,10 @@ attn_cache_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
           v[i][1] = w.y;
         }
       }
-      if (n < 16)                                // what lies past the last token may be anything
+      if (nv < 16)                               // what lies past the last token may be anything
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          if (2 * t + (i & 1) + 8 * (i >> 1) >= n)
+          if (2 * t + (i & 1) + 8 * (i >> 1) >= nv)
 #pragma unroll
             for (int k = 0; k < D / 32; ++k) v[i][k] = 0;
 #pragma unroll
@@ -432,7 +438,12 @@ attn_cache_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
           s_l[warp][j * 8 + 2 * t + i] = l[j][i];
         }
       }
+    if (lane == 0) s_lu[warp] = lu;
     __syncthreads();                            // the rings are done with
+    float high = s_lu[0];
+#pragma unroll
+    for (int q = 1; q < kWarps; ++q) high = fmaxf(high, s_lu[q]);
+    const float u = exp2_fast(high), mine_u = lu == -INFINITY ? 0.f : exp2_fast(lu - high) * (1.f / kPScale);
 #pragma unroll
     for (int j = 0; j < NT; ++j)
 #pragma unroll
@@ -440,7 +451,7 @@ attn_cache_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
 #pragma unroll
         for (int k = 0; k < 2; ++k)
           *reinterpret_cast<float2*>(&s_o[warp][j * 8 + 2 * t + k][D / 8 * g + 2 * i]) =
-              make_float2(o[j][i][k] * (1.f / kPScale), o[j][i][k + 2] * (1.f / kPScale));
+              make_float2(o[j][i][k] * mine_u, o[j][i][k + 2] * mine_u);
     __syncthreads();
     const bool whole = u0 == 0 && u1 == units;
     const int slot = 2 * (int)cta + (u0 > 0 ? 0 : 1);     // a piece that goes on is the CTA's first
@@ -462,11 +473,14 @@ attn_cache_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
         all.z = fmaf(f, w.z, all.z);
         all.w = fmaf(f, w.w, all.w);
       }
+      const bool none = sum == 0.f;
+      const float f = none ? 0.f : 1.0f / sum, lse2 = top + log2f(sum);   // (u by itself: a scale may be tiny)
+      all = make_float4(all.x * f * u, all.y * f * u, all.z * f * u, all.w * f * u);
       if (whole) {
-        finish<D>(a, x.s0, hk, row0 + r, c, top, sum, all);
+        finish<D>(a, x.s0, hk, row0 + r, c, none, lse2, all);
       } else {
-        *reinterpret_cast<float4*>(parts.sum + ((int64_t)slot * RT + r) * D + c) = all;
-        if (c == 0) parts.ml[(int64_t)slot * RT + r] = make_float2(top, sum);
+        *reinterpret_cast<float4*>(parts.o + ((int64_t)slot * RT + r) * D + c) = all;
+        if (c == 0) parts.ml[(int64_t)slot * RT + r] = make_float2(none ? -INFINITY : lse2, none ? 0.f : 1.f);
       }
     }
     if (!whole && u0 == 0 && threadIdx.x == 0) {
@@ -504,11 +518,10 @@ attn_cache_join_kernel(const CacheAttn a, const Parts parts) {
   float4 all = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
   for (int i = warp; i < count; i += W) {
-    const float2 ml = parts.ml[slot_of(i) * RT + r];
-    const float f = ml.y == 0.f ? 0.f : ml.x == -INFINITY ? 1.f : exp2_fast(ml.x - top);
-    sum = fmaf(f, ml.y, sum);
+    const float f = part_weight(parts.ml[slot_of(i) * RT + r], top);
+    sum += f;
     if (lane < L) {
-      const float4 w = *reinterpret_cast<const float4*>(parts.sum + (slot_of(i) * RT + r) * D + 4 * lane);
+      const float4 w = *reinterpret_cast<const float4*>(parts.o + (slot_of(i) * RT + r) * D + 4 * lane);
       all.x = fmaf(f, w.x, all.x);
       all.y = fmaf(f, w.y, all.y);
       all.z = fmaf(f, w.z, all.z);
@@ -530,7 +543,7 @@ attn_cache_join_kernel(const CacheAttn a, const Parts parts) {
     all.z += w.z;
     all.w += w.w;
   }
-  finish<D>(a, it.s0, it.hk, it.row0 + r, 4 * threadIdx.x, top, sum, all);
+  finish_join<D>(a, it.s0, it.hk, it.row0 + r, 4 * threadIdx.x, top, sum, all);
 }
 
 // Query rows of an item here: 8 where no request has more.

@@ -8,11 +8,8 @@
 // and q2 = e4m3(q - q1), but for what lies below 2^-18 of its row's largest value. Two products
 // of 8 bits cost what one of 16 does, and K needs no widening. O += P V takes P in f16 (11
 // bits) and V widened to f16, where an e4m3 code is exact, by four warps on its way.
-// The scale of a block's values goes into the exponent: with y the score in base 2 and R the
-// row's reference,
-//   P = 2^(y + log2 vs - R),  O = sum P V / l,  l = sum P / vs,  LSE = (R + log2 l) ln 2,
-// so that blocks of any scales add up in one accumulator; P is at most 2^15 (R follows when
-// it is passed by more than 2^4) and not below 2^-24 f16 has nothing to add.
+// The scale of a block's values goes into the exponent (cache_items.cuh); P is at most 2^15 (its reference follows when
+// it is passed by more than 2^4) and below 2^-24 f16 has nothing to add.
 //
 // Measured: 1,536 queries x 30,720 keys x 40 heads of d = 128 take 630 us when they come alone (0.81 of the bf16
 // peak for the two products, 0.73 back to back under the power cap), d = 64 525 us, 4 prompts of 4,096 tokens x 32
@@ -28,7 +25,7 @@
 // each loads one half of K's keys and of V's columns, so that every byte of the cache is loaded and widened once
 // for 256 rows, and shared memory is read half as often as with a tile to each SM. Work is counted in
 // stages of 128 keys over all items (request, key head, 256 rows) and dealt out evenly;
-// an item in several clusters leaves partial sums that a second kernel joins in order.
+// an item in several clusters leaves partial results that a second kernel joins in order.
 //   warps 0-7: softmax and epilogue of the CTA's rows, two threads to a row (= TMEM lane): one for the even
 //              stages and one for the odd, which pass the row's reference from stage to stage, so that one loads
 //              scores while the other takes exponentials. Each has half of the columns of Q, which they
@@ -76,11 +73,13 @@ enum Bars {
 struct Piece {
   int s0, hk, row0, rows, n, len, e0, e1, part;   // part: -1: the whole item, else the slot of its sums
 };
-// What is to be known of half a stage (64 keys): position of the first, how many exist, scale of K, log2 and inverse
-// of the scale of V. The producer leaves them by batches of 16 stages of a piece.
+// What is to be known of half a stage (64 keys): position of the first, how many exist, scale of K, log2 and inverse of
+// vs / u, log2 of how much u has risen since the stage before, of u, and how many keys have values beside u. The
+// producer leaves them by batches of 16 stages of a piece, of one u.
 struct alignas(16) Info {
   int pos, valid;
-  float ks, lv, inv;
+  float ks, lv, inv, rise, lu;
+  int held;
 };
 constexpr int kBatch = 16;
 struct Batch {
@@ -406,7 +405,7 @@ attn_cache_tc_kernel(const __grid_constant__ CUtensorMap tk, const __grid_consta
           int page, row;
         };
         auto look = [&](int u) -> Half {
-          Half h{{0, 0, 1.f, 0.f, 1.f}, 0, 0};
+          Half h{{0, 0, 1.f, 0.f, 1.f, 0.f, 0.f, 0}, 0, 0};
           if (u >= 2 * e1 || u >= x.units) return h;
           int j = u / per_block;
           if (list != nullptr) j = __ldg(list + j);
@@ -421,12 +420,27 @@ attn_cache_tc_kernel(const __grid_constant__ CUtensorMap tk, const __grid_consta
           }
           const int64_t block = (int64_t)page * a.c.heads + hk;
           const int in_block = u % per_block * kUnit;
-          const float vs = fmaxf(__ldg(a.vs + block), 0x1p-120f);
           h.page = page;
           h.row = hk * a.c.bt + in_block;
-          h.info = Info{j * a.c.bt + in_block, max(0, min(kUnit, x.len - j * a.c.bt - in_block)), __ldg(a.ks + block), log2f(vs),
-                        1.0f / vs};
+          h.info.pos = j * a.c.bt + in_block;
+          h.info.valid = max(0, min(kUnit, x.len - j * a.c.bt - in_block));
+          h.info.ks = __ldg(a.ks + block);
+          h.info.lv = log2f(fmaxf(__ldg(a.vs + block), kLeastScale));
           return h;
+        };
+        // ... against u, the largest of the batch where that is far above what it was
+        float lu = 0.f;
+        auto place = [&](Info& f, bool first) {
+          float most = f.valid > 0 ? f.lv : -INFINITY;
+#pragma unroll
+          for (int off = 16; off > 0; off >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, off));
+          const float was = lu;
+          if (most > -INFINITY && (first || most > lu + kAbove)) lu = most;
+          f.lu = lu;
+          f.rise = lane < 2 ? lu - was : 0.f;    // (of a piece's first stage: no matter)
+          f.held = f.valid > 0 && f.lv >= lu - kBelow ? f.valid : 0;
+          f.lv = f.held > 0 ? f.lv - lu : 0.f;
+          f.inv = exp2f(-f.lv);
         };
         Half now, ahead = look(2 * e0 + lane);
         for (int e = e0; e < e1; ++e) {
@@ -434,6 +448,7 @@ attn_cache_tc_kernel(const __grid_constant__ CUtensorMap tk, const __grid_consta
           if (i == 0) {
             now = ahead;
             ahead = look(2 * e + 32 + lane);
+            place(now.info, e == e0);
             const uint32_t is = n_batch++ % kNInfo;
             infos[is].half[lane >> 1][lane & 1] = now.info;
             __syncwarp();
@@ -549,7 +564,7 @@ attn_cache_tc_kernel(const __grid_constant__ CUtensorMap tk, const __grid_consta
             ++n_batch;
           }
           const Info* half = infos[(n_batch - 1) % kNInfo].half[(e - x.e0) % kBatch];
-          const int valid0 = half[0].valid, valid1 = half[1].valid;
+          const int held0 = half[0].held, held1 = half[1].held;
           if (!(ok = wait_warp(bar(V_FULL + vs), (n / kNV) & 1u, g))) break;
           if (!(ok = wait_warp(bar(W_EMPTY + ws), ((n / kNW) & 1u) ^ 1u, g))) break;
           const uint4* from = reinterpret_cast<const uint4*>(gbase + C::kOffV + vs * C::kV);
@@ -558,7 +573,7 @@ attn_cache_tc_kernel(const __grid_constant__ CUtensorMap tk, const __grid_consta
           for (int i = 0; i < kStageKeys * CH / 128; ++i) {
             const int v = id + 128 * i, r = v / CH, c = v % CH;   // row, and columns 16 c .. of the half
             uint4 w = from[v];
-            if ((r & 63) >= (r < 64 ? valid0 : valid1)) w = make_uint4(0, 0, 0, 0);
+            if ((r & 63) >= (r < 64 ? held0 : held1)) w = make_uint4(0, 0, 0, 0);
             const uint32_t in[4] = {w.x, w.y, w.z, w.w};
             uint32_t out[8];
 #pragma unroll
@@ -673,22 +688,24 @@ attn_cache_tc_kernel(const __grid_constant__ CUtensorMap tk, const __grid_consta
       float ref = -INFINITY, l = 0.f;            // R; l times 2^11, of this thread's stages
       // what the row sees of a stage's halves, and their scales
       int see[2];
-      float c[2], lv[2], inv[2];
+      float c[2], lv[2], inv[2], rise;
       const uint32_t begin_n = n, end_n = n + (uint32_t)(x.e1 - x.e0);
       int known = -1;                            // batches of this piece that are there
       auto facts = [&](uint32_t n) {
         const int j = (int)(n - begin_n), batch = j / kBatch;
+        rise = 0.f;                              // only with a batch's first stage
         const uint32_t is = (n_batch + batch) % kNInfo;
         if (batch > known) {
           ok = ok && wait_warp(bar(INFO + is), ((n_batch + batch) / kNInfo) & 1u, g);
           known = batch;
+          rise = infos[is].half[j % kBatch][0].rise;
         }
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
           const Info& f = infos[is].half[j % kBatch][k];
           const int4 w = *reinterpret_cast<const int4*>(&f);
           see[k] = min(w.y, last - w.x < 63 ? last - w.x + 1 : 64);
-          c[k] = see[k] > 0 ? score_factor(factor, __int_as_float(w.z)) : 1.f;   // what is hidden says nothing
+          c[k] = see[k] > 0 ? score_factor<true>(factor, __int_as_float(w.z)) : 1.f;   // what is hidden says nothing
           lv[k] = __int_as_float(w.w);
           inv[k] = f.inv;
         }
@@ -734,7 +751,8 @@ attn_cache_tc_kernel(const __grid_constant__ CUtensorMap tk, const __grid_consta
         *ref_at = ok ? now : __uint_as_float(kGone);
         asm volatile("bar.arrive %0, 64;\n" ::"r"(ref_bar + 4 * half) : "memory");
         if (!ok) break;
-        const float f = moves ? exp2_fast(was - now) : 1.f;   // 0 for the first
+        float f = moves ? exp2_fast(was - now) : 1.f;         // 0 for the first
+        if (rise != 0.f) f *= exp2_fast(-rise);
         if (now != ref) l *= exp2_fast(ref - now);            // from where this thread left it
         ref = now;
         const float against = ref == -INFINITY ? 0.f : ref;
@@ -760,7 +778,7 @@ attn_cache_tc_kernel(const __grid_constant__ CUtensorMap tk, const __grid_consta
           sum[k] = (rs[0] + rs[1]) + (rs[2] + rs[3]);
         }
         l = fmaf(sum[0], inv[0], fmaf(sum[1], inv[1], l));
-        if (n > begin_n && __any_sync(0xffffffffu, moves)) {   // O follows the reference, after the PV of the last stage
+        if (n > begin_n && __any_sync(0xffffffffu, f != 1.f)) {   // O follows the reference, after the PV of the last stage
           ok = ok && wait_warp(bar(PV_DONE + (n - 1) % kNS), ((n - 1) / kNS) & 1u, g);
           fence_after();
 #pragma unroll
@@ -791,9 +809,10 @@ attn_cache_tc_kernel(const __grid_constant__ CUtensorMap tk, const __grid_consta
       l = half ? theirs + l : l + theirs;
       fence_after();
       const uint32_t t_o = col_o + lanes + (uint32_t)half * (D / 2);
-      const float scale = l == 0.f ? 0.f : x.part < 0 ? 1.0f / l : 1.f;
+      const bool none = l == 0.f;
+      const float scale = none ? 0.f : 1.0f / l, u = exp2_fast(infos[(n_batch - 1) % kNInfo].half[0][0].lu);
       const int64_t at = (int64_t)(x.s0 + tok) * a.H + h;
-      float* sums = parts.sum + ((int64_t)max(x.part, 0) * kItemRows + rank * kTileRows + r) * D + half * (D / 2);
+      float* part_o = parts.o + ((int64_t)max(x.part, 0) * kItemRows + rank * kTileRows + r) * D + half * (D / 2);
 #pragma unroll
       for (int i = 0; i < D / 64; ++i) {
         uint32_t ov[32];
@@ -801,7 +820,7 @@ attn_cache_tc_kernel(const __grid_constant__ CUtensorMap tk, const __grid_consta
         wait_ld();
         if (!live) continue;
 #pragma unroll
-        for (int k = 0; k < 32; ++k) ov[k] = l == 0.f ? 0u : __float_as_uint(__uint_as_float(ov[k]) * scale);
+        for (int k = 0; k < 32; ++k) ov[k] = none ? 0u : __float_as_uint(__uint_as_float(ov[k]) * scale * u);   // (u may be tiny)
         if (x.part < 0) {
           uint4* to = reinterpret_cast<uint4*>(a.o + at * D + half * (D / 2) + 32 * i);
 #pragma unroll
@@ -818,15 +837,16 @@ attn_cache_tc_kernel(const __grid_constant__ CUtensorMap tk, const __grid_consta
         } else {
 #pragma unroll
           for (int k = 0; k < 8; ++k)
-            *reinterpret_cast<uint4*>(sums + 32 * i + 4 * k) = make_uint4(ov[4 * k], ov[4 * k + 1], ov[4 * k + 2], ov[4 * k + 3]);
+            *reinterpret_cast<uint4*>(part_o + 32 * i + 4 * k) = make_uint4(ov[4 * k], ov[4 * k + 1], ov[4 * k + 2], ov[4 * k + 3]);
         }
       }
       fence_before();
       __syncwarp();
       if (lane == 0) arrive_cluster(lead(O_EMPTY));
       if (live && half == 0) {
-        if (x.part < 0) a.lse[at] = l == 0.f ? -INFINITY : (ref - kShift + log2f(l)) * 0.6931471805599453f;
-        else parts.ml[(int64_t)x.part * kItemRows + rank * kTileRows + r] = make_float2(ref - kShift, l);
+        const float lse2 = none ? -INFINITY : ref - kShift + log2f(l);
+        if (x.part < 0) a.lse[at] = lse2 * 0.6931471805599453f;
+        else parts.ml[(int64_t)x.part * kItemRows + rank * kTileRows + r] = make_float2(lse2, none ? 0.f : 1.f);
       }
     }
   }
@@ -859,18 +879,17 @@ attn_cache_tc_join_kernel(const CacheAttn a, const Parts parts) {
     float4 all = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
     for (int i = 0; i < count; ++i) {
-      const float2 ml = parts.ml[row_of(i, r)];
-      const float f = ml.y == 0.f ? 0.f : ml.x == -INFINITY ? 1.f : exp2_fast(ml.x - top);
-      sum = fmaf(f, ml.y, sum);
+      const float f = part_weight(parts.ml[row_of(i, r)], top);
+      sum += f;
       if (4 * lane < D) {
-        const float4 w = *reinterpret_cast<const float4*>(parts.sum + row_of(i, r) * D + 4 * lane);
+        const float4 w = *reinterpret_cast<const float4*>(parts.o + row_of(i, r) * D + 4 * lane);
         all.x = fmaf(f, w.x, all.x);
         all.y = fmaf(f, w.y, all.y);
         all.z = fmaf(f, w.z, all.z);
         all.w = fmaf(f, w.w, all.w);
       }
     }
-    if (4 * lane < D) finish<D>(a, it.s0, it.hk, it.row0 + r, 4 * lane, top, sum, all);
+    if (4 * lane < D) finish_join<D>(a, it.s0, it.hk, it.row0 + r, 4 * lane, top, sum, all);
   }
 }
 

@@ -80,8 +80,8 @@ struct Open {
 };
 struct Parts {
   Open* open;      // [ctas]
-  float2* ml;      // [2 ctas][rows] reference (base 2) and sum; a CTA's parts: an item that goes on, one that starts
-  float* sum;      // [2 ctas][rows][d]
+  float2* ml;      // [2 ctas][rows] log2 of the sum of the weights, and 1 (0: none); a CTA's parts: an item that goes on, one that starts
+  float* o;        // [2 ctas][rows][d] the part's own result
 };
 inline size_t parts_align(size_t n) { return (n + 255) & ~(size_t)255; }
 inline size_t parts_bytes(int ctas, int rows, int d) {
@@ -95,7 +95,7 @@ inline Parts parts_of(void* ws, int ctas, int rows) {
   at += parts_align(ctas * sizeof(Open));
   p.ml = (float2*)at;
   at += parts_align((size_t)2 * ctas * rows * sizeof(float2));
-  p.sum = (float*)at;
+  p.o = (float*)at;
   return p;
 }
 
@@ -114,25 +114,46 @@ __device__ __forceinline__ float exp2_fast(float x) {
   return r;
 }
 
-// What a product of codes is a score by: the row's factor times the keys' scale, but a normal number (or NaN).
-// Rows of zeros and blocks of zeros have the least factors there are, whose product is 0 in fp32: 0 times the -inf of
-// a hidden key would be NaN. At 2^-126 a product of codes (below 2^32) still is a score of 0, and a
-// product of 0 stays one at the other end.
+// What a product of codes is a score by: the row's factor times the keys' scale, but a number (or NaN) in whose place a
+// product of 0 gives 0; with SIZE a normal one, so that the -inf of a hidden key stays -inf. (Rows of zeros and blocks of
+// zeros have the least factors there are, and their product is 0 in fp32. At 2^-126 a product of codes, below
+// 2^32, still is a score of 0.)
+template <bool SIZE>
 __device__ __forceinline__ float score_factor(float row, float ks) {
   const float f = row * ks;
-  return f < FLT_MIN ? FLT_MIN : f > FLT_MAX ? FLT_MAX : f;
+  return SIZE && f < FLT_MIN ? FLT_MIN : f > FLT_MAX ? FLT_MAX : f;
 }
 
-// Writes four columns of a finished row, and its LSE.
+// The scales vs of V's blocks go into the exponents against u, a scale near the largest of a piece's blocks so far:
+//   P = 2^(y + log2 (vs / u) - R),  l = sum P u / vs,  O = u sum P V / l,  LSE = (R + log2 l) ln 2
+// (y: scores in base 2), so that blocks of different scales add up in one accumulator and l holds plain weights. u
+// rises where a scale is 2^kAbove beyond it, and what has been summed of O goes down by as much. The values of a block
+// 2^kBelow under u are 0 beside the others' (its vs counts as u). So P of a row's largest weights is at least
+// 2^-(kAbove + kBelow), which neither vanishes nor, in l, overflows, whatever scales come side by side: zeros are held
+// under 2^-100.
+constexpr float kAbove = 8.f, kBelow = 80.f;
+constexpr float kLeastScale = 0x1p-120f;   // of V that counts
+
+// Writes four columns of a finished row, and its LSE (in base 2 here); none: it has seen nothing.
 template <int D>
-__device__ __forceinline__ void finish(const CacheAttn& a, int s0, int hk, int row, int c, float top, float sum,
-                                       const float4& all) {
+__device__ __forceinline__ void finish(const CacheAttn& a, int s0, int hk, int row, int c, bool none, float lse2,
+                                       const float4& o) {
   const int64_t at = (int64_t)(s0 + row / a.group) * a.H + hk * a.group + row % a.group;
-  const float f = sum == 0.f ? 0.f : 1.0f / sum;
-  const __nv_bfloat162 lo = __floats2bfloat162_rn(all.x * f, all.y * f), hi = __floats2bfloat162_rn(all.z * f, all.w * f);
+  const __nv_bfloat162 lo = __floats2bfloat162_rn(o.x, o.y), hi = __floats2bfloat162_rn(o.z, o.w);
   *reinterpret_cast<uint2*>(a.o + at * D + c) =
       make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
-  if (c == 0) a.lse[at] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
+  if (c == 0) a.lse[at] = none ? -INFINITY : lse2 * 0.6931471805599453f;
+}
+
+// A part's weight in its row's join, against the largest part's: at most 1.
+__device__ __forceinline__ float part_weight(const float2& ml, float top) { return ml.y == 0.f ? 0.f : exp2_fast(ml.x - top); }
+// The joined row, of the weights' sum and the weighted results.
+template <int D>
+__device__ __forceinline__ void finish_join(const CacheAttn& a, int s0, int hk, int row, int c, float top, float sum,
+                                            const float4& all) {
+  const bool none = sum == 0.f;
+  const float f = none ? 0.f : 1.0f / sum;
+  finish<D>(a, s0, hk, row, c, none, top + log2f(sum), make_float4(all.x * f, all.y * f, all.z * f, all.w * f));
 }
 
 }  // namespace sparsp

@@ -99,3 +99,77 @@ def test_hidden_block_with_a_scale_of_nan(add):
     sees = (pos >= 320) & (torch.arange(sum(add), device="cuda") >= add[0])
     assert torch.isnan(o[sees]).all() and torch.isnan(lse[sees]).all()
     assert torch.equal(o[~sees], clean[0][~sees]) and torch.equal(lse[~sees], clean[1][~sees])
+
+
+# ------------------------------------------------------------------- scales of V
+
+@pytest.mark.parametrize("add", ROWS)
+@pytest.mark.parametrize("d,bt", [(64, 128), (128, 64)])
+@pytest.mark.parametrize("exponent", [-120, -100, 60, 100])
+def test_scales_of_values_all_alike(add, d, bt, exponent):
+    lengths = [200, 333]
+    pool, table, _ = filled(lengths, 2, d, bt)
+    pool.v_scale.copy_(torch.full_like(pool.v_scale, 2.0 ** exponent))
+    check(pool, table, lengths, add, queries(add, 4, d))
+
+
+@pytest.mark.parametrize("add", ROWS)
+@pytest.mark.parametrize("d,bt", [(64, 128), (128, 64)])
+@pytest.mark.parametrize("exponents", [(-100, 0), (-100, 20), (-120, 100), (-100, 1, -40, 30)])
+@pytest.mark.parametrize("seed", [0, 1])
+def test_scales_of_values_far_apart(add, d, bt, exponents, seed):
+    """Keys in a block of tiny values weigh as much as others, whatever order the scales come in."""
+    lengths = [700, 1111]
+    pool, table, _ = filled(lengths, 2, d, bt)
+    pick = torch.randint(0, len(exponents), pool.v_scale.shape, generator=gen(seed), device="cuda")
+    pool.v_scale.copy_(torch.exp2(torch.tensor(exponents, device="cuda").float()[pick]))
+    check(pool, table, lengths, add, queries(add, 4, d))
+
+
+@pytest.mark.parametrize("add", ROWS)
+@pytest.mark.parametrize("which", ["zero", "tiny"])
+def test_heavy_keys_with_values_of_no_size(add, which):
+    """The keys that hold nearly all of the weight have values of 0, or of 2^-100."""
+    lengths = [700, 1111]
+    pool, table, _ = filled(lengths, 2, 64, 64)
+    for b, j in ((0, 3), (0, 10), (1, 0), (1, 8)):
+        page = int(table[b, j])
+        if which == "zero":
+            clear(pool, table, b, j, "v")
+        else:
+            pool.v_scale[page] = 2.0 ** -100
+        pool.k_scale[page] *= 8.0
+    check(pool, table, lengths, add, 2.0 * queries(add, 4, 64))
+
+
+@pytest.mark.parametrize("add", [1, 40])
+@pytest.mark.parametrize("low", [True, False])
+def test_many_keys_without_values(add, low):
+    """2^17 and more keys of zero values: the sum of the weights is what it is without values. With `low`, the scores
+    rise by less than what moves a row's reference, after the first keys."""
+    n, d, bt = (1 << 17) + 4000, 64, 128
+    blocks = -(-n // bt)
+    pool, table = sp.block_pool(blocks, 1, d, bt), i32([list(range(blocks))])
+    k = torch.zeros(n, 1, d, device="cuda")
+    if low:
+        k[512:, 0, 0] = 1.0
+    sp.cache_write(pool, k, torch.zeros_like(k), torch.arange(n, dtype=torch.int32, device="cuda"))
+    q = torch.zeros(add, 1, d, device="cuda")
+    q[:, 0, 0] = 20.0                                # 20 / 8 * log2(e) = 3.6 < 4
+    o, lse = sp.attn_cache_fwd(pool, q.bfloat16(), i32([0, add]), i32([n]), table, add, causal=False)
+    assert (o == 0).all()
+    want = torch.full((add, 1), 2.5 if low else 0.0, dtype=torch.float64, device="cuda")
+    want += torch.log(torch.tensor(n - 512 + 512 * torch.exp(torch.tensor(-2.5)).item() if low else float(n), dtype=torch.float64))
+    # fp32 sums of at most 2^13 additions in a row (n keys of 64 lanes or more), 2^-24 each, and the far tolerance
+    assert ((lse.double() - want).abs() <= 2.0 ** -11 + 4 * LOG2 * 2.0 ** -24).all(), lse.flatten()[:4]
+
+
+@pytest.mark.parametrize("add", [1, 40])
+@pytest.mark.parametrize("B", [1, 3])
+def test_far_scales_over_many_parts(add, B):
+    """A request that many CTAs share, each with scales of its own."""
+    lengths = [30000 + 77 * b for b in range(B)]
+    pool, table, _ = filled(lengths, 1, 64, 64)
+    e = torch.randint(0, 5, pool.v_scale.shape, generator=gen(5), device="cuda")
+    pool.v_scale.copy_(torch.exp2(torch.tensor([-120., -100., -30., 0., 40.], device="cuda")[e]))
+    check(pool, table, lengths, [add] * B, queries([add] * B, 2, 64))
