@@ -260,8 +260,7 @@ attn_cache_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
 #pragma unroll
       for (int o = D / 16; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
       // 2^14 <= most * 2^-e < 2^15 (bf16's 8 bits stay whole down to 2^-32 of the row's largest)
-      int e = (int)(__float_as_uint(most) >> 23) - 127 - 14;
-      e = max(-100, min(100, e));
+      const int e = max(-100, (int)(__float_as_uint(most) >> 23) - 127 - 14);   // at most 113
       const float down = __uint_as_float((uint32_t)(127 - e) << 23);
       uint4 w;
       w.x = pack_f16(f[0] * down, f[1] * down);

@@ -101,6 +101,19 @@ def test_hidden_block_with_a_scale_of_nan(add):
     assert torch.equal(o[~sees], clean[0][~sees]) and torch.equal(lse[~sees], clean[1][~sees])
 
 
+@pytest.mark.parametrize("add", ROWS)
+@pytest.mark.parametrize("d", [64, 128])
+def test_queries_near_the_end_of_bf16(add, d):
+    """Queries of up to 3.3e38 and keys so small that the scores are ordinary."""
+    lengths = [200, 333]
+    pool, table, _ = filled(lengths, 2, d, 64)
+    q = queries(add, 4, d).bfloat16().float()
+    q *= 2.0 ** 125 / q.abs().amax()
+    pool.k_scale.mul_(2.0 ** -122)
+    o, _ = check(pool, table, lengths, add, q)
+    assert torch.isfinite(o.float()).all()
+
+
 # ------------------------------------------------------------------- scales of V
 
 @pytest.mark.parametrize("add", ROWS)
