@@ -89,6 +89,8 @@ def _rows(name: str, t, heads: int, d: int, dev: int, n: int | None = None) -> t
     shape, st = t.shape, t.stride()
     if shape[1] != heads or shape[2] != d or n is not None and shape[0] != n or shape[0] and st[2] != 1:
         _refuse(name, t, f"a [tokens, {heads}, {d}] tensor with contiguous columns")
+    if shape[0] > 1 and st[0] == 0 or shape[0] and heads > 1 and st[1] == 0:   # the call takes 0 for packed rows
+        _refuse(name, t, f"a [tokens, {heads}, {d}] tensor of its own, not a broadcast view,")
     # a stride over a single token or head says nothing
     return t.data_ptr(), st[0] if shape[0] > 1 else 0, st[1] if heads > 1 else 0
 
@@ -96,7 +98,7 @@ def _rows(name: str, t, heads: int, d: int, dev: int, n: int | None = None) -> t
 def cache_write(pool: CachePool, k, v, slots, status=None, stream=None) -> None:
     """Rounds new keys and values [tokens, heads, d] (float32 or bfloat16; any strides
     between tokens and heads, e.g. slices of a fused projection, or tile order
-    transposed) into the pool's blocks at `slots` (of cache_extend; negative: left out),
+    transposed; no broadcast views) into the pool's blocks at `slots` (of cache_extend; negative: left out),
     with one power-of-two scale per block and head."""
     s, dev = pool.shape, torch.cuda.current_device()
     if not isinstance(slots, torch.Tensor) or slots.dim() != 1:
