@@ -26,20 +26,12 @@ sparsp_status_t check_requests(const CacheDims& c, int32_t B, int32_t max_blocks
 }
 
 // Elements between tokens and between heads of new keys or values (0: heads * d and d).
-sparsp_status_t check_strides(const CacheDims& c, int elem, int64_t* token, int64_t* head) {
+sparsp_status_t check_strides(const CacheDims& c, int elem, int64_t tokens, int64_t* token, int64_t* head) {
   if (*token == 0) *token = (int64_t)c.heads * c.d;
   if (*head == 0) *head = c.d;
   if (*token < c.d || *head < c.d || *token > (int64_t)1 << 40 || *head > (int64_t)1 << 40) return SPARSP_ERR_SHAPE;
+  if (tokens > 0 && *token > ((int64_t)1 << 60) / tokens) return SPARSP_ERR_SHAPE;   // (heads below 2^16)
   if (*token * elem % 16 != 0 || *head * elem % 16 != 0) return SPARSP_ERR_ALIGN;
-  return SPARSP_OK;
-}
-
-// The pools' pointers.
-sparsp_status_t check_pools(const void* kc, const float* ks, const void* vc, const float* vs) {
-  CHECK_PTR(kc);
-  CHECK_PTR(ks);
-  CHECK_PTR(vc);
-  CHECK_PTR(vs);
   return SPARSP_OK;
 }
 
@@ -51,6 +43,29 @@ struct Words {
     return n > 0 && o.n > 0 && (const uint8_t*)p < (const uint8_t*)o.p + 4 * o.n && (const uint8_t*)o.p < (const uint8_t*)p + 4 * n;
   }
 };
+bool apart(const Words* out, int n_out, const Words* in, int n_in) {
+  for (int o = 0; o < n_out; ++o) {
+    for (int i = 0; i < n_in; ++i)
+      if (out[o].meets(in[i])) return false;
+    for (int other = 0; other < o; ++other)
+      if (out[o].meets(out[other])) return false;
+  }
+  return true;
+}
+
+// The pools' pointers, and what they take up: codes and scales of K, of V.
+sparsp_status_t check_pools(const CacheDims& c, const void* kc, const float* ks, const void* vc, const float* vs, Words* pools) {
+  CHECK_PTR(kc);
+  CHECK_PTR(ks);
+  CHECK_PTR(vc);
+  CHECK_PTR(vs);
+  const int64_t scales = (int64_t)c.blocks * c.heads, codes = scales * c.bt * c.d / 4;
+  pools[0] = {kc, codes};
+  pools[1] = {ks, scales};
+  pools[2] = {vc, codes};
+  pools[3] = {vs, scales};
+  return SPARSP_OK;
+}
 
 sparsp_status_t check_attn(const sparsp_cache_t* cache, int32_t B, int32_t H, int64_t tokens, int32_t max_add,
                            int32_t max_blocks, CacheDims* c) {
@@ -119,12 +134,17 @@ sparsp_status_t sparsp_cache_write(const sparsp_cache_t* cache, int32_t dtype, c
     CHECK_PTR(slots);
   }
   const int elem = dtype == SPARSP_F32 ? 4 : 2;
-  r = check_strides(c, elem, &k_stride, &k_head);
-  if (r == SPARSP_OK) r = check_strides(c, elem, &v_stride, &v_head);
-  if (r == SPARSP_OK) r = check_pools(kc, ks, vc, vs);
+  Words pools[4];
+  r = check_strides(c, elem, tokens, &k_stride, &k_head);
+  if (r == SPARSP_OK) r = check_strides(c, elem, tokens, &v_stride, &v_head);
+  if (r == SPARSP_OK) r = check_pools(c, kc, ks, vc, vs, pools);
   if (r != SPARSP_OK) return r;
-  if (kc == vc || ks == vs) return SPARSP_ERR_INVALID_ARG;
   CHECK_OPT_PTR(d_status);
+  auto rows = [&](const void* p, int64_t token, int64_t head) {
+    return Words{p, tokens == 0 ? 0 : ((tokens - 1) * token + (c.heads - 1) * head + c.d) * elem / 4};
+  };
+  const Words in[] = {rows(k, k_stride, k_head), rows(v, v_stride, v_head), {slots, tokens}};
+  if (!apart(pools, 4, in, 3)) return SPARSP_ERR_INVALID_ARG;
   CacheWrite a{k, v, k_stride, k_head, v_stride, v_head, slots, (int)tokens, (uint8_t*)kc, (uint8_t*)vc, ks, vs};
   return launch_cache_write(c, dtype, a, d_status, (cudaStream_t)stream);
 }
@@ -159,7 +179,8 @@ sparsp_status_t sparsp_attn_cache_fwd(const sparsp_cache_t* cache, int32_t B, in
   CHECK_PTR(start);
   CHECK_PTR(len);
   CHECK_PTR(table);
-  r = check_pools(kc, ks, vc, vs);
+  Words in[10];   // what is read
+  r = check_pools(a.c, kc, ks, vc, vs, in);
   if (r != SPARSP_OK) return r;
   if ((row_ptr == nullptr) != (col_idx == nullptr) || col_cap < 0) return SPARSP_ERR_INVALID_ARG;
   CHECK_OPT_PTR(row_ptr);
@@ -168,9 +189,14 @@ sparsp_status_t sparsp_attn_cache_fwd(const sparsp_cache_t* cache, int32_t B, in
   CHECK_PTR(ws);
   if (ws_bytes < attn_cache_ws(a.c, H / a.c.heads, max_add)) return SPARSP_ERR_WORKSPACE;
   if (tokens == 0) return SPARSP_OK;
-  // (row is even)
-  const Words wq{q, ((tokens - 1) * q_stride + row) / 2}, wo{o, tokens * row / 2}, wl{lse, tokens * H};
-  if (wq.meets(wo) || wq.meets(wl) || wo.meets(wl)) return SPARSP_ERR_INVALID_ARG;
+  in[4] = {q, ((tokens - 1) * q_stride + row) / 2};   // (row is even)
+  in[5] = {start, (int64_t)B + 1};
+  in[6] = {len, B};
+  in[7] = {table, (int64_t)B * max_blocks};
+  in[8] = {row_ptr, row_ptr != nullptr ? (int64_t)B * a.c.heads + 1 : 0};
+  in[9] = {col_idx, col_idx != nullptr ? (col_cap < (int64_t)1 << 60 ? col_cap : (int64_t)1 << 60) : 0};
+  const Words out[] = {{o, tokens * row / 2}, {lse, tokens * H}};
+  if (!apart(out, 2, in, 10)) return SPARSP_ERR_INVALID_ARG;
   a.B = B;
   a.H = H;
   a.group = H / a.c.heads;

@@ -758,6 +758,7 @@ SPARSP_API sparsp_status_t sparsp_cache_extend(const sparsp_cache_t* cache, int3
  * (as slots of sparsp_cache_extend have); with two its contents are not defined. Where a
  * run starts inside a block whose scale is not positive and at most 2^120, SPARSP_ERR_DATA
  * is set, the old scale does not count and the tokens before the run are left as they are.
+ * The pools' codes and scales may overlap neither one another nor k, v (from their first value to their last) or slots.
  */
 SPARSP_API sparsp_status_t sparsp_cache_write(const sparsp_cache_t* cache, int32_t dtype, const void* k,
                                               int64_t k_stride, int64_t k_head, const void* v, int64_t v_stride,
@@ -790,7 +791,7 @@ SPARSP_API sparsp_status_t sparsp_cache_write(const sparsp_cache_t* cache, int32
  * request's are left out), a length outside [0, max_blocks * bt] (counts as 0), a CSR row that is
  * malformed (counts as empty), an entry of it without tokens or a block outside the pool
  * (its keys are left out).
- * ws: at least sparsp_attn_cache_workspace_size() bytes. o and lse may not overlap q or each other.
+ * ws: at least sparsp_attn_cache_workspace_size() bytes. o and lse may not overlap each other nor anything that is read.
  */
 enum { SPARSP_CACHE_CAUSAL = 1u << 0 };
 SPARSP_API size_t sparsp_attn_cache_workspace_size(const sparsp_cache_t* cache, int32_t B, int32_t H, int64_t tokens,
