@@ -58,7 +58,9 @@ def cache_extend(shape: CacheShape, length, add, free, table, tokens: int, used=
     and are entered into table (int32 [B, blocks per request], in place). tokens: the packed
     new tokens there is room for. Returns (len_out [B], start [B+1], slots [tokens],
     used_out [1]); len_out may be length and used_out used. Requests that find too few
-    blocks or slots wait (CAPACITY in status): their length stays and their slots are -1."""
+    blocks or slots wait (CAPACITY in status): their length stays and their slots are -1. Their
+    tokens keep their place in start, so attn_cache_fwd's rows there mean nothing: drop rows whose
+    slot is -1 and bring those tokens again."""
     dev, i32 = torch.cuda.current_device(), torch.int32
     if not isinstance(length, torch.Tensor) or length.dim() != 1:
         _refuse("length", length, "a contiguous int32 [B] tensor")
@@ -125,7 +127,8 @@ def attn_cache_fwd(pool: CachePool, q, start, length, table, max_add: int, scale
     projection) over the cache: request b has rows start[b] .. start[b+1]-1 (at most
     max_add), the last of its length[b] tokens, in the blocks table[b]. H is a multiple of
     the pool's heads. causal: a row sees the tokens up to its own, else all of its
-    request. row_ptr, col_idx: the blocks seen, per request and key head (CSR). Returns
+    request. row_ptr, col_idx: the blocks seen, per request and key head (CSR). Rows of a
+    request that waits in cache_extend (slots of -1) mean nothing. Returns
     (O [tokens, H, d], LSE [tokens, H]); a row that sees nothing has O = 0, LSE = -inf."""
     s, dev, i32 = pool.shape, torch.cuda.current_device(), torch.int32
     if not isinstance(length, torch.Tensor) or length.dim() != 1:

@@ -735,7 +735,8 @@ typedef struct {
  * A request whose need is not covered, or whose tokens do not fit in `tokens`, sets
  * SPARSP_ERR_CAPACITY and waits, and so does every later one that needs a block (or
  * brings tokens past the end): len_out = len, slots -1, no blocks; its tokens keep their
- * place in the packed order. A request with a negative len or add, or more than
+ * place in the packed order, so that the rows of sparsp_attn_cache_fwd there, of which it knows nothing, mean nothing:
+ * rows whose slot is -1 are to be dropped, and their tokens brought again. A request with a negative len or add, or more than
  * max_blocks * bt tokens, sets SPARSP_ERR_DATA and brings nothing; a block number
  * outside [0, blocks) sets SPARSP_ERR_DATA and gives slots of -1.
  */
@@ -768,7 +769,8 @@ SPARSP_API sparsp_status_t sparsp_cache_write(const sparsp_cache_t* cache, int32
 /*
  * Attention of new tokens over that cache. q: packed rows [tokens, H, d] of bf16, q_stride
  * elements between tokens (0: H*d); request b has rows start[b] .. start[b+1]-1, at most
- * max_add of them, which are the last of its len[b] tokens. H is a multiple of the cache's
+ * max_add of them, which are the last of its len[b] tokens (those of a request that waits in sparsp_cache_extend are not:
+ * its rows are taken for the last of its older tokens, and what they give is to be dropped). H is a multiple of the cache's
  * heads; query head h reads key head h / (H / heads). Over the keys it sees,
  *   O_q = sum_k softmax_k(scale q.k) v_k,  LSE_q = ln sum_k exp(scale q.k),
  * k and v the values that the codes stand for; scale <= 0 means 1/sqrt(d).
