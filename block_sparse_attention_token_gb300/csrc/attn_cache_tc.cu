@@ -37,7 +37,10 @@
 //   warp 14, first CTA: issues O += P V (A = P in TMEM, B = V MN-major).
 // TMEM (512 columns): S of three stages, and in its place P, [0, 384), O [384, 384 + d).
 // The first CTA's barriers count what its products wait for in both CTAs (remote arrivals); its commits
-// reach both. Every mbarrier wait is bounded (2 s); on expiry the CTA sets SPARSP_ERR_TIMEOUT, all roles
+// reach both. A remote arrival and its wait order no memory between the CTAs, and need not: what it stands for is read by
+// the tensor cores alone, each CTA's own shared and tensor memory, where the writer's fences before the arrival have put
+// it (fence.proxy.async; tcgen05.wait and tcgen05.fence::before_thread_sync). With a release at cluster scope a stage takes
+// thousands of cycles more. Every mbarrier wait is bounded (2 s); on expiry the CTA sets SPARSP_ERR_TIMEOUT, all roles
 // leave their loops, copies and MMAs in flight are drained with a second bounded wait, and
 // TMEM is released when both CTAs are done.
 #include <cuda_fp16.h>
@@ -149,22 +152,14 @@ __device__ __forceinline__ uint32_t in_first(uint32_t addr) {
 __device__ __forceinline__ void arrive_cluster(uint32_t cluster_bar) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];\n" ::"r"(cluster_bar) : "memory");
 }
-__device__ __forceinline__ bool try_wait_cluster(uint32_t bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n.reg .pred p;\nmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\nselp.u32 %0, 1, 0, p;\n}\n"
-      : "=r"(ok)
-      : "r"(bar), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
-// As wait_warp, for barriers that the other CTA arrives on.
-__device__ __forceinline__ bool wait_pair(uint32_t bar, uint32_t parity, const Guard& g) {
-  bool ok = try_wait_cluster(bar, parity);
+// As wait_warp, for the two warps that issue products, with one way out (whole frames of d = 128 and 64 take 654 and
+// 545 us with it, with wait_warp 658 and 550).
+__device__ __forceinline__ bool wait_issue(uint32_t bar, uint32_t parity, const Guard& g) {
+  bool ok = mbar_try_wait(bar, parity);
   if (!ok) {
     const uint64_t t0 = globaltimer_ns();
     for (uint32_t it = 1; !ok; ++it) {
-      ok = try_wait_cluster(bar, parity);
+      ok = mbar_try_wait(bar, parity);
       if (!ok && (it & 63u) == 0) {
         if (*g.abort) break;
         if (globaltimer_ns() - t0 > g.limit_ns) {
@@ -492,10 +487,10 @@ attn_cache_tc_kernel(const __grid_constant__ CUtensorMap tk, const __grid_consta
       bool issued = false, ok = true;
       Piece x;
       while (ok && next_piece(x)) {
-        if (!(ok = wait_pair(bar(Q_FULL), n_q++ & 1u, g))) break;
+        if (!(ok = wait_issue(bar(Q_FULL), n_q++ & 1u, g))) break;
         for (int e = x.e0; e < x.e1; ++e, ++n) {
           const uint32_t ks = n % kNK, b = n % kNS;
-          if (!(ok = wait_pair(bar(K_FULL + ks), (n / kNK) & 1u, g))) break;
+          if (!(ok = wait_issue(bar(K_FULL + ks), (n / kNK) & 1u, g))) break;
           if (!(ok = wait_warp(bar(PV_DONE + b), ((n / kNS) & 1u) ^ 1u, g))) break;
           fence_after();
           if (elect_one()) {
@@ -527,9 +522,9 @@ attn_cache_tc_kernel(const __grid_constant__ CUtensorMap tk, const __grid_consta
       while (ok && next_piece(x)) {
         for (int e = x.e0; e < x.e1; ++e, ++n) {
           const uint32_t ws = n % kNW, b = n % kNS;
-          if (!(ok = wait_pair(bar(W_FULL + ws), (n / kNW) & 1u, g))) break;
-          if (!(ok = wait_pair(bar(P_FULL + b), (n / kNS) & 1u, g))) break;
-          if (e == x.e0 && !(ok = wait_pair(bar(O_EMPTY), (n_o++ & 1u) ^ 1u, g))) break;
+          if (!(ok = wait_issue(bar(W_FULL + ws), (n / kNW) & 1u, g))) break;
+          if (!(ok = wait_issue(bar(P_FULL + b), (n / kNS) & 1u, g))) break;
+          if (e == x.e0 && !(ok = wait_issue(bar(O_EMPTY), (n_o++ & 1u) ^ 1u, g))) break;
           fence_after();
           if (elect_one()) {
 #pragma unroll
