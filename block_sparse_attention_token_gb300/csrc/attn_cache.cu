@@ -188,7 +188,7 @@ attn_cache_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
     };
     auto page_of = [&](int u, int j) -> int {  // -1: none
       if (u >= stop) return -1;
-      if (j < 0 || ((int64_t)j << shift) * kUnit >= x.len) {
+      if (!has_tokens(a, x, j)) {
         report(a.d_status, SPARSP_ERR_DATA);
         return -1;
       }
@@ -205,7 +205,7 @@ attn_cache_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
       if (i < steps && (!wide || (i & 3) == 0)) {
         const int in_block = (unit & ((1 << shift) - 1)) * kUnit;
         exist = 0;
-        if (page1 >= 0 && page1 < a.c.blocks) {
+        if (in_pool(a, page1)) {
           pos = (block1 << shift) * kUnit + in_block;
           exist = min(kUnit, x.len - pos);
           row = hk * a.c.bt + in_block;

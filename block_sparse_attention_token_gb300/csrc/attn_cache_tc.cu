@@ -43,8 +43,6 @@
 // thousands of cycles more. Every mbarrier wait is bounded (2 s); on expiry the CTA sets SPARSP_ERR_TIMEOUT, all roles
 // leave their loops, copies and MMAs in flight are drained with a second bounded wait, and
 // TMEM is released when both CTAs are done.
-#include <cuda_fp16.h>
-
 #include "cache_items.cuh"
 #include "rows.cuh"
 
@@ -205,12 +203,6 @@ __device__ __forceinline__ float tmem_ld32_max(uint32_t taddr, uint32_t* r) {
         "=r"(r[29]), "=r"(r[30]), "=r"(r[31]), "=f"(m)
       : "r"(taddr));
   return m;
-}
-
-__device__ __forceinline__ uint32_t e4m3_pair(float lo, float hi) {   // lo in the low byte
-  uint16_t r;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;\n" : "=h"(r) : "f"(hi), "f"(lo));
-  return r;
 }
 
 // Items of the whole call, for this kernel: entries are requests, or with lists request
@@ -404,12 +396,12 @@ attn_cache_tc_kernel(const __grid_constant__ CUtensorMap tk, const __grid_consta
           if (u >= 2 * e1 || u >= x.units) return h;
           int j = u / per_block;
           if (list != nullptr) j = __ldg(list + j);
-          if (j < 0 || (int64_t)j * a.c.bt >= x.len) {
+          if (!has_tokens(a, x, j)) {
             report(a.d_status, SPARSP_ERR_DATA);
             return h;
           }
           const int page = __ldg(table + j);
-          if (page < 0 || page >= a.c.blocks) {
+          if (!in_pool(a, page)) {
             report(a.d_status, SPARSP_ERR_DATA);
             return h;
           }
@@ -660,8 +652,8 @@ attn_cache_tc_kernel(const __grid_constant__ CUtensorMap tk, const __grid_consta
             float f0 = __uint_as_float(p[i] << 16), f1 = __uint_as_float(p[i] & 0xffff0000u);
             f0 = fabsf(f0) < INFINITY ? f0 * down : NAN;   // what is not finite is NaN to the scores
             f1 = fabsf(f1) < INFINITY ? f1 * down : NAN;
-            const uint32_t big = e4m3_pair(f0, f1), back = f16x2_of_e4m3(big);
-            const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&back));
+            const uint32_t big = e4m3_pair(f0, f1);
+            const float2 b = e4m3_values(big);
             const uint32_t small = e4m3_pair(f0 - b.x, f1 - b.y);
             if (i & 1) {
               hi4[i / 2] |= big << 16;

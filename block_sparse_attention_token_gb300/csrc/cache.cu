@@ -21,8 +21,6 @@
 // (K and V of several heads to a CTA, the next ones on their way meanwhile; with one task to a CTA 199). 256 runs of
 // one token take 7 us on the device, a chain of four dependent loads; tables of 4,096 requests 14 us, 5 of
 // them the scan, of 64 requests 8.
-#include <cuda_fp16.h>
-
 #include <type_traits>
 
 #include "cache.cuh"
@@ -183,18 +181,6 @@ cache_extend_kernel(const CacheDims c, const CacheExtend a, int what, int32_t* d
   }
 }
 
-// Two fp32 values as e4m3 codes, lo in the low byte (round to nearest even, at most +-448).
-__device__ __forceinline__ uint32_t e4m3_pair(float lo, float hi) {
-  uint16_t r;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;\n" : "=h"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-__device__ __forceinline__ float2 e4m3_values(uint32_t pair) {
-  uint32_t h;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;\n" : "=r"(h) : "h"((uint16_t)pair));
-  return __half22float2(*reinterpret_cast<__half2*>(&h));
-}
-
 // The scale of values of up to `most` (finite, not negative; as bits): 448 = 1.75 * 2^8.
 __device__ __forceinline__ float scale_of(uint32_t most) {
   const int e = (int)(most >> 23) - 127 - 8 + ((most & 0x7fffffu) > 0x600000u ? 1 : 0);
@@ -338,7 +324,7 @@ cache_write_kernel(const CacheDims c, const CacheWrite a, int granule, int heads
         for (int k = 0; k < kAt; ++k) held[k] = k * kStep < n ? codes[k * kStep] : 0;
 #pragma unroll
         for (int k = 0; k < kAt; ++k) {
-          const float2 lo = e4m3_values(held[k] & 0xffffu), hi = e4m3_values(held[k] >> 16);
+          const float2 lo = e4m3_values(held[k]), hi = e4m3_values(held[k] >> 16);
           if (k * kStep < n)
             codes[k * kStep] = e4m3_pair(lo.x * ratio, lo.y * ratio) | e4m3_pair(hi.x * ratio, hi.y * ratio) << 16;
         }

@@ -2,6 +2,8 @@
 // request, one scale per block and head.
 #pragma once
 
+#include <cuda_fp16.h>
+
 #include "common.cuh"
 
 namespace sparsp {
@@ -55,5 +57,22 @@ size_t attn_cache_ws(const CacheDims& c, int group, int max_add);
 sparsp_status_t launch_attn_cache(const CacheAttn& a, void* ws, cudaStream_t st);
 size_t attn_cache_tc_ws(const CacheDims& c);
 sparsp_status_t launch_attn_cache_tc(const CacheAttn& a, void* ws, cudaStream_t st);
+
+// Two fp32 values as e4m3 codes, lo in the low byte (round to nearest even, at most +-448), and the low two bytes as the
+// values that they stand for.
+__device__ __forceinline__ uint32_t e4m3_pair(float lo, float hi) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;\n" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ uint32_t f16x2_of_e4m3(uint32_t two) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;\n" : "=r"(r) : "h"((uint16_t)two));
+  return r;
+}
+__device__ __forceinline__ float2 e4m3_values(uint32_t two) {
+  const uint32_t h = f16x2_of_e4m3(two);
+  return __half22float2(*reinterpret_cast<const __half2*>(&h));
+}
 
 }  // namespace sparsp

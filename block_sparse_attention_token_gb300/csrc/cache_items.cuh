@@ -1,8 +1,7 @@
-// What the kernels of attention over the cache share: the items that work is dealt out by,
-// the partial sums of items that several CTAs share, and 8-bit arithmetic.
+// What the kernels of attention over the cache share: the items that work is dealt out by, the checks of look-ups,
+// the parts of items that several CTAs share, and what scales do to scores and weights.
 #pragma once
 
-#include <cuda_fp16.h>
 #include <float.h>
 
 #include "cache.cuh"
@@ -50,6 +49,10 @@ __device__ __forceinline__ Entry entry_at(const CacheAttn& a, int e, bool tell) 
   x.per_head = x.weight = 0;
   return x;
 }
+
+// Does a block that a list names hold tokens of the request; is what a table names a block of the pool?
+__device__ __forceinline__ bool has_tokens(const CacheAttn& a, const Entry& x, int j) { return j >= 0 && (int64_t)j * a.c.bt < x.len; }
+__device__ __forceinline__ bool in_pool(const CacheAttn& a, int page) { return page >= 0 && page < a.c.blocks; }
 
 // The sum over the CTA's threads below this one, and over all of its WARPS warps.
 template <int WARPS>
@@ -99,11 +102,6 @@ inline Parts parts_of(void* ws, int ctas, int rows) {
   return p;
 }
 
-__device__ __forceinline__ uint32_t f16x2_of_e4m3(uint32_t two) {   // the low two bytes
-  uint32_t r;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;\n" : "=r"(r) : "h"((uint16_t)two));
-  return r;
-}
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
