@@ -33,7 +33,8 @@ struct Cfg {
   static constexpr int P2 = Unit<T, HALF>::P2;                 // the same, two to a packed operand
   static constexpr int UPR = D / NE;                           // units (lanes) per row
   static constexpr int VECS = GR * D / E;                      // vectors of a granule
-  static constexpr int THREADS = VECS >= 2048 ? 512 : 256;      // 4 to 8 vectors a thread
+  static constexpr int THREADS = 256;                          // 2 or 4 vectors each
+  static_assert(VECS == 512 || VECS == 1024, "vectors of a thread");
   static constexpr int U = GR * UPR / THREADS;                 // units (rows) per thread
   static constexpr int kRowStep = THREADS / UPR;
   static_assert(UPR <= 32 && THREADS % UPR == 0 && U >= 1 && U * THREADS == GR * UPR, "granule split");
@@ -195,7 +196,7 @@ constexpr int kDepth = 3;
 // tile, granule after granule, and leaves its means: each warp keeps its columns' sums of every
 // head in shared memory, so that they are joined once, at the end.
 template <typename T, int D, int GR, bool HALF, bool POOL, bool BIAS, bool BLOCKED>
-__global__ void __launch_bounds__(Cfg<T, D, GR, HALF>::THREADS, Cfg<T, D, GR, HALF>::THREADS == 256 ? 2 : 1)
+__global__ void __launch_bounds__(Cfg<T, D, GR, HALF>::THREADS, 2)
 norm_rope_fwd_kernel(const Fwd q, const Fwd k, const Tokens tk, const RopeArgs a, bool rms, float eps,
                      int heads_per_cta, int32_t* d_status) {
   using C = Cfg<T, D, GR, HALF>;
@@ -351,7 +352,7 @@ norm_rope_fwd_kernel(const Fwd q, const Fwd k, const Tokens tk, const RopeArgs a
 
 // Each CTA leaves its columns' sums in part [CTA of q, then of k][dw, db][D].
 template <typename T, int D, int GR, bool HALF, bool RMS, bool BLOCKED>
-__global__ void __launch_bounds__(Cfg<T, D, GR, HALF>::THREADS, !HALF && Cfg<T, D, GR, HALF>::THREADS == 256 ? 2 : 1)
+__global__ void __launch_bounds__(Cfg<T, D, GR, HALF>::THREADS, HALF ? 1 : 2)
 norm_rope_bwd_kernel(const Bwd q, const Bwd k, const Tokens tk, const RopeArgs a, float eps,
                      int heads_per_cta, float* __restrict__ part, int32_t* d_status) {
   using C = Cfg<T, D, GR, HALF>;
