@@ -154,7 +154,7 @@ sparsp_status_t check_rows(const sparsp_shape_t* sh, bool tiles, Dims* s) {
 struct Span {
   const uint8_t* p;
   int64_t stride, row, bytes;
-  bool meets(const Span& o) const { return p < o.p + o.bytes && o.p < p + bytes; }
+  bool meets(const Span& o) const { return bytes > 0 && o.bytes > 0 && p < o.p + o.bytes && o.p < p + bytes; }
   // do two outputs share a value? Slices of one wider tensor lie side by side in each row.
   bool clashes(const Span& o) const {
     if (!meets(o)) return false;
@@ -203,8 +203,11 @@ sparsp_status_t check_norm_rope(const sparsp_shape_t* shape, uint32_t flags, flo
   CHECK_OPT_PTR(pos);
   if (tq->heads != s->H || tk->heads < 0 || (k != nullptr && tk->heads == 0)) return SPARSP_ERR_SHAPE;
   if ((int64_t)s->B * tk->heads > 65535) return SPARSP_ERR_UNSUPPORTED;
-  Span in[4], out[2];
-  int n_in = 0, n_out = 0;
+  Span in[10], out[2], small[4];   // small: means, or weights' gradients
+  int n_in = 0, n_out = 0, n_small = 0;
+  auto piece = [](const void* p, int64_t bytes) { return Span{(const uint8_t*)p, bytes, bytes, p != nullptr ? bytes : 0}; };
+  in[n_in++] = piece(table, rope_table_entries(*rope) * 8);
+  in[n_in++] = piece(pos, (int64_t)s->B * s->N * 12);
   for (sparsp_norm_rope_t* t : {tq, tk}) {
     if (t->heads == 0) continue;
     CHECK_PTR(t->x);
@@ -222,10 +225,26 @@ sparsp_status_t check_norm_rope(const sparsp_shape_t* shape, uint32_t flags, flo
     if (r == SPARSP_OK && backward) r = span_of(*s, t->heads, t->dy, &t->dy_stride, blocked, &in[n_in++]);
     if (r == SPARSP_OK) r = span_of(*s, t->heads, t->out, &t->out_stride, !backward && blocked, &out[n_out++]);
     if (r != SPARSP_OK) return r;
+    in[n_in++] = piece(t->w, 4 * s->d);
+    if (backward) {
+      small[n_small++] = piece(t->dw, 4 * s->d);
+      small[n_small++] = piece(t->db, 4 * s->d);
+    } else {
+      in[n_in++] = piece(t->b, 4 * s->d);
+      small[n_small++] = piece(t->means, (int64_t)s->B * t->heads * s->nb * s->d * 4);
+    }
   }
   for (int o = 0; o < n_out; ++o)
     for (int i = 0; i < n_in; ++i)
       if (out[o].meets(in[i])) return SPARSP_ERR_INVALID_ARG;
+  for (int o = 0; o < n_small; ++o) {
+    for (int i = 0; i < n_in; ++i)
+      if (small[o].meets(in[i])) return SPARSP_ERR_INVALID_ARG;
+    for (int i = 0; i < n_out; ++i)
+      if (small[o].meets(out[i])) return SPARSP_ERR_INVALID_ARG;
+    for (int i = 0; i < o; ++i)
+      if (small[o].meets(small[i])) return SPARSP_ERR_INVALID_ARG;
+  }
   if (n_out == 2 && out[0].clashes(out[1])) return SPARSP_ERR_INVALID_ARG;
   return SPARSP_OK;
 }

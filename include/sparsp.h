@@ -579,7 +579,8 @@ SPARSP_API sparsp_status_t sparsp_rope(const sparsp_shape_t* shape, const sparsp
  * table, pos and d_status as in sparsp_rope, eps and strides as in sparsp_norm_fwd (strides
  * below 2^32 bytes, else SPARSP_ERR_UNSUPPORTED).
  * The byte range of neither out may overlap that of an input; the two outs may be
- * slices of one wider tensor.
+ * slices of one wider tensor. Means, dw and db overlap nothing else (nor one another: q and k with one
+ * weight have two gradients, to be added by the caller).
  */
 typedef struct {
   int32_t heads;
