@@ -3,7 +3,7 @@
 import pytest
 
 import block_sparse_attention_token_gb300 as sp
-from test_cache_cpu import FAKE, GAP, at, attn, cache, lib, write  # noqa: F401
+from tests.test_cache_cpu import FAKE, GAP, at, attn, cache, lib, write  # noqa: F401
 
 CODES, SCALES = 10 * 2 * 64 * 64, 4 * 10 * 2    # bytes of the pools of cache()
 ROWS = 5 * 2 * 64 * 2                           # bytes of packed k and v

@@ -4,7 +4,7 @@ import pytest
 import torch
 
 import block_sparse_attention_token_gb300 as sp
-from test_gpu_cache import attn_ref, built, fresh_pool, gen, i32, values, word  # noqa: F401
+from tests.test_gpu_cache import attn_ref, built, fresh_pool, gen, i32, values, word  # noqa: F401
 
 pytestmark = [pytest.mark.gpu, pytest.mark.timeout(300)]
 

@@ -3,7 +3,7 @@ call here fails on the host before anything is launched (no GPU needed)."""
 import pytest
 
 import block_sparse_attention_token_gb300 as sp
-from test_norm_rope_pass_cpu import FAKE, GAP, axes, call, lib, part  # noqa: F401
+from tests.test_norm_rope_pass_cpu import FAKE, GAP, axes, call, lib, part  # noqa: F401
 
 FREE = FAKE + 60 * GAP
 OUT_Q, OUT_K = FAKE + 2 * GAP, FAKE + 10 * GAP
