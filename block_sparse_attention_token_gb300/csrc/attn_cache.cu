@@ -15,7 +15,7 @@
 // spans several CTAs leaves partial results that a second kernel joins in order. vs goes into the weights and out of
 // their sum again (cache_items.cuh), so that the products of all blocks add up in place.
 // Measured (32 heads over 8, d = 128): 64 uneven requests of up to 32,768 tokens 80 us (0.82 of a copy's rate); 8 x 4
-// rows over a tenth of 131,072 keys 55 us (0.57; 20 us of it fixed: scan and look-ups at the latency of a cold cache,
+// rows over a tenth of 131,072 keys 56 us (0.56; 20 us of it fixed: scan and look-ups at the latency of a cold cache,
 // the warps' join, the second kernel); one request of 1,024 keys 11 us on the device.
 #include "cache_items.cuh"
 #include "rows.cuh"
@@ -568,8 +568,8 @@ sparsp_status_t go(const CacheAttn& a, void* ws, cudaStream_t st) {
 // Requests with up to kFew rows (tokens times heads that share a key head) are this file's
 // kernel's, the others those of attn_cache_tc.cu. Only the device knows the requests, so where there may be both
 // both are launched (the one without work takes 8 us); a single request is taken at its word, max_add.
-// 32 requests of 8,192 keys, 8 key heads of 128, with 16, 32, 64, 128 rows: here 116, 156, 247, 424 us (rows beyond 16 read
-// the cache again), there 312, 181, 206, 223.
+// 32 requests of 8,192 keys, 8 key heads of 128, with 16, 32, 64, 128 rows: here 122, 163, 255, 433 us (rows beyond 16 read
+// the cache again), there 178, 204, 218, 237 (8 of each a captured call's own).
 constexpr int kFew = 32;
 bool many(int group, int max_add) { return (int64_t)group * max_add > kFew; }
 

@@ -11,9 +11,10 @@
 // The scale of a block's values goes into the exponent (cache_items.cuh); P is at most 2^15 (its reference follows when
 // it is passed by more than 2^4) and below 2^-24 f16 has nothing to add.
 //
-// Measured: 1,536 queries x 30,720 keys x 40 heads of d = 128 take 630 us when they come alone (0.81 of the bf16
-// peak for the two products, 0.73 back to back under the power cap), d = 64 525 us, 4 prompts of 4,096 tokens x 32
-// heads 442 us. Counted in cycles, a stage of 128 keys is 1,570 (d = 64: 1,290) where its products take 1,090
+// Measured: 1,536 queries x 30,720 keys x 40 heads of d = 128 take 650 us when they come alone (0.79 of the bf16
+// peak for the two products, 0.73 back to back under the power cap), d = 64 543 us, 4 prompts of 4,096 tokens x 32
+// heads 452 us (captured calls, 8 us each the replay's own). Counted in cycles, a stage of 128 keys is 1,570 (d = 64:
+// 1,290) where its products take 1,090
 // (545): a row's thread spends 3,140 on each second stage, 950 of them on 128 exponentials and their sum, 200 on
 // handing P over, 300 each on reading what it has to know of the keys and on waiting for the other thread's
 // reference, 470 on waiting for S (d = 64: 230). No pipe is full (tensor 0.70, exponentials 0.33); what bounds it

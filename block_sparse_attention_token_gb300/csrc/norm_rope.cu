@@ -16,8 +16,8 @@
 // copied into shared-memory slots of its own some heads ahead (cp.async).
 // Measured at 30,720 tokens and 40 + 40 heads of 128 in bf16 (of a copy's rate): forward 200 us (0.93),
 // with tile means 227 (0.82: a tile's means are joined over the warps at its end, through
-// shared memory), backward 304 (0.91); backward of 8,192 tokens and 12 + 12 heads of 64 in fp32 35 us (0.63: short
-// CTAs, and 5 us the sum of their parts); 64 tokens 5 us on the device. Norm and rotation
+// shared memory), backward 304 (0.91); backward of 8,192 tokens and 12 + 12 heads of 64 in fp32 35 us (0.63: the
+// heads go 8 and 4 to a CTA, and 5 us are the sum of the parts); 64 tokens 5 us on the device. Norm and rotation
 // one after the other take 435 us forward, without means.
 #include "rows.cuh"
 
