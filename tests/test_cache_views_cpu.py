@@ -37,10 +37,13 @@ def test_strides_as_they_are():
 
 
 @pytest.mark.gpu
+@pytest.mark.timeout(300)
 @pytest.mark.parametrize("to", [(6, 3, 64), (1, 3, 64), (6, 1, 64)])
 def test_calls_refuse_broadcast_views(to):
     """Keys, values or queries of one head or token given to several: an error before anything runs, and what a copy
     of the view gives is what the rows say."""
+    import __graft_entry__
+    __graft_entry__.build()
     n, heads, d = to
     i32 = dict(dtype=torch.int32, device="cuda")
     pool = sp.block_pool(2, heads, d, 64)
