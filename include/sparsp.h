@@ -785,8 +785,8 @@ SPARSP_API sparsp_status_t sparsp_cache_write(const sparsp_cache_t* cache, int32
  * (tokens past len may hold anything). Scales must be finite, those of K not negative and those of V positive (as
  * sparsp_cache_write leaves them; of V, below 2^-120 they count as that, and values under a scale that is 2^80 below
  * another one of their request and key head may count as 0); a scale of K that is NaN makes the rows NaN that see a key
- * of its block. Products are exact and summed in fp32; the softmax's weights
- * are rounded to 11 bits. Of a request with more than 32 rows per key head (its tokens * H / heads;
+ * of its block. Products are exact and summed in fp32; the softmax's weights, times their block's scale of V, are
+ * rounded to 11 bits and lost below 2^-35 of their row's largest. Of a request with more than 32 rows per key head (its tokens * H / heads;
  * with B = 1, max_add * H / heads), a query loses what is below 2^-18 of its largest value in magnitude.
  * Sums are taken in an order that depends on the lengths (and lists) of the whole call: the
  * same call gives the same bits, but a row's last bits may depend on the other requests.
